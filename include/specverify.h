@@ -19,9 +19,9 @@
  *     a message (per host thread).
  *   - Problems only the device can see (a draft token outside [0, V), a bad
  *     k_b, non-finite logits, a bad temperature or uniform, a KV capacity
- *     overflow, a bounded wait that ran out) never trap: the affected
- *     sequence's outputs become n_accepted = 0 and out_tokens = -1, and a bit
- *     is set in the workspace's flag word (SV_FLAG_*), readable with
+ *     overflow, a bad page, a bounded wait that ran out) never trap: the
+ *     affected sequence's outputs become n_accepted = 0 and out_tokens = -1 (NaN
+ *     where they are not tokens), and a bit is set in the workspace's flag word (SV_FLAG_*), readable with
  *     sv_read_device_flags.
  *   - Each call runs on the calling thread's current device.  The kernels'
  *     launch attributes and the device's properties are set up by the first
@@ -50,7 +50,19 @@ typedef enum {
   SV_ERR_UNSUPPORTED = 8   /* valid request this build does not implement        */
 } sv_status;
 
-typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+/* SV_E4M3 (8-bit floating point, 4 exponent and 3 mantissa bits, largest value
+ * 448, no infinities) is a type of sv_rmsnorm_residual's output and of
+ * sv_linear's operands only; every other call refuses it. */
+typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_E4M3 = 2 } sv_dtype;
+
+/* Activations of sv_linear. */
+enum {
+  SV_ACT_NONE = 0,
+  SV_ACT_RELU = 1,     /* max(z, 0)                                             */
+  SV_ACT_SILU = 2,     /* z / (1 + exp(-z))                                     */
+  SV_ACT_GELU = 3,     /* z/2 * (1 + erf(z / sqrt(2)))                          */
+  SV_ACT_GELU_TANH = 4 /* z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3)))     */
+};
 
 /* Per-row verify mode ([SSD §2.4]: greedy decoding is its own branch). */
 enum { SV_SAMPLED = 0, SV_GREEDY = 1 };
@@ -66,7 +78,9 @@ enum {
   SV_FLAG_BAD_MODE = 32,       /* mode[b] not SV_SAMPLED / SV_GREEDY               */
   SV_FLAG_CAPACITY = 64,       /* kv_commit: seq_len + n would pass capacity       */
   SV_FLAG_TIMEOUT = 128,       /* a bounded device wait ran out                    */
-  SV_FLAG_BAD_N = 256          /* kv_commit: n_accepted outside [0, K] or above k_b */
+  SV_FLAG_BAD_N = 256,         /* kv_commit: n_accepted outside [0, K] or above k_b;
+                                  prefix_attention: a length outside the table      */
+  SV_FLAG_BAD_PAGE = 512       /* prefix_attention: a needed page id outside the pool */
 };
 
 /* Optional per-(sequence, position) diagnostics, float32 [B][K+1][SV_DIAG_FIELDS],
@@ -351,6 +365,125 @@ size_t sv_lmhead_workspace_size(int M, int H);
 sv_status sv_lmhead_rmsnorm(const void* hidden, const void* norm_w, float eps, const void* W,
                             void* logits, sv_dtype out_dtype, int M, int H, int V,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * sv_prefix_attention - attention of one round's query positions over a paged
+ * KV cache whose sequences share a prefix [SD §2.1: the target scores the k+1
+ * positions of a draft in one forward pass; SSD §3.3, §4.5: the paged cache
+ * that sv_kv_commit_paged rolls back].  The prefix is read and multiplied once
+ * for the whole batch, not once per sequence.
+ *   Sequence b has L = seq_lens[b] committed tokens of its own behind the
+ *   prefix's P = prefix_len tokens, and its drafts' keys and values at
+ *   L .. L + k_b - 1 (the convention of sv_kv_commit_paged).  The query at
+ *   position i (0 <= i <= k_b) is that of the token before draft i: it sees the
+ *   whole prefix and the own tokens 0 .. L + i - 1.  For query head h, reading
+ *   the key head h / (Hq / Hkv):
+ *     s_j = scale * sum_d q[b][i][h][d] * k_j[d]   over the tokens j it sees,
+ *     out[b][i][h][:] = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *     lse[b][i][h] = log sum_j exp(s_j).
+ *   A query that sees no token gets out = 0 and lse = -inf.  Nothing is
+ *   written for positions i > k_b.  K = 0 is the single-token decode step.
+ *
+ *   q            device bf16, element (b,i,h,d) at b*q_seq_stride +
+ *                i*q_pos_stride + h*q_head_stride + d; strides in elements,
+ *                0 selects the packed [B][K+1][Hq][D] layout.
+ *   k_pool, v_pool  device bf16, token t of page p, key head h, at
+ *                p*page_stride + t*token_stride + h*head_stride + d; 0 strides
+ *                select [num_pages][page_size][Hkv][D].
+ *   prefix_pages device int32 [ceil(P / page_size)]: the prefix's pages, or
+ *                NULL if prefix_len is 0.
+ *   block_table  device int32 [B][max_pages]: each sequence's own pages.
+ *   seq_lens     device int32 [B]; k_per_row device int32 [B] or NULL (= K).
+ *   scale        finite.
+ *   out          device bf16, strides as q's, 0 selects packed [B][K+1][Hq][D].
+ *   lse          device float32 [B][K+1][Hq], or NULL.
+ *   dtype        SV_BF16.
+ *   B, K         B >= 1, 0 <= K <= 20, B * (K + 1) * Hq <= 2^30.
+ *   Hq, Hkv, D   Hq a multiple of Hkv, Hq / Hkv <= 64; D 64 or 128.
+ *   page_size, max_pages >= 1, num_pages >= 1, prefix_len >= 0; lengths are
+ *                int32: P + max_pages * page_size must fit in int32.
+ *   workspace    device, >= sv_prefix_attention_workspace_size(...) bytes,
+ *                256-byte aligned; contents need no initialisation; its first
+ *                four bytes are the device flag word (cleared by the call).
+ *                Calls that share a workspace must be ordered on one stream.
+ * q, k_pool, v_pool and out must be 16-byte aligned and their strides
+ * multiples of 8 elements.  Products and the softmax's sums are float32; the
+ * unnormalised weights are rounded to bf16 for the product with v.
+ * Values past a sequence's end (the rest of a page, pages that are not its
+ * own) are never used, whatever they hold; a value of v at a draft position
+ * that is not finite makes the queries that see it not finite and no other.
+ * A sequence with k_b outside [0, K] (SV_FLAG_BAD_K), with L < 0 or L + k_b
+ * past its table (SV_FLAG_BAD_N), or with a page it needs outside
+ * [0, num_pages) (SV_FLAG_BAD_PAGE; a bad prefix page fails every sequence)
+ * gets NaN in out and lse at every position 0 .. k_b (0 .. K for a bad k_b).
+ */
+size_t sv_prefix_attention_workspace_size(int B, int K, int Hq, int Hkv, int D, int prefix_len,
+                                          int max_own_len);
+sv_status sv_prefix_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_stride,
+                              int64_t q_head_stride, const void* k_pool, const void* v_pool,
+                              int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                              int num_pages, int page_size, const int32_t* prefix_pages,
+                              int prefix_len, const int32_t* block_table, int max_pages,
+                              const int32_t* seq_lens, const int32_t* k_per_row, float scale,
+                              void* out, int64_t out_seq_stride, int64_t out_pos_stride,
+                              int64_t out_head_stride, float* lse, sv_dtype dtype, int B, int K,
+                              int Hq, int Hkv, int D, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * sv_rmsnorm_residual - the RMSNorm of sv_lmhead_rmsnorm [SSD §3.1] between
+ * two layers: with the residual's addition before it and, on request, its
+ * output in 8 bits with a scale per row (the operands of sv_linear).
+ *     s[m][k] = x[m][k] + residual[m][k]
+ *     y[m][k] = norm_w[k] * s[m][k] / sqrt(mean_k s[m][k]^2 + eps)
+ *   out_dtype SV_BF16: out = y.  SV_E4M3: out_scale[m] = max(max_k |y[m][k]| / 448,
+ *   2^-126) and out = y / out_scale[m], rounded to the nearest e4m3 value.
+ *   x            device [M][H] of dtype (SV_BF16 or SV_F32), row stride ldx.
+ *   residual     device [M][H] of dtype, row stride ldr, or NULL (s = x).
+ *   norm_w       device bf16 [H].
+ *   residual_out device [M][H] of dtype, row stride ldro, or NULL: s, rounded
+ *                once (y comes from the unrounded s).  May be x or residual
+ *                itself (same address and stride).
+ *   out          device [M][H] of out_dtype, row stride ldo; not an input.
+ *   out_scale    device float32 [M]; required for SV_E4M3, else ignored.
+ *   M, H         each >= 1; row strides in elements, 0 selects H.
+ * Pointers need only their element's alignment.  A row with a value that is
+ * not finite gets NaN where its formula does (its whole e4m3 row and scale).
+ */
+sv_status sv_rmsnorm_residual(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                              const void* norm_w, float eps, void* residual_out, int64_t ldro,
+                              sv_dtype dtype, void* out, int64_t ldo, sv_dtype out_dtype,
+                              float* out_scale, int M, int H, void* stream);
+
+/*
+ * sv_linear - a matrix product on the tensor cores with bias, activation and
+ * residual in its epilogue: the projections around sv_prefix_attention, and
+ * the residual block x + act(W x + b) of a draft head in front of
+ * sv_lmhead_rmsnorm [FS §2.3].
+ *     z[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] W[n][k] + bias[n]
+ *     out[m][n] = act(z[m][n]) + residual[m][n]
+ *   x         device [M][K] of in_dtype (SV_BF16 or SV_E4M3), row stride ldx.
+ *   W         device [N][K] of in_dtype, row stride ldw (K contiguous).
+ *   x_scale   device float32 [M] or NULL (1); w_scale device float32 [N] or NULL.
+ *   bias      device bf16 [N] or NULL.
+ *   residual  device [M][N] of out_dtype, row stride ldr, or NULL.  May be out
+ *             itself (same address and stride).
+ *   act       SV_ACT_*.
+ *   out       device [M][N] of out_dtype (SV_BF16 or SV_F32), row stride ldo.
+ *   M, N, K   each >= 1; row strides in elements, 0 selects K, K, N, N.
+ *   workspace >= sv_linear_workspace_size(M, N, K) bytes, 256-byte aligned; its
+ *             first four bytes are the device flag word (OR-ed, not cleared:
+ *             zero it once).
+ * x and W must be 16-byte aligned with row strides of a multiple of 16 bytes
+ * (values between K and the stride are not used); the rest needs its
+ * element's alignment.  Products and sums are float32, rounded once at the end.
+ */
+size_t sv_linear_workspace_size(int M, int N, int K);
+sv_status sv_linear(const void* x, int64_t ldx, const float* x_scale, const void* W, int64_t ldw,
+                    const float* w_scale, sv_dtype in_dtype, const void* bias,
+                    const void* residual, int64_t ldr, int act, void* out, int64_t ldo,
+                    sv_dtype out_dtype, int M, int N, int K, void* workspace,
+                    size_t workspace_bytes, void* stream);
 
 /*
  * sv_read_device_flags - synchronise `stream` and copy the workspace's flag

@@ -30,7 +30,12 @@ Parity status of each function (what pins it, see tests/test_oracle_*.py):
   paged.kv_commit_paged        pinned: hand-worked page boundaries, per-token
                                page ownership on random cases, all-or-nothing
                                capacity
+  layer.prefix_attention       pinned: plain loops over single tokens, one key,
+                               equal keys, no key
+  layer.rmsnorm_residual / row_scale / e4m3_values
+                               pinned: lmhead.rmsnorm, torch's e4m3 values
+  layer.linear / activation    pinned: triple loop, torch's activations
 Planted mistakes that the pins must catch: tests/test_oracle_mutations*.py.
 """
 
-from . import analytics, dynk, lmhead, paged, sample, verify  # noqa: F401
+from . import analytics, dynk, layer, lmhead, paged, sample, verify  # noqa: F401

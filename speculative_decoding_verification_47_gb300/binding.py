@@ -29,6 +29,13 @@ SV_ERR_UNSUPPORTED = 8
 # sv_dtype
 SV_F32 = 0
 SV_BF16 = 1
+SV_E4M3 = 2
+# activations
+SV_ACT_NONE = 0
+SV_ACT_RELU = 1
+SV_ACT_SILU = 2
+SV_ACT_GELU = 3
+SV_ACT_GELU_TANH = 4
 # modes
 SV_SAMPLED = 0
 SV_GREEDY = 1
@@ -42,6 +49,7 @@ SV_FLAG_BAD_MODE = 32
 SV_FLAG_CAPACITY = 64
 SV_FLAG_TIMEOUT = 128
 SV_FLAG_BAD_N = 256
+SV_FLAG_BAD_PAGE = 512
 # diag fields
 SV_DIAG_M_T = 0
 SV_DIAG_S_T = 1
@@ -111,6 +119,21 @@ def lib() -> ctypes.CDLL:
         L.sv_dynk_init.argtypes = [_vp, _i32, _i32, _vp]
         L.sv_dynk_update.restype = _i32
         L.sv_dynk_update.argtypes = [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+        L.sv_prefix_attention_workspace_size.restype = _sz
+        L.sv_prefix_attention_workspace_size.argtypes = [_i32] * 7
+        L.sv_prefix_attention.restype = _i32
+        L.sv_prefix_attention.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i32,
+                                          _i32, _vp, _i32, _vp, _i32, _vp, _vp, _f32, _vp, _i64,
+                                          _i64, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp,
+                                          _sz, _vp]
+        L.sv_rmsnorm_residual.restype = _i32
+        L.sv_rmsnorm_residual.argtypes = [_vp, _i64, _vp, _i64, _vp, _f32, _vp, _i64, _i32, _vp,
+                                          _i64, _i32, _vp, _i32, _i32, _vp]
+        L.sv_linear_workspace_size.restype = _sz
+        L.sv_linear_workspace_size.argtypes = [_i32, _i32, _i32]
+        L.sv_linear.restype = _i32
+        L.sv_linear.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _i32, _vp,
+                                _i64, _i32, _i32, _i32, _i32, _vp, _sz, _vp]
         L.sv_read_device_flags.restype = _i32
         L.sv_read_device_flags.argtypes = [_vp, _c.POINTER(_c.c_uint32), _vp]
         L.sv_last_error.restype = _c.c_char_p
@@ -241,6 +264,42 @@ def sv_dynk_update(state, B, n_accepted, k_used, cap, k_next, workspace, workspa
                    stream=None):
     _check(lib().sv_dynk_update(_ptr(state), B, _ptr(n_accepted), _ptr(k_used), _ptr(cap),
                                 _ptr(k_next), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sv_prefix_attention_workspace_size(B: int, K: int, Hq: int, Hkv: int, D: int, prefix_len: int,
+                                       max_own_len: int) -> int:
+    return lib().sv_prefix_attention_workspace_size(B, K, Hq, Hkv, D, prefix_len, max_own_len)
+
+
+def sv_prefix_attention(q, q_seq_stride, q_pos_stride, q_head_stride, k_pool, v_pool, page_stride,
+                        token_stride, head_stride, num_pages, page_size, prefix_pages, prefix_len,
+                        block_table, max_pages, seq_lens, k_per_row, scale, out, out_seq_stride,
+                        out_pos_stride, out_head_stride, lse, dtype, B, K, Hq, Hkv, D, workspace,
+                        workspace_bytes, stream=None):
+    _check(lib().sv_prefix_attention(
+        _ptr(q), q_seq_stride, q_pos_stride, q_head_stride, _ptr(k_pool), _ptr(v_pool), page_stride,
+        token_stride, head_stride, num_pages, page_size, _ptr(prefix_pages), prefix_len,
+        _ptr(block_table), max_pages, _ptr(seq_lens), _ptr(k_per_row), scale, _ptr(out),
+        out_seq_stride, out_pos_stride, out_head_stride, _ptr(lse), dtype, B, K, Hq, Hkv, D,
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sv_rmsnorm_residual(x, ldx, residual, ldr, norm_w, eps, residual_out, ldro, dtype, out, ldo,
+                        out_dtype, out_scale, M, H, stream=None):
+    _check(lib().sv_rmsnorm_residual(_ptr(x), ldx, _ptr(residual), ldr, _ptr(norm_w), eps,
+                                     _ptr(residual_out), ldro, dtype, _ptr(out), ldo, out_dtype,
+                                     _ptr(out_scale), M, H, _stream(stream)))
+
+
+def sv_linear_workspace_size(M: int, N: int, K: int) -> int:
+    return lib().sv_linear_workspace_size(M, N, K)
+
+
+def sv_linear(x, ldx, x_scale, W, ldw, w_scale, in_dtype, bias, residual, ldr, act, out, ldo,
+              out_dtype, M, N, K, workspace, workspace_bytes, stream=None):
+    _check(lib().sv_linear(_ptr(x), ldx, _ptr(x_scale), _ptr(W), ldw, _ptr(w_scale), in_dtype,
+                           _ptr(bias), _ptr(residual), ldr, act, _ptr(out), ldo, out_dtype, M, N, K,
+                           _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def sv_read_device_flags(workspace, stream=None) -> int:

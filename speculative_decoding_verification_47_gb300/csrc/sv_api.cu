@@ -19,6 +19,7 @@ sv_status fail(sv_status s, const std::string& msg) {
 constexpr int kMaxK = 20;
 constexpr long long kMaxItems = 0x7fffffffLL / 16;  // items per call: the grid is items x <= 16 CTAs
 constexpr int kMaxSeqs = 1 << 30;                   // one thread per sequence
+constexpr int kMaxRows = 1 << 30;                   // query rows of an attention call
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -294,6 +295,190 @@ sv_status sv_lmhead_rmsnorm(const void* hidden, const void* norm_w, float eps, c
   std::string err;
   int s = sv::lmhead_launch(hidden, norm_w, eps, W, logits, out_dtype, M, H, V, workspace,
                             workspace_bytes, stream, &err);
+  if (s != SV_OK) return fail(static_cast<sv_status>(s), err);
+  return SV_OK;
+}
+
+// Shapes of the attention call, for its workspace too; NULL if they are in range.
+static const char* attention_shape(int B, int K, int Hq, int Hkv, int D, long long prefix_len,
+                                   long long max_own) {
+  if (B < 1 || K < 0 || K > kMaxK || Hq < 1 || Hkv < 1 || prefix_len < 0 || max_own < 1)
+    return "need B >= 1, 0 <= K <= 20, Hq >= 1, Hkv >= 1, prefix_len >= 0";
+  if (D != 64 && D != 128) return "D must be 64 or 128";
+  if (Hq % Hkv != 0 || Hq / Hkv > 64) return "Hq must be a multiple of Hkv, at most 64 times";
+  if ((long long)B * (K + 1) > kMaxRows / Hq) return "B * (K + 1) * Hq must be at most 2^30";
+  if (prefix_len + max_own > 0x7fffffffLL - 4096) return "prefix_len + max_pages * page_size must fit in int32";
+  return nullptr;
+}
+
+size_t sv_prefix_attention_workspace_size(int B, int K, int Hq, int Hkv, int D, int prefix_len,
+                                          int max_own_len) {
+  if (attention_shape(B, K, Hq, Hkv, D, prefix_len, max_own_len)) return 0;
+  return sv::attention_workspace_bytes(B, K, Hq, Hkv, D, prefix_len, max_own_len);
+}
+
+sv_status sv_prefix_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_stride,
+                              int64_t q_head_stride, const void* k_pool, const void* v_pool,
+                              int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                              int num_pages, int page_size, const int32_t* prefix_pages,
+                              int prefix_len, const int32_t* block_table, int max_pages,
+                              const int32_t* seq_lens, const int32_t* k_per_row, float scale,
+                              void* out, int64_t out_seq_stride, int64_t out_pos_stride,
+                              int64_t out_head_stride, float* lse, sv_dtype dtype, int B, int K,
+                              int Hq, int Hkv, int D, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (dtype != SV_BF16) return fail(SV_ERR_DTYPE, "dtype must be SV_BF16");
+  if (max_pages < 1 || page_size < 1 || num_pages < 1)
+    return fail(SV_ERR_SHAPE, "need max_pages >= 1, page_size >= 1, num_pages >= 1");
+  const long long own = (long long)max_pages * page_size;
+  if (const char* why = attention_shape(B, K, Hq, Hkv, D, prefix_len, own)) return fail(SV_ERR_SHAPE, why);
+  if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !out)
+    return fail(SV_ERR_ARG, "q, k_pool, v_pool, block_table, seq_lens and out are required");
+  if (prefix_len > 0 && !prefix_pages) return fail(SV_ERR_ARG, "prefix_pages is required when prefix_len > 0");
+  if (!(scale - scale == 0.0f)) return fail(SV_ERR_ARG, "scale must be finite");
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
+    return fail(SV_ERR_ARG, "q, k_pool, v_pool and out must be 16-byte aligned");
+  if (!aligned(lse, 4)) return fail(SV_ERR_ARG, "lse must be aligned to its element size");
+  sv::AttentionLaunch L;
+  L.q = q;
+  L.q_head = q_head_stride ? q_head_stride : D;
+  L.q_pos = q_pos_stride ? q_pos_stride : (long long)Hq * D;
+  L.q_seq = q_seq_stride ? q_seq_stride : (long long)(K + 1) * Hq * D;
+  L.k = k_pool;
+  L.v = v_pool;
+  L.head = head_stride ? head_stride : D;
+  L.token = token_stride ? token_stride : (long long)Hkv * D;
+  L.page = page_stride ? page_stride : (long long)page_size * Hkv * D;
+  L.out = out;
+  L.o_head = out_head_stride ? out_head_stride : D;
+  L.o_pos = out_pos_stride ? out_pos_stride : (long long)Hq * D;
+  L.o_seq = out_seq_stride ? out_seq_stride : (long long)(K + 1) * Hq * D;
+  for (long long s : {L.q_head, L.q_pos, L.q_seq, L.head, L.token, L.page, L.o_head, L.o_pos, L.o_seq})
+    if (s < 0 || s % 8 != 0) return fail(SV_ERR_SHAPE, "strides must be >= 0 and multiples of 8 elements");
+  if (L.o_head < D && Hq > 1) return fail(SV_ERR_SHAPE, "out head stride is smaller than D");
+  L.num_pages = num_pages;
+  L.page_size = page_size;
+  L.prefix_pages = prefix_pages;
+  L.prefix_len = prefix_len;
+  L.table = block_table;
+  L.max_pages = max_pages;
+  L.lens = seq_lens;
+  L.kpr = k_per_row;
+  L.scale = scale;
+  L.lse = lse;
+  L.B = B;
+  L.K = K;
+  L.Hq = Hq;
+  L.Hkv = Hkv;
+  L.D = D;
+  if (!workspace || !aligned(workspace, 256))
+    return fail(SV_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");
+  if (workspace_bytes < sv::attention_workspace_bytes(B, K, Hq, Hkv, D, prefix_len, (int)own))
+    return fail(SV_ERR_WORKSPACE, "workspace smaller than sv_prefix_attention_workspace_size()");
+  L.workspace = workspace;
+  L.stream = stream;
+  std::string err;
+  const int s = sv::attention_launch(L, &err);
+  if (s != SV_OK) return fail(static_cast<sv_status>(s), err);
+  return SV_OK;
+}
+
+sv_status sv_rmsnorm_residual(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                              const void* norm_w, float eps, void* residual_out, int64_t ldro,
+                              sv_dtype dtype, void* out, int64_t ldo, sv_dtype out_dtype,
+                              float* out_scale, int M, int H, void* stream) {
+  if (dtype != SV_F32 && dtype != SV_BF16) return fail(SV_ERR_DTYPE, "dtype must be SV_F32 or SV_BF16");
+  if (out_dtype != SV_BF16 && out_dtype != SV_E4M3)
+    return fail(SV_ERR_DTYPE, "out_dtype must be SV_BF16 or SV_E4M3");
+  if (M < 1 || H < 1) return fail(SV_ERR_SHAPE, "need M >= 1, H >= 1");
+  if (!x || !norm_w || !out) return fail(SV_ERR_ARG, "x, norm_w and out are required");
+  if (out_dtype == SV_E4M3 && !out_scale) return fail(SV_ERR_ARG, "out_scale is required for SV_E4M3");
+  if (!(eps >= 0.0f)) return fail(SV_ERR_ARG, "eps must be >= 0");
+  const size_t es = dtype == SV_BF16 ? 2 : 4;
+  if (!aligned(x, es) || !aligned(residual, es) || !aligned(residual_out, es) || !aligned(norm_w, 2) ||
+      !aligned(out, out_dtype == SV_BF16 ? 2 : 1) || !aligned(out_scale, 4))
+    return fail(SV_ERR_ARG, "pointers must be aligned to their element size");
+  sv::NormLaunch L;
+  L.x = x;
+  L.ldx = ldx ? ldx : H;
+  L.residual = residual;
+  L.ldr = ldr ? ldr : H;
+  L.w = norm_w;
+  L.eps = eps;
+  L.residual_out = residual_out;
+  L.ldro = ldro ? ldro : H;
+  L.dtype = dtype;
+  L.out = out;
+  L.ldo = ldo ? ldo : H;
+  L.out_dtype = out_dtype;
+  L.out_scale = out_scale;
+  L.M = M;
+  L.H = H;
+  L.stream = stream;
+  if (L.ldx < H || L.ldr < H || L.ldro < H || L.ldo < H)
+    return fail(SV_ERR_SHAPE, "row strides must be 0 or at least H");
+  if ((residual_out == x && L.ldro != L.ldx) || (residual && residual_out == residual && L.ldro != L.ldr))
+    return fail(SV_ERR_ARG, "residual_out over an input needs that input's row stride");
+  if (out == x || (residual && out == residual) || out == residual_out)
+    return fail(SV_ERR_ARG, "out must not be x, residual or residual_out");
+  std::string err;
+  const int s = sv::norm_launch(L, &err);
+  if (s != SV_OK) return fail(static_cast<sv_status>(s), err);
+  return SV_OK;
+}
+
+size_t sv_linear_workspace_size(int M, int N, int K) { return M < 1 || N < 1 || K < 1 ? 0 : 256; }
+
+sv_status sv_linear(const void* x, int64_t ldx, const float* x_scale, const void* W, int64_t ldw,
+                    const float* w_scale, sv_dtype in_dtype, const void* bias,
+                    const void* residual, int64_t ldr, int act, void* out, int64_t ldo,
+                    sv_dtype out_dtype, int M, int N, int K, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (in_dtype != SV_BF16 && in_dtype != SV_E4M3)
+    return fail(SV_ERR_DTYPE, "in_dtype must be SV_BF16 or SV_E4M3");
+  if (out_dtype != SV_F32 && out_dtype != SV_BF16)
+    return fail(SV_ERR_DTYPE, "out_dtype must be SV_F32 or SV_BF16");
+  if (M < 1 || N < 1 || K < 1) return fail(SV_ERR_SHAPE, "need M >= 1, N >= 1, K >= 1");
+  if (act < SV_ACT_NONE || act > SV_ACT_GELU_TANH) return fail(SV_ERR_ARG, "unknown activation");
+  if (!x || !W || !out) return fail(SV_ERR_ARG, "x, W and out are required");
+  const int es = in_dtype == SV_BF16 ? 2 : 1, os = out_dtype == SV_BF16 ? 2 : 4;
+  if (!aligned(x, 16) || !aligned(W, 16)) return fail(SV_ERR_ARG, "x and W must be 16-byte aligned");
+  if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 2) || !aligned(residual, os) ||
+      !aligned(out, os))
+    return fail(SV_ERR_ARG, "pointers must be aligned to their element size");
+  sv::LinearLaunch L;
+  L.x = x;
+  L.ldx = ldx ? ldx : K;
+  L.x_scale = x_scale;
+  L.W = W;
+  L.ldw = ldw ? ldw : K;
+  L.w_scale = w_scale;
+  L.in_dtype = in_dtype;
+  L.bias = bias;
+  L.residual = residual;
+  L.ldr = ldr ? ldr : N;
+  L.act = act;
+  L.out = out;
+  L.ldo = ldo ? ldo : N;
+  L.out_dtype = out_dtype;
+  L.M = M;
+  L.N = N;
+  L.K = K;
+  if (L.ldx < K || L.ldw < K || L.ldr < N || L.ldo < N)
+    return fail(SV_ERR_SHAPE, "row strides must be 0 or at least the row's length");
+  // the tensor-map limits of the operand copies
+  if (L.ldx * es % 16 != 0 || L.ldw * es % 16 != 0 || L.ldx >= (1LL << 38) || L.ldw >= (1LL << 38))
+    return fail(SV_ERR_SHAPE, "row strides of x and W must be multiples of 16 bytes below 2^38 elements");
+  if (residual == out && L.ldr != L.ldo) return fail(SV_ERR_ARG, "residual over out needs its row stride");
+  if (out == x || out == W) return fail(SV_ERR_ARG, "out must not be x or W");
+  if (!workspace || !aligned(workspace, 256))
+    return fail(SV_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");
+  if (workspace_bytes < sv_linear_workspace_size(M, N, K))
+    return fail(SV_ERR_WORKSPACE, "workspace smaller than sv_linear_workspace_size()");
+  L.flags = static_cast<uint32_t*>(workspace);
+  L.stream = stream;
+  std::string err;
+  const int s = sv::linear_launch(L, &err);
   if (s != SV_OK) return fail(static_cast<sv_status>(s), err);
   return SV_OK;
 }

@@ -89,4 +89,74 @@ int lmhead_launch(const void* hidden, const void* norm_w, float eps, const void*
                   void* stream, std::string* err);
 size_t lmhead_workspace_bytes(int M, int H);
 
+struct NormLaunch {
+  const void* x;
+  long long ldx;  // elements
+  const void* residual;
+  long long ldr;
+  const void* w;
+  float eps;
+  void* residual_out;
+  long long ldro;
+  sv_dtype dtype;
+  void* out;
+  long long ldo;
+  sv_dtype out_dtype;
+  float* out_scale;
+  int M, H;
+  void* stream;
+};
+
+// Enqueue the residual RMSNorm.  Returns an sv_status; fills *err on failure.
+int norm_launch(const NormLaunch& L, std::string* err);
+
+struct LinearLaunch {
+  const void* x;
+  long long ldx;  // elements
+  const float* x_scale;
+  const void* W;
+  long long ldw;
+  const float* w_scale;
+  sv_dtype in_dtype;
+  const void* bias;
+  const void* residual;
+  long long ldr;
+  int act;
+  void* out;
+  long long ldo;
+  sv_dtype out_dtype;
+  int M, N, K;
+  uint32_t* flags;
+  void* stream;
+};
+
+// Enqueue the product with its epilogue.  Returns an sv_status; fills *err on failure.
+int linear_launch(const LinearLaunch& L, std::string* err);
+
+struct AttentionLaunch {
+  const void* q;
+  long long q_seq, q_pos, q_head;  // elements
+  const void* k;
+  const void* v;
+  long long page, token, head;  // elements
+  int num_pages, page_size;
+  const int32_t* prefix_pages;
+  int prefix_len;
+  const int32_t* table;
+  int max_pages;
+  const int32_t* lens;
+  const int32_t* kpr;
+  float scale;
+  void* out;
+  long long o_seq, o_pos, o_head;  // elements
+  float* lse;
+  int B, K, Hq, Hkv, D;
+  void* workspace;
+  void* stream;
+};
+
+// Enqueue the shared-prefix attention.  Returns an sv_status; fills *err on failure.
+int attention_launch(const AttentionLaunch& L, std::string* err);
+size_t attention_workspace_bytes(int B, int K, int Hq, int Hkv, int D, int prefix_len, int max_own);
+
 }  // namespace sv

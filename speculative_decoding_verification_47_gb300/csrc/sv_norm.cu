@@ -1,0 +1,299 @@
+// Residual addition, RMSNorm and 8-bit quantisation of a row in one pass: the
+// norm of "Self-speculative decoding with layer skip and KV reuse" §3.1
+// between two layers.
+//
+//   s = x + residual,  y = w s / sqrt(mean(s^2) + eps)
+//   e4m3:  c = max(max|y| / 448, 2^-126),  q = rn(y / c)
+//
+// max|y| = rsqrt(..) * max|w s|, so the sum of squares and the maximum come
+// from the same pass and one reduction.  The row stays in registers (float32)
+// between that pass and the scaling: x and residual are read once.  s is
+// rounded only where it is stored; y comes from the unrounded sum.
+#include <cstdint>
+
+#include "sv_common.cuh"
+#include "sv_internal.h"
+
+namespace sv {
+namespace norm {
+
+constexpr float kE4M3Max = 448.f;
+constexpr float kTiny = 1.17549435e-38f;  // 2^-126: 1 / c stays finite
+
+struct Args {
+  const void* x;
+  long long ldx;
+  const void* res;
+  long long ldr;
+  const uint16_t* w;
+  float eps;
+  void* sum;
+  long long lds;
+  void* out;
+  long long ldo;
+  float* scale;
+  int M, H;
+};
+
+// max that keeps a NaN (fmaxf drops it)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+template <int VEC>
+struct alignas(VEC * 2) Half {
+  uint16_t v[VEC];
+};
+template <int VEC>
+struct alignas(VEC * 4 > 16 ? 16 : VEC * 4) Full {
+  float v[VEC];
+};
+
+template <int VEC>
+__device__ __forceinline__ void load(const uint16_t* p, float (&f)[VEC]) {
+  const Half<VEC> h = *reinterpret_cast<const Half<VEC>*>(p);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) f[i] = __uint_as_float((uint32_t)h.v[i] << 16);
+}
+template <int VEC>
+__device__ __forceinline__ void load(const float* p, float (&f)[VEC]) {
+  const Full<VEC> h = *reinterpret_cast<const Full<VEC>*>(p);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) f[i] = h.v[i];
+}
+template <int VEC>
+__device__ __forceinline__ void store(uint16_t* p, const float (&f)[VEC]) {
+  Half<VEC> h;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) h.v[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+  *reinterpret_cast<Half<VEC>*>(p) = h;
+}
+template <int VEC>
+__device__ __forceinline__ void store(float* p, const float (&f)[VEC]) {
+  Full<VEC> h;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) h.v[i] = f[i];
+  *reinterpret_cast<Full<VEC>*>(p) = h;
+}
+
+// two values to e4m3 (round to nearest, out of range to +-448, NaN kept)
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <int VEC>
+struct alignas(VEC) Bytes {
+  uint8_t v[VEC];
+};
+template <int VEC>
+__device__ __forceinline__ void store8(uint8_t* p, const float (&f)[VEC]) {
+  Bytes<VEC> b;
+  if (VEC == 1) {
+    b.v[0] = (uint8_t)e4m3x2(f[0], 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i + 1 < VEC; i += 2) {
+      const uint16_t two = e4m3x2(f[i], f[i + 1]);
+      b.v[i] = (uint8_t)two;
+      b.v[i + 1] = (uint8_t)(two >> 8);
+    }
+  }
+  *reinterpret_cast<Bytes<VEC>*>(p) = b;
+}
+
+// Sum and maximum over the threads of a row, to all of them.
+__device__ __forceinline__ void reduce(float (&part)[2][32], float& sum, float& top) {
+  const int t = threadIdx.x, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+  if (warps == 1) return;  // (else blockDim.y is 1)
+  if ((t & 31) == 0) {
+    part[0][t >> 5] = sum;
+    part[1][t >> 5] = top;
+  }
+  __syncthreads();
+  sum = (t & 31) < warps ? part[0][t & 31] : 0.f;
+  top = (t & 31) < warps ? part[1][t & 31] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+}
+
+// One row per blockDim.x threads (blockDim.y rows per CTA only with one warp
+// per row).  Thread t holds elements (j * blockDim.x + t) * VEC .., j < NV;
+// rows longer than NV * VEC * blockDim.x are read again for the scaling, each
+// element by the thread that overwrites it.
+template <typename T, bool Q8, int VEC, int NV>
+__global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
+  __shared__ float part[2][32];
+  pdl_launch_dependents();
+  const int t = threadIdx.x, n = blockDim.x;
+  const long long m = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  const bool live = m < a.M;
+  const T* x = static_cast<const T*>(a.x) + (live ? m : 0) * a.ldx;
+  const T* res = a.res ? static_cast<const T*>(a.res) + (live ? m : 0) * a.ldr : nullptr;
+  pdl_wait();  // the launch may overlap the kernel that wrote x
+
+  auto sum_at = [&](int k, float (&s)[VEC]) {
+    load<VEC>(x + k, s);
+    if (res) {
+      float r[VEC];
+      load<VEC>(res + k, r);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[i] += r[i];
+    }
+  };
+  float s[NV][VEC], ss = 0.f, top = 0.f;
+  auto gather = [&](const float (&v)[VEC], int k) {
+    float w[VEC];
+    if (Q8) load<VEC>(a.w + k, w);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      ss = __fmaf_rn(v[i], v[i], ss);
+      if (Q8) top = max_nan(top, fabsf(v[i] * w[i]));
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int k = (j * n + t) * VEC;
+    if (k < a.H) {
+      sum_at(k, s[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[j][i] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int k = (j * n + t) * VEC;
+    if (k < a.H) gather(s[j], k);
+  }
+  for (long long k = (long long)(NV * n + t) * VEC; k < a.H; k += (long long)n * VEC) {
+    float v[VEC];
+    sum_at((int)k, v);
+    gather(v, (int)k);
+  }
+  reduce(part, ss, top);
+  float r = rsqrtf(ss / (float)a.H + a.eps);
+  // |w s| may leave float32's range where |w s r| does not (s far from 1 and w
+  // with it): then the maximum is taken again, from the values themselves
+  if (Q8 && !(top > 1e-30f && top < 1e30f)) {  // (the same in every thread of the row)
+    top = 0.f;
+    auto again = [&](const float (&v)[VEC], int k) {
+      float w[VEC];
+      load<VEC>(a.w + k, w);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) top = max_nan(top, fabsf(v[i] * r * w[i]));
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int k = (j * n + t) * VEC;
+      if (k < a.H) again(s[j], k);
+    }
+    for (long long k = (long long)(NV * n + t) * VEC; k < a.H; k += (long long)n * VEC) {
+      float v[VEC];
+      sum_at((int)k, v);
+      again(v, (int)k);
+    }
+    if (n > 32) __syncthreads();  // (part[] is free again)
+    float none = 0.f;
+    reduce(part, none, top);
+  } else {
+    top *= r;
+  }
+  if (!live) return;
+  float inv = 1.f;
+  if (Q8) {
+    float c = top / kE4M3Max;
+    if (c < kTiny) c = kTiny;  // (a NaN stays)
+    inv = 1.f / c;
+    if (t == 0) a.scale[m] = c;
+  }
+  T* sum = a.sum ? static_cast<T*>(a.sum) + m * a.lds : nullptr;
+  auto finish = [&](const float (&v)[VEC], int k) {
+    float w[VEC], y[VEC];
+    load<VEC>(a.w + k, w);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) y[i] = v[i] * r * w[i] * inv;
+    if (sum) store<VEC>(sum + k, v);
+    if (Q8)
+      store8<VEC>(static_cast<uint8_t*>(a.out) + m * a.ldo + k, y);
+    else
+      store<VEC>(static_cast<uint16_t*>(a.out) + m * a.ldo + k, y);
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int k = (j * n + t) * VEC;
+    if (k < a.H) finish(s[j], k);
+  }
+  for (long long k = (long long)(NV * n + t) * VEC; k < a.H; k += (long long)n * VEC) {
+    float v[VEC];
+    sum_at((int)k, v);
+    finish(v, (int)k);
+  }
+}
+
+template <typename T, bool Q8, int VEC, int NV>
+static cudaError_t launch(const Args& a, int threads, int rows, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.M + (long long)rows - 1) / rows), 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, (unsigned)rows, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_kernel<T, Q8, VEC, NV>, a);
+}
+
+template <typename T, bool Q8>
+static cudaError_t dispatch(const Args& a, int vec, cudaStream_t st) {
+  constexpr int kPer = 16;  // elements a thread keeps
+  int threads = 32;
+  while (threads < 1024 && (long long)threads * kPer < a.H) threads *= 2;
+  const int rows = threads == 32 ? 4 : 1;
+  if (vec == 8) return launch<T, Q8, 8, kPer / 8>(a, threads, rows, st);
+  if (vec == 2) return launch<T, Q8, 2, kPer / 2>(a, threads, rows, st);
+  return launch<T, Q8, 1, kPer>(a, threads, rows, st);
+}
+
+}  // namespace norm
+
+int norm_launch(const NormLaunch& L, std::string* err) {
+  norm::Args a = {L.x, L.ldx, L.residual, L.ldr, static_cast<const uint16_t*>(L.w), L.eps,
+                  L.residual_out, L.ldro, L.out, L.ldo, L.out_scale, L.M, L.H};
+  const size_t es = L.dtype == SV_BF16 ? 2 : 4, os = L.out_dtype == SV_BF16 ? 2 : 1;
+  // the widest vector that every row of every array starts on a multiple of
+  auto fits = [&](int v) {
+    auto on = [&](const void* p, long long ld, size_t e) {
+      const size_t bytes = v * e > 16 ? 16 : v * e;
+      return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (L.M == 1 || ld * e % bytes == 0);
+    };
+    return L.H % v == 0 && on(L.x, L.ldx, es) && (!L.residual || on(L.residual, L.ldr, es)) &&
+           (!L.residual_out || on(L.residual_out, L.ldro, es)) && on(L.w, 0, 2) && on(L.out, L.ldo, os);
+  };
+  const int vec = fits(8) ? 8 : (fits(2) ? 2 : 1);
+  cudaStream_t st = static_cast<cudaStream_t>(L.stream);
+  const bool q8 = L.out_dtype == SV_E4M3;
+  cudaError_t e;
+  if (L.dtype == SV_BF16)
+    e = q8 ? norm::dispatch<uint16_t, true>(a, vec, st) : norm::dispatch<uint16_t, false>(a, vec, st);
+  else
+    e = q8 ? norm::dispatch<float, true>(a, vec, st) : norm::dispatch<float, false>(a, vec, st);
+  if (e != cudaSuccess) {
+    *err = std::string("residual norm launch: ") + cudaGetErrorString(e);
+    return SV_ERR_CUDA;
+  }
+  return SV_OK;
+}
+
+}  // namespace sv
