@@ -470,7 +470,7 @@ sv_status sv_rmsnorm_residual(const void* x, int64_t ldx, const void* residual, 
  *             itself (same address and stride).
  *   act       SV_ACT_*.
  *   out       device [M][N] of out_dtype (SV_BF16 or SV_F32), row stride ldo.
- *   M, N, K   each >= 1; row strides in elements, 0 selects K, K, N, N.
+ *   M, N, K   each in 1 .. 2^30; row strides in elements, 0 selects K, K, N, N.
  *   workspace >= sv_linear_workspace_size(M, N, K) bytes, 256-byte aligned; its
  *             first four bytes are the device flag word (OR-ed, not cleared:
  *             zero it once).

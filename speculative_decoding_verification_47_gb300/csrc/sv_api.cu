@@ -19,7 +19,7 @@ sv_status fail(sv_status s, const std::string& msg) {
 constexpr int kMaxK = 20;
 constexpr long long kMaxItems = 0x7fffffffLL / 16;  // items per call: the grid is items x <= 16 CTAs
 constexpr int kMaxSeqs = 1 << 30;                   // one thread per sequence
-constexpr int kMaxRows = 1 << 30;                   // query rows of an attention call
+constexpr int kMaxRows = 1 << 30;                   // rows of an attention or linear call
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -438,7 +438,8 @@ sv_status sv_linear(const void* x, int64_t ldx, const float* x_scale, const void
     return fail(SV_ERR_DTYPE, "in_dtype must be SV_BF16 or SV_E4M3");
   if (out_dtype != SV_F32 && out_dtype != SV_BF16)
     return fail(SV_ERR_DTYPE, "out_dtype must be SV_F32 or SV_BF16");
-  if (M < 1 || N < 1 || K < 1) return fail(SV_ERR_SHAPE, "need M >= 1, N >= 1, K >= 1");
+  if (M < 1 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K > kMaxRows)
+    return fail(SV_ERR_SHAPE, "need M, N and K in 1 .. 2^30");
   if (act < SV_ACT_NONE || act > SV_ACT_GELU_TANH) return fail(SV_ERR_ARG, "unknown activation");
   if (!x || !W || !out) return fail(SV_ERR_ARG, "x, W and out are required");
   const int es = in_dtype == SV_BF16 ? 2 : 1, os = out_dtype == SV_BF16 ? 2 : 4;

@@ -1,104 +1,645 @@
-// out = act(sx sw x W^T + bias) + residual: one 16 x 16 tile of outputs per
-// CTA, operands staged in shared memory as float32.
+// The matrix product of a layer with bias, activation and residual in its
+// epilogue, on the 5th-generation tensor cores:
+//
+//   z[m][n] = sx[m] sw[n] sum_k x[m][k] W[n][k] + bias[n]
+//   out[m][n] = act(z[m][n]) + residual[m][n]
+//
+// x and W are bf16 or e4m3, K contiguous in both: both operands are K-major,
+// one 128-byte swizzle row (64 bf16 or 128 e4m3 values) per k block, so the two
+// types share every tile and differ in the instruction alone.  Sums are float32
+// in tensor memory; the scales, which leave the sum, come in the epilogue.
+//
+// Two kernels:
+//  * rows_kernel (few rows of x): W is the MMA's 128-row operand and x its N
+//    side, 16 to 128 columns.  Bound by the bytes of W.  A cluster splits K and
+//    adds its partial sums through distributed shared memory in rank order.
+//  * pair_kernel (more rows): persistent CTA pairs, tiles of MS x 256 rows by BN
+//    columns with cta_group::2, each CTA staging its rows of x and half of W's.
 #include <cstdint>
+#include <string>
 
-#include <cuda_fp8.h>
-
-#include "sv_common.cuh"
-#include "sv_internal.h"
+#include "sv_tc.cuh"
 
 namespace sv {
 namespace lin {
 
-struct Args {
-  const void* x;
-  long long ldx;
+struct Epilogue {
   const float* sx;
-  const void* W;
-  long long ldw;
   const float* sw;
   const uint16_t* bias;
   const void* res;
   long long ldr;
   void* out;
   long long ldo;
-  int act, out_f32, M, N, K;
+  int act, out_f32, M, N;
+  int vec;  // rows of out and residual start on 16-byte boundaries
 };
 
-__device__ __forceinline__ float activate(float z, int act) {
-  switch (act) {
-    case SV_ACT_RELU: return z < 0.f ? 0.f : z;  // (a NaN stays)
-    case SV_ACT_SILU: return z / (1.f + __expf(-z));
-    case SV_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case SV_ACT_GELU_TANH:
-      return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-    default: return z;
+__device__ __forceinline__ float silu(float z) { return z / (1.f + __expf(-z)); }
+__device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.f + erff(z * 0.70710678118654752f)); }
+__device__ __forceinline__ float gelu_tanh(float z) {
+  return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+}
+
+// the activation of n values (one test of `act` for all of them)
+template <int n>
+__device__ __forceinline__ void activate(float (&z)[n], int act) {
+  if (act == SV_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];  // (a NaN stays)
+  } else if (act == SV_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) z[i] = silu(z[i]);
+  } else if (act == SV_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) z[i] = gelu(z[i]);
+  } else if (act == SV_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) z[i] = gelu_tanh(z[i]);
   }
 }
 
-__device__ __forceinline__ float value(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
-__device__ __forceinline__ float value(const __nv_fp8_e4m3* p) { return float(*p); }
+__device__ __forceinline__ float bf16(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
-template <typename T>
-__global__ void __launch_bounds__(256) linear_kernel(const Args a) {
-  __shared__ float xs[16][17], ws[16][17];
+// One output from its sum.
+__device__ __forceinline__ void finish(const Epilogue& e, long long m, int n, float acc, float sw, float bias) {
+  float z[1] = {acc * (e.sx ? e.sx[m] : 1.f) * sw + bias};
+  activate(z, e.act);
+  if (e.out_f32) {
+    if (e.res) z[0] += static_cast<const float*>(e.res)[m * e.ldr + n];
+    static_cast<float*>(e.out)[m * e.ldo + n] = z[0];
+  } else {
+    if (e.res) z[0] += bf16(static_cast<const uint16_t*>(e.res) + m * e.ldr + n);
+    static_cast<uint16_t*>(e.out)[m * e.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z[0]));
+  }
+}
+
+// The tensor cores add a product of one k step to the float32 accumulator by
+// cutting, not rounding: over K = 16384 (bf16) a float32 result is off by 1.9e-5
+// of its norm, sixty times the rounding sums' error.  Below a bf16 output that is
+// nothing (2^-9); for a float32 one the accumulation is cut into kChunk k blocks
+// (128 instructions, about 2e-6) whose sums are added with rounding.
+constexpr int kChunk = 32;
+
+constexpr int kRowBytes = 128;       // a k block of one row
+constexpr int kTile = 128 * kRowBytes;  // 128 rows of one k block
+
+// ---------------------------------------------------------------------------
+// Few rows of x: a tile is 128 rows of W by TM rows of x.
+// ---------------------------------------------------------------------------
+constexpr int kRowsThreads = 192;
+
+template <int TM>
+struct RowsShape {
+  static constexpr int kStageBytes = kTile + TM * kRowBytes;
+  static constexpr int kStages = 100 * 1024 / kStageBytes;  // two CTAs per SM
+  static constexpr int kSmem = kStages * kStageBytes + 1024;
+  static constexpr uint32_t kColumns = TM < 32 ? 32 : TM;
+  static_assert(kStages * kStageBytes >= TM * 128 * 4, "the partial sums fit over the ring");
+};
+
+template <int TM, bool F8>
+__global__ void __launch_bounds__(kRowsThreads, 2)
+    rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Epilogue e,
+                int KB, int split, uint32_t* flags) {
+  using S = RowsShape<TM>;
+  constexpr uint32_t kId = tc::idesc(F8, false, 128, TM);
+  constexpr int kElems = F8 ? 128 : 64;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], done;
+  __shared__ uint32_t tmem_base;
+  __shared__ int issued, consumed, failed;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % split, tile = blockIdx.x / split, n0 = tile * 128;
+  const int k_lo = (int)((long long)KB * rank / split), k_hi = (int)((long long)KB * (rank + 1) / split);
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    issued = consumed = failed = 0;
+    fence_mbar_init();
+    tc::prefetch_map(&tmX);
+    tc::prefetch_map(&tmW);
+    // W's first boxes into L2 while an earlier kernel of the stream may still run
+    for (int k = k_lo; k < k_hi && k < k_lo + S::kStages; ++k) tc::tma_prefetch(&tmW, k * kElems, n0);
+  }
+  if (warp == 0) tc::alloc<1>(&tmem_base, S::kColumns);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_launch_dependents();  // (behind the allocation: a dependent cannot take this CTA's columns)
   pdl_wait();
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const long long tiles_n = (a.N + 15) / 16;
-  const long long m0 = blockIdx.x / tiles_n * 16, n0 = blockIdx.x % tiles_n * 16;
-  const T* x = static_cast<const T*>(a.x);
-  const T* W = static_cast<const T*>(a.W);
-  float acc = 0.f;
-  for (int k0 = 0; k0 < a.K; k0 += 16) {
-    const int k = k0 + tx;
-    xs[ty][tx] = m0 + ty < a.M && k < a.K ? value(x + (m0 + ty) * a.ldx + k) : 0.f;
-    ws[ty][tx] = n0 + ty < a.N && k < a.K ? value(W + (n0 + ty) * a.ldw + k) : 0.f;
-    __syncthreads();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int g = 0;
+      for (int k = k_lo; k < k_hi; ++k, ++g) {
+        const int s = g % S::kStages, use = g / S::kStages;
+        if (use > 0 && !mbar_wait_bounded(&empty[s], (uint32_t)((use - 1) & 1))) {
+          failed = 1;
+          break;
+        }
+        uint8_t* w = smem + s * S::kStageBytes;
+        mbar_arrive_expect_tx(&full[s], (uint32_t)S::kStageBytes);
+        tc::tma_load(w, &tmW, k * kElems, n0, &full[s]);
+        tc::tma_load(w + kTile, &tmX, k * kElems, 0, &full[s]);
+      }
+      issued = g;
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int g = 0;
+      for (int k = k_lo; k < k_hi; ++k, ++g) {
+        const int s = g % S::kStages;
+        if (!mbar_wait_bounded(&full[s], (uint32_t)((g / S::kStages) & 1))) {
+          failed = 1;
+          break;
+        }
+        tc::fence_after();
+        const uint32_t w = smem_addr(smem + s * S::kStageBytes);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc = __fmaf_rn(xs[ty][j], ws[tx][j], acc);
+        for (int q = 0; q < 4; ++q)
+          tc::mma<1, F8>(tmem, tc::desc_sw128(w + 32 * q, 16, 1024), tc::desc_sw128(w + kTile + 32 * q, 16, 1024), kId,
+                         (g | q) != 0);
+        tc::commit<1>(smem_addr(&empty[s]));
+      }
+      consumed = g;
+      tc::commit<1>(smem_addr(&done));
+    }
+  }
+  __syncwarp();
+  // every thread: the accumulator is complete (so all loads have landed, too)
+  if (!mbar_wait_bounded(&done, 0)) failed = 1;
+  tc::fence_after();
+  __syncthreads();
+  if (failed) {  // a wait ran out: let the copies already issued land
+    if (tid == 0) {
+      atomicOr(flags, SV_FLAG_TIMEOUT);
+      for (int g = consumed; g < issued; ++g)
+        (void)mbar_wait_bounded(&full[g % S::kStages], (uint32_t)((g / S::kStages) & 1), 64);
+    }
     __syncthreads();
   }
-  const long long m = m0 + ty, n = n0 + tx;
-  if (m >= a.M || n >= a.N) return;
-  float z = acc * (a.sx ? a.sx[m] : 1.f) * (a.sw ? a.sw[n] : 1.f);
-  if (a.bias) z += value(a.bias + n);
-  z = activate(z, a.act);
-  if (a.out_f32) {
-    if (a.res) z += static_cast<const float*>(a.res)[m * a.ldr + n];
-    static_cast<float*>(a.out)[m * a.ldo + n] = z;
+  const int n = n0 + (warp & 3) * 32 + lane;
+  const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  if (split == 1) {
+    if (warp >= 2) {
+      const float sw = e.sw && n < e.N ? e.sw[n] : 1.f, bias = e.bias && n < e.N ? bf16(e.bias + n) : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < TM && c < e.M; c += 16) {
+        uint32_t v[16];
+        tc::ld16(lanes + c, v);
+        tc::ld_wait(v);
+        if (n < e.N) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < e.M) finish(e, c + j, n, __uint_as_float(v[j]), sw, bias);
+        }
+      }
+    }
   } else {
-    if (a.res) z += value(static_cast<const uint16_t*>(a.res) + m * a.ldr + n);
-    static_cast<uint16_t*>(a.out)[m * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
+    float* part = reinterpret_cast<float*>(smem);  // [TM][128]
+    if (warp >= 2) {
+#pragma unroll 1
+      for (int c = 0; c < TM && c < e.M; c += 16) {
+        uint32_t v[16];
+        tc::ld16(lanes + c, v);
+        tc::ld_wait(v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * 128 + (warp & 3) * 32 + lane] = __uint_as_float(v[j]);
+      }
+    }
+    tc::cluster_sync();
+    // each CTA adds its share of the tile over the ranks, in rank order
+    const uint32_t base = smem_addr(part);
+    for (int i = rank * kRowsThreads + tid; i < e.M * 128; i += split * kRowsThreads) {
+      const int nn = n0 + (i & 127);
+      if (nn >= e.N) continue;
+      float acc = 0.f;
+      for (int r = 0; r < split; ++r) {
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + 4u * i), "r"(r));
+        acc += tc::ld_cluster(at);
+      }
+      finish(e, i >> 7, nn, acc, e.sw ? e.sw[nn] : 1.f, e.bias ? bf16(e.bias + nn) : 0.f);
+    }
+    tc::cluster_sync();  // no CTA leaves while another reads its sums
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 0) tc::dealloc<1>(tmem, S::kColumns);
+}
+
+// ---------------------------------------------------------------------------
+// More rows: pairs of CTAs.
+// ---------------------------------------------------------------------------
+constexpr int kEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kEpiWarps;
+constexpr int kPairSmem = 4 * 3 * kTile + 1024;  // 192 KB of stages
+
+template <int MS>
+struct PairShape {
+  static constexpr int kStageBytes = (MS + 1) * kTile;
+  static constexpr int kStages = (kPairSmem - 1024) / kStageBytes;  // 6 (MS 1) or 4 (MS 2)
+  static constexpr int kBufs = 2 / MS;
+};
+
+// 16 columns of one row: scale, bias, activation, residual, store
+__device__ __forceinline__ void finish16(const Epilogue& e, long long m, int n, const uint32_t (&v)[16], float sx,
+                                         const float* sw, const float* bias) {
+  float z[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) z[j] = __fmaf_rn(__uint_as_float(v[j]), sx * sw[j], bias[j]);
+  activate(z, e.act);
+  const bool whole = e.vec && n + 16 <= e.N;
+  if (e.out_f32) {
+    float* o = static_cast<float*>(e.out) + m * e.ldo + n;
+    const float* r = e.res ? static_cast<const float*>(e.res) + m * e.ldr + n : nullptr;
+    if (whole) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r) a = reinterpret_cast<const float4*>(r)[q];
+        reinterpret_cast<float4*>(o)[q] =
+            make_float4(z[4 * q] + a.x, z[4 * q + 1] + a.y, z[4 * q + 2] + a.z, z[4 * q + 3] + a.w);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (n + j < e.N) o[j] = r ? z[j] + r[j] : z[j];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(e.out) + m * e.ldo + n;
+    const uint16_t* r = e.res ? static_cast<const uint16_t*>(e.res) + m * e.ldr + n : nullptr;
+    if (whole) {
+      if (r) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint4 a = reinterpret_cast<const uint4*>(r)[q];
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            z[8 * q + 2 * j] += bf16_lo(w[j]);
+            z[8 * q + 2 * j + 1] += bf16_hi(w[j]);
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        reinterpret_cast<uint4*>(o)[q] =
+            make_uint4(tc::pack_bf16x2(z[8 * q], z[8 * q + 1]), tc::pack_bf16x2(z[8 * q + 2], z[8 * q + 3]),
+                       tc::pack_bf16x2(z[8 * q + 4], z[8 * q + 5]), tc::pack_bf16x2(z[8 * q + 6], z[8 * q + 7]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (n + j < e.N) o[j] = __bfloat16_as_ushort(__float2bfloat16_rn(r ? z[j] + bf16(r + j) : z[j]));
+    }
+  }
+}
+
+// LONG: at most kChunk k blocks are summed in tensor memory; the chunks' sums
+// are added in registers (columns of a thread: BN / 2).
+template <int BN, int MS, bool F8, bool LONG>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Epilogue e,
+                int KB, uint32_t* flags) {
+  using PS = PairShape<MS>;
+  constexpr int kSt = PS::kStages, kSB = PS::kStageBytes, NB = PS::kBufs, BH = BN / 2, TR = MS * 256;
+  constexpr uint32_t kId = tc::idesc(F8, false, 256, BN);
+  constexpr int kElems = F8 ? 128 : 64;
+  static_assert(!LONG || MS == 1, "a thread keeps the sums of one sub-tile");
+  constexpr uint32_t kTx = 2u * (uint32_t)(MS * kTile + BH * kRowBytes);  // both CTAs
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kSt], empty[kSt], accf[NB], acce[NB];
+  __shared__ __align__(16) float col[2][2][BN];  // w_scale and bias of the tile's columns, by the tile's parity
+  __shared__ uint32_t tmem_base;
+  __shared__ int issued, consumed, failed;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t half = blockIdx.x & 1u;  // cluster rank; 0 is the pair's leader
+  const int pid = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
+  const int mt = (e.M + TR - 1) / TR, nt = (e.N + BN - 1) / BN;
+  const long long tiles = (long long)mt * nt;  // numbered M-fastest: row tiles of one W block side by side
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (tid == 0) {
+    for (int s = 0; s < kSt; ++s) {
+      mbar_init(&full[s], 1);   // (the leader's: its arrival + both CTAs' bytes)
+      mbar_init(&empty[s], 1);  // one commit from the leader's MMA thread
+    }
+    for (int b = 0; b < NB; ++b) {
+      mbar_init(&accf[b], 1);
+      mbar_init(&acce[b], 2 * kEpiWarps);  // (the leader's: the epilogue warps of both CTAs)
+    }
+    issued = consumed = failed = 0;
+    fence_mbar_init();
+    tc::prefetch_map(&tmX);
+    tc::prefetch_map(&tmW);
+  }
+  if (warp == 0) tc::alloc<2>(&tmem_base, 512);
+  tc::fence_before();
+  tc::cluster_sync();  // both CTAs' barriers and columns exist before any remote use
+  tc::fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {  // ---- TMA producer (both CTAs): own rows of x, own half of W's ----
+      int g = 0;
+      bool ok = true;
+      for (long long t = pid; t < tiles && ok; t += npairs) {
+        const int m0 = (int)(t % mt) * TR + (int)half * 128, n0 = (int)(t / mt) * BN + (int)half * BH;
+        for (int kb = 0; kb < KB; ++kb, ++g) {
+          const int s = g % kSt, use = g / kSt;
+          if (use > 0 && !mbar_wait_bounded(&empty[s], (uint32_t)((use - 1) & 1))) {
+            ok = false;
+            break;
+          }
+          uint8_t* a = smem + s * kSB;
+          if (half == 0) mbar_arrive_expect_tx(&full[s], kTx);
+          const uint32_t fb = tc::cluster_addr(&full[s], 0u);
+#pragma unroll
+          for (int ms = 0; ms < MS; ++ms) tc::tma_load_pair(a + ms * kTile, &tmX, kb * kElems, m0 + ms * 256, fb);
+          tc::tma_load_pair(a + MS * kTile, &tmW, kb * kElems, n0, fb);
+        }
+      }
+      issued = g;
+      if (!ok) failed = 1;
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && half == 0) {  // ---- MMA issuer: the leader only ----
+      int g = 0, i = -1, b = 0;
+      bool ok = true;
+      for (long long t = pid; t < tiles && ok; t += npairs) {
+        for (int kb = 0; kb < KB; ++kb, ++g) {
+          const bool first = LONG ? kb % kChunk == 0 : kb == 0;
+          if (first) {  // the next accumulator, once the epilogue has left it
+            ++i;
+            b = i % NB;
+            if (i >= NB && !tc::wait_cluster_bounded(&acce[b], (uint32_t)((i / NB - 1) & 1))) {
+              ok = false;
+              break;
+            }
+            tc::fence_after();
+          }
+          const int s = g % kSt;
+          if (!mbar_wait_bounded(&full[s], (uint32_t)((g / kSt) & 1))) {
+            ok = false;
+            break;
+          }
+          tc::fence_after();
+          const uint32_t a = smem_addr(smem + s * kSB), w = a + MS * kTile;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int ms = 0; ms < MS; ++ms)
+              tc::mma<2, F8>(tmem + (uint32_t)((b * MS + ms) * 256), tc::desc_sw128(a + ms * kTile + 32 * q, 16, 1024),
+                             tc::desc_sw128(w + 32 * q, 16, 1024), kId, !first || q != 0);
+          tc::commit<2>(tc::cluster_addr(&empty[s], 0u));  // the stage is free in both CTAs
+          tc::commit<2>(tc::cluster_addr(&empty[s], 1u));
+          if (kb == KB - 1 || (LONG && kb % kChunk == kChunk - 1)) {
+            tc::commit<2>(tc::cluster_addr(&accf[b], 0u));
+            tc::commit<2>(tc::cluster_addr(&accf[b], 1u));
+          }
+        }
+      }
+      consumed = g;
+      if (!ok) failed = 1;
+    }
+  } else {
+    // ---- epilogue: two warps per 32 tensor-memory lanes, half of the columns each ----
+    const int lg = warp & 3, et = tid - 64, ch = (warp - 2) >> 2;
+    int i = 0, turn = 0;
+    uint32_t limit = 2048;
+    auto complete = [&](int b) {  // accumulator b, in its turn
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&accf[b], (uint32_t)((turn / NB) & 1), limit))) {
+        failed = 1;  // (and on, since the other warps meet at the barrier below, but without waiting again)
+        limit = 1;
+      }
+      tc::fence_after();
+    };
+    auto release = [&](int b) {
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::arrive_remote(tc::cluster_addr(&acce[b], 0u));
+      ++turn;
+    };
+    for (long long t = pid; t < tiles; t += npairs, ++i) {
+      const int m0 = (int)(t % mt) * TR + (int)half * 128, n0 = (int)(t / mt) * BN;
+      float(*c)[BN] = col[i & 1];
+      if (et < BN) {
+        const int n = n0 + et;
+        c[0][et] = e.sw && n < e.N ? e.sw[n] : 1.f;
+        c[1][et] = e.bias && n < e.N ? bf16(e.bias + n) : 0.f;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+      int b = turn % NB;
+      complete(b);
+      if constexpr (LONG) {
+        float sum[BH];
+#pragma unroll
+        for (int k = 0; k < BH; ++k) sum[k] = 0.f;
+        for (int left = (KB + kChunk - 1) / kChunk - 1;; --left) {
+          const uint32_t at = tmem + (uint32_t)(b * 256 + ch * BH) + ((uint32_t)(lg * 32) << 16);
+#pragma unroll
+          for (int k = 0; k < BH; k += 16) {
+            uint32_t v[16];
+            tc::ld16(at + k, v);
+            tc::ld_wait(v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              sum[k + j] += __uint_as_float(v[j]);
+              v[j] = __float_as_uint(sum[k + j]);
+            }
+            if (left == 0) tc::st16(at + k, v);  // the whole sum, for the loop below
+          }
+          if (left == 0) break;
+          release(b);
+          b = turn % NB;
+          complete(b);
+        }
+        tc::st_wait();
+      }
+#pragma unroll 1
+      for (int ms = 0; ms < MS; ++ms) {
+        const long long m = m0 + ms * 256 + lg * 32 + lane;
+        const uint32_t at = tmem + (uint32_t)((b * MS + ms) * 256) + ((uint32_t)(lg * 32) << 16);
+        const float sx = e.sx && m < e.M ? e.sx[m] : 1.f;
+#pragma unroll 1
+        for (int k = ch * BH; k < (ch + 1) * BH; k += 16) {
+          uint32_t v[16];
+          tc::ld16(at + k, v);
+          tc::ld_wait(v);
+          if (m < e.M && n0 + k < e.N) finish16(e, m, n0 + k, v, sx, &c[0][k], &c[1][k]);
+        }
+      }
+      release(b);
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  if (tid == 0 && failed) {
+    atomicOr(flags, SV_FLAG_TIMEOUT);
+    if (half == 0)  // let the copies already issued land before the pair exits
+      for (int g = consumed; g < issued; ++g) (void)mbar_wait_bounded(&full[g % kSt], (uint32_t)((g / kSt) & 1), 64);
+  }
+  tc::cluster_sync();  // no CTA leaves while its peer may still signal or read it
+  tc::fence_after();
+  if (warp == 0) tc::dealloc<2>(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+struct Job {
+  const LinearLaunch* L;
+  Epilogue e;
+  int KB;
+  tc::EncodeTiledFn enc;
+  cudaStream_t st;
+};
+
+static void config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, long long grid, int threads, int cluster,
+                   int smem, cudaStream_t st) {
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3((unsigned)grid, 1, 1);
+  cfg->blockDim = dim3((unsigned)threads, 1, 1);
+  cfg->dynamicSmemBytes = (size_t)smem;
+  cfg->stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = cluster > 1 ? 2 : 1;
+}
+
+// x's map (boxes of x_rows rows) and W's (w_rows)
+static bool maps(const Job& j, bool f8, int x_rows, int w_rows, CUtensorMap* x, CUtensorMap* w, std::string* err) {
+  const LinearLaunch& L = *j.L;
+  const uint64_t es = f8 ? 1 : 2;
+  return tc::make_map(j.enc, x, f8, L.x, (uint64_t)L.K, (uint64_t)L.M, (uint64_t)L.ldx * es, (uint32_t)x_rows, err) &&
+         tc::make_map(j.enc, w, f8, L.W, (uint64_t)L.K, (uint64_t)L.N, (uint64_t)L.ldw * es, (uint32_t)w_rows, err);
+}
+
+// Sets the kernel's shared-memory limit, once per device.
+template <typename K>
+static bool prepared(K kernel, int smem, std::atomic<int>* cache, std::string* err) {
+  const int d = current_device();
+  if (d < 0) {
+    *err = "no current device (or its ordinal is too high)";
+    return false;
+  }
+  if (cache[d].load(std::memory_order_acquire)) return true;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) {
+    *err = std::string("linear attributes: ") + cudaGetErrorString(e);
+    return false;
+  }
+  cache[d].store(1, std::memory_order_release);
+  return true;
+}
+
+static int launched(cudaError_t e, std::string* err) {
+  if (e == cudaSuccess) return SV_OK;
+  *err = std::string("linear launch: ") + cudaGetErrorString(e);
+  return SV_ERR_CUDA;
+}
+
+template <int TM, bool F8>
+static int launch_rows(const Job& j, std::string* err) {
+  static std::atomic<int> cache[kMaxDevices];
+  using S = RowsShape<TM>;
+  auto k = rows_kernel<TM, F8>;
+  if (!prepared(k, S::kSmem, cache, err)) return SV_ERR_CUDA;
+  CUtensorMap x, w;
+  if (!maps(j, F8, TM, 128, &x, &w, err)) return SV_ERR_CUDA;
+  const long long tiles = (j.e.N + 127LL) / 128;
+  int split = 1;
+  while (split < 8 && ((tiles * split * 2 <= 2 * tc::num_sms() && j.KB >= 8 * split) || (j.e.out_f32 && j.KB > kChunk * split)))
+    split *= 2;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  config(&cfg, attr, tiles * split, kRowsThreads, split, S::kSmem, j.st);
+  return launched(cudaLaunchKernelEx(&cfg, k, x, w, j.e, j.KB, split, j.L->flags), err);
+}
+
+template <int BN, int MS, bool F8, bool LONG = false>
+static int launch_pair(const Job& j, std::string* err) {
+  static std::atomic<int> cache[kMaxDevices];
+  auto k = pair_kernel<BN, MS, F8, LONG>;
+  if (!prepared(k, kPairSmem, cache, err)) return SV_ERR_CUDA;
+  CUtensorMap x, w;
+  if (!maps(j, F8, 128, BN / 2, &x, &w, err)) return SV_ERR_CUDA;
+  const long long tiles = ((j.e.M + MS * 256LL - 1) / (MS * 256)) * ((j.e.N + BN - 1LL) / BN);
+  const long long pairs = tc::num_sms() / 2;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  config(&cfg, attr, 2 * (tiles < pairs ? tiles : pairs), kPairThreads, 2, kPairSmem, j.st);
+  return launched(cudaLaunchKernelEx(&cfg, k, x, w, j.e, j.KB, j.L->flags), err);
+}
+
+template <bool F8>
+static int dispatch(const Job& j, std::string* err) {
+  const int M = j.e.M, N = j.e.N;
+  if (!j.e.out_f32 || j.KB <= 8 * kChunk) {
+    if (M <= 16) return launch_rows<16, F8>(j, err);
+    if (M <= 32) return launch_rows<32, F8>(j, err);
+    if (M <= 64) return launch_rows<64, F8>(j, err);
+    if (M <= 128) return launch_rows<128, F8>(j, err);
+  }
+  // rows and columns of a tile: the fewest rounds over the pairs, weighted by the tile's size
+  const int widths[4] = {256, 224, 192, 128};
+  const long long pairs = tc::num_sms() / 2;
+  int bw = 256, bms = 1;
+  long long best = -1;
+  for (int ms = 1; ms <= 2; ++ms)
+    for (int w : widths) {
+      const long long tiles = ((M + ms * 256LL - 1) / (ms * 256)) * ((N + w - 1LL) / w);
+      const long long cost = ((tiles + pairs - 1) / pairs) * w * ms * 100 + w;
+      if (best < 0 || cost < best) {
+        best = cost;
+        bw = w;
+        bms = ms;
+      }
+    }
+  if (j.e.out_f32 && j.KB > kChunk) {
+    const long long tiles = ((M + 255LL) / 256) * ((N + 255LL) / 256);
+    return tiles >= pairs ? launch_pair<256, 1, F8, true>(j, err) : launch_pair<128, 1, F8, true>(j, err);
+  }
+  switch (bw * 2 + bms - 1) {
+    case 256 * 2: return launch_pair<256, 1, F8>(j, err);
+    case 256 * 2 + 1: return launch_pair<256, 2, F8>(j, err);
+    case 224 * 2: return launch_pair<224, 1, F8>(j, err);
+    case 224 * 2 + 1: return launch_pair<224, 2, F8>(j, err);
+    case 192 * 2: return launch_pair<192, 1, F8>(j, err);
+    case 192 * 2 + 1: return launch_pair<192, 2, F8>(j, err);
+    case 128 * 2: return launch_pair<128, 1, F8>(j, err);
+    default: return launch_pair<128, 2, F8>(j, err);
   }
 }
 
 }  // namespace lin
 
 int linear_launch(const LinearLaunch& L, std::string* err) {
-  const lin::Args a = {L.x, L.ldx, L.x_scale, L.W, L.ldw, L.w_scale, static_cast<const uint16_t*>(L.bias),
-                       L.residual, L.ldr, L.out, L.ldo, L.act, L.out_dtype == SV_F32 ? 1 : 0, L.M, L.N, L.K};
-  const long long tiles = ((L.M + 15LL) / 16) * ((L.N + 15LL) / 16);
-  if (tiles > 0x7fffffffLL) {
-    *err = "M * N too large";
-    return SV_ERR_SHAPE;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)tiles, 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = static_cast<cudaStream_t>(L.stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = L.in_dtype == SV_BF16
-                            ? cudaLaunchKernelEx(&cfg, lin::linear_kernel<uint16_t>, a)
-                            : cudaLaunchKernelEx(&cfg, lin::linear_kernel<__nv_fp8_e4m3>, a);
-  if (e != cudaSuccess) {
-    *err = std::string("linear launch: ") + cudaGetErrorString(e);
-    return SV_ERR_CUDA;
-  }
-  return SV_OK;
+  lin::Job j;
+  j.L = &L;
+  j.enc = tc::encoder(err);
+  if (!j.enc) return SV_ERR_CUDA;
+  const int es = L.in_dtype == SV_BF16 ? 2 : 1, os = L.out_dtype == SV_BF16 ? 2 : 4;
+  const bool vec = reinterpret_cast<uintptr_t>(L.out) % 16 == 0 && L.ldo * os % 16 == 0 &&
+                   (!L.residual || (reinterpret_cast<uintptr_t>(L.residual) % 16 == 0 && L.ldr * os % 16 == 0));
+  j.e = {L.x_scale, L.w_scale, static_cast<const uint16_t*>(L.bias), L.residual, L.ldr, L.out, L.ldo,
+         L.act, L.out_dtype == SV_F32 ? 1 : 0, L.M, L.N, vec ? 1 : 0};
+  j.KB = (int)(((long long)L.K * es + lin::kRowBytes - 1) / lin::kRowBytes);
+  j.st = static_cast<cudaStream_t>(L.stream);
+  return L.in_dtype == SV_BF16 ? lin::dispatch<false>(j, err) : lin::dispatch<true>(j, err);
 }
 
 }  // namespace sv
