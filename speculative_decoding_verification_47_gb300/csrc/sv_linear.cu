@@ -35,10 +35,24 @@ struct Epilogue {
   int vec;  // rows of out and residual start on 16-byte boundaries
 };
 
-__device__ __forceinline__ float silu(float z) { return z / (1.f + __expf(-z)); }
-__device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.f + erff(z * 0.70710678118654752f)); }
+__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+// The upper tail of the normal distribution, 1/2 erfc(|z| / sqrt 2), by the
+// rational approximation 7.1.26 of Abramowitz and Stegun's Handbook of
+// Mathematical Functions (error at most 1.5e-7): half of erff's instructions,
+// which a tile's epilogue does not hide (512 x 16384 x 4096: 50.8 us with erff).
+__device__ __forceinline__ float gelu(float z) {
+  const float a = fabsf(z) * 0.70710678118654752f, t = __fdividef(1.f, __fmaf_rn(0.3275911f, a, 1.f));
+  float p = __fmaf_rn(1.061405429f, t, -1.453152027f);
+  p = __fmaf_rn(p, t, 1.421413741f);
+  p = __fmaf_rn(p, t, -0.284496736f);
+  p = __fmaf_rn(p, t, 0.254829592f);
+  const float tail = 0.5f * p * t * ex2(-1.4426950408889634f * a * a);  // (z infinite: 0)
+  return z > 0.f ? z - z * tail : z * tail;
+}
+// z / 2 (1 + tanh u) = z / (1 + exp(-2u))
 __device__ __forceinline__ float gelu_tanh(float z) {
-  return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+  const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
+  return __fdividef(z, 1.f + __expf(-2.f * u));
 }
 
 // the activation of n values (one test of `act` for all of them)
@@ -61,17 +75,16 @@ __device__ __forceinline__ void activate(float (&z)[n], int act) {
 
 __device__ __forceinline__ float bf16(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
-// One output from its sum.
-__device__ __forceinline__ void finish(const Epilogue& e, long long m, int n, float acc, float sw, float bias) {
+// One output from its sum and its residual.
+__device__ __forceinline__ void finish(const Epilogue& e, long long m, int n, float acc, float sw, float bias,
+                                       float res) {
   float z[1] = {acc * (e.sx ? e.sx[m] : 1.f) * sw + bias};
   activate(z, e.act);
-  if (e.out_f32) {
-    if (e.res) z[0] += static_cast<const float*>(e.res)[m * e.ldr + n];
+  if (e.res) z[0] += res;
+  if (e.out_f32)
     static_cast<float*>(e.out)[m * e.ldo + n] = z[0];
-  } else {
-    if (e.res) z[0] += bf16(static_cast<const uint16_t*>(e.res) + m * e.ldr + n);
+  else
     static_cast<uint16_t*>(e.out)[m * e.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z[0]));
-  }
 }
 
 // The tensor cores add a product of one k step to the float32 accumulator by
@@ -191,13 +204,22 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       const float sw = e.sw && n < e.N ? e.sw[n] : 1.f, bias = e.bias && n < e.N ? bf16(e.bias + n) : 0.f;
 #pragma unroll 1
       for (int c = 0; c < TM && c < e.M; c += 16) {
+        float res[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const long long m = c + j;
+          res[j] = 0.f;
+          if (e.res && m < e.M && n < e.N)
+            res[j] = e.out_f32 ? static_cast<const float*>(e.res)[m * e.ldr + n]
+                               : bf16(static_cast<const uint16_t*>(e.res) + m * e.ldr + n);
+        }
         uint32_t v[16];
         tc::ld16(lanes + c, v);
         tc::ld_wait(v);
         if (n < e.N) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (c + j < e.M) finish(e, c + j, n, __uint_as_float(v[j]), sw, bias);
+            if (c + j < e.M) finish(e, c + j, n, __uint_as_float(v[j]), sw, bias, res[j]);
         }
       }
     }
@@ -214,18 +236,52 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       }
     }
     tc::cluster_sync();
-    // each CTA adds its share of the tile over the ranks, in rank order
+    // each CTA adds its share of the tile over the ranks, in rank order; kAtOnce
+    // outputs of a thread are in flight together (their residuals first)
+    constexpr int kAtOnce = 2;
     const uint32_t base = smem_addr(part);
-    for (int i = rank * kRowsThreads + tid; i < e.M * 128; i += split * kRowsThreads) {
-      const int nn = n0 + (i & 127);
-      if (nn >= e.N) continue;
-      float acc = 0.f;
-      for (int r = 0; r < split; ++r) {
+    const int nn = n0 + (tid & 63), step = split * (kRowsThreads / 64);  // a thread keeps two columns
+    float sw[2], bias[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sw[h] = e.sw && nn + 64 * h < e.N ? e.sw[nn + 64 * h] : 1.f;
+      bias[h] = e.bias && nn + 64 * h < e.N ? bf16(e.bias + nn + 64 * h) : 0.f;
+    }
+    for (int m = rank * (kRowsThreads / 64) + (tid >> 6); m < e.M; m += step * kAtOnce) {
+      float acc[kAtOnce][2], res[kAtOnce][2];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const long long mm = m + i * step;
+          acc[i][h] = res[i][h] = 0.f;
+          if (e.res && mm < e.M && nn + 64 * h < e.N)
+            res[i][h] = e.out_f32 ? static_cast<const float*>(e.res)[mm * e.ldr + nn + 64 * h]
+                                  : bf16(static_cast<const uint16_t*>(e.res) + mm * e.ldr + nn + 64 * h);
+        }
+      float of[kAtOnce][8][2];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
         uint32_t at;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + 4u * i), "r"(r));
-        acc += tc::ld_cluster(at);
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + 4u * (m * 128 + (tid & 63))), "r"(r < split ? r : 0));
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            of[i][r][h] = r < split && m + i * step < e.M ? tc::ld_cluster(at + 4u * (i * step * 128 + 64 * h)) : 0.f;
       }
-      finish(e, i >> 7, nn, acc, e.sw ? e.sw[nn] : 1.f, e.bias ? bf16(e.bias + nn) : 0.f);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) acc[i][h] += of[i][r][h];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (m + i * step < e.M)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (nn + 64 * h < e.N) finish(e, m + i * step, nn + 64 * h, acc[i][h], sw[h], bias[h], res[i][h]);
     }
     tc::cluster_sync();  // no CTA leaves while another reads its sums
   }
@@ -239,64 +295,134 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
 // ---------------------------------------------------------------------------
 constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 64 + 32 * kEpiWarps;
-constexpr int kPairSmem = 4 * 3 * kTile + 1024;  // 192 KB of stages
+constexpr int kPairRing = 12 * kTile;  // 192 KB
+constexpr int kOutStride = 17;         // floats: a row of 16 and one against bank conflicts
+constexpr int kPairSmem = kPairRing + kEpiWarps * 32 * kOutStride * 4 + 1024;
+constexpr int kBand = 8;
 
-template <int MS>
+template <int BN, int MS>
 struct PairShape {
-  static constexpr int kStageBytes = (MS + 1) * kTile;
-  static constexpr int kStages = (kPairSmem - 1024) / kStageBytes;  // 6 (MS 1) or 4 (MS 2)
+  static constexpr int kStageBytes = MS * kTile + BN / 2 * kRowBytes;
+  static constexpr int kStages = kPairRing / kStageBytes;  // 4 (512 x 256) to 8 (256 x 128)
   static constexpr int kBufs = 2 / MS;
 };
 
-// 16 columns of one row: scale, bias, activation, residual, store
-__device__ __forceinline__ void finish16(const Epilogue& e, long long m, int n, const uint32_t (&v)[16], float sx,
-                                         const float* sw, const float* bias) {
-  float z[16];
+// A chunk of W columns of this warp's 32 rows (one per lane, from row
+// m on), in two steps: the residual is asked for before the accumulator is waited
+// for.  Rows on 16-byte boundaries: every lane reads and writes its own row in
+// 16-byte words, whole 32-byte sectors.
+template <int W>
+struct RowChunk {
+  uint4 r[W / 4];  // (half of them for bf16)
+
+  __device__ __forceinline__ void ask(const Epilogue& e, long long m, int n) {
+    if (!e.res || m >= e.M) return;
+    if (e.out_f32) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(e.res) + m * e.ldr + n);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) z[j] = __fmaf_rn(__uint_as_float(v[j]), sx * sw[j], bias[j]);
-  activate(z, e.act);
-  const bool whole = e.vec && n + 16 <= e.N;
-  if (e.out_f32) {
-    float* o = static_cast<float*>(e.out) + m * e.ldo + n;
-    const float* r = e.res ? static_cast<const float*>(e.res) + m * e.ldr + n : nullptr;
-    if (whole) {
+      for (int q = 0; q < W / 4; ++q) r[q] = p[q];
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.res) + m * e.ldr + n);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r) a = reinterpret_cast<const float4*>(r)[q];
-        reinterpret_cast<float4*>(o)[q] =
-            make_float4(z[4 * q] + a.x, z[4 * q + 1] + a.y, z[4 * q + 2] + a.z, z[4 * q + 3] + a.w);
+      for (int q = 0; q < W / 8; ++q) r[q] = p[q];
+    }
+  }
+  __device__ __forceinline__ void put(const Epilogue& e, long long m, int n, float (&z)[W]) const {
+    if (m >= e.M) return;
+    if (e.out_f32) {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<float*>(e.out) + m * e.ldo + n);
+#pragma unroll
+      for (int q = 0; q < W / 4; ++q) {
+        if (e.res) {
+          z[4 * q] += __uint_as_float(r[q].x);
+          z[4 * q + 1] += __uint_as_float(r[q].y);
+          z[4 * q + 2] += __uint_as_float(r[q].z);
+          z[4 * q + 3] += __uint_as_float(r[q].w);
+        }
+        o[q] = make_uint4(__float_as_uint(z[4 * q]), __float_as_uint(z[4 * q + 1]), __float_as_uint(z[4 * q + 2]),
+                          __float_as_uint(z[4 * q + 3]));
       }
     } else {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + m * e.ldo + n);
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (n + j < e.N) o[j] = r ? z[j] + r[j] : z[j];
-    }
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(e.out) + m * e.ldo + n;
-    const uint16_t* r = e.res ? static_cast<const uint16_t*>(e.res) + m * e.ldr + n : nullptr;
-    if (whole) {
-      if (r) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint4 a = reinterpret_cast<const uint4*>(r)[q];
-          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+      for (int q = 0; q < W / 8; ++q) {
+        if (e.res) {
+          const uint32_t w[4] = {r[q].x, r[q].y, r[q].z, r[q].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             z[8 * q + 2 * j] += bf16_lo(w[j]);
             z[8 * q + 2 * j + 1] += bf16_hi(w[j]);
           }
         }
+        o[q] = make_uint4(tc::pack_bf16x2(z[8 * q], z[8 * q + 1]), tc::pack_bf16x2(z[8 * q + 2], z[8 * q + 3]),
+                          tc::pack_bf16x2(z[8 * q + 4], z[8 * q + 5]), tc::pack_bf16x2(z[8 * q + 6], z[8 * q + 7]));
       }
+    }
+  }
+};
+
+// Any other alignment, and a tile's ragged end: 16 columns of this warp's 32 rows,
+// which the lanes left in shared memory (`t`), two rows at a time with a lane per
+// column, so that a store still covers whole runs of a row.  o, r: this lane's
+// first element, `rows` rows above the matrix's end.
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ void narrow(float* p, float v) { *p = v; }
+__device__ __forceinline__ void narrow(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
+template <typename T>
+__device__ __noinline__ void put_by_columns(T* o, long long ldo, const T* r, long long ldr, int rows, const float* t) {
+  const int lane = threadIdx.x & 31;
+  t += (lane >> 4) * kOutStride + (lane & 15);
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        reinterpret_cast<uint4*>(o)[q] =
-            make_uint4(tc::pack_bf16x2(z[8 * q], z[8 * q + 1]), tc::pack_bf16x2(z[8 * q + 2], z[8 * q + 3]),
-                       tc::pack_bf16x2(z[8 * q + 4], z[8 * q + 5]), tc::pack_bf16x2(z[8 * q + 6], z[8 * q + 7]));
-    } else {
+  for (int h = 0; h < 32; h += 8) {
+    float a[4];
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (n + j < e.N) o[j] = __bfloat16_as_ushort(__float2bfloat16_rn(r ? z[j] + bf16(r + j) : z[j]));
+    for (int i = 0; i < 4; ++i) {
+      a[i] = t[(h + 2 * i) * kOutStride];
+      if (r) {
+        if (h + 2 * i < rows) a[i] += widen(*r);
+        r += 2 * ldr;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (h + 2 * i < rows) narrow(o, a[i]);
+      o += 2 * ldo;
+    }
+  }
+}
+
+// 16 columns from n on of this warp's rows: accumulator, scales, bias, activation,
+// residual, store.  rc holds the residual, if the rows are whole 16-byte words.
+__device__ __forceinline__ void chunk(const Epilogue& e, uint32_t at, long long m0, int n, float sx, const float* sw,
+                                      const float* bias, bool rows, const RowChunk<16>& rc, float* t) {
+  const long long m = m0 + (threadIdx.x & 31);
+  constexpr int W = 16;
+  uint32_t v[W];
+  tc::ld16(at, v);
+  tc::ld_wait(v);
+  float z[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) z[j] = __fmaf_rn(__uint_as_float(v[j]), sx * sw[j], bias[j]);
+  activate(z, e.act);
+  if (rows) {
+    rc.put(e, m, n, z);
+  } else {
+    __syncwarp();  // (the last chunk is read)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) t[(threadIdx.x & 31) * kOutStride + j] = z[j];
+    __syncwarp();
+    const int nl = n + (threadIdx.x & 15);
+    const long long ml = m0 + ((threadIdx.x >> 4) & 1);
+    const int left = e.M - ml < 32 ? (int)(e.M - ml) : 32;
+    if (nl < e.N) {
+      if (e.out_f32)
+        put_by_columns(static_cast<float*>(e.out) + ml * e.ldo + nl, e.ldo,
+                       e.res ? static_cast<const float*>(e.res) + ml * e.ldr + nl : nullptr, e.ldr, left, t);
+      else
+        put_by_columns(static_cast<uint16_t*>(e.out) + ml * e.ldo + nl, e.ldo,
+                       e.res ? static_cast<const uint16_t*>(e.res) + ml * e.ldr + nl : nullptr, e.ldr, left, t);
     }
   }
 }
@@ -307,7 +433,7 @@ template <int BN, int MS, bool F8, bool LONG>
 __global__ void __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Epilogue e,
                 int KB, uint32_t* flags) {
-  using PS = PairShape<MS>;
+  using PS = PairShape<BN, MS>;
   constexpr int kSt = PS::kStages, kSB = PS::kStageBytes, NB = PS::kBufs, BH = BN / 2, TR = MS * 256;
   constexpr uint32_t kId = tc::idesc(F8, false, 256, BN);
   constexpr int kElems = F8 ? 128 : 64;
@@ -322,7 +448,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t half = blockIdx.x & 1u;  // cluster rank; 0 is the pair's leader
   const int pid = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
   const int mt = (e.M + TR - 1) / TR, nt = (e.N + BN - 1) / BN;
-  const long long tiles = (long long)mt * nt;  // numbered M-fastest: row tiles of one W block side by side
+  const long long tiles = (long long)mt * nt;
+  // Tiles are numbered in bands of kBand row tiles, M-fastest inside a band, so
+  // that the tiles in flight share both operands' blocks.
+  const long long per_band = (long long)kBand * nt;
+  auto place = [&](long long t, int& tm, int& tn) {
+    const int bd = (int)(t / per_band), r0 = bd * kBand, h = mt - r0 < kBand ? mt - r0 : kBand;
+    const long long in = t - bd * per_band;
+    tm = r0 + (int)(in % h);
+    tn = (int)(in / h);
+  };
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (tid == 0) {
     for (int s = 0; s < kSt; ++s) {
@@ -351,7 +486,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int g = 0;
       bool ok = true;
       for (long long t = pid; t < tiles && ok; t += npairs) {
-        const int m0 = (int)(t % mt) * TR + (int)half * 128, n0 = (int)(t / mt) * BN + (int)half * BH;
+        int tm, tn;
+        place(t, tm, tn);
+        const int m0 = tm * TR + (int)half * 128, n0 = tn * BN + (int)half * BH;
         for (int kb = 0; kb < KB; ++kb, ++g) {
           const int s = g % kSt, use = g / kSt;
           if (use > 0 && !mbar_wait_bounded(&empty[s], (uint32_t)((use - 1) & 1))) {
@@ -412,6 +549,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else {
     // ---- epilogue: two warps per 32 tensor-memory lanes, half of the columns each ----
     const int lg = warp & 3, et = tid - 64, ch = (warp - 2) >> 2;
+    float* stage = reinterpret_cast<float*>(smem + kPairRing) + (warp - 2) * 32 * kOutStride;
     int i = 0, turn = 0;
     uint32_t limit = 2048;
     auto complete = [&](int b) {  // accumulator b, in its turn
@@ -428,12 +566,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       ++turn;
     };
     for (long long t = pid; t < tiles; t += npairs, ++i) {
-      const int m0 = (int)(t % mt) * TR + (int)half * 128, n0 = (int)(t / mt) * BN;
+      int tm, tn;
+      place(t, tm, tn);
+      const int m0 = tm * TR + (int)half * 128, n0 = tn * BN;
       float(*c)[BN] = col[i & 1];
       if (et < BN) {
         const int n = n0 + et;
         c[0][et] = e.sw && n < e.N ? e.sw[n] : 1.f;
         c[1][et] = e.bias && n < e.N ? bf16(e.bias + n) : 0.f;
+      }
+      if (e.res) {  // the tile's residual into L2 while the products run
+        const int es = e.out_f32 ? 4 : 2;
+#pragma unroll 1
+        for (int ms = 0; ms < MS; ++ms) {
+          const long long m = m0 + ms * 256 + lg * 32 + lane;
+          for (int k = ch * BH; m < e.M && k < (ch + 1) * BH && n0 + k < e.N; k += 128 / es)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(e.res) + (m * e.ldr + n0 + k) * es));
+        }
       }
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
       int b = turn % NB;
@@ -465,15 +614,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
 #pragma unroll 1
       for (int ms = 0; ms < MS; ++ms) {
-        const long long m = m0 + ms * 256 + lg * 32 + lane;
+        const long long row0 = m0 + ms * 256 + lg * 32, m = row0 + lane;
         const uint32_t at = tmem + (uint32_t)((b * MS + ms) * 256) + ((uint32_t)(lg * 32) << 16);
         const float sx = e.sx && m < e.M ? e.sx[m] : 1.f;
+        if (row0 >= e.M) break;
+        RowChunk<16> rc, next;  // the residual is asked for one chunk ahead
+        auto whole = [&](int k) { return e.vec && n0 + k + 16 <= e.N; };  // (the same in the whole warp)
+        if (whole(ch * BH)) next.ask(e, m, n0 + ch * BH);
 #pragma unroll 1
-        for (int k = ch * BH; k < (ch + 1) * BH; k += 16) {
-          uint32_t v[16];
-          tc::ld16(at + k, v);
-          tc::ld_wait(v);
-          if (m < e.M && n0 + k < e.N) finish16(e, m, n0 + k, v, sx, &c[0][k], &c[1][k]);
+        for (int k = ch * BH; k < (ch + 1) * BH && n0 + k < e.N; k += 16) {
+          rc = next;
+          if (k + 16 < (ch + 1) * BH && whole(k + 16)) next.ask(e, m, n0 + k + 16);
+          chunk(e, at + k, row0, n0 + k, sx, &c[0][k], &c[1][k], whole(k), rc, stage);
         }
       }
       release(b);
@@ -490,6 +642,208 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc::cluster_sync();  // no CTA leaves while its peer may still signal or read it
   tc::fence_after();
   if (warp == 0) tc::dealloc<2>(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Too few tiles for the card: `split` pairs of one cluster share a tile's K.
+// Each adds its k blocks in tensor memory, leaves the float32 sums in its ring
+// (which is idle by then), and finishes 128 / split rows of its half of the tile
+// over the pairs' sums, in rank order, read through distributed shared memory.
+// One pair alone walks K at 0.32 us a block: 256 x 4096 x 4096 took 27.2 us.
+// ---------------------------------------------------------------------------
+template <int BN, bool F8>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    split_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Epilogue e,
+                 int KB, int split, uint32_t* flags) {
+  constexpr int BH = BN / 2, kSB = kTile + BH * kRowBytes, kSt = kPairRing / kSB, kLd = BN + 4;
+  static_assert(128 * kLd * 4 <= kPairRing, "the sums fit over the ring");
+  constexpr uint32_t kId = tc::idesc(F8, false, 256, BN);
+  constexpr int kElems = F8 ? 128 : 64;
+  constexpr uint32_t kTx = 2u * kSB;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kSt], empty[kSt], done;
+  __shared__ uint32_t tmem_base;
+  __shared__ int issued, consumed, failed;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = blockIdx.x % (2 * split), half = rank & 1u, lead = rank & ~1u;
+  const int part = rank >> 1, tile = blockIdx.x / (2 * split), mt = (e.M + 255) / 256;
+  const int m0 = tile % mt * 256 + (int)half * 128, n0 = tile / mt * BN;
+  const int k_lo = (int)((long long)KB * part / split), k_hi = (int)((long long)KB * (part + 1) / split);
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (tid == 0) {
+    for (int s = 0; s < kSt; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    issued = consumed = failed = 0;
+    fence_mbar_init();
+    tc::prefetch_map(&tmX);
+    tc::prefetch_map(&tmW);
+  }
+  if (warp == 0) tc::alloc<2>(&tmem_base, 256);
+  tc::fence_before();
+  tc::cluster_sync();
+  tc::fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int g = 0;
+      for (int kb = k_lo; kb < k_hi; ++kb, ++g) {
+        const int s = g % kSt, use = g / kSt;
+        if (use > 0 && !mbar_wait_bounded(&empty[s], (uint32_t)((use - 1) & 1))) {
+          failed = 1;
+          break;
+        }
+        uint8_t* a = smem + s * kSB;
+        if (half == 0) mbar_arrive_expect_tx(&full[s], kTx);
+        const uint32_t fb = tc::cluster_addr(&full[s], lead);
+        tc::tma_load_pair(a, &tmX, kb * kElems, m0, fb);
+        tc::tma_load_pair(a + kTile, &tmW, kb * kElems, n0 + (int)half * BH, fb);
+      }
+      issued = g;
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && half == 0) {
+      int g = 0;
+      for (int kb = k_lo; kb < k_hi; ++kb, ++g) {
+        const int s = g % kSt;
+        if (!mbar_wait_bounded(&full[s], (uint32_t)((g / kSt) & 1))) {
+          failed = 1;
+          break;
+        }
+        tc::fence_after();
+        const uint32_t a = smem_addr(smem + s * kSB), w = a + kTile;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          tc::mma<2, F8>(tmem, tc::desc_sw128(a + 32 * q, 16, 1024), tc::desc_sw128(w + 32 * q, 16, 1024), kId,
+                         (g | q) != 0);
+        tc::commit<2>(tc::cluster_addr(&empty[s], lead));
+        tc::commit<2>(tc::cluster_addr(&empty[s], lead + 1));
+      }
+      consumed = g;
+      tc::commit<2>(tc::cluster_addr(&done, lead));
+      tc::commit<2>(tc::cluster_addr(&done, lead + 1));
+    }
+  }
+  __syncwarp();
+  if (!mbar_wait_bounded(&done, 0)) failed = 1;
+  tc::fence_after();
+  __syncthreads();
+  if (tid == 0 && failed) {
+    atomicOr(flags, SV_FLAG_TIMEOUT);
+    if (half == 0)  // let the copies already issued land
+      for (int g = consumed; g < issued; ++g) (void)mbar_wait_bounded(&full[g % kSt], (uint32_t)((g / kSt) & 1), 64);
+  }
+  tc::cluster_sync();  // (both halves' copies have landed: the ring may be written)
+  tc::fence_after();
+  float* sums = reinterpret_cast<float*>(smem);  // [128][kLd]
+  if (warp >= 2) {
+    const int lg = warp & 3, ch = (warp - 2) >> 2;
+    float* row = sums + (lg * 32 + lane) * kLd;
+#pragma unroll 1
+    for (int k = ch * BH; k < (ch + 1) * BH; k += 16) {
+      uint32_t v[16];
+      tc::ld16(tmem + ((uint32_t)(lg * 32) << 16) + k, v);
+      tc::ld_wait(v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(row + k + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    }
+  }
+  tc::fence_before();
+  tc::cluster_sync();
+  const int rows = 128 / split, r0 = part * rows;
+  const uint32_t base = smem_addr(sums);
+  const int c = (tid % (BN / 4)) * 4, n = n0 + c;  // four columns of a thread
+  constexpr int kLanes = kPairThreads / (BN / 4);   // rows at a time
+  float sw[4], bias[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    sw[j] = e.sw && n + j < e.N ? e.sw[n + j] : 1.f;
+    bias[j] = e.bias && n + j < e.N ? bf16(e.bias + n + j) : 0.f;
+  }
+  const bool whole = e.vec && n + 4 <= e.N;
+#pragma unroll 2
+  for (int r = tid / (BN / 4); r < rows; r += kLanes) {
+    const long long m = m0 + r0 + r;
+    if (m >= e.M || n >= e.N) break;
+    float res[4] = {0.f, 0.f, 0.f, 0.f};
+    if (e.res) {
+      if (e.out_f32) {
+        const float* p = static_cast<const float*>(e.res) + m * e.ldr + n;
+        if (whole) {
+          const float4 a = *reinterpret_cast<const float4*>(p);
+          res[0] = a.x, res[1] = a.y, res[2] = a.z, res[3] = a.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n + j < e.N) res[j] = p[j];
+        }
+      } else {
+        const uint16_t* p = static_cast<const uint16_t*>(e.res) + m * e.ldr + n;
+        if (whole) {
+          const uint2 a = *reinterpret_cast<const uint2*>(p);
+          res[0] = bf16_lo(a.x), res[1] = bf16_hi(a.x), res[2] = bf16_lo(a.y), res[3] = bf16_hi(a.y);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n + j < e.N) res[j] = bf16(p + j);
+        }
+      }
+    }
+    float of[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) of[q][j] = 0.f;
+      if (q < split) {
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at)
+                     : "r"(base + 4u * ((r0 + r) * kLd + c)), "r"(2 * q + (int)half));
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(of[q][0]), "=f"(of[q][1]), "=f"(of[q][2]), "=f"(of[q][3])
+                     : "r"(at)
+                     : "memory");
+      }
+    }
+    const float sx = e.sx ? e.sx[m] : 1.f;
+    float z[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      z[j] = __fmaf_rn(((of[0][j] + of[1][j]) + of[2][j]) + of[3][j], sx * sw[j], bias[j]);
+    activate(z, e.act);
+    if (e.res) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] += res[j];
+    }
+    if (e.out_f32) {
+      float* o = static_cast<float*>(e.out) + m * e.ldo + n;
+      if (whole) {
+        *reinterpret_cast<float4*>(o) = make_float4(z[0], z[1], z[2], z[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < e.N) o[j] = z[j];
+      }
+    } else {
+      uint16_t* o = static_cast<uint16_t*>(e.out) + m * e.ldo + n;
+      if (whole) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(tc::pack_bf16x2(z[0], z[1]), tc::pack_bf16x2(z[2], z[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < e.N) o[j] = __bfloat16_as_ushort(__float2bfloat16_rn(z[j]));
+      }
+    }
+  }
+  tc::cluster_sync();  // no CTA leaves while another reads its sums
+  tc::fence_after();
+  if (warp == 0) tc::dealloc<2>(tmem, 256);
 }
 
 // ---------------------------------------------------------------------------
@@ -585,24 +939,74 @@ static int launch_pair(const Job& j, std::string* err) {
   return launched(cudaLaunchKernelEx(&cfg, k, x, w, j.e, j.KB, j.L->flags), err);
 }
 
+// Clusters of 2 * split CTAs that fit the card at once (15 of 8, 36 of 4 measured).
+template <int BN, bool F8>
+static int split_clusters(int split) {
+  static std::atomic<int> cache[2][kMaxDevices];  // clusters + 1
+  const int d = current_device();
+  if (d < 0) return 0;
+  std::atomic<int>& slot = cache[split == 4][d];
+  int n = slot.load(std::memory_order_acquire) - 1;
+  if (n < 0) {
+    auto k = split_kernel<BN, F8>;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    config(&cfg, attr, 2 * split, kPairThreads, 2 * split, kPairRing + 1024, nullptr);
+    n = 0;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairRing + 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess)
+      n = 0;
+    slot.store(n + 1, std::memory_order_release);
+  }
+  return n;
+}
+
+template <int BN, bool F8>
+static int launch_split(const Job& j, int split, std::string* err) {
+  static std::atomic<int> cache[kMaxDevices];
+  auto k = split_kernel<BN, F8>;
+  if (!prepared(k, kPairRing + 1024, cache, err)) return SV_ERR_CUDA;
+  CUtensorMap x, w;
+  if (!maps(j, F8, 128, BN / 2, &x, &w, err)) return SV_ERR_CUDA;
+  const long long tiles = ((j.e.M + 255LL) / 256) * ((j.e.N + BN - 1LL) / BN);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  config(&cfg, attr, 2 * split * tiles, kPairThreads, 2 * split, kPairRing + 1024, j.st);
+  return launched(cudaLaunchKernelEx(&cfg, k, x, w, j.e, j.KB, split, j.L->flags), err);
+}
+
 template <bool F8>
 static int dispatch(const Job& j, std::string* err) {
   const int M = j.e.M, N = j.e.N;
+  const long long pairs = tc::num_sms() / 2;
   if (!j.e.out_f32 || j.KB <= 8 * kChunk) {
     if (M <= 16) return launch_rows<16, F8>(j, err);
     if (M <= 32) return launch_rows<32, F8>(j, err);
     if (M <= 64) return launch_rows<64, F8>(j, err);
     if (M <= 128) return launch_rows<128, F8>(j, err);
   }
-  // rows and columns of a tile: the fewest rounds over the pairs, weighted by the tile's size
+  // fewer tiles than half of the pairs, and K long enough to be worth the exchange
+  const long long t256 = ((M + 255LL) / 256) * ((N + 255LL) / 256), t128 = ((M + 255LL) / 256) * ((N + 127LL) / 128);
+  for (int split = 4; split >= 2; split /= 2) {
+    if (j.KB < 8 * split || (j.e.out_f32 && j.KB > kChunk * split)) continue;
+    if (t128 <= split_clusters<128, F8>(split)) return launch_split<128, F8>(j, split, err);
+    if (t256 <= split_clusters<256, F8>(split)) return launch_split<256, F8>(j, split, err);
+  }
+  // Rows (ms x 256) and columns of a tile, by the clocks that they would take: a
+  // k block costs the MMAs' 2 ms BN, but no less than a slot's turn through the
+  // ring (3650 over the slots, measured: 0.32 us a block for 256 x 128 and for
+  // 256 x 256 tiles in 6 slots, 0.47 for 512 x 128 in 4); an epilogue costs 20 a
+  // column and sub-tile, once a round where the accumulators fill tensor memory
+  // (ms = 2) and else once in all.
   const int widths[4] = {256, 224, 192, 128};
-  const long long pairs = tc::num_sms() / 2;
   int bw = 256, bms = 1;
   long long best = -1;
   for (int ms = 1; ms <= 2; ++ms)
     for (int w : widths) {
       const long long tiles = ((M + ms * 256LL - 1) / (ms * 256)) * ((N + w - 1LL) / w);
-      const long long cost = ((tiles + pairs - 1) / pairs) * w * ms * 100 + w;
+      const long long rounds = (tiles + pairs - 1) / pairs, slots = kPairRing / (ms * kTile + w / 2 * kRowBytes);
+      const long long block = 2 * ms * w > 3650 / slots ? 2 * ms * w : 3650 / slots;
+      const long long cost = rounds * block * j.KB + (ms == 2 ? rounds : 1) * 20 * ms * w;
       if (best < 0 || cost < best) {
         best = cost;
         bw = w;
