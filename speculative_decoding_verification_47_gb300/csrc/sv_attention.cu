@@ -1,89 +1,866 @@
-// Attention of a round's query positions over a shared prefix and the paged
-// cache of each sequence's own tokens: one warp per query row, one pass with
-// the running maximum and sum of the softmax.
+// Attention of a round's query positions over a prefix that the whole batch
+// shares and over each sequence's own tokens in a paged cache.
+//
+//   out = sum_j exp(s_j) v_j / sum_j exp(s_j),  s_j = scale q . k_j
+//
+// A softmax over a set of keys splits into softmaxes over parts of it: with the
+// part's maximum m_p, l_p = sum exp(s - m_p) and o_p = sum exp(s - m_p) v,
+//   out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p   (m in base 2, M the largest m_p).
+// So the prefix is one matrix product for ALL query rows of a key head (rows
+// (sequence, position, head of the group), 256 to an item), and only the own
+// tokens are read per sequence.
+//
+// Three kernels on the caller's stream, chained by programmatic launches:
+//  1. plan_kernel: lengths and draft counts live on the device, so the list of
+//     items does too: compact query rows, chunks of long sequences, splits of the
+//     prefix, sized so that the card is filled and the partial results stay bounded.
+//  2. part_kernel: persistent, one CTA per SM.  An item is up to 256 query rows
+//     (two streams of 128) over a run of keys in tiles of 128: S = Q K^T and
+//     O += P V with tcgen05, S, P and O in tensor memory, K and V through a ring of
+//     tiles in shared memory filled by 16-byte asynchronous copies row by row (a
+//     page may have any size and stride, and rows past the end become zeros).
+//     With 128 rows or fewer the two streams take alternate key tiles instead.
+//  3. merge_kernel: the parts of each row, in a fixed order, to out and lse.
 #include <cstdint>
 
-#include "sv_common.cuh"
 #include "sv_internal.h"
+#include "sv_tc.cuh"
 
 namespace sv {
 namespace att {
 
-__global__ void clear_kernel(uint32_t* flags) {
+constexpr int kTileKeys = 128;
+constexpr int kItemRows = 256;
+constexpr int kMaxGrid = 160;  // CTAs that the partial results are sized for
+constexpr int kSlack = 4;      // items per CTA that splitting aims at
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Workspace header (32-bit words); word 0 is the flag word.
+enum { H_FLAGS, H_BAD_PREFIX, H_NEXT_PRE, H_NEXT_OWN, H_QUERIES, H_CHUNKS, H_CHUNK_KEYS, H_SPLITS, H_SPLIT_TILES,
+       H_PRE_ITEMS, H_OWN_ITEMS, H_PRE_CTAS, H_WORDS = 64 };
+
+struct Layout {  // byte offsets into the workspace
+  size_t qrow, qoff, coff, chunk_of, stat, nan_from, pre_ml, pre_o, extra_ml, extra_o, own_ml, own_o, total;
+  long long pre_rows, extra_rows, own_slots;
+};
+
+__host__ inline Layout layout(int B, int K, int Hq, int Hkv, int D, long long prefix_len, long long max_own) {
+  Layout w;
+  const long long Q = (long long)B * (K + 1), G = Hq / Hkv, own_rows = (K + 1) * G;
+  const long long ptiles = (prefix_len + kTileKeys - 1) / kTileKeys;
+  const long long rt = (own_rows + kItemRows - 1) / kItemRows;
+  // splits * items <= items + kSlack * grid, and a split has a tile at least
+  const long long by_items = Q * Hq + (long long)kSlack * kMaxGrid * kItemRows, by_tiles = ptiles * Q * Hq;
+  w.pre_rows = by_items < by_tiles ? by_items : by_tiles;
+  const long long e_items = (long long)Hkv + kSlack * kMaxGrid, e_tiles = ptiles * Hkv;
+  w.extra_rows = 128 * (e_items < e_tiles ? e_items : e_tiles);
+  const long long c_items = B + (long long)kSlack * kMaxGrid / (Hkv * rt) + 1,
+                  c_tiles = B * ((max_own + 2 * kTileKeys - 1) / (2 * kTileKeys));
+  w.own_slots = (c_items < c_tiles ? c_items : c_tiles) * Hkv * 2;
+  size_t at = H_WORDS * 4;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = (at + bytes + 255) / 256 * 256;
+    return here;
+  };
+  w.qrow = take((size_t)Q * 4);
+  w.qoff = take((size_t)B * 4);
+  w.coff = take((size_t)B * 4);
+  w.chunk_of = take((size_t)(w.own_slots / (2 * Hkv)) * 4);
+  w.stat = take((size_t)B * 4);
+  w.nan_from = take((size_t)B * Hkv * 4);
+  w.pre_ml = take((size_t)w.pre_rows * 8);
+  w.pre_o = take((size_t)w.pre_rows * D * 4);
+  w.extra_ml = take((size_t)w.extra_rows * 8);
+  w.extra_o = take((size_t)w.extra_rows * D * 4);
+  w.own_ml = take((size_t)w.own_slots * own_rows * 8);
+  w.own_o = take((size_t)w.own_slots * own_rows * D * 4);
+  w.total = at;
+  return w;
+}
+
+struct Args {
+  AttentionLaunch a;
+  int G, Q, row_tiles, grid;  // heads per key head, K + 1, item tiles of a sequence's rows, CTAs of part_kernel
+  uint32_t* head;
+  int* qrow;      // compact query -> b * Q + i
+  int* qoff;      // first compact query of a sequence
+  int* coff;      // first chunk of a sequence
+  int* chunk_of;  // chunk -> sequence
+  int* stat;      // a sequence's flags
+  int* nan_from;  // [B][Hkv] first own token whose drafted value is not finite
+  float2 *pre_ml, *extra_ml, *own_ml;
+  float *pre_o, *extra_o, *own_o;
+  long long own_slots;
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// ---------------------------------------------------------------------------
+// 1. The plan: one CTA.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+// Inclusive prefix sum over the CTA (also the total).
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  int s = warp_sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const int before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return v + (warp > 0 ? before : 0);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
+  __shared__ int warp_sums[32];
+  __shared__ unsigned long long tiles2;  // of 2 * kTileKeys keys, all sequences
+  __shared__ unsigned flags;
+  const AttentionLaunch& a = p.a;
+  const int t = threadIdx.x;
+  if (t == 0) {
+    tiles2 = 0;
+    flags = 0;
+  }
+  pdl_launch_dependents();
   pdl_wait();
-  *flags = 0u;
+  __syncthreads();
+  const int step = 2 * kTileKeys;
+  auto look = [&](int b, int& k, int& len) {  // 0 or the sequence's flag
+    k = a.kpr ? a.kpr[b] : a.K;
+    len = a.lens[b];
+    if (k < 0 || k > a.K) return (int)SV_FLAG_BAD_K;
+    if (len < 0 || (long long)len + k > (long long)a.max_pages * a.page_size) return (int)SV_FLAG_BAD_N;
+    return 0;
+  };
+  unsigned long long mine = 0;
+  for (int b = t; b < a.B; b += kPlanThreads) {
+    int k, len;
+    const int bad = look(b, k, len);
+    p.stat[b] = bad;
+    if (bad)
+      atomicOr(&flags, (unsigned)bad);
+    else
+      mine += (unsigned)ceil_div(len + k, step);
+    for (int h = 0; h < a.Hkv; ++h) p.nan_from[(long long)b * a.Hkv + h] = 0x7fffffff;
+  }
+  if (mine) atomicAdd(&tiles2, mine);
+  __syncthreads();
+  // a chunk: long enough that all chunks together are at most kSlack per CTA beside one per sequence
+  const unsigned long long units = tiles2 * (unsigned)(a.Hkv * p.row_tiles), aim = (unsigned long long)kSlack * p.grid;
+  const int per = units > aim ? (int)((units + aim - 1) / aim) : 1;  // steps of a chunk
+  int queries = 0, chunks = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + t;
+    int k = 0, len = 0, q = 0, n = 0;
+    if (b < a.B && look(b, k, len) == 0) {
+      q = k + 1;
+      n = ceil_div(ceil_div(len + k, step), per);
+    }
+    int total;
+    const int qe = queries + block_scan(q, warp_sums, total) - q;
+    queries += total;
+    const int ce = chunks + block_scan(n, warp_sums, total) - n;
+    chunks += total;
+    if (b < a.B) {
+      p.qoff[b] = qe;
+      p.coff[b] = ce;
+    }
+    for (int i = 0; i < q; ++i) p.qrow[qe + i] = b * p.Q + i;
+    for (int c = 0; c < n; ++c) p.chunk_of[ce + c] = b;
+  }
+  if (t == 0) {
+    const int ptiles = ceil_div(a.prefix_len, kTileKeys);
+    const long long rows = (long long)queries * p.G;
+    const int row_items = (int)((rows + kItemRows - 1) / kItemRows) * a.Hkv;
+    int splits = 0, split_tiles = 0;
+    if (ptiles > 0 && row_items > 0) {
+      // work in units of one stream's tile; an item is to be a kSlack-th of a CTA's share
+      const double work = 2.0 * row_items * ptiles + 2.0 * (double)units;
+      const double share = work / p.grid / kSlack;
+      split_tiles = share >= 2.0 * ptiles ? ptiles : (int)(share / 2.0);
+      const int most = kSlack * p.grid / row_items;  // (what the partial results have room for)
+      const int least = ceil_div(ptiles, most < 1 ? 1 : most);
+      if (split_tiles < least) split_tiles = least;
+      splits = ceil_div(ptiles, split_tiles);
+      p.head[H_PRE_CTAS] = (unsigned)(p.grid * (2.0 * row_items * ptiles / work) + 0.5);
+    } else {
+      p.head[H_PRE_CTAS] = 0;
+    }
+    p.head[H_BAD_PREFIX] = p.head[H_NEXT_PRE] = p.head[H_NEXT_OWN] = 0;
+    p.head[H_QUERIES] = queries;
+    p.head[H_CHUNKS] = chunks;
+    p.head[H_CHUNK_KEYS] = per * step;
+    p.head[H_SPLITS] = splits;
+    p.head[H_SPLIT_TILES] = split_tiles;
+    p.head[H_PRE_ITEMS] = row_items * splits;
+    p.head[H_OWN_ITEMS] = chunks * a.Hkv * p.row_tiles;
+    p.head[H_FLAGS] = flags;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 2. The parts.
+// ---------------------------------------------------------------------------
+constexpr int kThreads = 384;  // warps 0-3, 4-7: softmax of stream 0, 1; 8: MMA; 9-11: loads
+constexpr int kLoaders = 3;
+constexpr int kSlots = 5;
+constexpr uint32_t kColS = 0, kColO = 256, kStreamCols = 128;
+
+template <int D>
+struct Shape {
+  static constexpr int kHalves = D / 64;                  // 128-byte columns of a row
+  static constexpr int kTileBytes = kTileKeys * D * 2;    // K, V or one stream's Q
+  static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + 1024;
+};
+
+struct Item {
+  int kind;  // 0 prefix, 1 own, -1 none left
+  int h, b;  // key head; sequence (own)
+  int row0, rows;    // first row (compact for the prefix, the sequence's for own) and count, at most 256
+  int key0, keys;    // first key and number of keys, prefix or own positions
+  int tiles;
+  int slot;          // split (prefix) or chunk (own)
+  int len;           // own: committed tokens
+  __device__ __forceinline__ bool pair() const { return rows > 128; }  // streams: two row tiles, or alternate key tiles
+  __device__ __forceinline__ int ahead() const { return pair() ? 1 : 2; }
+  __device__ __forceinline__ int stream_tiles(int s) const { return pair() ? tiles : (tiles + 1 - s) / 2; }
+};
+
+__device__ __forceinline__ Item decode(const Args& p, int kind, int idx) {
+  const AttentionLaunch& a = p.a;
+  Item it;
+  it.kind = kind;
+  it.b = it.len = 0;
+  if (kind == 0) {
+    // row tiles fastest: the items in flight share the keys' tiles in L2
+    const int queries = p.head[H_QUERIES], per = p.head[H_SPLIT_TILES];
+    const int row_items = (int)(((long long)queries * p.G + kItemRows - 1) / kItemRows);
+    it.row0 = idx % row_items * kItemRows;
+    it.h = idx / row_items % a.Hkv;
+    it.slot = idx / row_items / a.Hkv;
+    const long long left = (long long)queries * p.G - it.row0;
+    it.rows = left < kItemRows ? (int)left : kItemRows;
+    it.key0 = it.slot * per * kTileKeys;
+    const int end = a.prefix_len - it.key0;
+    it.keys = end < per * kTileKeys ? end : per * kTileKeys;
+  } else {
+    const int keys = p.head[H_CHUNK_KEYS];
+    const int rt = idx % p.row_tiles;
+    it.h = idx / p.row_tiles % a.Hkv;
+    it.slot = idx / p.row_tiles / a.Hkv;
+    it.b = p.chunk_of[it.slot];
+    const int k = a.kpr ? a.kpr[it.b] : a.K;
+    it.len = a.lens[it.b];
+    it.row0 = rt * kItemRows;
+    const int left = (k + 1) * p.G - it.row0;
+    it.rows = left < kItemRows ? left : kItemRows;
+    it.key0 = (it.slot - p.coff[it.b]) * keys;
+    const int end = it.len + k - it.key0;
+    it.keys = end < keys ? end : keys;
+    if (it.rows <= 0) it.keys = 0;  // (a sequence with fewer row tiles than the largest)
+  }
+  it.tiles = it.keys > 0 ? ceil_div(it.keys, kTileKeys) : 0;
+  return it;
+}
+
+// Next item for this CTA: from its preferred list until that is empty, then from the other.
+struct Feed {
+  int list, left;
+  __device__ __forceinline__ int2 next(const Args& p) {
+    while (left > 0) {
+      const int i = (int)atomicAdd(&p.head[list ? H_NEXT_OWN : H_NEXT_PRE], 1u);
+      if (i < (int)p.head[list ? H_OWN_ITEMS : H_PRE_ITEMS]) return make_int2(list, i);
+      list ^= 1;
+      --left;
+    }
+    return make_int2(-1, 0);
+  }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// bf16 pairs with an exponent of all ones (infinity or NaN)
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) rows_kernel(const AttentionLaunch a, uint32_t* flags) {
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int Q = a.K + 1, G = a.Hq / a.Hkv;
-  if (row >= (long long)a.B * Q * a.Hq) return;
-  const int h = (int)(row % a.Hq), i = (int)(row / a.Hq % Q), b = (int)(row / a.Hq / Q);
-  const int k = a.kpr ? a.kpr[b] : a.K, len = a.lens[b];
-  uint32_t bad = 0;
-  if (k < 0 || k > a.K) bad = SV_FLAG_BAD_K;
-  else if (i > k) return;
-  else if (len < 0 || (long long)len + k > (long long)a.max_pages * a.page_size) bad = SV_FLAG_BAD_N;
-  const uint16_t* K_ = static_cast<const uint16_t*>(a.k) + (h / G) * a.head;
-  const uint16_t* V_ = static_cast<const uint16_t*>(a.v) + (h / G) * a.head;
-  constexpr int E = D / 32;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  const uint16_t* qp = static_cast<const uint16_t*>(a.q) + b * a.q_seq + i * a.q_pos + h * a.q_head + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __uint_as_float((uint32_t)qp[e] << 16);
-    o[e] = 0.f;
-  }
-  const int P = a.prefix_len;
-  const int total = bad ? 0 : P + len + k;  // every key of the sequence: pages are checked for all of them
-  for (int j = 0; j < total; ++j) {
-    const int t = j < P ? j : j - P;
-    const int page = j < P ? a.prefix_pages[t / a.page_size] : a.table[(long long)b * a.max_pages + t / a.page_size];
-    if (page < 0 || page >= a.num_pages) {
-      bad |= SV_FLAG_BAD_PAGE;
-      continue;
+__global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
+  using S = Shape<D>;
+  constexpr uint32_t kIdS = tc::idesc(false, false, 128, kTileKeys), kIdO = tc::idesc(false, true, 128, D);
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], p_ready[2], o_full[2],
+      item_full[2], item_empty[2];
+  __shared__ int2 items[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed;
+  const AttentionLaunch& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t q_smem = smem_addr(smem), ring = q_smem + 2 * S::kTileBytes;
+  if (tid == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], 32);
+      mbar_init(&empty[s], 1);
     }
-    if (j >= P + len + i) continue;
-    const long long at = page * a.page + (t % a.page_size) * a.token + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += q[e] * __uint_as_float((uint32_t)K_[at + e] << 16);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale;
-    const float nm = s > m ? s : m;
-    const float c = nm == -INFINITY ? 1.f : __expf(m - nm), p = nm == -INFINITY ? 0.f : __expf(s - nm);
-    l = l * c + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * __uint_as_float((uint32_t)V_[at + e] << 16);
-    m = nm;
+    mbar_init(&q_full, 32 * kLoaders);
+    mbar_init(&q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_ready[s], 128);
+      mbar_init(&o_full[s], 1);
+      mbar_init(&item_full[s], 1);
+      mbar_init(&item_empty[s], 8 + 1 + kLoaders);  // a lane of every warp
+    }
+    failed = 0;
+    fence_mbar_init();
   }
-  uint16_t* op = static_cast<uint16_t*>(a.out) + b * a.o_seq + i * a.o_pos + h * a.o_head + lane * E;
-  const float nan = __int_as_float(0x7fffffff);
+  if (warp == 8) tc::alloc<1>(&tmem_base, 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // The items pass through two slots, written by the first loader warp.
+  auto fetch = [&](int n) {  // item n of this CTA, read by a whole warp
+    int2 got = make_int2(-1, 0);
+    const bool ok = mbar_wait_bounded(&item_full[n & 1], (uint32_t)((n >> 1) & 1));
+    if (__all_sync(0xffffffffu, ok)) got = items[n & 1];
+    else failed = 1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[n & 1]);
+    return got;
+  };
+  auto wait = [&](uint64_t* bar, int phase) {
+    if (mbar_wait_bounded(bar, (uint32_t)(phase & 1))) return true;
+    failed = 1;
+    return false;
+  };
+
+  if (warp >= 9) {
+    // ---- loads: Q rows by all three warps, K and V tiles in turn ----
+    const int w = warp - 9;
+    Feed feed;
+    feed.left = 2;
+    feed.list = (int)blockIdx.x < (int)p.head[H_PRE_CTAS] ? 0 : 1;
+    int turn = 0, live = 0;  // tiles of the ring so far (all warps), items with any
+    int pending = -1;  // the slot of this warp's last tile, not yet announced
+    bool ok = true;
+    auto announce = [&]() {
+      if (pending < 0) return;
+      fence_async();
+      mbar_arrive(&full[pending]);
+      pending = -1;
+    };
+    for (int n = 0; ok; ++n) {
+      if (w == 0) {
+        if (n >= 2 && !__all_sync(0xffffffffu, wait(&item_empty[n & 1], (n >> 1) - 1))) break;
+        if (lane == 0) {
+          items[n & 1] = feed.next(p);
+          mbar_arrive(&item_full[n & 1]);
+        }
+        __syncwarp();
+      }
+      const int2 got = fetch(n);
+      if (got.x < 0) break;
+      const Item it = decode(p, got.x, got.y);
+      if (it.tiles == 0) continue;  // (in every role)
+      // K and V tiles: K_0 .. K_{d-1}, then V_j, K_{j+d}
+      const int d = it.ahead();
+      const int total = 2 * it.tiles;
+      int q_done = 0;
+      for (int x = -1; x < total && ok; ++x) {
+        if (x < 0) {  // Q first (its place frees with the last item's last S)
+          ok = __all_sync(0xffffffffu, wait(&q_empty, live - 1));
+          if (!ok) break;
+          constexpr int kWords = D / 8, kRows = 32 / kWords;  // rows of one instruction
+          const int c = lane % kWords;
+          for (int r = w * kRows + lane / kWords; r < (it.pair() ? 256 : 128); r += kRows * kLoaders) {
+            const bool row_live = r < it.rows;
+            long long at = 0;
+            if (row_live) {
+              const int row = it.row0 + r, qi = row / p.G, g = row - qi * p.G;
+              const int bi = it.kind == 0 ? p.qrow[qi] : it.b * p.Q + qi;
+              const int b = bi / p.Q, i = bi - b * p.Q;
+              at = b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head + c * 8;
+            }
+            const int rr = r & 127;
+            cp16(q_smem + (r >> 7) * S::kTileBytes + (c >> 3) * (kTileKeys * 128) + rr * 128 +
+                     (((c & 7) ^ (rr & 7)) << 4),
+                 static_cast<const uint16_t*>(a.q) + at, row_live);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          continue;
+        }
+        const int mine = turn + x;
+        if (mine % kLoaders == w) {
+          // which tile: x < d: K_x; else pairs (V_j, K_{j+d}) while both exist, then the last V's
+          int j, is_v;
+          if (x < d && x < it.tiles) {
+            j = x;
+            is_v = 0;
+          } else {
+            const int dd = d < it.tiles ? d : it.tiles;
+            const int y = x - dd, both = 2 * (it.tiles - dd);
+            is_v = y >= both || (y & 1) == 0;
+            j = y >= both ? (it.tiles - dd) + (y - both) : (is_v ? y >> 1 : (y >> 1) + dd);
+          }
+          const int slot = mine % kSlots, use = mine / kSlots;
+          if (use > 0) ok = __all_sync(0xffffffffu, wait(&empty[slot], use - 1));
+          if (!ok) break;
+          const uint16_t* pool = static_cast<const uint16_t*>(is_v ? a.v : a.k) + it.h * a.head;
+          const uint32_t base = ring + slot * S::kTileBytes;
+          // this lane finds the pages of rows lane, lane + 32, ...
+          long long at[4];
+          bool plain = true;  // none of this tile's values needs a look
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    op[e] = __bfloat16_as_ushort(__float2bfloat16_rn(bad ? nan : (l == 0.f ? 0.f : o[e] / l)));
-  if (a.lse && lane == 0) a.lse[row] = bad ? nan : (l == 0.f ? -INFINITY : m + logf(l));
-  if (bad && lane == 0) atomicOr(flags, bad);
+          for (int u = 0; u < 4; ++u) {
+            const int r = u * 32 + lane, key = it.key0 + j * kTileKeys + r;
+            at[u] = -1;
+            if (j * kTileKeys + r < it.keys) {
+              const int pg = key / a.page_size;
+              const int id = it.kind == 0 ? a.prefix_pages[pg] : a.table[(long long)it.b * a.max_pages + pg];
+              if ((unsigned)id < (unsigned)a.num_pages) {
+                at[u] = id * a.page + (long long)(key - pg * a.page_size) * a.token;
+              } else {
+                if (it.kind == 0)
+                  p.head[H_BAD_PREFIX] = 1;
+                else
+                  atomicOr(&p.stat[it.b], SV_FLAG_BAD_PAGE);
+                atomicOr(&p.head[H_FLAGS], SV_FLAG_BAD_PAGE);
+              }
+              if (it.kind == 1 && is_v && key >= it.len) plain = false;
+            }
+          }
+          plain = __all_sync(0xffffffffu, plain);
+          constexpr int kWords = D / 8, kRows = 32 / kWords;  // rows of one instruction
+          const int c = lane % kWords;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+#pragma unroll 8
+            for (int v = 0; v < 32 / kRows; ++v) {
+              const int rl = v * kRows + lane / kWords, r = u * 32 + rl;
+              const long long from = __shfl_sync(0xffffffffu, at[u], rl);
+              const uint32_t dst = base + (c >> 3) * (kTileKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+              const uint16_t* src = pool + (from < 0 ? 0 : from) + c * 8;
+              const int key = it.key0 + j * kTileKeys + r;
+              if (plain || key < it.len || from < 0) {
+                cp16(dst, src, from >= 0);
+              } else {
+                // a drafted token's value: positions in front of it have weight 0 there,
+                // and 0 times a value that is not finite would reach their sums
+                uint4 q = *reinterpret_cast<const uint4*>(src);
+                if (not_finite(q.x) || not_finite(q.y) || not_finite(q.z) || not_finite(q.w)) {
+                  atomicMin(&p.nan_from[(long long)it.b * a.Hkv + it.h], key);
+                  q = make_uint4(0u, 0u, 0u, 0u);
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(q.x), "r"(q.y), "r"(q.z),
+                             "r"(q.w)
+                             : "memory");
+              }
+            }
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          // the tile before this one has landed (Q, too): announce it
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          if (!q_done) {
+            fence_async();
+            mbar_arrive(&q_full);
+            q_done = 1;
+          }
+          announce();
+          pending = slot;
+        }
+      }
+      if (!ok) break;
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (!q_done) {  // (this warp had no tile of the item)
+        fence_async();
+        mbar_arrive(&q_full);
+      }
+      announce();
+      turn += total;
+      ++live;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else if (warp == 8) {
+    // ---- the products: one thread issues them ----
+    int turn = 0, live = 0, s_turn[2] = {0, 0};
+    for (int n = 0;; ++n) {
+      const int2 got = fetch(n);
+      if (got.x < 0) break;
+      const Item it = decode(p, got.x, got.y);
+      if (it.tiles == 0) continue;
+      bool ok = true;
+      if (lane == 0) {
+        const int T = it.tiles, d = it.ahead() < T ? it.ahead() : T;
+        const bool pr = it.pair();
+        auto slot_of = [&](int x) { return (turn + x) % kSlots; };
+        auto landed = [&](int x) {
+          const bool r = wait(&full[slot_of(x)], (turn + x) / kSlots);
+          tc::fence_after();
+          return r;
+        };
+        auto free_slot = [&](int x) { tc::commit<1>(smem_addr(&empty[slot_of(x)])); };
+        auto scores = [&](int s, int x) {  // S_s = Q K^T, K in turn x
+          const uint32_t kb = ring + slot_of(x) * S::kTileBytes, qb = q_smem + (pr ? s * S::kTileBytes : 0);
+#pragma unroll
+          for (int q = 0; q < D / 16; ++q) {
+            const uint32_t off = (q >> 2) * (kTileKeys * 128) + (q & 3) * 32;
+            tc::mma<1, false>(tmem + kColS + s * kStreamCols, tc::desc_sw128(qb + off, 16, 1024),
+                              tc::desc_sw128(kb + off, 16, 1024), kIdS, q != 0);
+          }
+          tc::commit<1>(smem_addr(&s_full[s]));
+        };
+        auto values = [&](int s, int x, bool acc) {  // O_s += P_s V, V in turn x
+          const uint32_t vb = ring + slot_of(x) * S::kTileBytes;
+#pragma unroll
+          for (int q = 0; q < kTileKeys / 16; ++q)
+            tc::mma_ts(tmem + kColO + s * kStreamCols, tmem + kColS + s * kStreamCols + 8 * q,
+                       tc::desc_sw128(vb + q * 2048, kTileKeys * 128, 1024), kIdO, acc || q != 0);
+        };
+        ok = wait(&q_full, live);
+        tc::fence_after();
+        int x = 0;
+        for (; x < d && ok; ++x) {
+          ok = landed(x);
+          if (!ok) break;
+          if (pr) {
+            scores(0, x);
+            scores(1, x);
+          } else {
+            scores(x, x);
+          }
+          free_slot(x);
+          if (d == T && x == T - 1) tc::commit<1>(smem_addr(&q_empty));
+        }
+        for (int j = 0; j < T && ok; ++j) {
+          const int xv = x++, xk = j + d < T ? x++ : -1;
+          ok = landed(xv) && (xk < 0 || landed(xk));
+          for (int s = pr ? 0 : j & 1; s <= (pr ? 1 : j & 1) && ok; ++s) {
+            ok = wait(&p_ready[s], s_turn[s]++);
+            tc::fence_after();
+            if (!ok) break;
+            values(s, xv, pr ? j > 0 : j > 1);
+            if (xk >= 0)
+              scores(s, xk);
+            else
+              tc::commit<1>(smem_addr(&o_full[s]));
+          }
+          if (!ok) break;
+          free_slot(xv);
+          if (xk >= 0) {
+            free_slot(xk);
+            if (j + d == T - 1) tc::commit<1>(smem_addr(&q_empty));
+          }
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+      turn += 2 * it.tiles;
+      ++live;
+    }
+  } else {
+    // ---- softmax of one stream: a row per thread ----
+    const int s = warp >> 2, row = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t col_s = lanes + kColS + s * kStreamCols, col_o = lanes + kColO + s * kStreamCols;
+    const float c = a.scale * kLog2e;
+    const float worst = c >= 0.f ? -INFINITY : INFINITY;
+    int s_turn = 0, o_turn = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int2 got = fetch(n);
+      if (got.x < 0) break;
+      const Item it = decode(p, got.x, got.y);
+      const int tiles = it.stream_tiles(s);
+      if (it.tiles == 0 || tiles == 0) continue;
+      const int r = it.row0 + (it.pair() ? s * 128 : 0) + row;  // this thread's row
+      const bool live = (it.pair() ? s * 128 : 0) + row < it.rows;
+      // keys that the row sees, from the item's first on
+      int sees = 0;
+      if (live) sees = it.kind == 0 ? it.keys : min(it.keys, it.len + r / p.G - it.key0);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < tiles; ++j) {
+        const int first = (it.pair() ? j : 2 * j + s) * kTileKeys;
+        const int vis = max(0, min(kTileKeys, sees - first));
+        if (!__all_sync(0xffffffffu, wait(&s_full[s], s_turn))) {
+          ok = false;
+          break;
+        }
+        ++s_turn;
+        tc::fence_after();
+        const bool all = __all_sync(0xffffffffu, vis == kTileKeys);
+        // the tile's extreme score
+        float top = worst;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32];
+          tc::ld32(col_s + 32 * q, v);
+          tc::ld_wait(v);
+          if (!all) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * q + e >= vis) v[e] = __float_as_uint(worst);
+          }
+          float t4[4] = {worst, worst, worst, worst};
+          if (c >= 0.f) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(v[e]));
+            top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) t4[e & 3] = fminf(t4[e & 3], __uint_as_float(v[e]));
+            top = fminf(top, fminf(fminf(t4[0], t4[1]), fminf(t4[2], t4[3])));
+          }
+        }
+        // Weights are taken relative to a reference that follows the maximum only
+        // when that is 2^8 above it: float32 sums and bf16 weights lose nothing by
+        // it, and the accumulator is hardly ever rescaled.
+        const float mt = vis > 0 && top != worst ? top * c : -INFINITY;
+        const bool raise = mt > m + 8.f || (m == -INFINITY && mt > -INFINITY);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? (m == -INFINITY ? 0.f : ex2(m - mt)) : 1.f;
+          if (raise) m = mt;
+          l *= f;
+          if (j > 0) {  // (the product before this tile's scores is complete, too)
+#pragma unroll 1
+            for (int q = 0; q < D; q += 16) {
+              uint32_t v[16];
+              tc::ld16(col_o + q, v);
+              tc::ld_wait(v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+              tc::st16(col_o + q, v);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32], w[16];
+          tc::ld32(col_s + 32 * q, v);
+          tc::ld_wait(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x = ex2(__fmaf_rn(__uint_as_float(v[e]), c, -ref));
+            if (!all && 32 * q + e >= vis) x = 0.f;
+            sum[e & 3] += x;
+            v[e] = __float_as_uint(x);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = tc::pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+          // over scores that this thread has read: columns 16q.. of the row
+          tc::st16(col_s + 16 * q, w);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc::st_wait();
+        tc::fence_before();
+        mbar_arrive(&p_ready[s]);
+      }
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, wait(&o_full[s], o_turn));
+      ++o_turn;
+      if (!ok) break;
+      tc::fence_after();
+      // this row's part
+      long long at;
+      float2* ml;
+      float* o;
+      if (it.kind == 0) {
+        const int queries = p.head[H_QUERIES];
+        if (s == 1 && !it.pair()) {
+          at = ((long long)it.slot * a.Hkv + it.h) * 128 + row;
+          ml = p.extra_ml;
+          o = p.extra_o;
+        } else {
+          at = ((long long)it.slot * a.Hkv + it.h) * queries * p.G + r;
+          ml = p.pre_ml;
+          o = p.pre_o;
+        }
+      } else {
+        at = (((long long)it.slot * a.Hkv + it.h) * 2 + (it.pair() ? 0 : s)) * (p.Q * p.G) + r;
+        ml = p.own_ml;
+        o = p.own_o;
+      }
+      if (live) ml[at] = make_float2(m, l);
+#pragma unroll 1
+      for (int q = 0; q < D; q += 16) {
+        uint32_t v[16];
+        tc::ld16(col_o + q, v);
+        tc::ld_wait(v);
+        if (live) {
+          uint4* to = reinterpret_cast<uint4*>(o + at * D + q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+      }
+      tc::fence_before();  // (the next item's first weights follow: its product may overwrite O)
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (tid == 0 && failed) atomicOr(&p.head[H_FLAGS], SV_FLAG_TIMEOUT);
+  if (warp == 8) tc::dealloc<1>(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// 3. The parts of a row together: a warp per row.
+// ---------------------------------------------------------------------------
+constexpr int kMergeWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const Args p) {
+  const AttentionLaunch& a = p.a;
+  const long long id = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  constexpr int E = D / 32;
+  pdl_wait();
+  if (id >= (long long)a.B * p.Q * a.Hq) return;
+  const int hq = (int)(id % a.Hq), bi = (int)(id / a.Hq), b = bi / p.Q, i = bi - b * p.Q;
+  const int k = a.kpr ? a.kpr[b] : a.K;
+  const int bad = p.stat[b];
+  if (i > k && !(bad & SV_FLAG_BAD_K)) return;
+  uint16_t* op = static_cast<uint16_t*>(a.out) + b * a.o_seq + i * a.o_pos + hq * a.o_head + lane * E;
+  const int h = hq / p.G, g = hq - h * p.G;
+  float acc[E], M = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  auto add = [&](const float2* ml, const float* o, long long at) {
+    const float2 x = ml[at];
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = o[at * D + lane * E + e];
+    if (x.x == -INFINITY && x.y == 0.f) return;  // nothing seen (a NaN in l goes on)
+    const float n = x.x > M ? x.x : M, fo = M == -INFINITY ? 0.f : ex2(M - n);
+    const float fx = x.x == -INFINITY ? 1.f : ex2(x.x - n);
+    l = l * fo + x.y * fx;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * fo + v[e] * fx;
+    M = n;
+  };
+  const bool dead = bad || p.head[H_BAD_PREFIX];
+  const int len = a.lens[b];
+  if (!dead) {
+    const int queries = p.head[H_QUERIES], splits = p.head[H_SPLITS], per = p.head[H_SPLIT_TILES];
+    if (splits > 0) {
+      const long long r = (long long)(p.qoff[b] + i) * p.G + g, rows = (long long)queries * p.G;
+      const long long tile0 = r / kItemRows * kItemRows;
+      const bool two = rows - tile0 <= 128;
+      const int ptiles = ceil_div(a.prefix_len, kTileKeys);
+      for (int s = 0; s < splits; ++s) {
+        add(p.pre_ml, p.pre_o, ((long long)s * a.Hkv + h) * rows + r);
+        if (two && min(per, ptiles - s * per) >= 2) add(p.extra_ml, p.extra_o, ((long long)s * a.Hkv + h) * 128 + (r - tile0));
+      }
+    }
+    const int keys = p.head[H_CHUNK_KEYS], chunks = ceil_div(len + k, keys), r = i * p.G + g;
+    const bool two = (k + 1) * p.G - r / kItemRows * kItemRows <= 128;
+    for (int c = 0; c < chunks; ++c) {
+      const long long at = (((long long)(p.coff[b] + c) * a.Hkv + h) * 2) * (p.Q * p.G) + r;
+      add(p.own_ml, p.own_o, at);
+      if (two && len + k - c * keys > kTileKeys) add(p.own_ml, p.own_o, at + p.Q * p.G);
+    }
+  }
+  const float nan = __int_as_float(0x7fffffff);
+  const bool lost = !dead && len + i > p.nan_from[(long long)b * a.Hkv + h];
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = __bfloat16_as_ushort(__float2bfloat16_rn(dead || lost ? nan : acc[e] * inv));
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(op) = make_uint2(v[0] | ((uint32_t)v[1] << 16), v[2] | ((uint32_t)v[3] << 16));
+  else
+    *reinterpret_cast<uint32_t*>(op) = v[0] | ((uint32_t)v[1] << 16);
+  if (a.lse && lane == 0) a.lse[id] = dead ? nan : (l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2);
+}
+
+template <typename... A>
+static cudaError_t launch(void (*k)(A...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const Args& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, p);
+}
+
+template <int D>
+static cudaError_t run(const Args& p, cudaStream_t st) {
+  static std::atomic<int> ready[kMaxDevices];
+  const int d = current_device();
+  if (d < 0) return cudaErrorInvalidDevice;
+  if (!ready[d].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(part_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    ready[d].store(1, std::memory_order_release);
+  }
+  cudaError_t e = launch(plan_kernel, 1, kPlanThreads, 0, st, p);
+  if (e == cudaSuccess) e = launch(part_kernel<D>, (unsigned)p.grid, kThreads, Shape<D>::kSmem, st, p);
+  const long long rows = (long long)p.a.B * p.Q * p.a.Hq;
+  if (e == cudaSuccess)
+    e = launch(merge_kernel<D>, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps), 32 * kMergeWarps, 0, st, p);
+  return e;
 }
 
 }  // namespace att
 
-size_t attention_workspace_bytes(int, int, int, int, int, int, int) { return 256; }
+size_t attention_workspace_bytes(int B, int K, int Hq, int Hkv, int D, int prefix_len, int max_own) {
+  return att::layout(B, K, Hq, Hkv, D, prefix_len, max_own).total;
+}
 
 int attention_launch(const AttentionLaunch& L, std::string* err) {
+  att::Args p;
+  p.a = L;
+  p.G = L.Hq / L.Hkv;
+  p.Q = L.K + 1;
+  p.row_tiles = (p.Q * p.G + att::kItemRows - 1) / att::kItemRows;
+  const int sms = tc::num_sms();
+  p.grid = sms < att::kMaxGrid ? sms : att::kMaxGrid;
+  const att::Layout w = att::layout(L.B, L.K, L.Hq, L.Hkv, L.D, L.prefix_len, (long long)L.max_pages * L.page_size);
+  char* base = static_cast<char*>(L.workspace);
+  p.head = reinterpret_cast<uint32_t*>(base);
+  p.qrow = reinterpret_cast<int*>(base + w.qrow);
+  p.qoff = reinterpret_cast<int*>(base + w.qoff);
+  p.coff = reinterpret_cast<int*>(base + w.coff);
+  p.chunk_of = reinterpret_cast<int*>(base + w.chunk_of);
+  p.stat = reinterpret_cast<int*>(base + w.stat);
+  p.nan_from = reinterpret_cast<int*>(base + w.nan_from);
+  p.pre_ml = reinterpret_cast<float2*>(base + w.pre_ml);
+  p.pre_o = reinterpret_cast<float*>(base + w.pre_o);
+  p.extra_ml = reinterpret_cast<float2*>(base + w.extra_ml);
+  p.extra_o = reinterpret_cast<float*>(base + w.extra_o);
+  p.own_ml = reinterpret_cast<float2*>(base + w.own_ml);
+  p.own_o = reinterpret_cast<float*>(base + w.own_o);
+  p.own_slots = w.own_slots;
   cudaStream_t st = static_cast<cudaStream_t>(L.stream);
-  uint32_t* flags = static_cast<uint32_t*>(L.workspace);
-  att::clear_kernel<<<1, 1, 0, st>>>(flags);
-  const long long rows = (long long)L.B * (L.K + 1) * L.Hq;
-  const unsigned blocks = (unsigned)((rows + 7) / 8);
-  if (L.D == 128)
-    att::rows_kernel<128><<<blocks, 256, 0, st>>>(L, flags);
-  else
-    att::rows_kernel<64><<<blocks, 256, 0, st>>>(L, flags);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = L.D == 128 ? att::run<128>(p, st) : att::run<64>(p, st);
   if (e != cudaSuccess) {
     *err = std::string("attention launch: ") + cudaGetErrorString(e);
     return SV_ERR_CUDA;
