@@ -214,9 +214,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
 // ---------------------------------------------------------------------------
 // 2. The parts.
 // ---------------------------------------------------------------------------
-constexpr int kThreads = 384;  // warps 0-3, 4-7: softmax of stream 0, 1; 8: MMA; 9-11: loads
-constexpr int kLoaders = 3;
+constexpr int kThreads = 512;  // warps 0-3, 4-7: softmax of stream 0, 1; 8: MMA; 9: items; 10: Q; 11-15: K and V
 constexpr int kSlots = 5;
+constexpr int kLoaders = kSlots;  // a warp per slot of the ring: it waits for its own tile's release, never for an older one
+// The block is launched with 128 registers a thread; the softmax warps keep a row's
+// 128 scores in registers: (176 + 176 + 80 + 80) * 128 = 512 * 128.
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+static_assert(2 * (kSoftmaxRegs + kOtherRegs) * 128 <= kThreads * 128, "no more registers than the block was launched with");
 constexpr uint32_t kColS = 0, kColO = 256, kStreamCols = 128;
 
 template <int D>
@@ -226,7 +230,7 @@ struct Shape {
   static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + 1024;
 };
 
-struct Item {
+struct alignas(16) Item {
   int kind;  // 0 prefix, 1 own, -1 none left
   int h, b;  // key head; sequence (own)
   int row0, rows;    // first row (compact for the prefix, the sequence's for own) and count, at most 256
@@ -234,6 +238,7 @@ struct Item {
   int tiles;
   int slot;          // split (prefix) or chunk (own)
   int len;           // own: committed tokens
+  int unused;
   __device__ __forceinline__ bool pair() const { return rows > 128; }  // streams: two row tiles, or alternate key tiles
   __device__ __forceinline__ int ahead() const { return pair() ? 1 : 2; }
   __device__ __forceinline__ int stream_tiles(int s) const { return pair() ? tiles : (tiles + 1 - s) / 2; }
@@ -276,17 +281,24 @@ __device__ __forceinline__ Item decode(const Args& p, int kind, int idx) {
   return it;
 }
 
-// Next item for this CTA: from its preferred list until that is empty, then from the other.
+// Next item for this CTA: from its preferred list until that is empty, then from
+// the other.  Items without keys are passed over.
 struct Feed {
   int list, left;
-  __device__ __forceinline__ int2 next(const Args& p) {
+  __device__ __forceinline__ Item next(const Args& p) {
+    Item it;
     while (left > 0) {
       const int i = (int)atomicAdd(&p.head[list ? H_NEXT_OWN : H_NEXT_PRE], 1u);
-      if (i < (int)p.head[list ? H_OWN_ITEMS : H_PRE_ITEMS]) return make_int2(list, i);
-      list ^= 1;
-      --left;
+      if (i < (int)p.head[list ? H_OWN_ITEMS : H_PRE_ITEMS]) {
+        it = decode(p, list, i);
+        if (it.tiles > 0) return it;
+      } else {
+        list ^= 1;
+        --left;
+      }
     }
-    return make_int2(-1, 0);
+    it.kind = -1;
+    return it;
   }
 };
 
@@ -305,9 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
   using S = Shape<D>;
   constexpr uint32_t kIdS = tc::idesc(false, false, 128, kTileKeys), kIdO = tc::idesc(false, true, 128, D);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], p_ready[2], o_full[2],
+  __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2],
       item_full[2], item_empty[2];
-  __shared__ int2 items[2];
+  __shared__ Item items[2];
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
   const AttentionLaunch& a = p.a;
@@ -319,14 +331,14 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
       mbar_init(&full[s], 32);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(&q_full, 32 * kLoaders);
-    mbar_init(&q_empty, 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 32);
+      mbar_init(&q_empty[s], 1);
       mbar_init(&s_full[s], 1);
       mbar_init(&p_ready[s], 128);
       mbar_init(&o_full[s], 1);
       mbar_init(&item_full[s], 1);
-      mbar_init(&item_empty[s], 8 + 1 + kLoaders);  // a lane of every warp
+      mbar_init(&item_empty[s], 8 + 1 + 1 + kLoaders);  // a lane of every other warp
     }
     failed = 0;
     fence_mbar_init();
@@ -339,15 +351,31 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
   pdl_launch_dependents();
   pdl_wait();
 
-  // The items pass through two slots, written by the first loader warp.
+  // The items pass through two slots, written ahead by warp 9.
   auto fetch = [&](int n) {  // item n of this CTA, read by a whole warp
-    int2 got = make_int2(-1, 0);
-    const bool ok = mbar_wait_bounded(&item_full[n & 1], (uint32_t)((n >> 1) & 1));
-    if (__all_sync(0xffffffffu, ok)) got = items[n & 1];
-    else failed = 1;
+    // (word by word: as a structure it would live in local memory)
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&item_full[n & 1], (uint32_t)((n >> 1) & 1)));
+    if (!ok) failed = 1;
+    const int4* from = reinterpret_cast<const int4*>(&items[n & 1]);
+    const int4 w0 = from[0], w1 = from[1], w2 = from[2];
+    Item got;
+    got.kind = ok ? w0.x : -1;
+    got.h = w0.y;
+    got.b = w0.z;
+    got.row0 = w0.w;
+    got.rows = w1.x;
+    got.key0 = w1.y;
+    got.keys = w1.z;
+    got.tiles = w1.w;
+    got.slot = w2.x;
+    got.len = w2.y;
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_empty[n & 1]);
     return got;
+  };
+  auto landed = [&]() {  // this lane's copies, seen by the tensor cores once announced
+    asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+    fence_async();
   };
   auto wait = [&](uint64_t* bar, int phase) {
     if (mbar_wait_bounded(bar, (uint32_t)(phase & 1))) return true;
@@ -355,82 +383,88 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
     return false;
   };
 
-  if (warp >= 9) {
-    // ---- loads: Q rows by all three warps, K and V tiles in turn ----
-    const int w = warp - 9;
-    Feed feed;
-    feed.left = 2;
-    feed.list = (int)blockIdx.x < (int)p.head[H_PRE_CTAS] ? 0 : 1;
-    int turn = 0, live = 0;  // tiles of the ring so far (all warps), items with any
-    int pending = -1;  // the slot of this warp's last tile, not yet announced
-    bool ok = true;
-    auto announce = [&]() {
-      if (pending < 0) return;
-      fence_async();
-      mbar_arrive(&full[pending]);
-      pending = -1;
-    };
-    for (int n = 0; ok; ++n) {
-      if (w == 0) {
-        if (n >= 2 && !__all_sync(0xffffffffu, wait(&item_empty[n & 1], (n >> 1) - 1))) break;
-        if (lane == 0) {
-          items[n & 1] = feed.next(p);
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 9) {
+      // ---- the items ----
+      Feed feed;
+      feed.left = 2;
+      feed.list = (int)blockIdx.x < (int)p.head[H_PRE_CTAS] ? 0 : 1;
+      if (lane == 0) {
+        for (int n = 0;; ++n) {
+          const Item it = feed.next(p);
+          if (n >= 2 && !wait(&item_empty[n & 1], (n >> 1) - 1)) break;
+          items[n & 1] = it;
           mbar_arrive(&item_full[n & 1]);
+          if (it.kind < 0) break;
         }
-        __syncwarp();
       }
-      const int2 got = fetch(n);
-      if (got.x < 0) break;
-      const Item it = decode(p, got.x, got.y);
-      if (it.tiles == 0) continue;  // (in every role)
-      // K and V tiles: K_0 .. K_{d-1}, then V_j, K_{j+d}
-      const int d = it.ahead();
-      const int total = 2 * it.tiles;
-      int q_done = 0;
-      for (int x = -1; x < total && ok; ++x) {
-        if (x < 0) {  // Q first (its place frees with the last item's last S)
-          ok = __all_sync(0xffffffffu, wait(&q_empty, live - 1));
-          if (!ok) break;
-          constexpr int kWords = D / 8, kRows = 32 / kWords;  // rows of one instruction
-          const int c = lane % kWords;
-          for (int r = w * kRows + lane / kWords; r < (it.pair() ? 256 : 128); r += kRows * kLoaders) {
-            const bool row_live = r < it.rows;
-            long long at = 0;
-            if (row_live) {
+    } else if (warp == 10) {
+      // ---- Q: 128 rows to a half of its place once the scores of the half's last item
+      // are done; a lane finds one row of each 32, then the warp copies them ----
+      int q_uses[2] = {0, 0};
+      bool ok = true;
+      constexpr int kWords = D / 8, kRows = 32 / kWords;  // 16-byte words of a row, rows of one instruction
+      const int c = lane % kWords, sub = lane / kWords;
+      const uint16_t* from_q = static_cast<const uint16_t*>(a.q) + c * 8;
+      for (int n = 0; ok; ++n) {
+        const Item it = fetch(n);
+        if (it.kind < 0) break;
+        const int q_first = it.pair() ? 0 : n & 1, q_last = it.pair() ? 1 : n & 1;
+#pragma unroll 1
+        for (int h = q_first; h <= q_last; ++h) {
+          long long at[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = (h - q_first) * 128 + u * 32 + lane;
+            at[u] = -1;
+            if (r < it.rows) {
               const int row = it.row0 + r, qi = row / p.G, g = row - qi * p.G;
               const int bi = it.kind == 0 ? p.qrow[qi] : it.b * p.Q + qi;
               const int b = bi / p.Q, i = bi - b * p.Q;
-              at = b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head + c * 8;
+              at[u] = b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head;
             }
-            const int rr = r & 127;
-            cp16(q_smem + (r >> 7) * S::kTileBytes + (c >> 3) * (kTileKeys * 128) + rr * 128 +
-                     (((c & 7) ^ (rr & 7)) << 4),
-                 static_cast<const uint16_t*>(a.q) + at, row_live);
           }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          continue;
-        }
-        const int mine = turn + x;
-        if (mine % kLoaders == w) {
-          // which tile: x < d: K_x; else pairs (V_j, K_{j+d}) while both exist, then the last V's
-          int j, is_v;
-          if (x < d && x < it.tiles) {
-            j = x;
-            is_v = 0;
-          } else {
-            const int dd = d < it.tiles ? d : it.tiles;
-            const int y = x - dd, both = 2 * (it.tiles - dd);
-            is_v = y >= both || (y & 1) == 0;
-            j = y >= both ? (it.tiles - dd) + (y - both) : (is_v ? y >> 1 : (y >> 1) + dd);
-          }
-          const int slot = mine % kSlots, use = mine / kSlots;
-          if (use > 0) ok = __all_sync(0xffffffffu, wait(&empty[slot], use - 1));
+          ok = __all_sync(0xffffffffu, wait(&q_empty[h], q_uses[h]++ - 1));
           if (!ok) break;
-          const uint16_t* pool = static_cast<const uint16_t*>(is_v ? a.v : a.k) + it.h * a.head;
-          const uint32_t base = ring + slot * S::kTileBytes;
+          const uint32_t base = q_smem + h * S::kTileBytes + (c >> 3) * (kTileKeys * 128);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll 4
+            for (int v = 0; v < 32 / kRows; ++v) {
+              const int rr = u * 32 + v * kRows + sub;
+              const long long from = __shfl_sync(0xffffffffu, at[u], v * kRows + sub);
+              cp16(base + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), from_q + (from < 0 ? 0 : from), from >= 0);
+            }
+          landed();
+          mbar_arrive(&q_full[h]);
+        }
+      }
+    } else if (warp > 10) {
+      // ---- K and V: a warp per slot of the ring ----
+      const int slot = warp - 11;
+      int turn = 0, use = 0;  // tiles of all slots before this item; of this one
+      bool ok = true;
+      constexpr int kWords = D / 8, kRows = 32 / kWords;
+      const int c = lane % kWords, sub = lane / kWords;
+      const uint32_t base = ring + slot * S::kTileBytes + (c >> 3) * (kTileKeys * 128);
+      for (int n = 0; ok; ++n) {
+        const Item it = fetch(n);
+        if (it.kind < 0) break;
+        // K_0 .. K_{d-1}, then V_j, K_{j+d}
+        const int d = it.ahead() < it.tiles ? it.ahead() : it.tiles;
+        const int total = 2 * it.tiles;
+        for (int x = (slot + kSlots - turn % kSlots) % kSlots; x < total; x += kSlots, ++use) {
+          // which tile: x < d: K_x; else pairs (V_j, K_{j+d}) while both exist, then the last V's
+          int j = x, is_v = 0;
+          if (x >= d) {
+            const int y = x - d, both = 2 * (it.tiles - d);
+            is_v = y >= both || (y & 1) == 0;
+            j = y >= both ? (it.tiles - d) + (y - both) : (is_v ? y >> 1 : (y >> 1) + d);
+          }
+          const uint16_t* pool = static_cast<const uint16_t*>(is_v ? a.v : a.k) + it.h * a.head + c * 8;
           // this lane finds the pages of rows lane, lane + 32, ...
           long long at[4];
-          bool plain = true;  // none of this tile's values needs a look
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const int r = u * 32 + lane, key = it.key0 + j * kTileKeys + r;
@@ -447,137 +481,127 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
                   atomicOr(&p.stat[it.b], SV_FLAG_BAD_PAGE);
                 atomicOr(&p.head[H_FLAGS], SV_FLAG_BAD_PAGE);
               }
-              if (it.kind == 1 && is_v && key >= it.len) plain = false;
             }
           }
-          plain = __all_sync(0xffffffffu, plain);
-          constexpr int kWords = D / 8, kRows = 32 / kWords;  // rows of one instruction
-          const int c = lane % kWords;
+          if (use > 0) ok = __all_sync(0xffffffffu, wait(&empty[slot], use - 1));
+          if (!ok) break;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-#pragma unroll 8
+          for (int u = 0; u < 4; ++u)
+#pragma unroll 4
             for (int v = 0; v < 32 / kRows; ++v) {
-              const int rl = v * kRows + lane / kWords, r = u * 32 + rl;
-              const long long from = __shfl_sync(0xffffffffu, at[u], rl);
-              const uint32_t dst = base + (c >> 3) * (kTileKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-              const uint16_t* src = pool + (from < 0 ? 0 : from) + c * 8;
-              const int key = it.key0 + j * kTileKeys + r;
-              if (plain || key < it.len || from < 0) {
-                cp16(dst, src, from >= 0);
-              } else {
-                // a drafted token's value: positions in front of it have weight 0 there,
-                // and 0 times a value that is not finite would reach their sums
-                uint4 q = *reinterpret_cast<const uint4*>(src);
-                if (not_finite(q.x) || not_finite(q.y) || not_finite(q.z) || not_finite(q.w)) {
-                  atomicMin(&p.nan_from[(long long)it.b * a.Hkv + it.h], key);
-                  q = make_uint4(0u, 0u, 0u, 0u);
-                }
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(q.x), "r"(q.y), "r"(q.z),
-                             "r"(q.w)
-                             : "memory");
+              const int r = u * 32 + v * kRows + sub;
+              const long long from = __shfl_sync(0xffffffffu, at[u], v * kRows + sub);
+              cp16(base + r * 128 + (((c & 7) ^ (r & 7)) << 4), pool + (from < 0 ? 0 : from), from >= 0);
+            }
+          landed();
+          // Values of drafted tokens: positions in front of one have weight 0 there, and
+          // 0 times a value that is not finite would reach their sums.  Such words
+          // become zeros; the merge fails the positions that do see them.
+          const int keys_left = it.keys - j * kTileKeys;
+          int drafted = it.kind == 1 && is_v ? it.len - it.key0 - j * kTileKeys : kTileKeys;
+          if (drafted < 0) drafted = 0;
+          if (drafted < kTileKeys && drafted < keys_left) {
+            const int end = keys_left < kTileKeys ? keys_left : kTileKeys;
+            __syncwarp();
+#pragma unroll 1
+            for (int r = drafted + sub; r < end; r += kRows) {
+              const uint32_t at_s = base + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+              uint4 q;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                           : "r"(at_s)
+                           : "memory");
+              if (not_finite(q.x) || not_finite(q.y) || not_finite(q.z) || not_finite(q.w)) {
+                atomicMin(&p.nan_from[(long long)it.b * a.Hkv + it.h], it.key0 + j * kTileKeys + r);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at_s), "r"(0) : "memory");
               }
             }
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          // the tile before this one has landed (Q, too): announce it
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          if (!q_done) {
             fence_async();
-            mbar_arrive(&q_full);
-            q_done = 1;
           }
-          announce();
-          pending = slot;
+          mbar_arrive(&full[slot]);
         }
+        turn += total;
       }
-      if (!ok) break;
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      if (!q_done) {  // (this warp had no tile of the item)
-        fence_async();
-        mbar_arrive(&q_full);
-      }
-      announce();
-      turn += total;
-      ++live;
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-  } else if (warp == 8) {
-    // ---- the products: one thread issues them ----
-    int turn = 0, live = 0, s_turn[2] = {0, 0};
-    for (int n = 0;; ++n) {
-      const int2 got = fetch(n);
-      if (got.x < 0) break;
-      const Item it = decode(p, got.x, got.y);
-      if (it.tiles == 0) continue;
-      bool ok = true;
-      if (lane == 0) {
-        const int T = it.tiles, d = it.ahead() < T ? it.ahead() : T;
-        const bool pr = it.pair();
-        auto slot_of = [&](int x) { return (turn + x) % kSlots; };
-        auto landed = [&](int x) {
-          const bool r = wait(&full[slot_of(x)], (turn + x) / kSlots);
-          tc::fence_after();
-          return r;
-        };
-        auto free_slot = [&](int x) { tc::commit<1>(smem_addr(&empty[slot_of(x)])); };
-        auto scores = [&](int s, int x) {  // S_s = Q K^T, K in turn x
-          const uint32_t kb = ring + slot_of(x) * S::kTileBytes, qb = q_smem + (pr ? s * S::kTileBytes : 0);
-#pragma unroll
-          for (int q = 0; q < D / 16; ++q) {
-            const uint32_t off = (q >> 2) * (kTileKeys * 128) + (q & 3) * 32;
-            tc::mma<1, false>(tmem + kColS + s * kStreamCols, tc::desc_sw128(qb + off, 16, 1024),
-                              tc::desc_sw128(kb + off, 16, 1024), kIdS, q != 0);
-          }
-          tc::commit<1>(smem_addr(&s_full[s]));
-        };
-        auto values = [&](int s, int x, bool acc) {  // O_s += P_s V, V in turn x
-          const uint32_t vb = ring + slot_of(x) * S::kTileBytes;
-#pragma unroll
-          for (int q = 0; q < kTileKeys / 16; ++q)
-            tc::mma_ts(tmem + kColO + s * kStreamCols, tmem + kColS + s * kStreamCols + 8 * q,
-                       tc::desc_sw128(vb + q * 2048, kTileKeys * 128, 1024), kIdO, acc || q != 0);
-        };
-        ok = wait(&q_full, live);
-        tc::fence_after();
-        int x = 0;
-        for (; x < d && ok; ++x) {
-          ok = landed(x);
-          if (!ok) break;
-          if (pr) {
-            scores(0, x);
-            scores(1, x);
-          } else {
-            scores(x, x);
-          }
-          free_slot(x);
-          if (d == T && x == T - 1) tc::commit<1>(smem_addr(&q_empty));
-        }
-        for (int j = 0; j < T && ok; ++j) {
-          const int xv = x++, xk = j + d < T ? x++ : -1;
-          ok = landed(xv) && (xk < 0 || landed(xk));
-          for (int s = pr ? 0 : j & 1; s <= (pr ? 1 : j & 1) && ok; ++s) {
-            ok = wait(&p_ready[s], s_turn[s]++);
+    } else if (warp == 8) {
+      // ---- the products: one thread issues them ----
+      int turn = 0, s_turn[2] = {0, 0}, q_uses[2] = {0, 0};
+      for (int n = 0;; ++n) {
+        const Item it = fetch(n);
+        if (it.kind < 0) break;
+        bool ok = true;
+        if (lane == 0) {
+          const int T = it.tiles, d = it.ahead() < T ? it.ahead() : T;
+          const bool pr = it.pair();
+          auto slot_of = [&](int x) { return (turn + x) % kSlots; };
+          auto landed = [&](int x) {
+            const bool r = wait(&full[slot_of(x)], (turn + x) / kSlots);
             tc::fence_after();
+            return r;
+          };
+          auto free_slot = [&](int x) { tc::commit<1>(smem_addr(&empty[slot_of(x)])); };
+          auto scores = [&](int s, int x) {  // S_s = Q K^T, K in turn x
+            const uint32_t kb = ring + slot_of(x) * S::kTileBytes, qb = q_smem + (pr ? s : n & 1) * S::kTileBytes;
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+              const uint32_t off = (q >> 2) * (kTileKeys * 128) + (q & 3) * 32;
+              tc::mma<1, false>(tmem + kColS + s * kStreamCols, tc::desc_sw128(qb + off, 16, 1024),
+                                tc::desc_sw128(kb + off, 16, 1024), kIdS, q != 0);
+            }
+            tc::commit<1>(smem_addr(&s_full[s]));
+          };
+          auto values = [&](int s, int x, bool acc) {  // O_s += P_s V, V in turn x
+            const uint32_t vb = ring + slot_of(x) * S::kTileBytes;
+#pragma unroll
+            for (int q = 0; q < kTileKeys / 16; ++q)
+              tc::mma_ts(tmem + kColO + s * kStreamCols, tmem + kColS + s * kStreamCols + 8 * q,
+                         tc::desc_sw128(vb + q * 2048, kTileKeys * 128, 1024), kIdO, acc || q != 0);
+          };
+          const int q_first = pr ? 0 : n & 1, q_last = pr ? 1 : n & 1;
+          auto free_q = [&]() {
+            for (int h = q_first; h <= q_last; ++h) tc::commit<1>(smem_addr(&q_empty[h]));
+          };
+          for (int h = q_first; h <= q_last && ok; ++h) ok = wait(&q_full[h], q_uses[h]++);
+          tc::fence_after();
+          int x = 0;
+          for (; x < d && ok; ++x) {
+            ok = landed(x);
             if (!ok) break;
-            values(s, xv, pr ? j > 0 : j > 1);
-            if (xk >= 0)
-              scores(s, xk);
-            else
-              tc::commit<1>(smem_addr(&o_full[s]));
+            if (pr) {
+              scores(0, x);
+              scores(1, x);
+            } else {
+              scores(x, x);
+            }
+            free_slot(x);
+            if (d == T && x == T - 1) free_q();
           }
-          if (!ok) break;
-          free_slot(xv);
-          if (xk >= 0) {
-            free_slot(xk);
-            if (j + d == T - 1) tc::commit<1>(smem_addr(&q_empty));
+          for (int j = 0; j < T && ok; ++j) {
+            const int xv = x++, xk = j + d < T ? x++ : -1;
+            ok = landed(xv) && (xk < 0 || landed(xk));
+            for (int s = pr ? 0 : j & 1; s <= (pr ? 1 : j & 1) && ok; ++s) {
+              ok = wait(&p_ready[s], s_turn[s]++);
+              tc::fence_after();
+              if (!ok) break;
+              values(s, xv, pr ? j > 0 : j > 1);
+              if (xk >= 0)
+                scores(s, xk);
+              else
+                tc::commit<1>(smem_addr(&o_full[s]));
+            }
+            if (!ok) break;
+            free_slot(xv);
+            if (xk >= 0) {
+              free_slot(xk);
+              if (j + d == T - 1) free_q();
+            }
           }
         }
+        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+        turn += 2 * it.tiles;
       }
-      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-      turn += 2 * it.tiles;
-      ++live;
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax of one stream: a row per thread ----
     const int s = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -587,11 +611,10 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
     int s_turn = 0, o_turn = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
-      const int2 got = fetch(n);
-      if (got.x < 0) break;
-      const Item it = decode(p, got.x, got.y);
+      const Item it = fetch(n);
+      if (it.kind < 0) break;
       const int tiles = it.stream_tiles(s);
-      if (it.tiles == 0 || tiles == 0) continue;
+      if (tiles == 0) continue;
       const int r = it.row0 + (it.pair() ? s * 128 : 0) + row;  // this thread's row
       const bool live = (it.pair() ? s * 128 : 0) + row < it.rows;
       // keys that the row sees, from the item's first on
@@ -608,27 +631,30 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
         ++s_turn;
         tc::fence_after();
         const bool all = __all_sync(0xffffffffu, vis == kTileKeys);
-        // the tile's extreme score
-        float top = worst;
+        // the row's scores, and their extreme
+        uint32_t v[4][32];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[32];
-          tc::ld32(col_s + 32 * q, v);
-          tc::ld_wait(v);
-          if (!all) {
+        for (int q = 0; q < 4; ++q) tc::ld32(col_s + 32 * q, v[q]);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * q + e >= vis) v[e] = __float_as_uint(worst);
-          }
-          float t4[4] = {worst, worst, worst, worst};
+        for (int q = 0; q < 4; ++q) tc::ld_wait(v[q]);
+        if (!all) {
+#pragma unroll
+          for (int e = 0; e < kTileKeys; ++e)
+            if (e >= vis) v[e >> 5][e & 31] = __float_as_uint(worst);
+        }
+        float top;
+        {
+          float t8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t8[e] = worst;
           if (c >= 0.f) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(v[e]));
-            top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+            for (int e = 0; e < kTileKeys; ++e) t8[e & 7] = fmaxf(t8[e & 7], __uint_as_float(v[e >> 5][e & 31]));
+            top = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) t4[e & 3] = fminf(t4[e & 3], __uint_as_float(v[e]));
-            top = fminf(top, fminf(fminf(t4[0], t4[1]), fminf(t4[2], t4[3])));
+            for (int e = 0; e < kTileKeys; ++e) t8[e & 7] = fminf(t8[e & 7], __uint_as_float(v[e >> 5][e & 31]));
+            top = fminf(fminf(fminf(t8[0], t8[1]), fminf(t8[2], t8[3])), fminf(fminf(t8[4], t8[5]), fminf(t8[6], t8[7])));
           }
         }
         // Weights are taken relative to a reference that follows the maximum only
@@ -643,12 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
           if (j > 0) {  // (the product before this tile's scores is complete, too)
 #pragma unroll 1
             for (int q = 0; q < D; q += 16) {
-              uint32_t v[16];
-              tc::ld16(col_o + q, v);
-              tc::ld_wait(v);
+              uint32_t o[16];
+              tc::ld16(col_o + q, o);
+              tc::ld_wait(o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-              tc::st16(col_o + q, v);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc::st16(col_o + q, o);
             }
           }
         }
@@ -656,21 +682,20 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t v[32], w[16];
-          tc::ld32(col_s + 32 * q, v);
-          tc::ld_wait(v);
+          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float x = ex2(__fmaf_rn(__uint_as_float(v[e]), c, -ref));
-            if (!all && 32 * q + e >= vis) x = 0.f;
-            sum[e & 3] += x;
-            v[e] = __float_as_uint(x);
+          for (int e = 0; e < 32; e += 2) {
+            float x = ex2(__fmaf_rn(__uint_as_float(v[q][e]), c, -ref));
+            float y = ex2(__fmaf_rn(__uint_as_float(v[q][e + 1]), c, -ref));
+            if (!all) {
+              if (32 * q + e >= vis) x = 0.f;
+              if (32 * q + e + 1 >= vis) y = 0.f;
+            }
+            sum[e & 2] += x;
+            sum[(e & 2) + 1] += y;
+            w[e >> 1] = tc::pack_bf16x2(x, y);
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[e] = tc::pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-          // over scores that this thread has read: columns 16q.. of the row
-          tc::st16(col_s + 16 * q, w);
+          tc::st16(col_s + 16 * q, w);  // over scores that this thread has read
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tc::st_wait();
@@ -682,36 +707,41 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
       ++o_turn;
       if (!ok) break;
       tc::fence_after();
-      // this row's part
-      long long at;
+      // this row's part, in quads of columns: [D / 4][rows][4], so that a warp's 32 rows
+      // are 512 contiguous bytes of a store and not 32 lines
+      long long at, rows_o;
       float2* ml;
       float* o;
       if (it.kind == 0) {
         const int queries = p.head[H_QUERIES];
         if (s == 1 && !it.pair()) {
-          at = ((long long)it.slot * a.Hkv + it.h) * 128 + row;
-          ml = p.extra_ml;
-          o = p.extra_o;
+          rows_o = 128;
+          at = (long long)it.slot * a.Hkv + it.h;
+          ml = p.extra_ml + at * rows_o + row;
+          o = p.extra_o + at * rows_o * D + row * 4;
         } else {
-          at = ((long long)it.slot * a.Hkv + it.h) * queries * p.G + r;
-          ml = p.pre_ml;
-          o = p.pre_o;
+          rows_o = (long long)queries * p.G;
+          at = (long long)it.slot * a.Hkv + it.h;
+          ml = p.pre_ml + at * rows_o + r;
+          o = p.pre_o + at * rows_o * D + r * 4;
         }
       } else {
-        at = (((long long)it.slot * a.Hkv + it.h) * 2 + (it.pair() ? 0 : s)) * (p.Q * p.G) + r;
-        ml = p.own_ml;
-        o = p.own_o;
+        rows_o = p.Q * p.G;
+        at = ((long long)it.slot * a.Hkv + it.h) * 2 + (it.pair() ? 0 : s);
+        ml = p.own_ml + at * rows_o + r;
+        o = p.own_o + at * rows_o * D + r * 4;
       }
-      if (live) ml[at] = make_float2(m, l);
+      if (live) *ml = make_float2(m, l);
 #pragma unroll 1
       for (int q = 0; q < D; q += 16) {
         uint32_t v[16];
         tc::ld16(col_o + q, v);
         tc::ld_wait(v);
         if (live) {
-          uint4* to = reinterpret_cast<uint4*>(o + at * D + q);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) to[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(o + (q / 4 + e) * rows_o * 4) =
+                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
       }
       tc::fence_before();  // (the next item's first weights follow: its product may overwrite O)
@@ -726,73 +756,97 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
 }
 
 // ---------------------------------------------------------------------------
-// 3. The parts of a row together: a warp per row.
+// 3. The parts of a row together: four threads per row, each with every fourth
+// quad of its columns, so that eight rows' threads read whole lines.
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 8;
+constexpr int kMergeThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const Args p) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
   const AttentionLaunch& a = p.a;
-  const long long id = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  constexpr int E = D / 32;
+  constexpr int N = D / 16;  // quads of a thread
+  const float nan = __int_as_float(0x7fffffff);
   pdl_wait();
-  if (id >= (long long)a.B * p.Q * a.Hq) return;
-  const int hq = (int)(id % a.Hq), bi = (int)(id / a.Hq), b = bi / p.Q, i = bi - b * p.Q;
-  const int k = a.kpr ? a.kpr[b] : a.K;
-  const int bad = p.stat[b];
-  if (i > k && !(bad & SV_FLAG_BAD_K)) return;
-  uint16_t* op = static_cast<uint16_t*>(a.out) + b * a.o_seq + i * a.o_pos + hq * a.o_head + lane * E;
-  const int h = hq / p.G, g = hq - h * p.G;
-  float acc[E], M = -INFINITY, l = 0.f;
+  const long long id = ((long long)blockIdx.x * kMergeThreads + threadIdx.x) >> 2;
+  const int sub = threadIdx.x & 3, queries = p.head[H_QUERIES];
+  const long long rows = (long long)queries * p.G;
+
+  if (p.head[H_FLAGS] & (SV_FLAG_BAD_K | SV_FLAG_BAD_N)) {
+    // sequences that have no rows: every position that the caller reads is NaN
+    for (long long b = blockIdx.x; b < a.B; b += gridDim.x) {
+      const int bad = p.stat[b];
+      if (!(bad & (SV_FLAG_BAD_K | SV_FLAG_BAD_N))) continue;
+      const int n = bad & SV_FLAG_BAD_K ? p.Q : (a.kpr ? a.kpr[b] : a.K) + 1;
+      for (int e = threadIdx.x; e < n * a.Hq * D; e += kMergeThreads) {
+        const int i = e / (a.Hq * D), h = e / D % a.Hq;
+        static_cast<uint16_t*>(a.out)[b * a.o_seq + i * a.o_pos + h * a.o_head + e % D] = 0x7fff;
+        if (a.lse && e % D == 0) a.lse[(b * p.Q + i) * a.Hq + h] = nan;
+      }
+    }
+  }
+  if (id >= rows * a.Hkv) return;
+  const int h = (int)(id / rows);
+  const long long r = id - h * rows;
+  const int query = (int)(r / p.G), g = (int)(r - (long long)query * p.G);
+  const int bi = p.qrow[query], b = bi / p.Q, i = bi - b * p.Q, hq = h * p.G + g;
+  const int k = a.kpr ? a.kpr[b] : a.K, len = a.lens[b];
+  const int splits = p.head[H_SPLITS], per = p.head[H_SPLIT_TILES], keys = p.head[H_CHUNK_KEYS], first = p.coff[b];
+  const bool dead = p.stat[b] || p.head[H_BAD_PREFIX];
+  const bool lost = len + i > p.nan_from[(long long)b * a.Hkv + h];
+  float acc[N][4], M = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  auto add = [&](const float2* ml, const float* o, long long at) {
-    const float2 x = ml[at];
-    float v[E];
+  for (int q = 0; q < N; ++q)
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = o[at * D + lane * E + e];
+    for (int e = 0; e < 4; ++e) acc[q][e] = 0.f;
+  auto add = [&](const float2* ml, const float* o, long long part, long long rows_o, long long row) {
+    const float2 x = ml[part * rows_o + row];
+    float4 v[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      v[q] = *reinterpret_cast<const float4*>(o + part * rows_o * D + ((4 * q + sub) * rows_o + row) * 4);
     if (x.x == -INFINITY && x.y == 0.f) return;  // nothing seen (a NaN in l goes on)
     const float n = x.x > M ? x.x : M, fo = M == -INFINITY ? 0.f : ex2(M - n);
     const float fx = x.x == -INFINITY ? 1.f : ex2(x.x - n);
     l = l * fo + x.y * fx;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * fo + v[e] * fx;
+    for (int q = 0; q < N; ++q) {
+      acc[q][0] = acc[q][0] * fo + v[q].x * fx;
+      acc[q][1] = acc[q][1] * fo + v[q].y * fx;
+      acc[q][2] = acc[q][2] * fo + v[q].z * fx;
+      acc[q][3] = acc[q][3] * fo + v[q].w * fx;
+    }
     M = n;
   };
-  const bool dead = bad || p.head[H_BAD_PREFIX];
-  const int len = a.lens[b];
   if (!dead) {
-    const int queries = p.head[H_QUERIES], splits = p.head[H_SPLITS], per = p.head[H_SPLIT_TILES];
     if (splits > 0) {
-      const long long r = (long long)(p.qoff[b] + i) * p.G + g, rows = (long long)queries * p.G;
       const long long tile0 = r / kItemRows * kItemRows;
       const bool two = rows - tile0 <= 128;
       const int ptiles = ceil_div(a.prefix_len, kTileKeys);
       for (int s = 0; s < splits; ++s) {
-        add(p.pre_ml, p.pre_o, ((long long)s * a.Hkv + h) * rows + r);
-        if (two && min(per, ptiles - s * per) >= 2) add(p.extra_ml, p.extra_o, ((long long)s * a.Hkv + h) * 128 + (r - tile0));
+        add(p.pre_ml, p.pre_o, (long long)s * a.Hkv + h, rows, r);
+        if (two && min(per, ptiles - s * per) >= 2)
+          add(p.extra_ml, p.extra_o, (long long)s * a.Hkv + h, 128, r - tile0);
       }
     }
-    const int keys = p.head[H_CHUNK_KEYS], chunks = ceil_div(len + k, keys), r = i * p.G + g;
-    const bool two = (k + 1) * p.G - r / kItemRows * kItemRows <= 128;
+    const int chunks = ceil_div(len + k, keys), own = i * p.G + g, all = p.Q * p.G;
+    const bool two = (k + 1) * p.G - own / kItemRows * kItemRows <= 128;
     for (int c = 0; c < chunks; ++c) {
-      const long long at = (((long long)(p.coff[b] + c) * a.Hkv + h) * 2) * (p.Q * p.G) + r;
-      add(p.own_ml, p.own_o, at);
-      if (two && len + k - c * keys > kTileKeys) add(p.own_ml, p.own_o, at + p.Q * p.G);
+      const long long part = ((long long)(first + c) * a.Hkv + h) * 2;
+      add(p.own_ml, p.own_o, part, all, own);
+      if (two && len + k - c * keys > kTileKeys) add(p.own_ml, p.own_o, part + 1, all, own);
     }
   }
-  const float nan = __int_as_float(0x7fffffff);
-  const bool lost = !dead && len + i > p.nan_from[(long long)b * a.Hkv + h];
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t v[E];
+  uint16_t* op = static_cast<uint16_t*>(a.out) + b * a.o_seq + i * a.o_pos + hq * a.o_head;
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = __bfloat16_as_ushort(__float2bfloat16_rn(dead || lost ? nan : acc[e] * inv));
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(op) = make_uint2(v[0] | ((uint32_t)v[1] << 16), v[2] | ((uint32_t)v[3] << 16));
-  else
-    *reinterpret_cast<uint32_t*>(op) = v[0] | ((uint32_t)v[1] << 16);
-  if (a.lse && lane == 0) a.lse[id] = dead ? nan : (l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2);
+  for (int q = 0; q < N; ++q) {
+    uint2 w = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+    if (!dead && !lost)
+      w = make_uint2(tc::pack_bf16x2(acc[q][0] * inv, acc[q][1] * inv), tc::pack_bf16x2(acc[q][2] * inv, acc[q][3] * inv));
+    *reinterpret_cast<uint2*>(op + (4 * q + sub) * 4) = w;
+  }
+  if (a.lse && sub == 0)
+    a.lse[(long long)bi * a.Hq + hq] = dead ? nan : (l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2);
 }
 
 template <typename... A>
@@ -825,7 +879,7 @@ static cudaError_t run(const Args& p, cudaStream_t st) {
   if (e == cudaSuccess) e = launch(part_kernel<D>, (unsigned)p.grid, kThreads, Shape<D>::kSmem, st, p);
   const long long rows = (long long)p.a.B * p.Q * p.a.Hq;
   if (e == cudaSuccess)
-    e = launch(merge_kernel<D>, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps), 32 * kMergeWarps, 0, st, p);
+    e = launch(merge_kernel<D>, (unsigned)((rows * 4 + kMergeThreads - 1) / kMergeThreads), kMergeThreads, 0, st, p);
   return e;
 }
 
