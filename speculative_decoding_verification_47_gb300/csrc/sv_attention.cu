@@ -17,8 +17,8 @@
 //  2. part_kernel: persistent, one CTA per SM.  An item is up to 256 query rows
 //     (two streams of 128) over a run of keys in tiles of 128: S = Q K^T and
 //     O += P V with tcgen05, S, P and O in tensor memory, K and V through a ring of
-//     tiles in shared memory filled by 16-byte asynchronous copies row by row (a
-//     page may have any size and stride, and rows past the end become zeros).
+//     tiles in shared memory.  Pages of a power of two from 8 tokens on arrive as
+//     boxes of the TMA engine; other pages row by row in 16-byte asynchronous copies.
 //     With 128 rows or fewer the two streams take alternate key tiles instead.
 //  3. merge_kernel: the parts of each row, in a fixed order, to out and lse.
 #include <cstdint>
@@ -82,6 +82,7 @@ __host__ inline Layout layout(int B, int K, int Hq, int Hkv, int D, long long pr
 
 struct Args {
   AttentionLaunch a;
+  int box;  // tokens of one TMA box, 0: copies by row
   int G, Q, row_tiles, grid;  // heads per key head, K + 1, item tiles of a sequence's rows, CTAs of part_kernel
   uint32_t* head;
   int* qrow;      // compact query -> b * Q + i
@@ -313,11 +314,13 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    part_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV) {
   using S = Shape<D>;
   constexpr uint32_t kIdS = tc::idesc(false, false, 128, kTileKeys), kIdO = tc::idesc(false, true, 128, D);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2],
+  __shared__ __align__(8) uint64_t full[kSlots], raw[kSlots], empty[kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2],
       item_full[2], item_empty[2];
   __shared__ Item items[2];
   __shared__ uint32_t tmem_base;
@@ -329,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], 32);
+      mbar_init(&raw[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
   // The items pass through two slots, written ahead by warp 9.
   auto fetch = [&](int n) {  // item n of this CTA, read by a whole warp
     // (word by word: as a structure it would live in local memory)
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&item_full[n & 1], (uint32_t)((n >> 1) & 1)));
+    const bool ok = __all_sync(0xffffffffu, tc::wait_bounded(&item_full[n & 1], (uint32_t)((n >> 1) & 1)));
     if (!ok) failed = 1;
     const int4* from = reinterpret_cast<const int4*>(&items[n & 1]);
     const int4 w0 = from[0], w1 = from[1], w2 = from[2];
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
     fence_async();
   };
   auto wait = [&](uint64_t* bar, int phase) {
-    if (mbar_wait_bounded(bar, (uint32_t)(phase & 1))) return true;
+    if (tc::wait_bounded(bar, (uint32_t)(phase & 1))) return true;
     failed = 1;
     return false;
   };
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
     } else if (warp > 10) {
       // ---- K and V: a warp per slot of the ring ----
       const int slot = warp - 11;
-      int turn = 0, use = 0;  // tiles of all slots before this item; of this one
+      int turn = 0, use = 0, looks = 0;  // tiles of all slots before this item; of this one; of those looked at
       bool ok = true;
       constexpr int kWords = D / 8, kRows = 32 / kWords;
       const int c = lane % kWords, sub = lane / kWords;
@@ -462,46 +466,80 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
             is_v = y >= both || (y & 1) == 0;
             j = y >= both ? (it.tiles - d) + (y - both) : (is_v ? y >> 1 : (y >> 1) + d);
           }
-          const uint16_t* pool = static_cast<const uint16_t*>(is_v ? a.v : a.k) + it.h * a.head + c * 8;
-          // this lane finds the pages of rows lane, lane + 32, ...
-          long long at[4];
+          const int first = it.key0 + j * kTileKeys, keys_left = it.keys - j * kTileKeys;
+          const int end = keys_left < kTileKeys ? keys_left : kTileKeys;
+          int drafted = it.kind == 1 && is_v ? it.len - first : kTileKeys;  // first row of a drafted token's value
+          if (drafted < 0) drafted = 0;
+          auto page_of = [&](int key, int& off) {  // the page's id, -1 if it is not one
+            const int pg = key / a.page_size;
+            off = key - pg * a.page_size;
+            const int id = it.kind == 0 ? a.prefix_pages[pg] : a.table[(long long)it.b * a.max_pages + pg];
+            if ((unsigned)id < (unsigned)a.num_pages) return id;
+            if (it.kind == 0)
+              p.head[H_BAD_PREFIX] = 1;
+            else
+              atomicOr(&p.stat[it.b], SV_FLAG_BAD_PAGE);
+            atomicOr(&p.head[H_FLAGS], SV_FLAG_BAD_PAGE);
+            return -1;
+          };
+          // rows of V to be looked at once they have landed: drafted tokens', and those
+          // past the end, which a box brings along
+          const bool look = drafted < end || (p.box && is_v && end < kTileKeys);
+          if (p.box) {
+            // a lane per box: 64 columns of p.box tokens
+            const int at = lane / S::kHalves * p.box, half = lane % S::kHalves;
+            int off = 0, id = -1;
+            if (at < end) id = page_of(first + at, off);
+            if (use > 0) ok = __all_sync(0xffffffffu, wait(&empty[slot], use - 1));
+            if (!ok) break;
+            const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, id >= 0)) * p.box * 128);
+            uint64_t* bar = look ? &raw[slot] : &full[slot];
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            __syncwarp();
+            if (id >= 0)
+              tc::tma_load_4d(ring + slot * S::kTileBytes + half * (kTileKeys * 128) + at * 128, is_v ? &tmV : &tmK,
+                              half * 64, off, it.h, id, bar);
+            if (look) {
+              ok = __all_sync(0xffffffffu, wait(&raw[slot], looks++));
+              if (!ok) break;
+              for (int r = end + sub; r < kTileKeys; r += kRows)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 base + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                             "r"(0)
+                             : "memory");
+              fence_async();
+            } else if (lane != 0) {
+              mbar_arrive(&full[slot]);
+            }
+          } else {
+            const uint16_t* pool = static_cast<const uint16_t*>(is_v ? a.v : a.k) + it.h * a.head + c * 8;
+            // this lane finds the places of rows lane, lane + 32, ...
+            long long at[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int r = u * 32 + lane, key = it.key0 + j * kTileKeys + r;
-            at[u] = -1;
-            if (j * kTileKeys + r < it.keys) {
-              const int pg = key / a.page_size;
-              const int id = it.kind == 0 ? a.prefix_pages[pg] : a.table[(long long)it.b * a.max_pages + pg];
-              if ((unsigned)id < (unsigned)a.num_pages) {
-                at[u] = id * a.page + (long long)(key - pg * a.page_size) * a.token;
-              } else {
-                if (it.kind == 0)
-                  p.head[H_BAD_PREFIX] = 1;
-                else
-                  atomicOr(&p.stat[it.b], SV_FLAG_BAD_PAGE);
-                atomicOr(&p.head[H_FLAGS], SV_FLAG_BAD_PAGE);
+            for (int u = 0; u < 4; ++u) {
+              at[u] = -1;
+              int off;
+              if (u * 32 + lane < end) {
+                const int id = page_of(first + u * 32 + lane, off);
+                if (id >= 0) at[u] = id * a.page + off * a.token;
               }
             }
-          }
-          if (use > 0) ok = __all_sync(0xffffffffu, wait(&empty[slot], use - 1));
-          if (!ok) break;
+            if (use > 0) ok = __all_sync(0xffffffffu, wait(&empty[slot], use - 1));
+            if (!ok) break;
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll 4
-            for (int v = 0; v < 32 / kRows; ++v) {
-              const int r = u * 32 + v * kRows + sub;
-              const long long from = __shfl_sync(0xffffffffu, at[u], v * kRows + sub);
-              cp16(base + r * 128 + (((c & 7) ^ (r & 7)) << 4), pool + (from < 0 ? 0 : from), from >= 0);
-            }
-          landed();
+              for (int v = 0; v < 32 / kRows; ++v) {
+                const int r = u * 32 + v * kRows + sub;
+                const long long from = __shfl_sync(0xffffffffu, at[u], v * kRows + sub);
+                cp16(base + r * 128 + (((c & 7) ^ (r & 7)) << 4), pool + (from < 0 ? 0 : from), from >= 0);
+              }
+            landed();
+          }
           // Values of drafted tokens: positions in front of one have weight 0 there, and
           // 0 times a value that is not finite would reach their sums.  Such words
           // become zeros; the merge fails the positions that do see them.
-          const int keys_left = it.keys - j * kTileKeys;
-          int drafted = it.kind == 1 && is_v ? it.len - it.key0 - j * kTileKeys : kTileKeys;
-          if (drafted < 0) drafted = 0;
-          if (drafted < kTileKeys && drafted < keys_left) {
-            const int end = keys_left < kTileKeys ? keys_left : kTileKeys;
+          if (drafted < end) {
             __syncwarp();
 #pragma unroll 1
             for (int r = drafted + sub; r < end; r += kRows) {
@@ -512,19 +550,21 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
                            : "r"(at_s)
                            : "memory");
               if (not_finite(q.x) || not_finite(q.y) || not_finite(q.z) || not_finite(q.w)) {
-                atomicMin(&p.nan_from[(long long)it.b * a.Hkv + it.h], it.key0 + j * kTileKeys + r);
+                atomicMin(&p.nan_from[(long long)it.b * a.Hkv + it.h], first + r);
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at_s), "r"(0) : "memory");
               }
             }
             fence_async();
           }
-          mbar_arrive(&full[slot]);
+          if (look || !p.box) mbar_arrive(&full[slot]);
         }
         turn += total;
       }
     } else if (warp == 8) {
       // ---- the products: one thread issues them ----
-      int turn = 0, s_turn[2] = {0, 0}, q_uses[2] = {0, 0};
+      uint32_t slot = 0, phase = 0;  // the ring's next tile
+      uint32_t s_phase[2] = {0, 0}, q_phase[2] = {0, 0};
+      const uint32_t ring_lo = tc::desc_low(ring, kTileKeys * 128), q_lo = tc::desc_low(q_smem, 16);
       for (int n = 0;; ++n) {
         const Item it = fetch(n);
         if (it.kind < 0) break;
@@ -532,72 +572,92 @@ __global__ void __launch_bounds__(kThreads, 1) part_kernel(const Args p) {
         if (lane == 0) {
           const int T = it.tiles, d = it.ahead() < T ? it.ahead() : T;
           const bool pr = it.pair();
-          auto slot_of = [&](int x) { return (turn + x) % kSlots; };
-          auto landed = [&](int x) {
-            const bool r = wait(&full[slot_of(x)], (turn + x) / kSlots);
-            tc::fence_after();
-            return r;
+          const int q_first = pr ? 0 : n & 1, q_last = pr ? 1 : n & 1;
+          struct Tile {
+            uint32_t lo, empty;
           };
-          auto free_slot = [&](int x) { tc::commit<1>(smem_addr(&empty[slot_of(x)])); };
-          auto scores = [&](int s, int x) {  // S_s = Q K^T, K in turn x
-            const uint32_t kb = ring + slot_of(x) * S::kTileBytes, qb = q_smem + (pr ? s : n & 1) * S::kTileBytes;
+          auto take = [&]() {  // the next tile, once it has landed
+            if (ok) ok = wait(&full[slot], (int)phase);
+            tc::fence_after();
+            const Tile t = {ring_lo + slot * (S::kTileBytes >> 4), smem_addr(&empty[slot])};
+            if (++slot == kSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
+            return t;
+          };
+          auto scores = [&](int s, const Tile& k) {  // S_s = Q K^T
+            const uint32_t a_lo = q_lo + (pr ? s : n & 1) * (S::kTileBytes >> 4), to = tmem + kColS + s * kStreamCols;
 #pragma unroll
             for (int q = 0; q < D / 16; ++q) {
-              const uint32_t off = (q >> 2) * (kTileKeys * 128) + (q & 3) * 32;
-              tc::mma<1, false>(tmem + kColS + s * kStreamCols, tc::desc_sw128(qb + off, 16, 1024),
-                                tc::desc_sw128(kb + off, 16, 1024), kIdS, q != 0);
+              const uint32_t off = (q >> 2) * (kTileKeys * 128 >> 4) + (q & 3) * 2;
+              tc::mma_low(to, a_lo + off, k.lo + off, kIdS, q != 0);
             }
             tc::commit<1>(smem_addr(&s_full[s]));
           };
-          auto values = [&](int s, int x, bool acc) {  // O_s += P_s V, V in turn x
-            const uint32_t vb = ring + slot_of(x) * S::kTileBytes;
+          auto values = [&](int s, const Tile& v, bool acc) {  // O_s += P_s V
+            const uint32_t to = tmem + kColO + s * kStreamCols, from = tmem + kColS + s * kStreamCols;
 #pragma unroll
             for (int q = 0; q < kTileKeys / 16; ++q)
-              tc::mma_ts(tmem + kColO + s * kStreamCols, tmem + kColS + s * kStreamCols + 8 * q,
-                         tc::desc_sw128(vb + q * 2048, kTileKeys * 128, 1024), kIdO, acc || q != 0);
+              tc::mma_ts_low(to, from + 8 * q, v.lo + q * (2048 >> 4), kIdO, acc || q != 0);
           };
-          const int q_first = pr ? 0 : n & 1, q_last = pr ? 1 : n & 1;
+          auto weights = [&](int s) {  // P_s is ready
+            if (ok) ok = wait(&p_ready[s], (int)s_phase[s]);
+            s_phase[s] ^= 1;
+            tc::fence_after();
+          };
           auto free_q = [&]() {
             for (int h = q_first; h <= q_last; ++h) tc::commit<1>(smem_addr(&q_empty[h]));
           };
-          for (int h = q_first; h <= q_last && ok; ++h) ok = wait(&q_full[h], q_uses[h]++);
+          for (int h = q_first; h <= q_last && ok; ++h) {
+            ok = wait(&q_full[h], (int)q_phase[h]);
+            q_phase[h] ^= 1;
+          }
           tc::fence_after();
-          int x = 0;
-          for (; x < d && ok; ++x) {
-            ok = landed(x);
+          for (int x = 0; x < d && ok; ++x) {
+            const Tile k = take();
             if (!ok) break;
-            if (pr) {
-              scores(0, x);
-              scores(1, x);
-            } else {
-              scores(x, x);
-            }
-            free_slot(x);
+            scores(pr ? 0 : x, k);
+            if (pr) scores(1, k);
+            tc::commit<1>(k.empty);
             if (d == T && x == T - 1) free_q();
           }
           for (int j = 0; j < T && ok; ++j) {
-            const int xv = x++, xk = j + d < T ? x++ : -1;
-            ok = landed(xv) && (xk < 0 || landed(xk));
-            for (int s = pr ? 0 : j & 1; s <= (pr ? 1 : j & 1) && ok; ++s) {
-              ok = wait(&p_ready[s], s_turn[s]++);
-              tc::fence_after();
-              if (!ok) break;
-              values(s, xv, pr ? j > 0 : j > 1);
-              if (xk >= 0)
-                scores(s, xk);
-              else
-                tc::commit<1>(smem_addr(&o_full[s]));
-            }
+            // O_s += P_s(j) V_j, then the next scores over P's place (the products of one
+            // thread run in order)
+            const Tile v = take();
+            const bool more = j + d < T;
+            Tile k;
+            const int s0 = pr ? 0 : j & 1;
+            weights(s0);
             if (!ok) break;
-            free_slot(xv);
-            if (xk >= 0) {
-              free_slot(xk);
+            values(s0, v, pr ? j > 0 : j > 1);
+            if (more) {
+              k = take();
+              if (!ok) break;
+              scores(s0, k);
+            } else {
+              tc::commit<1>(smem_addr(&o_full[s0]));
+            }
+            if (pr) {
+              weights(1);
+              if (!ok) break;
+              values(1, v, j > 0);
+              tc::commit<1>(v.empty);
+              if (more)
+                scores(1, k);
+              else
+                tc::commit<1>(smem_addr(&o_full[1]));
+            } else {
+              tc::commit<1>(v.empty);
+            }
+            if (more) {
+              tc::commit<1>(k.empty);
               if (j + d == T - 1) free_q();
             }
           }
         }
         if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-        turn += 2 * it.tiles;
       }
     }
   } else {
@@ -850,7 +910,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
 }
 
 template <typename... A>
-static cudaError_t launch(void (*k)(A...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const Args& p) {
+static cudaError_t launch(void (*k)(A...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const A&... p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
@@ -861,11 +921,11 @@ static cudaError_t launch(void (*k)(A...), unsigned grid, unsigned threads, size
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, p);
+  return cudaLaunchKernelEx(&cfg, k, p...);
 }
 
 template <int D>
-static cudaError_t run(const Args& p, cudaStream_t st) {
+static cudaError_t run(const Args& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
   static std::atomic<int> ready[kMaxDevices];
   const int d = current_device();
   if (d < 0) return cudaErrorInvalidDevice;
@@ -876,11 +936,21 @@ static cudaError_t run(const Args& p, cudaStream_t st) {
     ready[d].store(1, std::memory_order_release);
   }
   cudaError_t e = launch(plan_kernel, 1, kPlanThreads, 0, st, p);
-  if (e == cudaSuccess) e = launch(part_kernel<D>, (unsigned)p.grid, kThreads, Shape<D>::kSmem, st, p);
+  if (e == cudaSuccess) e = launch(part_kernel<D>, (unsigned)p.grid, kThreads, Shape<D>::kSmem, st, p, k, v);
   const long long rows = (long long)p.a.B * p.Q * p.a.Hq;
   if (e == cudaSuccess)
     e = launch(merge_kernel<D>, (unsigned)((rows * 4 + kMergeThreads - 1) / kMergeThreads), kMergeThreads, 0, st, p);
   return e;
+}
+
+// The pool as a 4-D tensor map: 64 of D, `box` tokens of a page, key head, page.
+static bool pool_map(tc::EncodeTiledFn enc, CUtensorMap* map, const void* pool, const AttentionLaunch& a, int box) {
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)a.token * 2, (cuuint64_t)a.head * 2, (cuuint64_t)a.page * 2};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, boxes, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace att
@@ -914,7 +984,16 @@ int attention_launch(const AttentionLaunch& L, std::string* err) {
   p.own_o = reinterpret_cast<float*>(base + w.own_o);
   p.own_slots = w.own_slots;
   cudaStream_t st = static_cast<cudaStream_t>(L.stream);
-  const cudaError_t e = L.D == 128 ? att::run<128>(p, st) : att::run<64>(p, st);
+  // TMA boxes hold whole eights of rows (the swizzle's period) and divide a tile
+  CUtensorMap k = {}, v = {};
+  p.box = 0;
+  if (L.page_size >= 8 && (L.page_size & (L.page_size - 1)) == 0) {
+    tc::EncodeTiledFn enc = tc::encoder(err);
+    if (!enc) return SV_ERR_CUDA;
+    const int box = L.page_size < att::kTileKeys ? L.page_size : att::kTileKeys;
+    if (att::pool_map(enc, &k, L.k, L, box) && att::pool_map(enc, &v, L.v, L, box)) p.box = box;
+  }
+  const cudaError_t e = L.D == 128 ? att::run<128>(p, k, v, st) : att::run<64>(p, k, v, st);
   if (e != cudaSuccess) {
     *err = std::string("attention launch: ") + cudaGetErrorString(e);
     return SV_ERR_CUDA;

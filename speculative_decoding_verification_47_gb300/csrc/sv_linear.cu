@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (first) {  // the next accumulator, once the epilogue has left it
             ++i;
             b = i % NB;
-            if (i >= NB && !tc::wait_cluster_bounded(&acce[b], (uint32_t)((i / NB - 1) & 1))) {
+            if (i >= NB && !tc::wait_bounded<true>(&acce[b], (uint32_t)((i / NB - 1) & 1))) {
               ok = false;
               break;
             }

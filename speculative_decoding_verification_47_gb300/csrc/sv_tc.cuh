@@ -48,11 +48,21 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
   }
 }
 
-// the same with A (bf16 pairs, one row per lane) from tensor memory
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-               " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-               "r"(a), "l"(b), "r"(id), "r"(acc)
+// The same for bf16, and with A (bf16 pairs, one row per lane) from tensor memory,
+// with descriptors whose high word is kDescHigh given by their low words: in a loop of small products the issuing thread's arithmetic
+// counts (a product of 128 x 128 x 16 takes 64 clocks).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ void mma_low(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
+               "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHigh)
+               : "memory");
+}
+__device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}" ::"r"(d),
+               "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHigh)
                : "memory");
 }
 
@@ -147,6 +157,15 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// Box of a 4-D tensor map.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -158,20 +177,37 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 }
 
 // Arrival on a barrier of another CTA of the cluster, releasing this thread's
-// earlier operations at cluster scope; and the bounded wait that acquires them.
+// earlier operations at cluster scope.
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool wait_cluster_bounded(uint64_t* bar, uint32_t parity, uint32_t limit = 2048) {
-  for (uint32_t it = 0; it < limit; ++it) {
-    uint32_t ok;
+
+// Bounded waits: for the completion of the phase of this parity, at most about a
+// second (kWaitClocks).  Without a suspend-time hint: a thread that the hint put to
+// sleep woke up to a thousand clocks late.
+constexpr long long kWaitClocks = 2000000000LL;
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (CLUSTER)
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(500000u)
+        : "r"(smem_addr(bar)), "r"(parity)
         : "memory");
-    if (ok) return true;
-  }
+  else
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(smem_addr(bar)), "r"(parity)
+                 : "memory");
+  return ok != 0;
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, long long clocks = kWaitClocks) {
+  if (try_wait<CLUSTER>(bar, parity)) return true;
+  const long long start = clock64();
+  while (clock64() - start < clocks)
+    if (try_wait<CLUSTER>(bar, parity)) return true;
   return false;
 }
 
