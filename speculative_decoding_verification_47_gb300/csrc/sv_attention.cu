@@ -313,6 +313,12 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
   return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     part_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMap tmK,
@@ -320,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<D>;
   constexpr uint32_t kIdS = tc::idesc(false, false, 128, kTileKeys), kIdO = tc::idesc(false, true, 128, D);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kSlots], raw[kSlots], empty[kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2],
+  __shared__ __align__(8) uint64_t full[kSlots], raw[kSlots], empty[kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2],
       item_full[2], item_empty[2];
   __shared__ Item items[2];
   __shared__ uint32_t tmem_base;
@@ -339,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[s], 32);
       mbar_init(&q_empty[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_ready[s], 128);
+      mbar_init(&p_ready[s][0], 128);
+      mbar_init(&p_ready[s][1], 128);
       mbar_init(&o_full[s], 1);
       mbar_init(&item_full[s], 1);
       mbar_init(&item_empty[s], 8 + 1 + 1 + kLoaders);  // a lane of every other warp
@@ -595,16 +602,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::commit<1>(smem_addr(&s_full[s]));
           };
-          auto values = [&](int s, const Tile& v, bool acc) {  // O_s += P_s V
+          // O_s += P_s V, each half of the keys as soon as its weights are there
+          auto values = [&](int s, const Tile& v, bool acc) {
             const uint32_t to = tmem + kColO + s * kStreamCols, from = tmem + kColS + s * kStreamCols;
 #pragma unroll
-            for (int q = 0; q < kTileKeys / 16; ++q)
+            for (int q = 0; q < kTileKeys / 16; ++q) {
+              if (q % (kTileKeys / 32) == 0) {
+                if (ok) ok = wait(&p_ready[s][q / (kTileKeys / 32)], (int)s_phase[s]);
+                tc::fence_after();
+              }
               tc::mma_ts_low(to, from + 8 * q, v.lo + q * (2048 >> 4), kIdO, acc || q != 0);
-          };
-          auto weights = [&](int s) {  // P_s is ready
-            if (ok) ok = wait(&p_ready[s], (int)s_phase[s]);
+            }
             s_phase[s] ^= 1;
-            tc::fence_after();
           };
           auto free_q = [&]() {
             for (int h = q_first; h <= q_last; ++h) tc::commit<1>(smem_addr(&q_empty[h]));
@@ -629,9 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool more = j + d < T;
             Tile k;
             const int s0 = pr ? 0 : j & 1;
-            weights(s0);
-            if (!ok) break;
             values(s0, v, pr ? j > 0 : j > 1);
+            if (!ok) break;
             if (more) {
               k = take();
               if (!ok) break;
@@ -640,9 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::commit<1>(smem_addr(&o_full[s0]));
             }
             if (pr) {
-              weights(1);
-              if (!ok) break;
               values(1, v, j > 0);
+              if (!ok) break;
               tc::commit<1>(v.empty);
               if (more)
                 scores(1, k);
@@ -704,17 +711,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float top;
         {
-          float t8[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) t8[e] = worst;
+          float t[4] = {worst, worst, worst, worst};
           if (c >= 0.f) {
 #pragma unroll
-            for (int e = 0; e < kTileKeys; ++e) t8[e & 7] = fmaxf(t8[e & 7], __uint_as_float(v[e >> 5][e & 31]));
-            top = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
+            for (int e = 0; e < kTileKeys; e += 2)
+              t[e / 2 & 3] = max3(t[e / 2 & 3], __uint_as_float(v[e >> 5][e & 31]), __uint_as_float(v[e >> 5][(e & 31) + 1]));
+            top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
           } else {
 #pragma unroll
-            for (int e = 0; e < kTileKeys; ++e) t8[e & 7] = fminf(t8[e & 7], __uint_as_float(v[e >> 5][e & 31]));
-            top = fminf(fminf(fminf(t8[0], t8[1]), fminf(t8[2], t8[3])), fminf(fminf(t8[4], t8[5]), fminf(t8[6], t8[7])));
+            for (int e = 0; e < kTileKeys; ++e) t[e & 3] = fminf(t[e & 3], __uint_as_float(v[e >> 5][e & 31]));
+            top = fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
           }
         }
         // Weights are taken relative to a reference that follows the maximum only
@@ -739,28 +745,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const F2 c2 = f2_pack(c, c), ref2 = f2_pack(-ref, -ref);
+        F2 sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float x = ex2(__fmaf_rn(__uint_as_float(v[q][e]), c, -ref));
-            float y = ex2(__fmaf_rn(__uint_as_float(v[q][e + 1]), c, -ref));
+            float x, y;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])), c2, ref2), x, y);
+            x = ex2(x);
+            y = ex2(y);
             if (!all) {
               if (32 * q + e >= vis) x = 0.f;
               if (32 * q + e + 1 >= vis) y = 0.f;
             }
-            sum[e & 2] += x;
-            sum[(e & 2) + 1] += y;
+            sum[e / 2 & 1] = f2_add(sum[e / 2 & 1], f2_pack(x, y));
             w[e >> 1] = tc::pack_bf16x2(x, y);
           }
           tc::st16(col_s + 16 * q, w);  // over scores that this thread has read
+          if (q & 1) {
+            tc::st_wait();
+            tc::fence_before();
+            mbar_arrive(&p_ready[s][q >> 1]);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc::st_wait();
-        tc::fence_before();
-        mbar_arrive(&p_ready[s]);
+        float a0, a1, b0, b1;
+        f2_unpack(sum[0], a0, a1);
+        f2_unpack(sum[1], b0, b1);
+        l += (a0 + a1) + (b0 + b1);
       }
       if (!ok) break;
       ok = __all_sync(0xffffffffu, wait(&o_full[s], o_turn));
