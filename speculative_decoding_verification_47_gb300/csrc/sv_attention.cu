@@ -673,7 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t col_s = lanes + kColS + s * kStreamCols, col_o = lanes + kColO + s * kStreamCols;
-    const float c = a.scale * kLog2e;
+    // (a scale of 0 as one too small to be seen: a masked score of -inf then still has weight 0)
+    const float c = a.scale == 0.f ? 1e-30f : a.scale * kLog2e;
     const float worst = c >= 0.f ? -INFINITY : INFINITY;
     int s_turn = 0, o_turn = 0;
     bool ok = true;
@@ -756,10 +757,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             f2_unpack(f2_fma(f2_pack(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])), c2, ref2), x, y);
             x = ex2(x);
             y = ex2(y);
-            if (!all) {
-              if (32 * q + e >= vis) x = 0.f;
-              if (32 * q + e + 1 >= vis) y = 0.f;
-            }
             sum[e / 2 & 1] = f2_add(sum[e / 2 & 1], f2_pack(x, y));
             w[e >> 1] = tc::pack_bf16x2(x, y);
           }
