@@ -215,7 +215,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
 // ---------------------------------------------------------------------------
 // 2. The parts.
 // ---------------------------------------------------------------------------
-constexpr int kThreads = 512;  // warps 0-3, 4-7: softmax of stream 0, 1; 8: MMA; 9: items; 10: Q; 11-15: K and V
+// Warps 0-3, 4-7: softmax of stream 0, 1; 8, 9: their products (one issuing thread
+// alone spends as long on its waits and commits as on the products); 10: items and
+// Q; 11-15: K and V.
+constexpr int kThreads = 512;
 constexpr int kSlots = 5;
 constexpr int kLoaders = kSlots;  // a warp per slot of the ring: it waits for its own tile's release, never for an older one
 // The block is launched with 128 registers a thread; the softmax warps keep a row's
@@ -339,17 +342,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], 32);
       mbar_init(&raw[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);  // (both streams)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 32);
-      mbar_init(&q_empty[s], 1);
+      mbar_init(&q_empty[s], 2);
       mbar_init(&s_full[s], 1);
       mbar_init(&p_ready[s][0], 128);
       mbar_init(&p_ready[s][1], 128);
       mbar_init(&o_full[s], 1);
       mbar_init(&item_full[s], 1);
-      mbar_init(&item_empty[s], 8 + 1 + 1 + kLoaders);  // a lane of every other warp
+      mbar_init(&item_empty[s], 8 + 2 + kLoaders);  // a lane of every other warp
     }
     failed = 0;
     fence_mbar_init();
@@ -362,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   pdl_wait();
 
-  // The items pass through two slots, written ahead by warp 9.
-  auto fetch = [&](int n) {  // item n of this CTA, read by a whole warp
+  // The items pass through two slots, written ahead by warp 10.
+  auto peek = [&](int n) {  // item n of this CTA, read by a whole warp
     // (word by word: as a structure it would live in local memory)
     const bool ok = __all_sync(0xffffffffu, tc::wait_bounded(&item_full[n & 1], (uint32_t)((n >> 1) & 1)));
     if (!ok) failed = 1;
@@ -380,6 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     got.tiles = w1.w;
     got.slot = w2.x;
     got.len = w2.y;
+    return got;
+  };
+  auto fetch = [&](int n) {
+    const Item got = peek(n);
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_empty[n & 1]);
     return got;
@@ -396,30 +403,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 9) {
-      // ---- the items ----
+    if (warp == 10) {
+      // ---- the items, one ahead, and Q: 128 rows to a half of its place once the
+      // scores of the half's last item are done; a lane finds one row of each 32, then
+      // the warp copies them ----
       Feed feed;
       feed.left = 2;
       feed.list = (int)blockIdx.x < (int)p.head[H_PRE_CTAS] ? 0 : 1;
-      if (lane == 0) {
-        for (int n = 0;; ++n) {
-          const Item it = feed.next(p);
-          if (n >= 2 && !wait(&item_empty[n & 1], (n >> 1) - 1)) break;
-          items[n & 1] = it;
-          mbar_arrive(&item_full[n & 1]);
-          if (it.kind < 0) break;
-        }
-      }
-    } else if (warp == 10) {
-      // ---- Q: 128 rows to a half of its place once the scores of the half's last item
-      // are done; a lane finds one row of each 32, then the warp copies them ----
-      int q_uses[2] = {0, 0};
+      uint32_t q_uses[2] = {0, 0};
       bool ok = true;
       constexpr int kWords = D / 8, kRows = 32 / kWords;  // 16-byte words of a row, rows of one instruction
       const int c = lane % kWords, sub = lane / kWords;
       const uint16_t* from_q = static_cast<const uint16_t*>(a.q) + c * 8;
+      auto publish = [&](int n) {
+        if (n >= 2 && !__all_sync(0xffffffffu, wait(&item_empty[n & 1], (n >> 1) - 1))) return false;
+        if (lane == 0) {
+          items[n & 1] = feed.next(p);
+          mbar_arrive(&item_full[n & 1]);
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = publish(0);
       for (int n = 0; ok; ++n) {
-        const Item it = fetch(n);
+        const Item it = peek(n);
         if (it.kind < 0) break;
         const int q_first = it.pair() ? 0 : n & 1, q_last = it.pair() ? 1 : n & 1;
 #pragma unroll 1
@@ -436,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               at[u] = b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head;
             }
           }
-          ok = __all_sync(0xffffffffu, wait(&q_empty[h], q_uses[h]++ - 1));
+          ok = __all_sync(0xffffffffu, wait(&q_empty[h], (int)q_uses[h]++ - 1));
           if (!ok) break;
           const uint32_t base = q_smem + h * S::kTileBytes + (c >> 3) * (kTileKeys * 128);
 #pragma unroll
@@ -450,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           landed();
           mbar_arrive(&q_full[h]);
         }
+        if (ok) ok = publish(n + 1);
       }
     } else if (warp > 10) {
       // ---- K and V: a warp per slot of the ring ----
@@ -567,11 +575,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         turn += total;
       }
-    } else if (warp == 8) {
-      // ---- the products: one thread issues them ----
+    } else {
+      // ---- the products of one stream, issued by one thread ----
+      const int s = warp - 8;
       uint32_t slot = 0, phase = 0;  // the ring's next tile
-      uint32_t s_phase[2] = {0, 0}, q_phase[2] = {0, 0};
-      const uint32_t ring_lo = tc::desc_low(ring, kTileKeys * 128), q_lo = tc::desc_low(q_smem, 16);
+      uint32_t p_phase = 0, q_phase[2] = {0, 0};
+      const uint32_t ring_lo = tc::desc_low(ring, kTileKeys * 128);
+      const uint32_t col_s = tmem + kColS + s * kStreamCols, col_o = tmem + kColO + s * kStreamCols;
       for (int n = 0;; ++n) {
         const Item it = fetch(n);
         if (it.kind < 0) break;
@@ -579,88 +589,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           const int T = it.tiles, d = it.ahead() < T ? it.ahead() : T;
           const bool pr = it.pair();
-          const int q_first = pr ? 0 : n & 1, q_last = pr ? 1 : n & 1;
+          const int mine = pr ? s : n & 1;  // half of Q's place
+          const uint32_t q_lo = tc::desc_low(q_smem, 16) + mine * (S::kTileBytes >> 4);
           struct Tile {
-            uint32_t lo, empty;
+            uint32_t lo;
+            uint64_t* empty;
           };
           auto take = [&]() {  // the next tile, once it has landed
             if (ok) ok = wait(&full[slot], (int)phase);
-            tc::fence_after();
-            const Tile t = {ring_lo + slot * (S::kTileBytes >> 4), smem_addr(&empty[slot])};
+            const Tile t = {ring_lo + slot * (S::kTileBytes >> 4), &empty[slot]};
             if (++slot == kSlots) {
               slot = 0;
               phase ^= 1;
             }
             return t;
           };
-          auto scores = [&](int s, const Tile& k) {  // S_s = Q K^T
-            const uint32_t a_lo = q_lo + (pr ? s : n & 1) * (S::kTileBytes >> 4), to = tmem + kColS + s * kStreamCols;
+          auto scores = [&](const Tile& k) {  // S = Q K^T
+            tc::fence_after();
 #pragma unroll
             for (int q = 0; q < D / 16; ++q) {
               const uint32_t off = (q >> 2) * (kTileKeys * 128 >> 4) + (q & 3) * 2;
-              tc::mma_low(to, a_lo + off, k.lo + off, kIdS, q != 0);
+              tc::mma_low(col_s, q_lo + off, k.lo + off, kIdS, q != 0);
             }
             tc::commit<1>(smem_addr(&s_full[s]));
           };
-          // O_s += P_s V, each half of the keys as soon as its weights are there
-          auto values = [&](int s, const Tile& v, bool acc) {
-            const uint32_t to = tmem + kColO + s * kStreamCols, from = tmem + kColS + s * kStreamCols;
+          auto values = [&](const Tile& v, bool acc) {  // O += P V, half of the keys as soon as their weights are there
 #pragma unroll
             for (int q = 0; q < kTileKeys / 16; ++q) {
               if (q % (kTileKeys / 32) == 0) {
-                if (ok) ok = wait(&p_ready[s][q / (kTileKeys / 32)], (int)s_phase[s]);
+                if (ok) ok = wait(&p_ready[s][q / (kTileKeys / 32)], (int)p_phase);
                 tc::fence_after();
               }
-              tc::mma_ts_low(to, from + 8 * q, v.lo + q * (2048 >> 4), kIdO, acc || q != 0);
+              tc::mma_ts_low(col_o, col_s + 8 * q, v.lo + q * (2048 >> 4), kIdO, acc || q != 0);
             }
-            s_phase[s] ^= 1;
+            p_phase ^= 1;
           };
-          auto free_q = [&]() {
-            for (int h = q_first; h <= q_last; ++h) tc::commit<1>(smem_addr(&q_empty[h]));
-          };
-          for (int h = q_first; h <= q_last && ok; ++h) {
+          // both streams wait for every tile and every half of Q in use, and release
+          // them once each: a release can so never count for an earlier use
+          for (int h = pr ? 0 : mine; h <= (pr ? 1 : mine) && ok; ++h) {
             ok = wait(&q_full[h], (int)q_phase[h]);
             q_phase[h] ^= 1;
           }
-          tc::fence_after();
+          int left = it.stream_tiles(s);  // scores to come
+          auto scored = [&](const Tile& k) {
+            scores(k);
+            tc::commit<1>(smem_addr(k.empty));
+            if (--left == 0) tc::commit<1>(smem_addr(&q_empty[mine]));
+          };
+          if (ok && pr) mbar_arrive(&q_empty[s ^ 1]);
+          if (ok && left == 0) mbar_arrive(&q_empty[mine]);
           for (int x = 0; x < d && ok; ++x) {
             const Tile k = take();
             if (!ok) break;
-            scores(pr ? 0 : x, k);
-            if (pr) scores(1, k);
-            tc::commit<1>(k.empty);
-            if (d == T && x == T - 1) free_q();
+            if (pr || x == s)
+              scored(k);
+            else
+              mbar_arrive(k.empty);
           }
           for (int j = 0; j < T && ok; ++j) {
-            // O_s += P_s(j) V_j, then the next scores over P's place (the products of one
+            // O += P(j) V_j, then the next scores over P's place (the products of one
             // thread run in order)
             const Tile v = take();
-            const bool more = j + d < T;
-            Tile k;
-            const int s0 = pr ? 0 : j & 1;
-            values(s0, v, pr ? j > 0 : j > 1);
             if (!ok) break;
-            if (more) {
-              k = take();
+            const bool own = pr || (j & 1) == s, more = j + d < T;
+            if (own) {
+              values(v, pr ? j > 0 : j > 1);
+              tc::commit<1>(smem_addr(v.empty));
               if (!ok) break;
-              scores(s0, k);
+              if (!more) tc::commit<1>(smem_addr(&o_full[s]));
             } else {
-              tc::commit<1>(smem_addr(&o_full[s0]));
+              mbar_arrive(v.empty);
             }
-            if (pr) {
-              values(1, v, j > 0);
+            if (more) {
+              const Tile k = take();
               if (!ok) break;
-              tc::commit<1>(v.empty);
-              if (more)
-                scores(1, k);
+              if (own)
+                scored(k);
               else
-                tc::commit<1>(smem_addr(&o_full[1]));
-            } else {
-              tc::commit<1>(v.empty);
-            }
-            if (more) {
-              tc::commit<1>(k.empty);
-              if (j + d == T - 1) free_q();
+                mbar_arrive(k.empty);
             }
           }
         }
