@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<D>;
   constexpr uint32_t kIdS = tc::idesc(false, false, 128, kTileKeys), kIdO = tc::idesc(false, true, 128, D);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kSlots], raw[kSlots], empty[kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2],
+  __shared__ __align__(8) uint64_t full[kSlots], raw[kSlots], empty[kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], next[2],
       item_full[2], item_empty[2];
   __shared__ Item items[2];
   __shared__ uint32_t tmem_base;
@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[s], 32);
       mbar_init(&q_empty[s], 2);
       mbar_init(&s_full[s], 1);
+      mbar_init(&next[s], 1);
       mbar_init(&p_ready[s][0], 128);
       mbar_init(&p_ready[s][1], 128);
       mbar_init(&o_full[s], 1);
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the products of one stream, issued by one thread ----
       const int s = warp - 8;
       uint32_t slot = 0, phase = 0;  // the ring's next tile
-      uint32_t p_phase = 0, q_phase[2] = {0, 0};
+      uint32_t p_phase = 0, next_phase = 0, q_phase[2] = {0, 0};
       const uint32_t ring_lo = tc::desc_low(ring, kTileKeys * 128);
       const uint32_t col_s = tmem + kColS + s * kStreamCols, col_o = tmem + kColO + s * kStreamCols;
       for (int n = 0;; ++n) {
@@ -613,11 +614,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::commit<1>(smem_addr(&s_full[s]));
           };
-          auto values = [&](const Tile& v, bool acc) {  // O += P V, half of the keys as soon as their weights are there
+          // O += P V, half of the keys as soon as their weights are there.  Two row tiles
+          // take turns with their products: left alone they fall into step, both in
+          // their softmax at the same time and then both at the tensor cores (3900
+          // clocks a tile, 2048 of them products)
+          auto values = [&](const Tile& v, bool acc, bool in_turn) {
 #pragma unroll
             for (int q = 0; q < kTileKeys / 16; ++q) {
               if (q % (kTileKeys / 32) == 0) {
                 if (ok) ok = wait(&p_ready[s][q / (kTileKeys / 32)], (int)p_phase);
+                if (q == 0 && in_turn) {
+                  if (ok) ok = wait(&next[s], (int)next_phase);
+                  next_phase ^= 1;
+                }
                 tc::fence_after();
               }
               tc::mma_ts_low(col_o, col_s + 8 * q, v.lo + q * (2048 >> 4), kIdO, acc || q != 0);
@@ -652,21 +661,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Tile v = take();
             if (!ok) break;
             const bool own = pr || (j & 1) == s, more = j + d < T;
+            Tile k;
+            if (more) k = take();
+            if (!ok) break;
             if (own) {
-              values(v, pr ? j > 0 : j > 1);
+              values(v, pr ? j > 0 : j > 1, pr && (s == 1 || j > 0));
+              if (!ok) break;
               tc::commit<1>(smem_addr(v.empty));
-              if (!ok) break;
-              if (!more) tc::commit<1>(smem_addr(&o_full[s]));
-            } else {
-              mbar_arrive(v.empty);
-            }
-            if (more) {
-              const Tile k = take();
-              if (!ok) break;
-              if (own)
+              if (more)
                 scored(k);
               else
-                mbar_arrive(k.empty);
+                tc::commit<1>(smem_addr(&o_full[s]));
+              if (pr && (s == 0 || more)) mbar_arrive(&next[s ^ 1]);
+            } else {
+              mbar_arrive(v.empty);
+              if (more) mbar_arrive(k.empty);
             }
           }
         }
