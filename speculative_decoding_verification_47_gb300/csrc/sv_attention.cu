@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<D>;
   constexpr uint32_t kIdS = tc::idesc(false, false, 128, kTileKeys), kIdO = tc::idesc(false, true, 128, D);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kSlots], raw[kSlots], empty[kSlots], q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], next[2],
+  __shared__ __align__(8) uint64_t full[kSlots], raw[kSlots], empty[kSlots], q_full[2], q_empty[2], q_go, s_full[2], p_ready[2][2], o_full[2], next[2],
       item_full[2], item_empty[2];
   __shared__ Item items[2];
   __shared__ uint32_t tmem_base;
@@ -344,8 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&raw[s], 1);
       mbar_init(&empty[s], 2);  // (both streams)
     }
+    mbar_init(&q_go, 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&q_full[s], 32);
+      mbar_init(&q_full[s], 4);  // (four runs of 32 rows)
       mbar_init(&q_empty[s], 2);
       mbar_init(&s_full[s], 1);
       mbar_init(&next[s], 1);
@@ -402,20 +403,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
+  // Rows u * 32 .. + 31 of an item's Q into half h of its place, by one warp, once `bar`
+  // says that the scores of the half's last item are done: a lane finds a row, then the warp copies the rows together.  Rows past the end stay as
+  // they are: what comes of them is never read.
+  auto load_q = [&](const Item& it, int u, int h, uint64_t* bar, int phase) {
+    constexpr int kWords = D / 8, kRows = 32 / kWords;  // 16-byte words of a row, rows of one instruction
+    const int c = lane % kWords, sub = lane / kWords, r = u * 32 + lane;
+    const uint16_t* from = static_cast<const uint16_t*>(a.q) + c * 8;
+    long long at = -1;
+    if (r < it.rows) {
+      const int row = it.row0 + r, qi = row / p.G, g = row - qi * p.G;
+      const int bi = it.kind == 0 ? p.qrow[qi] : it.b * p.Q + qi;
+      const int b = bi / p.Q, i = bi - b * p.Q;
+      at = b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head;
+    }
+    if (!__all_sync(0xffffffffu, wait(bar, phase))) return false;
+    const uint32_t to = q_smem + h * S::kTileBytes + (c >> 3) * (kTileKeys * 128);
+    if (u * 32 < it.rows) {
+#pragma unroll
+      for (int v = 0; v < 32 / kRows; ++v) {
+        const int rr = (u & 3) * 32 + v * kRows + sub;
+        const long long row_at = __shfl_sync(0xffffffffu, at, v * kRows + sub);
+        if (row_at >= 0) cp16(to + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), from + row_at, true);
+      }
+    }
+    landed();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full[h]);
+    return true;
+  };
+
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 10) {
-      // ---- the items, one ahead, and Q: 128 rows to a half of its place once the
-      // scores of the half's last item are done; a lane finds one row of each 32, then
-      // the warp copies them ----
+      // ---- the items, one ahead, and Q of the items with 128 rows or fewer ----
       Feed feed;
       feed.left = 2;
       feed.list = (int)blockIdx.x < (int)p.head[H_PRE_CTAS] ? 0 : 1;
-      uint32_t q_uses[2] = {0, 0};
+      int q_uses[2] = {0, 0};
       bool ok = true;
-      constexpr int kWords = D / 8, kRows = 32 / kWords;  // 16-byte words of a row, rows of one instruction
-      const int c = lane % kWords, sub = lane / kWords;
-      const uint16_t* from_q = static_cast<const uint16_t*>(a.q) + c * 8;
       auto publish = [&](int n) {
         if (n >= 2 && !__all_sync(0xffffffffu, wait(&item_empty[n & 1], (n >> 1) - 1))) return false;
         if (lane == 0) {
@@ -429,34 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = 0; ok; ++n) {
         const Item it = peek(n);
         if (it.kind < 0) break;
-        const int q_first = it.pair() ? 0 : n & 1, q_last = it.pair() ? 1 : n & 1;
+        if (it.pair()) {  // the ring's warps load it
+          ok = __all_sync(0xffffffffu, wait(&q_empty[0], q_uses[0]++ - 1) && wait(&q_empty[1], q_uses[1]++ - 1));
+          if (ok && lane == 0) mbar_arrive(&q_go);
+        } else {
 #pragma unroll 1
-        for (int h = q_first; h <= q_last; ++h) {
-          long long at[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int r = (h - q_first) * 128 + u * 32 + lane;
-            at[u] = -1;
-            if (r < it.rows) {
-              const int row = it.row0 + r, qi = row / p.G, g = row - qi * p.G;
-              const int bi = it.kind == 0 ? p.qrow[qi] : it.b * p.Q + qi;
-              const int b = bi / p.Q, i = bi - b * p.Q;
-              at[u] = b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head;
-            }
-          }
-          ok = __all_sync(0xffffffffu, wait(&q_empty[h], (int)q_uses[h]++ - 1));
-          if (!ok) break;
-          const uint32_t base = q_smem + h * S::kTileBytes + (c >> 3) * (kTileKeys * 128);
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-#pragma unroll 4
-            for (int v = 0; v < 32 / kRows; ++v) {
-              const int rr = u * 32 + v * kRows + sub;
-              const long long from = __shfl_sync(0xffffffffu, at[u], v * kRows + sub);
-              cp16(base + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), from_q + (from < 0 ? 0 : from), from >= 0);
-            }
-          landed();
-          mbar_arrive(&q_full[h]);
+          for (int u = 0; u < 4 && ok; ++u) ok = load_q(it, u, n & 1, &q_empty[n & 1], q_uses[n & 1] - 1);
+          ++q_uses[n & 1];
         }
         if (ok) ok = publish(n + 1);
       }
@@ -464,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- K and V: a warp per slot of the ring ----
       const int slot = warp - 11;
       int turn = 0, use = 0, looks = 0;  // tiles of all slots before this item; of this one; of those looked at
+      int pairs = 0;  // items of two row tiles so far
       bool ok = true;
       constexpr int kWords = D / 8, kRows = 32 / kWords;
       const int c = lane % kWords, sub = lane / kWords;
@@ -474,6 +480,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // K_0 .. K_{d-1}, then V_j, K_{j+d}
         const int d = it.ahead() < it.tiles ? it.ahead() : it.tiles;
         const int total = 2 * it.tiles;
+        bool q_due = it.pair();  // two row tiles: Q is loaded by these warps, behind their first tile
+        auto my_q = [&]() {
+          q_due = false;
+          for (int u = slot; u < 8 && ok; u += kSlots) ok = load_q(it, u, u >> 2, &q_go, pairs);
+          ++pairs;
+        };
         for (int x = (slot + kSlots - turn % kSlots) % kSlots; x < total; x += kSlots, ++use) {
           // which tile: x < d: K_x; else pairs (V_j, K_{j+d}) while both exist, then the last V's
           int j = x, is_v = 0;
@@ -573,7 +585,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_async();
           }
           if (look || !p.box) mbar_arrive(&full[slot]);
+          if (q_due) my_q();
+          if (!ok) break;
         }
+        if (!ok) break;
+        if (q_due) my_q();
         turn += total;
       }
     } else {
