@@ -41,7 +41,7 @@ enum { H_FLAGS, H_BAD_PREFIX, H_NEXT_PRE, H_NEXT_OWN, H_QUERIES, H_CHUNKS, H_CHU
        H_PRE_ITEMS, H_OWN_ITEMS, H_PRE_CTAS, H_WORDS = 64 };
 
 struct Layout {  // byte offsets into the workspace
-  size_t qrow, qoff, coff, chunk_of, stat, nan_from, pre_ml, pre_o, extra_ml, extra_o, own_ml, own_o, total;
+  size_t qrow, coff, chunk_of, stat, nan_from, pre_ml, pre_o, extra_ml, extra_o, own_ml, own_o, total;
   long long pre_rows, extra_rows, own_slots;
 };
 
@@ -65,7 +65,6 @@ __host__ inline Layout layout(int B, int K, int Hq, int Hkv, int D, long long pr
     return here;
   };
   w.qrow = take((size_t)Q * 4);
-  w.qoff = take((size_t)B * 4);
   w.coff = take((size_t)B * 4);
   w.chunk_of = take((size_t)(w.own_slots / (2 * Hkv)) * 4);
   w.stat = take((size_t)B * 4);
@@ -86,14 +85,12 @@ struct Args {
   int G, Q, row_tiles, grid;  // heads per key head, K + 1, item tiles of a sequence's rows, CTAs of part_kernel
   uint32_t* head;
   int* qrow;      // compact query -> b * Q + i
-  int* qoff;      // first compact query of a sequence
   int* coff;      // first chunk of a sequence
   int* chunk_of;  // chunk -> sequence
   int* stat;      // a sequence's flags
   int* nan_from;  // [B][Hkv] first own token whose drafted value is not finite
   float2 *pre_ml, *extra_ml, *own_ml;
   float *pre_o, *extra_o, *own_o;
-  long long own_slots;
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -139,34 +136,45 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
   pdl_wait();
   __syncthreads();
   const int step = 2 * kTileKeys;
-  auto look = [&](int b, int& k, int& len) {  // 0 or the sequence's flag
+  // sequence b: its flag, drafts and length (0 tokens if it is flagged)
+  auto look = [&](int b, int& k, int& len) {
     k = a.kpr ? a.kpr[b] : a.K;
     len = a.lens[b];
     if (k < 0 || k > a.K) return (int)SV_FLAG_BAD_K;
     if (len < 0 || (long long)len + k > (long long)a.max_pages * a.page_size) return (int)SV_FLAG_BAD_N;
     return 0;
   };
+  int k0 = 0, len0 = 0, bad0 = 1;  // this thread's first sequence
   unsigned long long mine = 0;
   for (int b = t; b < a.B; b += kPlanThreads) {
     int k, len;
     const int bad = look(b, k, len);
+    if (b == t) {
+      k0 = k;
+      len0 = len;
+      bad0 = bad;
+    }
     p.stat[b] = bad;
     if (bad)
       atomicOr(&flags, (unsigned)bad);
     else
       mine += (unsigned)ceil_div(len + k, step);
-    for (int h = 0; h < a.Hkv; ++h) p.nan_from[(long long)b * a.Hkv + h] = 0x7fffffff;
   }
-  if (mine) atomicAdd(&tiles2, mine);
+  for (long long e = t; e < (long long)a.B * a.Hkv; e += kPlanThreads) p.nan_from[e] = 0x7fffffff;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if ((t & 31) == 0 && mine) atomicAdd(&tiles2, mine);
   __syncthreads();
   // a chunk: long enough that all chunks together are at most kSlack per CTA beside one per sequence
   const unsigned long long units = tiles2 * (unsigned)(a.Hkv * p.row_tiles), aim = (unsigned long long)kSlack * p.grid;
-  const int per = units > aim ? (int)((units + aim - 1) / aim) : 1;  // steps of a chunk
+  int per = 1;  // steps of a chunk
+  if (units > aim) per = units < 0xffffffffull ? (int)(((unsigned)units - 1) / (unsigned)aim + 1) : (int)((units - 1) / aim + 1);
   int queries = 0, chunks = 0;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + t;
-    int k = 0, len = 0, q = 0, n = 0;
-    if (b < a.B && look(b, k, len) == 0) {
+    int k = k0, len = len0, bad = bad0, q = 0, n = 0;
+    if (b0 > 0 && b < a.B) bad = look(b, k, len);
+    if (b < a.B && bad == 0) {
       q = k + 1;
       n = ceil_div(ceil_div(len + k, step), per);
     }
@@ -175,10 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
     queries += total;
     const int ce = chunks + block_scan(n, warp_sums, total) - n;
     chunks += total;
-    if (b < a.B) {
-      p.qoff[b] = qe;
-      p.coff[b] = ce;
-    }
+    if (b < a.B) p.coff[b] = ce;
     for (int i = 0; i < q; ++i) p.qrow[qe + i] = b * p.Q + i;
     for (int c = 0; c < n; ++c) p.chunk_of[ce + c] = b;
   }
@@ -189,14 +194,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
     int splits = 0, split_tiles = 0;
     if (ptiles > 0 && row_items > 0) {
       // work in units of one stream's tile; an item is to be a kSlack-th of a CTA's share
-      const double work = 2.0 * row_items * ptiles + 2.0 * (double)units;
-      const double share = work / p.grid / kSlack;
-      split_tiles = share >= 2.0 * ptiles ? ptiles : (int)(share / 2.0);
+      const float work = 2.f * row_items * ptiles + 2.f * (float)units;
+      const float share = work / (p.grid * kSlack);
+      split_tiles = share >= 2.f * ptiles ? ptiles : (int)(share / 2.f);
       const int most = kSlack * p.grid / row_items;  // (what the partial results have room for)
       const int least = ceil_div(ptiles, most < 1 ? 1 : most);
       if (split_tiles < least) split_tiles = least;
       splits = ceil_div(ptiles, split_tiles);
-      p.head[H_PRE_CTAS] = (unsigned)(p.grid * (2.0 * row_items * ptiles / work) + 0.5);
+      p.head[H_PRE_CTAS] = (unsigned)(p.grid * (2.f * row_items * ptiles / work) + 0.5f);
     } else {
       p.head[H_PRE_CTAS] = 0;
     }
@@ -857,20 +862,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// 3. The parts of a row together: four threads per row, each with every fourth
-// quad of its columns, so that eight rows' threads read whole lines.
+// 3. The parts of a row together.  A warp has eight rows and four quads of columns
+// of each (eight rows' quads are a whole line); kGroups warps share the rows.  The
+// parts' maxima and sums are read first, so that the sum over the parts is one of
+// independent loads.
 // ---------------------------------------------------------------------------
 constexpr int kMergeThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
   const AttentionLaunch& a = p.a;
-  constexpr int N = D / 16;  // quads of a thread
+  constexpr int N = 2, kGroups = D / 16 / N;  // quads of a thread, warps per eight rows
   const float nan = __int_as_float(0x7fffffff);
   pdl_wait();
-  const long long id = ((long long)blockIdx.x * kMergeThreads + threadIdx.x) >> 2;
-  const int sub = threadIdx.x & 3, queries = p.head[H_QUERIES];
-  const long long rows = (long long)queries * p.G;
+  const int lane = threadIdx.x & 31, sub = lane & 3;
+  const unsigned wid = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const int queries = p.head[H_QUERIES], group = (int)(wid % kGroups);
+  const unsigned rows = (unsigned)queries * p.G, id = wid / kGroups * 8 + (lane >> 2);
 
   if (p.head[H_FLAGS] & (SV_FLAG_BAD_K | SV_FLAG_BAD_N)) {
     // sequences that have no rows: every position that the caller reads is NaN
@@ -885,68 +893,76 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
       }
     }
   }
-  if (id >= rows * a.Hkv) return;
+  if (rows == 0 || id >= rows * a.Hkv) return;
   const int h = (int)(id / rows);
-  const long long r = id - h * rows;
-  const int query = (int)(r / p.G), g = (int)(r - (long long)query * p.G);
+  const unsigned r = id - h * rows, query = r / p.G;
+  const int g = (int)(r - query * p.G);
   const int bi = p.qrow[query], b = bi / p.Q, i = bi - b * p.Q, hq = h * p.G + g;
-  const int k = a.kpr ? a.kpr[b] : a.K, len = a.lens[b];
-  const int splits = p.head[H_SPLITS], per = p.head[H_SPLIT_TILES], keys = p.head[H_CHUNK_KEYS], first = p.coff[b];
+  const int k = a.kpr ? a.kpr[b] : a.K, len = a.lens[b], first = p.coff[b];
+  const int splits = p.head[H_SPLITS], per = p.head[H_SPLIT_TILES], keys = p.head[H_CHUNK_KEYS];
   const bool dead = p.stat[b] || p.head[H_BAD_PREFIX];
   const bool lost = len + i > p.nan_from[(long long)b * a.Hkv + h];
-  float acc[N][4], M = -INFINITY, l = 0.f;
+
+  // every part of the row: f(maximum and sum, its quads)
+  const unsigned tile0 = r / kItemRows * kItemRows;
+  const int ptiles = ceil_div(a.prefix_len, kTileKeys), extra = rows - tile0 > 128 ? 0 : splits;
+  const int own = i * p.G + g, all = p.Q * p.G, chunks = dead ? 0 : ceil_div(len + k, keys);
+  const bool two = (k + 1) * p.G - own / kItemRows * kItemRows <= 128;
+  const int quad = (group * N * 4 + sub) * 4;
+  auto parts = [&](auto f) {
+    if (dead) return;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const long long at = ((long long)s * a.Hkv + h) * rows;
+      f(p.pre_ml + at + r, p.pre_o + at * D + (long long)quad * rows + r * 4, rows);
+    }
+#pragma unroll 4
+    for (int s = 0; s < extra; ++s)
+      if (min(per, ptiles - s * per) >= 2) {
+        const long long at = ((long long)s * a.Hkv + h) * 128;
+        f(p.extra_ml + at + (r - tile0), p.extra_o + at * D + quad * 128 + (r - tile0) * 4, 128u);
+      }
+#pragma unroll 4
+    for (int c = 0; c < 2 * chunks; ++c)
+      if ((c & 1) == 0 || (two && len + k - (c >> 1) * keys > kTileKeys)) {
+        const long long at = (((long long)(first + (c >> 1)) * a.Hkv + h) * 2 + (c & 1)) * all;
+        f(p.own_ml + at + own, p.own_o + at * D + (long long)quad * all + own * 4, (unsigned)all);
+      }
+  };
+  float M = -INFINITY;
+  parts([&](const float2* ml, const float*, unsigned) {
+    const float2 x = *ml;
+    M = x.x > M ? x.x : M;
+  });
+  float l = 0.f, acc[N][4];
 #pragma unroll
   for (int q = 0; q < N; ++q)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[q][e] = 0.f;
-  auto add = [&](const float2* ml, const float* o, long long part, long long rows_o, long long row) {
-    const float2 x = ml[part * rows_o + row];
-    float4 v[N];
-#pragma unroll
-    for (int q = 0; q < N; ++q)
-      v[q] = *reinterpret_cast<const float4*>(o + part * rows_o * D + ((4 * q + sub) * rows_o + row) * 4);
-    if (x.x == -INFINITY && x.y == 0.f) return;  // nothing seen (a NaN in l goes on)
-    const float n = x.x > M ? x.x : M, fo = M == -INFINITY ? 0.f : ex2(M - n);
-    const float fx = x.x == -INFINITY ? 1.f : ex2(x.x - n);
-    l = l * fo + x.y * fx;
+  parts([&](const float2* ml, const float* o, unsigned rows_o) {
+    const float2 x = *ml;
+    // a part that saw nothing has weight 0, whatever is there (a NaN in its sum goes on)
+    const float w = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - M);
+    l += x.y * w;
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-      acc[q][0] = acc[q][0] * fo + v[q].x * fx;
-      acc[q][1] = acc[q][1] * fo + v[q].y * fx;
-      acc[q][2] = acc[q][2] * fo + v[q].z * fx;
-      acc[q][3] = acc[q][3] * fo + v[q].w * fx;
+      const float4 v = *reinterpret_cast<const float4*>(o + (long long)q * 16 * rows_o);
+      acc[q][0] = w == 0.f ? acc[q][0] : __fmaf_rn(v.x, w, acc[q][0]);
+      acc[q][1] = w == 0.f ? acc[q][1] : __fmaf_rn(v.y, w, acc[q][1]);
+      acc[q][2] = w == 0.f ? acc[q][2] : __fmaf_rn(v.z, w, acc[q][2]);
+      acc[q][3] = w == 0.f ? acc[q][3] : __fmaf_rn(v.w, w, acc[q][3]);
     }
-    M = n;
-  };
-  if (!dead) {
-    if (splits > 0) {
-      const long long tile0 = r / kItemRows * kItemRows;
-      const bool two = rows - tile0 <= 128;
-      const int ptiles = ceil_div(a.prefix_len, kTileKeys);
-      for (int s = 0; s < splits; ++s) {
-        add(p.pre_ml, p.pre_o, (long long)s * a.Hkv + h, rows, r);
-        if (two && min(per, ptiles - s * per) >= 2)
-          add(p.extra_ml, p.extra_o, (long long)s * a.Hkv + h, 128, r - tile0);
-      }
-    }
-    const int chunks = ceil_div(len + k, keys), own = i * p.G + g, all = p.Q * p.G;
-    const bool two = (k + 1) * p.G - own / kItemRows * kItemRows <= 128;
-    for (int c = 0; c < chunks; ++c) {
-      const long long part = ((long long)(first + c) * a.Hkv + h) * 2;
-      add(p.own_ml, p.own_o, part, all, own);
-      if (two && len + k - c * keys > kTileKeys) add(p.own_ml, p.own_o, part + 1, all, own);
-    }
-  }
+  });
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* op = static_cast<uint16_t*>(a.out) + b * a.o_seq + i * a.o_pos + hq * a.o_head;
+  uint16_t* op = static_cast<uint16_t*>(a.out) + b * a.o_seq + i * a.o_pos + hq * a.o_head + quad;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
     uint2 w = make_uint2(0x7fff7fffu, 0x7fff7fffu);
     if (!dead && !lost)
       w = make_uint2(tc::pack_bf16x2(acc[q][0] * inv, acc[q][1] * inv), tc::pack_bf16x2(acc[q][2] * inv, acc[q][3] * inv));
-    *reinterpret_cast<uint2*>(op + (4 * q + sub) * 4) = w;
+    *reinterpret_cast<uint2*>(op + q * 16) = w;
   }
-  if (a.lse && sub == 0)
+  if (a.lse && sub == 0 && group == 0)
     a.lse[(long long)bi * a.Hq + hq] = dead ? nan : (l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2);
 }
 
@@ -980,7 +996,8 @@ static cudaError_t run(const Args& p, const CUtensorMap& k, const CUtensorMap& v
   if (e == cudaSuccess) e = launch(part_kernel<D>, (unsigned)p.grid, kThreads, Shape<D>::kSmem, st, p, k, v);
   const long long rows = (long long)p.a.B * p.Q * p.a.Hq;
   if (e == cudaSuccess)
-    e = launch(merge_kernel<D>, (unsigned)((rows * 4 + kMergeThreads - 1) / kMergeThreads), kMergeThreads, 0, st, p);
+    e = launch(merge_kernel<D>, (unsigned)((((rows + 7) / 8) * (D / 32) * 32 + kMergeThreads - 1) / kMergeThreads), kMergeThreads,
+               0, st, p);
   return e;
 }
 
@@ -1012,7 +1029,6 @@ int attention_launch(const AttentionLaunch& L, std::string* err) {
   char* base = static_cast<char*>(L.workspace);
   p.head = reinterpret_cast<uint32_t*>(base);
   p.qrow = reinterpret_cast<int*>(base + w.qrow);
-  p.qoff = reinterpret_cast<int*>(base + w.qoff);
   p.coff = reinterpret_cast<int*>(base + w.coff);
   p.chunk_of = reinterpret_cast<int*>(base + w.chunk_of);
   p.stat = reinterpret_cast<int*>(base + w.stat);
@@ -1023,7 +1039,6 @@ int attention_launch(const AttentionLaunch& L, std::string* err) {
   p.extra_o = reinterpret_cast<float*>(base + w.extra_o);
   p.own_ml = reinterpret_cast<float2*>(base + w.own_ml);
   p.own_o = reinterpret_cast<float*>(base + w.own_o);
-  p.own_slots = w.own_slots;
   cudaStream_t st = static_cast<cudaStream_t>(L.stream);
   // TMA boxes hold whole eights of rows (the swizzle's period) and divide a tile
   CUtensorMap k = {}, v = {};
