@@ -99,6 +99,7 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 // 1. The plan: one CTA.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
+constexpr int kSplits = 256, kItemTiles = 4;
 
 // Inclusive prefix sum over the CTA (also the total).
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
@@ -187,33 +188,53 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
     for (int i = 0; i < q; ++i) p.qrow[qe + i] = b * p.Q + i;
     for (int c = 0; c < n; ++c) p.chunk_of[ce + c] = b;
   }
-  if (t == 0) {
-    const int ptiles = ceil_div(a.prefix_len, kTileKeys);
-    const long long rows = (long long)queries * p.G;
-    const int row_items = (int)((rows + kItemRows - 1) / kItemRows) * a.Hkv;
-    int splits = 0, split_tiles = 0;
+  const int ptiles = ceil_div(a.prefix_len, kTileKeys);
+  const long long rows = (long long)queries * p.G;
+  const int row_items = (int)((rows + kItemRows - 1) / kItemRows) * a.Hkv;
+  if (t < 32) {
+    // Splits of the prefix: the one of up to kSplits for which the CTAs that its share of
+    // the work gets are done first, where an item's beginning and end (Q, the parts'
+    // stores) cost kItemTiles tiles.  The partial results have room for kSlack * grid
+    // items beside one per row item.
+    int splits = 0, split_tiles = 0, ctas = 0;
     if (ptiles > 0 && row_items > 0) {
-      // work in units of one stream's tile; an item is to be a kSlack-th of a CTA's share
-      const float work = 2.f * row_items * ptiles + 2.f * (float)units;
-      const float share = work / (p.grid * kSlack);
-      split_tiles = share >= 2.f * ptiles ? ptiles : (int)(share / 2.f);
-      const int most = kSlack * p.grid / row_items;  // (what the partial results have room for)
-      const int least = ceil_div(ptiles, most < 1 ? 1 : most);
-      if (split_tiles < least) split_tiles = least;
-      splits = ceil_div(ptiles, split_tiles);
-      p.head[H_PRE_CTAS] = (unsigned)(p.grid * (2.f * row_items * ptiles / work) + 0.5f);
-    } else {
-      p.head[H_PRE_CTAS] = 0;
+      const float pre = (float)row_items * ptiles;
+      ctas = (int)(p.grid * (pre / (pre + (float)units)) + 0.5f);
+      if (ctas < 1) ctas = 1;
+      const int most = max(1, min(ptiles, kSlack * p.grid / row_items));
+      float best = 3e38f;
+      for (int c = t + 1; c <= most && c <= kSplits; c += 32) {
+        const int tiles = ceil_div(ptiles, c), parts = ceil_div(ptiles, tiles);
+        const float cost = (float)ceil_div(row_items * parts, ctas) * (float)(tiles + kItemTiles);
+        if (cost < best) {
+          best = cost;
+          splits = parts;
+          split_tiles = tiles;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float c = __shfl_xor_sync(0xffffffffu, best, o);
+        const int s = __shfl_xor_sync(0xffffffffu, splits, o), n = __shfl_xor_sync(0xffffffffu, split_tiles, o);
+        if (c < best || (c == best && s < splits)) {
+          best = c;
+          splits = s;
+          split_tiles = n;
+        }
+      }
     }
-    p.head[H_BAD_PREFIX] = p.head[H_NEXT_PRE] = p.head[H_NEXT_OWN] = 0;
-    p.head[H_QUERIES] = queries;
-    p.head[H_CHUNKS] = chunks;
-    p.head[H_CHUNK_KEYS] = per * step;
-    p.head[H_SPLITS] = splits;
-    p.head[H_SPLIT_TILES] = split_tiles;
-    p.head[H_PRE_ITEMS] = row_items * splits;
-    p.head[H_OWN_ITEMS] = chunks * a.Hkv * p.row_tiles;
-    p.head[H_FLAGS] = flags;
+    if (t == 0) {
+      p.head[H_PRE_CTAS] = ctas;
+      p.head[H_BAD_PREFIX] = p.head[H_NEXT_PRE] = p.head[H_NEXT_OWN] = 0;
+      p.head[H_QUERIES] = queries;
+      p.head[H_CHUNKS] = chunks;
+      p.head[H_CHUNK_KEYS] = per * step;
+      p.head[H_SPLITS] = splits;
+      p.head[H_SPLIT_TILES] = split_tiles;
+      p.head[H_PRE_ITEMS] = row_items * splits;
+      p.head[H_OWN_ITEMS] = chunks * a.Hkv * p.row_tiles;
+      p.head[H_FLAGS] = flags;
+    }
   }
 }
 
@@ -408,33 +429,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
-  // Rows u * 32 .. + 31 of an item's Q into half h of its place, by one warp, once `bar`
-  // says that the scores of the half's last item are done: a lane finds a row, then the warp copies the rows together.  Rows past the end stay as
-  // they are: what comes of them is never read.
-  auto load_q = [&](const Item& it, int u, int h, uint64_t* bar, int phase) {
+  // An item's Q, by a warp: first + count * 32 rows `stride` runs apart, into the
+  // halves of its place from `half` on, once `bar` says that the scores of their last
+  // items are done.  A lane finds a row of each run and asks for it in L2, then the
+  // warp copies the rows together.  Rows past the end stay as they are: what comes of
+  // them is never read.
+  constexpr int kQRuns = 4;
+  auto load_q = [&](const Item& it, int first, int stride, int end, int half, uint64_t* bar, int phase) {
     constexpr int kWords = D / 8, kRows = 32 / kWords;  // 16-byte words of a row, rows of one instruction
-    const int c = lane % kWords, sub = lane / kWords, r = u * 32 + lane;
+    const int c = lane % kWords, sub = lane / kWords;
     const uint16_t* from = static_cast<const uint16_t*>(a.q) + c * 8;
-    long long at = -1;
-    if (r < it.rows) {
-      const int row = it.row0 + r, qi = row / p.G, g = row - qi * p.G;
-      const int bi = it.kind == 0 ? p.qrow[qi] : it.b * p.Q + qi;
-      const int b = bi / p.Q, i = bi - b * p.Q;
-      at = b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head;
+    long long at[kQRuns];
+#pragma unroll
+    for (int w = 0; w < kQRuns; ++w) {
+      const int u = first + w * stride, r = u * 32 + lane;
+      at[w] = -1;
+      if (u < end && r < it.rows) {
+        const int row = it.row0 + r, qi = row / p.G, g = row - qi * p.G;
+        const int bi = it.kind == 0 ? p.qrow[qi] : it.b * p.Q + qi;
+        const int b = bi / p.Q, i = bi - b * p.Q;
+        at[w] = b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head;
+        const uint16_t* line = static_cast<const uint16_t*>(a.q) + at[w];
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(line + D - 8));
+      }
     }
     if (!__all_sync(0xffffffffu, wait(bar, phase))) return false;
-    const uint32_t to = q_smem + h * S::kTileBytes + (c >> 3) * (kTileKeys * 128);
-    if (u * 32 < it.rows) {
 #pragma unroll
+    for (int w = 0; w < kQRuns; ++w) {
+      const int u = first + w * stride;
+      if (u >= end || u * 32 >= it.rows) continue;  // (the same in the whole warp)
+      const uint32_t to = q_smem + (half + (u >> 2)) * S::kTileBytes + (c >> 3) * (kTileKeys * 128);
+#pragma unroll 4
       for (int v = 0; v < 32 / kRows; ++v) {
         const int rr = (u & 3) * 32 + v * kRows + sub;
-        const long long row_at = __shfl_sync(0xffffffffu, at, v * kRows + sub);
+        const long long row_at = __shfl_sync(0xffffffffu, at[w], v * kRows + sub);
         if (row_at >= 0) cp16(to + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), from + row_at, true);
       }
     }
     landed();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&q_full[h]);
+    if (lane == 0)
+      for (int u = first; u < end; u += stride) mbar_arrive(&q_full[half + (u >> 2)]);
     return true;
   };
 
@@ -464,8 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, wait(&q_empty[0], q_uses[0]++ - 1) && wait(&q_empty[1], q_uses[1]++ - 1));
           if (ok && lane == 0) mbar_arrive(&q_go);
         } else {
-#pragma unroll 1
-          for (int u = 0; u < 4 && ok; ++u) ok = load_q(it, u, n & 1, &q_empty[n & 1], q_uses[n & 1] - 1);
+          ok = load_q(it, 0, 1, 4, n & 1, &q_empty[n & 1], q_uses[n & 1] - 1);
           ++q_uses[n & 1];
         }
         if (ok) ok = publish(n + 1);
@@ -488,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool q_due = it.pair();  // two row tiles: Q is loaded by these warps, behind their first tile
         auto my_q = [&]() {
           q_due = false;
-          for (int u = slot; u < 8 && ok; u += kSlots) ok = load_q(it, u, u >> 2, &q_go, pairs);
+          ok = load_q(it, slot, kSlots, 8, 0, &q_go, pairs);
           ++pairs;
         };
         for (int x = (slot + kSlots - turn % kSlots) % kSlots; x < total; x += kSlots, ++use) {
@@ -590,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_async();
           }
           if (look || !p.box) mbar_arrive(&full[slot]);
-          if (q_due) my_q();
+          if (q_due && ok) my_q();
           if (!ok) break;
         }
         if (!ok) break;
