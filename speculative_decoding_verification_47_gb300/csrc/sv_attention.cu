@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<D>;
   constexpr uint32_t kIdS = tc::idesc(false, false, 128, kTileKeys), kIdO = tc::idesc(false, true, 128, D);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kSlots], raw[kSlots], empty[kSlots], q_full[2], q_empty[2], q_go, s_full[2], p_ready[2][2], o_full[2], next[2],
+  __shared__ __align__(8) uint64_t full[kSlots], raw[kSlots], empty[kSlots], q_full[2], q_empty[2], q_go, s_full[2], p_ready[2][2], o_full[2], turn_of[2],
       item_full[2], item_empty[2];
   __shared__ Item items[2];
   __shared__ uint32_t tmem_base;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[s], 4);  // (four runs of 32 rows)
       mbar_init(&q_empty[s], 2);
       mbar_init(&s_full[s], 1);
-      mbar_init(&next[s], 1);
+      mbar_init(&turn_of[s], 1);
       mbar_init(&p_ready[s][0], 128);
       mbar_init(&p_ready[s][1], 128);
       mbar_init(&o_full[s], 1);
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (q % (kTileKeys / 32) == 0) {
                 if (ok) ok = wait(&p_ready[s][q / (kTileKeys / 32)], (int)p_phase);
                 if (q == 0 && in_turn) {
-                  if (ok) ok = wait(&next[s], (int)next_phase);
+                  if (ok) ok = wait(&turn_of[s], (int)next_phase);
                   next_phase ^= 1;
                 }
                 tc::fence_after();
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 scored(k);
               else
                 tc::commit<1>(smem_addr(&o_full[s]));
-              if (pr && (s == 0 || more)) mbar_arrive(&next[s ^ 1]);
+              if (pr && (s == 0 || more)) mbar_arrive(&turn_of[s ^ 1]);
             } else {
               mbar_arrive(v.empty);
               if (more) mbar_arrive(k.empty);
@@ -749,11 +749,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float worst = c >= 0.f ? -INFINITY : INFINITY;
     int s_turn = 0, o_turn = 0;
     bool ok = true;
-    for (int n = 0; ok; ++n) {
-      const Item it = fetch(n);
-      if (it.kind < 0) break;
+    Item it = fetch(0);
+    for (int n = 1; it.kind >= 0; ++n) {
       const int tiles = it.stream_tiles(s);
-      if (tiles == 0) continue;
+      if (tiles == 0) {
+        it = fetch(n);
+        continue;
+      }
       const int r = it.row0 + (it.pair() ? s * 128 : 0) + row;  // this thread's row
       const bool live = (it.pair() ? s * 128 : 0) + row < it.rows;
       // keys that the row sees, from the item's first on
@@ -848,6 +850,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++o_turn;
       if (!ok) break;
       tc::fence_after();
+      // (the next item before the stores: the release of its place would wait for them)
+      const Item next = fetch(n);
       // this row's part, in quads of columns: [D / 4][rows][4], so that a warp's 32 rows
       // are 512 contiguous bytes of a store and not 32 lines
       long long at, rows_o;
@@ -886,6 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc::fence_before();  // (the next item's first weights follow: its product may overwrite O)
+      it = next;
     }
   }
   __syncwarp();
