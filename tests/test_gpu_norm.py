@@ -100,6 +100,34 @@ def test_row_counts(M):
     check(x, x, w, "e4m3", y, c, s)
 
 
+@pytest.mark.parametrize("M,H", [(2500, 520), (5000, 1024), (700, 4096), (2304, 4096), (400, 8192), (170, 16384),
+                                 (333, 9000)])
+def test_more_rows_than_fit_at_once(M, H):
+    """Rows that pass through a ring of shared memory, with and without a residual, the
+    sum over the residual, rows that are not finite or zero among others."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, H + 8, generator=g, device="cuda").to(torch.bfloat16)[:, :H]
+    r = (3 * torch.randn(M, H, generator=g, device="cuda")).to(torch.bfloat16)
+    w = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(torch.bfloat16)
+    x[7] = 0
+    x[M - 2] = 0
+    for out in ("e4m3", "bf16"):
+        for res in (r, None):
+            y, c, s = run(x, res, w, out)
+            check(x, res, w, out, y, c, s)
+    r2 = r.clone()
+    y2 = torch.zeros(M, H, dtype=torch.uint8, device="cuda")
+    c2 = torch.zeros(M, device="cuda")
+    sb.sv_rmsnorm_residual(x, x.stride(0), r2, 0, w, 1e-5, r2, 0, sb.SV_BF16, y2, 0, sb.SV_E4M3, c2, M, H)
+    y, c, s = run(x, r, w, "e4m3")
+    assert torch.equal(r2, s) and torch.equal(c2, c) and torch.equal(y2, y.view(torch.uint8))
+    x[11, 5] = float("nan")
+    y, c, _ = run(x, r, w, "e4m3")
+    assert torch.isnan(y.float()[11]).all() and torch.isnan(c[11])
+    keep = torch.arange(M, device="cuda") != 11
+    assert torch.equal(y.view(torch.uint8)[keep], y2[keep]) and torch.equal(c[keep], c2[keep])
+
+
 @pytest.mark.parametrize("off", [0, 1, 2, 4])
 def test_strides_and_alignment(off):
     """Rows inside wider buffers, from an odd start on: values outside the rows
