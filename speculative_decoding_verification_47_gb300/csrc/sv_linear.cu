@@ -999,21 +999,27 @@ static int dispatch(const Job& j, std::string* err) {
     if (t128 <= split_clusters<128, F8>(split)) return launch_split<128, F8>(j, split, err);
     if (t256 <= split_clusters<256, F8>(split)) return launch_split<256, F8>(j, split, err);
   }
-  // Rows (ms x 256) and columns of a tile, by the clocks that they would take: a
-  // k block costs the MMAs' 2 ms BN, but no less than a slot's turn through the
-  // ring (3650 over the slots, measured: 0.32 us a block for 256 x 128 and for
-  // 256 x 256 tiles in 6 slots, 0.47 for 512 x 128 in 4); an epilogue costs 20 a
-  // column and sub-tile, once a round where the accumulators fill tensor memory
-  // (ms = 2) and else once in all.
+  // Rows (ms x 256) and columns of a tile, by the clocks that they would take (all
+  // measured).  A k block costs the MMAs' 2 ms BN, but no less than a slot's turn
+  // through the ring (3650 over the slots: 0.32 us a block for 256 x 128 and for
+  // 256 x 256 tiles in 6 slots), and a part more under full load (18% with one
+  // sub-tile, which asks more of L2, and 12% with two).  An epilogue costs 37 a column
+  // and sub-tile, 25 more with a residual, up to 15 more for the activation; behind the
+  // last tile with one sub-tile, behind every one with two, which fill tensor memory.
+  // 8192 x 4096 x 4096 bf16: 182 and 174 us (ms 1 and 2), with a residual 189 and 199;
+  // K = 1024: 56 and 70.
   const int widths[4] = {256, 224, 192, 128};
+  const int act_clocks[5] = {0, 0, 5, 15, 11};
+  const int column = 37 + (j.e.res ? 25 : 0) + act_clocks[j.e.act];
   int bw = 256, bms = 1;
   long long best = -1;
   for (int ms = 1; ms <= 2; ++ms)
     for (int w : widths) {
       const long long tiles = ((M + ms * 256LL - 1) / (ms * 256)) * ((N + w - 1LL) / w);
       const long long rounds = (tiles + pairs - 1) / pairs, slots = kPairRing / (ms * kTile + w / 2 * kRowBytes);
-      const long long block = 2 * ms * w > 3650 / slots ? 2 * ms * w : 3650 / slots;
-      const long long cost = rounds * block * j.KB + (ms == 2 ? rounds : 1) * 20 * ms * w;
+      const long long block = (2 * ms * w > 3650 / slots ? 2 * ms * w : 3650 / slots) * (ms == 1 ? 118 : 112) / 100;
+      const long long loop = block * j.KB, end = (long long)ms * w * column;
+      const long long cost = ms == 1 ? rounds * (loop > end ? loop : end) + end : rounds * (loop + end);
       if (best < 0 || cost < best) {
         best = cost;
         bw = w;
