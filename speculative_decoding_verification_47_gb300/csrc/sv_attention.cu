@@ -270,6 +270,9 @@ struct alignas(16) Item {
   int len;           // own: committed tokens
   int unused;
   __device__ __forceinline__ bool pair() const { return rows > 128; }  // streams: two row tiles, or alternate key tiles
+  // up to 64 rows stand in Q's tile twice: the second stream uses the copy, whose rows
+  // belong to other warps (and schedulers) than the first one's
+  __device__ __forceinline__ bool twice() const { return rows <= 64; }
   __device__ __forceinline__ int ahead() const { return pair() ? 1 : 2; }
   __device__ __forceinline__ int stream_tiles(int s) const { return pair() ? tiles : (tiles + 1 - s) / 2; }
 };
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long at[kQRuns];
 #pragma unroll
     for (int w = 0; w < kQRuns; ++w) {
-      const int u = first + w * stride, r = u * 32 + lane;
+      const int u = first + w * stride, r = (it.twice() ? u & 1 : u) * 32 + lane;
       at[w] = -1;
       if (u < end && r < it.rows) {
         const int row = it.row0 + r, qi = row / p.G, g = row - qi * p.G;
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int w = 0; w < kQRuns; ++w) {
       const int u = first + w * stride;
-      if (u >= end || u * 32 >= it.rows) continue;  // (the same in the whole warp)
+      if (u >= end || (it.twice() ? u & 1 : u) * 32 >= it.rows) continue;  // (the same in the whole warp)
       const uint32_t to = q_smem + (half + (u >> 2)) * S::kTileBytes + (c >> 3) * (kTileKeys * 128);
 #pragma unroll 4
       for (int v = 0; v < 32 / kRows; ++v) {
@@ -718,12 +721,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const bool own = pr || (j & 1) == s, more = j + d < T;
             Tile k;
-            if (more) k = take();
+            if (pr && more) k = take();  // (before the turn)
             if (!ok) break;
             if (own) {
               values(v, pr ? j > 0 : j > 1, pr && (s == 1 || j > 0));
               if (!ok) break;
               tc::commit<1>(smem_addr(v.empty));
+              if (!pr && more) k = take();
+              if (!ok) break;
               if (more)
                 scored(k);
               else
@@ -731,6 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (pr && (s == 0 || more)) mbar_arrive(&turn_of[s ^ 1]);
             } else {
               mbar_arrive(v.empty);
+              if (more) k = take();
+              if (!ok) break;
               if (more) mbar_arrive(k.empty);
             }
           }
@@ -756,8 +763,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         it = fetch(n);
         continue;
       }
-      const int r = it.row0 + (it.pair() ? s * 128 : 0) + row;  // this thread's row
-      const bool live = (it.pair() ? s * 128 : 0) + row < it.rows;
+      // this thread's row, of the item and among all
+      const int mine = it.pair() ? s * 128 + row : (it.twice() ? row - 64 * s : row), r = it.row0 + mine;
+      const bool live = mine >= 0 && mine < it.rows;
+      const bool warp_live = __any_sync(0xffffffffu, live);
       // keys that the row sees, from the item's first on
       int sees = 0;
       if (live) sees = it.kind == 0 ? it.keys : min(it.keys, it.len + r / p.G - it.key0);
@@ -770,6 +779,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         ++s_turn;
+        if (!warp_live) {  // rows that nothing is read from: any weights will do
+          mbar_arrive(&p_ready[s][0]);
+          mbar_arrive(&p_ready[s][1]);
+          continue;
+        }
         tc::fence_after();
         const bool all = __all_sync(0xffffffffu, vis == kTileKeys);
         // the row's scores, and their extreme
@@ -862,8 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (s == 1 && !it.pair()) {
           rows_o = 128;
           at = (long long)it.slot * a.Hkv + it.h;
-          ml = p.extra_ml + at * rows_o + row;
-          o = p.extra_o + at * rows_o * D + row * 4;
+          ml = p.extra_ml + at * rows_o + mine;
+          o = p.extra_o + at * rows_o * D + mine * 4;
         } else {
           rows_o = (long long)queries * p.G;
           at = (long long)it.slot * a.Hkv + it.h;
@@ -878,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (live) *ml = make_float2(m, l);
 #pragma unroll 1
-      for (int q = 0; q < D; q += 16) {
+      for (int q = 0; q < D && warp_live; q += 16) {
         uint32_t v[16];
         tc::ld16(col_o + q, v);
         tc::ld_wait(v);
