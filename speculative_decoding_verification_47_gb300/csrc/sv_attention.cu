@@ -721,14 +721,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const bool own = pr || (j & 1) == s, more = j + d < T;
             Tile k;
-            if (pr && more) k = take();  // (before the turn)
+            if (more) k = take();
             if (!ok) break;
             if (own) {
               values(v, pr ? j > 0 : j > 1, pr && (s == 1 || j > 0));
               if (!ok) break;
               tc::commit<1>(smem_addr(v.empty));
-              if (!pr && more) k = take();
-              if (!ok) break;
               if (more)
                 scored(k);
               else
@@ -736,8 +734,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (pr && (s == 0 || more)) mbar_arrive(&turn_of[s ^ 1]);
             } else {
               mbar_arrive(v.empty);
-              if (more) k = take();
-              if (!ok) break;
               if (more) mbar_arrive(k.empty);
             }
           }
