@@ -699,8 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             q_phase[h] ^= 1;
           }
           int left = it.stream_tiles(s);  // scores to come
-          auto scored = [&](const Tile& k) {
-            scores(k);
+          auto scored = [&](const Tile& k) {  // (its slot and Q's, behind its scores)
             tc::commit<1>(smem_addr(k.empty));
             if (--left == 0) tc::commit<1>(smem_addr(&q_empty[mine]));
           };
@@ -709,10 +708,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < d && ok; ++x) {
             const Tile k = take();
             if (!ok) break;
-            if (pr || x == s)
+            if (pr || x == s) {
+              scores(k);
               scored(k);
-            else
+            } else {
               mbar_arrive(k.empty);
+            }
           }
           for (int j = 0; j < T && ok; ++j) {
             // O += P(j) V_j, then the next scores over P's place (the products of one
@@ -726,12 +727,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (own) {
               values(v, pr ? j > 0 : j > 1, pr && (s == 1 || j > 0));
               if (!ok) break;
-              tc::commit<1>(smem_addr(v.empty));
+              if (!pr) tc::commit<1>(smem_addr(v.empty));
               if (more)
-                scored(k);
+                scores(k);
               else
                 tc::commit<1>(smem_addr(&o_full[s]));
-              if (pr && (s == 0 || more)) mbar_arrive(&turn_of[s ^ 1]);
+              if (pr) {  // the other's turn before the release: each commit holds this thread up
+                if (s == 0 || more) mbar_arrive(&turn_of[s ^ 1]);
+                tc::commit<1>(smem_addr(v.empty));
+              }
+              if (more) scored(k);
             } else {
               mbar_arrive(v.empty);
               if (more) mbar_arrive(k.empty);
