@@ -47,40 +47,52 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-template <int VEC>
-struct alignas(VEC * 2) Half {
-  uint16_t v[VEC];
-};
-template <int VEC>
-struct alignas(VEC * 4 > 16 ? 16 : VEC * 4) Full {
-  float v[VEC];
+// Vectors of VEC elements as 32-bit words (bf16: two to a word, e4m3: four), so that
+// widening is a shift or a mask and narrowing one instruction for two values.
+template <int N>
+struct alignas(N * 4 > 16 ? 16 : N * 4) Words {
+  uint32_t v[N];
 };
 
 template <int VEC>
 __device__ __forceinline__ void load(const uint16_t* p, float (&f)[VEC]) {
-  const Half<VEC> h = *reinterpret_cast<const Half<VEC>*>(p);
+  if constexpr (VEC == 1) {
+    f[0] = __uint_as_float((uint32_t)*p << 16);
+  } else {
+    const Words<VEC / 2> h = *reinterpret_cast<const Words<VEC / 2>*>(p);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) f[i] = __uint_as_float((uint32_t)h.v[i] << 16);
+    for (int i = 0; i < VEC / 2; ++i) {
+      f[2 * i] = bf16_lo(h.v[i]);
+      f[2 * i + 1] = bf16_hi(h.v[i]);
+    }
+  }
 }
 template <int VEC>
 __device__ __forceinline__ void load(const float* p, float (&f)[VEC]) {
-  const Full<VEC> h = *reinterpret_cast<const Full<VEC>*>(p);
+  const Words<VEC> h = *reinterpret_cast<const Words<VEC>*>(p);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) f[i] = h.v[i];
+  for (int i = 0; i < VEC; ++i) f[i] = __uint_as_float(h.v[i]);
 }
 template <int VEC>
 __device__ __forceinline__ void store(uint16_t* p, const float (&f)[VEC]) {
-  Half<VEC> h;
+  if constexpr (VEC == 1) {
+    *p = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+  } else {
+    Words<VEC / 2> h;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) h.v[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
-  *reinterpret_cast<Half<VEC>*>(p) = h;
+    for (int i = 0; i < VEC / 2; ++i) {
+      const __nv_bfloat162 two = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      h.v[i] = *reinterpret_cast<const uint32_t*>(&two);
+    }
+    *reinterpret_cast<Words<VEC / 2>*>(p) = h;
+  }
 }
 template <int VEC>
 __device__ __forceinline__ void store(float* p, const float (&f)[VEC]) {
-  Full<VEC> h;
+  Words<VEC> h;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) h.v[i] = f[i];
-  *reinterpret_cast<Full<VEC>*>(p) = h;
+  for (int i = 0; i < VEC; ++i) h.v[i] = __float_as_uint(f[i]);
+  *reinterpret_cast<Words<VEC>*>(p) = h;
 }
 
 // two values to e4m3 (round to nearest, out of range to +-448, NaN kept)
@@ -90,23 +102,18 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
   return r;
 }
 template <int VEC>
-struct alignas(VEC) Bytes {
-  uint8_t v[VEC];
-};
-template <int VEC>
 __device__ __forceinline__ void store8(uint8_t* p, const float (&f)[VEC]) {
-  Bytes<VEC> b;
-  if (VEC == 1) {
-    b.v[0] = (uint8_t)e4m3x2(f[0], 0.f);
+  if constexpr (VEC == 1) {
+    *p = (uint8_t)e4m3x2(f[0], 0.f);
+  } else if constexpr (VEC == 2) {
+    *reinterpret_cast<uint16_t*>(p) = e4m3x2(f[0], f[1]);
   } else {
+    Words<VEC / 4> h;
 #pragma unroll
-    for (int i = 0; i + 1 < VEC; i += 2) {
-      const uint16_t two = e4m3x2(f[i], f[i + 1]);
-      b.v[i] = (uint8_t)two;
-      b.v[i + 1] = (uint8_t)(two >> 8);
-    }
+    for (int i = 0; i < VEC / 4; ++i)
+      h.v[i] = (uint32_t)e4m3x2(f[4 * i], f[4 * i + 1]) | ((uint32_t)e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16);
+    *reinterpret_cast<Words<VEC / 4>*>(p) = h;
   }
-  *reinterpret_cast<Bytes<VEC>*>(p) = b;
 }
 
 // Sum and maximum over the threads of a row, to all of them (one barrier: calls in a
