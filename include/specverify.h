@@ -381,8 +381,8 @@ sv_status sv_lmhead_rmsnorm(const void* hidden, const void* norm_w, float eps, c
  *     s_j = scale * sum_d q[b][i][h][d] * k_j[d]   over the tokens j it sees,
  *     out[b][i][h][:] = sum_j exp(s_j) v_j / sum_j exp(s_j),
  *     lse[b][i][h] = log sum_j exp(s_j).
- *   A query that sees no token gets out = 0 and lse = -inf.  Nothing is
- *   written for positions i > k_b.  K = 0 is the single-token decode step.
+ *   A query that sees no token (or none whose score is above -inf) gets out = 0
+ *   and lse = -inf.  Nothing is written for positions i > k_b.  K = 0 is the single-token decode step.
  *
  *   q            device bf16, element (b,i,h,d) at b*q_seq_stride +
  *                i*q_pos_stride + h*q_head_stride + d; strides in elements,
@@ -407,7 +407,7 @@ sv_status sv_lmhead_rmsnorm(const void* hidden, const void* norm_w, float eps, c
  *                four bytes are the device flag word (cleared by the call).
  *                Calls that share a workspace must be ordered on one stream.
  * q, k_pool, v_pool and out must be 16-byte aligned and their strides
- * multiples of 8 elements.  Products and the softmax's sums are float32; the
+ * multiples of 8 elements; out and lse must not overlap an input.  Products and the softmax's sums are float32; the
  * unnormalised weights are rounded to bf16 for the product with v.
  * Values past a sequence's end (the rest of a page, pages that are not its
  * own) are never used, whatever they hold; a value of v at a draft position
@@ -476,7 +476,7 @@ sv_status sv_rmsnorm_residual(const void* x, int64_t ldx, const void* residual, 
  *             zero it once).
  * x and W must be 16-byte aligned with row strides of a multiple of 16 bytes
  * (values between K and the stride are not used); the rest needs its
- * element's alignment.  Products and sums are float32, rounded once at the end.
+ * element's alignment.  out must not overlap x, W, bias or the scales.  Products and sums are float32, rounded once at the end.
  */
 size_t sv_linear_workspace_size(int M, int N, int K);
 sv_status sv_linear(const void* x, int64_t ldx, const float* x_scale, const void* W, int64_t ldw,

@@ -640,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = warp - 8;
       uint32_t slot = 0, phase = 0;  // the ring's next tile
       uint32_t p_phase = 0, next_phase = 0, q_phase[2] = {0, 0};
+      bool opening = s == 0;  // the first turn of all, which no other precedes
       const uint32_t ring_lo = tc::desc_low(ring, kTileKeys * 128);
       const uint32_t col_s = tmem + kColS + s * kStreamCols, col_o = tmem + kColO + s * kStreamCols;
       for (int n = 0;; ++n) {
@@ -725,7 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) k = take();
             if (!ok) break;
             if (own) {
-              values(v, pr ? j > 0 : j > 1, pr && (s == 1 || j > 0));
+              values(v, pr ? j > 0 : j > 1, pr && !opening);
+              if (pr) opening = false;
               if (!ok) break;
               if (!pr) tc::commit<1>(smem_addr(v.empty));
               if (more)
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               else
                 tc::commit<1>(smem_addr(&o_full[s]));
               if (pr) {  // the other's turn before the release: each commit holds this thread up
-                if (s == 0 || more) mbar_arrive(&turn_of[s ^ 1]);
+                mbar_arrive(&turn_of[s ^ 1]);
                 tc::commit<1>(smem_addr(v.empty));
               }
               if (more) scored(k);

@@ -349,3 +349,52 @@ def test_lengths_that_change_between_replays():
         g.replay()
         torch.cuda.synchronize()
         c.check()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams with workspaces of their own, and a product beside them."""
+    a = Case([400, 20, 7, 130] * 6, [2, 3, 0, 1] * 6, 3, prefix=500, seed=1)
+    b = Case([90, 300], [1, 1], 1, hq=16, hkv=4, prefix=1000, D=64, seed=2)
+    x = torch.randn(300, 1024, device="cuda").to(torch.bfloat16)
+    W = torch.randn(2048, 1024, device="cuda").to(torch.bfloat16)
+    o = torch.empty(300, 2048, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(streams[0]):
+            a.run()
+        with torch.cuda.stream(streams[1]):
+            b.run()
+        with torch.cuda.stream(streams[2]):
+            sb.sv_linear(x, 0, None, W, 0, None, sb.SV_BF16, None, None, 0, 0, o, 0, sb.SV_F32, 300, 2048, 1024, ws, 256)
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+    assert sb.sv_read_device_flags(ws) == 0
+    ref = x.double() @ W.double().T
+    # float32 sums of 1024 exact products, cut or rounded at each step of 16
+    assert ((o - ref).abs() <= 1100 * 2.0 ** -23 * (x.double().abs() @ W.double().abs().T)).all()
+
+
+@pytest.mark.parametrize("B,K,prefix", [(64, 7, 2048), (200, 3, 130), (3, 0, 5000)])
+def test_many_items_of_every_kind(B, K, prefix):
+    """Items of two row tiles, of alternate key tiles and of one tile, in every order
+    that the CTAs take them: the long and the short one after another."""
+    r = np.random.default_rng(B)
+    lens = np.where(r.uniform(size=B) < 0.3, r.integers(0, 3, B), r.integers(0, 900, B))
+    c = Case(lens, r.integers(0, K + 1, B), K, hq=32, hkv=8, D=64, prefix=prefix, seed=B, page=32)
+    a = c.run().out.clone()
+    c.check()
+    for _ in range(10):
+        assert torch.equal(a, c.run().out)
+    assert sb.sv_read_device_flags(c.ws) == 0
+
+
+def test_pages_used_twice():
+    """Sequences that share pages of their own, and a prefix that is one page over and over."""
+    c = Case([64, 64, 64], [0, 0, 0], 0, prefix=96, page=16, D=128)
+    c.table[1], c.table[2, :2] = c.table[0], c.table[0, 2:4]
+    c.prefix_pages[:] = c.prefix_pages[1]
+    c.upload()
+    c.run().check()

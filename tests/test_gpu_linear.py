@@ -46,7 +46,7 @@ class Case:
             buf[:, :K] = (torch.randn(n, K, generator=g, device="cuda") * scale).to(t)
             return buf
         self.x, self.W = rows(M, 1.0), rows(N, 1.0 if dtype == "e4m3" else 0.3)
-        scales = scales and dtype == "e4m3"
+        scales = scales and (dtype == "e4m3" or scales == "both")
         self.sx = torch.rand(M, generator=g, device="cuda") + 0.5 if scales else None
         self.sw = torch.rand(N, generator=g, device="cuda") + 0.5 if scales else None
         self.bias = torch.randn(N, generator=g, device="cuda").to(torch.bfloat16) if bias else None
@@ -106,6 +106,7 @@ def test_optional_arguments(M):
     for scales, bias, res in [(False, False, False), (True, False, False), (False, True, False),
                               (False, False, True)]:
         Case(M, 150, 96, dtype="e4m3", scales=scales, bias=bias, res=res).run().check()
+    Case(M, 150, 96, dtype="bf16", scales="both", out="f32").run().check()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
