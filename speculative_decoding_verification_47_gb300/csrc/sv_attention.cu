@@ -66,7 +66,7 @@ __host__ inline Layout layout(int B, int K, int Hq, int Hkv, int D, long long pr
   };
   w.qrow = take((size_t)Q * 4);
   w.coff = take((size_t)B * 4);
-  w.chunk_of = take((size_t)(w.own_slots / (2 * Hkv)) * 4);
+  w.chunk_of = take((size_t)(w.own_slots / (2 * Hkv)) * 16);
   w.stat = take((size_t)B * 4);
   w.nan_from = take((size_t)B * Hkv * 4);
   w.pre_ml = take((size_t)w.pre_rows * 8);
@@ -86,7 +86,7 @@ struct Args {
   uint32_t* head;
   int* qrow;      // compact query -> b * Q + i
   int* coff;      // first chunk of a sequence
-  int* chunk_of;  // chunk -> sequence
+  int4* chunk_of;  // chunk -> sequence, its drafts, committed tokens and first chunk
   int* stat;      // a sequence's flags
   int* nan_from;  // [B][Hkv] first own token whose drafted value is not finite
   float2 *pre_ml, *extra_ml, *own_ml;
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
     chunks += total;
     if (b < a.B) p.coff[b] = ce;
     for (int i = 0; i < q; ++i) p.qrow[qe + i] = b * p.Q + i;
-    for (int c = 0; c < n; ++c) p.chunk_of[ce + c] = b;
+    for (int c = 0; c < n; ++c) p.chunk_of[ce + c] = make_int4(b, k, len, ce);
   }
   const int ptiles = ceil_div(a.prefix_len, kTileKeys);
   const long long rows = (long long)queries * p.G;
@@ -225,7 +225,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
     }
     if (t == 0) {
       p.head[H_PRE_CTAS] = ctas;
-      p.head[H_BAD_PREFIX] = p.head[H_NEXT_PRE] = p.head[H_NEXT_OWN] = 0;
+      p.head[H_BAD_PREFIX] = 0;
+      p.head[H_NEXT_PRE] = ctas;  // (these many CTAs take the first ones by themselves)
+      p.head[H_NEXT_OWN] = p.grid - ctas;
       p.head[H_QUERIES] = queries;
       p.head[H_CHUNKS] = chunks;
       p.head[H_CHUNK_KEYS] = per * step;
@@ -277,53 +279,65 @@ struct alignas(16) Item {
   __device__ __forceinline__ int stream_tiles(int s) const { return pair() ? tiles : (tiles + 1 - s) / 2; }
 };
 
-__device__ __forceinline__ Item decode(const Args& p, int kind, int idx) {
-  const AttentionLaunch& a = p.a;
-  Item it;
-  it.kind = kind;
-  it.b = it.len = 0;
-  if (kind == 0) {
-    // row tiles fastest: the items in flight share the keys' tiles in L2
-    const int queries = p.head[H_QUERIES], per = p.head[H_SPLIT_TILES];
-    const int row_items = (int)(((long long)queries * p.G + kItemRows - 1) / kItemRows);
-    it.row0 = idx % row_items * kItemRows;
-    it.h = idx / row_items % a.Hkv;
-    it.slot = idx / row_items / a.Hkv;
-    const long long left = (long long)queries * p.G - it.row0;
-    it.rows = left < kItemRows ? (int)left : kItemRows;
-    it.key0 = it.slot * per * kTileKeys;
-    const int end = a.prefix_len - it.key0;
-    it.keys = end < per * kTileKeys ? end : per * kTileKeys;
-  } else {
-    const int keys = p.head[H_CHUNK_KEYS];
-    const int rt = idx % p.row_tiles;
-    it.h = idx / p.row_tiles % a.Hkv;
-    it.slot = idx / p.row_tiles / a.Hkv;
-    it.b = p.chunk_of[it.slot];
-    const int k = a.kpr ? a.kpr[it.b] : a.K;
-    it.len = a.lens[it.b];
-    it.row0 = rt * kItemRows;
-    const int left = (k + 1) * p.G - it.row0;
-    it.rows = left < kItemRows ? left : kItemRows;
-    it.key0 = (it.slot - p.coff[it.b]) * keys;
-    const int end = it.len + k - it.key0;
-    it.keys = end < keys ? end : keys;
-    if (it.rows <= 0) it.keys = 0;  // (a sequence with fewer row tiles than the largest)
-  }
-  it.tiles = it.keys > 0 ? ceil_div(it.keys, kTileKeys) : 0;
-  return it;
-}
-
-// Next item for this CTA: from its preferred list until that is empty, then from
-// the other.  Items without keys are passed over.
+// Items of this CTA, by one thread: from its preferred list until that is empty, then
+// from the other.  Items without keys are passed over.  The first one needs no
+// counter: the CTAs that begin with a list take its first items in their order.
 struct Feed {
   int list, left;
+  int start;  // its place in the order, -1 once that is taken
+  int queries, chunk_keys, split_tiles, pre_items, own_items;
+
+  __device__ __forceinline__ void init(const Args& p) {
+    const int4* head = reinterpret_cast<const int4*>(p.head);
+    const int4 h1 = head[1], h2 = head[2];
+    queries = h1.x;
+    chunk_keys = h1.z;
+    split_tiles = h2.x;
+    pre_items = h2.y;
+    own_items = h2.z;
+    const int ctas = h2.w;
+    list = (int)blockIdx.x < ctas ? 0 : 1;
+    start = (int)blockIdx.x - (list ? ctas : 0);
+    left = 2;
+  }
+  __device__ __forceinline__ Item decode(const Args& p, int idx) const {
+    const AttentionLaunch& a = p.a;
+    Item it;
+    it.kind = list;
+    it.b = it.len = 0;
+    if (list == 0) {
+      // row tiles fastest: the items in flight share the keys' tiles in L2
+      const int row_items = (int)(((long long)queries * p.G + kItemRows - 1) / kItemRows);
+      it.row0 = idx % row_items * kItemRows;
+      it.h = idx / row_items % a.Hkv;
+      it.slot = idx / row_items / a.Hkv;
+      const long long left = (long long)queries * p.G - it.row0;
+      it.rows = left < kItemRows ? (int)left : kItemRows;
+      it.key0 = it.slot * split_tiles * kTileKeys;
+      it.keys = min(a.prefix_len - it.key0, split_tiles * kTileKeys);
+    } else {
+      const int rt = idx % p.row_tiles;
+      it.h = idx / p.row_tiles % a.Hkv;
+      it.slot = idx / p.row_tiles / a.Hkv;
+      const int4 of = p.chunk_of[it.slot];
+      it.b = of.x;
+      it.len = of.z;
+      it.row0 = rt * kItemRows;
+      it.rows = min((of.y + 1) * p.G - it.row0, kItemRows);
+      it.key0 = (it.slot - of.w) * chunk_keys;
+      it.keys = min(it.len + of.y - it.key0, chunk_keys);
+      if (it.rows <= 0) it.keys = 0;  // (a sequence with fewer row tiles than the largest)
+    }
+    it.tiles = it.keys > 0 ? ceil_div(it.keys, kTileKeys) : 0;
+    return it;
+  }
   __device__ __forceinline__ Item next(const Args& p) {
     Item it;
     while (left > 0) {
-      const int i = (int)atomicAdd(&p.head[list ? H_NEXT_OWN : H_NEXT_PRE], 1u);
-      if (i < (int)p.head[list ? H_OWN_ITEMS : H_PRE_ITEMS]) {
-        it = decode(p, list, i);
+      const int i = start >= 0 ? start : (int)atomicAdd(&p.head[list ? H_NEXT_OWN : H_NEXT_PRE], 1u);
+      start = -1;
+      if (i < (list ? own_items : pre_items)) {
+        it = decode(p, i);
         if (it.tiles > 0) return it;
       } else {
         list ^= 1;
@@ -389,6 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 8) tc::alloc<1>(&tmem_base, 512);
+  if (tid == 9 * 32 && p.box) {
+    tc::prefetch_map(&tmK);
+    tc::prefetch_map(&tmV);
+  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -437,39 +455,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   // items are done.  A lane finds a row of each run and asks for it in L2, then the
   // warp copies the rows together.  Rows past the end stay as they are: what comes of
   // them is never read.
-  constexpr int kQRuns = 4;
+  // (loops, not straight code: a CTA of short items runs through this once for each of
+  // them, and its instructions push the softmax's out of the cache)
   auto load_q = [&](const Item& it, int first, int stride, int end, int half, uint64_t* bar, int phase) {
     constexpr int kWords = D / 8, kRows = 32 / kWords;  // 16-byte words of a row, rows of one instruction
     const int c = lane % kWords, sub = lane / kWords;
-    const uint16_t* from = static_cast<const uint16_t*>(a.q) + c * 8;
-    long long at[kQRuns];
-#pragma unroll
-    for (int w = 0; w < kQRuns; ++w) {
-      const int u = first + w * stride, r = (it.twice() ? u & 1 : u) * 32 + lane;
-      at[w] = -1;
-      if (u < end && r < it.rows) {
-        const int row = it.row0 + r, qi = row / p.G, g = row - qi * p.G;
-        const int bi = it.kind == 0 ? p.qrow[qi] : it.b * p.Q + qi;
-        const int b = bi / p.Q, i = bi - b * p.Q;
-        at[w] = b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head;
-        const uint16_t* line = static_cast<const uint16_t*>(a.q) + at[w];
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(line + D - 8));
+    bool ok = true;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass == 1) ok = __all_sync(0xffffffffu, wait(bar, phase));
+#pragma unroll 1
+      for (int u = first; u < end && ok; u += stride) {
+        const int run = (it.twice() ? u & 1 : u) * 32, r = run + lane;
+        if (run >= it.rows) continue;  // (the same in the whole warp)
+        const uint16_t* line = nullptr;
+        if (r < it.rows) {
+          const int row = it.row0 + r, qi = row / p.G, g = row - qi * p.G;
+          const int bi = it.kind == 0 ? p.qrow[qi] : it.b * p.Q + qi;
+          const int b = bi / p.Q, i = bi - b * p.Q;
+          line = static_cast<const uint16_t*>(a.q) + b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head;
+        }
+        if (pass == 0) {
+          if (line) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(line + D - 8));
+          }
+          continue;
+        }
+        const uint32_t to = q_smem + (half + (u >> 2)) * S::kTileBytes + (c >> 3) * (kTileKeys * 128);
+#pragma unroll 2
+        for (int v = 0; v < 32 / kRows; ++v) {
+          const int rr = (u & 3) * 32 + v * kRows + sub;
+          const uint16_t* from =
+              reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(line), v * kRows + sub));
+          if (from) cp16(to + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), from + c * 8, true);
+        }
       }
     }
-    if (!__all_sync(0xffffffffu, wait(bar, phase))) return false;
-#pragma unroll
-    for (int w = 0; w < kQRuns; ++w) {
-      const int u = first + w * stride;
-      if (u >= end || (it.twice() ? u & 1 : u) * 32 >= it.rows) continue;  // (the same in the whole warp)
-      const uint32_t to = q_smem + (half + (u >> 2)) * S::kTileBytes + (c >> 3) * (kTileKeys * 128);
-#pragma unroll 4
-      for (int v = 0; v < 32 / kRows; ++v) {
-        const int rr = (u & 3) * 32 + v * kRows + sub;
-        const long long row_at = __shfl_sync(0xffffffffu, at[w], v * kRows + sub);
-        if (row_at >= 0) cp16(to + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), from + row_at, true);
-      }
-    }
+    if (!ok) return false;
     landed();
     __syncwarp();
     if (lane == 0)
@@ -482,8 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 10) {
       // ---- the items, one ahead, and Q of the items with 128 rows or fewer ----
       Feed feed;
-      feed.left = 2;
-      feed.list = (int)blockIdx.x < (int)p.head[H_PRE_CTAS] ? 0 : 1;
+      feed.init(p);
       int q_uses[2] = {0, 0};
       bool ok = true;
       auto publish = [&](int n) {
@@ -495,8 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         return true;
       };
-      ok = publish(0);
       for (int n = 0; ok; ++n) {
+        ok = publish(n);
+        if (!ok) break;
         const Item it = peek(n);
         if (it.kind < 0) break;
         if (it.pair()) {  // the ring's warps load it
@@ -506,7 +529,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = load_q(it, 0, 1, 4, n & 1, &q_empty[n & 1], q_uses[n & 1] - 1);
           ++q_uses[n & 1];
         }
-        if (ok) ok = publish(n + 1);
       }
     } else if (warp > 10) {
       // ---- K and V: a warp per slot of the ring ----
@@ -1087,7 +1109,7 @@ int attention_launch(const AttentionLaunch& L, std::string* err) {
   p.head = reinterpret_cast<uint32_t*>(base);
   p.qrow = reinterpret_cast<int*>(base + w.qrow);
   p.coff = reinterpret_cast<int*>(base + w.coff);
-  p.chunk_of = reinterpret_cast<int*>(base + w.chunk_of);
+  p.chunk_of = reinterpret_cast<int4*>(base + w.chunk_of);
   p.stat = reinterpret_cast<int*>(base + w.stat);
   p.nan_from = reinterpret_cast<int*>(base + w.nan_from);
   p.pre_ml = reinterpret_cast<float2*>(base + w.pre_ml);
