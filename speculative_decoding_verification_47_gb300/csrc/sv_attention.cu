@@ -96,7 +96,7 @@ struct Args {
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // ---------------------------------------------------------------------------
-// 1. The plan: one CTA.
+// 1. The plan: one CTA, a thread per sequence (up to kPlanThreads).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kSplits = 256, kItemTiles = 4;
@@ -112,7 +112,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
   __syncthreads();
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  int s = warp_sums[lane];
+  int s = lane < (int)(blockDim.x >> 5) ? warp_sums[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, s, o);
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
   __shared__ unsigned long long tiles2;  // of 2 * kTileKeys keys, all sequences
   __shared__ unsigned flags;
   const AttentionLaunch& a = p.a;
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, threads = blockDim.x;  // (whole warps)
   if (t == 0) {
     tiles2 = 0;
     flags = 0;
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
   };
   int k0 = 0, len0 = 0, bad0 = 1;  // this thread's first sequence
   unsigned long long mine = 0;
-  for (int b = t; b < a.B; b += kPlanThreads) {
+  for (int b = t; b < a.B; b += threads) {
     int k, len;
     const int bad = look(b, k, len);
     if (b == t) {
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
     else
       mine += (unsigned)ceil_div(len + k, step);
   }
-  for (long long e = t; e < (long long)a.B * a.Hkv; e += kPlanThreads) p.nan_from[e] = 0x7fffffff;
+  for (long long e = t; e < (long long)a.B * a.Hkv; e += threads) p.nan_from[e] = 0x7fffffff;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if ((t & 31) == 0 && mine) atomicAdd(&tiles2, mine);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
   int per = 1;  // steps of a chunk
   if (units > aim) per = units < 0xffffffffull ? (int)(((unsigned)units - 1) / (unsigned)aim + 1) : (int)((units - 1) / aim + 1);
   int queries = 0, chunks = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
     const int b = b0 + t;
     int k = k0, len = len0, bad = bad0, q = 0, n = 0;
     if (b0 > 0 && b < a.B) bad = look(b, k, len);
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c = lane % kWords, sub = lane / kWords;
     bool ok = true;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int pass = phase < 0 ? 1 : 0; pass < 2; ++pass) {  // (nothing to wait for: no need to ask ahead)
       if (pass == 1) ok = __all_sync(0xffffffffu, wait(bar, phase));
 #pragma unroll 1
       for (int u = first; u < end && ok; u += stride) {
@@ -1071,7 +1071,8 @@ static cudaError_t run(const Args& p, const CUtensorMap& k, const CUtensorMap& v
     if (e != cudaSuccess) return e;
     ready[d].store(1, std::memory_order_release);
   }
-  cudaError_t e = launch(plan_kernel, 1, kPlanThreads, 0, st, p);
+  const int threads = p.a.B < kPlanThreads ? (p.a.B + 31) / 32 * 32 : kPlanThreads;
+  cudaError_t e = launch(plan_kernel, 1, (unsigned)threads, 0, st, p);
   if (e == cudaSuccess) e = launch(part_kernel<D>, (unsigned)p.grid, kThreads, Shape<D>::kSmem, st, p, k, v);
   const long long rows = (long long)p.a.B * p.Q * p.a.Hq;
   if (e == cudaSuccess)
