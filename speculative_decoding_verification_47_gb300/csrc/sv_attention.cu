@@ -99,7 +99,8 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 // 1. The plan: one CTA, a thread per sequence (up to kPlanThreads).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
-constexpr int kSplits = 256, kItemTiles = 4;
+constexpr int kSplits = 256;
+constexpr float kItemTiles = 4.f, kMergeTiles = 4.f, kOwnTiles = 0.8f, kOwnItemTiles = 1.5f;
 
 // Inclusive prefix sum over the CTA (also the total).
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
@@ -192,34 +193,42 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
   const long long rows = (long long)queries * p.G;
   const int row_items = (int)((rows + kItemRows - 1) / kItemRows) * a.Hkv;
   if (t < 32) {
-    // Splits of the prefix: the one of up to kSplits for which the CTAs that its share of
-    // the work gets are done first, where an item's beginning and end (Q, the parts'
-    // stores) cost kItemTiles tiles.  The partial results have room for kSlack * grid
-    // items beside one per row item.
+    // Splits of the prefix, and the CTAs that begin with it: those for which the call is
+    // estimated to be done first.  The unit is a key tile of a prefix item; an item's
+    // beginning and end cost kItemTiles and its parts in the merge kMergeTiles, 256 keys
+    // of a sequence kOwnTiles and an item of them kOwnItemTiles.  CTAs that are done with
+    // their list take from the other, so the last item ends with the average of all the
+    // work, or with the prefix's rounds where these take longer.  As many CTAs begin with the
+    // prefix as end it by then (its items are the longest: begun late they would be the
+    // last).  The partial results have room for kSlack * grid items beside one per row item.
     int splits = 0, split_tiles = 0, ctas = 0;
     if (ptiles > 0 && row_items > 0) {
-      const float pre = (float)row_items * ptiles;
-      ctas = (int)(p.grid * (pre / (pre + (float)units)) + 0.5f);
-      if (ctas < 1) ctas = 1;
+      const float own = kOwnTiles * (float)units + kOwnItemTiles * (float)(chunks * a.Hkv * p.row_tiles);
       const int most = max(1, min(ptiles, kSlack * p.grid / row_items));
       float best = 3e38f;
       for (int c = t + 1; c <= most && c <= kSplits; c += 32) {
-        const int tiles = ceil_div(ptiles, c), parts = ceil_div(ptiles, tiles);
-        const float cost = (float)ceil_div(row_items * parts, ctas) * (float)(tiles + kItemTiles);
+        const int tiles = ceil_div(ptiles, c), parts = ceil_div(ptiles, tiles), items = row_items * parts;
+        const float item = (float)tiles + kItemTiles, average = ((float)items * item + own) / (float)p.grid;
+        const int rounds = max(ceil_div(items, p.grid), min(items, (int)(average / item)));
+        const int first = ceil_div(items, rounds);
+        const float cost = fmaxf(average, (float)ceil_div(items, first) * item) + (float)items * kMergeTiles / (float)p.grid;
         if (cost < best) {
           best = cost;
           splits = parts;
           split_tiles = tiles;
+          ctas = first;
         }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const float c = __shfl_xor_sync(0xffffffffu, best, o);
         const int s = __shfl_xor_sync(0xffffffffu, splits, o), n = __shfl_xor_sync(0xffffffffu, split_tiles, o);
+        const int f = __shfl_xor_sync(0xffffffffu, ctas, o);
         if (c < best || (c == best && s < splits)) {
           best = c;
           splits = s;
           split_tiles = n;
+          ctas = f;
         }
       }
     }
