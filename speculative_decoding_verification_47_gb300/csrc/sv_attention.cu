@@ -64,7 +64,7 @@ __host__ inline Layout layout(int B, int K, int Hq, int Hkv, int D, long long pr
     at = (at + bytes + 255) / 256 * 256;
     return here;
   };
-  w.qrow = take((size_t)Q * 4);
+  w.qrow = take((size_t)Q * 16);
   w.coff = take((size_t)B * 4);
   w.chunk_of = take((size_t)(w.own_slots / (2 * Hkv)) * 16);
   w.stat = take((size_t)B * 4);
@@ -84,7 +84,7 @@ struct Args {
   int box;  // tokens of one TMA box, 0: copies by row
   int G, Q, row_tiles, grid;  // heads per key head, K + 1, item tiles of a sequence's rows, CTAs of part_kernel
   uint32_t* head;
-  int* qrow;      // compact query -> b * Q + i
+  int4* qrow;     // compact query -> b * Q + i, its sequence's drafts, committed tokens and first chunk
   int* coff;      // first chunk of a sequence
   int4* chunk_of;  // chunk -> sequence, its drafts, committed tokens and first chunk
   int* stat;      // a sequence's flags
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
     const int ce = chunks + block_scan(n, warp_sums, total) - n;
     chunks += total;
     if (b < a.B) p.coff[b] = ce;
-    for (int i = 0; i < q; ++i) p.qrow[qe + i] = b * p.Q + i;
+    for (int i = 0; i < q; ++i) p.qrow[qe + i] = make_int4(b * p.Q + i, k, len, ce);
     for (int c = 0; c < n; ++c) p.chunk_of[ce + c] = make_int4(b, k, len, ce);
   }
   const int ptiles = ceil_div(a.prefix_len, kTileKeys);
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint16_t* line = nullptr;
         if (r < it.rows) {
           const int row = it.row0 + r, qi = row / p.G, g = row - qi * p.G;
-          const int bi = it.kind == 0 ? p.qrow[qi] : it.b * p.Q + qi;
+          const int bi = it.kind == 0 ? p.qrow[qi].x : it.b * p.Q + qi;
           const int b = bi / p.Q, i = bi - b * p.Q;
           line = static_cast<const uint16_t*>(a.q) + b * a.q_seq + i * a.q_pos + (long long)(it.h * p.G + g) * a.q_head;
         }
@@ -951,9 +951,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // 3. The parts of a row together.  A warp has eight rows and four quads of columns
-// of each (eight rows' quads are a whole line); kGroups warps share the rows.  The
-// parts' maxima and sums are read first, so that the sum over the parts is one of
-// independent loads.
+// of each (eight rows' quads are a whole line); kGroups warps share the rows.  Small
+// calls are bound by the chain of loads that depend on each other (what a row is, its
+// parts): one word has all of a row, and kAtOnce parts come with their maxima and sums
+// under a running maximum (one token 17.5 -> 15.7 us, 64 x 8 round 62.8 -> 61.2, 33
+// sequences of 12 heads 35.6 -> 32.0, against maxima first and one more load of each).
 // ---------------------------------------------------------------------------
 constexpr int kMergeThreads = 256;
 
@@ -961,6 +963,7 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
   const AttentionLaunch& a = p.a;
   constexpr int N = 2, kGroups = D / 16 / N;  // quads of a thread, warps per eight rows
+  constexpr int kAtOnce = 3;  // (2 and 4: 33.0 and 32.1 us in the last of these, 16.9 and 16.3 in the first)
   const float nan = __int_as_float(0x7fffffff);
   pdl_wait();
   const int lane = threadIdx.x & 31, sub = lane & 3;
@@ -985,62 +988,82 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
   const int h = (int)(id / rows);
   const unsigned r = id - h * rows, query = r / p.G;
   const int g = (int)(r - query * p.G);
-  const int bi = p.qrow[query], b = bi / p.Q, i = bi - b * p.Q, hq = h * p.G + g;
-  const int k = a.kpr ? a.kpr[b] : a.K, len = a.lens[b], first = p.coff[b];
+  const int4 of = p.qrow[query];
+  const int bi = of.x, k = of.y, len = of.z, first = of.w;
+  const int b = bi / p.Q, i = bi - b * p.Q, hq = h * p.G + g;
   const int splits = p.head[H_SPLITS], per = p.head[H_SPLIT_TILES], keys = p.head[H_CHUNK_KEYS];
   const bool dead = p.stat[b] || p.head[H_BAD_PREFIX];
   const bool lost = len + i > p.nan_from[(long long)b * a.Hkv + h];
 
-  // every part of the row: f(maximum and sum, its quads)
+  // The row's parts: of the prefix, `extra` ones of second streams there (the last split
+  // has none if it is a single tile), and the chunks', of one stream or two.
   const unsigned tile0 = r / kItemRows * kItemRows;
-  const int ptiles = ceil_div(a.prefix_len, kTileKeys), extra = rows - tile0 > 128 ? 0 : splits;
-  const int own = i * p.G + g, all = p.Q * p.G, chunks = dead ? 0 : ceil_div(len + k, keys);
+  const int ptiles = ceil_div(a.prefix_len, kTileKeys), own = i * p.G + g, all = p.Q * p.G, chunks = ceil_div(len + k, keys);
+  const int extra = rows - tile0 > 128 || per < 2 ? 0 : splits - (ptiles - (splits - 1) * per < 2 ? 1 : 0);
   const bool two = (k + 1) * p.G - own / kItemRows * kItemRows <= 128;
+  const int before = splits + extra, last = len + k - (chunks - 1) * keys;
+  const int parts = dead ? 0 : before + (two ? 2 * chunks - (last > kTileKeys ? 0 : 1) : chunks);
   const int quad = (group * N * 4 + sub) * 4;
-  auto parts = [&](auto f) {
-    if (dead) return;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const long long at = ((long long)s * a.Hkv + h) * rows;
-      f(p.pre_ml + at + r, p.pre_o + at * D + (long long)quad * rows + r * 4, rows);
-    }
-#pragma unroll 4
-    for (int s = 0; s < extra; ++s)
-      if (min(per, ptiles - s * per) >= 2) {
-        const long long at = ((long long)s * a.Hkv + h) * 128;
-        f(p.extra_ml + at + (r - tile0), p.extra_o + at * D + quad * 128 + (r - tile0) * 4, 128u);
-      }
-#pragma unroll 4
-    for (int c = 0; c < 2 * chunks; ++c)
-      if ((c & 1) == 0 || (two && len + k - (c >> 1) * keys > kTileKeys)) {
-        const long long at = (((long long)(first + (c >> 1)) * a.Hkv + h) * 2 + (c & 1)) * all;
-        f(p.own_ml + at + own, p.own_o + at * D + (long long)quad * all + own * 4, (unsigned)all);
-      }
-  };
-  float M = -INFINITY;
-  parts([&](const float2* ml, const float*, unsigned) {
-    const float2 x = *ml;
-    M = x.x > M ? x.x : M;
-  });
-  float l = 0.f, acc[N][4];
+  float M = -INFINITY, l = 0.f, acc[N][4];
 #pragma unroll
   for (int q = 0; q < N; ++q)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[q][e] = 0.f;
-  parts([&](const float2* ml, const float* o, unsigned rows_o) {
-    const float2 x = *ml;
-    // a part that saw nothing has weight 0, whatever is there (a NaN in its sum goes on)
-    const float w = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - M);
-    l += x.y * w;
+  for (int n = 0; n < parts; n += kAtOnce) {
+    // kAtOnce parts' loads in flight together
+    float2 x[kAtOnce];
+    float4 v[kAtOnce][N];
 #pragma unroll
-    for (int q = 0; q < N; ++q) {
-      const float4 v = *reinterpret_cast<const float4*>(o + (long long)q * 16 * rows_o);
-      acc[q][0] = w == 0.f ? acc[q][0] : __fmaf_rn(v.x, w, acc[q][0]);
-      acc[q][1] = w == 0.f ? acc[q][1] : __fmaf_rn(v.y, w, acc[q][1]);
-      acc[q][2] = w == 0.f ? acc[q][2] : __fmaf_rn(v.z, w, acc[q][2]);
-      acc[q][3] = w == 0.f ? acc[q][3] : __fmaf_rn(v.w, w, acc[q][3]);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int at = n + u;
+      x[u] = make_float2(-INFINITY, 0.f);
+      if (at >= parts) continue;
+      const float2* ml;
+      const float* o;
+      long long rows_o;
+      if (at < before) {
+        const bool second = at >= splits;
+        const long long part = (long long)(second ? at - splits : at) * a.Hkv + h;
+        rows_o = second ? 128 : rows;
+        const unsigned row = second ? r - tile0 : r;
+        ml = (second ? p.extra_ml : p.pre_ml) + part * rows_o + row;
+        o = (second ? p.extra_o : p.pre_o) + part * rows_o * D + row * 4;
+      } else {
+        const int c = two ? at - before : 2 * (at - before);
+        const long long part = ((long long)(first + (c >> 1)) * a.Hkv + h) * 2 + (c & 1);
+        rows_o = all;
+        ml = p.own_ml + part * rows_o + own;
+        o = p.own_o + part * rows_o * D + own * 4;
+      }
+      x[u] = *ml;
+#pragma unroll
+      for (int q = 0; q < N; ++q) v[u][q] = *reinterpret_cast<const float4*>(o + (quad + q * 16) * rows_o);
     }
-  });
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) top = x[u].x > top ? x[u].x : top;
+    const float f = M == top ? 1.f : ex2(M - top);
+    M = top;
+    l *= f;
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[q][e] *= f;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      // a part that saw nothing has weight 0, whatever is there (a NaN in its sum goes on)
+      const float w = x[u].x == -INFINITY ? (x[u].y == 0.f ? 0.f : 1.f) : ex2(x[u].x - M);
+      l += x[u].y * w;
+      if (w == 0.f) continue;
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        acc[q][0] = __fmaf_rn(v[u][q].x, w, acc[q][0]);
+        acc[q][1] = __fmaf_rn(v[u][q].y, w, acc[q][1]);
+        acc[q][2] = __fmaf_rn(v[u][q].z, w, acc[q][2]);
+        acc[q][3] = __fmaf_rn(v[u][q].w, w, acc[q][3]);
+      }
+    }
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t* op = static_cast<uint16_t*>(a.out) + b * a.o_seq + i * a.o_pos + hq * a.o_head + quad;
 #pragma unroll
@@ -1117,7 +1140,7 @@ int attention_launch(const AttentionLaunch& L, std::string* err) {
   const att::Layout w = att::layout(L.B, L.K, L.Hq, L.Hkv, L.D, L.prefix_len, (long long)L.max_pages * L.page_size);
   char* base = static_cast<char*>(L.workspace);
   p.head = reinterpret_cast<uint32_t*>(base);
-  p.qrow = reinterpret_cast<int*>(base + w.qrow);
+  p.qrow = reinterpret_cast<int4*>(base + w.qrow);
   p.coff = reinterpret_cast<int*>(base + w.coff);
   p.chunk_of = reinterpret_cast<int4*>(base + w.chunk_of);
   p.stat = reinterpret_cast<int*>(base + w.stat);
