@@ -41,7 +41,7 @@ enum { H_FLAGS, H_BAD_PREFIX, H_NEXT_PRE, H_NEXT_OWN, H_QUERIES, H_CHUNKS, H_CHU
        H_PRE_ITEMS, H_OWN_ITEMS, H_PRE_CTAS, H_WORDS = 64 };
 
 struct Layout {  // byte offsets into the workspace
-  size_t qrow, coff, chunk_of, stat, nan_from, pre_ml, pre_o, extra_ml, extra_o, own_ml, own_o, total;
+  size_t qrow, chunk_of, stat, nan_from, pre_ml, pre_o, extra_ml, extra_o, own_ml, own_o, total;
   long long pre_rows, extra_rows, own_slots;
 };
 
@@ -65,7 +65,6 @@ __host__ inline Layout layout(int B, int K, int Hq, int Hkv, int D, long long pr
     return here;
   };
   w.qrow = take((size_t)Q * 16);
-  w.coff = take((size_t)B * 4);
   w.chunk_of = take((size_t)(w.own_slots / (2 * Hkv)) * 16);
   w.stat = take((size_t)B * 4);
   w.nan_from = take((size_t)B * Hkv * 4);
@@ -85,7 +84,6 @@ struct Args {
   int G, Q, row_tiles, grid;  // heads per key head, K + 1, item tiles of a sequence's rows, CTAs of part_kernel
   uint32_t* head;
   int4* qrow;     // compact query -> b * Q + i, its sequence's drafts, committed tokens and first chunk
-  int* coff;      // first chunk of a sequence
   int4* chunk_of;  // chunk -> sequence, its drafts, committed tokens and first chunk
   int* stat;      // a sequence's flags
   int* nan_from;  // [B][Hkv] first own token whose drafted value is not finite
@@ -185,7 +183,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
     queries += total;
     const int ce = chunks + block_scan(n, warp_sums, total) - n;
     chunks += total;
-    if (b < a.B) p.coff[b] = ce;
     for (int i = 0; i < q; ++i) p.qrow[qe + i] = make_int4(b * p.Q + i, k, len, ce);
     for (int c = 0; c < n; ++c) p.chunk_of[ce + c] = make_int4(b, k, len, ce);
   }
@@ -1141,7 +1138,6 @@ int attention_launch(const AttentionLaunch& L, std::string* err) {
   char* base = static_cast<char*>(L.workspace);
   p.head = reinterpret_cast<uint32_t*>(base);
   p.qrow = reinterpret_cast<int4*>(base + w.qrow);
-  p.coff = reinterpret_cast<int*>(base + w.coff);
   p.chunk_of = reinterpret_cast<int4*>(base + w.chunk_of);
   p.stat = reinterpret_cast<int*>(base + w.stat);
   p.nan_from = reinterpret_cast<int*>(base + w.nan_from);
