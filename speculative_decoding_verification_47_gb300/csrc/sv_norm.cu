@@ -25,6 +25,8 @@ namespace norm {
 constexpr float kE4M3Max = 448.f;
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126: 1 / c stays finite
 
+constexpr int kShifted = -8;  // in place of a vector's width: runs of 8 at a common phase
+
 struct Args {
   const void* x;
   long long ldx;
@@ -144,7 +146,11 @@ __device__ __forceinline__ void reduce(float (&part)[2][32], float& sum, float& 
 // per row).  Thread t holds elements (j * blockDim.x + t) * VEC .., j < NV;
 // rows longer than NV * VEC * blockDim.x are read again for the scaling, each
 // element by the thread that overwrites it.
-template <typename T, bool Q8, int VEC, int NV>
+//
+// SHIFT: rows that start anywhere, all arrays' at the same place of an aligned run of
+// VEC elements (`phase`).  The vectors are the aligned runs, so the first and the last
+// one of a row may be cut: these go element by element, as zeros outside of the row.
+template <typename T, bool Q8, int VEC, int NV, bool SHIFT = false>
 __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
   __shared__ float part[2][32];
   pdl_launch_dependents();
@@ -153,13 +159,46 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
   const bool live = m < a.M;
   const T* x = static_cast<const T*>(a.x) + (live ? m : 0) * a.ldx;
   const T* res = a.res ? static_cast<const T*>(a.res) + (live ? m : 0) * a.ldr : nullptr;
+  const int phase = SHIFT && live ? (int)((m * a.ldx) & (VEC - 1)) : 0;
   pdl_wait();  // the launch may overlap the kernel that wrote x
 
+  auto whole = [&](int k) { return !SHIFT || (k >= 0 && k + VEC <= a.H); };
+  auto get = [&](const auto* from, int k, float (&f)[VEC]) {
+    if (whole(k)) {
+      load<VEC>(from + k, f);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      float one[1] = {0.f};
+      if (k + i >= 0 && k + i < a.H) load<1>(from + k + i, one);
+      f[i] = one[0];
+    }
+  };
+  auto weight = [&](int k, float (&f)[VEC]) {
+    if constexpr (SHIFT && VEC > 1) {
+      if (whole(k)) {  // (words of two on 4 bytes, the elements between them)
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(a.w + (k & ~1));
+        uint32_t h[VEC / 2 + 1];
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) h[i] = at[i];
+        h[VEC / 2] = k & 1 ? a.w[k + VEC - 1] : 0u;
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+          const uint32_t two = k & 1 ? __funnelshift_r(h[i], h[i + 1], 16) : h[i];
+          f[2 * i] = bf16_lo(two);
+          f[2 * i + 1] = bf16_hi(two);
+        }
+        return;
+      }
+    }
+    get(a.w, k, f);
+  };
   auto sum_at = [&](int k, float (&s)[VEC]) {
-    load<VEC>(x + k, s);
+    get(x, k, s);
     if (res) {
       float r[VEC];
-      load<VEC>(res + k, r);
+      get(res, k, r);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) s[i] += r[i];
     }
@@ -167,7 +206,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
   float s[NV][VEC], ss = 0.f, top = 0.f;
   auto gather = [&](const float (&v)[VEC], int k) {
     float w[VEC];
-    if (Q8) load<VEC>(a.w + k, w);
+    if (Q8) weight(k, w);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       ss = __fmaf_rn(v[i], v[i], ss);
@@ -176,7 +215,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
   };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int k = (j * n + t) * VEC;
+    const int k = (j * n + t) * VEC - phase;
     if (k < a.H) {
       sum_at(k, s[j]);
     } else {
@@ -186,7 +225,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int k = (j * n + t) * VEC;
+    const int k = (j * n + t) * VEC - phase;
     if (k < a.H) gather(s[j], k);
   }
   for (long long k = (long long)(NV * n + t) * VEC; k < a.H; k += (long long)n * VEC) {
@@ -202,13 +241,13 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
     top = 0.f;
     auto again = [&](const float (&v)[VEC], int k) {
       float w[VEC];
-      load<VEC>(a.w + k, w);
+      weight(k, w);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) top = max_nan(top, fabsf(v[i] * r * w[i]));
     };
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int k = (j * n + t) * VEC;
+      const int k = (j * n + t) * VEC - phase;
       if (k < a.H) again(s[j], k);
     }
     for (long long k = (long long)(NV * n + t) * VEC; k < a.H; k += (long long)n * VEC) {
@@ -233,18 +272,31 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
   T* sum = a.sum ? static_cast<T*>(a.sum) + m * a.lds : nullptr;
   auto finish = [&](const float (&v)[VEC], int k) {
     float w[VEC], y[VEC];
-    load<VEC>(a.w + k, w);
+    weight(k, w);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) y[i] = v[i] * r * w[i] * inv;
-    if (sum) store<VEC>(sum + k, v);
-    if (Q8)
-      store8<VEC>(static_cast<uint8_t*>(a.out) + m * a.ldo + k, y);
-    else
-      store<VEC>(static_cast<uint16_t*>(a.out) + m * a.ldo + k, y);
+    if (whole(k)) {
+      if (sum) store<VEC>(sum + k, v);
+      if (Q8)
+        store8<VEC>(static_cast<uint8_t*>(a.out) + m * a.ldo + k, y);
+      else
+        store<VEC>(static_cast<uint16_t*>(a.out) + m * a.ldo + k, y);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      if (k + i < 0 || k + i >= a.H) continue;
+      const float v1[1] = {v[i]}, y1[1] = {y[i]};
+      if (sum) store<1>(sum + k + i, v1);
+      if (Q8)
+        store8<1>(static_cast<uint8_t*>(a.out) + m * a.ldo + k + i, y1);
+      else
+        store<1>(static_cast<uint16_t*>(a.out) + m * a.ldo + k + i, y1);
+    }
   };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int k = (j * n + t) * VEC;
+    const int k = (j * n + t) * VEC - phase;
     if (k < a.H) finish(s[j], k);
   }
   for (long long k = (long long)(NV * n + t) * VEC; k < a.H; k += (long long)n * VEC) {
@@ -415,7 +467,7 @@ static cudaError_t launch_ring(const Args& a, int threads, int slots, int ctas, 
   return cudaLaunchKernelEx(&cfg, ring_kernel<T, Q8>, a, slots);
 }
 
-template <typename T, bool Q8, int VEC, int NV>
+template <typename T, bool Q8, int VEC, int NV, bool SHIFT = false>
 static cudaError_t launch(const Args& a, int threads, int rows, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.M + (long long)rows - 1) / rows), 1, 1);
@@ -426,14 +478,15 @@ static cudaError_t launch(const Args& a, int threads, int rows, cudaStream_t st)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_kernel<T, Q8, VEC, NV>, a);
+  return cudaLaunchKernelEx(&cfg, norm_kernel<T, Q8, VEC, NV, SHIFT>, a);
 }
 
 template <typename T, bool Q8>
 static cudaError_t dispatch(const Args& a, int vec, cudaStream_t st) {
   constexpr int kPer = 16;  // elements a thread keeps
-  int threads = 32;
-  while (threads < 1024 && (long long)threads * kPer < a.H) threads *= 2;
+  int threads = 32;  // (not only powers of two: 2048 x 4097 34.4 us with 512 threads, 26.7 with 288)
+  const int spread = a.H + (vec == kShifted ? 7 : 0);
+  while (threads < 1024 && (long long)threads * kPer < spread) threads += 32;
   const int rows = threads == 32 ? 4 : 1;
   // More rows than the card holds CTAs of the plain kernel at once (1024 threads an
   // SM), and rows in whole 16-byte words.  Not for float32 rows: twice the bytes are in
@@ -445,6 +498,7 @@ static cudaError_t dispatch(const Args& a, int vec, cudaStream_t st) {
     if (sizeof(T) == 2 && ctas > 0) return launch_ring<uint16_t, Q8>(a, threads, slots, ctas, smem, st);
   }
   if (vec == 8) return launch<T, Q8, 8, kPer / 8>(a, threads, rows, st);
+  if (vec == kShifted && spread <= threads * kPer) return launch<T, Q8, 8, kPer / 8, true>(a, threads, rows, st);
   if (vec == 2) return launch<T, Q8, 2, kPer / 2>(a, threads, rows, st);
   return launch<T, Q8, 1, kPer>(a, threads, rows, st);
 }
@@ -464,7 +518,16 @@ int norm_launch(const NormLaunch& L, std::string* err) {
     return L.H % v == 0 && on(L.x, L.ldx, es) && (!L.residual || on(L.residual, L.ldr, es)) &&
            (!L.residual_out || on(L.residual_out, L.ldro, es)) && on(L.w, 0, 2) && on(L.out, L.ldo, os);
   };
-  const int vec = fits(8) ? 8 : (fits(2) ? 2 : 1);
+  // Odd rows: runs of 8 at a phase that a row's arrays share.  2048 x 4097 bf16 to e4m3
+  // 26.7 us element by element, 25.3 in runs; 1 x 5001 4.5 and 3.3; but 12000 x 33 (a
+  // warp per row, most of its runs cut) 9.5 and 10.8.
+  auto shares = [&](const void* p, long long ld, size_t e) {
+    return reinterpret_cast<uintptr_t>(p) % (e == 1 ? 8 : 16) == 0 && (L.M == 1 || (ld - L.ldx) % 8 == 0);
+  };
+  const bool shifted = shares(L.x, L.ldx, es) && (!L.residual || shares(L.residual, L.ldr, es)) &&
+                       (!L.residual_out || shares(L.residual_out, L.ldro, es)) && shares(L.out, L.ldo, os) &&
+                       reinterpret_cast<uintptr_t>(L.w) % 4 == 0 && L.H > 512 && L.H + 7LL <= 16 * 1024;
+  const int vec = fits(8) ? 8 : (fits(2) ? 2 : (shifted ? norm::kShifted : 1));
   cudaStream_t st = static_cast<cudaStream_t>(L.stream);
   const bool q8 = L.out_dtype == SV_E4M3;
   cudaError_t e;

@@ -215,3 +215,31 @@ def test_stream_and_graph():
         g.replay()
         torch.cuda.synchronize()
         check(x, x, w, "e4m3", y, c, s)
+
+
+@pytest.mark.parametrize("out", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [513, 519, 1001, 4097, 16377, 16379])
+def test_odd_rows_in_place(H, dtype, out):
+    """Rows that start at every place of an aligned run of eight, with a common stride, and
+    with strides that differ (16379: one element more than the runs hold).  The sum goes
+    over the residual; columns behind H, which the next row's run reaches into, and the
+    rows' neighbours stay as they are."""
+    g = torch.Generator(device="cuda").manual_seed(H)
+    M = 19
+    w = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(torch.bfloat16)
+    for pads in [(0, 0, 0), (4, 12, 20), (1, 1, 9), (1, 2, 0)]:
+        t, code = DT[dtype]
+        x, r = (torch.randn(M, H + p, generator=g, device="cuda").to(t) for p in pads[:2])
+        x0, r0 = x.clone(), r.clone()
+        ldo = H + pads[2]
+        y = torch.full((M, ldo), 77, dtype=torch.uint8, device="cuda") if out == "e4m3" else torch.full(
+            (M, ldo), 77.0, dtype=torch.bfloat16, device="cuda")
+        kept = y.clone()
+        c = torch.empty(M, device="cuda") if out == "e4m3" else None
+        sb.sv_rmsnorm_residual(x, H + pads[0], r, H + pads[1], w, 1e-5, r, H + pads[1], code, y, ldo, OUT[out][1],
+                               c, M, H)
+        assert torch.equal(x, x0)
+        assert torch.equal(r[:, H:], r0[:, H:]) and torch.equal(y[:, H:], kept[:, H:])
+        got = y.view(torch.float8_e4m3fn) if out == "e4m3" else y
+        check(x0[:, :H], r0[:, :H], w, out, got, c, r[:, :H])
