@@ -20,9 +20,9 @@
  *   - Problems only the device can see (a draft token outside [0, V), a bad
  *     k_b, non-finite logits, a bad temperature or uniform, a KV capacity
  *     overflow, a bad page, a bounded wait that ran out) never trap: the
- *     affected sequence's outputs become n_accepted = 0 and out_tokens = -1 (NaN
- *     where they are not tokens), and a bit is set in the workspace's flag word (SV_FLAG_*), readable with
- *     sv_read_device_flags.
+ *     affected sequence's outputs become n_accepted = 0 and out_tokens = -1 (each
+ *     call with other outputs says what becomes of them), and a bit is set in the
+ *     workspace's flag word (SV_FLAG_*), readable with sv_read_device_flags.
  *   - Each call runs on the calling thread's current device.  The kernels'
  *     launch attributes and the device's properties are set up by the first
  *     call on each device (ordinals 0..63; a call on a higher ordinal
@@ -416,6 +416,7 @@ sv_status sv_lmhead_rmsnorm(const void* hidden, const void* norm_w, float eps, c
  * past its table (SV_FLAG_BAD_N), or with a page it needs outside
  * [0, num_pages) (SV_FLAG_BAD_PAGE; a bad prefix page fails every sequence)
  * gets NaN in out and lse at every position 0 .. k_b (0 .. K for a bad k_b).
+ * After a bounded wait that ran out (SV_FLAG_TIMEOUT) every sequence does.
  */
 size_t sv_prefix_attention_workspace_size(int B, int K, int Hq, int Hkv, int D, int prefix_len,
                                           int max_own_len);

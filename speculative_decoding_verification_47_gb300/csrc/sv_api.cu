@@ -2,6 +2,7 @@
 // sizing and error reporting around the kernels' launchers.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <string>
 
@@ -10,6 +11,7 @@
 namespace {
 
 thread_local std::string g_last_error;
+std::atomic<int> g_wait_tries{sv::kWaitTries};
 
 sv_status fail(sv_status s, const std::string& msg) {
   g_last_error = msg;
@@ -371,6 +373,7 @@ sv_status sv_prefix_attention(const void* q, int64_t q_seq_stride, int64_t q_pos
   L.Hq = Hq;
   L.Hkv = Hkv;
   L.D = D;
+  L.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
   if (!workspace || !aligned(workspace, 256))
     return fail(SV_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");
   if (workspace_bytes < sv::attention_workspace_bytes(B, K, Hq, Hkv, D, prefix_len, (int)own))
@@ -496,5 +499,7 @@ sv_status sv_read_device_flags(const void* workspace, uint32_t* flags_host, void
 }
 
 const char* sv_last_error(void) { return g_last_error.c_str(); }
+
+void sv_internal_wait_tries(int tries) { g_wait_tries.store(tries < 0 ? sv::kWaitTries : tries); }
 
 }  // extern "C"

@@ -390,9 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kIdS = tc::idesc(false, false, 128, kTileKeys), kIdO = tc::idesc(false, true, 128, D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kSlots], raw[kSlots], empty[kSlots], q_full[2], q_empty[2], q_go, s_full[2],
-      p_ready[2][2], o_full[2], turn_of[2], item_full[2], item_empty[2];
+      p_ready[2][2], o_full[2], turn_of[2], item_full[2], item_empty[2], drained[2];
   __shared__ Item items[2];
   __shared__ uint32_t tmem_base;
+  __shared__ int2 loaded[kLoaders];  // tiles and looks of a ring slot, at the end
   __shared__ int failed;
   const AttentionLaunch& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -413,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_ready[s][0], 128);
       mbar_init(&p_ready[s][1], 128);
       mbar_init(&o_full[s], 1);
+      mbar_init(&drained[s], 1);
       mbar_init(&item_full[s], 1);
       mbar_init(&item_empty[s], 8 + 2 + kLoaders);  // a lane of every other warp
     }
@@ -434,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The items pass through two slots, written ahead by warp 10.
   auto peek = [&](int n) {  // item n of this CTA, read by a whole warp
     // (word by word: as a structure it would live in local memory)
-    const bool ok = __all_sync(0xffffffffu, tc::wait_bounded(&item_full[n & 1], (uint32_t)((n >> 1) & 1)));
+    const bool ok = __all_sync(
+        0xffffffffu, a.wait_tries > 0 && tc::wait_bounded(&item_full[n & 1], (uint32_t)((n >> 1) & 1)));
     if (!ok) failed = 1;
     const int4* from = reinterpret_cast<const int4*>(&items[n & 1]);
     const int4 w0 = from[0], w1 = from[1], w2 = from[2];
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = load_q(it, slot, kSlots, 8, 0, &q_go, pairs);
           ++pairs;
         };
-        for (int x = (slot + kSlots - turn % kSlots) % kSlots; x < total; x += kSlots, ++use) {
+        for (int x = (slot + kSlots - turn % kSlots) % kSlots; x < total; x += kSlots) {
           // which tile: x < d: K_x; else pairs (V_j, K_{j+d}) while both exist, then the last V's
           int j = x, is_v = 0;
           if (x >= d) {
@@ -667,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_async();
           }
           if (look || !p.box) mbar_arrive(&full[slot]);
+          ++use;
           if (q_due && ok) my_q();
           if (!ok) break;
         }
@@ -674,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q_due) my_q();
         turn += total;
       }
+      if (lane == 0) loaded[slot] = make_int2(use, looks);
     } else {
       // ---- the products of one stream, issued by one thread ----
       const int s = warp - 8;
@@ -953,7 +958,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (tid == 0 && failed) atomicOr(&p.head[H_FLAGS], SV_FLAG_TIMEOUT);
+  if (failed) {  // (the same in every thread) a wait ran out: copies and products on their way end first
+    if (lane == 0 && (warp == 8 || warp == 9)) {
+      tc::commit<1>(smem_addr(&drained[warp - 8]));
+      (void)tc::wait_bounded(&drained[warp - 8], 0);
+    }
+    if (lane == 0 && warp > 10) {
+      const int slot = warp - 11, use = loaded[slot].x, looks = loaded[slot].y;
+      if (looks > 0) (void)tc::wait_bounded(&raw[slot], (uint32_t)((looks - 1) & 1));
+      if (use > 0) (void)tc::wait_bounded(&full[slot], (uint32_t)((use - 1) & 1));
+    }
+    if (tid == 0) atomicOr(&p.head[H_FLAGS], SV_FLAG_TIMEOUT);
+    __syncthreads();
+  }
   if (warp == 8) tc::dealloc<1>(tmem, 512);
 }
 
@@ -979,7 +996,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
   const int queries = p.head[H_QUERIES], group = (int)(wid % kGroups);
   const unsigned rows = (unsigned)queries * p.G, id = wid / kGroups * 8 + (lane >> 2);
 
-  if (p.head[H_FLAGS] & (SV_FLAG_BAD_K | SV_FLAG_BAD_N)) {
+  const uint32_t flags = p.head[H_FLAGS];
+  if (flags & (SV_FLAG_BAD_K | SV_FLAG_BAD_N)) {
     // sequences that have no rows: every position that the caller reads is NaN
     for (long long b = blockIdx.x; b < a.B; b += gridDim.x) {
       const int bad = p.stat[b];
@@ -1000,7 +1018,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
   const int bi = of.x, k = of.y, len = of.z, first = of.w;
   const int b = bi / p.Q, i = bi - b * p.Q, hq = h * p.G + g;
   const int splits = p.head[H_SPLITS], per = p.head[H_SPLIT_TILES], keys = p.head[H_CHUNK_KEYS];
-  const bool dead = p.stat[b] || p.head[H_BAD_PREFIX];
+  // (a wait that ran out leaves parts unwritten: which ones is not known)
+  const bool dead = p.stat[b] || p.head[H_BAD_PREFIX] || (flags & SV_FLAG_TIMEOUT);
   const bool lost = len + i > p.nan_from[(long long)b * a.Hkv + h];
 
   // The row's parts: of the prefix, `extra` ones of second streams there (the last split

@@ -11,6 +11,11 @@
 
 namespace sv {
 
+// Tries of a bounded wait of the layer operators' kernels (a try suspends for up to half a
+// millisecond, so about a second); 0 gives up without trying, which takes a call down the path of
+// a wait that ran out.  sv_internal_wait_tries (not part of the header) changes it for tests.
+constexpr int kWaitTries = 2048;
+
 struct VerifyLaunch {
   const void* target;
   long long t_seq, t_pos;  // elements
@@ -153,6 +158,7 @@ struct AttentionLaunch {
   int B, K, Hq, Hkv, D;
   void* workspace;
   void* stream;
+  int wait_tries = kWaitTries;
 };
 
 // Enqueue the shared-prefix attention.  Returns an sv_status; fills *err on failure.

@@ -1,0 +1,44 @@
+"""A bounded wait that runs out: the call ends, reports SV_FLAG_TIMEOUT and leaves NaN, never
+results of an earlier call; the next call is sound.  The waits are told to give up without a
+try, so that the copies and products on their way have to be waited for at the kernel's end."""
+
+import contextlib
+
+import pytest
+
+from speculative_decoding_verification_47_gb300 import binding as sb
+from tests.conftest import gpu_available
+from tests.test_gpu_attention import SENTINEL
+from tests.test_gpu_attention import Case as Attention
+from tests.test_gpu_attention import _lib  # noqa: F401  (the fixture builds the library)
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not gpu_available(), reason="needs a CUDA GPU")]
+
+
+@contextlib.contextmanager
+def no_patience():
+    sb.lib().sv_internal_wait_tries(0)
+    try:
+        yield
+        torch.cuda.synchronize()
+    finally:
+        sb.lib().sv_internal_wait_tries(-1)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,page", [(1, 16), (40, 16), (3, 7)])
+def test_attention(B, page, D):
+    c = Attention([300 + 3 * b for b in range(B)], [b % 3 for b in range(B)], 2, prefix=200, page=page, D=D)
+    c.run().check()  # parts of an earlier call lie in the workspace
+    c.out.fill_(SENTINEL)
+    c.lse.fill_(SENTINEL)
+    with no_patience():
+        c.run()
+    assert sb.sv_read_device_flags(c.ws) == sb.SV_FLAG_TIMEOUT
+    for b in range(B):
+        k = int(c.ks[b])
+        assert torch.isnan(c.out[b, :k + 1]).all() and torch.isnan(c.lse[b, :k + 1]).all()
+        assert (c.out[b, k + 1:] == SENTINEL).all() and (c.lse[b, k + 1:] == SENTINEL).all()
+    c.run().check()
