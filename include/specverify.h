@@ -478,6 +478,8 @@ sv_status sv_rmsnorm_residual(const void* x, int64_t ldx, const void* residual, 
  * x and W must be 16-byte aligned with row strides of a multiple of 16 bytes
  * (values between K and the stride are not used); the rest needs its
  * element's alignment.  out must not overlap x, W, bias or the scales.  Products and sums are float32, rounded once at the end.
+ * After a bounded wait that ran out (SV_FLAG_TIMEOUT) the outputs whose sums did
+ * not come are NaN.
  */
 size_t sv_linear_workspace_size(int M, int N, int K);
 sv_status sv_linear(const void* x, int64_t ldx, const float* x_scale, const void* W, int64_t ldw,

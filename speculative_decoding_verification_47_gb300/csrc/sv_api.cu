@@ -481,6 +481,7 @@ sv_status sv_linear(const void* x, int64_t ldx, const float* x_scale, const void
     return fail(SV_ERR_WORKSPACE, "workspace smaller than sv_linear_workspace_size()");
   L.flags = static_cast<uint32_t*>(workspace);
   L.stream = stream;
+  L.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
   std::string err;
   const int s = sv::linear_launch(L, &err);
   if (s != SV_OK) return fail(static_cast<sv_status>(s), err);

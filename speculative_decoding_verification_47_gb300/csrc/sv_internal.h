@@ -133,6 +133,7 @@ struct LinearLaunch {
   int M, N, K;
   uint32_t* flags;
   void* stream;
+  int wait_tries = kWaitTries;
 };
 
 // Enqueue the product with its epilogue.  Returns an sv_status; fills *err on failure.

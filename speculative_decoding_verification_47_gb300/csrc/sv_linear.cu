@@ -33,6 +33,7 @@ struct Epilogue {
   long long ldo;
   int act, out_f32, M, N;
   int vec;  // rows of out and residual start on 16-byte boundaries
+  uint32_t tries;  // of a wait for a sum
 };
 
 __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
@@ -100,6 +101,9 @@ __device__ __forceinline__ void finish(const Epilogue& e, long long m, int n, fl
 // nothing (2^-9); for a float32 one the accumulation is cut into kChunk k blocks
 // (128 instructions, about 2e-6) whose sums are added with rounding.
 constexpr int kChunk = 32;
+
+// What a sum becomes whose wait ran out; every epilogue keeps it.
+constexpr uint32_t kNan = 0x7fffffffu;
 
 constexpr int kRowBytes = 128;       // a k block of one row
 constexpr int kTile = 128 * kRowBytes;  // 128 rows of one k block
@@ -193,14 +197,16 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   }
   __syncwarp();
   // every thread: the accumulator is complete (so all loads have landed, too)
-  if (!mbar_wait_bounded(&done, 0)) failed = 1;
+  if (!mbar_wait_bounded(&done, 0, e.tries)) failed = 1;
   tc::fence_after();
   __syncthreads();
-  if (failed) {  // a wait ran out: let the copies already issued land
+  const bool lost = failed != 0;  // (the same in every thread)
+  if (lost) {  // a wait ran out: copies and products on their way end first, and the tile is NaN
     if (tid == 0) {
       atomicOr(flags, SV_FLAG_TIMEOUT);
       for (int g = consumed; g < issued; ++g)
         (void)mbar_wait_bounded(&full[g % S::kStages], (uint32_t)((g / S::kStages) & 1), 64);
+      (void)mbar_wait_bounded(&done, 0);
     }
     __syncthreads();
   }
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
         if (n < e.N) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (c + j < e.M) finish(e, c + j, n, __uint_as_float(v[j]), sw, bias, res[j]);
+            if (c + j < e.M) finish(e, c + j, n, __uint_as_float(lost ? kNan : v[j]), sw, bias, res[j]);
         }
       }
     }
@@ -239,7 +245,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
         tc::ld16(lanes + c, v);
         tc::ld_wait(v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * 128 + (warp & 3) * 32 + lane] = __uint_as_float(v[j]);
+        for (int j = 0; j < 16; ++j)
+          part[(c + j) * 128 + (warp & 3) * 32 + lane] = __uint_as_float(lost ? kNan : v[j]);
       }
     }
     tc::cluster_sync();
@@ -558,18 +565,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int lg = warp & 3, et = tid - 64, ch = (warp - 2) >> 2;
     float* stage = reinterpret_cast<float*>(smem + kPairRing) + (warp - 2) * 32 * kOutStride;
     int i = 0, turn = 0;
-    uint32_t limit = 2048;
+    bool lost = false;
     auto complete = [&](int b) {  // accumulator b, in its turn
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&accf[b], (uint32_t)((turn / NB) & 1), limit))) {
-        failed = 1;  // (and on, since the other warps meet at the barrier below, but without waiting again)
-        limit = 1;
+      // a wait that runs out: on, since the other warps meet at the barrier below, but
+      // with NaN and no further wait.  Nothing is released either, or a phase that this
+      // warp did not see could end early and the products overwrite what others read.
+      if (!lost && !__all_sync(0xffffffffu, mbar_wait_bounded(&accf[b], (uint32_t)((turn / NB) & 1), e.tries))) {
+        failed = 1;
+        lost = true;
       }
       tc::fence_after();
     };
     auto release = [&](int b) {
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) tc::arrive_remote(tc::cluster_addr(&acce[b], 0u));
+      if (lane == 0 && !lost) tc::arrive_remote(tc::cluster_addr(&acce[b], 0u));
       ++turn;
     };
     for (long long t = pid; t < tiles; t += npairs, ++i) {
@@ -623,7 +633,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int ms = 0; ms < MS; ++ms) {
         const long long row0 = m0 + ms * 256 + lg * 32, m = row0 + lane;
         const uint32_t at = tmem + (uint32_t)((b * MS + ms) * 256) + ((uint32_t)(lg * 32) << 16);
-        const float sx = e.sx && m < e.M ? e.sx[m] : 1.f;
+        const float sx = lost ? __uint_as_float(kNan) : (e.sx && m < e.M ? e.sx[m] : 1.f);
         if (row0 >= e.M) break;
         RowChunk<16> rc, next;  // the residual is asked for one chunk ahead
         auto whole = [&](int k) { return e.vec && n0 + k + 16 <= e.N; };  // (the same in the whole warp)
@@ -643,8 +653,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   if (tid == 0 && failed) {
     atomicOr(flags, SV_FLAG_TIMEOUT);
-    if (half == 0)  // let the copies already issued land before the pair exits
+    if (half == 0) {  // copies and products on their way end before the pair exits
       for (int g = consumed; g < issued; ++g) (void)mbar_wait_bounded(&full[g % kSt], (uint32_t)((g / kSt) & 1), 64);
+      if (consumed > 0)
+        (void)mbar_wait_bounded(&empty[(consumed - 1) % kSt], (uint32_t)(((consumed - 1) / kSt) & 1), 64);
+    }
   }
   tc::cluster_sync();  // no CTA leaves while its peer may still signal or read it
   tc::fence_after();
@@ -737,16 +750,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   }
   __syncwarp();
-  if (!mbar_wait_bounded(&done, 0)) failed = 1;
+  if (!mbar_wait_bounded(&done, 0, e.tries)) failed = 1;
   tc::fence_after();
   __syncthreads();
-  if (tid == 0 && failed) {
+  if (tid == 0 && failed) {  // a wait ran out: copies and products on their way end first
     atomicOr(flags, SV_FLAG_TIMEOUT);
-    if (half == 0)  // let the copies already issued land
+    if (half == 0)
       for (int g = consumed; g < issued; ++g) (void)mbar_wait_bounded(&full[g % kSt], (uint32_t)((g / kSt) & 1), 64);
+    (void)mbar_wait_bounded(&done, 0);
+    for (uint32_t r = 0; r < 2u * split; ++r)  // (a half of the tile may be missing: all of it is NaN)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(tc::cluster_addr(&failed, r)), "r"(1) : "memory");
   }
   tc::cluster_sync();  // (both halves' copies have landed: the ring may be written)
   tc::fence_after();
+  const bool lost = failed != 0;  // (the same in the whole cluster)
   float* sums = reinterpret_cast<float*>(smem);  // [128][kLd]
   if (warp >= 2) {
     const int lg = warp & 3, ch = (warp - 2) >> 2;
@@ -756,6 +773,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       uint32_t v[16];
       tc::ld16(tmem + ((uint32_t)(lg * 32) << 16) + k, v);
       tc::ld_wait(v);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) v[q] = lost ? kNan : v[q];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         *reinterpret_cast<uint4*>(row + k + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
@@ -1053,7 +1072,7 @@ int linear_launch(const LinearLaunch& L, std::string* err) {
   const bool vec = reinterpret_cast<uintptr_t>(L.out) % 16 == 0 && L.ldo * os % 16 == 0 &&
                    (!L.residual || (reinterpret_cast<uintptr_t>(L.residual) % 16 == 0 && L.ldr * os % 16 == 0));
   j.e = {L.x_scale, L.w_scale, static_cast<const uint16_t*>(L.bias), L.residual, L.ldr, L.out, L.ldo,
-         L.act, L.out_dtype == SV_F32 ? 1 : 0, L.M, L.N, vec ? 1 : 0};
+         L.act, L.out_dtype == SV_F32 ? 1 : 0, L.M, L.N, vec ? 1 : 0, (uint32_t)L.wait_tries};
   j.KB = (int)(((long long)L.K * es + lin::kRowBytes - 1) / lin::kRowBytes);
   j.st = static_cast<cudaStream_t>(L.stream);
   return L.in_dtype == SV_BF16 ? lin::dispatch<false>(j, err) : lin::dispatch<true>(j, err);

@@ -11,6 +11,7 @@ from tests.conftest import gpu_available
 from tests.test_gpu_attention import SENTINEL
 from tests.test_gpu_attention import Case as Attention
 from tests.test_gpu_attention import _lib  # noqa: F401  (the fixture builds the library)
+from tests.test_gpu_linear import Case as Linear
 
 torch = pytest.importorskip("torch")
 pytestmark = [pytest.mark.gpu,
@@ -42,3 +43,25 @@ def test_attention(B, page, D):
         assert torch.isnan(c.out[b, :k + 1]).all() and torch.isnan(c.lse[b, :k + 1]).all()
         assert (c.out[b, k + 1:] == SENTINEL).all() and (c.lse[b, k + 1:] == SENTINEL).all()
     c.run().check()
+
+
+# M, N, K, output: one CTA and a cluster per tile of few rows; clusters that share K; pairs with
+# one tile, with more tiles than accumulators, and with sums in chunks
+@pytest.mark.parametrize("act", [sb.SV_ACT_NONE, sb.SV_ACT_RELU, sb.SV_ACT_GELU])
+@pytest.mark.parametrize("M,N,K,out", [(3, 200, 64, "bf16"), (100, 30000, 64, "f32"), (7, 300, 4096, "bf16"),
+                                       (256, 500, 2048, "bf16"), (300, 1030, 128, "f32"), (2500, 5000, 264, "bf16"),
+                                       (300, 300, 4096, "f32")])
+def test_linear(M, N, K, out, act):
+    c = Linear(M, N, K, out=out, act=act, ldo=N + 3)
+    with no_patience():
+        c.run()
+    assert sb.sv_read_device_flags(c.ws) == sb.SV_FLAG_TIMEOUT
+    assert torch.isnan(c.o[:, :N]).all() and (c.o[:, N:] == 77.0).all()
+    c.ws.zero_()
+    c.run()
+    assert sb.sv_read_device_flags(c.ws) == 0
+    assert not torch.isnan(c.o).any()
+    got = c.o.clone()
+    c.o.fill_(0)
+    c.run()
+    assert torch.equal(got[:, :N], c.o[:, :N])
