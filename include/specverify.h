@@ -450,6 +450,8 @@ sv_status sv_prefix_attention(const void* q, int64_t q_seq_stride, int64_t q_pos
  *   M, H         each >= 1; row strides in elements, 0 selects H.
  * Pointers need only their element's alignment.  A row with a value that is
  * not finite gets NaN where its formula does (its whole e4m3 row and scale).
+ * The call has no flag word: rows from a bounded wait that ran out on are NaN
+ * in out and out_scale, and in residual_out where their sums are missing.
  */
 sv_status sv_rmsnorm_residual(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                               const void* norm_w, float eps, void* residual_out, int64_t ldro,

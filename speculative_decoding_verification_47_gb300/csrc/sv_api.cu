@@ -418,6 +418,7 @@ sv_status sv_rmsnorm_residual(const void* x, int64_t ldx, const void* residual, 
   L.M = M;
   L.H = H;
   L.stream = stream;
+  L.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
   if (L.ldx < H || L.ldr < H || L.ldro < H || L.ldo < H)
     return fail(SV_ERR_SHAPE, "row strides must be 0 or at least H");
   if ((residual_out == x && L.ldro != L.ldx) || (residual && residual_out == residual && L.ldro != L.ldr))

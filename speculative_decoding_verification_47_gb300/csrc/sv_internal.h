@@ -110,6 +110,7 @@ struct NormLaunch {
   float* out_scale;
   int M, H;
   void* stream;
+  int wait_tries = kWaitTries;
 };
 
 // Enqueue the residual RMSNorm.  Returns an sv_status; fills *err on failure.

@@ -40,6 +40,7 @@ struct Args {
   long long ldo;
   float* scale;
   int M, H;
+  uint32_t tries;  // of a wait for a row's copy
 };
 
 // max that keeps a NaN (fmaxf drops it)
@@ -348,11 +349,12 @@ __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) 
     for (int s = 0; s < slots && blockIdx.x + (long long)s * gridDim.x < a.M; ++s)
       ask(blockIdx.x + (long long)s * gridDim.x, s);
   const uint16_t* w = reinterpret_cast<const uint16_t*>(ring);
-  int slot = 0, turn = 0;
+  int slot = 0, turn = 0, late = 0x7fffffff;  // the turn whose copy did not come in time
   uint32_t phase = 0;
   for (long long m = blockIdx.x; m < a.M; m += gridDim.x, ++turn) {
-    // (a copy that never lands leaves the rows behind it unwritten)
-    if (!mbar_wait_bounded(&full[slot], phase)) return;
+    // A thread whose wait runs out waits no more, asks for no more and brings NaN into
+    // this row and every one behind it.
+    if (late > turn && !mbar_wait_bounded(&full[slot], phase, a.tries)) late = turn;
     const T* x = reinterpret_cast<const T*>(base + slot * slot_bytes);
     float s[NV][VEC], ss = 0.f, top = 0.f;
 #pragma unroll
@@ -375,8 +377,15 @@ __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) 
         }
       }
     }
+    if (late <= turn) {
+      ss = top = __int_as_float(0x7fffffff);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[j][i] = ss;
+    }
     reduce(part[turn & 1], ss, top);  // (every thread has read the slot)
-    if (t == 0 && m + (long long)slots * gridDim.x < a.M) ask(m + (long long)slots * gridDim.x, slot);
+    if (t == 0 && late > turn && m + (long long)slots * gridDim.x < a.M) ask(m + (long long)slots * gridDim.x, slot);
     if (++slot == slots) {
       slot = 0;
       phase ^= 1;
@@ -423,6 +432,9 @@ __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) 
       }
     }
   }
+  if (t == 0 && late < turn)  // (copies on their way end before the CTA does)
+    for (int g = late; g < late + slots && blockIdx.x + (long long)g * gridDim.x < a.M; ++g)
+      (void)mbar_wait_bounded(&full[g % slots], (uint32_t)((g / slots) & 1), 64);
 }
 
 // The ring's launch: CTAs of H / 16 threads, as many as an SM's threads and shared
@@ -507,7 +519,7 @@ static cudaError_t dispatch(const Args& a, int vec, cudaStream_t st) {
 
 int norm_launch(const NormLaunch& L, std::string* err) {
   norm::Args a = {L.x, L.ldx, L.residual, L.ldr, static_cast<const uint16_t*>(L.w), L.eps,
-                  L.residual_out, L.ldro, L.out, L.ldo, L.out_scale, L.M, L.H};
+                  L.residual_out, L.ldro, L.out, L.ldo, L.out_scale, L.M, L.H, (uint32_t)L.wait_tries};
   const size_t es = L.dtype == SV_BF16 ? 2 : 4, os = L.out_dtype == SV_BF16 ? 2 : 1;
   // the widest vector that every row of every array starts on a multiple of
   auto fits = [&](int v) {

@@ -65,3 +65,30 @@ def test_linear(M, N, K, out, act):
     c.o.fill_(0)
     c.run()
     assert torch.equal(got[:, :N], c.o[:, :N])
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("out", ["e4m3", "bf16"])
+def test_norm(out, inplace):
+    """Rows that come through the ring of copies; the sum in a place of its own and over the
+    residual, whose later rows are still on their way when the waits run out."""
+    M, H = 2500, 1032
+    x, r = (torch.randn(M, H, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        res = r.clone()
+        s = res if inplace else torch.zeros_like(r)
+        y = torch.zeros(M, H + 8, dtype=torch.uint8 if out == "e4m3" else torch.bfloat16, device="cuda")
+        c = torch.zeros(M, device="cuda") if out == "e4m3" else None
+        sb.sv_rmsnorm_residual(x, 0, res, 0, w, 1e-5, s, 0, sb.SV_BF16, y, H + 8,
+                               sb.SV_E4M3 if out == "e4m3" else sb.SV_BF16, c, M, H)
+        return (y.view(torch.float8_e4m3fn).float() if out == "e4m3" else y), c, s
+
+    with no_patience():
+        y, c, s = call()
+    assert torch.isnan(y[:, :H]).all() and torch.isnan(s).all() and (y[:, H:] == 0).all()
+    assert c is None or torch.isnan(c).all()
+    y, c, s = call()
+    assert torch.isfinite(y).all() and torch.equal(s, (x.float() + r.float()).to(torch.bfloat16))
+    assert c is None or torch.isfinite(c).all()
