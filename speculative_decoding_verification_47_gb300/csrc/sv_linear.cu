@@ -37,25 +37,23 @@ struct Epilogue {
 };
 
 __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
-// The upper tail of the normal distribution, 1/2 erfc(|z| / sqrt 2), by
-// approximation 7.1.28 of Abramowitz and Stegun's Handbook of Mathematical
-// Functions: erfc(x) = 1 / (1 + a1 x + .. + a6 x^6)^16, error at most 3e-7.  One
-// reciprocal and no exponential: a tile's epilogue is not hidden where a CTA has one
-// tile (512 x 16384 x 4096 e4m3: 50.8 us with erff, 39.0 with a form that has both).
+// z times the normal distribution's mass below z, by its upper tail
+//   1/2 erfc(a / sqrt 2) = exp(-a^2 / 2) t Q(t),  a = |z|, t = 1 / (1 + 0.3075914 a),
+// Q of degree 7, fitted here to the least relative error (reweighted least squares over
+// a = 0 .. 15.5: 1.3e-7).  A relative error, since a tail's error is one of the result
+// where z is negative: a form whose error is absolute (3e-7) is off by 0.4% at z = -4.
+// An infinite z has a tail of 0.
 __device__ __forceinline__ float gelu(float z) {
-  const float a = fabsf(z) * 0.70710678118654752f;
-  float p = __fmaf_rn(0.0000430638f, a, 0.0002765672f);
-  p = __fmaf_rn(p, a, 0.0001520143f);
-  p = __fmaf_rn(p, a, 0.0092705272f);
-  p = __fmaf_rn(p, a, 0.0422820123f);
-  p = __fmaf_rn(p, a, 0.0705230784f);
-  p = __fmaf_rn(p, a, 1.f);
-  p *= p;
-  p *= p;
-  p *= p;
-  p *= p;
-  const float tail = __fdividef(0.5f, p);  // (0 where the power is above 2^126)
-  return z > 0.f ? z - z * tail : z * tail;
+  const float t = __fdividef(1.f, __fmaf_rn(0.30759143f, fabsf(z), 1.f));
+  float p = __fmaf_rn(0.03628622f, t, -0.14713992f);
+  p = __fmaf_rn(p, t, 0.16964923f);
+  p = __fmaf_rn(p, t, -0.02564602f);
+  p = __fmaf_rn(p, t, 0.11512012f);
+  p = __fmaf_rn(p, t, 0.10576703f);
+  p = __fmaf_rn(p, t, 0.12327711f);
+  p = __fmaf_rn(p, t, 0.12268629f);
+  const float tail = p * t * ex2(z * z * -0.72134752f);  // (log2(e) / 2)
+  return z * (z > 0.f ? 1.f - tail : tail);
 }
 // z / 2 (1 + tanh u) = z / (1 + exp(-2u))
 __device__ __forceinline__ float gelu_tanh(float z) {
