@@ -143,6 +143,74 @@ __device__ __forceinline__ void reduce(float (&part)[2][32], float& sum, float& 
   }
 }
 
+// A mean of squares (and eps) whose squares left float32's range: values above 1.8e19, or
+// below 1e-18 with so small an eps.
+__device__ __forceinline__ bool far(float mean) { return mean < 0x1p-120f || mean == INFINITY; }
+
+// Such a row, by the threads that have it and from memory again: it is scaled by a power of
+// two p that brings the larger of its largest magnitude and sqrt(eps) next to 1, and
+//   y = w (p s) / sqrt(mean((p s)^2) + p^2 eps).
+// p is 1 where no scaling helps (a value that is not finite, nothing but zeros).  From
+// memory, so that the usual path's registers are not held for it.
+template <typename T, bool Q8>
+__device__ __forceinline__ void far_row(const Args& a, long long m, float (&part)[2][32]) {
+  const int t = threadIdx.x, n = blockDim.x;
+  const T* x = static_cast<const T*>(a.x) + m * a.ldx;
+  const T* res = a.res ? static_cast<const T*>(a.res) + m * a.ldr : nullptr;
+  float s[1], r[1], w[1], y[1], none = 0.f, big = 0.f, p = 1.f, ss = 0.f, top = 0.f, c = 1.f;
+  auto sum_at = [&](long long k) {
+    load<1>(x + k, s);
+    if (res) {
+      load<1>(res + k, r);
+      s[0] += r[0];
+    }
+    return s[0];
+  };
+  auto all = [&](float& sum, float& most) {
+    if (n > 32)
+      __syncthreads();  // (part[] is free, and what the row's other threads stored lies before it)
+    else
+      __syncwarp();
+    reduce(part, sum, most);
+  };
+#pragma unroll 1
+  for (long long k = t; k < a.H; k += n) big = max_nan(big, fabsf(sum_at(k)));
+  all(none, big);
+  const float ref = fmaxf(big, sqrtf(a.eps));
+  if (big < INFINITY && ref < INFINITY && ref > 0.f) {
+    const int e = (int)(__float_as_uint(ref) >> 23) - 127;
+    p = __uint_as_float((uint32_t)(127 - min(max(e, -126), 126)) << 23);
+  }
+#pragma unroll 1
+  for (long long k = t; k < a.H; k += n) {
+    const float v = sum_at(k) * p;
+    ss = __fmaf_rn(v, v, ss);
+  }
+  all(ss, none);
+  const float inv = rsqrtf(ss / (float)a.H + a.eps * p * p);
+  if (Q8) {
+  #pragma unroll 1
+  for (long long k = t; k < a.H; k += n) {
+      load<1>(a.w + k, w);
+      top = max_nan(top, fabsf(sum_at(k) * p * inv * w[0]));
+    }
+    all(none, top);
+    c = top / kE4M3Max;
+    if (c < kTiny) c = kTiny;  // (a NaN stays)
+    if (t == 0) a.scale[m] = c;
+  }
+#pragma unroll 1
+  for (long long k = t; k < a.H; k += n) {
+    load<1>(a.w + k, w);
+    y[0] = sum_at(k) * p * inv * w[0] / c;
+    if (a.sum) store<1>(static_cast<T*>(a.sum) + m * a.lds + k, s);
+    if (Q8)
+      store8<1>(static_cast<uint8_t*>(a.out) + m * a.ldo + k, y);
+    else
+      store<1>(static_cast<uint16_t*>(a.out) + m * a.ldo + k, y);
+  }
+}
+
 // One row per blockDim.x threads (blockDim.y rows per CTA only with one warp
 // per row).  Thread t holds elements (j * blockDim.x + t) * VEC .., j < NV;
 // rows longer than NV * VEC * blockDim.x are read again for the scaling, each
@@ -176,24 +244,40 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
       f[i] = one[0];
     }
   };
-  auto weight = [&](int k, float (&f)[VEC]) {
-    if constexpr (SHIFT && VEC > 1) {
-      if (whole(k)) {  // (words of two on 4 bytes, the elements between them)
-        const uint32_t* at = reinterpret_cast<const uint32_t*>(a.w + (k & ~1));
-        uint32_t h[VEC / 2 + 1];
+  // the weight's run from k on as words of two (one element: alone), and widened
+  constexpr int WW = VEC > 1 ? VEC / 2 : 1;
+  auto weight_words = [&](int k, uint32_t (&h)[WW]) {
+    if constexpr (VEC == 1) {
+      h[0] = a.w[k];
+    } else if constexpr (!SHIFT) {
+      const Words<WW> in = *reinterpret_cast<const Words<WW>*>(a.w + k);
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) h[i] = at[i];
-        h[VEC / 2] = k & 1 ? a.w[k + VEC - 1] : 0u;
+      for (int i = 0; i < WW; ++i) h[i] = in.v[i];
+    } else if (whole(k)) {  // (words on 4 bytes, the elements between them)
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(a.w + (k & ~1));
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) {
-          const uint32_t two = k & 1 ? __funnelshift_r(h[i], h[i + 1], 16) : h[i];
-          f[2 * i] = bf16_lo(two);
-          f[2 * i + 1] = bf16_hi(two);
-        }
-        return;
+      for (int i = 0; i < WW; ++i) h[i] = at[i];
+      if (k & 1) {
+        const uint32_t last = a.w[k + VEC - 1];
+#pragma unroll
+        for (int i = 0; i < WW; ++i) h[i] = __funnelshift_r(h[i], i + 1 < WW ? h[i + 1] : last, 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const uint32_t one = k + i >= 0 && k + i < a.H ? a.w[k + i] : 0u;
+        h[i / 2] = i & 1 ? h[i / 2] | one << 16 : one;
       }
     }
-    get(a.w, k, f);
+  };
+  auto widen = [&](const uint32_t (&h)[WW], float (&f)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = i & 1 ? bf16_hi(h[i / 2]) : bf16_lo(h[i / 2]);
+  };
+  auto weight = [&](int k, float (&f)[VEC]) {
+    uint32_t h[WW];
+    weight_words(k, h);
+    widen(h, f);
   };
   auto sum_at = [&](int k, float (&s)[VEC]) {
     get(x, k, s);
@@ -205,37 +289,83 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
     }
   };
   float s[NV][VEC], ss = 0.f, top = 0.f;
-  auto gather = [&](const float (&v)[VEC], int k) {
-    float w[VEC];
-    if (Q8) weight(k, w);
+  uint32_t held[VEC == 1 ? 1 : NV][WW];
+  if constexpr (VEC > 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int k = (j * n + t) * VEC - phase;
+      if (k < a.H) weight_words(k, held[j]);
+    }
+  }
+  auto gather = [&](const float (&v)[VEC], const float (&w)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       ss = __fmaf_rn(v[i], v[i], ss);
       if (Q8) top = max_nan(top, fabsf(v[i] * w[i]));
     }
   };
+  if constexpr (!SHIFT && VEC * sizeof(T) >= 4) {
+    // every load before the first sum waits for one
+    using Raw = Words<VEC * sizeof(T) / 4>;
+    Raw rx[NV], rr[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int k = (j * n + t) * VEC - phase;
-    if (k < a.H) {
-      sum_at(k, s[j]);
-    } else {
+    for (int j = 0; j < NV; ++j) {
+      const int k = (j * n + t) * VEC;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s[j][i] = 0.f;
+      for (int i = 0; i < (int)(sizeof(Raw) / 4); ++i) rx[j].v[i] = rr[j].v[i] = 0;
+      if (k < a.H) rx[j] = *reinterpret_cast<const Raw*>(x + k);
+    }
+    if (res) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int k = (j * n + t) * VEC;
+        if (k < a.H) rr[j] = *reinterpret_cast<const Raw*>(res + k);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        if constexpr (sizeof(T) == 4)
+          s[j][i] = __uint_as_float(rx[j].v[i]) + (res ? __uint_as_float(rr[j].v[i]) : 0.f);
+        else
+          s[j][i] = (i & 1 ? bf16_hi(rx[j].v[i / 2]) : bf16_lo(rx[j].v[i / 2])) +
+                    (res ? (i & 1 ? bf16_hi(rr[j].v[i / 2]) : bf16_lo(rr[j].v[i / 2])) : 0.f);
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int k = (j * n + t) * VEC - phase;
+      if (k < a.H) {
+        sum_at(k, s[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[j][i] = 0.f;
+      }
     }
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int k = (j * n + t) * VEC - phase;
-    if (k < a.H) gather(s[j], k);
+    if (k < a.H) {
+      float w[VEC];
+      if constexpr (VEC > 1)
+        widen(held[j], w);
+      else
+        weight(k, w);
+      gather(s[j], w);
+    }
   }
   for (long long k = (long long)(NV * n + t) * VEC; k < a.H; k += (long long)n * VEC) {
     float v[VEC];
     sum_at((int)k, v);
-    gather(v, (int)k);
+    float w[VEC];
+    weight((int)k, w);
+    gather(v, w);
   }
   reduce(part, ss, top);
-  float r = rsqrtf(ss / (float)a.H + a.eps);
+  const float mean = ss / (float)a.H + a.eps;
+  float r = rsqrtf(mean);
   // |w s| may leave float32's range where |w s r| does not (s far from 1 and w
   // with it): then the maximum is taken again, from the values themselves
   if (Q8 && !(top > 1e-30f && top < 1e30f)) {  // (the same in every thread of the row)
@@ -270,10 +400,10 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
     inv = 1.f / c;
     if (t == 0) a.scale[m] = c;
   }
-  T* sum = a.sum ? static_cast<T*>(a.sum) + m * a.lds : nullptr;
-  auto finish = [&](const float (&v)[VEC], int k) {
-    float w[VEC], y[VEC];
-    weight(k, w);
+  // (a row that is done again below: its sum may lie over x, which that reads)
+  T* sum = a.sum && !far(mean) ? static_cast<T*>(a.sum) + m * a.lds : nullptr;
+  auto finish = [&](const float (&v)[VEC], const float (&w)[VEC], int k) {
+    float y[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) y[i] = v[i] * r * w[i] * inv;
     if (whole(k)) {
@@ -298,13 +428,22 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int k = (j * n + t) * VEC - phase;
-    if (k < a.H) finish(s[j], k);
+    if (k < a.H) {
+      float w[VEC];
+      if constexpr (VEC > 1)
+        widen(held[j], w);
+      else
+        weight(k, w);
+      finish(s[j], w, k);
+    }
   }
   for (long long k = (long long)(NV * n + t) * VEC; k < a.H; k += (long long)n * VEC) {
-    float v[VEC];
+    float v[VEC], w[VEC];
     sum_at((int)k, v);
-    finish(v, (int)k);
+    weight((int)k, w);
+    finish(v, w, (int)k);
   }
+  if (far(mean)) far_row<T, Q8>(a, m, part);  // (the same in every thread of the row)
 }
 
 // ---------------------------------------------------------------------------
@@ -390,7 +529,7 @@ __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) 
       slot = 0;
       phase ^= 1;
     }
-    const float r = rsqrtf(ss / (float)a.H + a.eps);
+    const float mean = ss / (float)a.H + a.eps, r = rsqrtf(mean);
     if (Q8 && !(top > 1e-30f && top < 1e30f)) {  // as in norm_kernel
       top = 0.f;
 #pragma unroll
@@ -415,7 +554,7 @@ __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) 
       inv = 1.f / c;
       if (t == 0) a.scale[m] = c;
     }
-    T* sum = a.sum ? static_cast<T*>(a.sum) + m * a.lds : nullptr;
+    T* sum = a.sum && !far(mean) ? static_cast<T*>(a.sum) + m * a.lds : nullptr;  // (as in norm_kernel)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int k = (j * n + t) * VEC;
@@ -431,6 +570,7 @@ __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) 
           store<VEC>(static_cast<uint16_t*>(a.out) + m * a.ldo + k, y);
       }
     }
+    if (far(mean)) far_row<T, Q8>(a, m, part[2 + (turn & 1)]);
   }
   if (t == 0 && late < turn)  // (copies on their way end before the CTA does)
     for (int g = late; g < late + slots && blockIdx.x + (long long)g * gridDim.x < a.M; ++g)
