@@ -143,6 +143,42 @@ __device__ __forceinline__ void reduce(float (&part)[2][32], float& sum, float& 
   }
 }
 
+// y / c for all values of a row by its scale's reciprocal in two words: off by little more than
+// half a step, as a division is (with one word 4 of 10000 values next to a border of e4m3
+// went to the wrong side).
+struct Divisor {
+  float hi, lo;
+  __device__ __forceinline__ explicit Divisor(float c) : hi(1.f / c) {
+    lo = c < INFINITY ? __fmaf_rn(-hi, c, 1.f) * hi : 0.f;
+  }
+};
+
+// y = v r w, divided for an 8-bit result, then two values an instruction.
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <bool Q8, int VEC>
+__device__ __forceinline__ void results(const float (&v)[VEC], float r, const float (&w)[VEC], const Divisor& by,
+                                        float (&y)[VEC]) {
+  if constexpr (VEC == 1 || !Q8) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      y[i] = v[i] * r * w[i];
+      if (Q8) y[i] = __fmaf_rn(y[i], by.hi, y[i] * by.lo);
+    }
+  } else {
+    const F2 r2 = f2_pack(r, r), hi = f2_pack(by.hi, by.hi), lo = f2_pack(by.lo, by.lo);
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+      F2 t = f2_mul(f2_mul(f2_pack(v[i], v[i + 1]), r2), f2_pack(w[i], w[i + 1]));
+      t = f2_fma(t, hi, f2_mul(t, lo));
+      f2_unpack(t, y[i], y[i + 1]);
+    }
+  }
+}
+
 // A mean of squares (and eps) whose squares left float32's range: values above 1.8e19, or
 // below 1e-18 with so small an eps.
 __device__ __forceinline__ bool far(float mean) { return mean < 0x1p-120f || mean == INFINITY; }
@@ -189,8 +225,8 @@ __device__ __forceinline__ void far_row(const Args& a, long long m, float (&part
   all(ss, none);
   const float inv = rsqrtf(ss / (float)a.H + a.eps * p * p);
   if (Q8) {
-  #pragma unroll 1
-  for (long long k = t; k < a.H; k += n) {
+#pragma unroll 1
+    for (long long k = t; k < a.H; k += n) {
       load<1>(a.w + k, w);
       top = max_nan(top, fabsf(sum_at(k) * p * inv * w[0]));
     }
@@ -393,19 +429,15 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
     top *= r;
   }
   if (!live) return;
-  float inv = 1.f;
-  if (Q8) {
-    float c = top / kE4M3Max;
-    if (c < kTiny) c = kTiny;  // (a NaN stays)
-    inv = 1.f / c;
-    if (t == 0) a.scale[m] = c;
-  }
+  float c = top / kE4M3Max;
+  if (c < kTiny) c = kTiny;  // (a NaN stays)
+  if (Q8 && t == 0) a.scale[m] = c;
+  const Divisor by(c);
   // (a row that is done again below: its sum may lie over x, which that reads)
   T* sum = a.sum && !far(mean) ? static_cast<T*>(a.sum) + m * a.lds : nullptr;
   auto finish = [&](const float (&v)[VEC], const float (&w)[VEC], int k) {
     float y[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) y[i] = v[i] * r * w[i] * inv;
+    results<Q8>(v, r, w, by, y);
     if (whole(k)) {
       if (sum) store<VEC>(sum + k, v);
       if (Q8)
@@ -464,38 +496,45 @@ __device__ __forceinline__ void bulk(void* dst, const void* src, uint32_t bytes,
 template <typename T, bool Q8>
 __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) {
   constexpr int VEC = 8, NV = 2;
-  extern __shared__ __align__(16) uint8_t ring[];  // the weight, then the slots
+  extern __shared__ __align__(16) uint8_t ring[];  // the slots
   __shared__ float part[4][2][32];
   __shared__ __align__(8) uint64_t full[kRing];
   const int t = threadIdx.x, n = blockDim.x;
   const uint32_t row_bytes = (uint32_t)a.H * sizeof(T), slot_bytes = a.res ? 2 * row_bytes : row_bytes;
-  uint8_t* base = ring + (uint32_t)a.H * 2;
   pdl_launch_dependents();
   if (t == 0) {
     for (int s = 0; s < slots; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
   }
   pdl_wait();  // the launch may overlap the kernel that wrote x
-  for (int k = t * VEC; k < a.H; k += n * VEC)
-    *reinterpret_cast<uint4*>(ring + 2 * k) = *reinterpret_cast<const uint4*>(a.w + k);
   __syncthreads();
   auto ask = [&](long long m, int s) {  // (one thread)
     mbar_arrive_expect_tx(&full[s], slot_bytes);
-    bulk(base + s * slot_bytes, static_cast<const T*>(a.x) + m * a.ldx, row_bytes, &full[s]);
-    if (a.res) bulk(base + s * slot_bytes + row_bytes, static_cast<const T*>(a.res) + m * a.ldr, row_bytes, &full[s]);
+    bulk(ring + s * slot_bytes, static_cast<const T*>(a.x) + m * a.ldx, row_bytes, &full[s]);
+    if (a.res) bulk(ring + s * slot_bytes + row_bytes, static_cast<const T*>(a.res) + m * a.ldr, row_bytes, &full[s]);
   };
   if (t == 0)
     for (int s = 0; s < slots && blockIdx.x + (long long)s * gridDim.x < a.M; ++s)
       ask(blockIdx.x + (long long)s * gridDim.x, s);
-  const uint16_t* w = reinterpret_cast<const uint16_t*>(ring);
+  Words<VEC / 2> w[NV];  // a thread's columns are the same in every row
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int k = (j * n + t) * VEC;
+    if (k < a.H) w[j] = *reinterpret_cast<const Words<VEC / 2>*>(a.w + k);
+  }
+  auto weight = [&](int j, float (&f)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = i & 1 ? bf16_hi(w[j].v[i / 2]) : bf16_lo(w[j].v[i / 2]);
+  };
   int slot = 0, turn = 0, late = 0x7fffffff;  // the turn whose copy did not come in time
   uint32_t phase = 0;
   for (long long m = blockIdx.x; m < a.M; m += gridDim.x, ++turn) {
     // A thread whose wait runs out waits no more, asks for no more and brings NaN into
     // this row and every one behind it.
     if (late > turn && !mbar_wait_bounded(&full[slot], phase, a.tries)) late = turn;
-    const T* x = reinterpret_cast<const T*>(base + slot * slot_bytes);
+    const T* x = reinterpret_cast<const T*>(ring + slot * slot_bytes);
     float s[NV][VEC], ss = 0.f, top = 0.f;
+    F2 squares = f2_pack(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int k = (j * n + t) * VEC;
@@ -508,14 +547,22 @@ __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) 
           for (int i = 0; i < VEC; ++i) s[j][i] += r[i];
         }
         float v[VEC];
-        if (Q8) load<VEC>(w + k, v);
+        if (Q8) weight(j, v);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          ss = __fmaf_rn(s[j][i], s[j][i], ss);
-          if (Q8) top = max_nan(top, fabsf(s[j][i] * v[i]));
+        for (int i = 0; i < VEC; i += 2) {
+          const F2 two = f2_pack(s[j][i], s[j][i + 1]);
+          squares = f2_fma(two, two, squares);
+          if (Q8) {
+            float p0, p1;
+            f2_unpack(f2_mul(two, f2_pack(v[i], v[i + 1])), p0, p1);
+            top = max_nan(top, max_nan(fabsf(p0), fabsf(p1)));
+          }
         }
       }
     }
+    float even, odd;
+    f2_unpack(squares, even, odd);
+    ss = even + odd;
     if (late <= turn) {
       ss = top = __int_as_float(0x7fffffff);
 #pragma unroll
@@ -537,7 +584,7 @@ __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) 
         const int k = (j * n + t) * VEC;
         if (k < a.H) {
           float v[VEC];
-          load<VEC>(w + k, v);
+          weight(j, v);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) top = max_nan(top, fabsf(s[j][i] * r * v[i]));
         }
@@ -547,22 +594,18 @@ __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) 
     } else {
       top *= r;
     }
-    float inv = 1.f;
-    if (Q8) {
-      float c = top / kE4M3Max;
-      if (c < kTiny) c = kTiny;  // (a NaN stays)
-      inv = 1.f / c;
-      if (t == 0) a.scale[m] = c;
-    }
+    float c = top / kE4M3Max;
+    if (c < kTiny) c = kTiny;  // (a NaN stays)
+    if (Q8 && t == 0) a.scale[m] = c;
+    const Divisor by(c);
     T* sum = a.sum && !far(mean) ? static_cast<T*>(a.sum) + m * a.lds : nullptr;  // (as in norm_kernel)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int k = (j * n + t) * VEC;
       if (k < a.H) {
         float v[VEC], y[VEC];
-        load<VEC>(w + k, v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) y[i] = s[j][i] * r * v[i] * inv;
+        weight(j, v);
+        results<Q8>(s[j], r, v, by, y);
         if (sum) store<VEC>(sum + k, s[j]);
         if (Q8)
           store8<VEC>(static_cast<uint8_t*>(a.out) + m * a.ldo + k, y);
@@ -580,15 +623,15 @@ __global__ void __launch_bounds__(1024, 1) ring_kernel(const Args a, int slots) 
 // The ring's launch: CTAs of H / 16 threads, as many as an SM's threads and shared
 // memory hold with `slots` rows each.  `ctas` = 0 if a row does not fit.
 static void ring_shape(const Args& a, int es, int threads, int* slots, int* ctas, int* smem) {
-  const int slot = a.H * es * (a.res ? 2 : 1), w = a.H * 2, room = 200 * 1024;
+  const int slot = a.H * es * (a.res ? 2 : 1), room = 200 * 1024;
   int per_sm = 1024 / threads;  // (64 registers a thread)
   if (per_sm > 8) per_sm = 8;
   *ctas = 0;
   for (; per_sm >= 1; --per_sm) {
-    const int fits = (room / per_sm - w - 2048) / slot;
+    const int fits = (room / per_sm - a.H * 2 - 2048) / slot;
     if (fits < 2) continue;
     *slots = fits < kRing ? fits : kRing;
-    *smem = w + *slots * slot;
+    *smem = *slots * slot;
     *ctas = per_sm;
     return;
   }

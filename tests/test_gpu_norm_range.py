@@ -6,6 +6,7 @@ power of two is exact)."""
 import numpy as np
 import pytest
 
+from speculative_decoding_verification_47_gb300 import binding as sb
 from tests.conftest import gpu_available
 from tests.test_gpu_norm import DT, _lib, check, run  # noqa: F401  (the fixture builds the library)
 
@@ -73,3 +74,42 @@ def test_zeros_and_values_that_are_not_finite_among_them():
     assert (y[~bad].float() == 1).all()
     y, c, _ = run(x[1:2], None, w, "e4m3", eps=1e-30)
     assert (y.float() == 0).all() and c.item() == 2.0 ** -126
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,H", SHAPES)
+def test_sums_over_the_residual(M, H, dtype):
+    """A row that is done again still has its inputs."""
+    g = torch.Generator(device="cuda").manual_seed(H + 1)
+    x, r = rows(M, H, dtype, g) * 0.25, rows(M, H, dtype, g) * 0.25
+    w = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(torch.bfloat16)
+    y, c, s = run(x, r, w, "e4m3", eps=0.0)
+    for over in (x.clone(), r.clone()):
+        first = torch.equal(over, x)
+        y2, c2 = torch.zeros(M, H, dtype=torch.uint8, device="cuda"), torch.zeros(M, device="cuda")
+        sb.sv_rmsnorm_residual(over if first else x, 0, r if first else over, 0, w, 0.0, over, 0, DT[dtype][1], y2, 0,
+                               sb.SV_E4M3, c2, M, H)
+        assert torch.equal(over, s) and torch.equal(y2, y.view(torch.uint8))
+        assert torch.equal(c2.isnan(), c.isnan()) and torch.equal(c2.nan_to_num(), c.nan_to_num())  # (0 / 0)
+
+
+@pytest.mark.parametrize("M,H", [(1, 512), (1, 1500), (1, 1501), (1, 20001), (2500, 1504)])
+def test_quotients_next_to_a_border(M, H):
+    """Rows of ones (their mean square is 1): y is the weight, so each 8-bit value is that of the
+    weight divided by the scale.  All bf16 values over nine powers of two below each of 128
+    largest ones: the quotients that lie between two e4m3 values are among them."""
+    x = torch.ones(M, H, device="cuda").to(torch.bfloat16)
+    steps = np.arange(1, 256, dtype=np.float32)
+    for top in range(128, 256):
+        v = np.unique(np.concatenate([steps * np.float32(2.0 ** -k) for k in range(9)]))
+        v = np.concatenate([[top], v[v <= top]]).astype(np.float32)
+        for at in range(0, len(v), H - 1):
+            w = np.zeros(H, np.float32)
+            w[0] = top
+            n = len(v[at:at + H - 1])
+            w[1:1 + n] = v[at:at + H - 1] * np.where(np.arange(n) % 2, 1, -1)
+            y, c, _ = run(x, None, torch.from_numpy(w).cuda().to(torch.bfloat16), "e4m3", eps=0.0)
+            scale = np.float32(top) / np.float32(448)  # (IEEE divisions: a GPU tensor over a number is a product)
+            assert (c.cpu().numpy() == scale).all()
+            want = torch.from_numpy(w / scale).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+            assert torch.equal(y.view(torch.uint8), want.expand(M, H))
