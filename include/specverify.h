@@ -407,8 +407,9 @@ sv_status sv_lmhead_rmsnorm(const void* hidden, const void* norm_w, float eps, c
  *                four bytes are the device flag word (cleared by the call).
  *                Calls that share a workspace must be ordered on one stream.
  * q, k_pool, v_pool and out must be 16-byte aligned and their strides
- * multiples of 8 elements; out and lse must not overlap an input.  Products and the softmax's sums are float32; the
- * unnormalised weights are rounded to bf16 for the product with v.
+ * multiples of 8 elements, the other arrays aligned to their elements; out and
+ * lse must not overlap an input.  Products and the softmax's sums are float32;
+ * the unnormalised weights are rounded to bf16 for the product with v.
  * Values past a sequence's end (the rest of a page, pages that are not its
  * own) are never used, whatever they hold; a value of v at a draft position
  * that is not finite makes the queries that see it not finite and no other.

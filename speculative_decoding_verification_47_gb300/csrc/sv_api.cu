@@ -340,7 +340,9 @@ sv_status sv_prefix_attention(const void* q, int64_t q_seq_stride, int64_t q_pos
   if (!(scale - scale == 0.0f)) return fail(SV_ERR_ARG, "scale must be finite");
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
     return fail(SV_ERR_ARG, "q, k_pool, v_pool and out must be 16-byte aligned");
-  if (!aligned(lse, 4)) return fail(SV_ERR_ARG, "lse must be aligned to its element size");
+  if (!aligned(lse, 4) || !aligned(prefix_pages, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(k_per_row, 4))
+    return fail(SV_ERR_ARG, "lse and the index arrays must be aligned to their element size");
   sv::AttentionLaunch L;
   L.q = q;
   L.q_head = q_head_stride ? q_head_stride : D;

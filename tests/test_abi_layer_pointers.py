@@ -1,0 +1,12 @@
+"""Misaligned index arrays are refused on the host: on the device they would be a fault."""
+
+import pytest
+
+from speculative_decoding_verification_47_gb300 import binding as sb
+from tests.test_abi_layer import ATTN, P, lib, refused  # noqa: F401  (the fixture builds the library)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("name", ["prefix_pages", "block_table", "seq_lens", "k_per_row"])
+def test_prefix_attention_index_arrays(name, off):
+    refused(sb.sv_prefix_attention, ATTN, {name: P + off}, sb.SV_ERR_ARG)
