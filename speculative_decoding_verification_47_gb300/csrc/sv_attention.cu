@@ -1003,10 +1003,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
       const int bad = p.stat[b];
       if (!(bad & (SV_FLAG_BAD_K | SV_FLAG_BAD_N))) continue;
       const int n = bad & SV_FLAG_BAD_K ? p.Q : (a.kpr ? a.kpr[b] : a.K) + 1;
-      for (int e = threadIdx.x; e < n * a.Hq * D; e += kMergeThreads) {
-        const int i = e / (a.Hq * D), h = e / D % a.Hq;
-        static_cast<uint16_t*>(a.out)[b * a.o_seq + i * a.o_pos + h * a.o_head + e % D] = 0x7fff;
-        if (a.lse && e % D == 0) a.lse[(b * p.Q + i) * a.Hq + h] = nan;
+      const long long heads = (long long)n * a.Hq;  // (times D: past 2^31)
+      for (long long e = threadIdx.x; e < heads * D; e += kMergeThreads) {
+        const int row = (int)(e / D), d = (int)(e % D), i = row / a.Hq, h = row - i * a.Hq;
+        static_cast<uint16_t*>(a.out)[b * a.o_seq + i * a.o_pos + h * a.o_head + d] = 0x7fff;
+        if (a.lse && d == 0) a.lse[(b * p.Q + i) * a.Hq + h] = nan;
       }
     }
   }
