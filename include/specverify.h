@@ -227,7 +227,9 @@ sv_status sv_spec_verify_noalloc(const void* target_logits, int64_t target_seq_s
  * length [SSD §3.3, §4.3; SD §4.3].  seq_lens[b] holds the length at the start
  * of the round (the drafts were written at seq_lens[b] .. seq_lens[b]+k_b-1);
  * afterwards it is seq_lens[b] + n_accepted[b], and cache entries at or past
- * it are stale.  The resampled / bonus token's KV is written next round.
+ * it are stale.  The resampled / bonus token's KV is written next round (at the
+ * new length, which that round then counts as committed: see
+ * sv_prefix_attention).
  *   seq_lens    device int32 [B], read and written.
  *   n_accepted  device int32 [B] (e.g. from sv_spec_verify).
  *   capacity    device int32 [B] or NULL: a row whose new length would exceed
@@ -382,7 +384,13 @@ sv_status sv_lmhead_rmsnorm(const void* hidden, const void* norm_w, float eps, c
  *     out[b][i][h][:] = sum_j exp(s_j) v_j / sum_j exp(s_j),
  *     lse[b][i][h] = log sum_j exp(s_j).
  *   A query that sees no token (or none whose score is above -inf) gets out = 0
- *   and lse = -inf.  Nothing is written for positions i > k_b.  K = 0 is the single-token decode step.
+ *   and lse = -inf.  Nothing is written for positions i > k_b.  K = 0 is the
+ *   single-token decode step.
+ *   So position 0 sees its own token's key if L counts that token.  After a
+ *   commit it does not yet: seq_lens is L + n, and the token that the verify
+ *   step emitted has no key or value.  The round that follows computes them (it
+ *   is that round's position 0), writes them at seq_lens[b], and passes
+ *   seq_lens[b] + 1 to this call and to its own commit, with its drafts behind.
  *
  *   q            device bf16, element (b,i,h,d) at b*q_seq_stride +
  *                i*q_pos_stride + h*q_head_stride + d; strides in elements,

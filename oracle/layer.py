@@ -7,11 +7,14 @@ float64 (already widened from their storage type); it shares no code with the
 CUDA path.
 
 Readings:
-  R31 the query at position i of sequence b is that of the token before draft
+  R32 the query at position i of sequence b is that of the token before draft
       i, so it sees the prefix and the own tokens 0 .. L_b + i - 1, where the
-      drafts were written at L_b .. L_b + k_b - 1 (the convention of R29).  A
-      query that sees nothing gets 0 and a log-sum of -inf.
-  R32 an 8-bit row is e4m3 (4 exponent and 3 mantissa bits, largest value 448)
+      drafts were written at L_b .. L_b + k_b - 1 (the convention of R29).  For
+      position 0 to see itself L_b counts its token: a round that follows a
+      commit writes the emitted token's keys and values at the committed length
+      and passes that length plus one.  A query that sees nothing gets 0 and a
+      log-sum of -inf.
+  R33 an 8-bit row is e4m3 (4 exponent and 3 mantissa bits, largest value 448)
       with the scale max(max|y| / 448, 2^-126), so that dividing by it stays
       finite; a zero row has zero values.
 """
