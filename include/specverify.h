@@ -402,7 +402,7 @@ sv_status sv_lmhead_rmsnorm(const void* hidden, const void* norm_w, float eps, c
  *                NULL if prefix_len is 0.
  *   block_table  device int32 [B][max_pages]: each sequence's own pages.
  *   seq_lens     device int32 [B]; k_per_row device int32 [B] or NULL (= K).
- *   scale        finite.
+ *   scale        at most 2^127 in magnitude.
  *   out          device bf16, strides as q's, 0 selects packed [B][K+1][Hq][D].
  *   lse          device float32 [B][K+1][Hq], or NULL.
  *   dtype        SV_BF16.

@@ -337,7 +337,8 @@ sv_status sv_prefix_attention(const void* q, int64_t q_seq_stride, int64_t q_pos
   if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !out)
     return fail(SV_ERR_ARG, "q, k_pool, v_pool, block_table, seq_lens and out are required");
   if (prefix_len > 0 && !prefix_pages) return fail(SV_ERR_ARG, "prefix_pages is required when prefix_len > 0");
-  if (!(scale - scale == 0.0f)) return fail(SV_ERR_ARG, "scale must be finite");
+  // (its product with log2(e) is what the kernel uses)
+  if (!(scale >= -0x1p127f && scale <= 0x1p127f)) return fail(SV_ERR_ARG, "scale must be within +-2^127");
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
     return fail(SV_ERR_ARG, "q, k_pool, v_pool and out must be 16-byte aligned");
   if (!aligned(lse, 4) || !aligned(prefix_pages, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||

@@ -1,4 +1,5 @@
-"""Misaligned index arrays are refused on the host: on the device they would be a fault."""
+"""Calls that the host refuses because the device could not answer them: misaligned index
+arrays, which would be a fault there, and scales whose product with log2(e) is infinite."""
 
 import pytest
 
@@ -10,3 +11,8 @@ from tests.test_abi_layer import ATTN, P, lib, refused  # noqa: F401  (the fixtu
 @pytest.mark.parametrize("name", ["prefix_pages", "block_table", "seq_lens", "k_per_row"])
 def test_prefix_attention_index_arrays(name, off):
     refused(sb.sv_prefix_attention, ATTN, {name: P + off}, sb.SV_ERR_ARG)
+
+
+@pytest.mark.parametrize("scale", [2.5e38, -2.5e38, 3.4e38])
+def test_prefix_attention_scales(scale):
+    refused(sb.sv_prefix_attention, ATTN, dict(scale=scale), sb.SV_ERR_ARG)
