@@ -10,9 +10,12 @@
 // between that pass and the scaling: x and residual are read once.  s is
 // rounded only where it is stored; y comes from the unrounded sum.
 //
-// Bound by memory.  Few rows, short ones and unaligned ones: a CTA (or a warp) per
-// row.  More rows than fit the card at once: CTAs that stay, with the next rows on
-// their way into shared memory by bulk copies while one is reduced and stored.
+// Bound by memory.  A CTA (or a warp) per row, all of its loads before the first sum; long rows,
+// more of them than fit the card at once: CTAs that stay, with the next rows on their way into
+// shared memory by bulk copies while one is reduced and stored.  Measured with inputs outside of
+// L2: 16384 x 8192 float32 to bf16 264 us (7.1 TB/s), bf16 with a residual to e4m3 162 us
+// (5.8 TB/s), 2304 x 4096 13.0 us (four rows a CTA: the first copies and the rows' chains of
+// reduction and stores, 63% of the issue slots), one row 1.8 us (latencies).
 #include <atomic>
 #include <cstdint>
 
@@ -481,8 +484,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
 // ---------------------------------------------------------------------------
 // Rows of 16-byte words through a ring of shared memory: `slots` rows of x and
 // residual ahead.  Thread t holds elements (j * blockDim.x + t) * 8 .., j < 2.
-// 16384 x 8192 bf16 with an 8-bit output: 245 us with a CTA per row (57% of the
-// measured bandwidth: a CTA's loads, reduction and stores follow one another).
+// 2304 x 12288 bf16 with a residual to e4m3: 32 us, 46 with a CTA per row, whose loads,
+// reduction and stores follow one another.
 // ---------------------------------------------------------------------------
 constexpr int kRing = 8;  // slots at most
 
@@ -628,6 +631,7 @@ static void ring_shape(const Args& a, int es, int threads, int* slots, int* ctas
   if (per_sm > 8) per_sm = 8;
   *ctas = 0;
   for (; per_sm >= 1; --per_sm) {
+    // (less 2 H: a third slot at H = 4096 and 8192 gains nothing, 16384 x 8192 168 us, 161 with two)
     const int fits = (room / per_sm - a.H * 2 - 2048) / slot;
     if (fits < 2) continue;
     *slots = fits < kRing ? fits : kRing;
@@ -679,15 +683,19 @@ static cudaError_t launch(const Args& a, int threads, int rows, cudaStream_t st)
 template <typename T, bool Q8>
 static cudaError_t dispatch(const Args& a, int vec, cudaStream_t st) {
   constexpr int kPer = 16;  // elements a thread keeps
-  int threads = 32;  // (not only powers of two: 2048 x 4097 34.4 us with 512 threads, 26.7 with 288)
+  int threads = 32;  // (not only powers of two: 2048 x 4097 29.6 us with 512 threads, 25.3 with 288)
   const int spread = a.H + (vec == kShifted ? 7 : 0);
   while (threads < 1024 && (long long)threads * kPer < spread) threads += 32;
   const int rows = threads == 32 ? 4 : 1;
-  // More rows than the card holds CTAs of the plain kernel at once (1024 threads an
-  // SM), and rows in whole 16-byte words.  Not for float32 rows: twice the bytes are in
-  // flight anyway, and half as many rows fit the ring (16384 x 8192: 263 us by the
-  // plain kernel, 317 us by the ring; bf16 with an 8-bit output 245 and 148).
-  if (sizeof(T) == 2 && vec == 8 && threads > 32 && a.H <= kPer * threads && a.M > 152LL * (1024 / threads)) {
+  // The ring: rows in whole 16-byte words, more of them than the card holds CTAs of the plain
+  // kernel at once (1024 threads an SM), and long ones.  Inputs outside of L2, ring and plain,
+  // us: with a residual to e4m3 2304 x 4096 13.0 and 14.1, 4096 x 6144 30 and 37, 2304 x 12288
+  // 32 and 46, but 16384 x 2048 42 and 38, 5000 x 1024 11.3 and 8.3; to bf16 4096 x 6144 36 and
+  // 37, 16384 x 4096 89 and 78; without a residual 16384 x 2048 28 and 30, 16384 x 8192 101 and
+  // 130, 5000 x 1024 9.0 and 7.6.  Not for float32 rows: twice the bytes are in flight anyway,
+  // and half as many rows fit the ring (16384 x 8192: 263 by the plain kernel, 317 by the ring).
+  const int ring_from = a.res ? (Q8 ? 4096 : 4097) : 2048;
+  if (sizeof(T) == 2 && vec == 8 && a.H >= ring_from && a.H <= kPer * threads && a.M > 152LL * (1024 / threads)) {
     int slots = 0, ctas = 0, smem = 0;
     ring_shape(a, sizeof(T), threads, &slots, &ctas, &smem);
     if (sizeof(T) == 2 && ctas > 0) return launch_ring<uint16_t, Q8>(a, threads, slots, ctas, smem, st);
@@ -714,8 +722,8 @@ int norm_launch(const NormLaunch& L, std::string* err) {
            (!L.residual_out || on(L.residual_out, L.ldro, es)) && on(L.w, 0, 2) && on(L.out, L.ldo, os);
   };
   // Odd rows: runs of 8 at a phase that a row's arrays share.  2048 x 4097 bf16 to e4m3
-  // 26.7 us element by element, 25.3 in runs; 1 x 5001 4.5 and 3.3; but 12000 x 33 (a
-  // warp per row, most of its runs cut) 9.5 and 10.8.
+  // 28.7 us element by element, 25.3 in runs; 1 x 5001 4.9 and 3.1; but 12000 x 33 (a
+  // warp per row, most of its runs cut) 9.3 and 10.2.
   auto shares = [&](const void* p, long long ld, size_t e) {
     return reinterpret_cast<uintptr_t>(p) % (e == 1 ? 8 : 16) == 0 && (L.M == 1 || (ld - L.ldx) % 8 == 0);
   };

@@ -16,7 +16,7 @@ pytestmark = [pytest.mark.gpu,
 
 # a warp's rows, a CTA's rows, odd ones in aligned runs and one by one, rows that are read
 # again, and (with enough rows) the ring of copies
-SHAPES = [(9, 64), (9, 510), (9, 1024), (9, 1001), (9, 16379), (9, 40002), (2500, 1032)]
+SHAPES = [(9, 64), (9, 510), (9, 1024), (9, 1001), (9, 16379), (9, 40002), (2500, 1032), (700, 4104)]
 SIZES = [1e30, 3e38, 1e20, 1.0, 1e-15, 1e-20, 1e-25, 1e-37, 1e-40]
 
 
@@ -93,7 +93,7 @@ def test_sums_over_the_residual(M, H, dtype):
         assert torch.equal(c2.isnan(), c.isnan()) and torch.equal(c2.nan_to_num(), c.nan_to_num())  # (0 / 0)
 
 
-@pytest.mark.parametrize("M,H", [(1, 512), (1, 1500), (1, 1501), (1, 20001), (2500, 1504)])
+@pytest.mark.parametrize("M,H", [(1, 512), (1, 1500), (1, 1501), (1, 20001), (2500, 1504), (700, 4104)])
 def test_quotients_next_to_a_border(M, H):
     """Rows of ones (their mean square is 1): y is the weight, so each 8-bit value is that of the
     weight divided by the scale.  All bf16 values over nine powers of two below each of 128
