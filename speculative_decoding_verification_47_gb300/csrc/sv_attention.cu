@@ -23,7 +23,7 @@
 //  3. merge_kernel: the parts of each row, in a fixed order, to out and lse.
 //
 // Measured with 32 query and 8 key heads of 128.  256 sequences with 2 to 8 drafts and
-// 128 to 4096 own tokens behind a prefix of 16384: 667 us; their own tokens alone 405 us
+// 128 to 4096 own tokens behind a prefix of 16384: about 660 us; their own tokens alone 405 us
 // (bound by HBM, 5.4 TB/s), the prefix alone 432 us (a stream's softmax and its products
 // alternate).  64 sequences x 8 behind 2048 tokens, 100 to 511 own ones: 60 us, one token
 // behind 256 and 100: 15 us (bound by latencies: the plan 3 us, the first item's Q and

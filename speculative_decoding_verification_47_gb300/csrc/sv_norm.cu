@@ -147,8 +147,8 @@ __device__ __forceinline__ void reduce(float (&part)[2][32], float& sum, float& 
 }
 
 // y / c for all values of a row by its scale's reciprocal in two words: off by little more than
-// half a step, as a division is (with one word 4 of 10000 values next to a border of e4m3
-// went to the wrong side).
+// half a step, as a division is.  (With one word 73 of 155584 quotients of bf16 values went to
+// the other side of a border between two e4m3 values.)
 struct Divisor {
   float hi, lo;
   __device__ __forceinline__ explicit Divisor(float c) : hi(1.f / c) {
