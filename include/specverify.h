@@ -362,7 +362,8 @@ size_t sv_lmhead_workspace_size(int M, int H);
  *   logits   device [M][V], out_dtype SV_BF16 or SV_F32.
  *   M, H, V  M >= 1; H % 64 == 0; V % 16 == 0 (tcgen05 tile and TMA rules).
  *   workspace   >= sv_lmhead_workspace_size(M, H) bytes, 256-byte aligned.
- * bf16 products, fp32 accumulation on the tensor cores.
+ * bf16 products, fp32 accumulation on the tensor cores.  After a bounded wait that
+ * ran out (SV_FLAG_TIMEOUT) the logits that were not finished are not written.
  */
 sv_status sv_lmhead_rmsnorm(const void* hidden, const void* norm_w, float eps, const void* W,
                             void* logits, sv_dtype out_dtype, int M, int H, int V,

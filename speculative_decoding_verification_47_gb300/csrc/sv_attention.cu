@@ -44,7 +44,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 // Workspace header (32-bit words); word 0 is the flag word.
-enum { H_FLAGS, H_BAD_PREFIX, H_NEXT_PRE, H_NEXT_OWN, H_QUERIES, H_CHUNKS, H_CHUNK_KEYS, H_SPLITS, H_SPLIT_TILES,
+enum { H_FLAGS, H_ALL_FAIL, H_NEXT_PRE, H_NEXT_OWN, H_QUERIES, H_CHUNKS, H_CHUNK_KEYS, H_SPLITS, H_SPLIT_TILES,
        H_PRE_ITEMS, H_OWN_ITEMS, H_PRE_CTAS, H_WORDS = 64 };
 
 struct Layout {  // byte offsets into the workspace
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args p) {
     }
     if (t == 0) {
       p.head[H_PRE_CTAS] = ctas;
-      p.head[H_BAD_PREFIX] = 0;
+      p.head[H_ALL_FAIL] = 0;
       p.head[H_NEXT_PRE] = ctas;  // (these many CTAs take the first ones by themselves)
       p.head[H_NEXT_OWN] = p.grid - ctas;
       p.head[H_QUERIES] = queries;
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int id = it.kind == 0 ? a.prefix_pages[pg] : a.table[(long long)it.b * a.max_pages + pg];
             if ((unsigned)id < (unsigned)a.num_pages) return id;
             if (it.kind == 0)
-              p.head[H_BAD_PREFIX] = 1;
+              p.head[H_ALL_FAIL] = 1;
             else
               atomicOr(&p.stat[it.b], SV_FLAG_BAD_PAGE);
             atomicOr(&p.head[H_FLAGS], SV_FLAG_BAD_PAGE);
@@ -968,7 +968,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (looks > 0) (void)tc::wait_bounded(&raw[slot], (uint32_t)((looks - 1) & 1));
       if (use > 0) (void)tc::wait_bounded(&full[slot], (uint32_t)((use - 1) & 1));
     }
-    if (tid == 0) atomicOr(&p.head[H_FLAGS], SV_FLAG_TIMEOUT);
+    if (tid == 0) {  // parts are missing, and which ones is not known
+      p.head[H_ALL_FAIL] = 1;
+      atomicOr(&p.head[H_FLAGS], SV_FLAG_TIMEOUT);
+    }
     __syncthreads();
   }
   if (warp == 8) tc::dealloc<1>(tmem, 512);
@@ -996,8 +999,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
   const int queries = p.head[H_QUERIES], group = (int)(wid % kGroups);
   const unsigned rows = (unsigned)queries * p.G, id = wid / kGroups * 8 + (lane >> 2);
 
-  const uint32_t flags = p.head[H_FLAGS];
-  if (flags & (SV_FLAG_BAD_K | SV_FLAG_BAD_N)) {
+  if (p.head[H_FLAGS] & (SV_FLAG_BAD_K | SV_FLAG_BAD_N)) {
     // sequences that have no rows: every position that the caller reads is NaN
     for (long long b = blockIdx.x; b < a.B; b += gridDim.x) {
       const int bad = p.stat[b];
@@ -1019,8 +1021,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args p) {
   const int bi = of.x, k = of.y, len = of.z, first = of.w;
   const int b = bi / p.Q, i = bi - b * p.Q, hq = h * p.G + g;
   const int splits = p.head[H_SPLITS], per = p.head[H_SPLIT_TILES], keys = p.head[H_CHUNK_KEYS];
-  // (a wait that ran out leaves parts unwritten: which ones is not known)
-  const bool dead = p.stat[b] || p.head[H_BAD_PREFIX] || (flags & SV_FLAG_TIMEOUT);
+  const bool dead = p.stat[b] || p.head[H_ALL_FAIL];
   const bool lost = len + i > p.nan_from[(long long)b * a.Hkv + h];
 
   // The row's parts: of the prefix, `extra` ones of second streams there (the last split
