@@ -84,7 +84,7 @@ __device__ __forceinline__ float bf16(const uint16_t* p) { return __uint_as_floa
 // One output from its sum and its residual.
 __device__ __forceinline__ void finish(const Epilogue& e, long long m, int n, float acc, float sw, float bias,
                                        float res) {
-  float z[1] = {acc * (e.sx ? e.sx[m] : 1.f) * sw + bias};
+  float z[1] = {__fmaf_rn(acc, (e.sx ? e.sx[m] : 1.f) * sw, bias)};
   activate(z, e.act);
   if (e.res) z[0] += res;
   if (e.out_f32)
