@@ -79,8 +79,9 @@ enum {
   SV_FLAG_CAPACITY = 64,       /* kv_commit: seq_len + n would pass capacity       */
   SV_FLAG_TIMEOUT = 128,       /* a bounded device wait ran out                    */
   SV_FLAG_BAD_N = 256,         /* kv_commit: n_accepted outside [0, K] or above k_b;
-                                  prefix_attention: a length outside the table      */
-  SV_FLAG_BAD_PAGE = 512       /* prefix_attention: a needed page id outside the pool */
+                                  prefix_attention, kv4: a length outside the table;
+                                  fork, free: a sequence that cannot be             */
+  SV_FLAG_BAD_PAGE = 512       /* a needed page id outside the pool                  */
 };
 
 /* Optional per-(sequence, position) diagnostics, float32 [B][K+1][SV_DIAG_FIELDS],
@@ -499,6 +500,202 @@ sv_status sv_linear(const void* x, int64_t ldx, const float* x_scale, const void
                     const void* residual, int64_t ldr, int act, void* out, int64_t ldo,
                     sv_dtype out_dtype, int M, int N, int K, void* workspace,
                     size_t workspace_bytes, void* stream);
+
+/*
+ * A draft held in 4 bits: the cache that self-speculative decoding keeps beside
+ * the target's [SSD §3.3, §4.5: one paged cache, rolled back by the commit],
+ * and the weights of a quantised draft [SD §4.1].
+ *
+ * The 4-bit cache.  A row (one head's key or value of a token, D values) is D
+ * codes c of 4 bits with a bf16 scale s and a bf16 minimum m:
+ *     s = bf16((max - min) / 15), m = min,
+ *     c = min(round((x - m) / s), 15) (0 if s = 0), value = m + s c,
+ * rounding to nearest, ties to even.  A row with a value that is not finite gets
+ * s = m = NaN.  A pool is [num_pages] pages of sv_kv4_page_bytes() bytes; in a
+ * page each of the Hkv heads has a block of page_size * (D + 8) bytes, rounded up
+ * to 16:
+ *     K codes [page_size][D / 2], V codes [page_size][D / 2] (value 2i in the
+ *     low half of byte i), K's (s, m) [page_size][2], V's (s, m) [page_size][2].
+ * Pools are 16-byte aligned.  Any bytes are a valid cache; scales are not negative.
+ */
+
+/* Bytes of a page; 0 if Hkv, D or page_size is out of range. */
+size_t sv_kv4_page_bytes(int Hkv, int D, int page_size);
+
+/*
+ * sv_kv4_append - write tokens' keys and values into the 4-bit cache: a prompt's,
+ * or a round's (the emitted token at the committed length and the drafts behind).
+ * sv_kv4_read - the values that the cache stands for (m + s c, rounded once), for
+ * example into pages of sv_prefix_attention.
+ *   Token i (0 <= i < n_per_row[b]) of sequence b stands at starts[b] + i of its
+ *   block table.  Nothing else is written.
+ *   k, v          device bf16, (b,i,h,d) at b*seq_stride + i*pos_stride +
+ *                 h*head_stride + d; 0 strides select the packed [B][T][Hkv][D].
+ *   k_out, v_out  the same, of dtype.
+ *   dtype         SV_BF16; of sv_kv4_read SV_F32 too.
+ *   pool          device, num_pages pages.
+ *   block_table   device int32 [B][max_pages]; no page may take two of the call's
+ *                 tokens at one slot (sequences that share a page append behind it).
+ *   starts        device int32 [B]; n_per_row device int32 [B] or NULL (= T).
+ *   B, T, Hkv     each >= 1, B * T * Hkv <= 2^40; D 64 or 128; page_size >= 1,
+ *                 max_pages * page_size <= 2^31 - 4096.
+ *   workspace     >= 4 bytes, 4-byte aligned: the flag word (OR-ed, not cleared).
+ * k, v, k_out and v_out must be 16-byte aligned, their strides multiples of 8
+ * elements.  A sequence with n outside [0, T] or tokens outside its table
+ * (SV_FLAG_BAD_N), and a token whose page is outside the pool (SV_FLAG_BAD_PAGE),
+ * are left out.
+ */
+sv_status sv_kv4_append(const void* k, const void* v, int64_t seq_stride, int64_t pos_stride,
+                        int64_t head_stride, sv_dtype dtype, void* pool, int num_pages,
+                        int page_size, const int32_t* block_table, int max_pages,
+                        const int32_t* starts, const int32_t* n_per_row, int B, int T, int Hkv,
+                        int D, void* workspace, size_t workspace_bytes, void* stream);
+sv_status sv_kv4_read(const void* pool, int num_pages, int page_size, const int32_t* block_table,
+                      int max_pages, const int32_t* starts, const int32_t* n_per_row, void* k_out,
+                      void* v_out, int64_t seq_stride, int64_t pos_stride, int64_t head_stride,
+                      sv_dtype dtype, int B, int T, int Hkv, int D, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * sv_kv4_attention - attention of a round's query positions over the 4-bit cache,
+ * with the positions of sv_prefix_attention: sequence b has L = seq_lens[b]
+ * committed tokens and its drafts' keys and values at L .. L + k_b - 1; the query
+ * at position i (0 <= i <= k_b) is that of token p = L + i - 1 and sees the tokens
+ * j <= p.  With window > 0 it sees of these only j > p - window and j < sinks.
+ *     z_j = scale * sum_d q[b][i][h][d] * k_j[d],  out = sum_j exp(z_j) v_j / sum_j exp(z_j),
+ *     lse = log sum_j exp(z_j)
+ *   A query that sees no token (or none whose score is above -inf) gets out = 0
+ *   and lse = -inf.  Nothing is written for positions i > k_b.  K = 0 is a draft's
+ *   single-token step.
+ *   q, out        device bf16, strides as sv_prefix_attention's.
+ *   pool, block_table  as above; seq_lens, k_per_row (or NULL) device int32 [B].
+ *   window        0 (none) or the tokens a query sees, its own among them.
+ *   sinks         first tokens that stay visible (of use with a window only), >= 0.
+ *   scale         finite, below 2^64 in magnitude.
+ *   lse           device float32 [B][K+1][Hq], or NULL.
+ *   dtype         SV_BF16.
+ *   B, K, Hq, D, page_size, max_pages  as sv_prefix_attention's.
+ *   workspace     >= sv_kv4_attention_workspace_size(...) bytes, 256-byte aligned,
+ *                 zeroed once before its first call; a call leaves it ready for the
+ *                 next, of any sizes that fit it.  Its first four bytes are the flag
+ *                 word (OR-ed, not cleared).  Calls that share a workspace must be
+ *                 ordered on one stream.
+ * q, out and pool must be 16-byte aligned, strides multiples of 8 elements.  The
+ * products take the codes and a float32 scale per token, the sums are float32; q
+ * and the weights p_j s_j are fp16 next to a power of two per row (11 bits for what
+ * is within 2^-29 of the row's largest; below that an absolute 2^-40 of it).  Values
+ * of q below 2^96 in magnitude; a query with one that is not finite gets NaN.
+ * Tokens that a query does not see are not used, whatever they hold; scales below
+ * 2^-126 count as 0 in v.  A sequence with k_b outside [0, K] (SV_FLAG_BAD_K), with
+ * L < 0 or L + k_b past its table (SV_FLAG_BAD_N), or with a page outside
+ * [0, num_pages) among those that its queries see (SV_FLAG_BAD_PAGE) gets NaN in
+ * out and lse at every position 0 .. k_b (0 .. K for a bad k_b).
+ */
+size_t sv_kv4_attention_workspace_size(int B, int K, int Hq, int Hkv, int D);
+sv_status sv_kv4_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_stride,
+                           int64_t q_head_stride, const void* pool, int num_pages, int page_size,
+                           const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                           const int32_t* k_per_row, int window, int sinks, float scale, void* out,
+                           int64_t out_seq_stride, int64_t out_pos_stride, int64_t out_head_stride,
+                           float* lse, sv_dtype dtype, int B, int K, int Hq, int Hkv, int D,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * sv_linear_w4 - sv_linear with 4-bit weights in groups along K: the projections of
+ * a draft step, where a few rows of x meet all of W.
+ *     z[m][n] = sum_k s[n][k / group] (c[n][k] - zero[n][k / group]) x[m][k] + bias[n]
+ *     out[m][n] = act(z[m][n]) + residual[m][n]
+ *   x         device bf16 [M][K], row stride ldx.
+ *   W         device uint8 [N][K / 2], row stride ldw bytes: code 2i in the low half
+ *             of byte i.
+ *   scales    device bf16 [N][K / group].
+ *   zeros     device uint8 [N][K / group], each 0 .. 15, or NULL (8 everywhere).
+ *   group     32, 64 or 128; K a multiple of it.
+ *   bias, residual, act, out, out_dtype  as sv_linear's.
+ *   M, N, K   each in 1 .. 2^30; strides 0 select K, K / 2, N, N.
+ *   workspace >= sv_linear_w4_workspace_size(M, N, K) bytes, 256-byte aligned,
+ *             zeroed once; calls that share it must be ordered on one stream.
+ * x and W must be 16-byte aligned with row strides of a multiple of 16 bytes; the
+ * rest needs its element's alignment.  out must not overlap an input but residual.
+ * Codes less their zeros are exact; sums are float32, rounded once at the end.
+ */
+size_t sv_linear_w4_workspace_size(int M, int N, int K);
+sv_status sv_linear_w4(const void* x, int64_t ldx, const void* W, int64_t ldw, const void* scales,
+                       const uint8_t* zeros, int group, const void* bias, const void* residual,
+                       int64_t ldr, int act, void* out, int64_t ldo, sv_dtype out_dtype, int M,
+                       int N, int K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Moves of a paged cache's pages: the block tables, lengths and free stack of
+ * sv_kv_commit_paged, with pages that several sequences own.
+ *   pools         host array of num_pools device addresses (1 .. 256): the page
+ *                 arrays that one page id names a page of (keys and values of every
+ *                 layer, a 4-bit pool), read during the call.
+ *   page_bytes    host array: bytes of a page of each, a multiple of 16; array i
+ *                 holds num_pages pages without gaps, 16-byte aligned.
+ *   block_table   device int32 [B][max_pages], -1 for none; seq_lens device int32 [B].
+ *   shares        device int32 [num_pages]: a page's owners (block-table entries)
+ *                 beyond the first; 0 for a free page.  The commit may be used beside
+ *                 these calls as it is: a page behind a sequence's committed tokens
+ *                 has one owner.
+ *   free_pages    device int32 [num_pages or more]: the free stack; free_top device
+ *                 int32 [1], at most num_pages.
+ *   workspace     >= sv_kv_pages_workspace_size(num_pages, n) bytes (n: the call's
+ *                 copies, forks or sequences; 0 for a compaction), 16-byte aligned; its
+ *                 first four bytes are the flag word (OR-ed, not cleared: zero it once).
+ *   B             1 <= B <= 2^24; (max_pages + 1) * page_size must fit in int32.
+ * Ids and places follow from the inputs alone, not from the order in which the
+ * device handles them.
+ *
+ * sv_kv_copy_pages - page dst[i] of every array becomes a copy of page src[i], i < n
+ *   (device int32).  A page may be the source of several copies; a page that is a
+ *   destination must be no other copy's source or destination.  A pair with an id
+ *   outside the pool is left out (SV_FLAG_BAD_PAGE).  1 <= n <= 2^24.
+ *
+ * sv_kv_fork - row dst[f] of the block table becomes a continuation of sequence
+ *   src[f], f < F (device int32, 1 <= F <= 4096): with L = seq_lens[src[f]], it shares
+ *   the floor(L / page_size) full pages, and gets a copy of the page that is partly
+ *   full, in a page from the free stack: the forks that need one take the pages from
+ *   its top in their order.  seq_lens[dst[f]] becomes L; drafts' tokens behind L are
+ *   not taken over (a page that holds nothing else is not).  A row may be forked from
+ *   several times.  A fork whose rows are out of range, equal, whose row dst[f] is not
+ *   empty (seq_lens 0, no pages), is another fork's source or destination, or whose
+ *   source has a length outside its table (SV_FLAG_BAD_N) or a page outside the pool
+ *   (SV_FLAG_BAD_PAGE) is left out.  If the free stack has too few pages for the rest
+ *   (SV_FLAG_CAPACITY), or an id outside the pool on its top (SV_FLAG_BAD_PAGE), nothing
+ *   changes.
+ *
+ * sv_kv_free - sequences seqs[i], i < n (device int32, 1 <= n <= 4096), end: their rows
+ *   become empty, their pages lose an owner each, and pages without one go on the free
+ *   stack, in descending order of their ids (the lowest is taken first).  free_capacity
+ *   >= num_pages.  A sequence out of range, or named again, is left out (SV_FLAG_BAD_N).
+ *   An entry outside the pool, or of a page with more entries than owners, is emptied and
+ *   sets SV_FLAG_BAD_PAGE.
+ *
+ * sv_kv_compact - with n pages in use (named in the block table, or in prefix_pages
+ *   [prefix_count], which may be NULL), those with ids >= n move to the unused ids below
+ *   n, the k-th lowest to the k-th lowest; table, prefix_pages and shares follow, and the
+ *   free stack becomes num_pages - 1 .. n.  free_capacity >= num_pages.  Entries outside
+ *   the pool are left as they are (SV_FLAG_BAD_PAGE).
+ */
+size_t sv_kv_pages_workspace_size(int num_pages, int n);
+sv_status sv_kv_copy_pages(void* const* pools, const int64_t* page_bytes, int num_pools,
+                           int num_pages, const int32_t* src, const int32_t* dst, int n,
+                           void* workspace, size_t workspace_bytes, void* stream);
+sv_status sv_kv_fork(void* const* pools, const int64_t* page_bytes, int num_pools, int num_pages,
+                     int page_size, int32_t* block_table, int max_pages, int32_t* seq_lens,
+                     int32_t* shares, const int32_t* free_pages, int32_t* free_top,
+                     const int32_t* src, const int32_t* dst, int F, int B, void* workspace,
+                     size_t workspace_bytes, void* stream);
+sv_status sv_kv_free(int32_t* block_table, int max_pages, int32_t* seq_lens, int32_t* shares,
+                     int num_pages, int32_t* free_pages, int32_t* free_top, int free_capacity,
+                     const int32_t* seqs, int n, int B, void* workspace, size_t workspace_bytes,
+                     void* stream);
+sv_status sv_kv_compact(void* const* pools, const int64_t* page_bytes, int num_pools,
+                        int num_pages, int32_t* block_table, int max_pages, int B,
+                        int32_t* prefix_pages, int prefix_count, int32_t* shares,
+                        int32_t* free_pages, int32_t* free_top, int free_capacity,
+                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * sv_read_device_flags - synchronise `stream` and copy the workspace's flag

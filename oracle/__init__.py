@@ -35,7 +35,12 @@ Parity status of each function (what pins it, see tests/test_oracle_*.py):
   layer.rmsnorm_residual / row_scale / e4m3_values
                                pinned: lmhead.rmsnorm, torch's e4m3 values
   layer.linear / activation    pinned: triple loop, torch's activations
+  draft4.bf16 / quantise / write_token / read_tokens
+                               pinned: torch's bf16, rows by hand, ties, pools
+  draft4.visible / attention   pinned: positions by hand, a softmax written out
+  draft4.weights               pinned: bytes by hand
+  draft4.Pages                 pinned: books by hand, what every sequence holds
 Planted mistakes that the pins must catch: tests/test_oracle_mutations*.py.
 """
 
-from . import analytics, dynk, layer, lmhead, paged, sample, verify  # noqa: F401
+from . import analytics, draft4, dynk, layer, lmhead, paged, sample, verify  # noqa: F401

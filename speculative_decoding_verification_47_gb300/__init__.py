@@ -8,9 +8,17 @@ draws seeded synthetic inputs.
 
 from .binding import (  # noqa: F401
     SVError,
+    sv_kv4_append,
+    sv_kv4_attention,
+    sv_kv4_read,
     sv_kv_commit,
+    sv_kv_compact,
+    sv_kv_copy_pages,
+    sv_kv_fork,
+    sv_kv_free,
     sv_last_error,
     sv_linear,
+    sv_linear_w4,
     sv_lmhead_rmsnorm,
     sv_lmhead_workspace_size,
     sv_prefix_attention,

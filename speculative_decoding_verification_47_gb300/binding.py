@@ -134,6 +134,37 @@ def lib() -> ctypes.CDLL:
         L.sv_linear.restype = _i32
         L.sv_linear.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _i32, _vp,
                                 _i64, _i32, _i32, _i32, _i32, _vp, _sz, _vp]
+        L.sv_kv4_page_bytes.restype = _sz
+        L.sv_kv4_page_bytes.argtypes = [_i32] * 3
+        L.sv_kv4_append.restype = _i32
+        L.sv_kv4_append.argtypes = [_vp, _vp, _i64, _i64, _i64, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp,
+                                    _i32, _i32, _i32, _i32, _vp, _sz, _vp]
+        L.sv_kv4_read.restype = _i32
+        L.sv_kv4_read.argtypes = [_vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32,
+                                  _i32, _i32, _i32, _i32, _vp, _sz, _vp]
+        L.sv_kv4_attention_workspace_size.restype = _sz
+        L.sv_kv4_attention_workspace_size.argtypes = [_i32] * 5
+        L.sv_kv4_attention.restype = _i32
+        L.sv_kv4_attention.argtypes = [_vp, _i64, _i64, _i64, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i32,
+                                       _i32, _f32, _vp, _i64, _i64, _i64, _vp, _i32, _i32, _i32, _i32,
+                                       _i32, _i32, _vp, _sz, _vp]
+        L.sv_linear_w4_workspace_size.restype = _sz
+        L.sv_linear_w4_workspace_size.argtypes = [_i32, _i32, _i32]
+        L.sv_linear_w4.restype = _i32
+        L.sv_linear_w4.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _i64, _i32, _vp, _i64,
+                                   _i32, _i32, _i32, _i32, _vp, _sz, _vp]
+        L.sv_kv_pages_workspace_size.restype = _sz
+        L.sv_kv_pages_workspace_size.argtypes = [_i32, _i32]
+        L.sv_kv_copy_pages.restype = _i32
+        L.sv_kv_copy_pages.argtypes = [_vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _sz, _vp]
+        L.sv_kv_fork.restype = _i32
+        L.sv_kv_fork.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                 _i32, _vp, _sz, _vp]
+        L.sv_kv_free.restype = _i32
+        L.sv_kv_free.argtypes = [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _sz, _vp]
+        L.sv_kv_compact.restype = _i32
+        L.sv_kv_compact.argtypes = [_vp, _vp, _i32, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _i32,
+                                    _vp, _sz, _vp]
         L.sv_read_device_flags.restype = _i32
         L.sv_read_device_flags.argtypes = [_vp, _c.POINTER(_c.c_uint32), _vp]
         L.sv_last_error.restype = _c.c_char_p
@@ -315,6 +346,101 @@ def sv_linear(x, ldx, x_scale, W, ldw, w_scale, in_dtype, bias, residual, ldr, a
     _check(lib().sv_linear(_ptr(x), ldx, _ptr(x_scale), _ptr(W), ldw, _ptr(w_scale), in_dtype,
                            _ptr(bias), _ptr(residual), ldr, act, _ptr(out), ldo, out_dtype, M, N, K,
                            _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sv_kv4_page_bytes(Hkv: int, D: int, page_size: int) -> int:
+    return lib().sv_kv4_page_bytes(Hkv, D, page_size)
+
+
+def sv_kv4_append(k, v, seq_stride, pos_stride, head_stride, dtype, pool, num_pages, page_size,
+                  block_table, max_pages, starts, n_per_row, B, T, Hkv, D, workspace,
+                  workspace_bytes, stream=None):
+    _check(lib().sv_kv4_append(_ptr(k), _ptr(v), seq_stride, pos_stride, head_stride, dtype,
+                               _ptr(pool), num_pages, page_size, _ptr(block_table), max_pages,
+                               _ptr(starts), _ptr(n_per_row), B, T, Hkv, D, _ptr(workspace),
+                               workspace_bytes, _stream(stream)))
+
+
+def sv_kv4_read(pool, num_pages, page_size, block_table, max_pages, starts, n_per_row, k_out, v_out,
+                seq_stride, pos_stride, head_stride, dtype, B, T, Hkv, D, workspace, workspace_bytes,
+                stream=None):
+    _check(lib().sv_kv4_read(_ptr(pool), num_pages, page_size, _ptr(block_table), max_pages,
+                             _ptr(starts), _ptr(n_per_row), _ptr(k_out), _ptr(v_out), seq_stride,
+                             pos_stride, head_stride, dtype, B, T, Hkv, D, _ptr(workspace),
+                             workspace_bytes, _stream(stream)))
+
+
+def sv_kv4_attention_workspace_size(B: int, K: int, Hq: int, Hkv: int, D: int) -> int:
+    return lib().sv_kv4_attention_workspace_size(B, K, Hq, Hkv, D)
+
+
+def sv_kv4_attention(q, q_seq_stride, q_pos_stride, q_head_stride, pool, num_pages, page_size,
+                     block_table, max_pages, seq_lens, k_per_row, window, sinks, scale, out,
+                     out_seq_stride, out_pos_stride, out_head_stride, lse, dtype, B, K, Hq, Hkv, D,
+                     workspace, workspace_bytes, stream=None):
+    _check(lib().sv_kv4_attention(
+        _ptr(q), q_seq_stride, q_pos_stride, q_head_stride, _ptr(pool), num_pages, page_size,
+        _ptr(block_table), max_pages, _ptr(seq_lens), _ptr(k_per_row), window, sinks, scale,
+        _ptr(out), out_seq_stride, out_pos_stride, out_head_stride, _ptr(lse), dtype, B, K, Hq, Hkv,
+        D, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sv_linear_w4_workspace_size(M: int, N: int, K: int) -> int:
+    return lib().sv_linear_w4_workspace_size(M, N, K)
+
+
+def sv_linear_w4(x, ldx, W, ldw, scales, zeros, group, bias, residual, ldr, act, out, ldo, out_dtype,
+                 M, N, K, workspace, workspace_bytes, stream=None):
+    _check(lib().sv_linear_w4(_ptr(x), ldx, _ptr(W), ldw, _ptr(scales), _ptr(zeros), group,
+                              _ptr(bias), _ptr(residual), ldr, act, _ptr(out), ldo, out_dtype, M, N,
+                              K, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sv_kv_pages_workspace_size(num_pages: int, n: int) -> int:
+    return lib().sv_kv_pages_workspace_size(num_pages, n)
+
+
+def _pools(pools, page_bytes, num_pools):
+    """The host arrays of page arrays' addresses and page sizes (None stays NULL)."""
+    if pools is not None and len(pools) != num_pools or page_bytes is not None and len(page_bytes) != num_pools:
+        raise ValueError(f"expected {num_pools} pools and page sizes")
+    return (None if pools is None else (_vp * num_pools)(*[_ptr(p) for p in pools]),
+            None if page_bytes is None else (_i64 * num_pools)(*page_bytes))
+
+
+def sv_kv_copy_pages(pools, page_bytes, num_pools, num_pages, src, dst, n, workspace, workspace_bytes,
+                     stream=None):
+    """``pools`` and ``page_bytes`` are sequences of tensors (or addresses) and of sizes."""
+    p, sizes = _pools(pools, page_bytes, num_pools)
+    _check(lib().sv_kv_copy_pages(p, sizes, num_pools, num_pages, _ptr(src), _ptr(dst), n,
+                                  _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sv_kv_fork(pools, page_bytes, num_pools, num_pages, page_size, block_table, max_pages, seq_lens,
+               shares, free_pages, free_top, src, dst, F, B, workspace, workspace_bytes, stream=None):
+    """``pools`` and ``page_bytes`` are sequences of tensors (or addresses) and of sizes."""
+    p, sizes = _pools(pools, page_bytes, num_pools)
+    _check(lib().sv_kv_fork(p, sizes, num_pools, num_pages, page_size, _ptr(block_table), max_pages,
+                            _ptr(seq_lens), _ptr(shares), _ptr(free_pages), _ptr(free_top), _ptr(src),
+                            _ptr(dst), F, B, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sv_kv_free(block_table, max_pages, seq_lens, shares, num_pages, free_pages, free_top, free_capacity,
+               seqs, n, B, workspace, workspace_bytes, stream=None):
+    _check(lib().sv_kv_free(_ptr(block_table), max_pages, _ptr(seq_lens), _ptr(shares), num_pages,
+                            _ptr(free_pages), _ptr(free_top), free_capacity, _ptr(seqs), n, B,
+                            _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sv_kv_compact(pools, page_bytes, num_pools, num_pages, block_table, max_pages, B, prefix_pages,
+                  prefix_count, shares, free_pages, free_top, free_capacity, workspace,
+                  workspace_bytes, stream=None):
+    """``pools`` and ``page_bytes`` are sequences of tensors (or addresses) and of sizes."""
+    p, sizes = _pools(pools, page_bytes, num_pools)
+    _check(lib().sv_kv_compact(p, sizes, num_pools, num_pages, _ptr(block_table), max_pages, B,
+                               _ptr(prefix_pages), prefix_count, _ptr(shares), _ptr(free_pages),
+                               _ptr(free_top), free_capacity, _ptr(workspace), workspace_bytes,
+                               _stream(stream)))
 
 
 def sv_read_device_flags(workspace, stream=None) -> int:

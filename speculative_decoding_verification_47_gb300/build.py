@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libspecverify.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["sv_verify.cu", "sv_commit.cu", "sv_dynk.cu", "sv_lmhead.cu", "sv_norm.cu", "sv_linear.cu",
-           "sv_attention.cu", "sv_api.cu"]
+           "sv_attention.cu", "sv_kv4.cu", "sv_linear_w4.cu", "sv_pages.cu", "sv_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -492,6 +492,311 @@ sv_status sv_linear(const void* x, int64_t ldx, const float* x_scale, const void
   return SV_OK;
 }
 
+// Geometry of a 4-bit cache and of a call's tokens; NULL if it is in range.
+static const char* kv4_shape(int num_pages, int page_size, int max_pages, int B, int Hkv, int D) {
+  if (B < 1 || Hkv < 1 || num_pages < 1 || page_size < 1 || max_pages < 1)
+    return "need B, Hkv, num_pages, page_size and max_pages >= 1";
+  if (D != 64 && D != 128) return "D must be 64 or 128";
+  if ((long long)max_pages * page_size > 0x7fffffffLL - 4096) return "max_pages * page_size must be at most 2^31 - 4096";
+  if (sv_kv4_page_bytes(Hkv, D, page_size) == 0) return "a page must be below 2^31 bytes";
+  return nullptr;
+}
+
+size_t sv_kv4_page_bytes(int Hkv, int D, int page_size) {
+  if (Hkv < 1 || (D != 64 && D != 128) || page_size < 1) return 0;
+  const size_t head = sv::kv4_head_bytes(D, page_size);
+  return head > 0x7fffffff / (size_t)Hkv ? 0 : head * Hkv;
+}
+
+static sv_status kv4_rows(const void* k_in, const void* v_in, void* k_out, void* v_out, int64_t seq_stride,
+                          int64_t pos_stride, int64_t head_stride, sv_dtype dtype, const void* pool, int num_pages,
+                          int page_size, const int32_t* block_table, int max_pages, const int32_t* starts,
+                          const int32_t* n_per_row, int B, int T, int Hkv, int D, void* workspace,
+                          size_t workspace_bytes, void* stream, bool append) {
+  if (dtype != SV_BF16 && (append || dtype != SV_F32))
+    return fail(SV_ERR_DTYPE, append ? "dtype must be SV_BF16" : "dtype must be SV_BF16 or SV_F32");
+  if (T < 1) return fail(SV_ERR_SHAPE, "need T >= 1");
+  if (const char* why = kv4_shape(num_pages, page_size, max_pages, B, Hkv, D)) return fail(SV_ERR_SHAPE, why);
+  if ((long long)B * T > (1LL << 40) / Hkv) return fail(SV_ERR_SHAPE, "B * T * Hkv must be at most 2^40");
+  const void* k = append ? k_in : k_out;
+  const void* v = append ? v_in : v_out;
+  if (!k || !v || !pool || !block_table || !starts)
+    return fail(SV_ERR_ARG, "keys, values, pool, block_table and starts are required");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pool, 16))
+    return fail(SV_ERR_ARG, "keys, values and pool must be 16-byte aligned");
+  if (!aligned(block_table, 4) || !aligned(starts, 4) || !aligned(n_per_row, 4))
+    return fail(SV_ERR_ARG, "the index arrays must be aligned to their element size");
+  sv::Kv4RowsLaunch L;
+  L.c = {const_cast<void*>(pool), num_pages, page_size, block_table, max_pages, Hkv};
+  L.k_in = k_in;
+  L.v_in = v_in;
+  L.k_out = k_out;
+  L.v_out = v_out;
+  L.head = head_stride ? head_stride : D;
+  L.pos = pos_stride ? pos_stride : (long long)Hkv * D;
+  L.seq = seq_stride ? seq_stride : (long long)T * Hkv * D;
+  for (long long s : {L.head, L.pos, L.seq})
+    if (s < 0 || s % 8 != 0) return fail(SV_ERR_SHAPE, "strides must be >= 0 and multiples of 8 elements");
+  if (!append && ((Hkv > 1 && L.head < D) || k_out == v_out))
+    return fail(SV_ERR_SHAPE, "outputs must not overlap");
+  L.dtype = dtype;
+  L.starts = starts;
+  L.n_per_row = n_per_row;
+  L.B = B;
+  L.T = T;
+  L.D = D;
+  if (!workspace || !aligned(workspace, 4) || workspace_bytes < 4)
+    return fail(SV_ERR_WORKSPACE, "workspace (its flag word) must be non-NULL, aligned, >= 4 bytes");
+  L.flags = static_cast<uint32_t*>(workspace);
+  L.stream = stream;
+  std::string err;
+  const int s = sv::kv4_rows_launch(L, &err);
+  if (s != SV_OK) return fail(static_cast<sv_status>(s), err);
+  return SV_OK;
+}
+
+sv_status sv_kv4_append(const void* k, const void* v, int64_t seq_stride, int64_t pos_stride, int64_t head_stride,
+                        sv_dtype dtype, void* pool, int num_pages, int page_size, const int32_t* block_table,
+                        int max_pages, const int32_t* starts, const int32_t* n_per_row, int B, int T, int Hkv, int D,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  return kv4_rows(k, v, nullptr, nullptr, seq_stride, pos_stride, head_stride, dtype, pool, num_pages, page_size,
+                  block_table, max_pages, starts, n_per_row, B, T, Hkv, D, workspace, workspace_bytes, stream, true);
+}
+
+sv_status sv_kv4_read(const void* pool, int num_pages, int page_size, const int32_t* block_table, int max_pages,
+                      const int32_t* starts, const int32_t* n_per_row, void* k_out, void* v_out, int64_t seq_stride,
+                      int64_t pos_stride, int64_t head_stride, sv_dtype dtype, int B, int T, int Hkv, int D,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  return kv4_rows(nullptr, nullptr, k_out, v_out, seq_stride, pos_stride, head_stride, dtype, pool, num_pages,
+                  page_size, block_table, max_pages, starts, n_per_row, B, T, Hkv, D, workspace, workspace_bytes,
+                  stream, false);
+}
+
+static const char* kv4_attention_shape(int B, int K, int Hq, int Hkv, int D) {
+  return attention_shape(B, K, Hq, Hkv, D, 0, 1);
+}
+
+size_t sv_kv4_attention_workspace_size(int B, int K, int Hq, int Hkv, int D) {
+  return kv4_attention_shape(B, K, Hq, Hkv, D) ? 0 : sv::kv4_attention_workspace_bytes(K, Hq, Hkv, D);
+}
+
+sv_status sv_kv4_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_stride, int64_t q_head_stride,
+                           const void* pool, int num_pages, int page_size, const int32_t* block_table, int max_pages,
+                           const int32_t* seq_lens, const int32_t* k_per_row, int window, int sinks, float scale,
+                           void* out, int64_t out_seq_stride, int64_t out_pos_stride, int64_t out_head_stride,
+                           float* lse, sv_dtype dtype, int B, int K, int Hq, int Hkv, int D, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (dtype != SV_BF16) return fail(SV_ERR_DTYPE, "dtype must be SV_BF16");
+  if (const char* why = kv4_attention_shape(B, K, Hq, Hkv, D)) return fail(SV_ERR_SHAPE, why);
+  if (const char* why = kv4_shape(num_pages, page_size, max_pages, B, Hkv, D)) return fail(SV_ERR_SHAPE, why);
+  if (window < 0 || sinks < 0) return fail(SV_ERR_SHAPE, "window and sinks must be >= 0");
+  if (!q || !pool || !block_table || !seq_lens || !out)
+    return fail(SV_ERR_ARG, "q, pool, block_table, seq_lens and out are required");
+  if (!(scale > -0x1p64f && scale < 0x1p64f)) return fail(SV_ERR_ARG, "scale must be within +-2^64");
+  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16))
+    return fail(SV_ERR_ARG, "q, pool and out must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(k_per_row, 4))
+    return fail(SV_ERR_ARG, "lse and the index arrays must be aligned to their element size");
+  sv::Kv4AttentionLaunch L;
+  L.c = {const_cast<void*>(pool), num_pages, page_size, block_table, max_pages, Hkv};
+  L.q = q;
+  L.q_head = q_head_stride ? q_head_stride : D;
+  L.q_pos = q_pos_stride ? q_pos_stride : (long long)Hq * D;
+  L.q_seq = q_seq_stride ? q_seq_stride : (long long)(K + 1) * Hq * D;
+  L.out = out;
+  L.o_head = out_head_stride ? out_head_stride : D;
+  L.o_pos = out_pos_stride ? out_pos_stride : (long long)Hq * D;
+  L.o_seq = out_seq_stride ? out_seq_stride : (long long)(K + 1) * Hq * D;
+  for (long long s : {L.q_head, L.q_pos, L.q_seq, L.o_head, L.o_pos, L.o_seq})
+    if (s < 0 || s % 8 != 0) return fail(SV_ERR_SHAPE, "strides must be >= 0 and multiples of 8 elements");
+  if (L.o_head < D && Hq > 1) return fail(SV_ERR_SHAPE, "out head stride is smaller than D");
+  L.lens = seq_lens;
+  L.kpr = k_per_row;
+  L.window = window;
+  L.sinks = sinks;
+  L.scale = scale;
+  L.lse = lse;
+  L.B = B;
+  L.K = K;
+  L.Hq = Hq;
+  L.D = D;
+  if (!workspace || !aligned(workspace, 256))
+    return fail(SV_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");
+  if (workspace_bytes < sv::kv4_attention_workspace_bytes(K, Hq, Hkv, D))
+    return fail(SV_ERR_WORKSPACE, "workspace smaller than sv_kv4_attention_workspace_size()");
+  L.workspace = workspace;
+  L.stream = stream;
+  std::string err;
+  const int s = sv::kv4_attention_launch(L, &err);
+  if (s != SV_OK) return fail(static_cast<sv_status>(s), err);
+  return SV_OK;
+}
+
+size_t sv_linear_w4_workspace_size(int M, int N, int K) {
+  if (M < 1 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K > kMaxRows) return 0;
+  return sv::linear_w4_workspace_bytes(M, N, K);
+}
+
+sv_status sv_linear_w4(const void* x, int64_t ldx, const void* W, int64_t ldw, const void* scales,
+                       const uint8_t* zeros, int group, const void* bias, const void* residual, int64_t ldr, int act,
+                       void* out, int64_t ldo, sv_dtype out_dtype, int M, int N, int K, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (out_dtype != SV_BF16 && out_dtype != SV_F32) return fail(SV_ERR_DTYPE, "out_dtype must be SV_BF16 or SV_F32");
+  if (M < 1 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K > kMaxRows)
+    return fail(SV_ERR_SHAPE, "M, N and K must be in 1 .. 2^30");
+  if (group != 32 && group != 64 && group != 128) return fail(SV_ERR_SHAPE, "group must be 32, 64 or 128");
+  if (K % group != 0) return fail(SV_ERR_SHAPE, "K must be a multiple of group");
+  if (act < SV_ACT_NONE || act > SV_ACT_GELU_TANH) return fail(SV_ERR_ARG, "unknown activation");
+  if (!x || !W || !scales || !out) return fail(SV_ERR_ARG, "x, W, scales and out are required");
+  const int os = out_dtype == SV_BF16 ? 2 : 4;
+  if (!aligned(x, 16) || !aligned(W, 16)) return fail(SV_ERR_ARG, "x and W must be 16-byte aligned");
+  if (!aligned(scales, 2) || !aligned(bias, 2) || !aligned(residual, os) || !aligned(out, os))
+    return fail(SV_ERR_ARG, "pointers must be aligned to their element size");
+  sv::LinearW4Launch L;
+  L.x = x;
+  L.ldx = ldx ? ldx : K;
+  L.W = W;
+  L.ldw = ldw ? ldw : K / 2;
+  L.scales = scales;
+  L.zeros = zeros;
+  L.group = group;
+  L.bias = bias;
+  L.residual = residual;
+  L.ldr = ldr ? ldr : N;
+  L.act = act;
+  L.out = out;
+  L.ldo = ldo ? ldo : N;
+  L.out_dtype = out_dtype;
+  L.M = M;
+  L.N = N;
+  L.K = K;
+  if (L.ldx < K || L.ldw < K / 2 || L.ldr < N || L.ldo < N)
+    return fail(SV_ERR_SHAPE, "row strides must be 0 or at least the row's length");
+  if (L.ldx % 8 != 0 || L.ldw % 16 != 0)
+    return fail(SV_ERR_SHAPE, "row strides of x and W must be multiples of 16 bytes");
+  if (residual == out && L.ldr != L.ldo) return fail(SV_ERR_ARG, "residual over out needs its row stride");
+  if (out == x || out == W) return fail(SV_ERR_ARG, "out must not be x or W");
+  if (!workspace || !aligned(workspace, 256))
+    return fail(SV_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");
+  if (workspace_bytes < sv::linear_w4_workspace_bytes(M, N, K))
+    return fail(SV_ERR_WORKSPACE, "workspace smaller than sv_linear_w4_workspace_size()");
+  L.workspace = workspace;
+  L.stream = stream;
+  std::string err;
+  const int s = sv::linear_w4_launch(L, &err);
+  if (s != SV_OK) return fail(static_cast<sv_status>(s), err);
+  return SV_OK;
+}
+
+constexpr int kMaxCopies = 1 << 24;  // copies of a call; sequences of a block table
+
+size_t sv_kv_pages_workspace_size(int num_pages, int n) {
+  return num_pages < 1 || num_pages > kMaxRows || n < 0 || n > kMaxCopies ? 0 : sv::kv_pages_workspace_bytes(num_pages, n);
+}
+
+static sv_status pages_args(void* const* pools, const int64_t* page_bytes, int num_pools, int num_pages, int n,
+                            void* workspace, size_t workspace_bytes, sv::PagePools* p) {
+  if (num_pages < 1 || num_pages > kMaxRows) return fail(SV_ERR_SHAPE, "num_pages must be in 1 .. 2^30");
+  if (p) {
+    if (num_pools < 1 || num_pools > sv::kMaxPools) return fail(SV_ERR_SHAPE, "num_pools must be in 1 .. 256");
+    if (!pools || !page_bytes) return fail(SV_ERR_ARG, "pools and page_bytes are required");
+    p->n = num_pools;
+    for (int i = 0; i < num_pools; ++i) {
+      if (!pools[i] || !aligned(pools[i], 16)) return fail(SV_ERR_ARG, "every pool must be non-NULL and 16-byte aligned");
+      if (page_bytes[i] < 16 || page_bytes[i] % 16 != 0 || page_bytes[i] > 0x7fffffffLL)
+        return fail(SV_ERR_SHAPE, "page_bytes must be a multiple of 16 below 2^31");
+      p->base[i] = static_cast<uint8_t*>(pools[i]);
+      p->bytes[i] = page_bytes[i];
+    }
+  }
+  if (!workspace || !aligned(workspace, 16))
+    return fail(SV_ERR_WORKSPACE, "workspace must be non-NULL and 16-byte aligned");
+  if (workspace_bytes < sv::kv_pages_workspace_bytes(num_pages, n))
+    return fail(SV_ERR_WORKSPACE, "workspace smaller than sv_kv_pages_workspace_size()");
+  return SV_OK;
+}
+
+static sv_status table_args(const int32_t* block_table, int max_pages, int page_size, int B) {
+  if (B < 1 || B > kMaxCopies || max_pages < 1 || page_size < 1)
+    return fail(SV_ERR_SHAPE, "need 1 <= B <= 2^24, max_pages >= 1, page_size >= 1");
+  if ((long long)max_pages * page_size + page_size > 0x7fffffffLL)
+    return fail(SV_ERR_SHAPE, "(max_pages + 1) * page_size must fit in int32");
+  if (!block_table || !aligned(block_table, 4)) return fail(SV_ERR_ARG, "block_table is required and must be aligned");
+  return SV_OK;
+}
+
+static bool index_array(const void* p) { return p && aligned(p, 4); }
+
+sv_status sv_kv_copy_pages(void* const* pools, const int64_t* page_bytes, int num_pools, int num_pages,
+                           const int32_t* src, const int32_t* dst, int n, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (n < 1 || n > kMaxCopies) return fail(SV_ERR_SHAPE, "n must be in 1 .. 2^24");
+  sv::PagePools p;
+  const sv_status a = pages_args(pools, page_bytes, num_pools, num_pages, n, workspace, workspace_bytes, &p);
+  if (a != SV_OK) return a;
+  if (!index_array(src) || !index_array(dst)) return fail(SV_ERR_ARG, "src and dst are required and must be aligned");
+  std::string err;
+  const int s = sv::kv_copy_launch(p, num_pages, src, dst, n, workspace, stream, &err);
+  return s == SV_OK ? SV_OK : fail(static_cast<sv_status>(s), err);
+}
+
+sv_status sv_kv_fork(void* const* pools, const int64_t* page_bytes, int num_pools, int num_pages, int page_size,
+                     int32_t* block_table, int max_pages, int32_t* seq_lens, int32_t* shares,
+                     const int32_t* free_pages, int32_t* free_top, const int32_t* src, const int32_t* dst, int F,
+                     int B, void* workspace, size_t workspace_bytes, void* stream) {
+  if (F < 1 || F > sv::kMaxForks) return fail(SV_ERR_SHAPE, "F must be in 1 .. 4096");
+  sv_status a = table_args(block_table, max_pages, page_size, B);
+  if (a != SV_OK) return a;
+  sv::PagePools p;
+  a = pages_args(pools, page_bytes, num_pools, num_pages, F, workspace, workspace_bytes, &p);
+  if (a != SV_OK) return a;
+  for (const void* v : {(const void*)seq_lens, (const void*)shares, (const void*)free_pages, (const void*)free_top,
+                        (const void*)src, (const void*)dst})
+    if (!index_array(v)) return fail(SV_ERR_ARG, "every array argument is required and must be aligned");
+  std::string err;
+  const int s = sv::kv_fork_launch(p, num_pages, page_size, block_table, max_pages, seq_lens, shares, free_pages,
+                                   free_top, src, dst, F, B, workspace, stream, &err);
+  return s == SV_OK ? SV_OK : fail(static_cast<sv_status>(s), err);
+}
+
+sv_status sv_kv_free(int32_t* block_table, int max_pages, int32_t* seq_lens, int32_t* shares, int num_pages,
+                     int32_t* free_pages, int32_t* free_top, int free_capacity, const int32_t* seqs, int n, int B,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (n < 1 || n > sv::kMaxForks) return fail(SV_ERR_SHAPE, "n must be in 1 .. 4096");
+  sv_status a = table_args(block_table, max_pages, 1, B);
+  if (a != SV_OK) return a;
+  a = pages_args(nullptr, nullptr, 0, num_pages, n, workspace, workspace_bytes, nullptr);
+  if (a != SV_OK) return a;
+  if (free_capacity < num_pages) return fail(SV_ERR_SHAPE, "free_capacity must be at least num_pages");
+  for (const void* v : {(const void*)seq_lens, (const void*)shares, (const void*)free_pages, (const void*)free_top,
+                        (const void*)seqs})
+    if (!index_array(v)) return fail(SV_ERR_ARG, "every array argument is required and must be aligned");
+  std::string err;
+  const int s = sv::kv_free_launch(block_table, max_pages, seq_lens, shares, num_pages, free_pages, free_top,
+                                   free_capacity, seqs, n, B, workspace, stream, &err);
+  return s == SV_OK ? SV_OK : fail(static_cast<sv_status>(s), err);
+}
+
+sv_status sv_kv_compact(void* const* pools, const int64_t* page_bytes, int num_pools, int num_pages,
+                        int32_t* block_table, int max_pages, int B, int32_t* prefix_pages, int prefix_count,
+                        int32_t* shares, int32_t* free_pages, int32_t* free_top, int free_capacity, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  sv_status a = table_args(block_table, max_pages, 1, B);
+  if (a != SV_OK) return a;
+  sv::PagePools p;
+  a = pages_args(pools, page_bytes, num_pools, num_pages, 0, workspace, workspace_bytes, &p);
+  if (a != SV_OK) return a;
+  if (free_capacity < num_pages) return fail(SV_ERR_SHAPE, "free_capacity must be at least num_pages");
+  if (prefix_count < 0 || (prefix_count > 0 && !index_array(prefix_pages)))
+    return fail(SV_ERR_ARG, "prefix_pages is required when prefix_count > 0 and must be aligned");
+  for (const void* v : {(const void*)shares, (const void*)free_pages, (const void*)free_top})
+    if (!index_array(v)) return fail(SV_ERR_ARG, "every array argument is required and must be aligned");
+  std::string err;
+  const int s = sv::kv_compact_launch(p, num_pages, block_table, max_pages, B, prefix_pages, prefix_count, shares,
+                                      free_pages, free_top, workspace, stream, &err);
+  return s == SV_OK ? SV_OK : fail(static_cast<sv_status>(s), err);
+}
+
 sv_status sv_read_device_flags(const void* workspace, uint32_t* flags_host, void* stream) {
   if (!workspace || !flags_host) return fail(SV_ERR_ARG, "null pointer");
   cudaStream_t st = static_cast<cudaStream_t>(stream);

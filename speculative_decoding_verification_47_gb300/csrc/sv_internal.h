@@ -167,4 +167,97 @@ struct AttentionLaunch {
 int attention_launch(const AttentionLaunch& L, std::string* err);
 size_t attention_workspace_bytes(int B, int K, int Hq, int Hkv, int D, int prefix_len, int max_own);
 
+// A cache in 4 bits and the block table of the call's sequences.
+struct Kv4Cache {
+  void* pool;
+  int num_pages, page_size;
+  const int32_t* table;
+  int max_pages, Hkv;
+};
+size_t kv4_head_bytes(int D, int page_size);  // of one key head in one page
+
+struct Kv4RowsLaunch {
+  Kv4Cache c;
+  const void* k_in;  // NULL: read the cache into k_out and v_out
+  const void* v_in;
+  void* k_out;
+  void* v_out;
+  long long seq, pos, head;  // elements
+  sv_dtype dtype;
+  const int32_t* starts;
+  const int32_t* n_per_row;
+  int B, T, D;
+  uint32_t* flags;
+  void* stream;
+};
+
+// Enqueue the writing or the reading of tokens.  Returns an sv_status; fills *err on failure.
+int kv4_rows_launch(const Kv4RowsLaunch& L, std::string* err);
+
+struct Kv4AttentionLaunch {
+  Kv4Cache c;
+  const void* q;
+  long long q_seq, q_pos, q_head;  // elements
+  const int32_t* lens;
+  const int32_t* kpr;
+  int window, sinks;
+  float scale;
+  void* out;
+  long long o_seq, o_pos, o_head;  // elements
+  float* lse;
+  int B, K, Hq, D;
+  void* workspace;
+  void* stream;
+};
+
+// Enqueue the attention over the 4-bit cache.  Returns an sv_status; fills *err on failure.
+int kv4_attention_launch(const Kv4AttentionLaunch& L, std::string* err);
+size_t kv4_attention_workspace_bytes(int K, int Hq, int Hkv, int D);
+
+struct LinearW4Launch {
+  const void* x;
+  long long ldx;  // elements
+  const void* W;
+  long long ldw;  // bytes
+  const void* scales;
+  const void* zeros;
+  int group;
+  const void* bias;
+  const void* residual;
+  long long ldr;
+  int act;
+  void* out;
+  long long ldo;
+  sv_dtype out_dtype;
+  int M, N, K;
+  void* workspace;
+  void* stream;
+};
+
+// Enqueue the product with 4-bit weights.  Returns an sv_status; fills *err on failure.
+int linear_w4_launch(const LinearW4Launch& L, std::string* err);
+size_t linear_w4_workspace_bytes(int M, int N, int K);
+
+// Page arrays whose pages move together (one page id names a page of each).
+constexpr int kMaxPools = 256;
+struct PagePools {
+  uint8_t* base[kMaxPools];
+  long long bytes[kMaxPools];  // of a page, a multiple of 16
+  int n;
+};
+constexpr int kMaxForks = 4096;
+
+size_t kv_pages_workspace_bytes(int num_pages, int n);
+int kv_copy_launch(const PagePools& p, int num_pages, const int32_t* src, const int32_t* dst, int n, void* workspace,
+                   void* stream, std::string* err);
+int kv_fork_launch(const PagePools& p, int num_pages, int page_size, int32_t* table, int max_pages, int32_t* lens,
+                   int32_t* shares, const int32_t* free_pages, int32_t* free_top, const int32_t* src,
+                   const int32_t* dst, int F, int B, void* workspace, void* stream, std::string* err);
+int kv_free_launch(int32_t* table, int max_pages, int32_t* lens, int32_t* shares, int num_pages, int32_t* free_pages,
+                   int32_t* free_top, int free_capacity, const int32_t* seqs, int n, int B, void* workspace,
+                   void* stream, std::string* err);
+int kv_compact_launch(const PagePools& p, int num_pages, int32_t* table, int max_pages, int B, int32_t* prefix_pages,
+                      int prefix_count, int32_t* shares, int32_t* free_pages, int32_t* free_top, void* workspace,
+                      void* stream, std::string* err);
+
 }  // namespace sv
