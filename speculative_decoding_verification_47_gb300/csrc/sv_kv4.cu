@@ -231,8 +231,11 @@ constexpr int kTok = 16;           // tokens of a tile
 constexpr int kStages = 4;         // tiles of a warp on their way
 constexpr int kMaxSeqs = 1024;     // sequences of a launch
 constexpr int kMaxCtas = 1024;
-constexpr int kMinTiles = 8;       // of a CTA: two a warp
+constexpr int kMinShare = 14;      // of a CTA
+// What a group costs beside its tiles, in tiles: Q, the join of the warps, the way to the next.
+constexpr int kGroupCost = 6;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr float kNone = -3e38f;    // a reference before the first score
 
 struct Args {
   Cache c;
@@ -251,9 +254,12 @@ struct Args {
   float* parts;        // [CTA][2][rows * (D + 2)]
 };
 
-template <int D, int NT>
+// ROWS query rows a block: 4 (a column of the product is then a row and half of the tile's tokens
+// for everything between the two products), 8 or 16.
+template <int D, int ROWS>
 struct Shape {
-  static constexpr int kRows = 8 * NT;
+  static constexpr int kRows = ROWS;
+  static constexpr int NT = ROWS == 16 ? 2 : 1;
   static constexpr int kRowBytes = D / 2;
   static constexpr int kTileBytes = 2 * kTok * kRowBytes + 2 * kTok * 4;  // K, V, (s, m) of both
   static constexpr int kRing = kWarps * kStages * kTileBytes;
@@ -299,11 +305,52 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b, int rows) {
   return s;
 }
 
-__device__ __forceinline__ void cp16(uint32_t to, const void* from, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+// A CTA's run of tiles of one group (sequence b, key head h, block of query rows).
+struct Segment {
+  Seq s;
+  int b, h, block, t0, t1;
+  unsigned long long group;  // where the group begins, in units of a tile's cost
+};
+
+// The first run with tiles at or behind `at` (below `end`), which moves behind it.
+__device__ __forceinline__ bool next_segment(const Args& a, const unsigned long long* prefix, int rows,
+                                             unsigned long long& at, unsigned long long end, Segment& g) {
+  while (at < end) {
+    int lo = 0, hi = a.B - 1;  // the last b with prefix[b] <= at
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= at) lo = mid; else hi = mid - 1;
+    }
+    g.b = lo;
+    g.s = seq_of(a, lo, rows);
+    const unsigned long long off = at - prefix[lo];
+    const uint32_t cost = (uint32_t)(g.s.tiles + kGroupCost);
+    const uint32_t group = off >> 32 ? (uint32_t)(off / cost) : (uint32_t)off / cost;
+    const int u0 = (int)(off - (unsigned long long)group * cost);
+    const int u1 = (int)min((unsigned long long)cost, u0 + (end - at));
+    g.group = at - u0;
+    g.h = (int)(group / (uint32_t)g.s.blocks);
+    g.block = (int)(group - (uint32_t)g.h * g.s.blocks);
+    g.t0 = max(0, u0 - kGroupCost);
+    g.t1 = max(0, u1 - kGroupCost);
+    at += u1 - u0;
+    if (g.t0 < g.t1) return true;
+  }
+  return false;
 }
-__device__ __forceinline__ void cp4(uint32_t to, const void* from, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+
+__device__ __forceinline__ void cp16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+// zeros in place of what is not there
+__device__ __forceinline__ void cp16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -347,53 +394,104 @@ __device__ __forceinline__ float log2_of(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// x - ref, 2^ of it: a reference of -inf (nothing seen yet) counts as 0
-__device__ __forceinline__ float weight_of(float x, float ref) { return ex2(x - (ref == -INFINITY ? 0.f : ref)); }
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
-// Where a warp's tile is loaded from, for this lane's token of it.
-template <int D>
-__device__ __forceinline__ void issue_tile(const Cache& c, const Seq& s, int tile, int lane, int b, int h, uint32_t ring,
-                                           bool* bad_page) {
-  constexpr int RB = D / 2, CHUNKS = RB / 16;  // 16-byte pieces of a row
-  const int tok = (tile + (tile < s.sink_tiles ? 0 : s.skip)) * kTok + (lane & 15);
-  long long at = -1, word = -1;
-  if (tok < s.len + s.k) {
-    const int p = divide(tok, c.by_page), slot = tok - p * c.page_size;
-    const int page = c.table[(long long)b * c.max_pages + p];
-    if (page >= 0 && page < c.num_pages) {
-      const long long head = page * c.page_bytes + (long long)h * c.head_bytes;
-      at = head + (long long)slot * RB;
-      word = head + (long long)c.page_size * D + slot * 4LL;
-    } else {
-      *bad_page = true;
+// The loads of a warp's tiles: kWarps apart, each tile's page ids read while the one before is asked for.
+template <int D, bool ALIGNED>
+struct Loader {
+  static constexpr int RB = D / 2, CHUNKS = RB / 16, COPIES = kTok * CHUNKS / 32;
+  const uint8_t* head;   // the pool's pages, at this segment's head
+  const int32_t* row;    // of the block table
+  int sink_tiles, skip, end, tile, last, page;  // page: of the next tile (this lane's token of it)
+  bool bad;
+
+  __device__ __forceinline__ int first_token(int t) const { return (t + (t < sink_tiles ? 0 : skip)) * kTok; }
+  __device__ __forceinline__ void look_up(const Cache& c, int lane) {
+    page = 0;
+    if (tile < last) {
+      const int tok = first_token(tile) + (ALIGNED ? 0 : lane & 15);
+      if (ALIGNED || tok < end) page = __ldg(row + divide(tok, c.by_page));
     }
   }
-  const long long values = (long long)c.page_size * RB;
-#pragma unroll
-  for (int j = 0; j < kTok * CHUNKS / 32; ++j) {
-    const int row = (lane + 32 * j) / CHUNKS, chunk = lane % CHUNKS;
-    const long long from = __shfl_sync(kFull, at, row);
-    const uint32_t bytes = from < 0 ? 0 : 16;
-    const uint8_t* src = c.pool + (from < 0 ? 0 : from + chunk * 16);
-    const uint32_t to = ring + row * RB + ((chunk ^ (row >> 1)) & (CHUNKS - 1)) * 16;
-    cp16(to, src, bytes);
-    cp16(to + kTok * RB, src + (from < 0 ? 0 : values), bytes);
+  __device__ __forceinline__ void begin(const Cache& c, const Segment& g, int warp, int lane) {
+    head = c.pool + (long long)g.h * c.head_bytes;
+    row = c.table + (long long)g.b * c.max_pages;
+    sink_tiles = g.s.sink_tiles, skip = g.s.skip, end = g.s.bad ? 0 : g.s.len + g.s.k;
+    tile = g.t0 + warp, last = end > 0 ? g.t1 : 0;
+    bad = false;
+    look_up(c, lane);
   }
-  const bool of_values = lane >= 16;
-  cp4(ring + 2 * kTok * RB + lane * 4, c.pool + (word < 0 ? 0 : word + (of_values ? c.page_size * 4LL : 0)),
-      word < 0 ? 0 : 4);
-}
+  // one group of copies, an empty one behind the last tile
+  __device__ __forceinline__ void issue(const Cache& c, uint32_t buf, int lane) {
+    if (tile < last) {
+      const int tok0 = first_token(tile), here = page;
+      const int values = c.page_size * RB, words = c.page_size * D;
+      const uint32_t to = buf + lane / CHUNKS * RB + ((lane ^ (lane / CHUNKS >> 1)) & (CHUNKS - 1)) * 16;
+      tile += kWarps;
+      look_up(c, lane);
+      if constexpr (ALIGNED) {
+        const int slot = tok0 - divide(tok0, c.by_page) * c.page_size;
+        bool sound = (unsigned)here < (unsigned)c.num_pages;
+        bad = bad || !sound;
+        const uint8_t* base = head + (sound ? here : 0) * c.page_bytes;
+        const uint8_t* from = base + slot * RB + lane * 16;
+        const uint8_t* word = base + words + slot * 4 + (lane & 15) * 4 + (lane >= 16 ? c.page_size * 4 : 0);
+        if (tok0 + kTok <= end && sound) {
+#pragma unroll
+          for (int j = 0; j < COPIES; ++j) {
+            cp16(to + j * 512, from + j * 512);
+            cp16(to + kTok * RB + j * 512, from + values + j * 512);
+          }
+          cp4(buf + 2 * kTok * RB + lane * 4, word);
+        } else {
+          const int there = sound ? end - tok0 : 0;
+#pragma unroll
+          for (int j = 0; j < COPIES; ++j) {
+            cp16(to + j * 512, from + j * 512, (lane + 32 * j) / CHUNKS < there);
+            cp16(to + kTok * RB + j * 512, from + values + j * 512, (lane + 32 * j) / CHUNKS < there);
+          }
+          cp4(buf + 2 * kTok * RB + lane * 4, word, (lane & 15) < there);
+        }
+      } else {
+        const int tok = tok0 + (lane & 15);
+        long long at = -1;  // of this lane's token's codes
+        int slot = 0;
+        if (tok < end) {
+          slot = tok - divide(tok, c.by_page) * c.page_size;
+          if ((unsigned)here < (unsigned)c.num_pages) at = here * c.page_bytes + slot * RB;
+          else bad = true;
+        }
+#pragma unroll
+        for (int j = 0; j < COPIES; ++j) {
+          const long long from = __shfl_sync(kFull, at, (lane + 32 * j) / CHUNKS);
+          const uint8_t* src = head + (from < 0 ? 0 : from) + lane % CHUNKS * 16;
+          cp16(to + j * 512, src, from >= 0);
+          cp16(to + kTok * RB + j * 512, src + values, from >= 0);
+        }
+        const uint8_t* word = head + (at < 0 ? 0 : at - slot * RB) + words + slot * 4 + (lane >= 16 ? c.page_size * 4 : 0);
+        cp4(buf + 2 * kTok * RB + lane * 4, word, at >= 0);
+      }
+    }
+    cp_commit();
+  }
+};
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_kernel(const __grid_constant__ Args a) {
-  using S = Shape<D, NT>;
-  constexpr int RB = D / 2;
+template <int D, int ROWS, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_kernel(const __grid_constant__ Args a) {
+  using S = Shape<D, ROWS>;
+  constexpr int NT = S::NT, RB = D / 2;
+  constexpr bool HALF = ROWS == 4;
+  constexpr int TP = HALF ? 1 : 2;      // tokens a lane holds scores of
   constexpr int WK = D / 32;            // code words of a key per lane
   constexpr int TILES = D / 16;         // 16-row tiles of O^T
+  constexpr uint32_t TB = S::kTileBytes;
   extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* ring_base = smem;
   float* join = reinterpret_cast<float*>(smem + S::kRing);                   // [warp][row][pitch]
   float* join_r = join + kWarps * S::kRows * S::kPitch;                      // [warp][row]
   float* join_l = join_r + kWarps * S::kRows;
@@ -402,9 +500,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
   __shared__ uint32_t bad_of_cta, last_of_group;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  // the columns of the product whose scores the lane holds: col0, col0 + 1, for tokens g (+ 8)
+  const int col0 = HALF ? 2 * (t & 1) : 2 * t, tok_of = HALF ? g + (t >> 1) * 8 : g;
   pdl_wait();
 
-  // the groups' tiles in a row: prefix[b] is where sequence b's begin
+  // the groups in a row, each as long as its tiles and kGroupCost: prefix[b] is where sequence b's begin
   {
     const int each = (a.B + kThreads - 1) / kThreads;
     unsigned long long mine = 0;
@@ -412,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
       const int b = tid * each + j;
       if (b < a.B) {
         const Seq s = seq_of(a, b, S::kRows);
-        mine += (unsigned long long)s.tiles * s.blocks * a.Hkv;
+        mine += (unsigned long long)(s.tiles + kGroupCost) * s.blocks * a.Hkv;
         prefix[b + 1] = mine;  // (within this thread's run)
       }
     }
@@ -435,46 +535,28 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
   }
   const unsigned long long total = prefix[a.B];
   unsigned long long share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < kMinTiles) share = kMinTiles;
-  const unsigned long long begin = blockIdx.x * share;
-  const unsigned long long end = min(begin + share, total);
-  const uint32_t ring = smem_addr(ring_base) + warp * kStages * S::kTileBytes;
+  if (share < kMinShare) share = kMinShare;
+  const unsigned long long begin = blockIdx.x * share, end = min(begin + share, total);
+  const uint32_t ring = smem_addr(smem) + warp * kStages * TB;
 
-  for (unsigned long long at = begin; at < end;) {
-    // the group that `at` lies in
-    int b = 0;
-    {
-      int lo = 0, hi = a.B - 1;  // the last b with prefix[b] <= at
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= at) lo = mid; else hi = mid - 1;
-      }
-      b = lo;
-    }
-    const Seq s = seq_of(a, b, S::kRows);
-    const unsigned long long off = at - prefix[b];
-    const int group = (int)(off / s.tiles);
-    const int t0 = (int)(off - (unsigned long long)group * s.tiles);
-    const int t1 = (int)min((unsigned long long)s.tiles, t0 + (end - at));
-    const int h = group / s.blocks, block = group - h * s.blocks;
-    const int row0 = block * S::kRows, rows = min(S::kRows, a.G * (s.k + 1) - row0);
-    bool bad_page = false;
-
-    // the first tiles
-    int ahead = t0 + warp;
-    if (!s.bad) {
+  unsigned long long at = begin;
+  Segment sg, next;
+  Loader<D, ALIGNED> ld;
+  bool more = next_segment(a, prefix, S::kRows, at, end, next);
+  if (more) {
+    ld.begin(a.c, next, warp, lane);
 #pragma unroll
-      for (int st = 0; st < kStages - 1; ++st) {
-        if (ahead < t1) issue_tile<D>(a.c, s, ahead, lane, b, h, ring + st * S::kTileBytes, &bad_page);
-        cp_commit();
-        ahead += kWarps;
-      }
-    }
+    for (int st = 0; st < kStages - 1; ++st) ld.issue(a.c, ring + st * TB, lane);
+  }
+  while (more) {
+    sg = next;
+    const Seq& s = sg.s;
+    const int row0 = sg.block * S::kRows, rows = min(S::kRows, a.G * (s.k + 1) - row0);
 
     // Q's rows in fp16 next to 2^15, in the order of the codes' halves
     uint32_t qf[NT][2 * WK][2];
-    float fr[NT][2], sq[NT][2];  // of the columns 2t, 2t + 1: score = s (acc fr) + m sq
-    int limit[NT][2];            // the first token that the column's query does not see
+    F2 fr[NT], sq[NT];     // of the lane's columns: score = s (acc fr) + m sq
+    int limit[NT][2];      // the first token that the column's query does not see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g;
@@ -482,8 +564,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
 #pragma unroll
       for (int w = 0; w < WK; ++w) v[w] = make_uint4(0, 0, 0, 0);
       if (r < rows && !s.bad) {
-        const int i = (row0 + r) / a.G, head = h * a.G + (row0 + r) % a.G;
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + b * a.q_seq + i * a.q_pos + head * a.q_head + t * (D / 4));
+        const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + sg.b * a.q_seq + i * a.q_pos + head * a.q_head + t * (D / 4));
 #pragma unroll
         for (int w = 0; w < WK; ++w) v[w] = __ldg(src + w);
       }
@@ -516,11 +598,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
         qf[nt][2 * w + 1][1] = half2_of(bf16_hi(u.y) * f16, bf16_hi(u.w) * f16);
       }
       const float mine_fr = a.scale * __uint_as_float((uint32_t)(254 - fb) << 23) * 16777216.f, mine_sq = a.scale * sum;
+      fr[nt] = f2_pack(__shfl_sync(kFull, mine_fr, col0 * 4), __shfl_sync(kFull, mine_fr, col0 * 4 + 4));
+      sq[nt] = f2_pack(__shfl_sync(kFull, mine_sq, col0 * 4), __shfl_sync(kFull, mine_sq, col0 * 4 + 4));
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        fr[nt][j] = __shfl_sync(kFull, mine_fr, (2 * t + j) * 4);
-        sq[nt][j] = __shfl_sync(kFull, mine_sq, (2 * t + j) * 4);
-        const int col = nt * 8 + 2 * t + j;
+        const int col = nt * 8 + col0 + j;
         limit[nt][j] = col < rows ? s.len + (row0 + col) / a.G : 0;
       }
     }
@@ -529,40 +611,43 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
     const int widest = s.len + (row0 + rows - 1) / a.G - a.window;  // the last row's window begins here
 
     float o[NT][TILES][4] = {};
-    float sum[NT][2] = {}, low[NT][2] = {};
-    float ref[NT][2], vref[NT][2];  // references of p and of p s'
+    F2 sum[NT], low[NT];
+    float ref[NT][2], vref[NT][2];  // references of p, and of 2^7 p s'
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) ref[nt][j] = vref[nt][j] = -INFINITY;
+    for (int nt = 0; nt < NT; ++nt) {
+      sum[nt] = low[nt] = f2_pack(0.f, 0.f);
+      ref[nt][0] = ref[nt][1] = vref[nt][0] = vref[nt][1] = kNone;
+    }
 
-    if (!s.bad) {
-      int stage = 0;
-      for (int tile = t0 + warp; tile < t1; tile += kWarps) {
-        const uint32_t buf = ring + stage * S::kTileBytes;
-        if (ahead < t1)
-          issue_tile<D>(a.c, s, ahead, lane, b, h, ring + ((stage + kStages - 1) & (kStages - 1)) * S::kTileBytes, &bad_page);
-        cp_commit();
-        ahead += kWarps;
+    {
+      uint32_t stage = 0;
+      const int t1 = s.bad ? 0 : sg.t1;
+      for (int tile = sg.t0 + warp; tile < t1; tile += kWarps) {
+        const uint32_t buf = ring + stage * TB;
+        ld.issue(a.c, ring + ((stage + kStages - 1) & (kStages - 1)) * TB, lane);
         cp_wait<kStages - 1>();
         __syncwarp();
 
         const int tok0 = (tile + (tile < s.sink_tiles ? 0 : s.skip)) * kTok;
-        const uint32_t kw0 = lds32(buf + 2 * kTok * RB + g * 4), kw1 = lds32(buf + 2 * kTok * RB + (g + 8) * 4);
-        const uint32_t vw0 = lds32(buf + 2 * kTok * RB + (16 + g) * 4), vw1 = lds32(buf + 2 * kTok * RB + (24 + g) * 4);
+        uint32_t kw[TP], vw[TP];
+#pragma unroll
+        for (int e = 0; e < TP; ++e) {
+          kw[e] = lds32(buf + 2 * kTok * RB + (tok_of + 8 * e) * 4);
+          vw[e] = lds32(buf + 2 * kTok * RB + 64 + (tok_of + 8 * e) * 4);
+        }
 
-        // S^T: tokens g and g + 8 by rows 2t and 2t + 1
+        // S^T: tokens g and g + 8 by columns 2t and 2t + 1
         float acc[NT][4] = {};
         {
           uint32_t x[WK], y[WK];
           if constexpr (D == 128) {
             const uint4 p = lds128(buf + g * RB + ((t ^ (g >> 1)) & 3) * 16);
-            const uint4 r = lds128(buf + (g + 8) * RB + ((t ^ ((g + 8) >> 1)) & 3) * 16);
+            const uint4 r = lds128(buf + (g + 8) * RB + ((t ^ (g >> 1)) & 3) * 16);
             x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w;
             y[0] = r.x, y[1] = r.y, y[2] = r.z, y[3] = r.w;
           } else {
             const uint2 p = lds64(buf + g * RB + (((t >> 1) ^ (g >> 1)) & 1) * 16 + (t & 1) * 8);
-            const uint2 r = lds64(buf + (g + 8) * RB + (((t >> 1) ^ ((g + 8) >> 1)) & 1) * 16 + (t & 1) * 8);
+            const uint2 r = lds64(buf + (g + 8) * RB + (((t >> 1) ^ (g >> 1)) & 1) * 16 + (t & 1) * 8);
             x[0] = p.x, x[1] = p.y;
             y[0] = r.x, y[1] = r.y;
           }
@@ -578,78 +663,124 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
           }
         }
 
-        const float ks0 = bf16_lo(kw0), km0 = bf16_hi(kw0), ks1 = bf16_lo(kw1), km1 = bf16_hi(kw1);
-        const float vm0 = bf16_hi(vw0), vm1 = bf16_hi(vw1);
-        const float lg0 = log2_of(bf16_lo(vw0)), lg1 = log2_of(bf16_lo(vw1));
-        const bool edge = tok0 + kTok > all_see || (a.window > 0 && tok0 < widest && tok0 + kTok > a.sinks);
-        uint32_t pt[NT][2];
-        bool raise = false;
-        float z[NT][4], zv[NT][4];
+        F2 z[NT][TP], zv[NT][TP], vm[TP];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int e = 0; e < TP; ++e) {
+          const float ks = bf16_lo(kw[e]), km = bf16_hi(kw[e]), m = bf16_hi(vw[e]), lg = log2_of(bf16_lo(vw[e]));
+          vm[e] = f2_pack(m, m);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            z[nt][j] = __fmaf_rn(ks0, acc[nt][j] * fr[nt][j], km0 * sq[nt][j]);
-            z[nt][2 + j] = __fmaf_rn(ks1, acc[nt][2 + j] * fr[nt][j], km1 * sq[nt][j]);
-          }
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tok = tok0 + g + (e >> 1) * 8, lim = limit[nt][e & 1];
-              const bool seen = tok < lim && (a.window <= 0 || tok >= lim - a.window || tok < a.sinks);
-              z[nt][e] = seen ? z[nt][e] : -INFINITY;
-              zv[nt][e] = seen ? z[nt][e] + (e < 2 ? lg0 : lg1) : -INFINITY;
+          for (int nt = 0; nt < NT; ++nt) {
+            F2 c;
+            if constexpr (HALF) {  // tokens g + 8 to the lanes of the columns that have no row
+              const float c2 = __shfl_xor_sync(kFull, acc[nt][2], 2), c3 = __shfl_xor_sync(kFull, acc[nt][3], 2);
+              c = f2_pack(t < 2 ? acc[nt][0] : c2, t < 2 ? acc[nt][1] : c3);
+            } else {
+              c = f2_pack(acc[nt][2 * e], acc[nt][2 * e + 1]);
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) zv[nt][e] = z[nt][e] + (e < 2 ? lg0 : lg1);
+            z[nt][e] = f2_fma(f2_pack(ks, ks), f2_mul(c, fr[nt]), f2_mul(f2_pack(km, km), sq[nt]));
+            zv[nt][e] = f2_add(z[nt][e], f2_pack(lg, lg));
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            raise = raise || z[nt][e] > ref[nt][e & 1] + 8.f || zv[nt][e] > vref[nt][e & 1] + 8.f;
         }
-        // a reference follows its maximum only when that has grown by 2^8
-        if (__any_sync(kFull, raise)) {
+        if (tok0 + kTok > all_see || (a.window > 0 && tok0 < widest && tok0 + kTok > a.sinks)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float m = fmaxf(z[nt][j], z[nt][2 + j]), mv = fmaxf(zv[nt][j], zv[nt][2 + j]);
+            for (int e = 0; e < TP; ++e) {
+              float u[2], v[2];
+              f2_unpack(z[nt][e], u[0], u[1]);
+              f2_unpack(zv[nt][e], v[0], v[1]);
+              const int tok = tok0 + tok_of + 8 * e;
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) {
+              for (int j = 0; j < 2; ++j) {
+                const int lim = limit[nt][j];
+                const bool seen = tok < lim && (a.window <= 0 || tok >= lim - a.window || tok < a.sinks);
+                u[j] = seen ? u[j] : -INFINITY;
+                v[j] = seen ? v[j] : -INFINITY;
+              }
+              z[nt][e] = f2_pack(u[0], u[1]);
+              zv[nt][e] = f2_pack(v[0], v[1]);
+            }
+        }
+        // a reference follows its maximum only when that has grown by 2^8
+        bool raise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float u[2], v[2];
+          f2_unpack(z[nt][0], u[0], u[1]);
+          f2_unpack(zv[nt][0], v[0], v[1]);
+          if constexpr (!HALF) {
+            float x, y;
+            f2_unpack(z[nt][1], x, y);
+            u[0] = fmaxf(u[0], x), u[1] = fmaxf(u[1], y);
+            f2_unpack(zv[nt][1], x, y);
+            v[0] = fmaxf(v[0], x), v[1] = fmaxf(v[1], y);
+          }
+          raise = raise || fmaxf(u[0] - ref[nt][0], u[1] - ref[nt][1]) > 8.f ||
+                  fmaxf(v[0] - vref[nt][0], v[1] - vref[nt][1]) > 15.f;
+        }
+        if (__any_sync(kFull, raise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float u[TP][2], v[TP][2];
+#pragma unroll
+            for (int e = 0; e < TP; ++e) {
+              f2_unpack(z[nt][e], u[e][0], u[e][1]);
+              f2_unpack(zv[nt][e], v[e][0], v[e][1]);
+            }
+            float f[2], fv[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float m = fmaxf(u[0][j], u[TP - 1][j]), mv = fmaxf(v[0][j], v[TP - 1][j]);
+#pragma unroll
+              for (int d = HALF ? 2 : 4; d < 32; d <<= 1) {
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
                 mv = fmaxf(mv, __shfl_xor_sync(kFull, mv, d));
               }
-              if (m > ref[nt][j]) {
-                const float f = ex2(ref[nt][j] - m);
-                sum[nt][j] *= f;
-                low[nt][j] *= f;
-                ref[nt][j] = m;
-              }
-              if (mv > vref[nt][j]) {
-                const float f = ex2(vref[nt][j] - mv);
-                vref[nt][j] = mv;
-#pragma unroll
-                for (int n = 0; n < TILES; ++n) {
-                  o[nt][n][j] *= f;
-                  o[nt][n][2 + j] *= f;
-                }
-              }
+              m = fmaxf(m, ref[nt][j]);
+              mv = fmaxf(mv - 7.f, vref[nt][j]);
+              f[j] = ex2(ref[nt][j] - m);
+              fv[j] = ex2(vref[nt][j] - mv);
+              ref[nt][j] = m;
+              vref[nt][j] = mv;
             }
+            sum[nt] = f2_mul(sum[nt], f2_pack(f[0], f[1]));
+            low[nt] = f2_mul(low[nt], f2_pack(f[0], f[1]));
+#pragma unroll
+            for (int n = 0; n < TILES; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][n][e] *= fv[e & 1];
+          }
         }
+        uint32_t pt[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float pv[4];
+          uint32_t h[TP];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p = weight_of(z[nt][e], ref[nt][e & 1]);
-            sum[nt][e & 1] += p;
-            // (a token that is not seen may have any minimum)
-            low[nt][e & 1] = p == 0.f ? low[nt][e & 1] : __fmaf_rn(p, e < 2 ? vm0 : vm1, low[nt][e & 1]);
-            pv[e] = weight_of(zv[nt][e] + 7.f, vref[nt][e & 1]);
+          for (int e = 0; e < TP; ++e) {
+            float u[2], v[2];
+            f2_unpack(f2_add(z[nt][e], f2_pack(-ref[nt][0], -ref[nt][1])), u[0], u[1]);
+            f2_unpack(f2_add(zv[nt][e], f2_pack(-vref[nt][0], -vref[nt][1])), v[0], v[1]);
+            const F2 p = f2_pack(ex2(u[0]), ex2(u[1]));
+            sum[nt] = f2_add(sum[nt], p);
+            // (the minimum of a token that is not seen may be anything)
+            const F2 more_low = f2_fma(p, vm[e], low[nt]);
+            if (tok0 + kTok > all_see || a.window > 0) {
+              float l0, l1, n0, n1;
+              f2_unpack(low[nt], l0, l1);
+              f2_unpack(more_low, n0, n1);
+              low[nt] = f2_pack(u[0] == -INFINITY ? l0 : n0, u[1] == -INFINITY ? l1 : n1);
+            } else {
+              low[nt] = more_low;
+            }
+            h[e] = half2_of(ex2(v[0]), ex2(v[1]));
           }
-          pt[nt][0] = transpose8(half2_of(pv[0], pv[1]));
-          pt[nt][1] = transpose8(half2_of(pv[2], pv[3]));
+          if constexpr (HALF) {
+            pt[nt][0] = transpose8(h[0]);
+            pt[nt][1] = __shfl_xor_sync(kFull, pt[nt][0], 16);
+          } else {
+            pt[nt][0] = transpose8(h[0]);
+            pt[nt][1] = transpose8(h[1]);
+          }
         }
 
         // O^T: pairs of tokens (2t, 2t + 1), (2t + 8, 2t + 9), this lane's codes of each
@@ -657,10 +788,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
         if constexpr (D == 128) {
           uint2 w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tok = 2 * t + (e & 1) + (e >> 1) * 8;
-            w[e] = lds64(vb + tok * RB + (((g >> 1) ^ (tok >> 1)) & 3) * 16 + (g & 1) * 8);
-          }
+          for (int e = 0; e < 4; ++e)
+            w[e] = lds64(vb + (2 * t + (e & 1) + (e >> 1) * 8) * RB + (((g >> 1) ^ t) & 3) * 16 + (g & 1) * 8);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const uint32_t sel = hf ? 0x7632u : 0x5410u;
@@ -679,10 +808,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
         } else {
           uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tok = 2 * t + (e & 1) + (e >> 1) * 8;
-            w[e] = lds32(vb + tok * RB + (((g >> 2) ^ (tok >> 1)) & 1) * 16 + (g & 3) * 4);
-          }
+          for (int e = 0; e < 4; ++e)
+            w[e] = lds32(vb + (2 * t + (e & 1) + (e >> 1) * 8) * RB + (((g >> 2) ^ t) & 1) * 16 + (g & 3) * 4);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const uint32_t sel = hf ? 0x7632u : 0x5410u;
@@ -699,59 +826,74 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
         __syncwarp();
         stage = (stage + 1) & (kStages - 1);
       }
-      cp_wait<0>();
+      cp_wait<0>();  // (empty groups)
+      __syncwarp();
+    }
+    const bool bad_page = ld.bad;
+
+    // the next segment's first tiles are on their way while this one's warps are joined
+    more = next_segment(a, prefix, S::kRows, at, end, next);
+    if (more) {
+      ld.begin(a.c, next, warp, lane);
+#pragma unroll
+      for (int st = 0; st < kStages - 1; ++st) ld.issue(a.c, ring + st * TB, lane);
     }
 
-    // join the warps' states
     if (tid == 0) bad_of_cta = 0;
     __syncthreads();  // (also: the join's words of the segment before have been read)
     if (s.bad || bad_page) bad_of_cta = 1;
-    if (tid == 0 && s.bad && at == prefix[b]) atomicOr(a.flags, s.bad);
-    if (bad_page && lane < 16) atomicOr(a.flags, SV_FLAG_BAD_PAGE);
+    if (tid == 0 && s.bad && sg.group == prefix[sg.b]) atomicOr(a.flags, s.bad);
+    if (bad_page) atomicOr(a.flags, SV_FLAG_BAD_PAGE);
+    float sums[NT][2], lows[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      f2_unpack(sum[nt], sums[nt][0], sums[nt][1]);
+      f2_unpack(low[nt], lows[nt][0], lows[nt][1]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          sum[nt][j] += __shfl_xor_sync(kFull, sum[nt][j], d);
-          low[nt][j] += __shfl_xor_sync(kFull, low[nt][j], d);
+        for (int d = HALF ? 2 : 4; d < 32; d <<= 1) {
+          sums[nt][j] += __shfl_xor_sync(kFull, sums[nt][j], d);
+          lows[nt][j] += __shfl_xor_sync(kFull, lows[nt][j], d);
         }
-        if (g == 0) join_r[warp * S::kRows + nt * 8 + 2 * t + j] = ref[nt][j];
+        if (g == 0) join_r[warp * S::kRows + nt * 8 + col0 + j] = ref[nt][j];
       }
+    }
     __syncthreads();
     const bool bad = bad_of_cta != 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int r = nt * 8 + 2 * t + j;
+        const int r = nt * 8 + col0 + j;
         float top = join_r[r];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) top = fmaxf(top, join_r[w * S::kRows + r]);
-        const float scale = weight_of(ref[nt][j], top);
-        if (g == 0) join_l[warp * S::kRows + r] = sum[nt][j] * scale;
-        const float add = low[nt][j] * scale;
-        // codes' subnormals and the weights' 2^7 undone; nothing was seen if the reference is -inf
-        const float even = vref[nt][j] == -INFINITY ? 0.f : ex2(vref[nt][j] - ref[nt][j]) * scale;
+        const float scale = ex2(ref[nt][j] - top);
+        if (g == 0) join_l[warp * S::kRows + r] = sums[nt][j] * scale;
+        const float add = lows[nt][j] * scale;
+        const float even = ex2(vref[nt][j] - ref[nt][j]) * scale;
         float* to = join + (warp * S::kRows + r) * S::kPitch;
+        if (!HALF || t < 2) {
 #pragma unroll
-        for (int n = 0; n < TILES; ++n) {
-          const int d0 = D == 128 ? 16 * g + n : 8 * g + 2 * n, d1 = D == 128 ? d0 + 8 : d0 + 1;
-          // D = 128: odd values stand 4 bits up; D = 64: the second row of a tile does
-          const float u0 = D == 128 && (n & 1) ? 0x1p13f : 0x1p17f, u1 = D == 128 ? u0 : 0x1p13f;
-          to[d0 + d0 / S::kRun] = __fmaf_rn(o[nt][n][j] * u0, even, add);
-          to[d1 + d1 / S::kRun] = __fmaf_rn(o[nt][n][2 + j] * u1, even, add);
+          for (int n = 0; n < TILES; ++n) {
+            const int d0 = D == 128 ? 16 * g + n : 8 * g + 2 * n, d1 = D == 128 ? d0 + 8 : d0 + 1;
+            // the codes' subnormals undone; D = 128: odd values stand 4 bits up; D = 64: the second row of a tile does
+            const float u0 = D == 128 && (n & 1) ? 0x1p20f : 0x1p24f, u1 = D == 128 ? u0 : 0x1p20f;
+            to[d0 + d0 / S::kRun] = __fmaf_rn(o[nt][n][j] * u0, even, add);
+            to[d1 + d1 / S::kRun] = __fmaf_rn(o[nt][n][2 + j] * u1, even, add);
+          }
         }
       }
     __syncthreads();
 
-    const bool whole = t0 == 0 && t1 == s.tiles;
-    const unsigned long long group_begin = at - t0, group_end = group_begin + s.tiles;
-    float* part = a.parts + ((long long)blockIdx.x * 2 + (at == begin ? 0 : 1)) * S::kPart;
+    const bool whole = sg.t0 == 0 && sg.t1 == s.tiles;
+    // its place among the CTA's parts: the first of a group that began in front of the CTA's share
+    const bool early = begin >= sg.group;
+    float* part = a.parts + ((long long)blockIdx.x * 2 + (early ? 0 : 1)) * S::kPart;
     for (int x = tid; x < rows * (D / 2); x += kThreads) {
       const int r = x / (D / 2), d = (x % (D / 2)) * 2;
-      float n0 = 0.f, n1 = 0.f, l = 0.f, top = -INFINITY;
+      float n0 = 0.f, n1 = 0.f, l = 0.f, top = kNone;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float* from = join + (w * S::kRows + r) * S::kPitch + d + d / S::kRun;
@@ -762,15 +904,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
       }
       if (bad) l = __uint_as_float(0x7fc00000u);
       if (whole) {
-        const int i = (row0 + r) / a.G, head = h * a.G + (row0 + r) % a.G;
+        const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
         const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-        *reinterpret_cast<uint32_t*>(a.out + b * a.o_seq + i * a.o_pos + head * a.o_head + d) =
+        *reinterpret_cast<uint32_t*>(a.out + sg.b * a.o_seq + i * a.o_pos + head * a.o_head + d) =
             tc::pack_bf16x2(n0 * inv, n1 * inv);
         if (d == 0 && a.lse)
-          a.lse[((long long)b * (a.K + 1) + i) * a.Hq + head] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+          a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] =
+              l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
       } else {
-        part[r * D + d] = n0;
-        part[r * D + d + 1] = n1;
+        *reinterpret_cast<float2*>(part + r * D + d) = make_float2(n0, n1);
         if (d == 0) {
           part[S::kRows * D + r] = top;
           part[S::kRows * (D + 1) + r] = l;
@@ -779,7 +921,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
     }
     if (!whole) {
       // the last of the group's CTAs joins its parts
-      const unsigned first = (unsigned)(group_begin / share), last = (unsigned)((group_end - 1) / share);
+      const unsigned first = (unsigned)((sg.group + kGroupCost) / share);
+      const unsigned last = (unsigned)((sg.group + kGroupCost + s.tiles - 1) / share);
       __threadfence();
       __syncthreads();
       if (tid == 0) {
@@ -794,39 +937,36 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kMinCtas) attention_ke
       if (last_of_group) {
         constexpr int PER = kThreads / S::kRows, W = D / PER;  // threads of a row, values of a thread
         const int r = tid / PER, d0 = (tid % PER) * W;
-        const bool at_begin = group_begin == (unsigned long long)first * share;
+        const bool first_is_early = (unsigned long long)first * share >= sg.group;
         auto part_of = [&](unsigned c) {
-          return a.parts + ((long long)c * 2 + (c == first && !at_begin ? 1 : 0)) * S::kPart;
+          return a.parts + ((long long)c * 2 + (c == first && !first_is_early ? 1 : 0)) * S::kPart;
         };
         if (r < rows) {
-          float top = -INFINITY;
+          float top = kNone;
           for (unsigned c = first; c <= last; ++c) top = fmaxf(top, __ldcg(part_of(c) + S::kRows * D + r));
           float l = 0.f, n[W] = {};
           for (unsigned c = first; c <= last; ++c) {
             const float* p = part_of(c);
-            const float f = weight_of(__ldcg(p + S::kRows * D + r), top);
+            const float f = ex2(__ldcg(p + S::kRows * D + r) - top);
             l = __fmaf_rn(__ldcg(p + S::kRows * (D + 1) + r), f, l);
 #pragma unroll
-            for (int e = 0; e < W; e += 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(p + r * D + d0 + e));
+            for (int e = 0; e < W; e += 2) {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(p + r * D + d0 + e));
               n[e] = __fmaf_rn(v.x, f, n[e]);
               n[e + 1] = __fmaf_rn(v.y, f, n[e + 1]);
-              n[e + 2] = __fmaf_rn(v.z, f, n[e + 2]);
-              n[e + 3] = __fmaf_rn(v.w, f, n[e + 3]);
             }
           }
-          const int i = (row0 + r) / a.G, head = h * a.G + (row0 + r) % a.G;
+          const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
           const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-          uint32_t* to = reinterpret_cast<uint32_t*>(a.out + b * a.o_seq + i * a.o_pos + head * a.o_head + d0);
+          uint32_t* to = reinterpret_cast<uint32_t*>(a.out + sg.b * a.o_seq + i * a.o_pos + head * a.o_head + d0);
 #pragma unroll
           for (int e = 0; e < W / 2; ++e) to[e] = tc::pack_bf16x2(n[2 * e] * inv, n[2 * e + 1] * inv);
           if (d0 == 0 && a.lse)
-            a.lse[((long long)b * (a.K + 1) + i) * a.Hq + head] =
+            a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] =
                 l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
         }
       }
     }
-    at += t1 - t0;
   }
 }
 
@@ -848,9 +988,9 @@ int failed(const char* what, cudaError_t e, std::string* err) {
   return SV_ERR_CUDA;
 }
 
-template <int D, int NT>
+template <int D, int ROWS, bool ALIGNED>
 int attention_t(Args a, std::string* err, void* stream) {
-  using S = Shape<D, NT>;
+  using S = Shape<D, ROWS>;
   static std::atomic<int> ready[kMaxDevices];
   const int dev = current_device();
   if (dev < 0) {
@@ -858,7 +998,7 @@ int attention_t(Args a, std::string* err, void* stream) {
     return SV_ERR_CUDA;
   }
   const size_t most = S::kRing + S::kJoin + (kMaxSeqs + 1) * 8;
-  auto* kernel = attention_kernel<D, NT>;
+  auto* kernel = attention_kernel<D, ROWS, ALIGNED>;
   cudaError_t e;
   if (!ready[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
@@ -886,6 +1026,16 @@ int attention_t(Args a, std::string* err, void* stream) {
     if (e != cudaSuccess) return failed("kv4_attention launch", e, err);
   }
   return SV_OK;
+}
+
+// The fewest columns that hold a call's rows; a page that begins and ends with a tile needs one look-up a tile.
+template <int D>
+int attention_d(const Args& a, std::string* err, void* stream) {
+  const int rows = a.G * (a.K + 1);
+  const bool aligned = a.c.page_size % kTok == 0;
+  if (rows <= 4) return aligned ? attention_t<D, 4, true>(a, err, stream) : attention_t<D, 4, false>(a, err, stream);
+  if (rows <= 8) return aligned ? attention_t<D, 8, true>(a, err, stream) : attention_t<D, 8, false>(a, err, stream);
+  return aligned ? attention_t<D, 16, true>(a, err, stream) : attention_t<D, 16, false>(a, err, stream);
 }
 
 }  // namespace kv4
@@ -924,9 +1074,7 @@ int kv4_attention_launch(const Kv4AttentionLaunch& L, std::string* err) {
   a.flags = reinterpret_cast<uint32_t*>(ws);
   a.counters = reinterpret_cast<uint32_t*>(ws + kKv4Counters);
   a.parts = reinterpret_cast<float*>(ws + kKv4Counters + kv4::kMaxCtas * 4);
-  const bool wide = a.G * (L.K + 1) > 8;
-  if (L.D == 128) return wide ? kv4::attention_t<128, 2>(a, err, L.stream) : kv4::attention_t<128, 1>(a, err, L.stream);
-  return wide ? kv4::attention_t<64, 2>(a, err, L.stream) : kv4::attention_t<64, 1>(a, err, L.stream);
+  return L.D == 128 ? kv4::attention_d<128>(a, err, L.stream) : kv4::attention_d<64>(a, err, L.stream);
 }
 
 int kv4_rows_launch(const Kv4RowsLaunch& L, std::string* err) {
