@@ -625,6 +625,7 @@ sv_status sv_kv4_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_st
   if (workspace_bytes < sv::kv4_attention_workspace_bytes(K, Hq, Hkv, D))
     return fail(SV_ERR_WORKSPACE, "workspace smaller than sv_kv4_attention_workspace_size()");
   L.workspace = workspace;
+  L.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
   L.stream = stream;
   std::string err;
   const int s = sv::kv4_attention_launch(L, &err);

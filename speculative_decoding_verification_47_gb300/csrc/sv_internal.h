@@ -208,6 +208,7 @@ struct Kv4AttentionLaunch {
   int B, K, Hq, D;
   void* workspace;
   void* stream;
+  int wait_tries = kWaitTries;
 };
 
 // Enqueue the attention over the 4-bit cache.  Returns an sv_status; fills *err on failure.

@@ -230,10 +230,12 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTok = 16;           // tokens of a tile
 constexpr int kStages = 4;         // tiles of a warp on their way
 constexpr int kMaxSeqs = 1024;     // sequences of a launch
-constexpr int kMaxCtas = 1024;
-constexpr int kMinShare = 14;      // of a CTA
-// What a group costs beside its tiles, in tiles: Q, the join of the warps, the way to the next.
-constexpr int kGroupCost = 6;
+constexpr int kMaxCtas = 640;
+constexpr int kMaxWarps = kMaxCtas * kWarps;
+constexpr int kMinShare = 6;       // of a warp
+constexpr int kGroupCost = 2;      // what a group costs beside its tiles, in tiles: Q, the stores, the way to the next
+constexpr int kList = 16;          // segments that a warp looks up at a time
+constexpr int kJoin = 16;          // parts that are joined at once
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kNone = -3e38f;    // a reference before the first score
 
@@ -250,8 +252,9 @@ struct Args {
   float* lse;
   int B, K, Hq, Hkv, G;
   uint32_t* flags;
-  uint32_t* counters;  // [kMaxCtas]: finished parts of the group that a CTA's share ends in; 0 between calls
-  float* parts;        // [CTA][2][rows * (D + 2)]
+  uint32_t* counters;  // [2][kMaxWarps]: finished parts (and joins of kJoin parts) of cut groups; 0 between calls
+  float* parts;        // [warp][2][rows * (D + 2)]
+  long long clocks;    // of a wait for a copy; 0: none is waited for
 };
 
 // ROWS query rows a block: 4 (a column of the product is then a row and half of the tile's tokens
@@ -263,13 +266,10 @@ struct Shape {
   static constexpr int kRowBytes = D / 2;
   static constexpr int kTileBytes = 2 * kTok * kRowBytes + 2 * kTok * 4;  // K, V, (s, m) of both
   static constexpr int kRing = kWarps * kStages * kTileBytes;
-  // a row's numerators in float32, a word left out after each of a lane's runs, so that the lanes of a
-  // store (rows 2t, values 16g or 8g apart) meet 32 banks
-  static constexpr int kRun = D == 128 ? 16 : 8;
-  static constexpr int kPitch = D == 128 ? 148 : 84;
-  static constexpr int kJoin = kWarps * kRows * (kPitch + 2) * 4;
   static constexpr int kPart = kRows * (D + 2);  // floats of a part in memory
   static constexpr int kMinCtas = NT == 1 ? 4 : 3;
+  // shared memory beside the ring: lists, barriers, and the fragments of Q of two blocks of columns (bytes, about)
+  static constexpr int kStatic = 4600 + (NT == 1 ? 0 : kWarps * (NT * D * 16 + 128));
 };
 
 // One sequence: what its queries see, in tiles.
@@ -305,46 +305,64 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b, int rows) {
   return s;
 }
 
-// A CTA's run of tiles of one group (sequence b, key head h, block of query rows).
+// A warp's run of tiles of one group (sequence b, key head h, block of query rows).
 struct Segment {
   Seq s;
   int b, h, block, t0, t1;
   unsigned long long group;  // where the group begins, in units of a tile's cost
+
+  __device__ __forceinline__ int count() const { return s.bad || s.len + s.k == 0 ? 0 : t1 - t0; }
 };
 
-// The first run with tiles at or behind `at` (below `end`), which moves behind it.
-__device__ __forceinline__ bool next_segment(const Args& a, const unsigned long long* prefix, int rows,
-                                             unsigned long long& at, unsigned long long end, Segment& g) {
-  while (at < end) {
-    int lo = 0, hi = a.B - 1;  // the last b with prefix[b] <= at
+// Where the sequences' groups begin, by cost and by number.
+struct Books {
+  unsigned long long* cost;  // [B + 1]
+  uint32_t* groups;          // [B + 1]
+};
+
+// The number of the group that unit `at` lies in.
+__device__ __forceinline__ uint32_t group_at(const Args& a, const Books& k, int rows, unsigned long long at) {
+  int lo = 0, hi = a.B - 1;  // the last b with cost[b] <= at
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (k.cost[mid] <= at) lo = mid; else hi = mid - 1;
+  }
+  const unsigned long long off = at - k.cost[lo];
+  const uint32_t cost = (uint32_t)(seq_of(a, lo, rows).tiles + kGroupCost);
+  return k.groups[lo] + (off >> 32 ? (uint32_t)(off / cost) : (uint32_t)off / cost);
+}
+
+// The runs of the warp's share [begin, end) in the groups first .. first + kList - 1, a lane per group;
+// those without a tile are left out.  Returns their number.
+__device__ __forceinline__ int list_segments(const Args& a, const Books& k, int rows, uint32_t first,
+                                             unsigned long long begin, unsigned long long end, int lane, Segment* list) {
+  Segment g;
+  g.t0 = g.t1 = 0;
+  if (lane < kList && first + lane < k.groups[a.B]) {
+    const uint32_t number = first + lane;
+    int lo = 0, hi = a.B - 1;  // the last b with groups[b] <= number
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (prefix[mid] <= at) lo = mid; else hi = mid - 1;
+      if (k.groups[mid] <= number) lo = mid; else hi = mid - 1;
     }
     g.b = lo;
     g.s = seq_of(a, lo, rows);
-    const unsigned long long off = at - prefix[lo];
-    const uint32_t cost = (uint32_t)(g.s.tiles + kGroupCost);
-    const uint32_t group = off >> 32 ? (uint32_t)(off / cost) : (uint32_t)off / cost;
-    const int u0 = (int)(off - (unsigned long long)group * cost);
-    const int u1 = (int)min((unsigned long long)cost, u0 + (end - at));
-    g.group = at - u0;
+    const uint32_t group = number - k.groups[lo], cost = (uint32_t)(g.s.tiles + kGroupCost);
+    g.group = k.cost[lo] + (unsigned long long)group * cost;
     g.h = (int)(group / (uint32_t)g.s.blocks);
     g.block = (int)(group - (uint32_t)g.h * g.s.blocks);
-    g.t0 = max(0, u0 - kGroupCost);
-    g.t1 = max(0, u1 - kGroupCost);
-    at += u1 - u0;
-    if (g.t0 < g.t1) return true;
+    if (g.group < end) {
+      g.t0 = begin > g.group ? max(0, (int)(begin - g.group) - kGroupCost) : 0;
+      g.t1 = max(0, (int)min((unsigned long long)cost, end - g.group) - kGroupCost);
+    }
   }
-  return false;
+  const unsigned some = __ballot_sync(kFull, g.t0 < g.t1);
+  __syncwarp();  // (the list before is read no more)
+  if (g.t0 < g.t1) list[__popc(some & ((1u << lane) - 1u))] = g;
+  __syncwarp();
+  return __popc(some);
 }
 
-__device__ __forceinline__ void cp16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t to, const void* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
-}
 // zeros in place of what is not there
 __device__ __forceinline__ void cp16(uint32_t to, const void* from, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
@@ -402,85 +420,272 @@ __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
 
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
-// The loads of a warp's tiles: kWarps apart, each tile's page ids read while the one before is asked for.
+// The loads of a warp's tiles into its ring, in the order of the list's segments: they run ahead of the
+// products, over the ends of segments too.  A page of whole tiles has a tile's four pieces (codes and
+// (s, m) of K and V) as runs of bytes, one run if the page is a tile: bulk copies.  Lane l looks up and
+// asks for the l-th tile of a batch of 32 (or what the segment has left), so that a tile costs the warp a
+// dozen instructions (a copy per 16 bytes and lane: some fifty); the next batch's page ids are read
+// while one is asked for.
 template <int D, bool ALIGNED>
-struct Loader {
-  static constexpr int RB = D / 2, CHUNKS = RB / 16, COPIES = kTok * CHUNKS / 32;
-  const uint8_t* head;   // the pool's pages, at this segment's head
-  const int32_t* row;    // of the block table
-  int sink_tiles, skip, end, tile, last, page;  // page: of the next tile (this lane's token of it)
-  bool bad;
+struct Loader;
 
-  __device__ __forceinline__ int first_token(int t) const { return (t + (t < sink_tiles ? 0 : skip)) * kTok; }
-  __device__ __forceinline__ void look_up(const Cache& c, int lane) {
-    page = 0;
-    if (tile < last) {
-      const int tok = first_token(tile) + (ALIGNED ? 0 : lane & 15);
-      if (ALIGNED || tok < end) page = __ldg(row + divide(tok, c.by_page));
+template <int D>
+struct Loader<D, true> {
+  static constexpr int RB = D / 2;
+  static constexpr uint32_t TB = 2 * kTok * RB + 2 * kTok * 4;
+  const Segment* list;
+  uint64_t* bars;
+  uint32_t ring;         // of the warp
+  int segments;
+  uint32_t bad;          // a bit per segment: a page that is not there
+  int i, batch;          // tiles of the batch: asked for, all
+  const uint8_t* src;    // this lane's tile's K codes; NULL: a page that is not there
+  int words;             // from there to K's (s, m)
+  int next, base, page;  // the next batch: its segment, its first tile's number there, this lane's page
+  uint32_t asked, taken; // over all segments
+  bool dead;             // a wait ran out
+
+  __device__ __forceinline__ void init(const Segment* list_, uint64_t* bars_, uint32_t ring_, int lane) {
+    list = list_, bars = bars_, ring = ring_;
+    asked = taken = 0;
+    dead = false;
+    if (lane < kStages) mbar_init(bars + lane, 1);
+    fence_mbar_init();
+  }
+  __device__ __forceinline__ int token(const Segment& g, int lane) const {
+    const int tile = g.t0 + base + lane;
+    return (tile + (tile < g.s.sink_tiles ? 0 : g.s.skip)) * kTok;
+  }
+  __device__ __forceinline__ void look_up(const Args& a, int lane) {
+    while (next < segments && base >= list[next].count()) ++next, base = 0;
+    page = -1;
+    if (next < segments && base + lane < list[next].count()) {
+      const Segment& g = list[next];
+      page = a.c.table[(long long)g.b * a.c.max_pages + divide(token(g, lane), a.c.by_page)];
     }
   }
-  __device__ __forceinline__ void begin(const Cache& c, const Segment& g, int warp, int lane) {
-    head = c.pool + (long long)g.h * c.head_bytes;
-    row = c.table + (long long)g.b * c.max_pages;
-    sink_tiles = g.s.sink_tiles, skip = g.s.skip, end = g.s.bad ? 0 : g.s.len + g.s.k;
-    tile = g.t0 + warp, last = end > 0 ? g.t1 : 0;
-    bad = false;
-    look_up(c, lane);
+  __device__ __forceinline__ void begin(const Args& a, int segments_, int lane) {
+    segments = segments_;
+    bad = 0;
+    i = batch = next = base = 0;
+    look_up(a, lane);
   }
-  // one group of copies, an empty one behind the last tile
-  __device__ __forceinline__ void issue(const Cache& c, uint32_t buf, int lane) {
-    if (tile < last) {
-      const int tok0 = first_token(tile), here = page;
-      const int values = c.page_size * RB, words = c.page_size * D;
-      const uint32_t to = buf + lane / CHUNKS * RB + ((lane ^ (lane / CHUNKS >> 1)) & (CHUNKS - 1)) * 16;
-      tile += kWarps;
-      look_up(c, lane);
-      if constexpr (ALIGNED) {
-        const int slot = tok0 - divide(tok0, c.by_page) * c.page_size;
-        bool sound = (unsigned)here < (unsigned)c.num_pages;
-        bad = bad || !sound;
-        const uint8_t* base = head + (sound ? here : 0) * c.page_bytes;
-        const uint8_t* from = base + slot * RB + lane * 16;
-        const uint8_t* word = base + words + slot * 4 + (lane & 15) * 4 + (lane >= 16 ? c.page_size * 4 : 0);
-        if (tok0 + kTok <= end && sound) {
-#pragma unroll
-          for (int j = 0; j < COPIES; ++j) {
-            cp16(to + j * 512, from + j * 512);
-            cp16(to + kTok * RB + j * 512, from + values + j * 512);
-          }
-          cp4(buf + 2 * kTok * RB + lane * 4, word);
+  __device__ __forceinline__ void issue(const Args& a, int lane) {
+    if (dead) return;
+    if (i == batch) {
+      if (next >= segments) return;
+      const Segment& g = list[next];
+      batch = min(32, g.count() - base);
+      i = 0;
+      src = nullptr;
+      if (lane < batch) {
+        const int tok = token(g, lane), slot = tok - divide(tok, a.c.by_page) * a.c.page_size;
+        if ((unsigned)page < (unsigned)a.c.num_pages)
+          src = a.c.pool + page * a.c.page_bytes + (long long)g.h * a.c.head_bytes + slot * RB;
+        else
+          bad |= 1u << next;
+        words = a.c.page_size * D + slot * (4 - RB);
+      }
+      base += 32;
+      look_up(a, lane);
+    }
+    if (lane == i) {
+      const uint32_t slot = asked & (kStages - 1), to = ring + slot * TB;
+      uint64_t* bar = bars + slot;
+      if (src) {
+        mbar_arrive_expect_tx(bar, TB);
+        if (a.c.page_size == kTok) {
+          bulk(to, src, TB, bar);
         } else {
-          const int there = sound ? end - tok0 : 0;
-#pragma unroll
-          for (int j = 0; j < COPIES; ++j) {
-            cp16(to + j * 512, from + j * 512, (lane + 32 * j) / CHUNKS < there);
-            cp16(to + kTok * RB + j * 512, from + values + j * 512, (lane + 32 * j) / CHUNKS < there);
-          }
-          cp4(buf + 2 * kTok * RB + lane * 4, word, (lane & 15) < there);
+          bulk(to, src, kTok * RB, bar);
+          bulk(to + kTok * RB, src + a.c.page_size * RB, kTok * RB, bar);
+          bulk(to + 2 * kTok * RB, src + words, kTok * 4, bar);
+          bulk(to + 2 * kTok * RB + kTok * 4, src + words + a.c.page_size * 4, kTok * 4, bar);
         }
       } else {
-        const int tok = tok0 + (lane & 15);
-        long long at = -1;  // of this lane's token's codes
-        int slot = 0;
-        if (tok < end) {
-          slot = tok - divide(tok, c.by_page) * c.page_size;
-          if ((unsigned)here < (unsigned)c.num_pages) at = here * c.page_bytes + slot * RB;
-          else bad = true;
-        }
-#pragma unroll
-        for (int j = 0; j < COPIES; ++j) {
-          const long long from = __shfl_sync(kFull, at, (lane + 32 * j) / CHUNKS);
-          const uint8_t* src = head + (from < 0 ? 0 : from) + lane % CHUNKS * 16;
-          cp16(to + j * 512, src, from >= 0);
-          cp16(to + kTok * RB + j * 512, src + values, from >= 0);
-        }
-        const uint8_t* word = head + (at < 0 ? 0 : at - slot * RB) + words + slot * 4 + (lane >= 16 ? c.page_size * 4 : 0);
-        cp4(buf + 2 * kTok * RB + lane * 4, word, at >= 0);
+        mbar_arrive(bar);
       }
+    }
+    ++i, ++asked;
+  }
+  static __device__ __forceinline__ void bulk(uint32_t to, const uint8_t* from, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                 "l"(from), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+  }
+  // the next tile, once it is there
+  __device__ __forceinline__ uint32_t take(const Args& a) {
+    const uint32_t slot = taken & (kStages - 1);
+    if (!dead) {
+      const bool ok = a.clocks > 0 && tc::wait_bounded(bars + slot, taken / kStages & 1, a.clocks);
+      dead = !__all_sync(kFull, ok);
+    }
+    if (!dead) ++taken;
+    return ring + slot * TB;
+  }
+  // copies of a ring that was given up come to their end before the CTA does
+  __device__ __forceinline__ void leave() {
+    if (dead)
+      for (; taken != asked; ++taken) tc::wait_bounded(bars + (taken & (kStages - 1)), taken / kStages & 1);
+  }
+};
+
+// Pages of any size: a copy per 16 bytes (and per (s, m)), each from its token's own page.  One group of
+// copies a call, an empty one behind the last tile.
+template <int D>
+struct Loader<D, false> {
+  static constexpr int RB = D / 2, CHUNKS = RB / 16, COPIES = kTok * CHUNKS / 32;
+  static constexpr uint32_t TB = 2 * kTok * RB + 2 * kTok * 4;
+  const Segment* list;
+  uint32_t ring;
+  int segments;
+  uint32_t bad;
+  int next, base, page;  // the next tile: its segment, its number there, the page of this lane's token
+  uint32_t asked, taken;
+  bool dead;
+
+  __device__ __forceinline__ void init(const Segment* list_, uint64_t*, uint32_t ring_, int) {
+    list = list_, ring = ring_;
+    asked = taken = 0;
+    dead = false;
+  }
+  // this lane's token of the next tile; -1 if no query sees it
+  __device__ __forceinline__ int token(const Args& a, const Segment& g, int lane) const {
+    const int tile = g.t0 + base;
+    const int tok = (tile + (tile < g.s.sink_tiles ? 0 : g.s.skip)) * kTok + (lane & 15);
+    return tok < g.s.len + g.s.k && (a.window <= 0 || tok >= g.s.len - a.window || tok < a.sinks) ? tok : -1;
+  }
+  __device__ __forceinline__ void look_up(const Args& a, int lane) {
+    while (next < segments && base >= list[next].count()) ++next, base = 0;
+    page = -1;
+    if (next < segments) {
+      const int tok = token(a, list[next], lane);
+      if (tok >= 0) page = a.c.table[(long long)list[next].b * a.c.max_pages + divide(tok, a.c.by_page)];
+    }
+  }
+  __device__ __forceinline__ void begin(const Args& a, int segments_, int lane) {
+    segments = segments_;
+    bad = 0;
+    next = base = 0;
+    look_up(a, lane);
+  }
+  __device__ __forceinline__ void issue(const Args& a, int lane) {
+    if (next < segments) {
+      const Segment& g = list[next];
+      const int tok = token(a, g, lane), values = a.c.page_size * RB;
+      const uint8_t* head = a.c.pool + (long long)g.h * a.c.head_bytes;
+      const uint32_t buf = ring + (asked & (kStages - 1)) * TB, to = buf + lane * 16;
+      long long at = -1;  // of this lane's token's codes
+      int slot = 0;
+      if (tok >= 0) {
+        slot = tok - divide(tok, a.c.by_page) * a.c.page_size;
+        if ((unsigned)page < (unsigned)a.c.num_pages) at = page * a.c.page_bytes + slot * RB;
+        else bad |= 1u << next;
+      }
+      ++base, ++asked;
+      look_up(a, lane);
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j) {
+        const long long from = __shfl_sync(kFull, at, (lane + 32 * j) / CHUNKS);
+        const uint8_t* src = head + (from < 0 ? 0 : from) + lane % CHUNKS * 16;
+        cp16(to + j * 512, src, from >= 0);
+        cp16(to + kTok * RB + j * 512, src + values, from >= 0);
+      }
+      const uint8_t* word =
+          head + (at < 0 ? 0 : at - slot * RB) + a.c.page_size * D + slot * 4 + (lane >= 16 ? a.c.page_size * 4 : 0);
+      cp4(buf + 2 * kTok * RB + lane * 4, word, at >= 0);
     }
     cp_commit();
   }
+  __device__ __forceinline__ uint32_t take(const Args&) {
+    cp_wait<kStages - 1>();
+    __syncwarp();
+    return ring + (taken++ & (kStages - 1)) * TB;
+  }
+  __device__ __forceinline__ void leave() { cp_wait<0>(); }
 };
+
+// What a lane reads of Q: row r of the segment's block (key head's queries of a position, then the next
+// position's), a quarter of it.
+template <int D>
+__device__ __forceinline__ void load_q(const Args& a, const Segment& g, int rows, int row0, int r, int t, uint4 (&v)[D / 32]) {
+  if (r < rows && !g.s.bad) {
+    const int i = (row0 + r) / a.G, head = g.h * a.G + (row0 + r) % a.G;
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + g.b * a.q_seq + i * a.q_pos + head * a.q_head + t * (D / 4));
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) v[w] = __ldg(src + w);
+  } else {
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) v[w] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Where a warp's part of a group lies: the first of a group that began in front of the warp's share, the
+// second of one that begins inside it.
+template <int PART>
+__device__ __forceinline__ float* part_of(const Args& a, unsigned warp, unsigned long long share, unsigned long long group) {
+  return a.parts + ((long long)warp * 2 + (warp * share >= group ? 0 : 1)) * PART;
+}
+
+// The parts of the warps first, first + step, .. (n of them) joined, a row at a time: numerators of the
+// lane's D / 32 values, the sum and the reference.  In the order of the warps.
+template <int D, int ROWS, typename Put>
+__device__ __forceinline__ void join_parts(const Args& a, unsigned first, unsigned step, int n, unsigned long long share,
+                                           unsigned long long group, int rows, int lane, Put put) {
+  constexpr int PART = ROWS * (D + 2), W = D / 32;
+  for (int r = 0; r < rows; ++r) {
+    float top = kNone, l = 0.f, num[W] = {};
+    for (int c = 0; c < n; c += kJoin) {
+      const int m = min(kJoin, n - c);
+      float ref = kNone, sum = 0.f;
+      if (lane < m) {
+        const float* p = part_of<PART>(a, first + (c + lane) * step, share, group) + ROWS * D;
+        ref = __ldcg(p + r);
+        sum = __ldcg(p + ROWS + r);
+      }
+      float most = fmaxf(ref, top);
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, k));
+      const float old = ex2(top - most), f = ex2(ref - most);
+      sum *= f;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(kFull, sum, k);
+      top = most;
+      l = __fmaf_rn(l, old, sum);
+#pragma unroll
+      for (int e = 0; e < W; ++e) num[e] *= old;
+#pragma unroll 4
+      for (int j = 0; j < m; ++j) {
+        const float fj = __shfl_sync(kFull, f, j);
+        const float* p = part_of<PART>(a, first + (c + j) * step, share, group) + r * D + lane * W;
+        if constexpr (W == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+          num[0] = __fmaf_rn(v.x, fj, num[0]), num[1] = __fmaf_rn(v.y, fj, num[1]);
+          num[2] = __fmaf_rn(v.z, fj, num[2]), num[3] = __fmaf_rn(v.w, fj, num[3]);
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
+          num[0] = __fmaf_rn(v.x, fj, num[0]), num[1] = __fmaf_rn(v.y, fj, num[1]);
+        }
+      }
+    }
+    put(r, top, l, num);
+  }
+}
+
+// One more of `all` is done (with what the warp wrote before); true if it was the last, which leaves 0.
+__device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t all, int lane) {
+  __syncwarp();
+  uint32_t before = 0;
+  if (lane == 0) {
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    if (before == all - 1) *counter = 0;
+  }
+  return __shfl_sync(kFull, before, 0) == all - 1;
+}
+
+__device__ __forceinline__ float log_of_sum(float top, float l) {
+  return l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+}
 
 template <int D, int ROWS, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_kernel(const __grid_constant__ Args a) {
@@ -492,88 +697,97 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
   constexpr int TILES = D / 16;         // 16-row tiles of O^T
   constexpr uint32_t TB = S::kTileBytes;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* join = reinterpret_cast<float*>(smem + S::kRing);                   // [warp][row][pitch]
-  float* join_r = join + kWarps * S::kRows * S::kPitch;                      // [warp][row]
-  float* join_l = join_r + kWarps * S::kRows;
-  unsigned long long* prefix = reinterpret_cast<unsigned long long*>(smem + S::kRing + S::kJoin);  // [B + 1]
-  __shared__ unsigned long long warp_sum[kWarps];
-  __shared__ uint32_t bad_of_cta, last_of_group;
+  Books books;
+  books.cost = reinterpret_cast<unsigned long long*>(smem + S::kRing);
+  books.groups = reinterpret_cast<uint32_t*>(books.cost + a.B + 1);
+  __shared__ unsigned long long warp_cost[kWarps];
+  __shared__ uint32_t warp_groups[kWarps];
+  __shared__ Segment lists[kWarps][kList];
+  __shared__ uint64_t bars[kWarps][kStages];
+  __shared__ uint2 q_frags[NT == 1 ? 1 : kWarps][NT == 1 ? 1 : NT * 2 * WK * 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  // the columns of the product whose scores the lane holds: col0, col0 + 1, for tokens g (+ 8)
-  const int col0 = HALF ? 2 * (t & 1) : 2 * t, tok_of = HALF ? g + (t >> 1) * 8 : g;
+  // row g of a product stands for token `tau` of its 8: pairs of rows (2t, 2t + 1), which a lane reads
+  // V's codes of, are tokens t and t + 4, so that the four t's rows lie beside each other
+  const int tau = (g >> 1) + (g & 1) * 4;
+  // the columns of the product whose scores the lane holds: col0, col0 + 1, for tokens tok_of (+ 8)
+  const int col0 = HALF ? 2 * (t & 1) : 2 * t, tok_of = HALF ? tau + (t >> 1) * 8 : tau;
+  Segment* list = lists[warp];
+  uint2* q_frag = q_frags[NT == 1 ? 0 : warp];
+  const uint32_t q_at = smem_addr(q_frag) + lane * 8;
+  Loader<D, ALIGNED> ld;
+  ld.init(list, bars[warp], smem_addr(smem) + warp * kStages * TB, lane);
   pdl_wait();
 
-  // the groups in a row, each as long as its tiles and kGroupCost: prefix[b] is where sequence b's begin
+  // the groups in a row, each as long as its tiles and kGroupCost
   {
     const int each = (a.B + kThreads - 1) / kThreads;
-    unsigned long long mine = 0;
+    unsigned long long cost = 0;
+    uint32_t groups = 0;
     for (int j = 0; j < each; ++j) {
       const int b = tid * each + j;
       if (b < a.B) {
         const Seq s = seq_of(a, b, S::kRows);
-        mine += (unsigned long long)(s.tiles + kGroupCost) * s.blocks * a.Hkv;
-        prefix[b + 1] = mine;  // (within this thread's run)
+        groups += (uint32_t)s.blocks * a.Hkv;
+        cost += (unsigned long long)(s.tiles + kGroupCost) * s.blocks * a.Hkv;
+        books.cost[b + 1] = cost;  // (within this thread's run)
+        books.groups[b + 1] = groups;
       }
     }
-    unsigned long long up = mine;
+    unsigned long long up = cost;
+    uint32_t up_groups = groups;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const unsigned long long v = __shfl_up_sync(kFull, up, m);
-      if (lane >= m) up += v;
+      const uint32_t w = __shfl_up_sync(kFull, up_groups, m);
+      if (lane >= m) up += v, up_groups += w;
     }
-    if (lane == 31) warp_sum[warp] = up;
+    if (lane == 31) warp_cost[warp] = up, warp_groups[warp] = up_groups;
     __syncthreads();
-    unsigned long long before = up - mine;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    up -= cost, up_groups -= groups;
+    for (int w = 0; w < warp; ++w) up += warp_cost[w], up_groups += warp_groups[w];
     for (int j = 0; j < each; ++j) {
       const int b = tid * each + j;
-      if (b < a.B) prefix[b + 1] += before;
+      if (b < a.B) books.cost[b + 1] += up, books.groups[b + 1] += up_groups;
     }
-    if (tid == 0) prefix[0] = 0;
+    if (tid == 0) books.cost[0] = books.groups[0] = 0;
     __syncthreads();
   }
-  const unsigned long long total = prefix[a.B];
-  unsigned long long share = (total + gridDim.x - 1) / gridDim.x;
+  // the share of this warp; from here on the warps go their own ways
+  const unsigned worker = blockIdx.x * kWarps + warp;
+  const unsigned long long total = books.cost[a.B];
+  unsigned long long share = (total + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);
   if (share < kMinShare) share = kMinShare;
-  const unsigned long long begin = blockIdx.x * share, end = min(begin + share, total);
-  const uint32_t ring = smem_addr(smem) + warp * kStages * TB;
+  const unsigned long long begin = worker * share, end = min(begin + share, total);
+  if (begin >= end) return;
 
-  unsigned long long at = begin;
-  Segment sg, next;
-  Loader<D, ALIGNED> ld;
-  bool more = next_segment(a, prefix, S::kRows, at, end, next);
-  if (more) {
-    ld.begin(a.c, next, warp, lane);
-#pragma unroll
-    for (int st = 0; st < kStages - 1; ++st) ld.issue(a.c, ring + st * TB, lane);
-  }
-  while (more) {
-    sg = next;
-    const Seq& s = sg.s;
+  const uint32_t last_group = group_at(a, books, S::kRows, end - 1);
+#pragma unroll 1
+  for (uint32_t first = group_at(a, books, S::kRows, begin); first <= last_group; first += kList) {
+  const int segments = list_segments(a, books, S::kRows, first, begin, end, lane, list);
+  ld.begin(a, segments, lane);
+#pragma unroll 1
+  for (int st = 0; st < kStages - 1; ++st) ld.issue(a, lane);
+#pragma unroll 1
+  for (int at = 0; at < segments; ++at) {
+    const Segment& sg = list[at];
+    const Seq s = sg.s;
     const int row0 = sg.block * S::kRows, rows = min(S::kRows, a.G * (s.k + 1) - row0);
 
-    // Q's rows in fp16 next to 2^15, in the order of the codes' halves
-    uint32_t qf[NT][2 * WK][2];
+    // Q's rows in fp16 next to 2^15, in the order of the codes' halves; those of two blocks of columns stay
+    // in shared memory (32 registers less)
+    uint32_t qf[2 * WK][2];
     F2 fr[NT], sq[NT];     // of the lane's columns: score = s (acc fr) + m sq
     int limit[NT][2];      // the first token that the column's query does not see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
-      uint4 v[WK];
-#pragma unroll
-      for (int w = 0; w < WK; ++w) v[w] = make_uint4(0, 0, 0, 0);
-      if (r < rows && !s.bad) {
-        const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + sg.b * a.q_seq + i * a.q_pos + head * a.q_head + t * (D / 4));
-#pragma unroll
-        for (int w = 0; w < WK; ++w) v[w] = __ldg(src + w);
-      }
+      uint4 qv[WK];
+      load_q<D>(a, sg, rows, row0, nt * 8 + g, t, qv);
       uint32_t top = 0;
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < WK; ++w) {
-        const uint32_t u[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
+        const uint32_t u[4] = {qv[w].x, qv[w].y, qv[w].z, qv[w].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           top = max(top, max(u[e] & 0x7fffu, (u[e] >> 16) & 0x7fffu));
@@ -591,15 +805,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
       const float f16 = f * 0.0625f;
 #pragma unroll
       for (int w = 0; w < WK; ++w) {
-        const uint4 u = v[w];  // values 0 1 | 2 3 | 4 5 | 6 7
-        qf[nt][2 * w][0] = half2_of(bf16_lo(u.x) * f, bf16_lo(u.z) * f);
-        qf[nt][2 * w][1] = half2_of(bf16_hi(u.x) * f16, bf16_hi(u.z) * f16);
-        qf[nt][2 * w + 1][0] = half2_of(bf16_lo(u.y) * f, bf16_lo(u.w) * f);
-        qf[nt][2 * w + 1][1] = half2_of(bf16_hi(u.y) * f16, bf16_hi(u.w) * f16);
+        const uint4 u = qv[w];  // values 0 1 | 2 3 | 4 5 | 6 7
+        qf[2 * w][0] = half2_of(bf16_lo(u.x) * f, bf16_lo(u.z) * f);
+        qf[2 * w][1] = half2_of(bf16_hi(u.x) * f16, bf16_hi(u.z) * f16);
+        qf[2 * w + 1][0] = half2_of(bf16_lo(u.y) * f, bf16_lo(u.w) * f);
+        qf[2 * w + 1][1] = half2_of(bf16_hi(u.y) * f16, bf16_hi(u.w) * f16);
       }
       const float mine_fr = a.scale * __uint_as_float((uint32_t)(254 - fb) << 23) * 16777216.f, mine_sq = a.scale * sum;
       fr[nt] = f2_pack(__shfl_sync(kFull, mine_fr, col0 * 4), __shfl_sync(kFull, mine_fr, col0 * 4 + 4));
       sq[nt] = f2_pack(__shfl_sync(kFull, mine_sq, col0 * 4), __shfl_sync(kFull, mine_sq, col0 * 4 + 4));
+      if constexpr (NT > 1) {
+#pragma unroll
+        for (int w = 0; w < 2 * WK; ++w) q_frag[(nt * 2 * WK + w) * 32 + lane] = make_uint2(qf[w][0], qf[w][1]);  // (read by this lane alone)
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int col = nt * 8 + col0 + j;
@@ -620,13 +838,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
     }
 
     {
-      uint32_t stage = 0;
-      const int t1 = s.bad ? 0 : sg.t1;
-      for (int tile = sg.t0 + warp; tile < t1; tile += kWarps) {
-        const uint32_t buf = ring + stage * TB;
-        ld.issue(a.c, ring + ((stage + kStages - 1) & (kStages - 1)) * TB, lane);
-        cp_wait<kStages - 1>();
-        __syncwarp();
+      const int n = sg.count();
+      int tile = sg.t0;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j, ++tile) {
+        ld.issue(a, lane);
+        const uint32_t buf = ld.take(a);
 
         const int tok0 = (tile + (tile < s.sink_tiles ? 0 : s.skip)) * kTok;
         uint32_t kw[TP], vw[TP];
@@ -636,30 +853,38 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
           vw[e] = lds32(buf + 2 * kTok * RB + 64 + (tok_of + 8 * e) * 4);
         }
 
-        // S^T: tokens g and g + 8 by columns 2t and 2t + 1
+        // S^T: tokens tau and tau + 8 by columns 2t and 2t + 1
         float acc[NT][4] = {};
         {
           uint32_t x[WK], y[WK];
           if constexpr (D == 128) {
-            const uint4 p = lds128(buf + g * RB + ((t ^ (g >> 1)) & 3) * 16);
-            const uint4 r = lds128(buf + (g + 8) * RB + ((t ^ (g >> 1)) & 3) * 16);
+            const uint4 p = lds128(buf + tau * RB + t * 16), r = lds128(buf + (tau + 8) * RB + t * 16);
             x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w;
             y[0] = r.x, y[1] = r.y, y[2] = r.z, y[3] = r.w;
           } else {
-            const uint2 p = lds64(buf + g * RB + (((t >> 1) ^ (g >> 1)) & 1) * 16 + (t & 1) * 8);
-            const uint2 r = lds64(buf + (g + 8) * RB + (((t >> 1) ^ (g >> 1)) & 1) * 16 + (t & 1) * 8);
+            const uint2 p = lds64(buf + tau * RB + t * 8), r = lds64(buf + (tau + 8) * RB + t * 8);
             x[0] = p.x, x[1] = p.y;
             y[0] = r.x, y[1] = r.y;
           }
 #pragma unroll
           for (int w = 0; w < WK; ++w) {
             const uint32_t x8 = x[w] >> 8, y8 = y[w] >> 8;
+            uint2 b0[NT], b1[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (NT == 1) {
+                b0[nt] = make_uint2(qf[2 * w][0], qf[2 * w][1]);
+                b1[nt] = make_uint2(qf[2 * w + 1][0], qf[2 * w + 1][1]);
+              } else {
+                b0[nt] = lds64(q_at + (nt * 2 * WK + 2 * w) * 256);
+                b1[nt] = lds64(q_at + (nt * 2 * WK + 2 * w + 1) * 256);
+              }
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16(acc[nt], x[w] & kLow, y[w] & kLow, x[w] & kHigh, y[w] & kHigh, qf[nt][2 * w][0], qf[nt][2 * w][1]);
+              mma_f16(acc[nt], x[w] & kLow, y[w] & kLow, x[w] & kHigh, y[w] & kHigh, b0[nt].x, b0[nt].y);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(acc[nt], x8 & kLow, y8 & kLow, x8 & kHigh, y8 & kHigh, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], x8 & kLow, y8 & kLow, x8 & kHigh, y8 & kHigh, b1[nt].x, b1[nt].y);
           }
         }
 
@@ -671,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             F2 c;
-            if constexpr (HALF) {  // tokens g + 8 to the lanes of the columns that have no row
+            if constexpr (HALF) {  // tokens tau + 8 to the lanes of the columns that have no row
               const float c2 = __shfl_xor_sync(kFull, acc[nt][2], 2), c3 = __shfl_xor_sync(kFull, acc[nt][3], 2);
               c = f2_pack(t < 2 ? acc[nt][0] : c2, t < 2 ? acc[nt][1] : c3);
             } else {
@@ -783,13 +1008,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
           }
         }
 
-        // O^T: pairs of tokens (2t, 2t + 1), (2t + 8, 2t + 9), this lane's codes of each
+        // O^T: pairs of tokens (t, t + 4), (t + 8, t + 12), this lane's codes of each
         const uint32_t vb = buf + kTok * RB;
         if constexpr (D == 128) {
           uint2 w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            w[e] = lds64(vb + (2 * t + (e & 1) + (e >> 1) * 8) * RB + (((g >> 1) ^ t) & 3) * 16 + (g & 1) * 8);
+            w[e] = lds64(vb + (t + 4 * e) * RB + g * 8);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const uint32_t sel = hf ? 0x7632u : 0x5410u;
@@ -809,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            w[e] = lds32(vb + (2 * t + (e & 1) + (e >> 1) * 8) * RB + (((g >> 2) ^ t) & 1) * 16 + (g & 3) * 4);
+            w[e] = lds32(vb + (t + 4 * e) * RB + g * 4);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const uint32_t sel = hf ? 0x7632u : 0x5410u;
@@ -824,150 +1049,111 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
           }
         }
         __syncwarp();
-        stage = (stage + 1) & (kStages - 1);
       }
-      cp_wait<0>();  // (empty groups)
-      __syncwarp();
-    }
-    const bool bad_page = ld.bad;
-
-    // the next segment's first tiles are on their way while this one's warps are joined
-    more = next_segment(a, prefix, S::kRows, at, end, next);
-    if (more) {
-      ld.begin(a.c, next, warp, lane);
-#pragma unroll
-      for (int st = 0; st < kStages - 1; ++st) ld.issue(a.c, ring + st * TB, lane);
     }
 
-    if (tid == 0) bad_of_cta = 0;
-    __syncthreads();  // (also: the join's words of the segment before have been read)
-    if (s.bad || bad_page) bad_of_cta = 1;
-    if (tid == 0 && s.bad && sg.group == prefix[sg.b]) atomicOr(a.flags, s.bad);
-    if (bad_page) atomicOr(a.flags, SV_FLAG_BAD_PAGE);
-    float sums[NT][2], lows[NT][2];
+    // the lanes' sums joined: all lanes of a column hold them
+    const bool bad = s.bad || ld.dead || __any_sync(kFull, ld.bad >> at & 1);
+    if (lane == 0 && s.bad && sg.group == books.cost[sg.b]) atomicOr(a.flags, s.bad);
+    if (lane == 0 && bad && !s.bad && !ld.dead) atomicOr(a.flags, SV_FLAG_BAD_PAGE);
+    const bool whole = sg.t0 == 0 && sg.t1 == s.tiles;
+    float* part = part_of<S::kPart>(a, worker, share, sg.group);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      f2_unpack(sum[nt], sums[nt][0], sums[nt][1]);
-      f2_unpack(low[nt], lows[nt][0], lows[nt][1]);
+      float l[2], add[2];
+      f2_unpack(sum[nt], l[0], l[1]);
+      f2_unpack(low[nt], add[0], add[1]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int d = HALF ? 2 : 4; d < 32; d <<= 1) {
-          sums[nt][j] += __shfl_xor_sync(kFull, sums[nt][j], d);
-          lows[nt][j] += __shfl_xor_sync(kFull, lows[nt][j], d);
+          l[j] += __shfl_xor_sync(kFull, l[j], d);
+          add[j] += __shfl_xor_sync(kFull, add[j], d);
         }
-        if (g == 0) join_r[warp * S::kRows + nt * 8 + col0 + j] = ref[nt][j];
-      }
-    }
-    __syncthreads();
-    const bool bad = bad_of_cta != 0;
+        if (bad) l[j] = __uint_as_float(0x7fc00000u);
+        const int r = nt * 8 + 2 * t + j;
+        if (r >= rows || (HALF && t >= 2)) continue;
+        // the codes' subnormals undone; D = 128: odd values stand 4 bits up; D = 64: the second row of a tile does
+        float even = ex2(vref[nt][j] - ref[nt][j]), inv = 1.f;
+        if (whole) inv = l[j] == 0.f ? 0.f : __frcp_rn(l[j]);
+        float x[TILES], y[TILES];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = nt * 8 + col0 + j;
-        float top = join_r[r];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, join_r[w * S::kRows + r]);
-        const float scale = ex2(ref[nt][j] - top);
-        if (g == 0) join_l[warp * S::kRows + r] = sums[nt][j] * scale;
-        const float add = lows[nt][j] * scale;
-        const float even = ex2(vref[nt][j] - ref[nt][j]) * scale;
-        float* to = join + (warp * S::kRows + r) * S::kPitch;
-        if (!HALF || t < 2) {
-#pragma unroll
-          for (int n = 0; n < TILES; ++n) {
-            const int d0 = D == 128 ? 16 * g + n : 8 * g + 2 * n, d1 = D == 128 ? d0 + 8 : d0 + 1;
-            // the codes' subnormals undone; D = 128: odd values stand 4 bits up; D = 64: the second row of a tile does
-            const float u0 = D == 128 && (n & 1) ? 0x1p20f : 0x1p24f, u1 = D == 128 ? u0 : 0x1p20f;
-            to[d0 + d0 / S::kRun] = __fmaf_rn(o[nt][n][j] * u0, even, add);
-            to[d1 + d1 / S::kRun] = __fmaf_rn(o[nt][n][2 + j] * u1, even, add);
+        for (int n = 0; n < TILES; ++n) {
+          const float u0 = D == 128 && (n & 1) ? 0x1p20f : 0x1p24f, u1 = D == 128 ? u0 : 0x1p20f;
+          x[n] = __fmaf_rn(o[nt][n][j] * u0, even, add[j]) * inv;
+          y[n] = __fmaf_rn(o[nt][n][2 + j] * u1, even, add[j]) * inv;
+        }
+        // this lane's run of the row: 16g .. 16g + 15 (x, then y), or 8g .. 8g + 7 (in turn)
+        if (whole) {
+          const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
+          uint4* to = reinterpret_cast<uint4*>(a.out + sg.b * a.o_seq + i * a.o_pos + head * a.o_head + g * (D / 8));
+          if constexpr (D == 128) {
+            to[0] = make_uint4(tc::pack_bf16x2(x[0], x[1]), tc::pack_bf16x2(x[2], x[3]), tc::pack_bf16x2(x[4], x[5]),
+                               tc::pack_bf16x2(x[6], x[7]));
+            to[1] = make_uint4(tc::pack_bf16x2(y[0], y[1]), tc::pack_bf16x2(y[2], y[3]), tc::pack_bf16x2(y[4], y[5]),
+                               tc::pack_bf16x2(y[6], y[7]));
+          } else {
+            to[0] = make_uint4(tc::pack_bf16x2(x[0], y[0]), tc::pack_bf16x2(x[1], y[1]), tc::pack_bf16x2(x[2], y[2]),
+                               tc::pack_bf16x2(x[3], y[3]));
           }
-        }
-      }
-    __syncthreads();
-
-    const bool whole = sg.t0 == 0 && sg.t1 == s.tiles;
-    // its place among the CTA's parts: the first of a group that began in front of the CTA's share
-    const bool early = begin >= sg.group;
-    float* part = a.parts + ((long long)blockIdx.x * 2 + (early ? 0 : 1)) * S::kPart;
-    for (int x = tid; x < rows * (D / 2); x += kThreads) {
-      const int r = x / (D / 2), d = (x % (D / 2)) * 2;
-      float n0 = 0.f, n1 = 0.f, l = 0.f, top = kNone;
+          if (g == 0 && a.lse)
+            a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] = log_of_sum(ref[nt][j], l[j]);
+        } else {
+          float2* to = reinterpret_cast<float2*>(part + r * D + g * (D / 8));
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float* from = join + (w * S::kRows + r) * S::kPitch + d + d / S::kRun;
-        n0 += from[0];
-        n1 += from[1];
-        l += join_l[w * S::kRows + r];
-        top = fmaxf(top, join_r[w * S::kRows + r]);
-      }
-      if (bad) l = __uint_as_float(0x7fc00000u);
-      if (whole) {
-        const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
-        const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-        *reinterpret_cast<uint32_t*>(a.out + sg.b * a.o_seq + i * a.o_pos + head * a.o_head + d) =
-            tc::pack_bf16x2(n0 * inv, n1 * inv);
-        if (d == 0 && a.lse)
-          a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] =
-              l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
-      } else {
-        *reinterpret_cast<float2*>(part + r * D + d) = make_float2(n0, n1);
-        if (d == 0) {
-          part[S::kRows * D + r] = top;
-          part[S::kRows * (D + 1) + r] = l;
+          for (int n = 0; n < TILES / 2; ++n) {
+            if constexpr (D == 128) {
+              to[n] = make_float2(x[2 * n], x[2 * n + 1]);
+              to[n + 4] = make_float2(y[2 * n], y[2 * n + 1]);
+            } else {
+              to[2 * n] = make_float2(x[2 * n], y[2 * n]);
+              to[2 * n + 1] = make_float2(x[2 * n + 1], y[2 * n + 1]);
+            }
+          }
+          if (g == 0) {
+            part[S::kRows * D + r] = ref[nt][j];
+            part[S::kRows * (D + 1) + r] = l[j];
+          }
         }
       }
     }
     if (!whole) {
-      // the last of the group's CTAs joins its parts
-      const unsigned first = (unsigned)((sg.group + kGroupCost) / share);
-      const unsigned last = (unsigned)((sg.group + kGroupCost + s.tiles - 1) / share);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const uint32_t before = atomicAdd(a.counters + first, 1u);
-        last_of_group = before == last - first;
-        if (last_of_group) {
-          a.counters[first] = 0;
-          __threadfence();
-        }
-      }
-      __syncthreads();
-      if (last_of_group) {
-        constexpr int PER = kThreads / S::kRows, W = D / PER;  // threads of a row, values of a thread
-        const int r = tid / PER, d0 = (tid % PER) * W;
-        const bool first_is_early = (unsigned long long)first * share >= sg.group;
-        auto part_of = [&](unsigned c) {
-          return a.parts + ((long long)c * 2 + (c == first && !first_is_early ? 1 : 0)) * S::kPart;
-        };
-        if (r < rows) {
-          float top = kNone;
-          for (unsigned c = first; c <= last; ++c) top = fmaxf(top, __ldcg(part_of(c) + S::kRows * D + r));
-          float l = 0.f, n[W] = {};
-          for (unsigned c = first; c <= last; ++c) {
-            const float* p = part_of(c);
-            const float f = ex2(__ldcg(p + S::kRows * D + r) - top);
-            l = __fmaf_rn(__ldcg(p + S::kRows * (D + 1) + r), f, l);
+      // the last warp of kJoin neighbours joins their parts into its first's, the last of these writes the result
+      const unsigned w0 = (unsigned)((sg.group + kGroupCost) / share);
+      const unsigned w1 = (unsigned)((sg.group + kGroupCost + s.tiles - 1) / share);
+      const unsigned blocks = (w1 - w0) / kJoin + 1, mine = w0 + (worker - w0) / kJoin * kJoin;
+      const int n = (int)min((unsigned)kJoin, w1 - mine + 1);
+      auto finish = [&](int r, float top, float l, const float (&num)[D / 32]) {
+        const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
+        const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+        uint32_t* to = reinterpret_cast<uint32_t*>(a.out + sg.b * a.o_seq + i * a.o_pos + head * a.o_head + lane * (D / 32));
 #pragma unroll
-            for (int e = 0; e < W; e += 2) {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(p + r * D + d0 + e));
-              n[e] = __fmaf_rn(v.x, f, n[e]);
-              n[e + 1] = __fmaf_rn(v.y, f, n[e + 1]);
-            }
-          }
-          const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
-          const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-          uint32_t* to = reinterpret_cast<uint32_t*>(a.out + sg.b * a.o_seq + i * a.o_pos + head * a.o_head + d0);
+        for (int e = 0; e < D / 64; ++e) to[e] = tc::pack_bf16x2(num[2 * e] * inv, num[2 * e + 1] * inv);
+        if (lane == 0 && a.lse) a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] = log_of_sum(top, l);
+      };
+      if (last_of(a.counters + mine, n, lane)) {
+        if (blocks == 1) {
+          join_parts<D, ROWS>(a, mine, 1, n, share, sg.group, rows, lane, finish);
+        } else {
+          float* to = part_of<S::kPart>(a, mine, share, sg.group);
+          join_parts<D, ROWS>(a, mine, 1, n, share, sg.group, rows, lane,
+                              [&](int r, float top, float l, const float (&num)[D / 32]) {
 #pragma unroll
-          for (int e = 0; e < W / 2; ++e) to[e] = tc::pack_bf16x2(n[2 * e] * inv, n[2 * e + 1] * inv);
-          if (d0 == 0 && a.lse)
-            a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] =
-                l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+                                for (int e = 0; e < D / 32; ++e) to[r * D + lane * (D / 32) + e] = num[e];
+                                if (lane == 0) {
+                                  to[S::kRows * D + r] = top;
+                                  to[S::kRows * (D + 1) + r] = l;
+                                }
+                              });
+          if (last_of(a.counters + kMaxWarps + w0, blocks, lane))
+            join_parts<D, ROWS>(a, w0, kJoin, (int)blocks, share, sg.group, rows, lane, finish);
         }
       }
     }
   }
+  }
+  if (ld.dead && lane == 0) atomicOr(a.flags, SV_FLAG_TIMEOUT);
+  ld.leave();
 }
 
 cudaLaunchConfig_t config(int blocks, int threads, size_t smem, void* stream, cudaLaunchAttribute* attr) {
@@ -997,7 +1183,7 @@ int attention_t(Args a, std::string* err, void* stream) {
     *err = "kv4_attention: no current device, or its ordinal is above 63";
     return SV_ERR_CUDA;
   }
-  const size_t most = S::kRing + S::kJoin + (kMaxSeqs + 1) * 8;
+  const size_t most = S::kRing + (kMaxSeqs + 1) * 12;
   auto* kernel = attention_kernel<D, ROWS, ALIGNED>;
   cudaError_t e;
   if (!ready[dev].load(std::memory_order_acquire)) {
@@ -1014,8 +1200,8 @@ int attention_t(Args a, std::string* err, void* stream) {
     a.kpr = all.kpr ? all.kpr + b0 : nullptr;
     a.out = all.out + b0 * all.o_seq;
     a.lse = all.lse ? all.lse + (long long)b0 * (all.K + 1) * all.Hq : nullptr;
-    const size_t smem = S::kRing + S::kJoin + (a.B + 1) * 8;
-    int ctas = 227 * 1024 / (int)(smem + 1024);
+    const size_t smem = S::kRing + (a.B + 1) * 12;
+    int ctas = 227 * 1024 / (int)(smem + 1024 + S::kStatic);
     ctas = ctas < S::kMinCtas ? ctas : S::kMinCtas;
     int grid = tc::num_sms() * ctas;
     if (grid > kMaxCtas) grid = kMaxCtas;
@@ -1044,8 +1230,8 @@ size_t kv4_head_bytes(int D, int page_size) { return ((size_t)page_size * (D + 8
 
 constexpr size_t kKv4Counters = 256;  // behind the flag word
 size_t kv4_attention_workspace_bytes(int K, int Hq, int Hkv, int D) {
-  const int rows = Hq / Hkv * (K + 1) > 8 ? 16 : 8;
-  return kKv4Counters + kv4::kMaxCtas * 4 + (size_t)kv4::kMaxCtas * 2 * rows * (D + 2) * 4;
+  const int need = Hq / Hkv * (K + 1), rows = need <= 4 ? 4 : need <= 8 ? 8 : 16;
+  return kKv4Counters + kv4::kMaxWarps * 8 + (size_t)kv4::kMaxWarps * 2 * rows * (D + 2) * 4;
 }
 
 int kv4_attention_launch(const Kv4AttentionLaunch& L, std::string* err) {
@@ -1071,9 +1257,10 @@ int kv4_attention_launch(const Kv4AttentionLaunch& L, std::string* err) {
   a.Hkv = L.c.Hkv;
   a.G = L.Hq / L.c.Hkv;
   uint8_t* ws = static_cast<uint8_t*>(L.workspace);
+  a.clocks = L.wait_tries > 0 ? tc::kWaitClocks : 0;
   a.flags = reinterpret_cast<uint32_t*>(ws);
   a.counters = reinterpret_cast<uint32_t*>(ws + kKv4Counters);
-  a.parts = reinterpret_cast<float*>(ws + kKv4Counters + kv4::kMaxCtas * 4);
+  a.parts = reinterpret_cast<float*>(ws + kKv4Counters + kv4::kMaxWarps * 8);
   return L.D == 128 ? kv4::attention_d<128>(a, err, L.stream) : kv4::attention_d<64>(a, err, L.stream);
 }
 
