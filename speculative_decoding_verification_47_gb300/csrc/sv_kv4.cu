@@ -314,30 +314,33 @@ struct Segment {
   __device__ __forceinline__ int count() const { return s.bad || s.len + s.k == 0 ? 0 : t1 - t0; }
 };
 
-// Where the sequences' groups begin, by cost and by number.
+// Where the sequences' groups begin, by cost and by number, and what one costs.
 struct Books {
   unsigned long long* cost;  // [B + 1]
   uint32_t* groups;          // [B + 1]
+  uint32_t* each;            // [B]
+  static constexpr int kBytes = 16;  // of a sequence
 };
 
 // The number of the group that unit `at` lies in.
-__device__ __forceinline__ uint32_t group_at(const Args& a, const Books& k, int rows, unsigned long long at) {
-  int lo = 0, hi = a.B - 1;  // the last b with cost[b] <= at
+__device__ __forceinline__ uint32_t group_at(const Books& k, int B, unsigned long long at) {
+  int lo = 0, hi = B - 1;  // the last b with cost[b] <= at
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (k.cost[mid] <= at) lo = mid; else hi = mid - 1;
   }
   const unsigned long long off = at - k.cost[lo];
-  const uint32_t cost = (uint32_t)(seq_of(a, lo, rows).tiles + kGroupCost);
-  return k.groups[lo] + (off >> 32 ? (uint32_t)(off / cost) : (uint32_t)off / cost);
+  return k.groups[lo] + (off >> 32 ? (uint32_t)(off / k.each[lo]) : (uint32_t)off / k.each[lo]);
 }
 
 // The runs of the warp's share [begin, end) in the groups first .. first + kList - 1, a lane per group;
-// those without a tile are left out.  Returns their number.
+// those without a tile are left out.  Returns their number; *more: whether groups follow.
 __device__ __forceinline__ int list_segments(const Args& a, const Books& k, int rows, uint32_t first,
-                                             unsigned long long begin, unsigned long long end, int lane, Segment* list) {
+                                             unsigned long long begin, unsigned long long end, int lane, Segment* list,
+                                             bool* more) {
   Segment g;
   g.t0 = g.t1 = 0;
+  bool goes_on = false;
   if (lane < kList && first + lane < k.groups[a.B]) {
     const uint32_t number = first + lane;
     int lo = 0, hi = a.B - 1;  // the last b with groups[b] <= number
@@ -347,7 +350,7 @@ __device__ __forceinline__ int list_segments(const Args& a, const Books& k, int 
     }
     g.b = lo;
     g.s = seq_of(a, lo, rows);
-    const uint32_t group = number - k.groups[lo], cost = (uint32_t)(g.s.tiles + kGroupCost);
+    const uint32_t group = number - k.groups[lo], cost = k.each[lo];
     g.group = k.cost[lo] + (unsigned long long)group * cost;
     g.h = (int)(group / (uint32_t)g.s.blocks);
     g.block = (int)(group - (uint32_t)g.h * g.s.blocks);
@@ -355,8 +358,10 @@ __device__ __forceinline__ int list_segments(const Args& a, const Books& k, int 
       g.t0 = begin > g.group ? max(0, (int)(begin - g.group) - kGroupCost) : 0;
       g.t1 = max(0, (int)min((unsigned long long)cost, end - g.group) - kGroupCost);
     }
+    goes_on = g.group + cost < end;
   }
   const unsigned some = __ballot_sync(kFull, g.t0 < g.t1);
+  *more = __ballot_sync(kFull, goes_on) >> (kList - 1) & 1;
   __syncwarp();  // (the list before is read no more)
   if (g.t0 < g.t1) list[__popc(some & ((1u << lane) - 1u))] = g;
   __syncwarp();
@@ -627,50 +632,44 @@ __device__ __forceinline__ float* part_of(const Args& a, unsigned warp, unsigned
   return a.parts + ((long long)warp * 2 + (warp * share >= group ? 0 : 1)) * PART;
 }
 
-// The parts of the warps first, first + step, .. (n of them) joined, a row at a time: numerators of the
-// lane's D / 32 values, the sum and the reference.  In the order of the warps.
-template <int D, int ROWS, typename Put>
-__device__ __forceinline__ void join_parts(const Args& a, unsigned first, unsigned step, int n, unsigned long long share,
-                                           unsigned long long group, int rows, int lane, Put put) {
-  constexpr int PART = ROWS * (D + 2), W = D / 32;
-  for (int r = 0; r < rows; ++r) {
-    float top = kNone, l = 0.f, num[W] = {};
-    for (int c = 0; c < n; c += kJoin) {
-      const int m = min(kJoin, n - c);
-      float ref = kNone, sum = 0.f;
-      if (lane < m) {
-        const float* p = part_of<PART>(a, first + (c + lane) * step, share, group) + ROWS * D;
-        ref = __ldcg(p + r);
-        sum = __ldcg(p + ROWS + r);
-      }
-      float most = fmaxf(ref, top);
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, k));
-      const float old = ex2(top - most), f = ex2(ref - most);
-      sum *= f;
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(kFull, sum, k);
-      top = most;
-      l = __fmaf_rn(l, old, sum);
-#pragma unroll
-      for (int e = 0; e < W; ++e) num[e] *= old;
+// The parts of the warps first, first + step, .. (n of them) joined, in the order of the warps, for all
+// rows at once: numerators of the lane's D / 32 values, and lane r's sum and reference of row r.
+template <int D, int ROWS>
+struct Joined {
+  float num[ROWS][D / 32], l, top;
+
+  __device__ __forceinline__ void of(const Args& a, unsigned first, unsigned step, int n, unsigned long long share,
+                                     unsigned long long group, int lane) {
+    constexpr int PART = ROWS * (D + 2), W = D / 32;
+    const int mine = ROWS * D + lane % ROWS;  // (rows that the block does not have are read too: any values)
+    top = kNone;
 #pragma unroll 4
-      for (int j = 0; j < m; ++j) {
-        const float fj = __shfl_sync(kFull, f, j);
-        const float* p = part_of<PART>(a, first + (c + j) * step, share, group) + r * D + lane * W;
+    for (int p = 0; p < n; ++p) top = fmaxf(top, __ldcg(part_of<PART>(a, first + p * step, share, group) + mine));
+    l = 0.f;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int e = 0; e < W; ++e) num[r][e] = 0.f;
+#pragma unroll 2
+    for (int p = 0; p < n; ++p) {
+      const float* part = part_of<PART>(a, first + p * step, share, group);
+      const float f = ex2(__ldcg(part + mine) - top);
+      l = __fmaf_rn(__ldcg(part + mine + ROWS), f, l);
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const float fr = __shfl_sync(kFull, f, r);
         if constexpr (W == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
-          num[0] = __fmaf_rn(v.x, fj, num[0]), num[1] = __fmaf_rn(v.y, fj, num[1]);
-          num[2] = __fmaf_rn(v.z, fj, num[2]), num[3] = __fmaf_rn(v.w, fj, num[3]);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(part + r * D + lane * W));
+          num[r][0] = __fmaf_rn(v.x, fr, num[r][0]), num[r][1] = __fmaf_rn(v.y, fr, num[r][1]);
+          num[r][2] = __fmaf_rn(v.z, fr, num[r][2]), num[r][3] = __fmaf_rn(v.w, fr, num[r][3]);
         } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
-          num[0] = __fmaf_rn(v.x, fj, num[0]), num[1] = __fmaf_rn(v.y, fj, num[1]);
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(part + r * D + lane * W));
+          num[r][0] = __fmaf_rn(v.x, fr, num[r][0]), num[r][1] = __fmaf_rn(v.y, fr, num[r][1]);
         }
       }
     }
-    put(r, top, l, num);
   }
-}
+};
 
 // One more of `all` is done (with what the warp wrote before); true if it was the last, which leaves 0.
 __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t all, int lane) {
@@ -700,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
   Books books;
   books.cost = reinterpret_cast<unsigned long long*>(smem + S::kRing);
   books.groups = reinterpret_cast<uint32_t*>(books.cost + a.B + 1);
+  books.each = books.groups + a.B + 1;
   __shared__ unsigned long long warp_cost[kWarps];
   __shared__ uint32_t warp_groups[kWarps];
   __shared__ Segment lists[kWarps][kList];
@@ -732,6 +732,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
         cost += (unsigned long long)(s.tiles + kGroupCost) * s.blocks * a.Hkv;
         books.cost[b + 1] = cost;  // (within this thread's run)
         books.groups[b + 1] = groups;
+        books.each[b] = (uint32_t)(s.tiles + kGroupCost);
       }
     }
     unsigned long long up = cost;
@@ -761,10 +762,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
   const unsigned long long begin = worker * share, end = min(begin + share, total);
   if (begin >= end) return;
 
-  const uint32_t last_group = group_at(a, books, S::kRows, end - 1);
+  bool more = true;
 #pragma unroll 1
-  for (uint32_t first = group_at(a, books, S::kRows, begin); first <= last_group; first += kList) {
-  const int segments = list_segments(a, books, S::kRows, first, begin, end, lane, list);
+  for (uint32_t first = group_at(books, a.B, begin); more; first += kList) {
+  const int segments = list_segments(a, books, S::kRows, first, begin, end, lane, list, &more);
+  // Q's rows of all of them towards L2
+  for (int x = lane; x < segments * S::kRows; x += 32) {
+    const Segment& sg = list[x / S::kRows];
+    const int r = sg.block * S::kRows + x % S::kRows;
+    if (r < a.G * (sg.s.k + 1))
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + sg.b * a.q_seq + (r / a.G) * a.q_pos + (sg.h * a.G + r % a.G) * a.q_head));
+  }
   ld.begin(a, segments, lane);
 #pragma unroll 1
   for (int st = 0; st < kStages - 1; ++st) ld.issue(a, lane);
@@ -854,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
         }
 
         // S^T: tokens tau and tau + 8 by columns 2t and 2t + 1
-        float acc[NT][4] = {};
+        float acc[NT][4] = {}, acc2[NT][4] = {};  // (two chains of products)
         {
           uint32_t x[WK], y[WK];
           if constexpr (D == 128) {
@@ -884,10 +892,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
             for (int nt = 0; nt < NT; ++nt)
               mma_f16(acc[nt], x[w] & kLow, y[w] & kLow, x[w] & kHigh, y[w] & kHigh, b0[nt].x, b0[nt].y);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], x8 & kLow, y8 & kLow, x8 & kHigh, y8 & kHigh, b1[nt].x, b1[nt].y);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(acc2[nt], x8 & kLow, y8 & kLow, x8 & kHigh, y8 & kHigh, b1[nt].x, b1[nt].y);
           }
         }
 
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nt][e] += acc2[nt][e];
         F2 z[NT][TP], zv[NT][TP], vm[TP];
 #pragma unroll
         for (int e = 0; e < TP; ++e) {
@@ -1123,30 +1135,35 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
       const unsigned w1 = (unsigned)((sg.group + kGroupCost + s.tiles - 1) / share);
       const unsigned blocks = (w1 - w0) / kJoin + 1, mine = w0 + (worker - w0) / kJoin * kJoin;
       const int n = (int)min((unsigned)kJoin, w1 - mine + 1);
-      auto finish = [&](int r, float top, float l, const float (&num)[D / 32]) {
-        const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
-        const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-        uint32_t* to = reinterpret_cast<uint32_t*>(a.out + sg.b * a.o_seq + i * a.o_pos + head * a.o_head + lane * (D / 32));
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e) to[e] = tc::pack_bf16x2(num[2 * e] * inv, num[2 * e + 1] * inv);
-        if (lane == 0 && a.lse) a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] = log_of_sum(top, l);
-      };
       if (last_of(a.counters + mine, n, lane)) {
-        if (blocks == 1) {
-          join_parts<D, ROWS>(a, mine, 1, n, share, sg.group, rows, lane, finish);
-        } else {
+        Joined<D, ROWS> all;
+        all.of(a, mine, 1, n, share, sg.group, lane);
+        bool result = blocks == 1;
+        if (!result) {
           float* to = part_of<S::kPart>(a, mine, share, sg.group);
-          join_parts<D, ROWS>(a, mine, 1, n, share, sg.group, rows, lane,
-                              [&](int r, float top, float l, const float (&num)[D / 32]) {
 #pragma unroll
-                                for (int e = 0; e < D / 32; ++e) to[r * D + lane * (D / 32) + e] = num[e];
-                                if (lane == 0) {
-                                  to[S::kRows * D + r] = top;
-                                  to[S::kRows * (D + 1) + r] = l;
-                                }
-                              });
-          if (last_of(a.counters + kMaxWarps + w0, blocks, lane))
-            join_parts<D, ROWS>(a, w0, kJoin, (int)blocks, share, sg.group, rows, lane, finish);
+          for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) to[r * D + lane * (D / 32) + e] = all.num[r][e];
+          if (lane < ROWS) {
+            to[ROWS * D + lane] = all.top;
+            to[ROWS * (D + 1) + lane] = all.l;
+          }
+          result = last_of(a.counters + kMaxWarps + w0, blocks, lane);
+          if (result) all.of(a, w0, kJoin, (int)blocks, share, sg.group, lane);
+        }
+        if (result) {
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            const float l = __shfl_sync(kFull, all.l, r), inv = l == 0.f ? 0.f : __frcp_rn(l);
+            const float top = __shfl_sync(kFull, all.top, r);
+            if (r >= rows) continue;
+            const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
+            uint32_t* to = reinterpret_cast<uint32_t*>(a.out + sg.b * a.o_seq + i * a.o_pos + head * a.o_head + lane * (D / 32));
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) to[e] = tc::pack_bf16x2(all.num[r][2 * e] * inv, all.num[r][2 * e + 1] * inv);
+            if (lane == 0 && a.lse) a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] = log_of_sum(top, l);
+          }
         }
       }
     }
@@ -1183,7 +1200,7 @@ int attention_t(Args a, std::string* err, void* stream) {
     *err = "kv4_attention: no current device, or its ordinal is above 63";
     return SV_ERR_CUDA;
   }
-  const size_t most = S::kRing + (kMaxSeqs + 1) * 12;
+  const size_t most = S::kRing + (kMaxSeqs + 1) * Books::kBytes;
   auto* kernel = attention_kernel<D, ROWS, ALIGNED>;
   cudaError_t e;
   if (!ready[dev].load(std::memory_order_acquire)) {
@@ -1200,7 +1217,7 @@ int attention_t(Args a, std::string* err, void* stream) {
     a.kpr = all.kpr ? all.kpr + b0 : nullptr;
     a.out = all.out + b0 * all.o_seq;
     a.lse = all.lse ? all.lse + (long long)b0 * (all.K + 1) * all.Hq : nullptr;
-    const size_t smem = S::kRing + (a.B + 1) * 12;
+    const size_t smem = S::kRing + (a.B + 1) * Books::kBytes;
     int ctas = 227 * 1024 / (int)(smem + 1024 + S::kStatic);
     ctas = ctas < S::kMinCtas ? ctas : S::kMinCtas;
     int grid = tc::num_sms() * ctas;
