@@ -232,8 +232,8 @@ constexpr int kStages = 4;         // tiles of a warp on their way
 constexpr int kMaxSeqs = 1024;     // sequences of a launch
 constexpr int kMaxCtas = 640;
 constexpr int kMaxWarps = kMaxCtas * kWarps;
-constexpr int kMinShare = 6;       // of a warp
-constexpr int kGroupCost = 2;      // what a group costs beside its tiles, in tiles: Q, the stores, the way to the next
+constexpr int kMinShare = 5;       // of a warp
+constexpr int kGroupCost = 5;      // what a group costs beside its tiles, in tiles: Q, the stores, the way to the next
 constexpr int kList = 16;          // segments that a warp looks up at a time
 constexpr int kJoin = 16;          // parts that are joined at once
 constexpr uint32_t kFull = 0xffffffffu;
@@ -269,7 +269,7 @@ struct Shape {
   static constexpr int kPart = kRows * (D + 2);  // floats of a part in memory
   static constexpr int kMinCtas = NT == 1 ? 4 : 3;
   // shared memory beside the ring: lists, barriers, and the fragments of Q of two blocks of columns (bytes, about)
-  static constexpr int kStatic = 4600 + (NT == 1 ? 0 : kWarps * (NT * D * 16 + 128));
+  static constexpr int kStatic = 5000 + kWarps * (kRows * D * 2 + (NT == 1 ? 0 : NT * D * 16));
 };
 
 // One sequence: what its queries see, in tiles.
@@ -425,6 +425,16 @@ __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
 
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
+__device__ __forceinline__ void bulk(uint32_t to, const void* from, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+               "l"(from), "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
+}
+// A wait of at most about a second; none at all if `clocks` is 0.
+__device__ __forceinline__ bool arrived(uint64_t* bar, uint32_t parity, long long clocks) {
+  return clocks > 0 && tc::wait_bounded(bar, parity, clocks);
+}
+
 // The loads of a warp's tiles into its ring, in the order of the list's segments: they run ahead of the
 // products, over the ends of segments too.  A page of whole tiles has a tile's four pieces (codes and
 // (s, m) of K and V) as runs of bytes, one run if the page is a tile: bulk copies.  Lane l looks up and
@@ -513,25 +523,17 @@ struct Loader<D, true> {
     }
     ++i, ++asked;
   }
-  static __device__ __forceinline__ void bulk(uint32_t to, const uint8_t* from, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
-                 "l"(from), "r"(bytes), "r"(smem_addr(bar))
-                 : "memory");
-  }
-  // the next tile, once it is there
+  // the next tile, once it is there (a lane whose wait runs out waits no more; the result is given up)
   __device__ __forceinline__ uint32_t take(const Args& a) {
     const uint32_t slot = taken & (kStages - 1);
-    if (!dead) {
-      const bool ok = a.clocks > 0 && tc::wait_bounded(bars + slot, taken / kStages & 1, a.clocks);
-      dead = !__all_sync(kFull, ok);
-    }
-    if (!dead) ++taken;
+    if (!dead) dead = !arrived(bars + slot, taken / kStages & 1, a.clocks);
+    ++taken;
     return ring + slot * TB;
   }
   // copies of a ring that was given up come to their end before the CTA does
   __device__ __forceinline__ void leave() {
-    if (dead)
-      for (; taken != asked; ++taken) tc::wait_bounded(bars + (taken & (kStages - 1)), taken / kStages & 1);
+    for (uint32_t p = asked > kStages ? asked - kStages : 0; p != asked; ++p)
+      tc::wait_bounded(bars + (p & (kStages - 1)), p / kStages & 1);
   }
 };
 
@@ -610,20 +612,44 @@ struct Loader<D, false> {
   __device__ __forceinline__ void leave() { cp_wait<0>(); }
 };
 
-// What a lane reads of Q: row r of the segment's block (key head's queries of a position, then the next
-// position's), a quarter of it.
-template <int D>
-__device__ __forceinline__ void load_q(const Args& a, const Segment& g, int rows, int row0, int r, int t, uint4 (&v)[D / 32]) {
-  if (r < rows && !g.s.bad) {
-    const int i = (row0 + r) / a.G, head = g.h * a.G + (row0 + r) % a.G;
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + g.b * a.q_seq + i * a.q_pos + head * a.q_head + t * (D / 4));
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) v[w] = __ldg(src + w);
-  } else {
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) v[w] = make_uint4(0, 0, 0, 0);
+// The rows of a segment's Q (the key head's queries of a position, then the next position's), on their way
+// into the warp's shared memory while the segment in front is computed.
+template <int D, int ROWS>
+struct QueryRows {
+  uint16_t* to;   // [ROWS][D]
+  uint64_t* bar;
+  uint32_t asked;
+  bool dead;
+
+  __device__ __forceinline__ void init(uint16_t* to_, uint64_t* bar_, int lane) {
+    to = to_, bar = bar_, asked = 0, dead = false;
+    if (lane == 0) mbar_init(bar, 1);
+    fence_mbar_init();
   }
-}
+  __device__ __forceinline__ void issue(const Args& a, const Segment& g, int lane) {
+    const int row0 = g.block * ROWS, rows = g.s.bad ? 0 : min(ROWS, a.G * (g.s.k + 1) - row0);
+    __syncwarp();  // (the rows before are read)
+    if (lane == 0) mbar_arrive_expect_tx(bar, rows * D * 2);
+    __syncwarp();
+    if (lane < rows) {
+      const int i = (row0 + lane) / a.G, head = g.h * a.G + (row0 + lane) % a.G;
+      bulk(smem_addr(to + lane * D), a.q + g.b * a.q_seq + i * a.q_pos + head * a.q_head, D * 2, bar);
+    }
+    ++asked;
+  }
+  __device__ __forceinline__ void wait(const Args& a) {
+    if (!dead) dead = !arrived(bar, (asked - 1) & 1, a.clocks);
+  }
+  // row r's quarter t
+  __device__ __forceinline__ void read(int r, int rows, int t, uint4 (&v)[D / 32]) const {
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w)
+      v[w] = r < rows ? *reinterpret_cast<const uint4*>(to + r * D + t * (D / 4) + w * 8) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void leave() {
+    if (asked) tc::wait_bounded(bar, (asked - 1) & 1);
+  }
+};
 
 // Where a warp's part of a group lies: the first of a group that began in front of the warp's share, the
 // second of one that begins inside it.
@@ -642,29 +668,42 @@ struct Joined {
                                      unsigned long long group, int lane) {
     constexpr int PART = ROWS * (D + 2), W = D / 32;
     const int mine = ROWS * D + lane % ROWS;  // (rows that the block does not have are read too: any values)
-    top = kNone;
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) top = fmaxf(top, __ldcg(part_of<PART>(a, first + p * step, share, group) + mine));
-    l = 0.f;
+    top = kNone, l = 0.f;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r)
 #pragma unroll
       for (int e = 0; e < W; ++e) num[r][e] = 0.f;
-#pragma unroll 2
-    for (int p = 0; p < n; ++p) {
-      const float* part = part_of<PART>(a, first + p * step, share, group);
-      const float f = ex2(__ldcg(part + mine) - top);
-      l = __fmaf_rn(__ldcg(part + mine + ROWS), f, l);
+    constexpr int U = ROWS == 4 ? 4 : ROWS == 8 ? 2 : 1;  // parts on their way
+#pragma unroll 1
+    for (int p0 = 0; p0 < n; p0 += U) {
+      float ref[U], sum[U], v[U][ROWS][W];
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        const float fr = __shfl_sync(kFull, f, r);
-        if constexpr (W == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(part + r * D + lane * W));
-          num[r][0] = __fmaf_rn(v.x, fr, num[r][0]), num[r][1] = __fmaf_rn(v.y, fr, num[r][1]);
-          num[r][2] = __fmaf_rn(v.z, fr, num[r][2]), num[r][3] = __fmaf_rn(v.w, fr, num[r][3]);
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(part + r * D + lane * W));
-          num[r][0] = __fmaf_rn(v.x, fr, num[r][0]), num[r][1] = __fmaf_rn(v.y, fr, num[r][1]);
+      for (int u = 0; u < U; ++u) {
+        const float* part = part_of<PART>(a, first + min(p0 + u, n - 1) * step, share, group);
+        ref[u] = __ldcg(part + mine);
+        sum[u] = __ldcg(part + mine + ROWS);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          if constexpr (W == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(part + r * D + lane * W));
+            v[u][r][0] = x.x, v[u][r][1] = x.y, v[u][r][2] = x.z, v[u][r][3] = x.w;
+          } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(part + r * D + lane * W));
+            v[u][r][0] = x.x, v[u][r][1] = x.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (p0 + u >= n) break;
+        const float most = fmaxf(top, ref[u]), old = ex2(top - most), f = ex2(ref[u] - most);
+        top = most;
+        l = __fmaf_rn(l, old, sum[u] * f);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          const float fr = __shfl_sync(kFull, f, r), or_ = __shfl_sync(kFull, old, r);
+#pragma unroll
+          for (int e = 0; e < W; ++e) num[r][e] = __fmaf_rn(v[u][r][e], fr, num[r][e] * or_);
         }
       }
     }
@@ -703,7 +742,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
   __shared__ unsigned long long warp_cost[kWarps];
   __shared__ uint32_t warp_groups[kWarps];
   __shared__ Segment lists[kWarps][kList];
-  __shared__ uint64_t bars[kWarps][kStages];
+  __shared__ uint64_t bars[kWarps][kStages], q_bars[kWarps];
+  __shared__ __align__(16) uint16_t q_rows[kWarps][ROWS * D];
   __shared__ uint2 q_frags[NT == 1 ? 1 : kWarps][NT == 1 ? 1 : NT * 2 * WK * 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -717,6 +757,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
   const uint32_t q_at = smem_addr(q_frag) + lane * 8;
   Loader<D, ALIGNED> ld;
   ld.init(list, bars[warp], smem_addr(smem) + warp * kStages * TB, lane);
+  QueryRows<D, ROWS> qr;
+  qr.init(q_rows[warp], q_bars + warp, lane);
   pdl_wait();
 
   // the groups in a row, each as long as its tiles and kGroupCost
@@ -766,13 +808,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
 #pragma unroll 1
   for (uint32_t first = group_at(books, a.B, begin); more; first += kList) {
   const int segments = list_segments(a, books, S::kRows, first, begin, end, lane, list, &more);
-  // Q's rows of all of them towards L2
-  for (int x = lane; x < segments * S::kRows; x += 32) {
-    const Segment& sg = list[x / S::kRows];
-    const int r = sg.block * S::kRows + x % S::kRows;
-    if (r < a.G * (sg.s.k + 1))
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + sg.b * a.q_seq + (r / a.G) * a.q_pos + (sg.h * a.G + r % a.G) * a.q_head));
-  }
+  if (segments > 0) qr.issue(a, list[0], lane);
   ld.begin(a, segments, lane);
 #pragma unroll 1
   for (int st = 0; st < kStages - 1; ++st) ld.issue(a, lane);
@@ -784,13 +820,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
 
     // Q's rows in fp16 next to 2^15, in the order of the codes' halves; those of two blocks of columns stay
     // in shared memory (32 registers less)
+    qr.wait(a);
     uint32_t qf[2 * WK][2];
     F2 fr[NT], sq[NT];     // of the lane's columns: score = s (acc fr) + m sq
     int limit[NT][2];      // the first token that the column's query does not see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       uint4 qv[WK];
-      load_q<D>(a, sg, rows, row0, nt * 8 + g, t, qv);
+      qr.read(nt * 8 + g, rows, t, qv);
       uint32_t top = 0;
       float sum = 0.f;
 #pragma unroll
@@ -832,6 +869,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
         limit[nt][j] = col < rows ? s.len + (row0 + col) / a.G : 0;
       }
     }
+    if (at + 1 < segments) qr.issue(a, list[at + 1], lane);
     // tokens below this are seen by every row of the block, if no window hides them
     const int all_see = s.len + row0 / a.G;
     const int widest = s.len + (row0 + rows - 1) / a.G - a.window;  // the last row's window begins here
@@ -1065,9 +1103,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
     }
 
     // the lanes' sums joined: all lanes of a column hold them
-    const bool bad = s.bad || ld.dead || __any_sync(kFull, ld.bad >> at & 1);
+    const bool dead = __any_sync(kFull, ld.dead || qr.dead), bad = s.bad || dead || __any_sync(kFull, ld.bad >> at & 1);
     if (lane == 0 && s.bad && sg.group == books.cost[sg.b]) atomicOr(a.flags, s.bad);
-    if (lane == 0 && bad && !s.bad && !ld.dead) atomicOr(a.flags, SV_FLAG_BAD_PAGE);
+    if (lane == 0 && bad && !s.bad && !dead) atomicOr(a.flags, SV_FLAG_BAD_PAGE);
     const bool whole = sg.t0 == 0 && sg.t1 == s.tiles;
     float* part = part_of<S::kPart>(a, worker, share, sg.group);
 #pragma unroll
@@ -1169,8 +1207,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
     }
   }
   }
-  if (ld.dead && lane == 0) atomicOr(a.flags, SV_FLAG_TIMEOUT);
-  ld.leave();
+  if (__any_sync(kFull, ld.dead || qr.dead)) {
+    if (lane == 0) atomicOr(a.flags, SV_FLAG_TIMEOUT);
+    ld.leave();
+    qr.leave();
+  }
 }
 
 cudaLaunchConfig_t config(int blocks, int threads, size_t smem, void* stream, cudaLaunchAttribute* attr) {
