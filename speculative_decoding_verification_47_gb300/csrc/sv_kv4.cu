@@ -417,12 +417,6 @@ __device__ __forceinline__ float log2_of(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
 __device__ __forceinline__ void bulk(uint32_t to, const void* from, uint32_t bytes, uint64_t* bar) {
@@ -822,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
     // in shared memory (32 registers less)
     qr.wait(a);
     uint32_t qf[2 * WK][2];
-    F2 fr[NT], sq[NT];     // of the lane's columns: score = s (acc fr) + m sq
+    float fr[NT][2], sq[NT][2];  // of the lane's columns: score = s (acc fr) + m sq
     int limit[NT][2];      // the first token that the column's query does not see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -857,41 +851,42 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
         qf[2 * w + 1][1] = half2_of(bf16_hi(u.y) * f16, bf16_hi(u.w) * f16);
       }
       const float mine_fr = a.scale * __uint_as_float((uint32_t)(254 - fb) << 23) * 16777216.f, mine_sq = a.scale * sum;
-      fr[nt] = f2_pack(__shfl_sync(kFull, mine_fr, col0 * 4), __shfl_sync(kFull, mine_fr, col0 * 4 + 4));
-      sq[nt] = f2_pack(__shfl_sync(kFull, mine_sq, col0 * 4), __shfl_sync(kFull, mine_sq, col0 * 4 + 4));
       if constexpr (NT > 1) {
 #pragma unroll
         for (int w = 0; w < 2 * WK; ++w) q_frag[(nt * 2 * WK + w) * 32 + lane] = make_uint2(qf[w][0], qf[w][1]);  // (read by this lane alone)
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        fr[nt][j] = __shfl_sync(kFull, mine_fr, (col0 + j) * 4);
+        sq[nt][j] = __shfl_sync(kFull, mine_sq, (col0 + j) * 4);
         const int col = nt * 8 + col0 + j;
         limit[nt][j] = col < rows ? s.len + (row0 + col) / a.G : 0;
       }
     }
     if (at + 1 < segments) qr.issue(a, list[at + 1], lane);
-    // tokens below this are seen by every row of the block, if no window hides them
-    const int all_see = s.len + row0 / a.G;
-    const int widest = s.len + (row0 + rows - 1) / a.G - a.window;  // the last row's window begins here
+    // tiles t0 + [sure, sure + plain) are seen whole by every row of the block: those in front of the last one's
+    // tokens (and behind the beginning of the last row's window)
+    int sure = 0, plain = (s.len + row0 / a.G) / kTok;
+    if (a.window > 0) {
+      const int widest = (max(0, s.len + (row0 + rows - 1) / a.G - a.window) + kTok - 1) / kTok;
+      sure = max(widest - s.skip, s.sink_tiles) - sg.t0;
+      plain -= s.skip;
+    }
+    plain = max(0, plain - sg.t0 - sure);
 
     float o[NT][TILES][4] = {};
-    F2 sum[NT], low[NT];
-    float ref[NT][2], vref[NT][2];  // references of p, and of 2^7 p s'
+    float sum[NT][2] = {}, low[NT][2] = {};
+    float ref[NT][2], vref[NT][2];  // references of p, and of 2^-7 p s', negated
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      sum[nt] = low[nt] = f2_pack(0.f, 0.f);
-      ref[nt][0] = ref[nt][1] = vref[nt][0] = vref[nt][1] = kNone;
-    }
+    for (int nt = 0; nt < NT; ++nt) ref[nt][0] = ref[nt][1] = vref[nt][0] = vref[nt][1] = -kNone;
 
     {
       const int n = sg.count();
-      int tile = sg.t0;
 #pragma unroll 1
-      for (int j = 0; j < n; ++j, ++tile) {
+      for (int j = 0; j < n; ++j) {
         ld.issue(a, lane);
         const uint32_t buf = ld.take(a);
 
-        const int tok0 = (tile + (tile < s.sink_tiles ? 0 : s.skip)) * kTok;
         uint32_t kw[TP], vw[TP];
 #pragma unroll
         for (int e = 0; e < TP; ++e) {
@@ -934,92 +929,74 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
           }
         }
 
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][e] += acc2[nt][e];
-        F2 z[NT][TP], zv[NT][TP], vm[TP];
+        float z[NT][TP][2], zv[NT][TP][2], vm[TP];
 #pragma unroll
         for (int e = 0; e < TP; ++e) {
-          const float ks = bf16_lo(kw[e]), km = bf16_hi(kw[e]), m = bf16_hi(vw[e]), lg = log2_of(bf16_lo(vw[e]));
-          vm[e] = f2_pack(m, m);
+          const float ks = bf16_lo(kw[e]), km = bf16_hi(kw[e]), lg = log2_of(bf16_lo(vw[e]));
+          vm[e] = bf16_hi(vw[e]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            F2 c;
+            float c[2] = {acc[nt][2 * e] + acc2[nt][2 * e], acc[nt][2 * e + 1] + acc2[nt][2 * e + 1]};
             if constexpr (HALF) {  // tokens tau + 8 to the lanes of the columns that have no row
-              const float c2 = __shfl_xor_sync(kFull, acc[nt][2], 2), c3 = __shfl_xor_sync(kFull, acc[nt][3], 2);
-              c = f2_pack(t < 2 ? acc[nt][0] : c2, t < 2 ? acc[nt][1] : c3);
-            } else {
-              c = f2_pack(acc[nt][2 * e], acc[nt][2 * e + 1]);
+              const float c2 = __shfl_xor_sync(kFull, acc[nt][2] + acc2[nt][2], 2);
+              const float c3 = __shfl_xor_sync(kFull, acc[nt][3] + acc2[nt][3], 2);
+              if (t >= 2) c[0] = c2, c[1] = c3;
             }
-            z[nt][e] = f2_fma(f2_pack(ks, ks), f2_mul(c, fr[nt]), f2_mul(f2_pack(km, km), sq[nt]));
-            zv[nt][e] = f2_add(z[nt][e], f2_pack(lg, lg));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              z[nt][e][i] = __fmaf_rn(ks, c[i] * fr[nt][i], km * sq[nt][i]);
+              zv[nt][e][i] = z[nt][e][i] + lg;
+            }
           }
         }
-        if (tok0 + kTok > all_see || (a.window > 0 && tok0 < widest && tok0 + kTok > a.sinks)) {
+        const bool edge = (unsigned)(j - sure) >= (unsigned)plain;
+        if (edge) {
+          const int tile = sg.t0 + j, tok0 = (tile + (tile < s.sink_tiles ? 0 : s.skip)) * kTok + tok_of;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < TP; ++e) {
-              float u[2], v[2];
-              f2_unpack(z[nt][e], u[0], u[1]);
-              f2_unpack(zv[nt][e], v[0], v[1]);
-              const int tok = tok0 + tok_of + 8 * e;
+            for (int e = 0; e < TP; ++e)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int lim = limit[nt][j];
+              for (int i = 0; i < 2; ++i) {
+                const int lim = limit[nt][i], tok = tok0 + 8 * e;
                 const bool seen = tok < lim && (a.window <= 0 || tok >= lim - a.window || tok < a.sinks);
-                u[j] = seen ? u[j] : -INFINITY;
-                v[j] = seen ? v[j] : -INFINITY;
+                z[nt][e][i] = seen ? z[nt][e][i] : -INFINITY;
+                zv[nt][e][i] = seen ? zv[nt][e][i] : -INFINITY;
               }
-              z[nt][e] = f2_pack(u[0], u[1]);
-              zv[nt][e] = f2_pack(v[0], v[1]);
-            }
         }
-        // a reference follows its maximum only when that has grown by 2^8
+        // less the references, which follow their maxima only when these have grown by 2^8
         bool raise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float u[2], v[2];
-          f2_unpack(z[nt][0], u[0], u[1]);
-          f2_unpack(zv[nt][0], v[0], v[1]);
-          if constexpr (!HALF) {
-            float x, y;
-            f2_unpack(z[nt][1], x, y);
-            u[0] = fmaxf(u[0], x), u[1] = fmaxf(u[1], y);
-            f2_unpack(zv[nt][1], x, y);
-            v[0] = fmaxf(v[0], x), v[1] = fmaxf(v[1], y);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            u[i] = fmaxf(z[nt][0][i], z[nt][TP - 1][i]) + ref[nt][i];
+            v[i] = fmaxf(zv[nt][0][i], zv[nt][TP - 1][i]) + vref[nt][i];
           }
-          raise = raise || fmaxf(u[0] - ref[nt][0], u[1] - ref[nt][1]) > 8.f ||
-                  fmaxf(v[0] - vref[nt][0], v[1] - vref[nt][1]) > 15.f;
+          raise = raise || fmaxf(u[0], u[1]) > 8.f || fmaxf(v[0], v[1]) > 15.f;
         }
         if (__any_sync(kFull, raise)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float u[TP][2], v[TP][2];
+            float fv[2];
 #pragma unroll
-            for (int e = 0; e < TP; ++e) {
-              f2_unpack(z[nt][e], u[e][0], u[e][1]);
-              f2_unpack(zv[nt][e], v[e][0], v[e][1]);
-            }
-            float f[2], fv[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float m = fmaxf(u[0][j], u[TP - 1][j]), mv = fmaxf(v[0][j], v[TP - 1][j]);
+            for (int i = 0; i < 2; ++i) {
+              float m = fmaxf(z[nt][0][i], z[nt][TP - 1][i]), mv = fmaxf(zv[nt][0][i], zv[nt][TP - 1][i]);
 #pragma unroll
               for (int d = HALF ? 2 : 4; d < 32; d <<= 1) {
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
                 mv = fmaxf(mv, __shfl_xor_sync(kFull, mv, d));
               }
-              m = fmaxf(m, ref[nt][j]);
-              mv = fmaxf(mv - 7.f, vref[nt][j]);
-              f[j] = ex2(ref[nt][j] - m);
-              fv[j] = ex2(vref[nt][j] - mv);
-              ref[nt][j] = m;
-              vref[nt][j] = mv;
+              m = fminf(-m, ref[nt][i]);
+              mv = fminf(7.f - mv, vref[nt][i]);
+              const float f = ex2(m - ref[nt][i]);
+              sum[nt][i] *= f;
+              low[nt][i] *= f;
+              fv[i] = ex2(mv - vref[nt][i]);
+              ref[nt][i] = m;
+              vref[nt][i] = mv;
             }
-            sum[nt] = f2_mul(sum[nt], f2_pack(f[0], f[1]));
-            low[nt] = f2_mul(low[nt], f2_pack(f[0], f[1]));
 #pragma unroll
             for (int n = 0; n < TILES; ++n)
 #pragma unroll
@@ -1032,22 +1009,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
           uint32_t h[TP];
 #pragma unroll
           for (int e = 0; e < TP; ++e) {
-            float u[2], v[2];
-            f2_unpack(f2_add(z[nt][e], f2_pack(-ref[nt][0], -ref[nt][1])), u[0], u[1]);
-            f2_unpack(f2_add(zv[nt][e], f2_pack(-vref[nt][0], -vref[nt][1])), v[0], v[1]);
-            const F2 p = f2_pack(ex2(u[0]), ex2(u[1]));
-            sum[nt] = f2_add(sum[nt], p);
-            // (the minimum of a token that is not seen may be anything)
-            const F2 more_low = f2_fma(p, vm[e], low[nt]);
-            if (tok0 + kTok > all_see || a.window > 0) {
-              float l0, l1, n0, n1;
-              f2_unpack(low[nt], l0, l1);
-              f2_unpack(more_low, n0, n1);
-              low[nt] = f2_pack(u[0] == -INFINITY ? l0 : n0, u[1] == -INFINITY ? l1 : n1);
-            } else {
-              low[nt] = more_low;
+            float v[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float p = ex2(z[nt][e][i] + ref[nt][i]);
+              sum[nt][i] += p;
+              // (the minimum of a token that is not seen may be anything)
+              if (!edge || z[nt][e][i] != -INFINITY) low[nt][i] = __fmaf_rn(p, vm[e], low[nt][i]);
+              v[i] = ex2(zv[nt][e][i] + vref[nt][i]);
             }
-            h[e] = half2_of(ex2(v[0]), ex2(v[1]));
+            h[e] = half2_of(v[0], v[1]);
           }
           if constexpr (HALF) {
             pt[nt][0] = transpose8(h[0]);
@@ -1110,9 +1081,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
     float* part = part_of<S::kPart>(a, worker, share, sg.group);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float l[2], add[2];
-      f2_unpack(sum[nt], l[0], l[1]);
-      f2_unpack(low[nt], add[0], add[1]);
+      float l[2] = {sum[nt][0], sum[nt][1]}, add[2] = {low[nt][0], low[nt][1]};
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -1124,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
         const int r = nt * 8 + 2 * t + j;
         if (r >= rows || (HALF && t >= 2)) continue;
         // the codes' subnormals undone; D = 128: odd values stand 4 bits up; D = 64: the second row of a tile does
-        float even = ex2(vref[nt][j] - ref[nt][j]), inv = 1.f;
+        float even = ex2(ref[nt][j] - vref[nt][j]), inv = 1.f;
         if (whole) inv = l[j] == 0.f ? 0.f : __frcp_rn(l[j]);
         float x[TILES], y[TILES];
 #pragma unroll
@@ -1147,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
                                tc::pack_bf16x2(x[3], y[3]));
           }
           if (g == 0 && a.lse)
-            a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] = log_of_sum(ref[nt][j], l[j]);
+            a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] = log_of_sum(-ref[nt][j], l[j]);
         } else {
           float2* to = reinterpret_cast<float2*>(part + r * D + g * (D / 8));
 #pragma unroll
@@ -1161,7 +1130,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
             }
           }
           if (g == 0) {
-            part[S::kRows * D + r] = ref[nt][j];
+            part[S::kRows * D + r] = -ref[nt][j];
             part[S::kRows * (D + 1) + r] = l[j];
           }
         }
