@@ -263,6 +263,7 @@ template <int D, int ROWS>
 struct Shape {
   static constexpr int kRows = ROWS;
   static constexpr int NT = ROWS == 16 ? 2 : 1;
+  static constexpr int kUnroll = NT == 1 ? 2 : 1;  // tiles a turn
   static constexpr int kRowBytes = D / 2;
   static constexpr int kTileBytes = 2 * kTok * kRowBytes + 2 * kTok * 4;  // K, V, (s, m) of both
   static constexpr int kRing = kWarps * kStages * kTileBytes;
@@ -435,11 +436,11 @@ __device__ __forceinline__ bool arrived(uint64_t* bar, uint32_t parity, long lon
 // asks for the l-th tile of a batch of 32 (or what the segment has left), so that a tile costs the warp a
 // dozen instructions (a copy per 16 bytes and lane: some fifty); the next batch's page ids are read
 // while one is asked for.
-template <int D, bool ALIGNED>
+template <int D, bool ALIGNED, int U>  // U tiles are taken at a time, so at most kStages - U more are on their way
 struct Loader;
 
-template <int D>
-struct Loader<D, true> {
+template <int D, int U>
+struct Loader<D, true, U> {
   static constexpr int RB = D / 2;
   static constexpr uint32_t TB = 2 * kTok * RB + 2 * kTok * 4;
   const Segment* list;
@@ -533,8 +534,8 @@ struct Loader<D, true> {
 
 // Pages of any size: a copy per 16 bytes (and per (s, m)), each from its token's own page.  One group of
 // copies a call, an empty one behind the last tile.
-template <int D>
-struct Loader<D, false> {
+template <int D, int U>
+struct Loader<D, false, U> {
   static constexpr int RB = D / 2, CHUNKS = RB / 16, COPIES = kTok * CHUNKS / 32;
   static constexpr uint32_t TB = 2 * kTok * RB + 2 * kTok * 4;
   const Segment* list;
@@ -599,7 +600,7 @@ struct Loader<D, false> {
     cp_commit();
   }
   __device__ __forceinline__ uint32_t take(const Args&) {
-    cp_wait<kStages - 1>();
+    cp_wait<kStages - U>();
     __syncwarp();
     return ring + (taken++ & (kStages - 1)) * TB;
   }
@@ -726,6 +727,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
   constexpr bool HALF = ROWS == 4;
   constexpr int TP = HALF ? 1 : 2;      // tokens a lane holds scores of
   constexpr int WK = D / 32;            // code words of a key per lane
+  constexpr int U = S::kUnroll;
   constexpr int TILES = D / 16;         // 16-row tiles of O^T
   constexpr uint32_t TB = S::kTileBytes;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -749,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
   Segment* list = lists[warp];
   uint2* q_frag = q_frags[NT == 1 ? 0 : warp];
   const uint32_t q_at = smem_addr(q_frag) + lane * 8;
-  Loader<D, ALIGNED> ld;
+  Loader<D, ALIGNED, U> ld;
   ld.init(list, bars[warp], smem_addr(smem) + warp * kStages * TB, lane);
   QueryRows<D, ROWS> qr;
   qr.init(q_rows[warp], q_bars + warp, lane);
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
   if (segments > 0) qr.issue(a, list[0], lane);
   ld.begin(a, segments, lane);
 #pragma unroll 1
-  for (int st = 0; st < kStages - 1; ++st) ld.issue(a, lane);
+  for (int st = 0; st < kStages - U; ++st) ld.issue(a, lane);
 #pragma unroll 1
   for (int at = 0; at < segments; ++at) {
     const Segment& sg = list[at];
@@ -881,29 +883,29 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
     for (int nt = 0; nt < NT; ++nt) ref[nt][0] = ref[nt][1] = vref[nt][0] = vref[nt][1] = -kNone;
 
     {
+      // U tiles a turn: their chains of products, exponentials and products do not wait for one another
       const int n = sg.count();
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        ld.issue(a, lane);
-        const uint32_t buf = ld.take(a);
-
-        uint32_t kw[TP], vw[TP];
+      for (int j = 0; j < n; j += U) {
+        uint32_t buf[U];
 #pragma unroll
-        for (int e = 0; e < TP; ++e) {
-          kw[e] = lds32(buf + 2 * kTok * RB + (tok_of + 8 * e) * 4);
-          vw[e] = lds32(buf + 2 * kTok * RB + 64 + (tok_of + 8 * e) * 4);
-        }
+        for (int u = 0; u < U; ++u)
+          if (u == 0 || j + u < n) ld.issue(a, lane);
+#pragma unroll
+        for (int u = 0; u < U; ++u) buf[u] = u == 0 || j + u < n ? ld.take(a) : buf[0];  // (no tile: none of its tokens counts)
 
-        // S^T: tokens tau and tau + 8 by columns 2t and 2t + 1
-        float acc[NT][4] = {}, acc2[NT][4] = {};  // (two chains of products)
-        {
+        float z[U][NT][TP][2], zv[U][NT][TP][2], vm[U][TP];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          // S^T: tokens tau and tau + 8 by columns 2t and 2t + 1
+          float acc[NT][4] = {}, acc2[NT][4] = {};  // (two chains of products)
           uint32_t x[WK], y[WK];
           if constexpr (D == 128) {
-            const uint4 p = lds128(buf + tau * RB + t * 16), r = lds128(buf + (tau + 8) * RB + t * 16);
+            const uint4 p = lds128(buf[u] + tau * RB + t * 16), r = lds128(buf[u] + (tau + 8) * RB + t * 16);
             x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w;
             y[0] = r.x, y[1] = r.y, y[2] = r.z, y[3] = r.w;
           } else {
-            const uint2 p = lds64(buf + tau * RB + t * 8), r = lds64(buf + (tau + 8) * RB + t * 8);
+            const uint2 p = lds64(buf[u] + tau * RB + t * 8), r = lds64(buf[u] + (tau + 8) * RB + t * 8);
             x[0] = p.x, x[1] = p.y;
             y[0] = r.x, y[1] = r.y;
           }
@@ -925,56 +927,65 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
             for (int nt = 0; nt < NT; ++nt)
               mma_f16(acc[nt], x[w] & kLow, y[w] & kLow, x[w] & kHigh, y[w] & kHigh, b0[nt].x, b0[nt].y);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(acc2[nt], x8 & kLow, y8 & kLow, x8 & kHigh, y8 & kHigh, b1[nt].x, b1[nt].y);
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(acc2[nt], x8 & kLow, y8 & kLow, x8 & kHigh, y8 & kHigh, b1[nt].x, b1[nt].y);
           }
-        }
-
-        float z[NT][TP][2], zv[NT][TP][2], vm[TP];
 #pragma unroll
-        for (int e = 0; e < TP; ++e) {
-          const float ks = bf16_lo(kw[e]), km = bf16_hi(kw[e]), lg = log2_of(bf16_lo(vw[e]));
-          vm[e] = bf16_hi(vw[e]);
+          for (int e = 0; e < TP; ++e) {
+            const uint32_t kw = lds32(buf[u] + 2 * kTok * RB + (tok_of + 8 * e) * 4);
+            const uint32_t vw = lds32(buf[u] + 2 * kTok * RB + 64 + (tok_of + 8 * e) * 4);
+            const float ks = bf16_lo(kw), km = bf16_hi(kw), lg = log2_of(bf16_lo(vw));
+            vm[u][e] = bf16_hi(vw);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float c[2] = {acc[nt][2 * e] + acc2[nt][2 * e], acc[nt][2 * e + 1] + acc2[nt][2 * e + 1]};
-            if constexpr (HALF) {  // tokens tau + 8 to the lanes of the columns that have no row
-              const float c2 = __shfl_xor_sync(kFull, acc[nt][2] + acc2[nt][2], 2);
-              const float c3 = __shfl_xor_sync(kFull, acc[nt][3] + acc2[nt][3], 2);
-              if (t >= 2) c[0] = c2, c[1] = c3;
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              z[nt][e][i] = __fmaf_rn(ks, c[i] * fr[nt][i], km * sq[nt][i]);
-              zv[nt][e][i] = z[nt][e][i] + lg;
-            }
-          }
-        }
-        const bool edge = (unsigned)(j - sure) >= (unsigned)plain;
-        if (edge) {
-          const int tile = sg.t0 + j, tok0 = (tile + (tile < s.sink_tiles ? 0 : s.skip)) * kTok + tok_of;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < TP; ++e)
+            for (int nt = 0; nt < NT; ++nt) {
+              float c[2] = {acc[nt][2 * e] + acc2[nt][2 * e], acc[nt][2 * e + 1] + acc2[nt][2 * e + 1]};
+              if constexpr (HALF) {  // tokens tau + 8 to the lanes of the columns that have no row
+                const float c2 = __shfl_xor_sync(kFull, acc[nt][2] + acc2[nt][2], 2);
+                const float c3 = __shfl_xor_sync(kFull, acc[nt][3] + acc2[nt][3], 2);
+                if (t >= 2) c[0] = c2, c[1] = c3;
+              }
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const int lim = limit[nt][i], tok = tok0 + 8 * e;
-                const bool seen = tok < lim && (a.window <= 0 || tok >= lim - a.window || tok < a.sinks);
-                z[nt][e][i] = seen ? z[nt][e][i] : -INFINITY;
-                zv[nt][e][i] = seen ? zv[nt][e][i] : -INFINITY;
+                z[u][nt][e][i] = __fmaf_rn(ks, c[i] * fr[nt][i], km * sq[nt][i]);
+                zv[u][nt][e][i] = z[u][nt][e][i] + lg;
               }
+            }
+          }
+        }
+        const bool edge = j < sure || j + U > sure + plain || j + U > n;
+        if (edge) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int tile = sg.t0 + j + u, tok0 = (tile + (tile < s.sink_tiles ? 0 : s.skip)) * kTok + tok_of;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < TP; ++e)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int lim = limit[nt][i], tok = tok0 + 8 * e;
+                  const bool seen = j + u < n && tok < lim && (a.window <= 0 || tok >= lim - a.window || tok < a.sinks);
+                  z[u][nt][e][i] = seen ? z[u][nt][e][i] : -INFINITY;
+                  zv[u][nt][e][i] = seen ? zv[u][nt][e][i] : -INFINITY;
+                }
+          }
         }
         // less the references, which follow their maxima only when these have grown by 2^8
+        float m[NT][2], mv[NT][2];
         bool raise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float u[2], v[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            u[i] = fmaxf(z[nt][0][i], z[nt][TP - 1][i]) + ref[nt][i];
-            v[i] = fmaxf(zv[nt][0][i], zv[nt][TP - 1][i]) + vref[nt][i];
+            m[nt][i] = z[0][nt][0][i], mv[nt][i] = zv[0][nt][0][i];
+#pragma unroll
+            for (int k = 1; k < U * TP; ++k) {
+              m[nt][i] = fmaxf(m[nt][i], z[k / TP][nt][k % TP][i]);
+              mv[nt][i] = fmaxf(mv[nt][i], zv[k / TP][nt][k % TP][i]);
+            }
           }
-          raise = raise || fmaxf(u[0], u[1]) > 8.f || fmaxf(v[0], v[1]) > 15.f;
+          raise = raise || fmaxf(m[nt][0] + ref[nt][0], m[nt][1] + ref[nt][1]) > 8.f ||
+                  fmaxf(mv[nt][0] + vref[nt][0], mv[nt][1] + vref[nt][1]) > 15.f;
         }
         if (__any_sync(kFull, raise)) {
 #pragma unroll
@@ -982,20 +993,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
             float fv[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float m = fmaxf(z[nt][0][i], z[nt][TP - 1][i]), mv = fmaxf(zv[nt][0][i], zv[nt][TP - 1][i]);
 #pragma unroll
               for (int d = HALF ? 2 : 4; d < 32; d <<= 1) {
-                m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-                mv = fmaxf(mv, __shfl_xor_sync(kFull, mv, d));
+                m[nt][i] = fmaxf(m[nt][i], __shfl_xor_sync(kFull, m[nt][i], d));
+                mv[nt][i] = fmaxf(mv[nt][i], __shfl_xor_sync(kFull, mv[nt][i], d));
               }
-              m = fminf(-m, ref[nt][i]);
-              mv = fminf(7.f - mv, vref[nt][i]);
-              const float f = ex2(m - ref[nt][i]);
+              const float to = fminf(-m[nt][i], ref[nt][i]), tov = fminf(7.f - mv[nt][i], vref[nt][i]);
+              const float f = ex2(to - ref[nt][i]);
               sum[nt][i] *= f;
               low[nt][i] *= f;
-              fv[i] = ex2(mv - vref[nt][i]);
-              ref[nt][i] = m;
-              vref[nt][i] = mv;
+              fv[i] = ex2(tov - vref[nt][i]);
+              ref[nt][i] = to;
+              vref[nt][i] = tov;
             }
 #pragma unroll
             for (int n = 0; n < TILES; ++n)
@@ -1003,69 +1012,69 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
               for (int e = 0; e < 4; ++e) o[nt][n][e] *= fv[e & 1];
           }
         }
-        uint32_t pt[NT][2];
+        uint32_t pt[U][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          uint32_t h[TP];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int e = 0; e < TP; ++e) {
-            float v[2];
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t h[TP];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float p = ex2(z[nt][e][i] + ref[nt][i]);
-              sum[nt][i] += p;
-              // (the minimum of a token that is not seen may be anything)
-              if (!edge || z[nt][e][i] != -INFINITY) low[nt][i] = __fmaf_rn(p, vm[e], low[nt][i]);
-              v[i] = ex2(zv[nt][e][i] + vref[nt][i]);
+            for (int e = 0; e < TP; ++e) {
+              float v[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float p = ex2(z[u][nt][e][i] + ref[nt][i]);
+                sum[nt][i] += p;
+                // (the minimum of a token that is not seen may be anything)
+                if (!edge || z[u][nt][e][i] != -INFINITY) low[nt][i] = __fmaf_rn(p, vm[u][e], low[nt][i]);
+                v[i] = ex2(zv[u][nt][e][i] + vref[nt][i]);
+              }
+              h[e] = half2_of(v[0], v[1]);
             }
-            h[e] = half2_of(v[0], v[1]);
+            pt[u][nt][0] = transpose8(h[0]);
+            if constexpr (HALF) pt[u][nt][1] = __shfl_xor_sync(kFull, pt[u][nt][0], 16);
+            else pt[u][nt][1] = transpose8(h[TP - 1]);
           }
-          if constexpr (HALF) {
-            pt[nt][0] = transpose8(h[0]);
-            pt[nt][1] = __shfl_xor_sync(kFull, pt[nt][0], 16);
-          } else {
-            pt[nt][0] = transpose8(h[0]);
-            pt[nt][1] = transpose8(h[1]);
-          }
-        }
 
         // O^T: pairs of tokens (t, t + 4), (t + 8, t + 12), this lane's codes of each
-        const uint32_t vb = buf + kTok * RB;
-        if constexpr (D == 128) {
-          uint2 w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = lds64(vb + (t + 4 * e) * RB + g * 8);
+        for (int u = 0; u < U; ++u) {
+          const uint32_t vb = buf[u] + kTok * RB;
+          if constexpr (D == 128) {
+            uint2 w[4];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t sel = hf ? 0x7632u : 0x5410u;
-            uint32_t a0 = __byte_perm(w[0].x, w[1].x, sel), a1 = __byte_perm(w[0].y, w[1].y, sel);
-            uint32_t a2 = __byte_perm(w[2].x, w[3].x, sel), a3 = __byte_perm(w[2].y, w[3].y, sel);
+            for (int e = 0; e < 4; ++e) w[e] = lds64(vb + (t + 4 * e) * RB + g * 8);
 #pragma unroll
-            for (int sh = 0; sh < 2; ++sh) {
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t sel = hf ? 0x7632u : 0x5410u;
+              uint32_t a0 = __byte_perm(w[0].x, w[1].x, sel), a1 = __byte_perm(w[0].y, w[1].y, sel);
+              uint32_t a2 = __byte_perm(w[2].x, w[3].x, sel), a3 = __byte_perm(w[2].y, w[3].y, sel);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma_f16(o[nt][hf * 4 + sh * 2], a0 & kLow, a1 & kLow, a2 & kLow, a3 & kLow, pt[nt][0], pt[nt][1]);
-                mma_f16(o[nt][hf * 4 + sh * 2 + 1], a0 & kHigh, a1 & kHigh, a2 & kHigh, a3 & kHigh, pt[nt][0], pt[nt][1]);
+              for (int sh = 0; sh < 2; ++sh) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma_f16(o[nt][hf * 4 + sh * 2], a0 & kLow, a1 & kLow, a2 & kLow, a3 & kLow, pt[u][nt][0], pt[u][nt][1]);
+                  mma_f16(o[nt][hf * 4 + sh * 2 + 1], a0 & kHigh, a1 & kHigh, a2 & kHigh, a3 & kHigh, pt[u][nt][0],
+                          pt[u][nt][1]);
+                }
+                a0 >>= 8, a1 >>= 8, a2 >>= 8, a3 >>= 8;
               }
-              a0 >>= 8, a1 >>= 8, a2 >>= 8, a3 >>= 8;
             }
-          }
-        } else {
-          uint32_t w[4];
+          } else {
+            uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = lds32(vb + (t + 4 * e) * RB + g * 4);
+            for (int e = 0; e < 4; ++e) w[e] = lds32(vb + (t + 4 * e) * RB + g * 4);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t sel = hf ? 0x7632u : 0x5410u;
-            uint32_t a0 = __byte_perm(w[0], w[1], sel), a2 = __byte_perm(w[2], w[3], sel);
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t sel = hf ? 0x7632u : 0x5410u;
+              uint32_t a0 = __byte_perm(w[0], w[1], sel), a2 = __byte_perm(w[2], w[3], sel);
 #pragma unroll
-            for (int sh = 0; sh < 2; ++sh) {
+              for (int sh = 0; sh < 2; ++sh) {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(o[nt][hf * 2 + sh], a0 & kLow, a0 & kHigh, a2 & kLow, a2 & kHigh, pt[nt][0], pt[nt][1]);
-              a0 >>= 8, a2 >>= 8;
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(o[nt][hf * 2 + sh], a0 & kLow, a0 & kHigh, a2 & kLow, a2 & kHigh, pt[u][nt][0], pt[u][nt][1]);
+                a0 >>= 8, a2 >>= 8;
+              }
             }
           }
         }
