@@ -68,11 +68,12 @@ inline Cache cache_of(const Kv4Cache& c, int D) {
 }
 
 // ---------------------------------------------------------------------------
-// Writing and reading.  D / 8 lanes share a row (16 bytes of it each), so a code
-// word of 8 values is a lane's; a warp takes the 32 / (D / 8) heads' rows that
-// stand beside each other.
+// Writing and reading.  D / 8 lanes share a row (16 bytes of it each), so a code word of 8 values is a
+// lane's.  A CTA takes a few tokens of one sequence, kRowsAhead rows a thread, whose loads are all on
+// their way before the first is used.  Bound by memory, and by some 12 instructions a value for its code.
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
+constexpr int kRowsAhead = 4;
 
 struct RowArgs {
   Cache c;
@@ -81,143 +82,186 @@ struct RowArgs {
   const uint16_t* in[2];  // K, V
   void* out[2];
   long long seq, pos, head;  // elements
-  int out_f32, B, T, Hkv;
+  long long items;           // of `tokens` tokens each: `per_seq` a sequence
+  int out_f32, B, T, Hkv, tokens, per_seq;
+  Divider by_rows;           // 2 * Hkv, a token's
   uint32_t* flags;
 };
 
-// The place of token i of sequence b; false (and a flag, once a sequence) if it has none.
-__device__ __forceinline__ bool place(const RowArgs& a, int b, int i, bool report, int* page, int* slot) {
-  const int start = a.starts[b], n = a.n_per_row ? a.n_per_row[b] : a.T;
-  if (n < 0 || n > a.T || start < 0 || (long long)start + n > (long long)a.c.max_pages * a.c.page_size) {
-    if (report && i == 0) atomicOr(a.flags, SV_FLAG_BAD_N);
+// A CTA's tokens: first .. last - 1 of sequence b.
+struct RowItem {
+  int b, first, last, start;
+};
+__device__ __forceinline__ bool row_item(const RowArgs& a, long long item, RowItem* it) {
+  it->b = (int)(item / a.per_seq);
+  it->first = (int)(item - (long long)it->b * a.per_seq) * a.tokens;
+  const int n = a.n_per_row ? a.n_per_row[it->b] : a.T;
+  it->start = a.starts[it->b];
+  if (n < 0 || n > a.T || it->start < 0 || (long long)it->start + n > (long long)a.c.max_pages * a.c.page_size) {
+    if (threadIdx.x == 0 && it->first == 0) atomicOr(a.flags, SV_FLAG_BAD_N);
     return false;
   }
-  if (i >= n) return false;
-  const int t = start + i, p = divide(t, a.c.by_page);
-  *slot = t - p * a.c.page_size;
-  *page = a.c.table[(long long)b * a.c.max_pages + p];
-  if (*page < 0 || *page >= a.c.num_pages) {
-    if (report) atomicOr(a.flags, SV_FLAG_BAD_PAGE);
-    return false;
-  }
-  return true;
+  it->last = min(it->first + a.tokens, n);
+  return it->first < it->last;
 }
 
-__device__ __forceinline__ float half_of(float x) { return 0.5f * x; }
+// A thread's row: of token i, part 0 (K) or 1 (V), head h.  codes: its bytes in the pool; NULL if it has none.
+struct Row {
+  int i, part, h;
+  uint8_t* codes;
+  uint32_t* scale;  // its (s, m)
+};
+template <int D>
+__device__ __forceinline__ Row row_of(const RowArgs& a, const RowItem& it, int r) {
+  Row w;
+  const int tok = divide(r, a.by_rows), rest = r - tok * 2 * a.Hkv;
+  w.i = it.first + tok;
+  w.part = rest >= a.Hkv;
+  w.h = rest - w.part * a.Hkv;
+  w.codes = nullptr;
+  w.scale = nullptr;
+  if (w.i < it.last) {
+    const int t = it.start + w.i, p = divide(t, a.c.by_page), slot = t - p * a.c.page_size;
+    const int page = a.c.table[(long long)it.b * a.c.max_pages + p];
+    if ((unsigned)page < (unsigned)a.c.num_pages) {
+      uint8_t* at = a.c.pool + page * a.c.page_bytes + (long long)w.h * a.c.head_bytes;
+      const int half = a.c.page_size * (D / 2);
+      w.codes = at + (long long)w.part * half + slot * (D / 2);
+      w.scale = reinterpret_cast<uint32_t*>(at + 2LL * half + (long long)w.part * a.c.page_size * 4) + slot;
+    } else if (rest == 0) {
+      atomicOr(a.flags, SV_FLAG_BAD_PAGE);
+    }
+  }
+  return w;
+}
 
-// Codes of 8 values whose row has minimum m and scale s > 0: the nearest integers to
-// (x - m) / s, ties to even.  By halves, since x - m may leave float32's range; a product
-// with the reciprocal is off by an ulp or so, and the remainder (exact: the factors of c s
-// have 4 and 8 bits) tells on which side of a border x lies.
+// The smaller (larger) of two pairs of bf16; NaN if one is.
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Codes of 8 values whose row has minimum m and scale s > 0: the nearest integers to (x - m) / s, ties to
+// even.  By halves, since x - m may leave float32's range.  The product with the reciprocal, rounded by the
+// addition of 1.5 2^23, is one off at most, where the quotient lies next to a border: the remainder (exact:
+// c and s have 4 and 8 bits) is then beyond half a step, or is half a step and c is odd.
 __device__ __forceinline__ uint32_t encode(const float (&x)[8], float m, float s) {
   const float up = s < 0x1p-60f ? 0x1p80f : 1.f;  // (a subnormal scale's reciprocal may be infinite)
-  const float hm = half_of(m), hs = half_of(s) * up, inv = __frcp_rn(hs);
+  const float hm = 0.5f * m, hs = 0.5f * s * up, inv = __frcp_rn(hs), half = 0.5f * hs;
+  const float below = __uint_as_float(__float_as_uint(half) - 1u);
   uint32_t word = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float t = __fmaf_rn(0.5f, x[e], -hm) * up;
-    float c = rintf(fminf(t * inv, 15.f));
-    const float r = __fmaf_rn(-c, hs, t), q = half_of(hs);
-    const bool odd = (int)c & 1;
-    c += r > q || (r == q && odd) ? 1.f : 0.f;
-    c -= r < -q || (r == -q && odd) ? 1.f : 0.f;
-    word |= (uint32_t)(int)fminf(fmaxf(c, 0.f), 15.f) << (4 * e);
+    const float y = fminf(__fmaf_rn(t, inv, 12582912.f), 12582927.f);  // (a subnormal scale may be rounded far down)
+    const float r = __fmaf_rn(12582912.f - y, hs, t);
+    int c = (int)(__float_as_uint(y) & 15u);
+    if (fabsf(r) > (c & 1 ? below : half)) c = min(c + (r > 0.f ? 1 : -1), 15);
+    word |= (uint32_t)c << (4 * e);
   }
   return word;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRowThreads) append_kernel(const RowArgs a) {
-  constexpr int LANES = D / 8;
+__global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int LANES = D / 8, PASS = kRowThreads / LANES, U = kRowsAhead;
   pdl_wait();
-  const long long rows = (long long)a.B * a.T * 2 * a.Hkv;
-  const long long stride = (long long)gridDim.x * (kRowThreads / LANES);
-  const int lane = threadIdx.x % LANES;
-  // (the lanes of a warp leave the loop together: `rounds` is the same for all)
-  const long long first = (long long)blockIdx.x * (kRowThreads / LANES);
-  for (long long base = first; base < rows; base += stride) {
-    const long long row = base + threadIdx.x / LANES;
-    const bool in_range = row < rows;
-    const int h = in_range ? (int)(row % a.Hkv) : 0;
-    const long long rest = in_range ? row / a.Hkv : 0;
-    const int part = (int)(rest & 1);
-    const int i = (int)((rest >> 1) % a.T), b = (int)((rest >> 1) / a.T);
-    int page = 0, slot = 0;
-    const bool ok = in_range && place(a, b, i, lane == 0 && h == 0 && part == 0, &page, &slot);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (ok)
-      v = *reinterpret_cast<const uint4*>((part ? a.in[1] : a.in[0]) + b * a.seq + i * a.pos + h * a.head + lane * 8);
-    const float x[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
-                        bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
-    float lo = x[0], hi = x[0];
-    bool fine = true;
+  const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
+  for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
+    RowItem it;
+    if (!row_item(a, item, &it)) continue;  // (the whole CTA)
+    const int rows = (it.last - it.first) * 2 * a.Hkv;
+    for (int r0 = 0; r0 < rows; r0 += U * PASS) {  // (every lane of a warp takes every turn)
+      Row w[U];
+      uint4 v[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, x[e]);
-      hi = fmaxf(hi, x[e]);
-      fine = fine && isfinite(x[e]);
-    }
+      for (int u = 0; u < U; ++u) {
+        w[u] = row_of<D>(a, it, r0 + u * PASS + mine);
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (w[u].codes)
+          v[u] = __ldcs(reinterpret_cast<const uint4*>((w[u].part ? a.in[1] : a.in[0]) + it.b * a.seq +
+                                                       w[u].i * a.pos + w[u].h * a.head + lane * 8));
+      }
 #pragma unroll
-    for (int m = 1; m < LANES; m <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-      const int other = __shfl_xor_sync(0xffffffffu, (int)fine, m);
-      fine = fine && other;
+      for (int u = 0; u < U; ++u) {
+        uint32_t lo2 = min2(min2(v[u].x, v[u].y), min2(v[u].z, v[u].w));
+        uint32_t hi2 = max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w));
+        lo2 = min2(lo2, lo2 >> 16 | lo2 << 16);
+        hi2 = max2(hi2, hi2 >> 16 | hi2 << 16);
+        uint32_t both = __byte_perm(lo2, hi2, 0x5410);  // the minimum and the maximum
+#pragma unroll
+        for (int m = 1; m < LANES; m <<= 1) {
+          const uint32_t o = __shfl_xor_sync(0xffffffffu, both, m);
+          both = __byte_perm(min2(both, o), max2(both, o), 0x7610);
+        }
+        if (!w[u].codes) continue;
+        const float lo = bf16_lo(both), hi = bf16_hi(both);
+        // (max - min) / 15, correctly rounded twice: a float32 quotient of values with 8 bits lies on
+        // a border of bf16 only if the exact one does
+        const float s = 2.f * __fdiv_rn(0.5f * hi - 0.5f * lo, 15.f);
+        uint16_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(s)), mb = (uint16_t)both;
+        const float sr = __uint_as_float((uint32_t)sb << 16);
+        uint32_t word = 0;
+        if (!(isfinite(lo) && isfinite(hi))) {
+          sb = mb = 0x7fc0u;  // a token that is not finite makes the scores of the queries that see it NaN
+        } else if (sr > 0.f) {
+          const float x[8] = {bf16_lo(v[u].x), bf16_hi(v[u].x), bf16_lo(v[u].y), bf16_hi(v[u].y),
+                              bf16_lo(v[u].z), bf16_hi(v[u].z), bf16_lo(v[u].w), bf16_hi(v[u].w)};
+          word = encode(x, lo, sr);
+        }
+        reinterpret_cast<uint32_t*>(w[u].codes)[lane] = word;
+        if (lane == 0) *w[u].scale = (uint32_t)sb | (uint32_t)mb << 16;
+      }
     }
-    if (!ok) continue;
-    // (max - min) / 15, correctly rounded twice: a float32 quotient of values with 8 bits lies on
-    // a border of bf16 only if the exact one does
-    const float s = 2.f * __fdiv_rn(half_of(hi) - half_of(lo), 15.f);
-    uint16_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(s)), mb = (uint16_t)(__float_as_uint(lo) >> 16);
-    const float sr = __uint_as_float((uint32_t)sb << 16);
-    uint32_t word = 0;
-    if (!fine) {
-      sb = mb = 0x7fc0u;  // a token that is not finite makes the scores of the queries that see it NaN
-    } else if (sr > 0.f) {
-      word = encode(x, lo, sr);
-    }
-    uint8_t* at = a.c.pool + page * a.c.page_bytes + (long long)h * a.c.head_bytes;
-    const int half = a.c.page_size * (D / 2);
-    reinterpret_cast<uint32_t*>(at + (long long)part * half + (long long)slot * (D / 2))[lane] = word;
-    if (lane == 0)
-      reinterpret_cast<uint32_t*>(at + 2LL * half + (long long)part * a.c.page_size * 4)[slot] =
-          (uint32_t)sb | (uint32_t)mb << 16;
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRowThreads) read_kernel(const RowArgs a) {
-  constexpr int LANES = D / 8;
+__global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int LANES = D / 8, PASS = kRowThreads / LANES, U = kRowsAhead;
   pdl_wait();
-  const long long rows = (long long)a.B * a.T * 2 * a.Hkv;
-  const int lane = threadIdx.x % LANES;
-  for (long long row = (long long)blockIdx.x * (kRowThreads / LANES) + threadIdx.x / LANES; row < rows;
-       row += (long long)gridDim.x * (kRowThreads / LANES)) {
-    const int h = (int)(row % a.Hkv);
-    const long long rest = row / a.Hkv;
-    const int part = (int)(rest & 1);
-    const int i = (int)((rest >> 1) % a.T), b = (int)((rest >> 1) / a.T);
-    int page, slot;
-    if (!place(a, b, i, lane == 0 && h == 0 && part == 0, &page, &slot)) continue;
-    const uint8_t* at = a.c.pool + page * a.c.page_bytes + (long long)h * a.c.head_bytes;
-    const int half = a.c.page_size * (D / 2);
-    const uint32_t w = reinterpret_cast<const uint32_t*>(at + (long long)part * half + (long long)slot * (D / 2))[lane];
-    const uint32_t sm =
-        reinterpret_cast<const uint32_t*>(at + 2LL * half + (long long)part * a.c.page_size * 4)[slot];
-    const float s = bf16_lo(sm), m = bf16_hi(sm);
-    float y[8];
+  const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
+  for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
+    RowItem it;
+    if (!row_item(a, item, &it)) continue;
+    const int rows = (it.last - it.first) * 2 * a.Hkv;
+    for (int r0 = mine; r0 < rows; r0 += U * PASS) {
+      Row w[U];
+      uint32_t word[U], sm[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __fmaf_rn((float)(w >> (4 * e) & 15u), s, m);
-    const long long to = b * a.seq + i * a.pos + h * a.head + lane * 8;
-    void* out = part ? a.out[1] : a.out[0];
-    if (a.out_f32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + to);
-      o[0] = make_float4(y[0], y[1], y[2], y[3]);
-      o[1] = make_float4(y[4], y[5], y[6], y[7]);
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to) =
-          make_uint4(tc::pack_bf16x2(y[0], y[1]), tc::pack_bf16x2(y[2], y[3]), tc::pack_bf16x2(y[4], y[5]),
-                     tc::pack_bf16x2(y[6], y[7]));
+      for (int u = 0; u < U; ++u) {
+        w[u] = row_of<D>(a, it, r0 + u * PASS);
+        word[u] = sm[u] = 0;
+        if (w[u].codes) {
+          word[u] = __ldcs(reinterpret_cast<const uint32_t*>(w[u].codes) + lane);
+          sm[u] = *w[u].scale;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!w[u].codes) continue;
+        const float s = bf16_lo(sm[u]), m = bf16_hi(sm[u]);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __fmaf_rn((float)(word[u] >> (4 * e) & 15u), s, m);
+        const long long to = it.b * a.seq + w[u].i * a.pos + w[u].h * a.head + lane * 8;
+        void* out = w[u].part ? a.out[1] : a.out[0];
+        if (a.out_f32) {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + to);
+          o[0] = make_float4(y[0], y[1], y[2], y[3]);
+          o[1] = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to) =
+              make_uint4(tc::pack_bf16x2(y[0], y[1]), tc::pack_bf16x2(y[2], y[3]), tc::pack_bf16x2(y[4], y[5]),
+                         tc::pack_bf16x2(y[6], y[7]));
+        }
+      }
     }
   }
 }
@@ -1317,8 +1361,14 @@ int kv4_rows_launch(const Kv4RowsLaunch& L, std::string* err) {
   a.T = L.T;
   a.Hkv = L.c.Hkv;
   a.flags = L.flags;
-  const int per = kv4::kRowThreads / (L.D / 8);
-  long long blocks = ((long long)L.B * L.T * 2 * L.c.Hkv + per - 1) / per;
+  // as many tokens a CTA as its threads take rows at a time
+  const int at_once = kv4::kRowThreads / (L.D / 8) * kv4::kRowsAhead;
+  a.tokens = at_once / (2 * L.c.Hkv) > 1 ? at_once / (2 * L.c.Hkv) : 1;
+  if (a.tokens > L.T) a.tokens = L.T;
+  a.per_seq = (L.T + a.tokens - 1) / a.tokens;
+  a.items = (long long)L.B * a.per_seq;
+  a.by_rows = kv4::divider(2 * L.c.Hkv);
+  long long blocks = a.items;
   const long long most = (long long)tc::num_sms() * 64;
   if (blocks > most) blocks = most;
   cudaLaunchAttribute attr;
