@@ -68,12 +68,11 @@ inline Cache cache_of(const Kv4Cache& c, int D) {
 }
 
 // ---------------------------------------------------------------------------
-// Writing and reading.  D / 8 lanes share a row (16 bytes of it each), so a code word of 8 values is a
-// lane's.  A CTA takes a few tokens of one sequence, kRowsAhead rows a thread, whose loads are all on
+// Writing and reading.  D / 16 lanes share a row, 16 values of it each: two words of codes.  A CTA takes a few tokens of one sequence, kRowsAhead rows a thread, whose loads are all on
 // their way before the first is used.  Bound by memory, and by some 12 instructions a value for its code.
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
-constexpr int kRowsAhead = 4;
+constexpr int kRowsAhead = 2;
 
 struct RowArgs {
   Cache c;
@@ -147,30 +146,47 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Codes of 8 values whose row has minimum m and scale s > 0: the nearest integers to (x - m) / s, ties to
-// even.  By halves, since x - m may leave float32's range.  The product with the reciprocal, rounded by the
-// addition of 1.5 2^23, is one off at most, where the quotient lies next to a border: the remainder (exact:
-// c and s have 4 and 8 bits) is then beyond half a step, or is half a step and c is odd.
-__device__ __forceinline__ uint32_t encode(const float (&x)[8], float m, float s) {
-  const float up = s < 0x1p-60f ? 0x1p80f : 1.f;  // (a subnormal scale's reciprocal may be infinite)
-  const float hm = 0.5f * m, hs = 0.5f * s * up, inv = __frcp_rn(hs), half = 0.5f * hs;
-  const float below = __uint_as_float(__float_as_uint(half) - 1u);
-  uint32_t word = 0;
+// What a row's codes take: minimum m and scale s > 0, by halves, since x - m may leave float32's range.
+struct Coder {
+  F2 hx, hm, inv, step;  // half of x's factor, -m / 2, 2 / s, -s / 2; times 2^80 for a scale whose reciprocal may be infinite
+  float half, below;     // half a step (of s / 2), and the value below
+
+  __device__ __forceinline__ Coder(float m, float s) {
+    const float up = s < 0x1p-60f ? 0x1p80f : 1.f;
+    const float hs = 0.5f * s * up, x = 0.5f * up, y = -0.5f * m * up, r = __frcp_rn(hs);
+    hx = f2_pack(x, x), hm = f2_pack(y, y), inv = f2_pack(r, r), step = f2_pack(-hs, -hs);
+    half = 0.5f * hs;
+    below = __uint_as_float(__float_as_uint(half) - 1u);
+  }
+  // Codes of 8 values: the nearest integers to (x - m) / s, ties to even.  The product with the reciprocal,
+  // rounded by the addition of 1.5 2^23, is one off at most, where the quotient lies next to a border: the
+  // remainder (exact: c and s have 4 and 8 bits) is then beyond half a step, or is half a step and c is odd.
+  __device__ __forceinline__ uint32_t word(const uint4& v) const {
+    const uint32_t pairs[4] = {v.x, v.y, v.z, v.w};
+    const F2 magic = f2_pack(12582912.f, 12582912.f), less = f2_pack(-12582912.f, -12582912.f);
+    uint32_t w = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float t = __fmaf_rn(0.5f, x[e], -hm) * up;
-    const float y = fminf(__fmaf_rn(t, inv, 12582912.f), 12582927.f);  // (a subnormal scale may be rounded far down)
-    const float r = __fmaf_rn(12582912.f - y, hs, t);
+    for (int p = 0; p < 4; ++p) {
+      const F2 t = f2_fma(f2_pack(bf16_lo(pairs[p]), bf16_hi(pairs[p])), hx, hm);
+      F2 y = f2_fma(t, inv, magic);
+      float y0, y1, r0, r1;
+      f2_unpack(y, y0, y1);
+      y0 = fminf(y0, 12582927.f), y1 = fminf(y1, 12582927.f);  // (a subnormal scale may be rounded far down)
+      f2_unpack(f2_fma(f2_add(f2_pack(y0, y1), less), step, t), r0, r1);
+      w |= code(y0, r0) << (8 * p) | code(y1, r1) << (8 * p + 4);
+    }
+    return w;
+  }
+  __device__ __forceinline__ uint32_t code(float y, float r) const {
     int c = (int)(__float_as_uint(y) & 15u);
     if (fabsf(r) > (c & 1 ? below : half)) c = min(c + (r > 0.f ? 1 : -1), 15);
-    word |= (uint32_t)c << (4 * e);
+    return (uint32_t)c;
   }
-  return word;
-}
+};
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_constant__ RowArgs a) {
-  constexpr int LANES = D / 8, PASS = kRowThreads / LANES, U = kRowsAhead;
+  constexpr int LANES = D / 16, PASS = kRowThreads / LANES, U = kRowsAhead;
   pdl_wait();
   const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
   for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
@@ -179,19 +195,24 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
     const int rows = (it.last - it.first) * 2 * a.Hkv;
     for (int r0 = 0; r0 < rows; r0 += U * PASS) {  // (every lane of a warp takes every turn)
       Row w[U];
-      uint4 v[U];
+      uint4 v[U][2];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         w[u] = row_of<D>(a, it, r0 + u * PASS + mine);
-        v[u] = make_uint4(0, 0, 0, 0);
-        if (w[u].codes)
-          v[u] = __ldcs(reinterpret_cast<const uint4*>((w[u].part ? a.in[1] : a.in[0]) + it.b * a.seq +
-                                                       w[u].i * a.pos + w[u].h * a.head + lane * 8));
+        v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+        if (w[u].codes) {
+          const uint4* from = reinterpret_cast<const uint4*>((w[u].part ? a.in[1] : a.in[0]) + it.b * a.seq + w[u].i * a.pos +
+                                                             w[u].h * a.head + lane * 16);
+          v[u][0] = __ldcs(from);
+          v[u][1] = __ldcs(from + 1);
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        uint32_t lo2 = min2(min2(v[u].x, v[u].y), min2(v[u].z, v[u].w));
-        uint32_t hi2 = max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w));
+        uint32_t lo2 = min2(min2(v[u][0].x, v[u][0].y), min2(v[u][0].z, v[u][0].w));
+        uint32_t hi2 = max2(max2(v[u][0].x, v[u][0].y), max2(v[u][0].z, v[u][0].w));
+        lo2 = min2(lo2, min2(min2(v[u][1].x, v[u][1].y), min2(v[u][1].z, v[u][1].w)));
+        hi2 = max2(hi2, max2(max2(v[u][1].x, v[u][1].y), max2(v[u][1].z, v[u][1].w)));
         lo2 = min2(lo2, lo2 >> 16 | lo2 << 16);
         hi2 = max2(hi2, hi2 >> 16 | hi2 << 16);
         uint32_t both = __byte_perm(lo2, hi2, 0x5410);  // the minimum and the maximum
@@ -207,15 +228,15 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
         const float s = 2.f * __fdiv_rn(0.5f * hi - 0.5f * lo, 15.f);
         uint16_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(s)), mb = (uint16_t)both;
         const float sr = __uint_as_float((uint32_t)sb << 16);
-        uint32_t word = 0;
+        uint2 words = make_uint2(0, 0);
         if (!(isfinite(lo) && isfinite(hi))) {
           sb = mb = 0x7fc0u;  // a token that is not finite makes the scores of the queries that see it NaN
         } else if (sr > 0.f) {
-          const float x[8] = {bf16_lo(v[u].x), bf16_hi(v[u].x), bf16_lo(v[u].y), bf16_hi(v[u].y),
-                              bf16_lo(v[u].z), bf16_hi(v[u].z), bf16_lo(v[u].w), bf16_hi(v[u].w)};
-          word = encode(x, lo, sr);
+          const Coder coder(lo, sr);
+          words.x = coder.word(v[u][0]);
+          words.y = coder.word(v[u][1]);
         }
-        reinterpret_cast<uint32_t*>(w[u].codes)[lane] = word;
+        reinterpret_cast<uint2*>(w[u].codes)[lane] = words;
         if (lane == 0) *w[u].scale = (uint32_t)sb | (uint32_t)mb << 16;
       }
     }
@@ -224,7 +245,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant__ RowArgs a) {
-  constexpr int LANES = D / 8, PASS = kRowThreads / LANES, U = kRowsAhead;
+  constexpr int LANES = D / 16, PASS = kRowThreads / LANES, U = kRowsAhead;
   pdl_wait();
   const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
   for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
@@ -233,13 +254,14 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
     const int rows = (it.last - it.first) * 2 * a.Hkv;
     for (int r0 = mine; r0 < rows; r0 += U * PASS) {
       Row w[U];
-      uint32_t word[U], sm[U];
+      uint2 words[U];
+      uint32_t sm[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         w[u] = row_of<D>(a, it, r0 + u * PASS);
-        word[u] = sm[u] = 0;
+        words[u] = make_uint2(0, 0), sm[u] = 0;
         if (w[u].codes) {
-          word[u] = __ldcs(reinterpret_cast<const uint32_t*>(w[u].codes) + lane);
+          words[u] = __ldcs(reinterpret_cast<const uint2*>(w[u].codes) + lane);
           sm[u] = *w[u].scale;
         }
       }
@@ -247,19 +269,24 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
       for (int u = 0; u < U; ++u) {
         if (!w[u].codes) continue;
         const float s = bf16_lo(sm[u]), m = bf16_hi(sm[u]);
-        float y[8];
+        float y[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = __fmaf_rn((float)(word[u] >> (4 * e) & 15u), s, m);
-        const long long to = it.b * a.seq + w[u].i * a.pos + w[u].h * a.head + lane * 8;
+        for (int e = 0; e < 16; ++e) {  // (the code as the low bits of 2^23 + c)
+          const uint32_t c = ((e < 8 ? words[u].x : words[u].y) >> (4 * (e & 7)) & 15u) | 0x4b000000u;
+          y[e] = __fmaf_rn(__uint_as_float(c) - 8388608.f, s, m);
+        }
+        const long long to = it.b * a.seq + w[u].i * a.pos + w[u].h * a.head + lane * 16;
         void* out = w[u].part ? a.out[1] : a.out[0];
         if (a.out_f32) {
           float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + to);
-          o[0] = make_float4(y[0], y[1], y[2], y[3]);
-          o[1] = make_float4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
         } else {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to) =
-              make_uint4(tc::pack_bf16x2(y[0], y[1]), tc::pack_bf16x2(y[2], y[3]), tc::pack_bf16x2(y[4], y[5]),
-                         tc::pack_bf16x2(y[6], y[7]));
+          uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            o[q] = make_uint4(tc::pack_bf16x2(y[8 * q], y[8 * q + 1]), tc::pack_bf16x2(y[8 * q + 2], y[8 * q + 3]),
+                              tc::pack_bf16x2(y[8 * q + 4], y[8 * q + 5]), tc::pack_bf16x2(y[8 * q + 6], y[8 * q + 7]));
         }
       }
     }
@@ -1362,7 +1389,7 @@ int kv4_rows_launch(const Kv4RowsLaunch& L, std::string* err) {
   a.Hkv = L.c.Hkv;
   a.flags = L.flags;
   // as many tokens a CTA as its threads take rows at a time
-  const int at_once = kv4::kRowThreads / (L.D / 8) * kv4::kRowsAhead;
+  const int at_once = kv4::kRowThreads / (L.D / 16) * kv4::kRowsAhead;
   a.tokens = at_once / (2 * L.c.Hkv) > 1 ? at_once / (2 * L.c.Hkv) : 1;
   if (a.tokens > L.T) a.tokens = L.T;
   a.per_seq = (L.T + a.tokens - 1) / a.tokens;
