@@ -612,7 +612,7 @@ sv_status sv_kv4_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_st
  *   zeros     device uint8 [N][K / group], each 0 .. 15, or NULL (8 everywhere).
  *   group     32, 64 or 128; K a multiple of it.
  *   bias, residual, act, out, out_dtype  as sv_linear's.
- *   M, N, K   each in 1 .. 2^30; strides 0 select K, K / 2, N, N.
+ *   M, N, K   each in 1 .. 2^30, N * K / group below 2^31; strides 0 select K, K / 2, N, N.
  *   workspace >= sv_linear_w4_workspace_size(M, N, K) bytes, 256-byte aligned,
  *             zeroed once; calls that share it must be ordered on one stream.
  * x and W must be 16-byte aligned with row strides of a multiple of 16 bytes; the

@@ -647,6 +647,7 @@ sv_status sv_linear_w4(const void* x, int64_t ldx, const void* W, int64_t ldw, c
     return fail(SV_ERR_SHAPE, "M, N and K must be in 1 .. 2^30");
   if (group != 32 && group != 64 && group != 128) return fail(SV_ERR_SHAPE, "group must be 32, 64 or 128");
   if (K % group != 0) return fail(SV_ERR_SHAPE, "K must be a multiple of group");
+  if ((long long)N * (K / group) > 0x7fffffffLL) return fail(SV_ERR_SHAPE, "N * K / group must be below 2^31");
   if (act < SV_ACT_NONE || act > SV_ACT_GELU_TANH) return fail(SV_ERR_ARG, "unknown activation");
   if (!x || !W || !scales || !out) return fail(SV_ERR_ARG, "x, W, scales and out are required");
   const int os = out_dtype == SV_BF16 ? 2 : 4;

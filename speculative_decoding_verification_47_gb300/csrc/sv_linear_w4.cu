@@ -21,7 +21,7 @@
 namespace sv {
 namespace w4 {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 128;  // k of a warp's step
 constexpr uint32_t kFull = 0xffffffffu;
@@ -39,6 +39,7 @@ struct Args {
   void* out;
   long long ldo;
   int act, out_f32, M, N, K, groups;
+  unsigned split;  // CTAs that share K
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -59,145 +60,196 @@ __device__ __forceinline__ uint32_t codes(uint32_t w, uint32_t zero) {
   return sub_bf16x2((w >> (4 * J) & 0x000f000fu) | 0x43004300u, zero);
 }
 
-// What a warp holds of a chunk: 4 words of each of its lane's rows, their scale and zero.
-template <int MT, int VEC>
-struct Step {
-  uint32_t w[2 * MT][4];
-  uint32_t sz[2 * MT];  // scale in the high half, zero in the low byte
-};
-
-// VEC words (VEC * 32 k: a group) a load.
-template <int MT, int VEC>
-__device__ __forceinline__ void load_step(Step<MT, VEC>& s, const Args& a, const uint8_t* const (&row)[2 * MT],
-                                          const long long (&srow)[2 * MT], int c, int t) {
-#pragma unroll
-  for (int r = 0; r < 2 * MT; ++r) {
-#pragma unroll
-    for (int l = 0; l < 4 / VEC; ++l) {
-      const int k = c * kChunk + l * 32 * VEC + t * 8 * VEC;
-      uint32_t* w = s.w[r] + l * VEC;
-      if (k < a.K) {
-        if constexpr (VEC == 4) {
-          const uint4 v = __ldcs(reinterpret_cast<const uint4*>(row[r] + k / 2));
-          w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else if constexpr (VEC == 2) {
-          const uint2 v = __ldcs(reinterpret_cast<const uint2*>(row[r] + k / 2));
-          w[0] = v.x, w[1] = v.y;
-        } else {
-          w[0] = __ldcs(reinterpret_cast<const uint32_t*>(row[r] + k / 2));
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) w[v] = 0;
-      }
-    }
-    // the lane's group of the chunk; the others' come by shuffle
-    const int group = c * (4 / VEC) + (t & (4 / VEC - 1));
-    uint32_t sz = 8;
-    if (group < a.groups) {
-      sz = (uint32_t)__ldg(a.scales + srow[r] + group) << 16;
-      sz |= a.zeros ? __ldg(a.zeros + srow[r] + group) : 8;
-    }
-    s.sz[r] = sz;
-  }
+__device__ __forceinline__ void cp16(uint32_t to, const void* from, bool there) {  // zeros if it is not
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 
-template <int MT, int NT, int VEC>
-__global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant__ Args a) {
-  constexpr int ROWS = 16 * MT, COLS = 8 * NT;
-  __shared__ float red[kWarps][COLS][ROWS + 4];
+// A warp's step: 16 rows of W by 128 k, 64 bytes a row, in rows of 80 bytes (a lane's words of its rows g and
+// g + 8, VEC words at a time, then meet 32 banks).
+constexpr int kTiles = 4;    // of a CTA, 16 rows each
+constexpr int kRows = 16 * kTiles;
+constexpr int kPitch = 80;
+constexpr int kStages = 8;   // of a warp: two chunks
+constexpr int kAhead = 6;    // steps on their way
+constexpr int kStageBytes = 16 * kPitch;
+
+// VEC words (VEC * 32 k) are a group.
+template <int NT, int VEC>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) rows_kernel(const __grid_constant__ Args a) {
+  constexpr int COLS = 8 * NT, L = 4 / VEC;
+  __shared__ __align__(16) uint8_t ring[kWarps][kStages][kStageBytes];
+  __shared__ float part[COLS][kRows];
+  float (*red)[COLS][kRows] = reinterpret_cast<float (*)[COLS][kRows]>(ring);  // behind the products
+  static_assert(sizeof(ring) >= kWarps * COLS * kRows * 4, "the warps' sums fit over the ring");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   pdl_wait();
-  const int blocks = (a.M + COLS - 1) / COLS, tile = (int)(blockIdx.x / blocks);
-  const int n0 = tile * ROWS, m0 = (int)(blockIdx.x - tile * blocks) * COLS;  // (CTAs of a tile are neighbours)
-  const uint8_t* row[2 * MT];
-  long long srow[2 * MT];
+  const unsigned block = blockIdx.x / a.split, rank = blockIdx.x - block * a.split;
+  const int blocks = (a.M + COLS - 1) / COLS, slab = (int)(block / blocks);
+  const int n0 = slab * kRows, m0 = (int)(block - slab * blocks) * COLS;  // (CTAs of the same rows of W are neighbours)
+  const int chunks = (a.K + kChunk - 1) / kChunk, workers = (int)a.split * kWarps, me = (int)rank * kWarps + warp;
+  const int c0 = (int)((long long)chunks * me / workers), c1 = (int)((long long)chunks * (me + 1) / workers);
+  const uint32_t base = smem_addr(ring[warp]);
+  // bytes 16 t .. of rows g and g + 8 of each tile, and the rows' scales (rows behind the last one: the last one's)
+  const uint8_t* from[kTiles][2];
+  uint32_t srow[kTiles][2];
 #pragma unroll
-  for (int r = 0; r < 2 * MT; ++r) {
-    const int n = min(n0 + g + 8 * r, a.N - 1);
-    row[r] = a.W + n * a.ldw;
-    srow[r] = (long long)n * a.groups;
-  }
-  const uint16_t* xrow[NT];
-  bool has[NT];
+  for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    has[nt] = m0 + nt * 8 + g < a.M;
-    xrow[nt] = a.x + (has[nt] ? m0 + nt * 8 + g : 0) * a.ldx;
-  }
-  const int chunks = (a.K + kChunk - 1) / kChunk;
-  float total[MT][NT][4] = {};
-
-  auto consume = [&](const Step<MT, VEC>& s, int c) {
-    float acc[MT][NT][4] = {};
+    for (int r = 0; r < 2; ++r) {
+      const int n = min(n0 + i * 16 + 8 * r + g, a.N - 1);
+      from[i][r] = a.W + n * a.ldw + t * 16;
+      srow[i][r] = (uint32_t)n * a.groups;
+    }
+  const uint32_t to = base + g * kPitch + t * 16;
+  auto issue = [&](int c, int i) {
+    if (c < c1) {
+      const bool there = VEC == 4 || c * kChunk + t * 32 < a.K;
+      const uint32_t at = to + (((c - c0) & 1) * kTiles + i) * kStageBytes;
+      cp16(at, from[i][0] + (there ? (long long)c * (kChunk / 2) : 0), there);
+      cp16(at + 8 * kPitch, from[i][1] + (there ? (long long)c * (kChunk / 2) : 0), there);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // What a chunk takes beside its codes is read a chunk ahead, all of it before any is used (a condition around a
+  // load makes it wait for the one before): behind the last chunk that chunk's again, behind the last row of x that
+  // row.  The scale and zero of a tile's rows g, g + 8 are the lane's group's of the chunk, the others' come by shuffle.
+  auto load_scales = [&](int c, uint32_t (&scale)[kTiles][2], uint32_t (&zero)[kTiles][2]) {
+    const uint32_t at = (uint32_t)min(c * L + (t & (L - 1)), a.groups - 1);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const int l = w / VEC, k = c * kChunk + l * 32 * VEC + t * 8 * VEC + (w % VEC) * 8;
-      uint32_t b[NT][4];
+    for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (has[nt] && k < a.K) v = __ldg(reinterpret_cast<const uint4*>(xrow[nt] + k));
-        b[nt][0] = __byte_perm(v.x, v.z, 0x5410);
-        b[nt][1] = __byte_perm(v.x, v.z, 0x7632);
-        b[nt][2] = __byte_perm(v.y, v.w, 0x5410);
-        b[nt][3] = __byte_perm(v.y, v.w, 0x7632);
+      for (int r = 0; r < 2; ++r) {
+        scale[i][r] = __ldg(a.scales + srow[i][r] + at);
+        zero[i][r] = 8;
       }
+    if (a.zeros) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const uint32_t sz0 = VEC == 4 ? s.sz[2 * mt] : __shfl_sync(kFull, s.sz[2 * mt], (lane & ~3) + l);
-        const uint32_t sz1 = VEC == 4 ? s.sz[2 * mt + 1] : __shfl_sync(kFull, s.sz[2 * mt + 1], (lane & ~3) + l);
-        const uint32_t z0 = 0x43004300u + (sz0 & 255u) * 0x10001u, z1 = 0x43004300u + (sz1 & 255u) * 0x10001u;
-        const uint32_t u = s.w[2 * mt][w], v = s.w[2 * mt + 1][w];
-        const uint32_t a0 = codes<0>(u, z0), a1 = codes<0>(v, z1), a2 = codes<1>(u, z0), a3 = codes<1>(v, z1);
-        const uint32_t c0 = codes<2>(u, z0), c1 = codes<2>(v, z1), c2 = codes<3>(u, z0), c3 = codes<3>(v, z1);
+      for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_bf16(acc[mt][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_bf16(acc[mt][nt], c0, c1, c2, c3, b[nt][2], b[nt][3]);
-        if ((w + 1) % VEC == 0) {  // the group is complete
-          const float s0 = bf16_hi(sz0), s1 = bf16_hi(sz1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              total[mt][nt][e] = __fmaf_rn(e < 2 ? s0 : s1, acc[mt][nt][e], total[mt][nt][e]);
-              acc[mt][nt][e] = 0.f;
-            }
-        }
-      }
+        for (int r = 0; r < 2; ++r) zero[i][r] = __ldg(a.zeros + srow[i][r] + at);
     }
   };
-
-  Step<MT, VEC> s0, s1;
-  int c = warp;
-  if (c < chunks) load_step<MT, VEC>(s0, a, row, srow, c, t);
-  if (c + kWarps < chunks) load_step<MT, VEC>(s1, a, row, srow, c + kWarps, t);
-  for (; c < chunks; c += 2 * kWarps) {
-    consume(s0, c);
-    if (c + 2 * kWarps < chunks) load_step<MT, VEC>(s0, a, row, srow, c + 2 * kWarps, t);
-    if (c + kWarps < chunks) {
-      consume(s1, c + kWarps);
-      if (c + 3 * kWarps < chunks) load_step<MT, VEC>(s1, a, row, srow, c + 3 * kWarps, t);
-    }
-  }
-
+  const uint16_t* xrow[NT];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nt = 0; nt < NT; ++nt) xrow[nt] = a.x + min(m0 + nt * 8 + g, a.M - 1) * a.ldx;
+  auto load_x = [&](int c, uint4 (&v)[NT][4]) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        red[warp][nt * 8 + 2 * t + (e & 1)][mt * 16 + g + 8 * (e >> 1)] = total[mt][nt][e];
-  __syncthreads();
-  for (int x = tid; x < ROWS * COLS; x += kThreads) {
-    const int r = x % ROWS, col = x / ROWS, n = n0 + r;
-    const long long m = m0 + col;
-    if (n >= a.N || m >= a.M) continue;
-    float z[1] = {0.f};
+      for (int w = 0; w < 4; ++w) {
+        const int k = c * kChunk + w / VEC * 32 * VEC + t * 8 * VEC + w % VEC * 8;
+        v[nt][w] = __ldg(reinterpret_cast<const uint4*>(xrow[nt] + (VEC == 4 ? k : min(k, a.K - 8))));
+      }
+  };
+
+  float total[kTiles][NT][4] = {};
+  uint4 xn[NT][4];
+  uint32_t sn[kTiles][2], zn[kTiles][2];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) z[0] += red[w][col][r];
+  for (int st = 0; st < kAhead; ++st) issue(c0 + st / kTiles, st % kTiles);
+  load_x(min(c0, chunks - 1), xn);
+  load_scales(min(c0, chunks - 1), sn, zn);
+#pragma unroll 1
+  for (int c = c0; c < c1; ++c) {
+    uint32_t b[NT][4][4], sz[kTiles][2];  // (a scale in the high half, its zero in the low byte)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint4 v = xn[nt][w];
+        if (VEC < 4 && c * kChunk + w / VEC * 32 * VEC + t * 8 * VEC >= a.K) v = make_uint4(0, 0, 0, 0);
+        b[nt][w][0] = __byte_perm(v.x, v.z, 0x5410);
+        b[nt][w][1] = __byte_perm(v.x, v.z, 0x7632);
+        b[nt][w][2] = __byte_perm(v.y, v.w, 0x5410);
+        b[nt][w][3] = __byte_perm(v.y, v.w, 0x7632);
+      }
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) sz[i][r] = sn[i][r] << 16 | zn[i][r];
+    load_x(min(c + 1, c1 - 1), xn);
+    load_scales(min(c + 1, c1 - 1), sn, zn);
+    const uint32_t here = base + ((c - c0) & 1) * kTiles * kStageBytes + g * kPitch + t * VEC * 4;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      issue(c + (i + kAhead) / kTiles, (i + kAhead) % kTiles);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+      __syncwarp();
+      uint32_t u[4], v[4];
+#pragma unroll
+      for (int l = 0; l < L; ++l) {
+        const uint32_t p = here + i * kStageBytes + l * VEC * 16;
+        if constexpr (VEC == 4) {
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(p) : "memory");
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(p + 8 * kPitch) : "memory");
+        } else if constexpr (VEC == 2) {
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[2 * l]), "=r"(u[2 * l + 1]) : "r"(p) : "memory");
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[2 * l]), "=r"(v[2 * l + 1]) : "r"(p + 8 * kPitch) : "memory");
+        } else {
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u[l]) : "r"(p) : "memory");
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[l]) : "r"(p + 8 * kPitch) : "memory");
+        }
+      }
+#pragma unroll
+      for (int l = 0; l < L; ++l) {
+        const uint32_t sz0 = VEC == 4 ? sz[i][0] : __shfl_sync(kFull, sz[i][0], (lane & ~3) + l);
+        const uint32_t sz1 = VEC == 4 ? sz[i][1] : __shfl_sync(kFull, sz[i][1], (lane & ~3) + l);
+        const uint32_t z0 = 0x43004300u + (sz0 & 255u) * 0x10001u, z1 = 0x43004300u + (sz1 & 255u) * 0x10001u;
+        float acc[NT][4] = {}, acc2[NT][4] = {};  // (two chains of products)
+#pragma unroll
+        for (int w = l * VEC; w < (l + 1) * VEC; ++w) {
+          const uint32_t a0 = codes<0>(u[w], z0), a1 = codes<0>(v[w], z1), a2 = codes<1>(u[w], z0), a3 = codes<1>(v[w], z1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_bf16(acc[nt], a0, a1, a2, a3, b[nt][w][0], b[nt][w][1]);
+          const uint32_t d0 = codes<2>(u[w], z0), d1 = codes<2>(v[w], z1), d2 = codes<3>(u[w], z0), d3 = codes<3>(v[w], z1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_bf16(acc2[nt], d0, d1, d2, d3, b[nt][w][2], b[nt][w][3]);
+        }
+        const float s0 = bf16_hi(sz0), s1 = bf16_hi(sz1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            total[i][nt][e] = __fmaf_rn(e < 2 ? s0 : s1, acc[nt][e] + acc2[nt][e], total[i][nt][e]);
+      }
+      __syncwarp();
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();  // (the ring is read no more)
+  const int cols = min(COLS, a.M - m0);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (nt * 8 + 2 * t + j < cols) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          red[warp][nt * 8 + 2 * t + j][i * 16 + g] = total[i][nt][j];
+          red[warp][nt * 8 + 2 * t + j][i * 16 + g + 8] = total[i][nt][2 + j];
+        }
+      }
+  __syncthreads();
+  for (int x = tid; x < kRows * cols; x += kThreads) {
+    float z = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) z += red[w][x / kRows][x % kRows];
+    part[x / kRows][x % kRows] = z;
+  }
+  if (a.split > 1) tc::cluster_sync();
+  else __syncthreads();
+  // the CTAs of a cluster add their sums in the order of their ranks, each for a part of the outputs
+  for (int x = (int)rank * kThreads + tid; x < kRows * cols; x += (int)a.split * kThreads) {
+    const int r = x % kRows, col = x / kRows, n = n0 + r;
+    const long long m = m0 + col;
+    float z[1] = {0.f};
+    if (a.split > 1) {
+      for (unsigned q = 0; q < a.split; ++q) z[0] += tc::ld_cluster(tc::cluster_addr(&part[col][r], q));
+    } else {
+      z[0] = part[col][r];
+    }
+    if (n >= a.N) continue;
     if (a.bias) z[0] += __uint_as_float((uint32_t)a.bias[n] << 16);
     lin::activate(z, a.act);
     if (a.out_f32) {
@@ -208,28 +260,36 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       static_cast<uint16_t*>(a.out)[m * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z[0]));
     }
   }
+  if (a.split > 1) tc::cluster_sync();  // (no CTA leaves while its sums are read)
 }
 
-template <int MT, int NT, int VEC>
-cudaError_t launch(const Args& a, void* stream) {
+template <int NT, int VEC>
+cudaError_t launch(Args a, void* stream) {
+  // CTAs for three an SM, as long as a warp keeps two chunks of k
+  const long long slabs = ((a.N + kRows - 1LL) / kRows) * ((a.M + 8 * NT - 1LL) / (8 * NT));
+  const int chunks = (a.K + kChunk - 1) / kChunk;
+  a.split = 1;
+  while (a.split < 8 && slabs * a.split < 3LL * tc::num_sms() && chunks >= (int)a.split * 2 * kWarps * 2) a.split *= 2;
+  if (slabs * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  const long long ctas = ((a.N + 16 * MT - 1LL) / (16 * MT)) * ((a.M + 8 * NT - 1LL) / (8 * NT));
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.gridDim = dim3((unsigned)(slabs * a.split), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, rows_kernel<MT, NT, VEC>, a);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, rows_kernel<NT, VEC>, a);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int MT, int NT>
+template <int NT>
 cudaError_t by_group(const Args& a, int group, void* stream) {
-  return group == 128 ? launch<MT, NT, 4>(a, stream) : group == 64 ? launch<MT, NT, 2>(a, stream) : launch<MT, NT, 1>(a, stream);
+  return group == 128 ? launch<NT, 4>(a, stream) : group == 64 ? launch<NT, 2>(a, stream) : launch<NT, 1>(a, stream);
 }
 
 }  // namespace w4
@@ -255,11 +315,7 @@ int linear_w4_launch(const LinearW4Launch& L, std::string* err) {
   a.N = L.N;
   a.K = L.K;
   a.groups = L.K / L.group;
-  // 32 rows of W a CTA halve the reads of x; 16 where 32 would leave SMs without a CTA
-  const bool wide = (L.N + 31) / 32 >= 2 * tc::num_sms();
-  cudaError_t e;
-  if (L.M <= 8) e = wide ? w4::by_group<2, 1>(a, L.group, L.stream) : w4::by_group<1, 1>(a, L.group, L.stream);
-  else e = wide ? w4::by_group<2, 2>(a, L.group, L.stream) : w4::by_group<1, 2>(a, L.group, L.stream);
+  const cudaError_t e = L.M <= 8 ? w4::by_group<1>(a, L.group, L.stream) : w4::by_group<2>(a, L.group, L.stream);
   if (e == cudaSuccess) return SV_OK;
   *err = std::string("linear_w4 launch: ") + cudaGetErrorString(e);
   return SV_ERR_CUDA;
