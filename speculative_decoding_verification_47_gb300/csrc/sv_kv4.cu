@@ -339,7 +339,7 @@ struct Shape {
   static constexpr int kTileBytes = 2 * kTok * kRowBytes + 2 * kTok * 4;  // K, V, (s, m) of both
   static constexpr int kRing = kWarps * kStages * kTileBytes;
   static constexpr int kPart = kRows * (D + 2);  // floats of a part in memory
-  static constexpr int kMinCtas = NT == 1 ? 4 : 3;
+  static constexpr int kMinCtas = NT == 1 ? 3 : 2;  // (two tiles a turn want 160 registers, two blocks of columns 230)
   // shared memory beside the ring: lists, barriers, and the fragments of Q of two blocks of columns (bytes, about)
   static constexpr int kStatic = 5000 + kWarps * (kRows * D * 2 + (NT == 1 ? 0 : NT * D * 16));
 };
