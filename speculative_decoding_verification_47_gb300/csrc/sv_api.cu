@@ -674,8 +674,8 @@ sv_status sv_linear_w4(const void* x, int64_t ldx, const void* W, int64_t ldw, c
   L.K = K;
   if (L.ldx < K || L.ldw < K / 2 || L.ldr < N || L.ldo < N)
     return fail(SV_ERR_SHAPE, "row strides must be 0 or at least the row's length");
-  if (L.ldx % 8 != 0 || L.ldw % 16 != 0)
-    return fail(SV_ERR_SHAPE, "row strides of x and W must be multiples of 16 bytes");
+  if (L.ldx % 8 != 0 || L.ldw % 16 != 0 || L.ldw >= (1LL << 38))
+    return fail(SV_ERR_SHAPE, "row strides of x and W must be multiples of 16 bytes, W's below 2^38");
   if (residual == out && L.ldr != L.ldo) return fail(SV_ERR_ARG, "residual over out needs its row stride");
   if (out == x || out == W) return fail(SV_ERR_ARG, "out must not be x or W");
   if (!workspace || !aligned(workspace, 256))
@@ -683,6 +683,7 @@ sv_status sv_linear_w4(const void* x, int64_t ldx, const void* W, int64_t ldw, c
   if (workspace_bytes < sv::linear_w4_workspace_bytes(M, N, K))
     return fail(SV_ERR_WORKSPACE, "workspace smaller than sv_linear_w4_workspace_size()");
   L.workspace = workspace;
+  L.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
   L.stream = stream;
   std::string err;
   const int s = sv::linear_w4_launch(L, &err);

@@ -233,6 +233,7 @@ struct LinearW4Launch {
   int M, N, K;
   void* workspace;
   void* stream;
+  int wait_tries = kWaitTries;
 };
 
 // Enqueue the product with 4-bit weights.  Returns an sv_status; fills *err on failure.

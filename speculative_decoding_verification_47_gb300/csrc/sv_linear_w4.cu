@@ -16,6 +16,7 @@
 // largest of the 128 values, what is smaller counts as 0.
 #include <atomic>
 #include <cstdint>
+#include <string>
 
 #include "sv_act.cuh"
 #include "sv_tc.cuh"
@@ -23,7 +24,7 @@
 namespace sv {
 namespace w4 {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 128;  // k of a warp's step
 constexpr uint32_t kFull = 0xffffffffu;
@@ -42,6 +43,8 @@ struct Args {
   long long ldo;
   int act, out_f32, M, N, K, groups;
   unsigned split;  // CTAs that share K
+  uint32_t* flags;
+  long long clocks;  // of a wait; 0: none is waited for
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -75,6 +78,32 @@ __device__ __forceinline__ uint32_t to_f16x2(uint32_t v, uint32_t low) {
   return (__vmaxu2(v & 0x7fff7fffu, low) - low) << 3 | (v & 0x80008000u);
 }
 
+// A tile's outputs from the sums part[column][row] of a cluster's CTAs, added in the order of their ranks; each
+// CTA writes a share of them.
+template <int ROWS, int THREADS>
+__device__ __forceinline__ void finish(const Args& a, const float* part, int n0, int m0, int cols, unsigned rank) {
+  for (int x = (int)rank * THREADS + (int)threadIdx.x; x < ROWS * cols; x += (int)a.split * THREADS) {
+    const int n = n0 + x % ROWS;
+    const long long m = m0 + x / ROWS;
+    float z[1] = {0.f};
+    if (a.split > 1) {
+      for (unsigned q = 0; q < a.split; ++q) z[0] += tc::ld_cluster(tc::cluster_addr(part + x, q));
+    } else {
+      z[0] = part[x];
+    }
+    if (n >= a.N) continue;
+    if (a.bias) z[0] += __uint_as_float((uint32_t)a.bias[n] << 16);
+    lin::activate(z, a.act);
+    if (a.out_f32) {
+      if (a.res) z[0] += static_cast<const float*>(a.res)[m * a.ldr + n];
+      static_cast<float*>(a.out)[m * a.ldo + n] = z[0];
+    } else {
+      if (a.res) z[0] += __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.res)[m * a.ldr + n] << 16);
+      static_cast<uint16_t*>(a.out)[m * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z[0]));
+    }
+  }
+}
+
 __device__ __forceinline__ void cp16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
@@ -89,21 +118,18 @@ constexpr int kStages = 8;   // of a warp
 constexpr int kAhead = 6;    // steps on their way
 constexpr int kStageBytes = 16 * kPitch;
 
-// NT blocks of 8 rows of x, tiles of 16 rows of W (as many as registers hold the sums of); VEC words (VEC * 32 k)
-// are a group.
-template <int NT>
-struct Shape {
-  static constexpr int kTiles = NT == 1 ? 8 : 4, kRows = 16 * kTiles;
-  static constexpr int kCtas = 3;  // of an SM
-};
+constexpr int kTiles = 4;    // of a CTA: more share the work on x, fewer want fewer registers
+constexpr int kRows = 16 * kTiles;
+constexpr int kCtas = 2;     // of an SM
 
-template <int NT, int VEC>
-__global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) rows_kernel(const __grid_constant__ Args a) {
-  constexpr int COLS = 8 * NT, L = 4 / VEC, kTiles = Shape<NT>::kTiles, kRows = Shape<NT>::kRows;
-  __shared__ __align__(16) uint8_t ring[kWarps][kStages][kStageBytes];
+// Up to 8 rows of x (a block of 8 of more).  VEC words (VEC * 32 k) are a group.
+template <int VEC>
+__global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_constant__ Args a) {
+  constexpr int COLS = 8, L = 4 / VEC;
+  extern __shared__ __align__(16) uint8_t ring[];  // [kWarps][kStages][kStageBytes]
   __shared__ float part[COLS][kRows];
   float (*red)[COLS][kRows] = reinterpret_cast<float (*)[COLS][kRows]>(ring);  // behind the products
-  static_assert(sizeof(ring) >= kWarps * COLS * kRows * 4, "the warps' sums fit over the ring");
+  static_assert(kWarps * kStages * kStageBytes >= kWarps * COLS * kRows * 4, "the warps' sums fit over the ring");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   pdl_wait();
@@ -111,8 +137,9 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) rows_kernel(const 
   const int blocks = (a.M + COLS - 1) / COLS, slab = (int)(block / blocks);
   const int n0 = slab * kRows, m0 = (int)(block - slab * blocks) * COLS;  // (CTAs of the same rows of W are neighbours)
   const int chunks = (a.K + kChunk - 1) / kChunk, workers = (int)a.split * kWarps, me = (int)rank * kWarps + warp;
-  const int c0 = (int)((long long)chunks * me / workers), c1 = (int)((long long)chunks * (me + 1) / workers);
-  const uint32_t base = smem_addr(ring[warp]);
+  // (neighbours in a row of W are read at about the same time: runs of 64 bytes alone are slow)
+  const int c0 = me, c1 = chunks;
+  const uint32_t base = smem_addr(ring) + warp * kStages * kStageBytes;
   // bytes 16 t .. of rows g and g + 8 of a tile
   const int n_mine = n0 + g;
   const bool full = n0 + kRows <= a.N;  // (behind the last row the last one's codes again)
@@ -132,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) rows_kernel(const 
         cp16(where, p + min(n_mine + 16 * i, a.N - 1) * a.ldw, there);
         cp16(where + 8 * kPitch, p + min(n_mine + 16 * i + 8, a.N - 1) * a.ldw, there);
       }
-      next += i == kTiles - 1 ? kChunk / 2 - (2 * kTiles - 2) * by8 : 2 * by8;
+      next += i == kTiles - 1 ? workers * (kChunk / 2) - (2 * kTiles - 2) * by8 : 2 * by8;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -153,39 +180,34 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) rows_kernel(const 
         zero[q][r] = __ldg(a.zeros ? a.zeros + at : reinterpret_cast<const uint8_t*>(a.scales + at));
       }
   };
-  const uint16_t* xrow[NT];
+  const uint16_t* xrow = a.x + min(m0 + g, a.M - 1) * a.ldx;
+  auto load_x = [&](int c, uint4 (&v)[4]) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) xrow[nt] = a.x + min(m0 + nt * 8 + g, a.M - 1) * a.ldx;
-  auto load_x = [&](int c, uint4 (&v)[NT][4]) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int k = c * kChunk + w / VEC * 32 * VEC + t * 8 * VEC + w % VEC * 8;
-        v[nt][w] = __ldg(reinterpret_cast<const uint4*>(xrow[nt] + (VEC == 4 ? k : min(k, a.K - 8))));
-      }
+    for (int w = 0; w < 4; ++w) {
+      const int k = c * kChunk + w / VEC * 32 * VEC + t * 8 * VEC + w % VEC * 8;
+      v[w] = __ldg(reinterpret_cast<const uint4*>(xrow + (VEC == 4 ? k : min(k, a.K - 8))));
+    }
   };
 
-  float total[kTiles][NT][4] = {};
-  uint4 xn[NT][4];
+  float total[kTiles][4] = {};
+  uint4 xn[4];
   uint16_t sn[Q][2];
   uint8_t zn[Q][2];
 #pragma unroll
-  for (int st = 0; st < kAhead; ++st) issue(c0 + st / kTiles, st % kTiles, st);
+  for (int st = 0; st < kAhead; ++st) issue(c0 + st / kTiles * workers, st % kTiles, st);
   load_x(min(c0, chunks - 1), xn);
   load_scales(min(c0, chunks - 1), sn, zn);
   int slot = 0;  // of the chunk's first step
 #pragma unroll 1
-  for (int c = c0; c < c1; ++c) {
-    uint32_t b[NT][4][4], sz[Q][2];  // (a scale in the high half, its zero in the low byte)
-    float undo[NT][2];  // x's power of two, of the lane's columns
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+  for (int c = c0; c < c1; c += workers) {
+    uint32_t b[4][4], sz[Q][2];  // (a scale in the high half, its zero in the low byte)
+    float undo[2];  // x's power of two, of the lane's columns
+    {
       uint32_t top = 0;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        if (VEC < 4 && c * kChunk + w / VEC * 32 * VEC + t * 8 * VEC >= a.K) xn[nt][w] = make_uint4(0, 0, 0, 0);
-        const uint4 v = xn[nt][w];
+        if (VEC < 4 && c * kChunk + w / VEC * 32 * VEC + t * 8 * VEC >= a.K) xn[w] = make_uint4(0, 0, 0, 0);
+        const uint4 v = xn[w];
         top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
                                      __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
       }
@@ -196,28 +218,28 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) rows_kernel(const 
       const uint32_t low = (uint32_t)max(ex - 30, 0) * 0x00800080u, low16 = low + 4 * 0x00800080u;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint4 v = xn[nt][w];
-        b[nt][w][0] = to_f16x2(__byte_perm(v.x, v.z, 0x5410), low);
-        b[nt][w][1] = to_f16x2(__byte_perm(v.x, v.z, 0x7632), low16);
-        b[nt][w][2] = to_f16x2(__byte_perm(v.y, v.w, 0x5410), low);
-        b[nt][w][3] = to_f16x2(__byte_perm(v.y, v.w, 0x7632), low16);
+        const uint4 v = xn[w];
+        b[w][0] = to_f16x2(__byte_perm(v.x, v.z, 0x5410), low);
+        b[w][1] = to_f16x2(__byte_perm(v.x, v.z, 0x7632), low16);
+        b[w][2] = to_f16x2(__byte_perm(v.y, v.w, 0x5410), low);
+        b[w][3] = to_f16x2(__byte_perm(v.y, v.w, 0x7632), low16);
       }
       // 2^(low - 112): fp16's exponents are biased by 15, bf16's by 127; NaN for a row that is not finite
       const int e = max(ex - 30, 0) + 15;
       const float f = ex == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)e << 23);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) undo[nt][j] = __shfl_sync(kFull, f, (2 * t + j) * 4);
+      for (int j = 0; j < 2; ++j) undo[j] = __shfl_sync(kFull, f, (2 * t + j) * 4);
     }
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
       for (int r = 0; r < 2; ++r) sz[q][r] = (uint32_t)sn[q][r] << 16 | (a.zeros ? zn[q][r] : 8u);
-    load_x(min(c + 1, c1 - 1), xn);
-    load_scales(min(c + 1, c1 - 1), sn, zn);
+    load_x(min(c + workers, c1 - 1), xn);
+    load_scales(min(c + workers, c1 - 1), sn, zn);
     const uint32_t here = base + g * kPitch + t * VEC * 4;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
-      issue(c + (i + kAhead) / kTiles, (i + kAhead) % kTiles, (slot + i + kAhead) & (kStages - 1));
+      issue(c + (i + kAhead) / kTiles * workers, (i + kAhead) % kTiles, (slot + i + kAhead) & (kStages - 1));
       asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
       __syncwarp();
       uint32_t u[4], v[4];
@@ -241,24 +263,17 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) rows_kernel(const 
         const uint32_t sz1 = __shfl_sync(kFull, sz[(i * L + l) / 4][1], (lane & ~3) + (i * L + l) % 4);
         const uint32_t z0 = (sz0 & 255u) * 0x10001u + kLess1024, z1 = (sz1 & 255u) * 0x10001u + kLess1024;
         const uint32_t y0 = (sz0 & 255u) * 0x100010u + kLess1024, y1 = (sz1 & 255u) * 0x100010u + kLess1024;
-        float acc[NT][4] = {}, acc2[NT][4] = {};  // (two chains of products)
+        float acc[4] = {}, acc2[4] = {};  // (two chains of products)
 #pragma unroll
         for (int w = l * VEC; w < (l + 1) * VEC; ++w) {
-          const uint32_t a0 = low_codes(u[w], z0), a1 = low_codes(v[w], z1), a2 = high_codes(u[w], y0), a3 = high_codes(v[w], y1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], a0, a1, a2, a3, b[nt][w][0], b[nt][w][1]);
+          mma_f16(acc, low_codes(u[w], z0), low_codes(v[w], z1), high_codes(u[w], y0), high_codes(v[w], y1), b[w][0], b[w][1]);
           const uint32_t u8 = u[w] >> 8, v8 = v[w] >> 8;
-          const uint32_t d0 = low_codes(u8, z0), d1 = low_codes(v8, z1), d2 = high_codes(u8, y0), d3 = high_codes(v8, y1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(acc2[nt], d0, d1, d2, d3, b[nt][w][2], b[nt][w][3]);
+          mma_f16(acc2, low_codes(u8, z0), low_codes(v8, z1), high_codes(u8, y0), high_codes(v8, y1), b[w][2], b[w][3]);
         }
         const float s0 = bf16_hi(sz0), s1 = bf16_hi(sz1);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            total[i][nt][e] =
-                __fmaf_rn(e < 2 ? s0 : s1, (acc[nt][e] + acc2[nt][e]) * undo[nt][e & 1], total[i][nt][e]);
+        for (int e = 0; e < 4; ++e)
+          total[i][e] = __fmaf_rn(e < 2 ? s0 : s1, (acc[e] + acc2[e]) * undo[e & 1], total[i][e]);
       }
       __syncwarp();
     }
@@ -268,16 +283,14 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) rows_kernel(const 
   __syncthreads();  // (the ring is read no more)
   const int cols = min(COLS, a.M - m0);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int j = 0; j < 2; ++j)
+    if (2 * t + j < cols) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (nt * 8 + 2 * t + j < cols) {
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          red[warp][nt * 8 + 2 * t + j][i * 16 + g] = total[i][nt][j];
-          red[warp][nt * 8 + 2 * t + j][i * 16 + g + 8] = total[i][nt][2 + j];
-        }
+      for (int i = 0; i < kTiles; ++i) {
+        red[warp][2 * t + j][i * 16 + g] = total[i][j];
+        red[warp][2 * t + j][i * 16 + g + 8] = total[i][2 + j];
       }
+    }
   __syncthreads();
   for (int x = tid; x < kRows * cols; x += kThreads) {
     float z = 0.f;
@@ -287,43 +300,291 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) rows_kernel(const 
   }
   if (a.split > 1) tc::cluster_sync();
   else __syncthreads();
-  // the CTAs of a cluster add their sums in the order of their ranks, each for a part of the outputs
-  for (int x = (int)rank * kThreads + tid; x < kRows * cols; x += (int)a.split * kThreads) {
-    const int r = x % kRows, col = x / kRows, n = n0 + r;
-    const long long m = m0 + col;
-    float z[1] = {0.f};
-    if (a.split > 1) {
-      for (unsigned q = 0; q < a.split; ++q) z[0] += tc::ld_cluster(tc::cluster_addr(&part[col][r], q));
-    } else {
-      z[0] = part[col][r];
-    }
-    if (n >= a.N) continue;
-    if (a.bias) z[0] += __uint_as_float((uint32_t)a.bias[n] << 16);
-    lin::activate(z, a.act);
-    if (a.out_f32) {
-      if (a.res) z[0] += static_cast<const float*>(a.res)[m * a.ldr + n];
-      static_cast<float*>(a.out)[m * a.ldo + n] = z[0];
-    } else {
-      if (a.res) z[0] += __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.res)[m * a.ldr + n] << 16);
-      static_cast<uint16_t*>(a.out)[m * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z[0]));
-    }
-  }
+  finish<kRows, kThreads>(a, part[0], n0, m0, cols, rank);
   if (a.split > 1) tc::cluster_sync();  // (no CTA leaves while its sums are read)
 }
 
-template <int NT, int VEC>
-cudaError_t launch(Args a, void* stream) {
-  // as many CTAs as the card holds at once, as long as a warp keeps a chunk of k
-  constexpr int rows = Shape<NT>::kRows;
-  const long long slabs = ((a.N + rows - 1LL) / rows) * ((a.M + 8 * NT - 1LL) / (8 * NT));
-  const int chunks = (a.K + kChunk - 1) / kChunk;
-  const long long fit = (long long)tc::num_sms() * Shape<NT>::kCtas / slabs;
+// ---------------------------------------------------------------------------
+// More rows of x: the 5th-generation tensor cores.  A CTA takes 128 rows of W by TM rows of x and a part of K, in
+// blocks of 128 k.  Codes arrive by TMA; eight warps make them bf16 integers (code less zero, exact) in the
+// 128-row operand's tile and bring x's block beside it; a thread issues a group's products into one of kAccs
+// accumulators of tensor memory; four warps take that out, times the group's scale, and add it to their float32 sums
+// in registers.  x's 8 values of a chunk follow the order of the codes' pairs (0, 4), (1, 5), (2, 6), (3, 7).
+// ---------------------------------------------------------------------------
+constexpr int kCodeWarps = 8;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kSumWarp = 10;
+constexpr int kTcThreads = 14 * 32;
+constexpr int kTcRows = 128;
+constexpr int kRaw = 6;              // blocks of codes on their way
+constexpr int kRawBytes = kTcRows * 64;
+constexpr int kAtom = kTcRows * 128;  // 128 rows by 64 k
+constexpr int kAccs = 4;
+
+template <int TM>
+struct TcShape {
+  static constexpr int kA = 2 * kAtom, kX = 2 * TM * 128;  // of a block
+  static constexpr int kSmem = 2 * kA + 2 * kX + kRaw * kRawBytes + 1024;
+  static constexpr uint32_t kColumns = kAccs * TM < 32 ? 32 : kAccs * TM;
+  static constexpr int kChunks = TM * 16 / (kCodeWarps * 32);  // 16-byte pieces of x's block of a thread
+  static_assert(2 * kA >= TM * kTcRows * 4, "the sums fit over the codes' tiles");
+};
+
+// four pairs of bf16 (code less zero) of a word; less = -(128 + zero) twice
+template <int J>
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t less) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * J)), "n"(0x000f000f), "r"(0x43004300u));
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(less));
+  return r;
+}
+// true in one lane of a whole warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void sts128(uint32_t p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <int TM, int GROUP>
+__global__ void __launch_bounds__(kTcThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Args a) {
+  using S = TcShape<TM>;
+  constexpr int PER = 128 / GROUP;  // groups of a block
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], a_full[2], a_empty[2], acc_full[kAccs], acc_empty[kAccs], done;
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed, issued;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);  // (the same in the whole warp, and known to be)
+  const unsigned block = blockIdx.x / a.split, rank = blockIdx.x - block * a.split;
+  const int blocks = (a.M + TM - 1) / TM, slab = (int)(block / blocks);
+  const int n0 = slab * kTcRows, m0 = (int)(block - slab * blocks) * TM;
+  const int all = (a.K + 127) / 128;
+  const int b0 = (int)((long long)all * rank / a.split), b1 = (int)((long long)all * (rank + 1) / a.split);
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t at_a = smem_addr(tiles), at_x = at_a + 2 * S::kA, at_raw = at_x + 2 * S::kX;
+  if (tid == 0) {
+    for (int s = 0; s < kRaw; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], kCodeWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&a_full[s], kCodeWarps);
+      mbar_init(&a_empty[s], 1);
+    }
+    for (int s = 0; s < kAccs; ++s) {
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 4);
+    }
+    mbar_init(&done, 1);
+    failed = issued = 0;
+    fence_mbar_init();
+    tc::prefetch_map(&tmW);
+  }
+  if (warp == kLoadWarp) tc::alloc<1>(&tmem_base, S::kColumns);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();
+  // a wait of at most about a second, none at all if `clocks` is 0; who gives up leaves its loop
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (a.clocks > 0 && tc::wait_bounded(bar, parity, a.clocks)) return true;
+    failed = 1;
+    return false;
+  };
+  float total[TM] = {};
+
+  if (warp < kCodeWarps) {
+    const int r = tid & 127, half = tid >> 7;  // 64 k of a row
+    const int n = min(n0 + r, a.N - 1);
+    const uint8_t* zrow = a.zeros ? a.zeros + (uint32_t)n * a.groups : nullptr;
+    constexpr int Z = GROUP == 32 ? 2 : 1;  // groups of 64 k, or one that has more
+    auto load_zeros = [&](int b, uint32_t (&z)[Z]) {
+#pragma unroll
+      for (int q = 0; q < Z; ++q) {
+        const int group = GROUP == 128 ? b : b * PER + half * Z + q;
+        z[q] = zrow ? __ldg(zrow + min(group, a.groups - 1)) : 8u;
+      }
+    };
+    const uint16_t* xrow[S::kChunks];
+#pragma unroll
+    for (int q = 0; q < S::kChunks; ++q) xrow[q] = a.x + min(m0 + ((tid + q * 256) >> 4), a.M - 1) * a.ldx;
+    auto load_x = [&](int b, uint4 (&v)[S::kChunks]) {
+      const int k = min(b * 128 + (tid & 15) * 8, a.K - 8);
+#pragma unroll
+      for (int q = 0; q < S::kChunks; ++q) v[q] = __ldg(reinterpret_cast<const uint4*>(xrow[q] + k));
+      // (what is behind x's end becomes 0 where it is stored: a choice here would wait for the load)
+    };
+    uint32_t zn[Z];
+    uint4 xn[S::kChunks];
+    if (b0 < b1) {
+      load_zeros(b0, zn);
+      load_x(b0, xn);
+    }
+    const uint32_t row_a = half * kAtom + r * 128, flip = (uint32_t)(r & 7);
+    const uint32_t raw_row = r * 64, raw_flip = (uint32_t)(r >> 1) & 3;
+    for (int b = b0, g = 0; b < b1; ++b, ++g) {
+      const int s = g % kRaw, side = g & 1;
+      uint32_t less[Z];
+#pragma unroll
+      for (int q = 0; q < Z; ++q) less[q] = zn[q] * 0x10001u + 0xc300c300u;
+      uint4 x[S::kChunks];
+#pragma unroll
+      for (int q = 0; q < S::kChunks; ++q) x[q] = xn[q];
+      load_zeros(min(b + 1, b1 - 1), zn);
+      load_x(min(b + 1, b1 - 1), xn);
+      if (!wait(&raw_full[s], g / kRaw & 1)) break;
+      uint32_t w[8];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                     : "r"(at_raw + s * kRawBytes + raw_row + (((uint32_t)(half * 2 + c) ^ raw_flip) << 4))
+                     : "memory");
+      if (g >= 2 && !wait(&a_empty[side], (g / 2 - 1) & 1)) break;
+      const uint32_t to = at_a + side * S::kA + row_a;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t l = less[Z == 2 ? c / 4 : 0];
+        sts128(to + ((c ^ flip) << 4), pair_of<0>(w[c], l), pair_of<1>(w[c], l), pair_of<2>(w[c], l), pair_of<3>(w[c], l));
+      }
+#pragma unroll
+      for (int q = 0; q < S::kChunks; ++q) {
+        const int m = (tid + q * 256) >> 4, c = tid & 15;
+        const uint4 v = m0 + m < a.M && b * 128 + c * 8 < a.K ? x[q] : make_uint4(0, 0, 0, 0);
+        sts128(at_x + side * S::kX + (c >> 3) * TM * 128 + m * 128 + (((c & 7) ^ (m & 7)) << 4), __byte_perm(v.x, v.z, 0x5410),
+               __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the tensor cores read what was stored)
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&a_full[side]);
+        mbar_arrive(&raw_empty[s]);
+      }
+    }
+  } else if (warp == kLoadWarp) {
+    if (lane == 0) {
+      int g = 0;
+      for (int b = b0; b < b1; ++b, ++g) {
+        const int s = g % kRaw;
+        if (g >= kRaw && !wait(&raw_empty[s], (g / kRaw - 1) & 1)) break;
+        mbar_arrive_expect_tx(&raw_full[s], kRawBytes);
+        tc::tma_load(tiles + 2 * S::kA + 2 * S::kX + s * kRawBytes, &tmW, b * 64, n0, &raw_full[s]);
+      }
+      issued = g;
+    }
+  } else if (warp == kMmaWarp) {
+    // The whole warp takes this way, so that descriptors are computed in uniform registers, where the instruction
+    // wants them; one lane issues.
+    constexpr uint32_t id = tc::idesc(false, false, 128, TM);
+    const uint32_t low_a = tc::desc_low(at_a, 16), low_x = tc::desc_low(at_x, 16);
+    const bool elected = elect_one();
+    int acc = 0;
+    bool ok = true;
+    for (int b = b0, g = 0; b < b1 && ok; ++b, ++g) {
+      const int side = g & 1;
+      const uint32_t block_a = low_a + side * (S::kA >> 4), block_x = low_x + side * (S::kX >> 4);
+      ok = __all_sync(kFull, wait(&a_full[side], g / 2 & 1));
+      tc::fence_after();
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        if (!ok || b * PER + q >= a.groups) break;
+        const int slot = acc % kAccs;
+        ok = acc < kAccs || __all_sync(kFull, wait(&acc_empty[slot], (acc / kAccs - 1) & 1));
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t d = tmem + slot * TM;
+        if (elected) {
+#pragma unroll
+          for (int i = 0; i < GROUP / 16; ++i) {
+            constexpr int kSteps = GROUP / 16;
+            const int k = q * kSteps + i;  // of the block's eight steps
+            tc::mma_low(d, block_a + (((k >> 2) * kAtom + (k & 3) * 32) >> 4), block_x + (((k >> 2) * TM * 128 + (k & 3) * 32) >> 4),
+                        id, i != 0);
+          }
+          tc::commit<1>(smem_addr(&acc_full[slot]));
+        }
+        ++acc;
+      }
+      if (ok && elected) tc::commit<1>(smem_addr(&a_empty[side]));
+    }
+    if (elected) tc::commit<1>(smem_addr(&done));  // (nothing arrives behind the CTA's end)
+    if (!tc::wait_bounded(&done, 0)) failed = 1;
+  } else {
+    const int quad = warp & 3, n = min(n0 + quad * 32 + lane, a.N - 1);
+    const uint16_t* srow = a.scales + (uint32_t)n * a.groups;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const int g0 = b0 * PER, g1 = min(b1 * PER, a.groups);
+    uint32_t next = g0 < g1 ? __ldg(srow + g0) : 0;
+    for (int group = g0, acc = 0; group < g1; ++group, ++acc) {
+      const float s = __uint_as_float(next << 16);
+      next = __ldg(srow + min(group + 1, a.groups - 1));
+      const int slot = acc % kAccs;
+      if (!wait(&acc_full[slot], acc / kAccs & 1)) break;
+      tc::fence_after();
+#pragma unroll
+      for (int c = 0; c < TM; c += 16) {
+        uint32_t v[16];
+        tc::ld16(lanes + slot * TM + c, v);
+        tc::ld_wait(v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) total[c + j] = __fmaf_rn(s, __uint_as_float(v[j]), total[c + j]);
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[slot]);
+    }
+  }
+  __syncthreads();
+  const bool lost = failed != 0;  // (the same in every thread)
+  if (lost) {  // a wait ran out: copies and products on their way end first, and the tile is NaN
+    if (tid == 0) {
+      atomicOr(a.flags, SV_FLAG_TIMEOUT);
+      for (int g = issued > kRaw ? issued - kRaw : 0; g < issued; ++g) tc::wait_bounded(&raw_full[g % kRaw], g / kRaw & 1);
+      tc::wait_bounded(&done, 0);
+    }
+    __syncthreads();
+  }
+  float* part = reinterpret_cast<float*>(tiles);  // [TM][128], over the codes' tiles
+  if (warp >= kSumWarp) {
+#pragma unroll
+    for (int c = 0; c < TM; ++c) part[c * kTcRows + (warp & 3) * 32 + lane] = lost ? __uint_as_float(0x7fffffffu) : total[c];
+  }
+  if (a.split > 1) tc::cluster_sync();
+  else __syncthreads();
+  finish<kTcRows, kTcThreads>(a, part, n0, m0, min(TM, a.M - m0), rank);
+  if (a.split > 1) tc::cluster_sync();  // (no CTA leaves while its sums are read)
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kLoadWarp) tc::dealloc<1>(tmem, S::kColumns);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+// Slabs of W times parts of K (at most 8, a cluster): as many CTAs as the card holds at once, as long as each of
+// `workers` of a CTA keeps a step of 128 k.
+template <typename Kernel, typename... A>
+cudaError_t launch(Kernel* kernel, std::atomic<int>* ready, long long slabs, int per_sm, int workers, int threads, int smem,
+                   Args a, void* stream, const A&... map) {
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(1, std::memory_order_release);
+  }
+  const long long fit = (long long)tc::num_sms() * per_sm / slabs;
+  const int steps = (a.K + 127) / 128;
   a.split = (unsigned)(fit < 1 ? 1 : fit > 8 ? 8 : fit);
-  while (a.split > 1 && chunks < (int)a.split * kWarps) --a.split;
+  while (a.split > 1 && steps < (int)a.split * workers) --a.split;
   if (slabs * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(slabs * a.split), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -333,13 +594,43 @@ cudaError_t launch(Args a, void* stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, rows_kernel<NT, VEC>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, map..., a);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int NT>
-cudaError_t by_group(const Args& a, int group, void* stream) {
-  return group == 128 ? launch<NT, 4>(a, stream) : group == 64 ? launch<NT, 2>(a, stream) : launch<NT, 1>(a, stream);
+template <int VEC>
+cudaError_t launch_rows(const Args& a, void* stream) {
+  static std::atomic<int> ready[kMaxDevices];
+  const long long slabs = ((a.N + kRows - 1LL) / kRows) * ((a.M + 7LL) / 8);
+  return launch(rows_kernel<VEC>, ready, slabs, kCtas, kWarps, kThreads, kWarps * kStages * kStageBytes, a, stream);
+}
+
+template <int TM, int GROUP>
+cudaError_t launch_tiles(const Args& a, const CUtensorMap& map, void* stream) {
+  static std::atomic<int> ready[kMaxDevices];
+  const long long slabs = ((a.N + kTcRows - 1LL) / kTcRows) * ((a.M + TM - 1LL) / TM);
+  return launch(tile_kernel<TM, GROUP>, ready, slabs, 1, 2, kTcThreads, TcShape<TM>::kSmem, a, stream, map);
+}
+
+template <int TM>
+cudaError_t tiles_by_group(const Args& a, int group, const CUtensorMap& map, void* stream) {
+  return group == 128  ? launch_tiles<TM, 128>(a, map, stream)
+         : group == 64 ? launch_tiles<TM, 64>(a, map, stream)
+                       : launch_tiles<TM, 32>(a, map, stream);
+}
+
+// Rows of K / 2 bytes of codes in boxes of 64 bytes by 128 rows, 64-byte swizzle, zeros outside.
+bool codes_map(CUtensorMap* map, const LinearW4Launch& L, std::string* err) {
+  const tc::EncodeTiledFn enc = tc::encoder(err);
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)(L.K / 2), (cuuint64_t)L.N};
+  const cuuint64_t strides[1] = {(cuuint64_t)L.ldw};
+  const cuuint32_t box[2] = {64, kTcRows}, estr[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(L.W), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) *err = "linear_w4: cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
+  return r == CUDA_SUCCESS;
 }
 
 }  // namespace w4
@@ -365,7 +656,20 @@ int linear_w4_launch(const LinearW4Launch& L, std::string* err) {
   a.N = L.N;
   a.K = L.K;
   a.groups = L.K / L.group;
-  const cudaError_t e = L.M <= 8 ? w4::by_group<1>(a, L.group, L.stream) : w4::by_group<2>(a, L.group, L.stream);
+  a.flags = static_cast<uint32_t*>(L.workspace);
+  a.clocks = L.wait_tries > 0 ? tc::kWaitClocks : 0;
+  cudaError_t e;
+  if (L.M <= 8) {
+    e = L.group == 128  ? w4::launch_rows<4>(a, L.stream)
+        : L.group == 64 ? w4::launch_rows<2>(a, L.stream)
+                        : w4::launch_rows<1>(a, L.stream);
+  } else {
+    CUtensorMap map;
+    if (!w4::codes_map(&map, L, err)) return SV_ERR_CUDA;
+    e = L.M <= 16   ? w4::tiles_by_group<16>(a, L.group, map, L.stream)
+        : L.M <= 32 ? w4::tiles_by_group<32>(a, L.group, map, L.stream)
+                    : w4::tiles_by_group<64>(a, L.group, map, L.stream);
+  }
   if (e == cudaSuccess) return SV_OK;
   *err = std::string("linear_w4 launch: ") + cudaGetErrorString(e);
   return SV_ERR_CUDA;
