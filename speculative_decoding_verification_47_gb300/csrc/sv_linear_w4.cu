@@ -306,27 +306,30 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
 
 // ---------------------------------------------------------------------------
 // More rows of x: the 5th-generation tensor cores.  A CTA takes 128 rows of W by TM rows of x and a part of K, in
-// blocks of 128 k.  Codes arrive by TMA; eight warps make them bf16 integers (code less zero, exact) in the
-// 128-row operand's tile and bring x's block beside it; a thread issues a group's products into one of kAccs
-// accumulators of tensor memory; four warps take that out, times the group's scale, and add it to their float32 sums
-// in registers.  x's 8 values of a chunk follow the order of the codes' pairs (0, 4), (1, 5), (2, 6), (3, 7).
+// blocks of 128 k.  Codes arrive by TMA; eight warps make them bf16 integers (code less zero, exact) in tensor
+// memory, where the 128-row operand may stand (through shared memory its bytes were the bound), and x's block in shared memory; a thread issues a group's products into one of a few
+// accumulators of tensor memory; four or eight warps take that out, times the group's scale, and add it to their
+// float32 sums in registers.  x's 8 values of a chunk follow the order of the codes' pairs (0, 4), (1, 5), (2, 6), (3, 7).
 // ---------------------------------------------------------------------------
-constexpr int kCodeWarps = 8;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kSumWarp = 10;
-constexpr int kTcThreads = 14 * 32;
+constexpr int kCodeWarps = 8;        // of a team; a team and an issuing warp for the even blocks, another for the odd ones
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kSumWarp = 19;
 constexpr int kTcRows = 128;
 constexpr int kRaw = 6;              // blocks of codes on their way
 constexpr int kRawBytes = kTcRows * 64;
-constexpr int kAtom = kTcRows * 128;  // 128 rows by 64 k
-constexpr int kAccs = 4;
+constexpr int kSides = 4;            // blocks ready for their products, or in them
 
 template <int TM>
 struct TcShape {
-  static constexpr int kA = 2 * kAtom, kX = 2 * TM * 128;  // of a block
-  static constexpr int kSmem = 2 * kA + 2 * kX + kRaw * kRawBytes + 1024;
-  static constexpr uint32_t kColumns = kAccs * TM < 32 ? 32 : kAccs * TM;
+  static constexpr int kAccs = TM == 64 ? 4 : 8;  // sums of a group
+  static constexpr int kX = 2 * TM * 128;  // of a block
+  static constexpr int kPart = TM * kTcRows * 4;
+  static constexpr int kTiles = kSides * kX + kRaw * kRawBytes, kSmem = (kTiles > kPart ? kTiles : kPart) + 1024;
+  static constexpr uint32_t kCodes = kAccs * TM;  // columns of the sums; then 64 of codes for each side
+  static constexpr uint32_t kColumns = 512;
+  static_assert(kCodes + kSides * 64 <= kColumns, "tensor memory");
   static constexpr int kChunks = TM * 16 / (kCodeWarps * 32);  // 16-byte pieces of x's block of a thread
-  static_assert(2 * kA >= TM * kTcRows * 4, "the sums fit over the codes' tiles");
+  static constexpr int kSumWarps = TM == 64 ? 8 : 4, kColumnsEach = TM * 4 / kSumWarps;
+  static constexpr int kThreads = (kSumWarp + kSumWarps) * 32;
 };
 
 // four pairs of bf16 (code less zero) of a word; less = -(128 + zero) twice
@@ -343,16 +346,23 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
   return p != 0;
 }
+// eight columns of the warp's 32 lanes into tensor memory
+__device__ __forceinline__ void st8(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                    uint32_t g, uint32_t h) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(a), "r"(b),
+               "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
 __device__ __forceinline__ void sts128(uint32_t p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 template <int TM, int GROUP>
-__global__ void __launch_bounds__(kTcThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(TcShape<TM>::kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Args a) {
   using S = TcShape<TM>;
   constexpr int PER = 128 / GROUP;  // groups of a block
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], a_full[2], a_empty[2], acc_full[kAccs], acc_empty[kAccs], done;
+  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], a_full[kSides], a_empty[kSides], acc_full[S::kAccs], acc_empty[S::kAccs], done;
   __shared__ uint32_t tmem_base;
   __shared__ int failed, issued;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -363,21 +373,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) tile_kernel(const __grid_consta
   const int all = (a.K + 127) / 128;
   const int b0 = (int)((long long)all * rank / a.split), b1 = (int)((long long)all * (rank + 1) / a.split);
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t at_a = smem_addr(tiles), at_x = at_a + 2 * S::kA, at_raw = at_x + 2 * S::kX;
+  const uint32_t at_x = smem_addr(tiles), at_raw = at_x + kSides * S::kX;
   if (tid == 0) {
     for (int s = 0; s < kRaw; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], kCodeWarps);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kSides; ++s) {
       mbar_init(&a_full[s], kCodeWarps);
       mbar_init(&a_empty[s], 1);
     }
-    for (int s = 0; s < kAccs; ++s) {
+    for (int s = 0; s < S::kAccs; ++s) {
       mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], 4);
+      mbar_init(&acc_empty[s], S::kSumWarps);
     }
-    mbar_init(&done, 1);
+    mbar_init(&done, 2);
     failed = issued = 0;
     fence_mbar_init();
     tc::prefetch_map(&tmW);
@@ -394,10 +404,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tile_kernel(const __grid_consta
     failed = 1;
     return false;
   };
-  float total[TM] = {};
+  float total[S::kColumnsEach] = {};
 
-  if (warp < kCodeWarps) {
-    const int r = tid & 127, half = tid >> 7;  // 64 k of a row
+  if (warp < 2 * kCodeWarps) {
+    const int team = warp / kCodeWarps, me = tid - team * kCodeWarps * 32;
+    const int r = me & 127, half = me >> 7;  // 64 k of a row
     const int n = min(n0 + r, a.N - 1);
     const uint8_t* zrow = a.zeros ? a.zeros + (uint32_t)n * a.groups : nullptr;
     constexpr int Z = GROUP == 32 ? 2 : 1;  // groups of 64 k, or one that has more
@@ -408,56 +419,53 @@ __global__ void __launch_bounds__(kTcThreads, 1) tile_kernel(const __grid_consta
         z[q] = zrow ? __ldg(zrow + min(group, a.groups - 1)) : 8u;
       }
     };
-    const uint16_t* xrow[S::kChunks];
-#pragma unroll
-    for (int q = 0; q < S::kChunks; ++q) xrow[q] = a.x + min(m0 + ((tid + q * 256) >> 4), a.M - 1) * a.ldx;
+    const int m_mine = m0 + (me >> 4);  // and each 16 rows on
     auto load_x = [&](int b, uint4 (&v)[S::kChunks]) {
-      const int k = min(b * 128 + (tid & 15) * 8, a.K - 8);
+      const uint16_t* from = a.x + min(b * 128 + (me & 15) * 8, a.K - 8);
 #pragma unroll
-      for (int q = 0; q < S::kChunks; ++q) v[q] = __ldg(reinterpret_cast<const uint4*>(xrow[q] + k));
+      for (int q = 0; q < S::kChunks; ++q)
+        v[q] = __ldg(reinterpret_cast<const uint4*>(from + min(m_mine + 16 * q, a.M - 1) * a.ldx));
       // (what is behind x's end becomes 0 where it is stored: a choice here would wait for the load)
     };
     uint32_t zn[Z];
     uint4 xn[S::kChunks];
-    if (b0 < b1) {
-      load_zeros(b0, zn);
-      load_x(b0, xn);
-    }
-    const uint32_t row_a = half * kAtom + r * 128, flip = (uint32_t)(r & 7);
+    load_zeros(min(b0 + team, all - 1), zn);
+    load_x(min(b0 + team, all - 1), xn);
+    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kCodes + half * 32;  // (r's lane)
     const uint32_t raw_row = r * 64, raw_flip = (uint32_t)(r >> 1) & 3;
-    for (int b = b0, g = 0; b < b1; ++b, ++g) {
-      const int s = g % kRaw, side = g & 1;
+    for (int b = b0 + team, g = team; b < b1; b += 2, g += 2) {
+      const int s = g % kRaw, side = g % kSides;
       uint32_t less[Z];
 #pragma unroll
       for (int q = 0; q < Z; ++q) less[q] = zn[q] * 0x10001u + 0xc300c300u;
-      uint4 x[S::kChunks];
-#pragma unroll
-      for (int q = 0; q < S::kChunks; ++q) x[q] = xn[q];
-      load_zeros(min(b + 1, b1 - 1), zn);
-      load_x(min(b + 1, b1 - 1), xn);
-      if (!wait(&raw_full[s], g / kRaw & 1)) break;
-      uint32_t w[8];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
-                     : "r"(at_raw + s * kRawBytes + raw_row + (((uint32_t)(half * 2 + c) ^ raw_flip) << 4))
-                     : "memory");
-      if (g >= 2 && !wait(&a_empty[side], (g / 2 - 1) & 1)) break;
-      const uint32_t to = at_a + side * S::kA + row_a;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint32_t l = less[Z == 2 ? c / 4 : 0];
-        sts128(to + ((c ^ flip) << 4), pair_of<0>(w[c], l), pair_of<1>(w[c], l), pair_of<2>(w[c], l), pair_of<3>(w[c], l));
-      }
+      load_zeros(min(b + 2, all - 1), zn);
+      if (g >= kSides && !__all_sync(kFull, wait(&a_empty[side], (g / kSides - 1) & 1))) break;  // (the whole warp)
+      tc::fence_after();
 #pragma unroll
       for (int q = 0; q < S::kChunks; ++q) {
-        const int m = (tid + q * 256) >> 4, c = tid & 15;
-        const uint4 v = m0 + m < a.M && b * 128 + c * 8 < a.K ? x[q] : make_uint4(0, 0, 0, 0);
+        const int m = (me >> 4) + 16 * q, c = me & 15;
+        const uint4 v = m0 + m < a.M && b * 128 + c * 8 < a.K ? xn[q] : make_uint4(0, 0, 0, 0);
         sts128(at_x + side * S::kX + (c >> 3) * TM * 128 + m * 128 + (((c & 7) ^ (m & 7)) << 4), __byte_perm(v.x, v.z, 0x5410),
                __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
       }
+      load_x(min(b + 2, all - 1), xn);
+      if (!__all_sync(kFull, wait(&raw_full[s], g / kRaw & 1))) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at_raw + s * kRawBytes + raw_row + (((uint32_t)(half * 2 + h) ^ raw_flip) << 4))
+                     : "memory");
+        const uint32_t l = less[Z == 2 ? h : 0];
+#pragma unroll
+        for (int c = 0; c < 4; c += 2)
+          st8(to + side * 64 + h * 16 + c * 4, pair_of<0>(w[c], l), pair_of<1>(w[c], l), pair_of<2>(w[c], l), pair_of<3>(w[c], l),
+              pair_of<0>(w[c + 1], l), pair_of<1>(w[c + 1], l), pair_of<2>(w[c + 1], l), pair_of<3>(w[c + 1], l));
+      }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the tensor cores read what was stored)
+      tc::st_wait();
+      tc::fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&a_full[side]);
@@ -471,28 +479,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) tile_kernel(const __grid_consta
         const int s = g % kRaw;
         if (g >= kRaw && !wait(&raw_empty[s], (g / kRaw - 1) & 1)) break;
         mbar_arrive_expect_tx(&raw_full[s], kRawBytes);
-        tc::tma_load(tiles + 2 * S::kA + 2 * S::kX + s * kRawBytes, &tmW, b * 64, n0, &raw_full[s]);
+        tc::tma_load(tiles + kSides * S::kX + s * kRawBytes, &tmW, b * 64, n0, &raw_full[s]);
       }
       issued = g;
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp < kSumWarp) {
     // The whole warp takes this way, so that descriptors are computed in uniform registers, where the instruction
     // wants them; one lane issues.
     constexpr uint32_t id = tc::idesc(false, false, 128, TM);
-    const uint32_t low_a = tc::desc_low(at_a, 16), low_x = tc::desc_low(at_x, 16);
     const bool elected = elect_one();
-    int acc = 0;
+    const int team = warp - kMmaWarp;
     bool ok = true;
-    for (int b = b0, g = 0; b < b1 && ok; ++b, ++g) {
-      const int side = g & 1;
-      const uint32_t block_a = low_a + side * (S::kA >> 4), block_x = low_x + side * (S::kX >> 4);
-      ok = __all_sync(kFull, wait(&a_full[side], g / 2 & 1));
+    for (int b = b0 + team, g = team; b < b1 && ok; b += 2, g += 2) {
+      const int side = g % kSides;
+      const uint32_t block_a = tmem + S::kCodes + side * 64, block_x = tc::desc_low(at_x, 16) + side * (S::kX >> 4);
+      ok = __all_sync(kFull, wait(&a_full[side], g / kSides & 1));
       tc::fence_after();
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
         if (!ok || b * PER + q >= a.groups) break;
-        const int slot = acc % kAccs;
-        ok = acc < kAccs || __all_sync(kFull, wait(&acc_empty[slot], (acc / kAccs - 1) & 1));
+        const int acc = g * PER + q, slot = acc % S::kAccs;
+        ok = acc < S::kAccs || __all_sync(kFull, wait(&acc_empty[slot], (acc / S::kAccs - 1) & 1));
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = tmem + slot * TM;
@@ -501,12 +508,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tile_kernel(const __grid_consta
           for (int i = 0; i < GROUP / 16; ++i) {
             constexpr int kSteps = GROUP / 16;
             const int k = q * kSteps + i;  // of the block's eight steps
-            tc::mma_low(d, block_a + (((k >> 2) * kAtom + (k & 3) * 32) >> 4), block_x + (((k >> 2) * TM * 128 + (k & 3) * 32) >> 4),
-                        id, i != 0);
+            tc::mma_ts_low(d, block_a + k * 8, block_x + (((k >> 2) * TM * 128 + (k & 3) * 32) >> 4), id, i != 0);
           }
           tc::commit<1>(smem_addr(&acc_full[slot]));
         }
-        ++acc;
       }
       if (ok && elected) tc::commit<1>(smem_addr(&a_empty[side]));
     }
@@ -515,17 +520,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) tile_kernel(const __grid_consta
   } else {
     const int quad = warp & 3, n = min(n0 + quad * 32 + lane, a.N - 1);
     const uint16_t* srow = a.scales + (uint32_t)n * a.groups;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (warp - kSumWarp) / 4 * S::kColumnsEach;
     const int g0 = b0 * PER, g1 = min(b1 * PER, a.groups);
     uint32_t next = g0 < g1 ? __ldg(srow + g0) : 0;
     for (int group = g0, acc = 0; group < g1; ++group, ++acc) {
       const float s = __uint_as_float(next << 16);
       next = __ldg(srow + min(group + 1, a.groups - 1));
-      const int slot = acc % kAccs;
-      if (!wait(&acc_full[slot], acc / kAccs & 1)) break;
+      const int slot = acc % S::kAccs;
+      if (!__all_sync(kFull, wait(&acc_full[slot], acc / S::kAccs & 1))) break;
       tc::fence_after();
 #pragma unroll
-      for (int c = 0; c < TM; c += 16) {
+      for (int c = 0; c < S::kColumnsEach; c += 16) {
         uint32_t v[16];
         tc::ld16(lanes + slot * TM + c, v);
         tc::ld_wait(v);
@@ -547,14 +552,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) tile_kernel(const __grid_consta
     }
     __syncthreads();
   }
-  float* part = reinterpret_cast<float*>(tiles);  // [TM][128], over the codes' tiles
+  float* part = reinterpret_cast<float*>(tiles);  // [TM][128], over the rings
   if (warp >= kSumWarp) {
 #pragma unroll
-    for (int c = 0; c < TM; ++c) part[c * kTcRows + (warp & 3) * 32 + lane] = lost ? __uint_as_float(0x7fffffffu) : total[c];
+    for (int c = 0; c < S::kColumnsEach; ++c)
+      part[((warp - kSumWarp) / 4 * S::kColumnsEach + c) * kTcRows + (warp & 3) * 32 + lane] =
+          lost ? __uint_as_float(0x7fffffffu) : total[c];
   }
   if (a.split > 1) tc::cluster_sync();
   else __syncthreads();
-  finish<kTcRows, kTcThreads>(a, part, n0, m0, min(TM, a.M - m0), rank);
+  finish<kTcRows, S::kThreads>(a, part, n0, m0, min(TM, a.M - m0), rank);
   if (a.split > 1) tc::cluster_sync();  // (no CTA leaves while its sums are read)
   tc::fence_before();
   __syncthreads();
@@ -609,7 +616,7 @@ template <int TM, int GROUP>
 cudaError_t launch_tiles(const Args& a, const CUtensorMap& map, void* stream) {
   static std::atomic<int> ready[kMaxDevices];
   const long long slabs = ((a.N + kTcRows - 1LL) / kTcRows) * ((a.M + TM - 1LL) / TM);
-  return launch(tile_kernel<TM, GROUP>, ready, slabs, 1, 2, kTcThreads, TcShape<TM>::kSmem, a, stream, map);
+  return launch(tile_kernel<TM, GROUP>, ready, slabs, 1, 2, TcShape<TM>::kThreads, TcShape<TM>::kSmem, a, stream, map);
 }
 
 template <int TM>
