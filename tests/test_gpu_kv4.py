@@ -405,3 +405,75 @@ def test_attention_refuses_sequences():
     ws.zero_()
     out, lse, ws = attend(q[6:].cuda(), dev(pool), dev(table[6:]), dev(lens[6:]), dev(ks[6:]), page, D, hkv, 0.1, 10, 0, ws=ws)
     assert sb.sv_read_device_flags(ws) == 0
+
+
+@pytest.mark.parametrize("page", [1, 3, 16, 48])
+@pytest.mark.parametrize("K", [0, 2])
+def test_attention_of_a_window_whose_old_pages_are_gone(page, K):
+    """Entries of pages that no query sees are -1 or past the pool; their pages hold NaN."""
+    r = np.random.default_rng(page + K)
+    window, sinks, D, hq, hkv = 37, 5, 128, 8, 2
+    lens, ks = [700, 333, 60, 40], [K, 0, K, K]
+    q, pool, table, max_pages = case(r, 4, K, hq, hkv, D, page, lens, ks)
+    for b, l in enumerate(lens):
+        gone = np.arange(-(-sinks // page), (l - 1 - window + 1) // page)  # the first query sees j > l - 1 - window
+        for i, j in enumerate(gone):
+            pool[table[b, j]] = 0xff
+            table[b, j] = -1 if i % 2 else 10 ** 6
+    out, lse, ws = attend(q.cuda(), dev(pool), dev(table), dev(np.int32(lens)), dev(np.int32(ks)), page, D, hkv, 0.1, window,
+                          sinks)
+    assert sb.sv_read_device_flags(ws) == 0
+    full = np.where((table < 0) | (table >= pool.shape[0]), 0, table)  # (read_tokens reads the unseen ones too)
+    compare(q, pool, full, lens, ks, page, D, hkv, 0.1, out, lse, window, sinks)
+
+
+def test_a_pool_past_four_gigabytes():
+    """Pages beyond 2^32 bytes (and 2^31 words): written, read back and attended to."""
+    B, K, hq, hkv, D, page = 2, 0, 16, 8, 128, 16
+    size = sb.sv_kv4_page_bytes(hkv, D, page)
+    num_pages = (1 << 32) // size + 2000
+    pool = torch.zeros(num_pages, size, dtype=torch.uint8, device="cuda")
+    r = np.random.default_rng(15)
+    table = (num_pages - 1 - r.permutation(1000)[:8].reshape(B, 4)).astype(np.int32)
+    lens = np.int32([61, 33])
+    k, v = bf(r.standard_normal((B, 64, hkv, D))), bf(r.standard_normal((B, 64, hkv, D)))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    sb.sv_kv4_append(k.cuda(), v.cuda(), 0, 0, 0, sb.SV_BF16, pool, num_pages, page, dev(table), 4, dev(np.int32([0, 0])),
+                     dev(lens), B, 64, hkv, D, ws, 256)
+    used = np.sort(table.reshape(-1))
+    small, local = pool[torch.from_numpy(used).cuda().long()].cpu().numpy(), np.searchsorted(used, table).astype(np.int32)
+    want = np.zeros_like(small)
+    for b in range(B):
+        for t in range(lens[b]):
+            o4.write_token(want, local[b, t // page], t % page, page, f64(k[b, t]), f64(v[b, t]))
+    assert np.array_equal(small, want)
+    assert not pool[:num_pages - 1000].any()
+    q = bf(r.standard_normal((B, 1, hq, D)))
+    out, lse, ws = attend(q.cuda(), pool, dev(table), dev(lens), None, page, D, hkv, 0.09)
+    compare(q, small, local, lens, [0, 0], page, D, hkv, 0.09, out, lse)
+    back = torch.zeros(2, B, 64, hkv, D, device="cuda")
+    sb.sv_kv4_read(pool, num_pages, page, dev(table), 4, dev(np.int32([0, 0])), dev(lens), back[0], back[1], 0, 0, 0,
+                   sb.SV_F32, B, 64, hkv, D, ws, ws.numel())
+    for b in range(B):
+        codes, s, m = o4.read_tokens(want, local[b], page, lens[b], hkv, D)
+        assert np.allclose(f64(back[:, b, :lens[b]]), m[..., None] + s[..., None] * codes, rtol=2.0 ** -23, atol=1e-30)
+
+
+def test_attention_on_two_streams_at_once():
+    """Two calls in flight together, each with its own workspace and output, many times."""
+    r = np.random.default_rng(16)
+    cases = []
+    for hq, hkv, D, page, lens in ((8, 2, 128, 16, [4000, 100, 900]), (12, 1, 64, 24, [2000] * 5)):
+        B = len(lens)
+        q, pool, table, _ = case(r, B, 1, hq, hkv, D, page, lens, [1] * B)
+        args = [q.cuda(), dev(pool), dev(table), dev(np.int32(lens)), None, page, D, hkv, 0.1]
+        first, lse, ws = attend(*args)
+        cases.append((args, first, torch.zeros_like(ws), torch.cuda.Stream(), [torch.full_like(first, 7.0) for _ in range(20)]))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for args, first, ws, stream, outs in cases:
+            with torch.cuda.stream(stream):
+                attend(*args, ws=ws, out=outs[i], lse=False, stream=stream)
+    torch.cuda.synchronize()
+    for args, first, ws, stream, outs in cases:
+        assert sb.sv_read_device_flags(ws) == 0 and all(torch.equal(o, first) for o in outs)
