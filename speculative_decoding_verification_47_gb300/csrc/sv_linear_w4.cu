@@ -306,37 +306,46 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
 
 // ---------------------------------------------------------------------------
 // More rows of x: the 5th-generation tensor cores.  A CTA takes 128 rows of W by TM rows of x and a part of K, in
-// blocks of 128 k.  Codes arrive by TMA; eight warps make them bf16 integers (code less zero, exact) in tensor
-// memory, where the 128-row operand may stand (through shared memory its bytes were the bound), and x's block in shared memory; a thread issues a group's products into one of a few
-// accumulators of tensor memory; four or eight warps take that out, times the group's scale, and add it to their
-// float32 sums in registers.  x's 8 values of a chunk follow the order of the codes' pairs (0, 4), (1, 5), (2, 6), (3, 7).
+// blocks of 128 k.  Codes and x arrive by TMA; eight warps make the codes bf16 integers (code less zero, exact) in
+// tensor memory, where the 128-row operand may stand (through shared memory its bytes were the bound); a thread issues
+// the groups' products, each group's into an accumulator of tensor memory of its own; four or eight warps take those
+// out, times the groups' scales, and add them to their float32 sums in registers.
 // ---------------------------------------------------------------------------
-constexpr int kCodeWarps = 8;        // of a team; a team and an issuing warp for the even blocks, another for the odd ones
+constexpr int kTeams = 4;            // a team takes every kTeams-th block, of the two issuing warps each every other one
+constexpr int kCodeWarps = 16 / kTeams;
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kSumWarp = 19;
 constexpr int kTcRows = 128;
-constexpr int kRaw = 6;              // blocks of codes on their way
+constexpr int kRaw = 8;              // blocks of codes and x on their way
 constexpr int kRawBytes = kTcRows * 64;
-constexpr int kSides = 4;            // blocks ready for their products, or in them
+constexpr int kSides = 4;            // blocks of bf16 codes ready for their products, or in them
 
-template <int TM>
+template <int TM, int GROUP>
 struct TcShape {
-  static constexpr int kAccs = TM == 64 ? 4 : 8;  // sums of a group
+  static constexpr int kPer = 128 / GROUP;  // groups of a block
+  // Groups that are told to be done at once: those of a block, as long as two such units fit.  (A commit keeps the
+  // issuing warp for some 200 cycles, and a wait costs as much.)
+  static constexpr int kUnit = kPer * TM <= 128 ? kPer : 128 / TM;
+  static constexpr int kAccs = kUnit * TM <= 32 ? 8 : 256 / (kUnit * TM);  // units of accumulators
+  // A wait tells a phase from the one before only if the waiter has seen that one end.  So a ring's slot is always
+  // waited for by the same warp: two warps issue, taking turns, only where the accumulators hold two blocks.
+  static constexpr int kIssuers = kAccs * kUnit >= 2 * kPer ? 2 : 1;
+  static_assert(kSides % kTeams == 0 && kRaw % kTeams == 0 && kAccs * kUnit % (kIssuers * kPer) == 0, "waits in turn");
   static constexpr int kX = 2 * TM * 128;  // of a block
   static constexpr int kPart = TM * kTcRows * 4;
-  static constexpr int kTiles = kSides * kX + kRaw * kRawBytes, kSmem = (kTiles > kPart ? kTiles : kPart) + 1024;
-  static constexpr uint32_t kCodes = kAccs * TM;  // columns of the sums; then 64 of codes for each side
+  static constexpr int kStage = kX + kRawBytes;
+  static constexpr int kTiles = kRaw * kStage, kSmem = (kTiles > kPart ? kTiles : kPart) + 1024;
+  static constexpr uint32_t kCodes = 256;  // columns of the accumulators; then 64 of codes for each side
   static constexpr uint32_t kColumns = 512;
-  static_assert(kCodes + kSides * 64 <= kColumns, "tensor memory");
-  static constexpr int kChunks = TM * 16 / (kCodeWarps * 32);  // 16-byte pieces of x's block of a thread
+  static_assert(kAccs * kUnit * TM <= (int)kCodes && kCodes + kSides * 64 <= kColumns, "tensor memory");
   static constexpr int kSumWarps = TM == 64 ? 8 : 4, kColumnsEach = TM * 4 / kSumWarps;
   static constexpr int kThreads = (kSumWarp + kSumWarps) * 32;
 };
 
-// four pairs of bf16 (code less zero) of a word; less = -(128 + zero) twice
+// Pair J of a word's four pairs of bf16 (code less zero); w4 = w >> 4, less = -(128 + zero) twice.
 template <int J>
-__device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t less) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * J)), "n"(0x000f000f), "r"(0x43004300u));
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t w4, uint32_t less) {
+  uint32_t r = __byte_perm(w, w4, 0x0400 + J * 0x0101);  // byte J of both, one in each half
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(r), "n"(0x000f000f), "r"(0x43004300u));
   asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(less));
   return r;
 }
@@ -353,14 +362,12 @@ __device__ __forceinline__ void st8(uint32_t taddr, uint32_t a, uint32_t b, uint
                "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
                : "memory");
 }
-__device__ __forceinline__ void sts128(uint32_t p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 
 template <int TM, int GROUP>
-__global__ void __launch_bounds__(TcShape<TM>::kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Args a) {
-  using S = TcShape<TM>;
-  constexpr int PER = 128 / GROUP;  // groups of a block
+__global__ void __launch_bounds__(TcShape<TM, GROUP>::kThreads, 1) tile_kernel(
+    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ Args a) {
+  using S = TcShape<TM, GROUP>;
+  constexpr int PER = S::kPer, UNIT = S::kUnit;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], a_full[kSides], a_empty[kSides], acc_full[S::kAccs], acc_empty[S::kAccs], done;
   __shared__ uint32_t tmem_base;
@@ -373,11 +380,11 @@ __global__ void __launch_bounds__(TcShape<TM>::kThreads, 1) tile_kernel(const __
   const int all = (a.K + 127) / 128;
   const int b0 = (int)((long long)all * rank / a.split), b1 = (int)((long long)all * (rank + 1) / a.split);
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t at_x = smem_addr(tiles), at_raw = at_x + kSides * S::kX;
+  const uint32_t at_x = smem_addr(tiles), at_raw = at_x + S::kX;  // of the first stage
   if (tid == 0) {
     for (int s = 0; s < kRaw; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], kCodeWarps);
+      mbar_init(&raw_empty[s], 1);
     }
     for (int s = 0; s < kSides; ++s) {
       mbar_init(&a_full[s], kCodeWarps);
@@ -391,6 +398,7 @@ __global__ void __launch_bounds__(TcShape<TM>::kThreads, 1) tile_kernel(const __
     failed = issued = 0;
     fence_mbar_init();
     tc::prefetch_map(&tmW);
+    tc::prefetch_map(&tmX);
   }
   if (warp == kLoadWarp) tc::alloc<1>(&tmem_base, S::kColumns);
   tc::fence_before();
@@ -406,71 +414,51 @@ __global__ void __launch_bounds__(TcShape<TM>::kThreads, 1) tile_kernel(const __
   };
   float total[S::kColumnsEach] = {};
 
-  if (warp < 2 * kCodeWarps) {
+  if (warp < kLoadWarp) {
     const int team = warp / kCodeWarps, me = tid - team * kCodeWarps * 32;
-    const int r = me & 127, half = me >> 7;  // 64 k of a row
+    constexpr int PARTS = kCodeWarps / 4, RUNS = 4 / PARTS;  // a thread has one of a row's parts, RUNS times 32 k
+    const int r = me & 127, part = me >> 7;
     const int n = min(n0 + r, a.N - 1);
-    const uint8_t* zrow = a.zeros ? a.zeros + (uint32_t)n * a.groups : nullptr;
-    constexpr int Z = GROUP == 32 ? 2 : 1;  // groups of 64 k, or one that has more
+    // (without zeros the bytes of W are loaded in their place and not used: a choice at the load would wait for it)
+    const bool has_zeros = a.zeros != nullptr;
+    const uint8_t* zrow = has_zeros ? a.zeros + (uint32_t)n * a.groups : a.W + n * a.ldw;
+    constexpr int Z = RUNS * 32 > GROUP ? RUNS * 32 / GROUP : 1;  // groups of the part
     auto load_zeros = [&](int b, uint32_t (&z)[Z]) {
 #pragma unroll
-      for (int q = 0; q < Z; ++q) {
-        const int group = GROUP == 128 ? b : b * PER + half * Z + q;
-        z[q] = zrow ? __ldg(zrow + min(group, a.groups - 1)) : 8u;
-      }
-    };
-    const int m_mine = m0 + (me >> 4);  // and each 16 rows on
-    auto load_x = [&](int b, uint4 (&v)[S::kChunks]) {
-      const uint16_t* from = a.x + min(b * 128 + (me & 15) * 8, a.K - 8);
-#pragma unroll
-      for (int q = 0; q < S::kChunks; ++q)
-        v[q] = __ldg(reinterpret_cast<const uint4*>(from + min(m_mine + 16 * q, a.M - 1) * a.ldx));
-      // (what is behind x's end becomes 0 where it is stored: a choice here would wait for the load)
+      for (int q = 0; q < Z; ++q) z[q] = __ldg(zrow + min(b * PER + part * RUNS * 32 / GROUP + q, a.groups - 1));
     };
     uint32_t zn[Z];
-    uint4 xn[S::kChunks];
-    load_zeros(min(b0 + team, all - 1), zn);
-    load_x(min(b0 + team, all - 1), xn);
-    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kCodes + half * 32;  // (r's lane)
+    load_zeros(b0 + team, zn);
+    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kCodes + part * (RUNS * 16);  // (r's lane)
     const uint32_t raw_row = r * 64, raw_flip = (uint32_t)(r >> 1) & 3;
-    for (int b = b0 + team, g = team; b < b1; b += 2, g += 2) {
+    for (int b = b0 + team, g = team; b < b1; b += kTeams, g += kTeams) {
       const int s = g % kRaw, side = g % kSides;
       uint32_t less[Z];
 #pragma unroll
-      for (int q = 0; q < Z; ++q) less[q] = zn[q] * 0x10001u + 0xc300c300u;
-      load_zeros(min(b + 2, all - 1), zn);
+      for (int q = 0; q < Z; ++q) less[q] = (has_zeros ? zn[q] : 8u) * 0x10001u + 0xc300c300u;
+      load_zeros(b + kTeams, zn);
       if (g >= kSides && !__all_sync(kFull, wait(&a_empty[side], (g / kSides - 1) & 1))) break;  // (the whole warp)
       tc::fence_after();
-#pragma unroll
-      for (int q = 0; q < S::kChunks; ++q) {
-        const int m = (me >> 4) + 16 * q, c = me & 15;
-        const uint4 v = m0 + m < a.M && b * 128 + c * 8 < a.K ? xn[q] : make_uint4(0, 0, 0, 0);
-        sts128(at_x + side * S::kX + (c >> 3) * TM * 128 + m * 128 + (((c & 7) ^ (m & 7)) << 4), __byte_perm(v.x, v.z, 0x5410),
-               __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-      }
-      load_x(min(b + 2, all - 1), xn);
       if (!__all_sync(kFull, wait(&raw_full[s], g / kRaw & 1))) break;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < RUNS; ++h) {
         uint32_t w[4];
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(at_raw + s * kRawBytes + raw_row + (((uint32_t)(half * 2 + h) ^ raw_flip) << 4))
+                     : "r"(at_raw + s * S::kStage + raw_row + (((uint32_t)(part * RUNS + h) ^ raw_flip) << 4))
                      : "memory");
-        const uint32_t l = less[Z == 2 ? h : 0];
+        const uint32_t l = less[h * Z / RUNS];
 #pragma unroll
-        for (int c = 0; c < 4; c += 2)
-          st8(to + side * 64 + h * 16 + c * 4, pair_of<0>(w[c], l), pair_of<1>(w[c], l), pair_of<2>(w[c], l), pair_of<3>(w[c], l),
-              pair_of<0>(w[c + 1], l), pair_of<1>(w[c + 1], l), pair_of<2>(w[c + 1], l), pair_of<3>(w[c + 1], l));
+        for (int c = 0; c < 4; c += 2) {
+          const uint32_t u = w[c], v = w[c + 1], u4 = u >> 4, v4 = v >> 4;
+          st8(to + side * 64 + h * 16 + c * 4, pair_of<0>(u, u4, l), pair_of<1>(u, u4, l), pair_of<2>(u, u4, l),
+              pair_of<3>(u, u4, l), pair_of<0>(v, v4, l), pair_of<1>(v, v4, l), pair_of<2>(v, v4, l), pair_of<3>(v, v4, l));
+        }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the tensor cores read what was stored)
       tc::st_wait();
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&a_full[side]);
-        mbar_arrive(&raw_empty[s]);
-      }
+      if (lane == 0) mbar_arrive(&a_full[side]);
     }
   } else if (warp == kLoadWarp) {
     if (lane == 0) {
@@ -478,8 +466,10 @@ __global__ void __launch_bounds__(TcShape<TM>::kThreads, 1) tile_kernel(const __
       for (int b = b0; b < b1; ++b, ++g) {
         const int s = g % kRaw;
         if (g >= kRaw && !wait(&raw_empty[s], (g / kRaw - 1) & 1)) break;
-        mbar_arrive_expect_tx(&raw_full[s], kRawBytes);
-        tc::tma_load(tiles + kSides * S::kX + s * kRawBytes, &tmW, b * 64, n0, &raw_full[s]);
+        mbar_arrive_expect_tx(&raw_full[s], S::kStage);
+        tc::tma_load(tiles + s * S::kStage + S::kX, &tmW, b * 64, n0, &raw_full[s]);
+        tc::tma_load(tiles + s * S::kStage, &tmX, b * 128, m0, &raw_full[s]);
+        tc::tma_load(tiles + s * S::kStage + S::kX / 2, &tmX, b * 128 + 64, m0, &raw_full[s]);
       }
       issued = g;
     }
@@ -490,19 +480,21 @@ __global__ void __launch_bounds__(TcShape<TM>::kThreads, 1) tile_kernel(const __
     const bool elected = elect_one();
     const int team = warp - kMmaWarp;
     bool ok = true;
-    for (int b = b0 + team, g = team; b < b1 && ok; b += 2, g += 2) {
-      const int side = g % kSides;
-      const uint32_t block_a = tmem + S::kCodes + side * 64, block_x = tc::desc_low(at_x, 16) + side * (S::kX >> 4);
-      ok = __all_sync(kFull, wait(&a_full[side], g / kSides & 1));
+    for (int b = b0 + team, g = team; b < b1 && ok && team < S::kIssuers; b += S::kIssuers, g += S::kIssuers) {
+      const int side = g % kSides, s = g % kRaw;
+      const uint32_t block_a = tmem + S::kCodes + side * 64, block_x = tc::desc_low(at_x, 16) + s * (S::kStage >> 4);
+      ok = __all_sync(kFull, wait(&raw_full[s], g / kRaw & 1) && wait(&a_full[side], g / kSides & 1));
       tc::fence_after();
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
         if (!ok || b * PER + q >= a.groups) break;
-        const int acc = g * PER + q, slot = acc % S::kAccs;
-        ok = acc < S::kAccs || __all_sync(kFull, wait(&acc_empty[slot], (acc / S::kAccs - 1) & 1));
-        if (!ok) break;
-        tc::fence_after();
-        const uint32_t d = tmem + slot * TM;
+        const int acc = (g * PER + q) / UNIT, slot = acc % S::kAccs;
+        if (q % UNIT == 0) {
+          ok = acc < S::kAccs || __all_sync(kFull, wait(&acc_empty[slot], (acc / S::kAccs - 1) & 1));
+          if (!ok) break;
+          tc::fence_after();
+        }
+        const uint32_t d = tmem + (slot * UNIT + q % UNIT) * TM;
         if (elected) {
 #pragma unroll
           for (int i = 0; i < GROUP / 16; ++i) {
@@ -510,10 +502,9 @@ __global__ void __launch_bounds__(TcShape<TM>::kThreads, 1) tile_kernel(const __
             const int k = q * kSteps + i;  // of the block's eight steps
             tc::mma_ts_low(d, block_a + k * 8, block_x + (((k >> 2) * TM * 128 + (k & 3) * 32) >> 4), id, i != 0);
           }
-          tc::commit<1>(smem_addr(&acc_full[slot]));
+          if (q % UNIT == UNIT - 1 || b * PER + q + 1 == a.groups) tc::commit<1>(smem_addr(&acc_full[slot]));
         }
       }
-      if (ok && elected) tc::commit<1>(smem_addr(&a_empty[side]));
     }
     if (elected) tc::commit<1>(smem_addr(&done));  // (nothing arrives behind the CTA's end)
     if (!tc::wait_bounded(&done, 0)) failed = 1;
@@ -522,20 +513,42 @@ __global__ void __launch_bounds__(TcShape<TM>::kThreads, 1) tile_kernel(const __
     const uint16_t* srow = a.scales + (uint32_t)n * a.groups;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (warp - kSumWarp) / 4 * S::kColumnsEach;
     const int g0 = b0 * PER, g1 = min(b1 * PER, a.groups);
-    uint32_t next = g0 < g1 ? __ldg(srow + g0) : 0;
-    for (int group = g0, acc = 0; group < g1; ++group, ++acc) {
-      const float s = __uint_as_float(next << 16);
-      next = __ldg(srow + min(group + 1, a.groups - 1));
+    uint32_t next[UNIT];
+#pragma unroll
+    for (int i = 0; i < UNIT; ++i) next[i] = __ldg(srow + min(g0 + i, a.groups - 1));
+    for (int group = g0, acc = 0; group < g1; group += UNIT, ++acc) {
+      float s[UNIT];
+#pragma unroll
+      for (int i = 0; i < UNIT; ++i) {
+        s[i] = __uint_as_float(next[i] << 16);
+        next[i] = __ldg(srow + min(group + UNIT + i, a.groups - 1));
+      }
       const int slot = acc % S::kAccs;
       if (!__all_sync(kFull, wait(&acc_full[slot], acc / S::kAccs & 1))) break;
       tc::fence_after();
+      if (tid == kSumWarp * 32 && ((group + UNIT) % PER == 0 || group + UNIT >= g1)) {
+        // the block's products are done, and with them its codes and x
+        const int g = group / PER - b0;
+        tc::fence_before();
+        mbar_arrive(&a_empty[g % kSides]);
+        mbar_arrive(&raw_empty[g % kRaw]);
+      }
+      constexpr int kPieces = S::kColumnsEach / 16, kAll = UNIT * kPieces, kTwo = kAll > 1 ? 2 : 1;
 #pragma unroll
-      for (int c = 0; c < S::kColumnsEach; c += 16) {
-        uint32_t v[16];
-        tc::ld16(lanes + slot * TM + c, v);
-        tc::ld_wait(v);
+      for (int p = 0; p < kAll; p += kTwo) {
+        uint32_t v[kTwo][16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) total[c + j] = __fmaf_rn(s, __uint_as_float(v[j]), total[c + j]);
+        for (int j = 0; j < kTwo; ++j)
+          tc::ld16(lanes + (slot * UNIT + (p + j) / kPieces) * TM + (p + j) % kPieces * 16, v[j]);
+#pragma unroll
+        for (int j = 0; j < kTwo; ++j) {
+          tc::ld_wait(v[j]);
+          const int i = (p + j) / kPieces, c = (p + j) % kPieces * 16;
+          if (group + i < g1) {  // (behind the last group nothing was written)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) total[c + e] = __fmaf_rn(s[i], __uint_as_float(v[j][e]), total[c + e]);
+          }
+        }
       }
       tc::fence_before();
       __syncwarp();
@@ -613,31 +626,36 @@ cudaError_t launch_rows(const Args& a, void* stream) {
 }
 
 template <int TM, int GROUP>
-cudaError_t launch_tiles(const Args& a, const CUtensorMap& map, void* stream) {
+cudaError_t launch_tiles(const Args& a, const CUtensorMap& codes, const CUtensorMap& x, void* stream) {
   static std::atomic<int> ready[kMaxDevices];
   const long long slabs = ((a.N + kTcRows - 1LL) / kTcRows) * ((a.M + TM - 1LL) / TM);
-  return launch(tile_kernel<TM, GROUP>, ready, slabs, 1, 2, TcShape<TM>::kThreads, TcShape<TM>::kSmem, a, stream, map);
+  return launch(tile_kernel<TM, GROUP>, ready, slabs, 1, 2, TcShape<TM, GROUP>::kThreads, TcShape<TM, GROUP>::kSmem, a, stream, codes,
+                x);
 }
 
-template <int TM>
-cudaError_t tiles_by_group(const Args& a, int group, const CUtensorMap& map, void* stream) {
-  return group == 128  ? launch_tiles<TM, 128>(a, map, stream)
-         : group == 64 ? launch_tiles<TM, 64>(a, map, stream)
-                       : launch_tiles<TM, 32>(a, map, stream);
-}
-
-// Rows of K / 2 bytes of codes in boxes of 64 bytes by 128 rows, 64-byte swizzle, zeros outside.
-bool codes_map(CUtensorMap* map, const LinearW4Launch& L, std::string* err) {
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* at, long long cols, long long rows, long long pitch,
+            int box_cols, int box_rows, CUtensorMapSwizzle swizzle, std::string* err) {
   const tc::EncodeTiledFn enc = tc::encoder(err);
   if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)(L.K / 2), (cuuint64_t)L.N};
-  const cuuint64_t strides[1] = {(cuuint64_t)L.ldw};
-  const cuuint32_t box[2] = {64, kTcRows}, estr[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(L.W), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+  const CUresult r = enc(map, type, 2, const_cast<void*>(at), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) *err = "linear_w4: cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
   return r == CUDA_SUCCESS;
+}
+
+// Rows of K / 2 bytes of codes in boxes of 64 bytes by 128 rows, of K values of x in boxes of 64 by TM; zeros outside.
+template <int TM>
+cudaError_t tiles_by_group(const Args& a, int group, void* stream, std::string* err) {
+  CUtensorMap codes, x;
+  if (!encode(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, a.K / 2, a.N, a.ldw, 64, kTcRows, CU_TENSOR_MAP_SWIZZLE_64B, err) ||
+      !encode(&x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.K, a.M, a.ldx * 2, 64, TM, CU_TENSOR_MAP_SWIZZLE_128B, err))
+    return cudaErrorInvalidValue;
+  return group == 128  ? launch_tiles<TM, 128>(a, codes, x, stream)
+         : group == 64 ? launch_tiles<TM, 64>(a, codes, x, stream)
+                       : launch_tiles<TM, 32>(a, codes, x, stream);
 }
 
 }  // namespace w4
@@ -671,12 +689,11 @@ int linear_w4_launch(const LinearW4Launch& L, std::string* err) {
         : L.group == 64 ? w4::launch_rows<2>(a, L.stream)
                         : w4::launch_rows<1>(a, L.stream);
   } else {
-    CUtensorMap map;
-    if (!w4::codes_map(&map, L, err)) return SV_ERR_CUDA;
-    e = L.M <= 16   ? w4::tiles_by_group<16>(a, L.group, map, L.stream)
-        : L.M <= 32 ? w4::tiles_by_group<32>(a, L.group, map, L.stream)
-                    : w4::tiles_by_group<64>(a, L.group, map, L.stream);
+    e = L.M <= 16   ? w4::tiles_by_group<16>(a, L.group, L.stream, err)
+        : L.M <= 32 ? w4::tiles_by_group<32>(a, L.group, L.stream, err)
+                    : w4::tiles_by_group<64>(a, L.group, L.stream, err);
   }
+  if (e != cudaSuccess && !err->empty()) return SV_ERR_CUDA;
   if (e == cudaSuccess) return SV_OK;
   *err = std::string("linear_w4 launch: ") + cudaGetErrorString(e);
   return SV_ERR_CUDA;
