@@ -10,6 +10,7 @@ Every computation happens in the library's kernels; there is no fallback.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -404,8 +405,14 @@ def _pools(pools, page_bytes, num_pools):
     """The host arrays of page arrays' addresses and page sizes (None stays NULL)."""
     if pools is not None and len(pools) != num_pools or page_bytes is not None and len(page_bytes) != num_pools:
         raise ValueError(f"expected {num_pools} pools and page sizes")
-    return (None if pools is None else (_vp * num_pools)(*[_ptr(p) for p in pools]),
-            None if page_bytes is None else (_i64 * num_pools)(*page_bytes))
+    # (through array.array: half the time of filling a ctypes array item by item)
+    addresses = None if pools is None else [p.data_ptr() if getattr(p, "is_cuda", False) else _ptr(p) or 0 for p in pools]
+    return _host_array("Q", addresses), _host_array("q", page_bytes)
+
+
+def _host_array(code, values):
+    """A host array of 64-bit values; NULL for None and for no values."""
+    return (_i64 * len(values)).from_buffer(array.array(code, values)) if values else None
 
 
 def sv_kv_copy_pages(pools, page_bytes, num_pools, num_pages, src, dst, n, workspace, workspace_bytes,
