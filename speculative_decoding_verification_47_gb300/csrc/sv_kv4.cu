@@ -81,56 +81,53 @@ struct RowArgs {
   const uint16_t* in[2];  // K, V
   void* out[2];
   long long seq, pos, head;  // elements
-  long long items;           // of `tokens` tokens each: `per_seq` a sequence
-  int out_f32, B, T, Hkv, tokens, per_seq;
+  int out_f32, B, T, Hkv, tokens;  // tokens of a CTA's turn
   Divider by_rows;           // 2 * Hkv, a token's
   uint32_t* flags;
 };
 
-// A CTA's tokens: first .. last - 1 of sequence b.
-struct RowItem {
-  int b, first, last, start;
+// A sequence's tokens: n of them from `start`; 0 of one that is left out.
+struct RowSeq {
+  int b, n, start;
+  const int32_t* table;
 };
-__device__ __forceinline__ bool row_item(const RowArgs& a, long long item, RowItem* it) {
-  it->b = (int)(item / a.per_seq);
-  it->first = (int)(item - (long long)it->b * a.per_seq) * a.tokens;
-  const int n = a.n_per_row ? a.n_per_row[it->b] : a.T;
-  it->start = a.starts[it->b];
-  if (n < 0 || n > a.T || it->start < 0 || (long long)it->start + n > (long long)a.c.max_pages * a.c.page_size) {
-    if (threadIdx.x == 0 && it->first == 0) atomicOr(a.flags, SV_FLAG_BAD_N);
-    return false;
+__device__ __forceinline__ RowSeq row_seq(const RowArgs& a, int b) {
+  RowSeq q;
+  q.b = b;
+  q.n = a.n_per_row ? a.n_per_row[b] : a.T;
+  q.start = a.starts[b];
+  q.table = a.c.table + (long long)b * a.c.max_pages;
+  if (q.n < 0 || q.n > a.T || q.start < 0 || (long long)q.start + q.n > (long long)a.c.max_pages * a.c.page_size) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.flags, SV_FLAG_BAD_N);
+    q.n = 0;
   }
-  it->last = min(it->first + a.tokens, n);
-  return it->first < it->last;
+  return q;
 }
 
-// A thread's row: of token i, part 0 (K) or 1 (V), head h.  codes: its bytes in the pool; NULL if it has none.
+// A thread's row: of token i, part 0 (K) or 1 (V), head h; its bytes in the pool.  One that is behind the last token or
+// on a bad page is not `there`, and stands for another, so that nothing waits before its loads.
 struct Row {
   int i, part, h;
+  bool there;
   uint8_t* codes;
-  uint32_t* scale;  // its (s, m)
+  int scale;  // from its codes to its (s, m)
 };
 template <int D>
-__device__ __forceinline__ Row row_of(const RowArgs& a, const RowItem& it, int r) {
+__device__ __forceinline__ Row row_of(const RowArgs& a, const RowSeq& q, int first, int last, int r) {
   Row w;
   const int tok = divide(r, a.by_rows), rest = r - tok * 2 * a.Hkv;
-  w.i = it.first + tok;
+  w.i = min(first + tok, last - 1);
   w.part = rest >= a.Hkv;
   w.h = rest - w.part * a.Hkv;
-  w.codes = nullptr;
-  w.scale = nullptr;
-  if (w.i < it.last) {
-    const int t = it.start + w.i, p = divide(t, a.c.by_page), slot = t - p * a.c.page_size;
-    const int page = a.c.table[(long long)it.b * a.c.max_pages + p];
-    if ((unsigned)page < (unsigned)a.c.num_pages) {
-      uint8_t* at = a.c.pool + page * a.c.page_bytes + (long long)w.h * a.c.head_bytes;
-      const int half = a.c.page_size * (D / 2);
-      w.codes = at + (long long)w.part * half + slot * (D / 2);
-      w.scale = reinterpret_cast<uint32_t*>(at + 2LL * half + (long long)w.part * a.c.page_size * 4) + slot;
-    } else if (rest == 0) {
-      atomicOr(a.flags, SV_FLAG_BAD_PAGE);
-    }
-  }
+  const int t = q.start + w.i, p = divide(t, a.c.by_page), slot = t - p * a.c.page_size;
+  const int page = q.table[p];
+  const bool good = (unsigned)page < (unsigned)a.c.num_pages;
+  if (!good && rest == 0) atomicOr(a.flags, SV_FLAG_BAD_PAGE);
+  w.there = good && first + tok < last;
+  const int half = a.c.page_size * (D / 2);  // (a page has fewer than 2^31 bytes)
+  w.codes = a.c.pool + (unsigned long long)(good ? (uint32_t)page : 0u) * (uint32_t)a.c.page_bytes +
+            (uint32_t)(w.h * a.c.head_bytes + w.part * half + slot * (D / 2));
+  w.scale = (2 - w.part) * half + w.part * a.c.page_size * 4 - slot * (D / 2 - 4);
   return w;
 }
 
@@ -161,26 +158,30 @@ struct Coder {
   // Codes of 8 values: the nearest integers to (x - m) / s, ties to even.  The product with the reciprocal,
   // rounded by the addition of 1.5 2^23, is one off at most, where the quotient lies next to a border: the
   // remainder (exact: c and s have 4 and 8 bits) is then beyond half a step, or is half a step and c is odd.
+  // Remainders of half a step or more are looked for together (of 8 normal values one in sixty has any).
   __device__ __forceinline__ uint32_t word(const uint4& v) const {
     const uint32_t pairs[4] = {v.x, v.y, v.z, v.w};
     const F2 magic = f2_pack(12582912.f, 12582912.f), less = f2_pack(-12582912.f, -12582912.f);
-    uint32_t w = 0;
+    float y[8], r[8], far = 0.f;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const F2 t = f2_fma(f2_pack(bf16_lo(pairs[p]), bf16_hi(pairs[p])), hx, hm);
-      F2 y = f2_fma(t, inv, magic);
-      float y0, y1, r0, r1;
-      f2_unpack(y, y0, y1);
-      y0 = fminf(y0, 12582927.f), y1 = fminf(y1, 12582927.f);  // (a subnormal scale may be rounded far down)
-      f2_unpack(f2_fma(f2_add(f2_pack(y0, y1), less), step, t), r0, r1);
-      w |= code(y0, r0) << (8 * p) | code(y1, r1) << (8 * p + 4);
+      f2_unpack(f2_fma(t, inv, magic), y[2 * p], y[2 * p + 1]);
+#pragma unroll
+      for (int e = 2 * p; e < 2 * p + 2; ++e) y[e] = fminf(y[e], 12582927.f);  // (a subnormal scale may be rounded far down)
+      f2_unpack(f2_fma(f2_add(f2_pack(y[2 * p], y[2 * p + 1]), less), step, t), r[2 * p], r[2 * p + 1]);
+      far = fmaxf(far, fmaxf(fabsf(r[2 * p]), fabsf(r[2 * p + 1])));
     }
-    return w;
-  }
-  __device__ __forceinline__ uint32_t code(float y, float r) const {
-    int c = (int)(__float_as_uint(y) & 15u);
-    if (fabsf(r) > (c & 1 ? below : half)) c = min(c + (r > 0.f ? 1 : -1), 15);
-    return (uint32_t)c;
+    if (far >= half) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (fabsf(r[e]) > (__float_as_uint(y[e]) & 1u ? below : half)) y[e] = fminf(y[e] + (r[e] > 0.f ? 1.f : -1.f), 12582927.f);
+    }
+    // the codes are the low bits of their floats, and the rest of these is known
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 7; e >= 0; --e) w = w * 16u + __float_as_uint(y[e]);
+    return w - 0x4b400000u * 0x11111111u;
   }
 };
 
@@ -189,55 +190,53 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
   constexpr int LANES = D / 16, PASS = kRowThreads / LANES, U = kRowsAhead;
   pdl_wait();
   const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
-  for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
-    RowItem it;
-    if (!row_item(a, item, &it)) continue;  // (the whole CTA)
-    const int rows = (it.last - it.first) * 2 * a.Hkv;
-    for (int r0 = 0; r0 < rows; r0 += U * PASS) {  // (every lane of a warp takes every turn)
-      Row w[U];
-      uint4 v[U][2];
+  for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
+    const RowSeq q = row_seq(a, b);
+    for (long long at = (long long)blockIdx.x * a.tokens; at < q.n; at += (long long)gridDim.x * a.tokens) {
+      const int first = (int)at, last = min(first + a.tokens, q.n), rows = (last - first) * 2 * a.Hkv;
+      for (int r0 = 0; r0 < rows; r0 += U * PASS) {  // (every lane of a warp takes every turn)
+        Row w[U];
+        uint4 v[U][2];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        w[u] = row_of<D>(a, it, r0 + u * PASS + mine);
-        v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
-        if (w[u].codes) {
-          const uint4* from = reinterpret_cast<const uint4*>((w[u].part ? a.in[1] : a.in[0]) + it.b * a.seq + w[u].i * a.pos +
+        for (int u = 0; u < U; ++u) {
+          w[u] = row_of<D>(a, q, first, last, r0 + u * PASS + mine);
+          const uint4* from = reinterpret_cast<const uint4*>((w[u].part ? a.in[1] : a.in[0]) + b * a.seq + w[u].i * a.pos +
                                                              w[u].h * a.head + lane * 16);
           v[u][0] = __ldcs(from);
           v[u][1] = __ldcs(from + 1);
         }
-      }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint32_t lo2 = min2(min2(v[u][0].x, v[u][0].y), min2(v[u][0].z, v[u][0].w));
-        uint32_t hi2 = max2(max2(v[u][0].x, v[u][0].y), max2(v[u][0].z, v[u][0].w));
-        lo2 = min2(lo2, min2(min2(v[u][1].x, v[u][1].y), min2(v[u][1].z, v[u][1].w)));
-        hi2 = max2(hi2, max2(max2(v[u][1].x, v[u][1].y), max2(v[u][1].z, v[u][1].w)));
-        lo2 = min2(lo2, lo2 >> 16 | lo2 << 16);
-        hi2 = max2(hi2, hi2 >> 16 | hi2 << 16);
-        uint32_t both = __byte_perm(lo2, hi2, 0x5410);  // the minimum and the maximum
+        for (int u = 0; u < U; ++u) {
+          uint32_t lo2 = min2(min2(v[u][0].x, v[u][0].y), min2(v[u][0].z, v[u][0].w));
+          uint32_t hi2 = max2(max2(v[u][0].x, v[u][0].y), max2(v[u][0].z, v[u][0].w));
+          lo2 = min2(lo2, min2(min2(v[u][1].x, v[u][1].y), min2(v[u][1].z, v[u][1].w)));
+          hi2 = max2(hi2, max2(max2(v[u][1].x, v[u][1].y), max2(v[u][1].z, v[u][1].w)));
+          lo2 = min2(lo2, lo2 >> 16 | lo2 << 16);
+          hi2 = max2(hi2, hi2 >> 16 | hi2 << 16);
+          uint32_t both = __byte_perm(lo2, hi2, 0x5410);  // the minimum and the maximum
 #pragma unroll
-        for (int m = 1; m < LANES; m <<= 1) {
-          const uint32_t o = __shfl_xor_sync(0xffffffffu, both, m);
-          both = __byte_perm(min2(both, o), max2(both, o), 0x7610);
+          for (int m = 1; m < LANES; m <<= 1) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, both, m);
+            both = __byte_perm(min2(both, o), max2(both, o), 0x7610);
+          }
+          if (!w[u].there) continue;
+          const float lo = bf16_lo(both), hi = bf16_hi(both);
+          // (max - min) / 15, correctly rounded twice: a float32 quotient of values with 8 bits lies on
+          // a border of bf16 only if the exact one does
+          const float s = 2.f * __fdiv_rn(0.5f * hi - 0.5f * lo, 15.f);
+          uint16_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(s)), mb = (uint16_t)both;
+          const float sr = __uint_as_float((uint32_t)sb << 16);
+          uint2 words = make_uint2(0, 0);
+          if (!(isfinite(lo) && isfinite(hi))) {
+            sb = mb = 0x7fc0u;  // a token that is not finite makes the scores of the queries that see it NaN
+          } else if (sr > 0.f) {
+            const Coder coder(lo, sr);
+            words.x = coder.word(v[u][0]);
+            words.y = coder.word(v[u][1]);
+          }
+          reinterpret_cast<uint2*>(w[u].codes)[lane] = words;
+          if (lane == 0) *reinterpret_cast<uint32_t*>(w[u].codes + w[u].scale) = (uint32_t)sb | (uint32_t)mb << 16;
         }
-        if (!w[u].codes) continue;
-        const float lo = bf16_lo(both), hi = bf16_hi(both);
-        // (max - min) / 15, correctly rounded twice: a float32 quotient of values with 8 bits lies on
-        // a border of bf16 only if the exact one does
-        const float s = 2.f * __fdiv_rn(0.5f * hi - 0.5f * lo, 15.f);
-        uint16_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(s)), mb = (uint16_t)both;
-        const float sr = __uint_as_float((uint32_t)sb << 16);
-        uint2 words = make_uint2(0, 0);
-        if (!(isfinite(lo) && isfinite(hi))) {
-          sb = mb = 0x7fc0u;  // a token that is not finite makes the scores of the queries that see it NaN
-        } else if (sr > 0.f) {
-          const Coder coder(lo, sr);
-          words.x = coder.word(v[u][0]);
-          words.y = coder.word(v[u][1]);
-        }
-        reinterpret_cast<uint2*>(w[u].codes)[lane] = words;
-        if (lane == 0) *w[u].scale = (uint32_t)sb | (uint32_t)mb << 16;
       }
     }
   }
@@ -248,45 +247,45 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
   constexpr int LANES = D / 16, PASS = kRowThreads / LANES, U = kRowsAhead;
   pdl_wait();
   const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
-  for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
-    RowItem it;
-    if (!row_item(a, item, &it)) continue;
-    const int rows = (it.last - it.first) * 2 * a.Hkv;
-    for (int r0 = mine; r0 < rows; r0 += U * PASS) {
-      Row w[U];
-      uint2 words[U];
-      uint32_t sm[U];
+  for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
+    const RowSeq q = row_seq(a, b);
+    for (long long at = (long long)blockIdx.x * a.tokens; at < q.n; at += (long long)gridDim.x * a.tokens) {
+      const int first = (int)at, last = min(first + a.tokens, q.n), rows = (last - first) * 2 * a.Hkv;
+      for (int r0 = mine; r0 < rows; r0 += U * PASS) {
+        Row w[U];
+        uint2 words[U];
+        uint32_t sm[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        w[u] = row_of<D>(a, it, r0 + u * PASS);
-        words[u] = make_uint2(0, 0), sm[u] = 0;
-        if (w[u].codes) {
+        for (int u = 0; u < U; ++u) {
+          w[u] = row_of<D>(a, q, first, last, r0 + u * PASS);
           words[u] = __ldcs(reinterpret_cast<const uint2*>(w[u].codes) + lane);
-          sm[u] = *w[u].scale;
+          sm[u] = *reinterpret_cast<const uint32_t*>(w[u].codes + w[u].scale);
         }
-      }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (!w[u].codes) continue;
-        const float s = bf16_lo(sm[u]), m = bf16_hi(sm[u]);
-        float y[16];
+        for (int u = 0; u < U; ++u) {
+          if (!w[u].there) continue;
+          const float s = bf16_lo(sm[u]), m = bf16_hi(sm[u]);
+          const F2 ss = f2_pack(s, s), mm = f2_pack(m, m), less = f2_pack(-8388608.f, -8388608.f);
+          float y[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {  // (the code as the low bits of 2^23 + c)
-          const uint32_t c = ((e < 8 ? words[u].x : words[u].y) >> (4 * (e & 7)) & 15u) | 0x4b000000u;
-          y[e] = __fmaf_rn(__uint_as_float(c) - 8388608.f, s, m);
-        }
-        const long long to = it.b * a.seq + w[u].i * a.pos + w[u].h * a.head + lane * 16;
-        void* out = w[u].part ? a.out[1] : a.out[0];
-        if (a.out_f32) {
-          float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + to);
+          for (int e = 0; e < 16; e += 2) {  // (the codes as the low bits of 2^23 + c)
+            const uint32_t word = e < 8 ? words[u].x : words[u].y;
+            const uint32_t c0 = (word >> (4 * (e & 7)) & 15u) | 0x4b000000u, c1 = (word >> (4 * (e & 7) + 4) & 15u) | 0x4b000000u;
+            f2_unpack(f2_fma(f2_add(f2_pack(__uint_as_float(c0), __uint_as_float(c1)), less), ss, mm), y[e], y[e + 1]);
+          }
+          const long long to = b * a.seq + w[u].i * a.pos + w[u].h * a.head + lane * 16;
+          void* out = w[u].part ? a.out[1] : a.out[0];
+          if (a.out_f32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + to);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) o[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-        } else {
-          uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to);
+            for (int q = 0; q < 4; ++q) o[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+          } else {
+            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to);
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            o[q] = make_uint4(tc::pack_bf16x2(y[8 * q], y[8 * q + 1]), tc::pack_bf16x2(y[8 * q + 2], y[8 * q + 3]),
-                              tc::pack_bf16x2(y[8 * q + 4], y[8 * q + 5]), tc::pack_bf16x2(y[8 * q + 6], y[8 * q + 7]));
+            for (int q = 0; q < 2; ++q)
+              o[q] = make_uint4(tc::pack_bf16x2(y[8 * q], y[8 * q + 1]), tc::pack_bf16x2(y[8 * q + 2], y[8 * q + 3]),
+                                tc::pack_bf16x2(y[8 * q + 4], y[8 * q + 5]), tc::pack_bf16x2(y[8 * q + 6], y[8 * q + 7]));
+          }
         }
       }
     }
@@ -1392,14 +1391,13 @@ int kv4_rows_launch(const Kv4RowsLaunch& L, std::string* err) {
   const int at_once = kv4::kRowThreads / (L.D / 16) * kv4::kRowsAhead;
   a.tokens = at_once / (2 * L.c.Hkv) > 1 ? at_once / (2 * L.c.Hkv) : 1;
   if (a.tokens > L.T) a.tokens = L.T;
-  a.per_seq = (L.T + a.tokens - 1) / a.tokens;
-  a.items = (long long)L.B * a.per_seq;
   a.by_rows = kv4::divider(2 * L.c.Hkv);
-  long long blocks = a.items;
-  const long long most = (long long)tc::num_sms() * 64;
-  if (blocks > most) blocks = most;
+  // a row of CTAs a sequence, no more in all than keep every SM busy with several
+  const long long per_seq = (L.T + a.tokens - 1) / a.tokens, most = (long long)tc::num_sms() * 16;
+  const int across = (int)(per_seq < most ? per_seq : most), rows = (int)(most / across);
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = kv4::config((int)blocks, kv4::kRowThreads, 0, L.stream, &attr);
+  cudaLaunchConfig_t cfg = kv4::config(across, kv4::kRowThreads, 0, L.stream, &attr);
+  cfg.gridDim.y = (unsigned)(rows < 1 ? 1 : rows < L.B ? rows : L.B);
   auto* kernel = L.k_in ? (L.D == 128 ? kv4::append_kernel<128> : kv4::append_kernel<64>)
                         : (L.D == 128 ? kv4::read_kernel<128> : kv4::read_kernel<64>);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
