@@ -589,7 +589,9 @@ sv_status sv_kv4_read(const void* pool, int num_pages, int page_size, const int3
  * 2^-126 count as 0 in v.  A sequence with k_b outside [0, K] (SV_FLAG_BAD_K), with
  * L < 0 or L + k_b past its table (SV_FLAG_BAD_N), or with a page outside
  * [0, num_pages) among those that its queries see (SV_FLAG_BAD_PAGE) gets NaN in
- * out and lse at every position 0 .. k_b (0 .. K for a bad k_b).
+ * out and lse at every position 0 .. k_b (0 .. K for a bad k_b).  Waits are bounded
+ * (about a second): one that runs out sets SV_FLAG_TIMEOUT, and what was waited for
+ * is NaN.
  */
 size_t sv_kv4_attention_workspace_size(int B, int K, int Hq, int Hkv, int D);
 sv_status sv_kv4_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_stride,
@@ -617,7 +619,13 @@ sv_status sv_kv4_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_st
  *             zeroed once; calls that share it must be ordered on one stream.
  * x and W must be 16-byte aligned with row strides of a multiple of 16 bytes; the
  * rest needs its element's alignment.  out must not overlap an input but residual.
- * Codes less their zeros are exact; sums are float32, rounded once at the end.
+ * Codes less their zeros are exact; sums are float32, rounded once at the end.  With
+ * M > 8 x is taken as it is.  With M <= 8 each row's 128 values of x (from a multiple
+ * of 128 on) become fp16 next to a power of two: their 8 bits are kept down to 2^-25
+ * of the largest of the 128, what is smaller counts as 0.  A value of x, a scale, a
+ * bias or a residual that is not finite makes the outputs that it belongs to not
+ * finite, no others.  Waits are bounded (about a second): one that runs out sets
+ * SV_FLAG_TIMEOUT and leaves NaN in its outputs.
  */
 size_t sv_linear_w4_workspace_size(int M, int N, int K);
 sv_status sv_linear_w4(const void* x, int64_t ldx, const void* W, int64_t ldw, const void* scales,

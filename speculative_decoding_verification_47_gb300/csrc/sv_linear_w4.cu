@@ -118,6 +118,8 @@ constexpr int kStages = 8;   // of a warp
 constexpr int kAhead = 6;    // steps on their way
 constexpr int kStageBytes = 16 * kPitch;
 
+// 1 x 16384 x 4096 in groups of 128: 15 to 19 us, where W's 34 MB take 5; the start, the ends of the chunks' chains and
+// the instructions (45% of the issue slots) share the rest.
 constexpr int kTiles = 4;    // of a CTA: more share the work on x, fewer want fewer registers
 constexpr int kRows = 16 * kTiles;
 constexpr int kCtas = 2;     // of an SM
@@ -247,8 +249,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
       for (int l = 0; l < L; ++l) {
         const uint32_t p = here + ((slot + i) & (kStages - 1)) * kStageBytes + l * VEC * 16;
         if constexpr (VEC == 4) {
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(p) : "memory");
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(p + 8 * kPitch) : "memory");
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                       : "r"(p)
+                       : "memory");
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(p + 8 * kPitch)
+                       : "memory");
         } else if constexpr (VEC == 2) {
           asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[2 * l]), "=r"(u[2 * l + 1]) : "r"(p) : "memory");
           asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[2 * l]), "=r"(v[2 * l + 1]) : "r"(p + 8 * kPitch) : "memory");
@@ -306,13 +314,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
 
 // ---------------------------------------------------------------------------
 // More rows of x: the 5th-generation tensor cores.  A CTA takes 128 rows of W by TM rows of x and a part of K, in
-// blocks of 128 k.  Codes and x arrive by TMA; eight warps make the codes bf16 integers (code less zero, exact) in
-// tensor memory, where the 128-row operand may stand (through shared memory its bytes were the bound); a thread issues
+// blocks of 128 k.  Codes and x arrive by TMA; four warps of a block make its codes bf16 integers (code less zero,
+// exact) in tensor memory, where the 128-row operand may stand (through shared memory its bytes were the bound); a thread issues
 // the groups' products, each group's into an accumulator of tensor memory of its own; four or eight warps take those
-// out, times the groups' scales, and add them to their float32 sums in registers.
+// out, times the groups' scales, and add them to their float32 sums in registers.  64 x 16384 x 4096 in groups of 128:
+// 21.5 us, 16 x 8192 x 8192 in groups of 64: 19.9 us, where W's 34 MB take 5; bound by the way of a block through these
+// warps (its parts take 400 to 800 cycles each, and four are under way), next by the instructions that take codes
+// apart.  mma.sync took 66 us for the first, since each warp then multiplies all rows of x and the codes have to be
+// taken apart again for every 8 of them.
 // ---------------------------------------------------------------------------
-constexpr int kTeams = 4;            // a team takes every kTeams-th block, of the two issuing warps each every other one
-constexpr int kCodeWarps = 16 / kTeams;
+constexpr int kTeams = 4;            // a team takes every fourth block, of the two issuing warps each every other one
+constexpr int kCodeWarps = 4;        // of a team: a row of W a thread
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kSumWarp = 19;
 constexpr int kTcRows = 128;
 constexpr int kRaw = 8;              // blocks of codes and x on their way
@@ -369,7 +381,8 @@ __global__ void __launch_bounds__(TcShape<TM, GROUP>::kThreads, 1) tile_kernel(
   using S = TcShape<TM, GROUP>;
   constexpr int PER = S::kPer, UNIT = S::kUnit;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], a_full[kSides], a_empty[kSides], acc_full[S::kAccs], acc_empty[S::kAccs], done;
+  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], a_full[kSides], a_empty[kSides];
+  __shared__ __align__(8) uint64_t acc_full[S::kAccs], acc_empty[S::kAccs], done;
   __shared__ uint32_t tmem_base;
   __shared__ int failed, issued;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -415,39 +428,35 @@ __global__ void __launch_bounds__(TcShape<TM, GROUP>::kThreads, 1) tile_kernel(
   float total[S::kColumnsEach] = {};
 
   if (warp < kLoadWarp) {
-    const int team = warp / kCodeWarps, me = tid - team * kCodeWarps * 32;
-    constexpr int PARTS = kCodeWarps / 4, RUNS = 4 / PARTS;  // a thread has one of a row's parts, RUNS times 32 k
-    const int r = me & 127, part = me >> 7;
-    const int n = min(n0 + r, a.N - 1);
+    const int team = warp / kCodeWarps, r = tid - team * kCodeWarps * 32, n = min(n0 + r, a.N - 1);
     // (without zeros the bytes of W are loaded in their place and not used: a choice at the load would wait for it)
     const bool has_zeros = a.zeros != nullptr;
     const uint8_t* zrow = has_zeros ? a.zeros + (uint32_t)n * a.groups : a.W + n * a.ldw;
-    constexpr int Z = RUNS * 32 > GROUP ? RUNS * 32 / GROUP : 1;  // groups of the part
-    auto load_zeros = [&](int b, uint32_t (&z)[Z]) {
+    auto load_zeros = [&](int b, uint32_t (&z)[PER]) {
 #pragma unroll
-      for (int q = 0; q < Z; ++q) z[q] = __ldg(zrow + min(b * PER + part * RUNS * 32 / GROUP + q, a.groups - 1));
+      for (int q = 0; q < PER; ++q) z[q] = __ldg(zrow + min(b * PER + q, a.groups - 1));
     };
-    uint32_t zn[Z];
+    uint32_t zn[PER];
     load_zeros(b0 + team, zn);
-    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kCodes + part * (RUNS * 16);  // (r's lane)
+    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kCodes;  // (r's lane)
     const uint32_t raw_row = r * 64, raw_flip = (uint32_t)(r >> 1) & 3;
     for (int b = b0 + team, g = team; b < b1; b += kTeams, g += kTeams) {
       const int s = g % kRaw, side = g % kSides;
-      uint32_t less[Z];
+      uint32_t less[PER];
 #pragma unroll
-      for (int q = 0; q < Z; ++q) less[q] = (has_zeros ? zn[q] : 8u) * 0x10001u + 0xc300c300u;
+      for (int q = 0; q < PER; ++q) less[q] = (has_zeros ? zn[q] : 8u) * 0x10001u + 0xc300c300u;
       load_zeros(b + kTeams, zn);
       if (g >= kSides && !__all_sync(kFull, wait(&a_empty[side], (g / kSides - 1) & 1))) break;  // (the whole warp)
       tc::fence_after();
       if (!__all_sync(kFull, wait(&raw_full[s], g / kRaw & 1))) break;
 #pragma unroll
-      for (int h = 0; h < RUNS; ++h) {
+      for (int h = 0; h < 4; ++h) {  // 32 k
         uint32_t w[4];
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(at_raw + s * S::kStage + raw_row + (((uint32_t)(part * RUNS + h) ^ raw_flip) << 4))
+                     : "r"(at_raw + s * S::kStage + raw_row + (((uint32_t)h ^ raw_flip) << 4))
                      : "memory");
-        const uint32_t l = less[h * Z / RUNS];
+        const uint32_t l = less[h * PER / 4];
 #pragma unroll
         for (int c = 0; c < 4; c += 2) {
           const uint32_t u = w[c], v = w[c + 1], u4 = u >> 4, v4 = v >> 4;
@@ -629,8 +638,8 @@ template <int TM, int GROUP>
 cudaError_t launch_tiles(const Args& a, const CUtensorMap& codes, const CUtensorMap& x, void* stream) {
   static std::atomic<int> ready[kMaxDevices];
   const long long slabs = ((a.N + kTcRows - 1LL) / kTcRows) * ((a.M + TM - 1LL) / TM);
-  return launch(tile_kernel<TM, GROUP>, ready, slabs, 1, 2, TcShape<TM, GROUP>::kThreads, TcShape<TM, GROUP>::kSmem, a, stream, codes,
-                x);
+  using S = TcShape<TM, GROUP>;
+  return launch(tile_kernel<TM, GROUP>, ready, slabs, 1, 2, S::kThreads, S::kSmem, a, stream, codes, x);
 }
 
 bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* at, long long cols, long long rows, long long pitch,

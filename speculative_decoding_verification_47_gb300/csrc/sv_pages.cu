@@ -9,7 +9,10 @@
 // of an id among the free or the live ones), never by the order of atomics: the
 // same inputs give the same ids.  The copies are bound by memory: a warp takes 2 KB
 // of a page at a time, four 16-byte words a lane in flight, and every page array
-// has its own row of the grid.
+// has its own row of the grid.  64 forks over 64 arrays of 32 KB pages: 24 to 27 us,
+// 252 MB in and out, partly through L2 (37 us at the measured copy rate); a pool of
+// 4096 pages of which 2048 move half: 21 us for the copies (19.8 us by their bytes).
+// The plans are single kernels of a few us before them.
 #include <cstdint>
 
 #include "sv_tc.cuh"
