@@ -617,8 +617,8 @@ sv_status sv_kv4_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_st
  *   M, N, K   each in 1 .. 2^30, N * K / group below 2^31; strides 0 select K, K / 2, N, N.
  *   workspace >= sv_linear_w4_workspace_size(M, N, K) bytes, 256-byte aligned,
  *             zeroed once; calls that share it must be ordered on one stream.
- * x and W must be 16-byte aligned with row strides of a multiple of 16 bytes; the
- * rest needs its element's alignment.  out must not overlap an input but residual.
+ * x and W must be 16-byte aligned with row strides of a multiple of 16 bytes (below
+ * 2^38 elements, of W bytes); the rest needs its element's alignment.  out must not overlap an input but residual.
  * Codes less their zeros are exact; sums are float32, rounded once at the end.  With
  * M > 8 x is taken as it is.  With M <= 8 each row's 128 values of x (from a multiple
  * of 128 on) become fp16 next to a power of two: their 8 bits are kept down to 2^-25

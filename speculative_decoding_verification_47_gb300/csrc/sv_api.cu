@@ -674,8 +674,9 @@ sv_status sv_linear_w4(const void* x, int64_t ldx, const void* W, int64_t ldw, c
   L.K = K;
   if (L.ldx < K || L.ldw < K / 2 || L.ldr < N || L.ldo < N)
     return fail(SV_ERR_SHAPE, "row strides must be 0 or at least the row's length");
-  if (L.ldx % 8 != 0 || L.ldw % 16 != 0 || L.ldw >= (1LL << 38))
-    return fail(SV_ERR_SHAPE, "row strides of x and W must be multiples of 16 bytes, W's below 2^38");
+  // the tensor-map limits of the operand copies
+  if (L.ldx % 8 != 0 || L.ldw % 16 != 0 || L.ldx >= (1LL << 38) || L.ldw >= (1LL << 38))
+    return fail(SV_ERR_SHAPE, "row strides of x and W must be multiples of 16 bytes below 2^38 elements");
   if (residual == out && L.ldr != L.ldo) return fail(SV_ERR_ARG, "residual over out needs its row stride");
   if (out == x || out == W) return fail(SV_ERR_ARG, "out must not be x or W");
   if (!workspace || !aligned(workspace, 256))

@@ -124,7 +124,7 @@ constexpr int kTiles = 4;    // of a CTA: more share the work on x, fewer want f
 constexpr int kRows = 16 * kTiles;
 constexpr int kCtas = 2;     // of an SM
 
-// Up to 8 rows of x (a block of 8 of more).  VEC words (VEC * 32 k) are a group.
+// Up to 8 rows of x.  VEC words (VEC * 32 k) are a group.
 template <int VEC>
 __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_constant__ Args a) {
   constexpr int COLS = 8, L = 4 / VEC;
@@ -135,9 +135,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   pdl_wait();
-  const unsigned block = blockIdx.x / a.split, rank = blockIdx.x - block * a.split;
-  const int blocks = (a.M + COLS - 1) / COLS, slab = (int)(block / blocks);
-  const int n0 = slab * kRows, m0 = (int)(block - slab * blocks) * COLS;  // (CTAs of the same rows of W are neighbours)
+  const unsigned slab = blockIdx.x / a.split, rank = blockIdx.x - slab * a.split;
+  const int n0 = (int)slab * kRows;
   const int chunks = (a.K + kChunk - 1) / kChunk, workers = (int)a.split * kWarps, me = (int)rank * kWarps + warp;
   // (neighbours in a row of W are read at about the same time: runs of 64 bytes alone are slow)
   const int c0 = me, c1 = chunks;
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
         zero[q][r] = __ldg(a.zeros ? a.zeros + at : reinterpret_cast<const uint8_t*>(a.scales + at));
       }
   };
-  const uint16_t* xrow = a.x + min(m0 + g, a.M - 1) * a.ldx;
+  const uint16_t* xrow = a.x + min(g, a.M - 1) * a.ldx;
   auto load_x = [&](int c, uint4 (&v)[4]) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -289,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();  // (the ring is read no more)
-  const int cols = min(COLS, a.M - m0);
+  const int cols = a.M;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     if (2 * t + j < cols) {
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
   }
   if (a.split > 1) tc::cluster_sync();
   else __syncthreads();
-  finish<kRows, kThreads>(a, part[0], n0, m0, cols, rank);
+  finish<kRows, kThreads>(a, part[0], n0, 0, cols, rank);
   if (a.split > 1) tc::cluster_sync();  // (no CTA leaves while its sums are read)
 }
 
@@ -630,7 +629,7 @@ cudaError_t launch(Kernel* kernel, std::atomic<int>* ready, long long slabs, int
 template <int VEC>
 cudaError_t launch_rows(const Args& a, void* stream) {
   static std::atomic<int> ready[kMaxDevices];
-  const long long slabs = ((a.N + kRows - 1LL) / kRows) * ((a.M + 7LL) / 8);
+  const long long slabs = (a.N + kRows - 1LL) / kRows;
   return launch(rows_kernel<VEC>, ready, slabs, kCtas, kWarps, kThreads, kWarps * kStages * kStageBytes, a, stream);
 }
 

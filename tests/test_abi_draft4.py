@@ -98,7 +98,7 @@ LINEAR = dict(x=P, ldx=0, W=2 * P, ldw=0, scales=P, zeros=None, group=64, bias=N
     (dict(residual=3 * P, ldr=64), sb.SV_ERR_ARG), (dict(out=3 * P + 1), sb.SV_ERR_ARG),
     (dict(workspace=None), sb.SV_ERR_WORKSPACE), (dict(workspace=P + 4), sb.SV_ERR_WORKSPACE),
     (dict(workspace_bytes=4), sb.SV_ERR_WORKSPACE), (dict(N=1 << 30, K=256, out=1 << 45), sb.SV_ERR_SHAPE),
-    (dict(ldw=1 << 38), sb.SV_ERR_SHAPE),
+    (dict(ldw=1 << 38), sb.SV_ERR_SHAPE), (dict(ldx=1 << 38), sb.SV_ERR_SHAPE),
 ])
 def test_linear_w4_host_checks(kw, status):
     refused(sb.sv_linear_w4, LINEAR, kw, status)

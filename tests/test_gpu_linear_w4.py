@@ -148,3 +148,21 @@ def test_linear_w4_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M", [9, 20, 64])
+@pytest.mark.parametrize("N,K,group", [(5, 32, 32), (130, 64, 64), (1, 64, 32), (129, 128, 128), (300, 96, 32)])
+def test_linear_w4_of_less_than_a_block(M, N, K, group):
+    """K below a block's 128, rows below a tile's: what the copies' boxes reach outside of counts nothing."""
+    s = inputs(M + N + K, M, N, K, group, True, True, False, torch.float32)
+    check(s, run(s, M, N, K, group, sb.SV_ACT_NONE, torch.float32), sb.SV_ACT_NONE, torch.float32, group)
+
+
+@pytest.mark.parametrize("M,N,K,group", [(64, 128, 8192, 32), (50, 200, 32768, 32), (17, 128, 16384, 32), (16, 64, 16384, 128)])
+def test_linear_w4_many_blocks(M, N, K, group):
+    """Every ring comes round many times, with one block of accumulators and with several."""
+    s = inputs(M + N, M, N, K, group, True, False, False, torch.float32)
+    first = run(s, M, N, K, group, sb.SV_ACT_NONE, torch.float32)
+    check(s, first, sb.SV_ACT_NONE, torch.float32, group)
+    for _ in range(20):
+        assert torch.equal(run(s, M, N, K, group, sb.SV_ACT_NONE, torch.float32), first)
