@@ -350,7 +350,9 @@ struct Shape {
   static constexpr int kTileBytes = 2 * kTok * kRowBytes + 2 * kTok * 4;  // K, V, (s, m) of both
   static constexpr int kRing = kWarps * kStages * kTileBytes;
   static constexpr int kPart = kRows * (D + 2);  // floats of a part in memory
-  static constexpr int kMinCtas = NT == 1 ? 3 : 2;  // (two tiles a turn want 160 registers, two blocks of columns 230)
+  // Two tiles a turn want 160 registers; so do two blocks of columns of 64 (32 sequences of up to 8192 tokens, 8 heads
+  // of 64, 40 rows a group: 83 us with two CTAs an SM, 71 with three), of 128 they want 230 (163 us against 176).
+  static constexpr int kMinCtas = NT == 1 || D == 64 ? 3 : 2;
   // shared memory beside the ring: lists, barriers, and the fragments of Q of two blocks of columns (bytes, about)
   static constexpr int kStatic = 5000 + kWarps * (kRows * D * 2 + (NT == 1 ? 0 : NT * D * 16));
 };
