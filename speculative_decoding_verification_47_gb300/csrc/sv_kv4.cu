@@ -23,11 +23,11 @@
 //
 // 256 sequences of up to 4096 tokens, 32 query and 8 key heads of 128: 122 us, 592 MB at 72% of
 // the measured copy rate, and next to that bound by the integer instructions that take codes
-// apart (half the rate of the others; 53% of the slots).  64 sequences, 4 positions, a window of
-// 1024: 43 us for 75 MB, bound by the chains of a tile (two blocks of columns take 232 registers,
-// so eight warps share an SM).
+// apart (half the rate of the others; 53% of the slots).  64 sequences, 1 to 4 positions, a window
+// of 1024: 40 us for 75 MB, some 15 of it the way to the first tile and the joins of the parts.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -1337,13 +1337,26 @@ int attention_t(Args a, std::string* err, void* stream) {
   return SV_OK;
 }
 
+// 9 to 16 rows fit one block of 16, whose tiles are taken apart once, or two of 8, on half as many more warps with two
+// tiles a turn.  Rounds whose positions vary leave many of the second blocks empty: 64 sequences, 8 heads, 4 rows a
+// position and 1 to 4 positions behind a window of 256 / 1024 / 2048 tokens take 30.8 / 45.6 / 67.5 us with blocks of
+// 16 and 24.7 / 41.4 / 62.3 with 8.  With every row there it is 30.8 / 47.2 / 67.8 against 31.7 / 51.5 / 78.8, and 16
+// short sequences (6 tiles a warp) take 30.8 against 26.2.
+bool in_eights(const Args& a) {
+  long long tokens = (long long)a.c.max_pages * a.c.page_size;
+  if (a.window > 0) tokens = std::min(tokens, (long long)a.window + a.sinks + a.K + 2 * kTok);
+  const long long warps = tc::num_sms() * 2LL * kWarps, tiles = tokens / kTok * a.B * a.Hkv;  // (at most)
+  return tiles < warps * (a.kpr && a.K > 0 ? 40 : 7);
+}
+
 // The fewest columns that hold a call's rows; a page that begins and ends with a tile needs one look-up a tile.
 template <int D>
 int attention_d(const Args& a, std::string* err, void* stream) {
   const int rows = a.G * (a.K + 1);
   const bool aligned = a.c.page_size % kTok == 0;
   if (rows <= 4) return aligned ? attention_t<D, 4, true>(a, err, stream) : attention_t<D, 4, false>(a, err, stream);
-  if (rows <= 8) return aligned ? attention_t<D, 8, true>(a, err, stream) : attention_t<D, 8, false>(a, err, stream);
+  if (rows <= 8 || (rows <= 16 && in_eights(a)))
+    return aligned ? attention_t<D, 8, true>(a, err, stream) : attention_t<D, 8, false>(a, err, stream);
   return aligned ? attention_t<D, 16, true>(a, err, stream) : attention_t<D, 16, false>(a, err, stream);
 }
 

@@ -477,3 +477,17 @@ def test_attention_on_two_streams_at_once():
     torch.cuda.synchronize()
     for args, first, ws, stream, outs in cases:
         assert sb.sv_read_device_flags(ws) == 0 and all(torch.equal(o, first) for o in outs)
+
+
+@pytest.mark.parametrize("D,hq,hkv,K,page", [(128, 24, 2, 0, 16), (64, 16, 1, 0, 7), (128, 8, 2, 3, 16), (64, 9, 3, 4, 16)])
+def test_attention_of_blocks_of_sixteen_rows(D, hq, hkv, K, page):
+    """9 to 16 rows of a key head beside a table that could hold many tokens: they stay one block."""
+    r = np.random.default_rng(D + hq + K)
+    lens = [0, 1, 300, 77, 16, 33]
+    ks = [K, 0, K, K // 2, 0, K]
+    q, pool, table, max_pages = case(r, 6, K, hq, hkv, D, page, lens, ks)
+    wide = np.full((6, 4_000_000 // page), -1, np.int32)
+    wide[:, :max_pages] = table
+    out, lse, ws = attend(q.cuda(), dev(pool), dev(wide), dev(np.int32(lens)), dev(np.int32(ks)), page, D, hkv, 0.1)
+    assert sb.sv_read_device_flags(ws) == 0
+    compare(q, pool, table, lens, ks, page, D, hkv, 0.1, out, lse)
