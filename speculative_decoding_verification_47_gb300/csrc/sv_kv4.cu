@@ -199,6 +199,7 @@ struct Coder {
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_constant__ RowArgs a) {
   constexpr int LANES = D / 16, PASS = kRowThreads / LANES, U = kRowsAhead;
+  pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
@@ -256,6 +257,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant__ RowArgs a) {
   constexpr int LANES = D / 16, PASS = kRowThreads / LANES, U = kRowsAhead;
+  pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {

@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
   static_assert(kWarps * kStages * kStageBytes >= kWarps * COLS * kRows * 4, "the warps' sums fit over the ring");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  pdl_launch_dependents();
   pdl_wait();
   const unsigned slab = blockIdx.x / a.split, rank = blockIdx.x - slab * a.split;
   const int n0 = (int)slab * kRows;
@@ -417,6 +418,7 @@ __global__ void __launch_bounds__(TcShape<TM, GROUP>::kThreads, 1) tile_kernel(
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_base;
+  pdl_launch_dependents();  // (behind the allocation: a dependent cannot take this CTA's columns)
   pdl_wait();
   // a wait of at most about a second, none at all if `clocks` is 0; who gives up leaves its loop
   auto wait = [&](uint64_t* bar, uint32_t parity) {

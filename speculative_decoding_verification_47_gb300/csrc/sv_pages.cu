@@ -76,6 +76,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads)
     copy_kernel(const __grid_constant__ Pools<N> p, int num_pages, const int32_t* src, const int32_t* dst, int n,
                 uint32_t* ws) {
+  pdl_launch_dependents();
   pdl_wait();
   copy_pages(p.base[blockIdx.y], p.bytes[blockIdx.y], src, dst, n, num_pages, ws);
 }
@@ -98,6 +99,7 @@ struct ForkArgs {
 
 // A warp per fork: is it sound, and does it copy a page?
 __global__ void __launch_bounds__(kThreads) fork_check_kernel(const ForkArgs a) {
+  pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int f = (int)((blockIdx.x * (long long)kThreads + threadIdx.x) >> 5);
@@ -144,6 +146,7 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const __grid_const
   __shared__ int32_t from[kMaxForks], to[kMaxForks];
   __shared__ int warp_sum[kThreads / 32];
   __shared__ int unsound;
+  pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (a.F + kThreads - 1) / kThreads;
@@ -226,6 +229,7 @@ struct FreeArgs {
 
 // A warp per sequence: each of its pages loses an owner.  A page without one is left with -1.
 __global__ void __launch_bounds__(kThreads) free_rows_kernel(const FreeArgs a) {
+  pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int f = (int)((blockIdx.x * (long long)kThreads + threadIdx.x) >> 5);
@@ -253,6 +257,7 @@ __global__ void __launch_bounds__(kThreads) free_rows_kernel(const FreeArgs a) {
 // One CTA: the pages below 0 go on the stack, the lowest id last.
 __global__ void __launch_bounds__(kPlanThreads) free_push_kernel(const FreeArgs a) {
   __shared__ int warp_sum[kPlanThreads / 32];
+  pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int top = *a.top;
@@ -306,6 +311,7 @@ struct CompactArgs {
 };
 
 __global__ void __launch_bounds__(kThreads) mark_kernel(const CompactArgs a) {
+  pdl_launch_dependents();
   pdl_wait();
   const long long entries = (long long)a.B * a.max_pages;
   bool sound = true;
@@ -322,6 +328,7 @@ __global__ void __launch_bounds__(kThreads) mark_kernel(const CompactArgs a) {
 __global__ void __launch_bounds__(kPlanThreads) moves_kernel(const CompactArgs a) {
   __shared__ int warp_sum[kPlanThreads / 32];
   __shared__ int below;  // live pages with ids below their number
+  pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int live = 0;
@@ -371,6 +378,7 @@ __global__ void __launch_bounds__(kPlanThreads) moves_kernel(const CompactArgs a
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ Pools<N> p, const CompactArgs a) {
+  pdl_launch_dependents();
   pdl_wait();
   const int moves = (int)a.ws[1], live = (int)a.ws[2];
   if (blockIdx.y == 0) {
