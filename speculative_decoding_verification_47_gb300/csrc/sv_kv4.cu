@@ -409,6 +409,11 @@ struct Books {
   static constexpr int kBytes = 16;  // of a sequence
 };
 
+// a / b, in 32 bits where they fit (a third of the time).
+__device__ __forceinline__ unsigned long long quotient(unsigned long long a, unsigned long long b) {
+  return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
+}
+
 // The number of the group that unit `at` lies in.
 __device__ __forceinline__ uint32_t group_at(const Books& k, int B, unsigned long long at) {
   int lo = 0, hi = B - 1;  // the last b with cost[b] <= at
@@ -416,8 +421,7 @@ __device__ __forceinline__ uint32_t group_at(const Books& k, int B, unsigned lon
     const int mid = (lo + hi + 1) >> 1;
     if (k.cost[mid] <= at) lo = mid; else hi = mid - 1;
   }
-  const unsigned long long off = at - k.cost[lo];
-  return k.groups[lo] + (off >> 32 ? (uint32_t)(off / k.each[lo]) : (uint32_t)off / k.each[lo]);
+  return k.groups[lo] + (uint32_t)quotient(at - k.cost[lo], k.each[lo]);
 }
 
 // The runs of the warp's share [begin, end) in the groups first .. first + kList - 1, a lane per group;
@@ -881,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
   // the share of this warp; from here on the warps go their own ways
   const unsigned worker = blockIdx.x * kWarps + warp;
   const unsigned long long total = books.cost[a.B];
-  unsigned long long share = (total + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);
+  unsigned long long share = quotient(total + gridDim.x * kWarps - 1, gridDim.x * kWarps);
   if (share < kMinShare) share = kMinShare;
   const unsigned long long begin = worker * share, end = min(begin + share, total);
   if (begin >= end) return;
@@ -1235,8 +1239,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
     }
     if (!whole) {
       // the last warp of kJoin neighbours joins their parts into its first's, the last of these writes the result
-      const unsigned w0 = (unsigned)((sg.group + kGroupCost) / share);
-      const unsigned w1 = (unsigned)((sg.group + kGroupCost + s.tiles - 1) / share);
+      const unsigned w0 = (unsigned)quotient(sg.group + kGroupCost, share);
+      const unsigned w1 = (unsigned)quotient(sg.group + kGroupCost + s.tiles - 1, share);
       const unsigned blocks = (w1 - w0) / kJoin + 1, mine = w0 + (worker - w0) / kJoin * kJoin;
       const int n = (int)min((unsigned)kJoin, w1 - mine + 1);
       if (last_of(a.counters + mine, n, lane)) {
@@ -1257,17 +1261,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
           if (result) all.of(a, w0, kJoin, (int)blocks, share, sg.group, lane);
         }
         if (result) {
+          // lane r: where row r goes, and what it is multiplied by
+          const int i = (row0 + lane) / a.G, head = sg.h * a.G + (row0 + lane) % a.G;
+          const long long to_mine = sg.b * a.o_seq + i * a.o_pos + head * a.o_head;
+          const float inv_mine = all.l == 0.f ? 0.f : __frcp_rn(all.l);
+          if (lane < rows && a.lse) a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] = log_of_sum(all.top, all.l);
 #pragma unroll
           for (int r = 0; r < ROWS; ++r) {
-            const float l = __shfl_sync(kFull, all.l, r), inv = l == 0.f ? 0.f : __frcp_rn(l);
-            const float top = __shfl_sync(kFull, all.top, r);
+            const float inv = __shfl_sync(kFull, inv_mine, r);
+            uint32_t* to = reinterpret_cast<uint32_t*>(a.out + __shfl_sync(kFull, to_mine, r) + lane * (D / 32));
             if (r >= rows) continue;
-            const int i = (row0 + r) / a.G, head = sg.h * a.G + (row0 + r) % a.G;
-            uint16_t* row = a.out + sg.b * a.o_seq + i * a.o_pos + head * a.o_head;
-            uint32_t* to = reinterpret_cast<uint32_t*>(row + lane * (D / 32));
 #pragma unroll
             for (int e = 0; e < D / 64; ++e) to[e] = tc::pack_bf16x2(all.num[r][2 * e] * inv, all.num[r][2 * e + 1] * inv);
-            if (lane == 0 && a.lse) a.lse[((long long)sg.b * (a.K + 1) + i) * a.Hq + head] = log_of_sum(top, l);
           }
         }
       }
