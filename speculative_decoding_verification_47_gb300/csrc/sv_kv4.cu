@@ -24,7 +24,7 @@
 // 256 sequences of up to 4096 tokens, 32 query and 8 key heads of 128: 122 us, 592 MB at 72% of
 // the measured copy rate, and next to that bound by the integer instructions that take codes
 // apart (half the rate of the others; 53% of the slots).  64 sequences, 1 to 4 positions, a window
-// of 1024: 40 us for 75 MB, some 15 of it the way to the first tile and the joins of the parts.
+// of 1024: 37 us for 75 MB, some 15 of it the way to the first tile and the joins of the parts.
 #include <cuda_fp16.h>
 
 #include <algorithm>

@@ -118,7 +118,7 @@ constexpr int kStages = 8;   // of a warp
 constexpr int kAhead = 6;    // steps on their way
 constexpr int kStageBytes = 16 * kPitch;
 
-// 1 x 16384 x 4096 in groups of 128: 15 to 19 us, where W's 34 MB take 5; the start, the ends of the chunks' chains and
+// 1 x 16384 x 4096 in groups of 128: 14 to 17 us, where W's 34 MB take 5; the start, the ends of the chunks' chains and
 // the instructions (45% of the issue slots) share the rest.
 constexpr int kTiles = 4;    // of a CTA: more share the work on x, fewer want fewer registers
 constexpr int kRows = 16 * kTiles;
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
 // exact) in tensor memory, where the 128-row operand may stand (through shared memory its bytes were the bound); a thread issues
 // the groups' products, each group's into an accumulator of tensor memory of its own; four or eight warps take those
 // out, times the groups' scales, and add them to their float32 sums in registers.  64 x 16384 x 4096 in groups of 128:
-// 21.5 us, 16 x 8192 x 8192 in groups of 64: 19.9 us, where W's 34 MB take 5; bound by the way of a block through these
+// 20.5 us, 16 x 8192 x 8192 in groups of 64: 19.5 us, where W's 34 MB take 5; bound by the way of a block through these
 // warps (its parts take 400 to 800 cycles each, and four are under way), next by the instructions that take codes
 // apart.  mma.sync took 66 us for the first, since each warp then multiplies all rows of x and the codes have to be
 // taken apart again for every 8 of them.
