@@ -894,8 +894,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
 #pragma unroll 1
   for (uint32_t first = group_at(books, a.B, begin); more; first += kList) {
   const int segments = list_segments(a, books, S::kRows, first, begin, end, lane, list, &more);
+  ld.begin(a, segments, lane);  // (page ids are on their way while Q is asked for)
   if (segments > 0) qr.issue(a, list[0], lane);
-  ld.begin(a, segments, lane);
 #pragma unroll 1
   for (int st = 0; st < kStages - U; ++st) ld.issue(a, lane);
 #pragma unroll 1
