@@ -24,7 +24,7 @@
 // 256 sequences of up to 4096 tokens, 32 query and 8 key heads of 128: 122 us, 592 MB at 72% of
 // the measured copy rate, and next to that bound by the integer instructions that take codes
 // apart (half the rate of the others; 53% of the slots).  64 sequences, 1 to 4 positions, a window
-// of 1024: 37 us for 75 MB, some 15 of it the way to the first tile and the joins of the parts.
+// of 1024: 34 us for 75 MB, some 15 of it the way to the first tile and the joins of the parts.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -316,8 +316,10 @@ constexpr int kStages = 4;         // tiles of a warp on their way
 constexpr int kMaxSeqs = 1024;     // sequences of a launch
 constexpr int kMaxCtas = 640;
 constexpr int kMaxWarps = kMaxCtas * kWarps;
-constexpr int kMinShare = 5;       // of a warp
-constexpr int kGroupCost = 5;      // what a group costs beside its tiles, in tiles: Q, the stores, the way to the next
+constexpr int kMinShare = 7;       // of a warp (5: 4 sequences of a round 21.2 us, 7: 19.7)
+// What a group costs beside its tiles, in tiles: Q, the stores, the way to the next.  The 256 sequences take 135.5 /
+// 128.9 / 126.8 / 129.1 us in a graph with 3 / 5 / 9 / 13.
+constexpr int kGroupCost = 9;
 constexpr int kList = 16;          // segments that a warp looks up at a time
 constexpr int kJoin = 16;          // parts that are joined at once
 constexpr uint32_t kFull = 0xffffffffu;
