@@ -32,6 +32,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "sv_kv4_shares.h"
 #include "sv_tc.cuh"
 
 namespace sv {
@@ -316,12 +317,7 @@ constexpr int kStages = 4;         // tiles of a warp on their way
 constexpr int kMaxSeqs = 1024;     // sequences of a launch
 constexpr int kMaxCtas = 640;
 constexpr int kMaxWarps = kMaxCtas * kWarps;
-constexpr int kMinShare = 7;       // of a warp (5: 4 sequences of a round 21.2 us, 7: 19.7)
-// What a group costs beside its tiles, in tiles: Q, the stores, the way to the next.  The 256 sequences take 135.5 /
-// 128.9 / 126.8 / 129.1 us in a graph with 3 / 5 / 9 / 13.
-constexpr int kGroupCost = 9;
 constexpr int kList = 16;          // segments that a warp looks up at a time
-constexpr int kJoin = 16;          // parts that are joined at once
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kNone = -3e38f;    // a reference before the first score
 
@@ -338,7 +334,7 @@ struct Args {
   float* lse;
   int B, K, Hq, Hkv, G;
   uint32_t* flags;
-  uint32_t* counters;  // [2][kMaxWarps]: finished parts (and joins of kJoin parts) of cut groups; 0 between calls
+  uint32_t* counters;  // [2][kMaxWarps]: finished parts of runs, and joined runs, of cut groups; 0 between calls
   float* parts;        // [warp][2][rows * (D + 2)]
   long long clocks;    // of a wait for a copy; 0: none is waited for
 };
@@ -410,11 +406,6 @@ struct Books {
   uint32_t* each;            // [B]
   static constexpr int kBytes = 16;  // of a sequence
 };
-
-// a / b, in 32 bits where they fit (a third of the time).
-__device__ __forceinline__ unsigned long long quotient(unsigned long long a, unsigned long long b) {
-  return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
-}
 
 // The number of the group that unit `at` lies in.
 __device__ __forceinline__ uint32_t group_at(const Books& k, int B, unsigned long long at) {
@@ -738,11 +729,9 @@ struct QueryRows {
   }
 };
 
-// Where a warp's part of a group lies: the first of a group that began in front of the warp's share, the
-// second of one that begins inside it.
 template <int PART>
 __device__ __forceinline__ float* part_of(const Args& a, unsigned warp, unsigned long long share, unsigned long long group) {
-  return a.parts + ((long long)warp * 2 + (warp * share >= group ? 0 : 1)) * PART;
+  return a.parts + ((long long)warp * 2 + part_place(warp, share, group)) * PART;
 }
 
 // The parts of the warps first, first + step, .. (n of them) joined, in the order of the warps, for all
@@ -797,7 +786,8 @@ struct Joined {
   }
 };
 
-// One more of `all` is done (with what the warp wrote before); true if it was the last, which leaves 0.
+// One more of `all` is done (with what the warp wrote before); true if it was the last, which leaves 0 (no other
+// group counts at the word).
 __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t all, int lane) {
   __syncwarp();
   uint32_t before = 0;
@@ -887,8 +877,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
   // the share of this warp; from here on the warps go their own ways
   const unsigned worker = blockIdx.x * kWarps + warp;
   const unsigned long long total = books.cost[a.B];
-  unsigned long long share = quotient(total + gridDim.x * kWarps - 1, gridDim.x * kWarps);
-  if (share < kMinShare) share = kMinShare;
+  const unsigned long long share = share_of(total, gridDim.x * kWarps);
   const unsigned long long begin = worker * share, end = min(begin + share, total);
   if (begin >= end) return;
 
@@ -1240,17 +1229,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
       }
     }
     if (!whole) {
-      // the last warp of kJoin neighbours joins their parts into its first's, the last of these writes the result
-      const unsigned w0 = (unsigned)quotient(sg.group + kGroupCost, share);
-      const unsigned w1 = (unsigned)quotient(sg.group + kGroupCost + s.tiles - 1, share);
-      const unsigned blocks = (w1 - w0) / kJoin + 1, mine = w0 + (worker - w0) / kJoin * kJoin;
-      const int n = (int)min((unsigned)kJoin, w1 - mine + 1);
-      if (last_of(a.counters + mine, n, lane)) {
+      // the last warp of a run joins its parts into the first's, the last of these writes the result
+      const Run run = run_of(sg.group, s.tiles, share, worker);
+      __syncwarp();  // (a run of one reads what its own lanes wrote)
+      if (run.n == 1 || last_of(a.counters + run.first, run.n, lane)) {
         Joined<D, ROWS> all;
-        all.of(a, mine, 1, n, share, sg.group, lane);
-        bool result = blocks == 1;
+        all.of(a, run.first, 1, run.n, share, sg.group, lane);
+        bool result = run.runs == 1;
         if (!result) {
-          float* to = part_of<S::kPart>(a, mine, share, sg.group);
+          __syncwarp();  // (the part is read before it is written again)
+          float* to = part_of<S::kPart>(a, run.first, share, sg.group);
 #pragma unroll
           for (int r = 0; r < ROWS; ++r)
 #pragma unroll
@@ -1259,8 +1247,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
             to[ROWS * D + lane] = all.top;
             to[ROWS * (D + 1) + lane] = all.l;
           }
-          result = last_of(a.counters + kMaxWarps + w0, blocks, lane);
-          if (result) all.of(a, w0, kJoin, (int)blocks, share, sg.group, lane);
+          result = last_of(a.counters + kMaxWarps + run.w0, run.runs, lane);
+          if (result) all.of(a, run.w0, kJoin, (int)run.runs, share, sg.group, lane);
         }
         if (result) {
           // lane r: where row r goes, and what it is multiplied by
