@@ -795,7 +795,9 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t all, int lan
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
     if (before == all - 1) *counter = 0;
   }
-  return __shfl_sync(kFull, before, 0) == all - 1;
+  before = __shfl_sync(kFull, before, 0);
+  __syncwarp();  // (a shuffle orders no memory: what lane 0 acquired is there for the others behind this)
+  return before == all - 1;
 }
 
 __device__ __forceinline__ float log_of_sum(float top, float l) {
