@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kPlanThreads) moves_kernel(const CompactArgs a
       const int o = __shfl_up_sync(kFull, at, k);
       if (lane >= k) at += o;
     }
-    if (w < a.words) a.before[w] = live + __shfl_sync(kFull, at - v, warp) + up - mine;
-    else __shfl_sync(kFull, at - v, warp);
+    const int in_front = __shfl_sync(kFull, at - v, warp);  // (of every lane, those without a word too)
+    if (w < a.words) a.before[w] = live + in_front + up - mine;
     live += __shfl_sync(kFull, at, 31);
     __syncthreads();
   }
