@@ -286,6 +286,23 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
   }
 }
 
+// The bf16 values of a word of codes of a row that is far_apart: to odd in float32, so that the rounding to bf16 is
+// that of the value itself (to the nearest, a minimum below float32's bits may leave a border that the value is not on).
+__device__ __noinline__ uint4 far_values(uint32_t word, float s, float m) {
+  uint32_t v[4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    float y[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float c = (float)(word >> (8 * p + 4 * e) & 15u), down = __fmaf_rd(c, s, m), up = __fmaf_ru(c, s, m);
+      y[e] = __float_as_uint(down) & 1u ? down : up;
+    }
+    v[p] = tc::pack_bf16x2(y[0], y[1]);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant__ RowArgs a) {
   constexpr int LANES = D / 16, PASS = kRowThreads / LANES, U = kRowsAhead;
@@ -327,6 +344,11 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
             for (int q = 0; q < 4; ++q) o[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
           } else {
             uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to);
+            if (far_apart(sm[u] & 0xffffu, sm[u] >> 16)) {
+              o[0] = far_values(words[u].x, s, m);
+              o[1] = far_values(words[u].y, s, m);
+              continue;
+            }
 #pragma unroll
             for (int q = 0; q < 2; ++q)
               o[q] = make_uint4(tc::pack_bf16x2(y[8 * q], y[8 * q + 1]), tc::pack_bf16x2(y[8 * q + 2], y[8 * q + 3]),

@@ -1,5 +1,6 @@
 """Rows of the 4-bit cache whose minimum is far below values on the borders of the codes: the codes
-are those of exact arithmetic (fractions), whichever side of the border x - m lies on."""
+are those of exact arithmetic (fractions), whichever side of the border x - m lies on.  And values that
+are read back as bf16: m + s c rounded once, wherever a sum in between might have been rounded too."""
 
 from fractions import Fraction
 
@@ -64,3 +65,50 @@ def test_codes_next_to_borders(D, at):
             ties += sum(2 * (Fraction(float(v)) / Fraction(float(s[part, t, 0]))) % 2 == 1 for v in rows[t])
     assert not off, (len(off), off[:5])
     assert ties > 100  # values on borders but for the minimum
+
+
+def nearest_bf16(v):
+    """The bf16 value nearest to a fraction, ties to even; 2^-133 is the smallest step."""
+    if v == 0:
+        return 0.0
+    e = -126
+    while abs(v) >= Fraction(2) ** (e + 1):
+        e += 1
+    step = Fraction(2) ** (e - 7)
+    return float(round(v / step) * step)
+
+
+def test_read_back_rounds_once():
+    """Scales and minima any number of powers of two apart, products s c on the borders of bf16 among them."""
+    r = np.random.default_rng(4)
+    D, n = 64, 700
+    pool = r.integers(0, 256, (1, o4.head_bytes(D, n))).astype(np.uint8)
+    s = r.integers(128, 256, (2, n)) * 2.0 ** -7                             # every scale's 8 bits
+    s = np.where(r.uniform(size=(2, n)) < 0.5, r.choice([131, 129, 171, 215], (2, n)) / 128, s)
+    far = r.integers(-6, 60, (2, n))
+    m = r.choice([-1.0, 1.0], (2, n)) * r.integers(128, 256, (2, n)) * 2.0 ** -7 * 2.0 ** -far.astype(float)
+    base = 2.0 ** r.choice([-120, -30, 0, 90], (2, n))
+    s, m = s * base, o4.bf16(m * base)
+    pool[0, n * D:n * (D + 8)] = np.stack([o4.bf16_bits(s), o4.bf16_bits(m)], -1).astype(np.uint16).view(np.uint8).reshape(-1)
+    codes, gs, gm = o4.read_tokens(pool, [0], n, n, 1, D)
+    assert np.array_equal(gs[..., 0], s) and np.array_equal(gm[..., 0], m)
+    out = torch.zeros(2, 1, n, 1, D, dtype=torch.bfloat16, device="cuda")
+    wide = torch.zeros(2, 1, n, 1, D, device="cuda")
+    ws = torch.zeros(4, dtype=torch.uint8, device="cuda")
+    i32 = lambda v: torch.tensor([v], dtype=torch.int32, device="cuda")
+    for o, t in ((out, sb.SV_BF16), (wide, sb.SV_F32)):
+        sb.sv_kv4_read(torch.from_numpy(pool).cuda(), 1, n, i32(0).reshape(1, 1), 1, i32(0), None, o[0], o[1], 0, 0, 0, t, 1, n,
+                       1, D, ws, 4)
+    got, wide = out.double().cpu().numpy(), wide.cpu().numpy()
+    twice = 0
+    for part in range(2):
+        for t in range(n):
+            for c in set(codes[part, t, 0].astype(int)):
+                v = Fraction(float(m[part, t])) + Fraction(float(s[part, t])) * c
+                want = nearest_bf16(v)
+                here = got[part, 0, t, 0][codes[part, t, 0] == c]
+                assert np.all(here == want), (part, t, c, float(v), want, here[0])
+                w = wide[part, 0, t, 0][codes[part, t, 0] == c][0]
+                assert w == np.float32(float(v)) or abs(Fraction(float(w)) - v) <= abs(v) * Fraction(1, 2 ** 24)
+                twice += float(o4.bf16(float(w))) != want
+    assert twice > 20  # a rounding by way of float32 gives another value there
