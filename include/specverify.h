@@ -621,8 +621,8 @@ sv_status sv_kv4_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_st
  * 2^38 elements, of W bytes); the rest needs its element's alignment.  out must not overlap an input but residual.
  * Codes less their zeros are exact; sums are float32, rounded once at the end.  With
  * M > 8 x is taken as it is.  With M <= 8 each row's 128 values of x (from a multiple
- * of 128 on) become fp16 next to a power of two: their 8 bits are kept down to 2^-25
- * of the largest of the 128, what is smaller counts as 0.  A value of x, a scale, a
+ * of 128 on) become fp16 next to a power of two: their 8 bits are kept down to 2^-28
+ * of the largest of the 128, smaller ones are off by at most 2^-36 of it.  A value of x, a scale, a
  * bias or a residual that is not finite makes the outputs that it belongs to not
  * finite, no others.  Waits are bounded (about a second): one that runs out sets
  * SV_FLAG_TIMEOUT and leaves NaN in its outputs.

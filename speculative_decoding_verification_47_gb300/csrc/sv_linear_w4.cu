@@ -12,8 +12,10 @@
 // two steps' operands in registers: w & 0x000f000f | 0x64006400 is the pair of fp16 1024 + c and
 // w & 0x00f000f0 | 0x64006400 the pair 1024 + 16 c, from which 1024 and the zero are subtracted; 16 goes into
 // x.  Five integer instructions for 8 codes (bf16, with 7 bits behind the leading one, takes seven).  x becomes
-// fp16 next to a power of two for each of its rows and 128 k: bf16's 8 bits are kept down to 2^-25 of the
-// largest of the 128 values, what is smaller counts as 0.
+// fp16 next to a power of two for each of its rows and 128 k: bf16's 8 bits are kept down to 2^-28 of the
+// largest of the 128 values, what is smaller is off by at most 2^-36 of it.
+#include <cuda_fp16.h>
+
 #include <atomic>
 #include <cstdint>
 #include <string>
@@ -72,10 +74,9 @@ constexpr uint32_t kLess1024 = 0xe400e400u;  // -1024 twice; a zero in its low b
 __device__ __forceinline__ uint32_t low_codes(uint32_t w, uint32_t less) { return add_f16x2(on_1024<0x000f000fu>(w), less); }
 __device__ __forceinline__ uint32_t high_codes(uint32_t w, uint32_t less) { return add_f16x2(on_1024<0x00f000f0u>(w), less); }
 
-// A pair of bf16 whose exponents lie in `low` (both halves, bf16 with no bits behind the leading one) .. low + 30
-// as fp16 with exponents 0 .. 30; smaller values become 0.
-__device__ __forceinline__ uint32_t to_f16x2(uint32_t v, uint32_t low) {
-  return (__vmaxu2(v & 0x7fff7fffu, low) - low) << 3 | (v & 0x80008000u);
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // A tile's outputs from the sums part[column][row] of a cluster's CTAs, added in the order of their ranks; each
@@ -216,19 +217,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
       top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 1));
       top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 2));
       const int ex = (int)(max(top & 0xffffu, top >> 16) >> 7);  // biased exponent of the largest value
-      // the largest value's exponent becomes 30; the 1/16 of the high codes takes four more
-      const uint32_t low = (uint32_t)max(ex - 30, 0) * 0x00800080u, low16 = low + 4 * 0x00800080u;
+      // the largest value becomes 2^15 or more, below 2^16, with a factor of at most 2^126 (which makes every bf16
+      // value a multiple of 2^-7); the high codes' sixteenth of it loses four bits at the lower end
+      const int fb = min(269 - ex, 253);
+      const float up = __uint_as_float((uint32_t)fb << 23), up16 = up * 0.0625f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const uint4 v = xn[w];
-        b[w][0] = to_f16x2(__byte_perm(v.x, v.z, 0x5410), low);
-        b[w][1] = to_f16x2(__byte_perm(v.x, v.z, 0x7632), low16);
-        b[w][2] = to_f16x2(__byte_perm(v.y, v.w, 0x5410), low);
-        b[w][3] = to_f16x2(__byte_perm(v.y, v.w, 0x7632), low16);
+        b[w][0] = half2_of(bf16_lo(v.x) * up, bf16_lo(v.z) * up);
+        b[w][1] = half2_of(bf16_hi(v.x) * up16, bf16_hi(v.z) * up16);
+        b[w][2] = half2_of(bf16_lo(v.y) * up, bf16_lo(v.w) * up);
+        b[w][3] = half2_of(bf16_hi(v.y) * up16, bf16_hi(v.w) * up16);
       }
-      // 2^(low - 112): fp16's exponents are biased by 15, bf16's by 127; NaN for a row that is not finite
-      const int e = max(ex - 30, 0) + 15;
-      const float f = ex == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)e << 23);
+      // NaN for a row that is not finite
+      const float f = ex == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(254 - fb) << 23);
 #pragma unroll
       for (int j = 0; j < 2; ++j) undo[j] = __shfl_sync(kFull, f, (2 * t + j) * 4);
     }
