@@ -1239,13 +1239,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, ROWS>::kMinCtas) attention_
         if (bad) l[j] = __uint_as_float(0x7fc00000u);
         const int r = nt * 8 + 2 * t + j;
         if (r >= rows || (HALF && t >= 2)) continue;
-        // the codes' subnormals undone; D = 128: odd values stand 4 bits up; D = 64: the second row of a tile does
-        float even = ex2(ref[nt][j] - vref[nt][j]), inv = 1.f;
+        // the codes' subnormals undone, and the 2^7 of the weights (here, so that a v scale next to 2^-126 is a
+        // factor above it); D = 128: odd values stand 4 bits up; D = 64: the second row of a tile does
+        float even = ex2(ref[nt][j] - vref[nt][j] + 7.f), inv = 1.f;
         if (whole) inv = l[j] == 0.f ? 0.f : __frcp_rn(l[j]);
         float x[TILES], y[TILES];
 #pragma unroll
         for (int n = 0; n < TILES; ++n) {
-          const float u0 = D == 128 && (n & 1) ? 0x1p20f : 0x1p24f, u1 = D == 128 ? u0 : 0x1p20f;
+          const float u0 = D == 128 && (n & 1) ? 0x1p13f : 0x1p17f, u1 = D == 128 ? u0 : 0x1p13f;
           x[n] = __fmaf_rn(o[nt][n][j] * u0, even, add[j]) * inv;
           y[n] = __fmaf_rn(o[nt][n][2 + j] * u1, even, add[j]) * inv;
         }
