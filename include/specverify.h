@@ -581,11 +581,13 @@ sv_status sv_kv4_read(const void* pool, int num_pages, int page_size, const int3
  *                 word (OR-ed, not cleared).  Calls that share a workspace must be
  *                 ordered on one stream.
  * q, out and pool must be 16-byte aligned, strides multiples of 8 elements.  The
- * products take the codes and a float32 scale per token, the sums are float32; q
- * and the weights p_j s_j are fp16 next to a power of two per row (11 bits for what
- * is within 2^-29 of the row's largest; below that an absolute 2^-40 of it).  Values
- * of q, their products with scale, and values of v below 2^96 in magnitude (beyond,
- * a sum may be infinite); a query with one that is not finite gets NaN.
+ * products take the codes and a float32 scale per token; scores, the logarithms of the
+ * weights p_j s_j and all sums are float32.  q is fp16 next to a power of two per row:
+ * its 8 bits are kept down to 2^-27 of the row's largest value, smaller ones are off by
+ * at most 2^-35 of it.  The weights are fp16 next to another: 11 bits down to 2^-21 of
+ * the row's largest, smaller ones are off by at most 2^-32 of it.  Values of q, their
+ * products with scale, scores and values of v below 2^96 in magnitude (beyond, a sum may
+ * be infinite and a weight 0); a query with a value that is not finite gets NaN.
  * Tokens that a query does not see are not used, whatever they hold; scales below
  * 2^-126 count as 0 in v.  A sequence with k_b outside [0, K] (SV_FLAG_BAD_K), with
  * L < 0 or L + k_b past its table (SV_FLAG_BAD_N), or with a page outside
