@@ -1476,7 +1476,7 @@ int kv4_rows_launch(const Kv4RowsLaunch& L, std::string* err) {
   if (a.tokens > L.T) a.tokens = L.T;
   a.by_rows = kv4::divider(2 * L.c.Hkv);
   // a row of CTAs a sequence, no more in all than keep every SM busy with several
-  const long long per_seq = (L.T + a.tokens - 1) / a.tokens, most = (long long)tc::num_sms() * 16;
+  const long long per_seq = (L.T - 1) / a.tokens + 1LL, most = (long long)tc::num_sms() * 16;
   const int across = (int)(per_seq < most ? per_seq : most), rows = (int)(most / across);
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = kv4::config(across, kv4::kRowThreads, 0, L.stream, &attr);
