@@ -15,6 +15,8 @@ std::atomic<int> g_wait_tries{sv::kWaitTries};
 
 sv_status fail(sv_status s, const std::string& msg) {
   g_last_error = msg;
+  // a launch that failed leaves its error for the next cudaGetLastError(), which would be a good call's
+  if (s == SV_ERR_CUDA) (void)cudaGetLastError();
   return s;
 }
 
