@@ -588,6 +588,8 @@ sv_status sv_kv4_read(const void* pool, int num_pages, int page_size, const int3
  * the row's largest, smaller ones are off by at most 2^-32 of it.  Values of q, their
  * products with scale, scores and values of v below 2^96 in magnitude (beyond, a sum may
  * be infinite and a weight 0); a query with a value that is not finite gets NaN.
+ * A call gives the same bits again; how a row's sums are parted depends on the batch's
+ * lengths, on max_pages and on the window, so these may change the last bits.
  * Tokens that a query does not see are not used, whatever they hold; scales below
  * 2^-126 count as 0 in v.  A sequence with k_b outside [0, K] (SV_FLAG_BAD_K), with
  * L < 0 or L + k_b past its table (SV_FLAG_BAD_N), or with a page outside
@@ -625,9 +627,9 @@ sv_status sv_kv4_attention(const void* q, int64_t q_seq_stride, int64_t q_pos_st
  * Codes less their zeros are exact; sums are float32, rounded once at the end.  With
  * M > 8 x is taken as it is.  With M <= 8 each row's 128 values of x (from a multiple
  * of 128 on) become fp16 next to a power of two: their 8 bits are kept down to 2^-28
- * of the largest of the 128, smaller ones are off by at most 2^-36 of it.  A value of x, a scale, a
- * bias or a residual that is not finite makes the outputs that it belongs to not
- * finite, no others.  Waits are bounded (about a second): one that runs out sets
+ * of the largest of the 128, smaller ones are off by at most 2^-36 of it.  A value of
+ * x, a scale or a bias that is not finite makes the z that it belongs to not finite, a
+ * residual the out, and no others.  Waits are bounded (about a second): one that runs out sets
  * SV_FLAG_TIMEOUT and leaves NaN in its outputs.
  */
 size_t sv_linear_w4_workspace_size(int M, int N, int K);

@@ -18,13 +18,15 @@
 // tokens on the 16-row side of mma.m16n8k16 a step of one query position (8 rows of a key
 // head) wastes nothing, and codes never leave registers: 4 bits at the bottom of a half are
 // the fp16 subnormal c 2^-24 (8 bits up c 2^-20), exact, so one AND makes two operands.  Q is
-// fp16 with a power of two per row, which keeps bf16's 8 bits down to 2^-25 of the row's
-// largest value; p_j s'_j is fp16 next to a running maximum of its own.
+// fp16 with a power of two per row, which keeps bf16's 8 bits down to 2^-27 of the row's
+// largest value; p_j s'_j is fp16 next to a running maximum of its own (2^7 to 2^15 there, so that the maximum may
+// grow by 2^8 before sums are scaled: 11 bits down to 2^-21 of the largest, 2^-32 of it below; the plain float32
+// form's distance from 64 bits is the output's own rounding, 0.0017, and so is this one's).
 //
 // 256 sequences of up to 4096 tokens, 32 query and 8 key heads of 128: 122 us, 592 MB at 72% of
 // the measured copy rate, and next to that bound by the integer instructions that take codes
 // apart (half the rate of the others; 53% of the slots).  64 sequences, 1 to 4 positions, a window
-// of 1024: 34 us for 75 MB, some 15 of it the way to the first tile and the joins of the parts.
+// of 1024: 35 us for 75 MB, some 15 of it the way to the first tile and the joins of the parts.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -78,8 +80,8 @@ inline Cache cache_of(const Kv4Cache& c, int D) {
 // ---------------------------------------------------------------------------
 // Writing and reading.  D / 16 lanes share a row, 16 values of it each: two words of codes.  A CTA takes a
 // few tokens of one sequence, kRowsAhead rows a thread, whose loads are all on their way before the first is
-// used.  8 prompts of up to 4096 tokens and 8 heads: writing 39 us, reading back 27 us, where the bytes take
-// 14 each; the instructions for addresses and codes bound both (73% and 67% of the issue slots).
+// used.  8 prompts of up to 4096 tokens and 8 heads: writing 40 us, reading back 28 us, where the bytes take
+// 14 each; the instructions for addresses and codes bound both (73% and 68% of the issue slots).
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 constexpr int kRowsAhead = 2;

@@ -119,8 +119,9 @@ constexpr int kStages = 8;   // of a warp
 constexpr int kAhead = 6;    // steps on their way
 constexpr int kStageBytes = 16 * kPitch;
 
-// 1 x 16384 x 4096 in groups of 128: 14 to 17 us, where W's 34 MB take 5; the start, the ends of the chunks' chains and
-// the instructions (45% of the issue slots) share the rest.
+// 1 x 16384 x 4096 in groups of 128: 14.0 us a call in a row of calls whose W come from HBM, where its 34 MB take 5
+// (alone, behind an emptied L2, 19 to 21 us with the launch); the start, the ends of the chunks' chains and the
+// instructions (46% of the issue slots) share the rest.
 constexpr int kTiles = 4;    // of a CTA: more share the work on x, fewer want fewer registers
 constexpr int kRows = 16 * kTiles;
 constexpr int kCtas = 2;     // of an SM
@@ -218,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
       top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 2));
       const int ex = (int)(max(top & 0xffffu, top >> 16) >> 7);  // biased exponent of the largest value
       // the largest value becomes 2^15 or more, below 2^16, with a factor of at most 2^126 (which makes every bf16
-      // value a multiple of 2^-7); the high codes' sixteenth of it loses four bits at the lower end
+      // value a multiple of 2^-7); the high codes' sixteenth of it loses four bits at the lower end.  (Exponents
+      // subtracted in integers were no faster, 14.2 us for 14.0, and had no subnormal values.)
       const int fb = min(269 - ex, 253);
       const float up = __uint_as_float((uint32_t)fb << 23), up16 = up * 0.0625f;
 #pragma unroll
@@ -320,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) rows_kernel(const __grid_cons
 // exact) in tensor memory, where the 128-row operand may stand (through shared memory its bytes were the bound); a thread issues
 // the groups' products, each group's into an accumulator of tensor memory of its own; four or eight warps take those
 // out, times the groups' scales, and add them to their float32 sums in registers.  64 x 16384 x 4096 in groups of 128:
-// 20.5 us, 16 x 8192 x 8192 in groups of 64: 19.5 us, where W's 34 MB take 5; bound by the way of a block through these
-// warps (its parts take 400 to 800 cycles each, and four are under way), next by the instructions that take codes
+// 20.8 us, 16 x 8192 x 8192 in groups of 64: 19.7 us a call in a row of calls whose W come from HBM, where its 34 MB
+// take 5 (alone, behind an emptied L2, 29 and 27 us with the launch); bound by the way of a block through these warps (its parts take 400 to 800 cycles each, and four are under way), next by the instructions that take codes
 // apart.  mma.sync took 66 us for the first, since each warp then multiplies all rows of x and the codes have to be
 // taken apart again for every 8 of them.
 // ---------------------------------------------------------------------------

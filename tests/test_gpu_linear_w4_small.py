@@ -50,6 +50,20 @@ def test_values_far_below_their_largest(far, largest):
     assert np.all(np.abs(got - ref) <= 2.0 ** -15 * absp + lost)
 
 
+@pytest.mark.parametrize("M", [3, 12])
+def test_infinite_biases_before_the_activation(M):
+    """What is not finite is z: an activation may take it back to a number, as its formula does."""
+    s = inputs(M, M, 40, 64, 32, False, True, False, torch.float32)
+    s["bias"][3], s["bias"][7] = float("-inf"), float("inf")
+    z = run(s, M, 40, 64, 32, sb.SV_ACT_NONE, torch.float32).cpu()
+    relu = run(s, M, 40, 64, 32, sb.SV_ACT_RELU, torch.float32).cpu()
+    assert torch.all(z[:, 3] == float("-inf")) and torch.all(z[:, 7] == float("inf"))
+    assert torch.all(relu[:, 3] == 0) and torch.all(relu[:, 7] == float("inf"))
+    keep = torch.ones(40, dtype=torch.bool)
+    keep[[3, 7]] = False
+    assert torch.isfinite(z[:, keep]).all() and torch.equal(relu[:, keep], z[:, keep].clamp(min=0))
+
+
 @pytest.mark.parametrize("N,K,group", [(300, 1024, 128), (130, 416, 32)])
 def test_rows_of_eight_and_of_nine(N, K, group):
     """The same rows in calls of 8 and of 9 differ by their roundings: float32 sums of at most 128 terms on either side
