@@ -80,7 +80,7 @@ inline Cache cache_of(const Kv4Cache& c, int D) {
 // ---------------------------------------------------------------------------
 // Writing and reading.  D / 16 lanes share a row, 16 values of it each: two words of codes.  A CTA takes a
 // few tokens of one sequence, kRowsAhead rows a thread, whose loads are all on their way before the first is
-// used.  8 prompts of up to 4096 tokens and 8 heads: writing 40 us, reading back 28 us, where the bytes take
+// used.  8 prompts of up to 4096 tokens and 8 heads: writing 42 us, reading back 28 us, where the bytes take
 // 14 each; the instructions for addresses and codes bound both (73% and 68% of the issue slots).
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
@@ -175,6 +175,21 @@ struct Coder {
     half = 0.5f * hs;
     below = __uint_as_float(__float_as_uint(half) - 1u);
   }
+  // Whether 0 - m lies on a border (an odd number of half steps), and one of 16 values is next to it: not 0, but 2^16 or
+  // more times smaller than m.  Then x - m may be rounded onto that border.  (Another border is too far from m for an x
+  // of so few bits, where the row is not far_apart.)
+  __device__ __forceinline__ bool next_to_border(const uint4& v, const uint4& w, uint32_t m_bits) const {
+    float low, r, same;
+    f2_unpack(hm, low, same);
+    f2_unpack(inv, r, same);
+    const float y = __fmaf_rn(low, 2.f * r, 12582912.f);  // (-m in half steps)
+    if (!(__float_as_uint(y) & 1u) || (y - 12582912.f) * half != low) return false;
+    const uint32_t words[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
+    uint32_t least = ~0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) least = __vminu2(least, __vsub2(words[i] & 0x7fff7fffu, 0x00010001u));
+    return (int)min(least & 0xffffu, least >> 16) < (int)(m_bits & 0x7fffu) - (16 << 7);
+  }
   // Codes of 8 values: the nearest integers to (x - m) / s, ties to even.  The product with the reciprocal,
   // rounded by the addition of 1.5 2^23, is one off at most, where the quotient lies next to a border: the
   // remainder (exact: c and s have 4 and 8 bits) is then beyond half a step, or is half a step and c is odd.
@@ -206,9 +221,9 @@ struct Coder {
   }
 };
 
-// The same for a row that is far_apart: x - m may have been rounded onto a border from either side, and what that
-// rounding lost decides.  (In the function above it costs registers that every row pays for: the prompts take 50 us
-// instead of 42.)
+// The same for a row that is far_apart, or a value next_to_border: x - m may have been rounded onto a border from
+// either side, and what that rounding lost decides.  (In the function above it costs registers that every row pays
+// for: the prompts take 50 us instead of 44.)
 __device__ __noinline__ uint32_t far_word(uint4 v, float m, float s) {
   const uint32_t pairs[4] = {v.x, v.y, v.z, v.w};
   const float up = s < 0x1p-60f ? 0x1p80f : 1.f;
@@ -272,13 +287,15 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
           uint2 words = make_uint2(0, 0);
           if (!(isfinite(lo) && isfinite(hi))) {
             sb = mb = 0x7fc0u;  // a token that is not finite makes the scores of the queries that see it NaN
-          } else if (far_apart(sb, mb)) {
-            words.x = far_word(v[u][0], lo, sr);
-            words.y = far_word(v[u][1], lo, sr);
           } else if (sr > 0.f) {
             const Coder coder(lo, sr);
-            words.x = coder.word(v[u][0]);
-            words.y = coder.word(v[u][1]);
+            if (far_apart(sb, mb) || coder.next_to_border(v[u][0], v[u][1], mb)) {
+              words.x = far_word(v[u][0], lo, sr);
+              words.y = far_word(v[u][1], lo, sr);
+            } else {
+              words.x = coder.word(v[u][0]);
+              words.y = coder.word(v[u][1]);
+            }
           }
           reinterpret_cast<uint2*>(w[u].codes)[lane] = words;
           if (lane == 0) *reinterpret_cast<uint32_t*>(w[u].codes + w[u].scale) = (uint32_t)sb | (uint32_t)mb << 16;

@@ -67,6 +67,40 @@ def test_codes_next_to_borders(D, at):
     assert ties > 100  # values on borders but for the minimum
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("at", [0, -100, 100])
+def test_codes_of_values_next_to_zero(D, at):
+    """Rows in which 0 lies on a border (a minimum of an odd number of half steps), with values so near to 0 that the
+    difference to the minimum rounds onto the border: the side decides."""
+    r = np.random.default_rng(D + at + 200)
+    rows = []
+    for odd in range(1, 30, 2):
+        for step in (1.0, 1.25, 0.625, 1.375, 1.625, 129 / 128):
+            low, high = -odd * 0.5 * step, (30 - odd) * 0.5 * step
+            if o4.bf16(low) != low or o4.bf16(high) != high:
+                continue
+            x = r.uniform(low, high, D)
+            tiny = r.choice([-1, 1], D) * r.integers(128, 256, D) / 128 * 2.0 ** -r.integers(10, 27, D).astype(float)
+            x = np.where(r.uniform(size=D) < 0.4, tiny, x)
+            x[:4] = 0.0, low, high, -2.0 ** -25
+            rows.append(o4.bf16(r.permutation(x)) * 2.0 ** at)
+    rows = np.array(rows)
+    n = len(rows)
+    assert n > 40
+    x = torch.from_numpy(rows).to(torch.bfloat16).reshape(1, n, 1, D)
+    pool = torch.zeros(1, sb.sv_kv4_page_bytes(1, D, n), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(4, dtype=torch.uint8, device="cuda")
+    i32 = lambda v: torch.tensor([v], dtype=torch.int32, device="cuda")
+    sb.sv_kv4_append(x.cuda(), (-x).cuda(), 0, 0, 0, sb.SV_BF16, pool, 1, n, i32(0).reshape(1, 1), 1, i32(0), None, 1, n, 1, D,
+                     ws, 4)
+    codes, s, m = o4.read_tokens(pool.cpu().numpy(), [0], n, n, 1, D)
+    for part, sign in enumerate((1, -1)):
+        want_s, want_m = o4.quantise(sign * rows)[1:]
+        assert np.array_equal(s[part, :, 0], want_s) and np.array_equal(m[part, :, 0], want_m)
+        for t in range(n):
+            assert codes[part, t, 0].tolist() == exact_codes(sign * rows[t], s[part, t, 0]), (part, t)
+
+
 def nearest_bf16(v):
     """The bf16 value nearest to a fraction, ties to even; 2^-133 is the smallest step."""
     if v == 0:
